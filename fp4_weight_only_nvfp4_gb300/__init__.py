@@ -13,6 +13,9 @@ import ctypes
 import torch
 
 from ._lib import GemmOpts, LaunchInfo, VtError, check, lib
+from .rows import (LoraAdapters, RowGroups, group_rows, group_workspace, lora_add, moe_ffn,
+                   moe_route, w4a16_gemm_ragged, w4a16_gemm_ragged_combine,
+                   w4a16_gemm_ragged_silu_mul)
 
 NVFP4, MXFP4 = 0, 1
 GROUP = {NVFP4: 16, MXFP4: 32}
@@ -20,7 +23,9 @@ GROUP = {NVFP4: 16, MXFP4: 32}
 __all__ = ["NVFP4", "MXFP4", "GROUP", "PackedWeight", "w4a16_gemm", "w4a16_gemm_noalloc",
            "w4a16_gemm_greedy", "w4a16_gemm_silu_mul", "w4a16_gemm_moe", "w4a4_gemm",
            "quantize_act", "quantize", "prepack_bytes", "workspace_status", "noalloc_status", "VtError",
-           "algorithmic_bytes"]
+           "algorithmic_bytes", "RowGroups", "group_rows", "group_workspace", "moe_route",
+           "w4a16_gemm_ragged", "w4a16_gemm_ragged_silu_mul", "w4a16_gemm_ragged_combine",
+           "moe_ffn", "LoraAdapters", "lora_add"]
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -129,6 +134,42 @@ class PackedWeight:
         W = cls(h, packed, fmt, N, K)
         W.E = E
         return W
+
+    @classmethod
+    def grouped_gate_up(cls, gate: tuple, up: tuple, fmt: int, E: int, I: int, K: int,
+                        stream=None) -> "PackedWeight":
+        """E experts' fused gate and up weights, paired for the SiLU-and-multiply epilogue of the
+        ragged products: ``gate``/``up`` are (codes [E, I, K/2], scales [E, I, K/g], one global
+        per expert) (vt_fp4_prepack_grouped_gate_up); N = 2*I."""
+        args = []
+        for codes, scales, globals_ in (gate, up):
+            if codes.shape != (E, I, K // 2) or scales.shape != (E, I, K // GROUP[fmt]):
+                raise ValueError("codes [E, I, K/2] and scales [E, I, K/g] expected")
+            _check_src(codes, scales, E * I, K, fmt)
+            if len(globals_) != E:
+                raise ValueError("one global per expert expected")
+            args += [_ptr(codes), _ptr(scales), (ctypes.c_float * E)(*[float(x) for x in globals_])]
+        if gate[0].device != up[0].device:
+            raise ValueError("gate and up must be on one GPU")
+        out = ctypes.c_size_t(0)
+        check(lib().vt_fp4_prepack_grouped_bytes(fmt, E, 2 * I, K, ctypes.byref(out)),
+              "vt_fp4_prepack_grouped_bytes")
+        packed = torch.empty(out.value, dtype=torch.uint8, device=gate[0].device)
+        h = ctypes.c_void_p(0)
+        check(lib().vt_fp4_prepack_grouped_gate_up(*args, fmt, E, I, K, _ptr(packed), out.value,
+                                                   _stream(stream), ctypes.byref(h)),
+              "vt_fp4_prepack_grouped_gate_up")
+        W = cls(h, packed, fmt, 2 * I, K)
+        W.E, W.I, W.paired = E, I, True
+        return W
+
+    def ragged_workspace(self, M_max: int, topk: int) -> torch.Tensor:
+        """A zeroed workspace for the ragged products on this weight of up to M_max tokens of
+        topk pairs each (zero once; any smaller call may share it in stream order)."""
+        out = ctypes.c_size_t(0)
+        check(lib().vt_fp4_ragged_workspace_bytes(self.handle, M_max, topk, ctypes.byref(out)),
+              "vt_fp4_ragged_workspace_bytes")
+        return torch.zeros(out.value, dtype=torch.uint8, device=self.packed.device)
 
     def moe_workspace(self, M_max: int, topk: int) -> torch.Tensor:
         out = ctypes.c_size_t(0)

@@ -67,6 +67,19 @@ SIGNATURES = {
     "vt_fp4_w4a4_gemm": (_ST, [_P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P, _SZ, _P]),
     "vt_fp4_w4a4_gemm_ex": (_ST, [_P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P, _SZ, _P,
                                   ctypes.POINTER(GemmOpts)]),
+    "vt_fp4_group_workspace_bytes": (_ST, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "vt_fp4_group_rows": (_ST, [_P, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "vt_fp4_moe_route": (_ST, [_P, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_int, _P,
+                               ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _P, _SZ, _P]),
+    "vt_fp4_prepack_grouped_gate_up": (_ST, [_P, _P, _P, _P, _P, _P, ctypes.c_int, _I64, _I64,
+                                             _I64, _P, _SZ, _P, ctypes.POINTER(_P)]),
+    "vt_fp4_ragged_workspace_bytes": (_ST, [_P, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "vt_fp4_w4a16_gemm_ragged": (_ST, [_P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_int, _P, _I64,
+                                       _P, _SZ, _P]),
+    "vt_fp4_w4a16_gemm_ragged_combine": (_ST, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _I64,
+                                               _P, _SZ, _P]),
+    "vt_fp4_lora_add": (_ST, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P,
+                              _I64, _P, _I64, _P]),
     "vt_fp4_last_error": (ctypes.c_char_p, []),
 }
 

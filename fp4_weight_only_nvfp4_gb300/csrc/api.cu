@@ -327,6 +327,45 @@ vt_status vt_fp4_prepack_grouped(const uint8_t* codes, const uint8_t* scales,
   return VT_OK;
 }
 
+vt_status vt_fp4_prepack_grouped_gate_up(const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                         const float* gate_globals, const uint8_t* up_codes,
+                                         const uint8_t* up_scales, const float* up_globals,
+                                         vt_fp4_format fmt, int64_t E, int64_t I, int64_t K,
+                                         void* packed_dst, size_t dst_bytes, vt_stream_t s,
+                                         vt_fp4_handle* out) {
+  if (!out) return fail(VT_ERR_INVALID_ARG, "out handle pointer is NULL");
+  *out = nullptr;
+  if (I <= 0 || I > (int64_t)1 << 30) return fail(VT_ERR_INVALID_ARG, "I must be in [1, 2^30]");
+  size_t need = 0;
+  if (vt_status st = vt_fp4_prepack_grouped_bytes(fmt, E, 2 * I, K, &need)) return st;
+  if (!gate_codes || !gate_scales || !gate_globals || !up_codes || !up_scales || !up_globals ||
+      !packed_dst)
+    return fail(VT_ERR_INVALID_ARG, "codes, scales, globals and packed_dst must be set");
+  if (dst_bytes < need)
+    return fail(VT_ERR_INVALID_ARG, "packed_dst holds %zu bytes, %zu needed", dst_bytes, need);
+  const size_t per = packed_size(fmt, 2 * I, K);
+  const int64_t cb = I * (K / 2), sb = I * (K / group_of(fmt));
+  vt_fp4_handle first = nullptr;
+  for (int64_t e = 0; e < E; ++e) {
+    vt_fp4_handle h = nullptr;
+    vt_status st = vt_fp4_prepack_gate_up_paired(
+        gate_codes + e * cb, gate_scales + e * sb, gate_globals[e], up_codes + e * cb,
+        up_scales + e * sb, up_globals[e], fmt, I, K, static_cast<uint8_t*>(packed_dst) + e * per,
+        per, s, &h);
+    if (st) {
+      delete first;
+      return st;
+    }
+    if (e == 0) first = h;
+    else delete h;
+  }
+  first->E = E;
+  first->expert_bytes = (int64_t)per;
+  first->packed_bytes = need;
+  *out = first;
+  return VT_OK;
+}
+
 vt_status vt_fp4_destroy(vt_fp4_handle W) {
   delete W;
   return VT_OK;

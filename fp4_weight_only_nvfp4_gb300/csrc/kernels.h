@@ -115,4 +115,73 @@ cudaError_t launch_quantize_act(const void* A, int64_t M, int64_t lda, int64_t K
 
 constexpr int kMaxDecodeGrid = 512;
 
+// ---------------------------------------------------------- rows grouped by an index
+constexpr int kMaxGroups = 1024;  // indices E
+constexpr int kMaxTopk = 32;
+constexpr int kMaxRank = 128;     // of a low-rank adapter
+
+// Router (logits set) and grouping (ids read when logits is NULL, else written).
+struct RouteLaunch {
+  const void* logits;  // [M][ld] fp32 or bf16, or NULL
+  int bf16;
+  int64_t ld;
+  int scoring;         // 0 softmax, 1 sigmoid
+  const float* bias;   // [E] or NULL
+  int renormalize;
+  float scale;
+  int64_t M;
+  int E, topk;
+  int32_t* ids;        // [M][topk]
+  float* weights;      // [M][topk]
+  int32_t* order;      // [M * topk]
+  int32_t* offsets;    // [E + 1]
+  void* workspace;
+};
+size_t route_workspace_bytes(int64_t pairs, int64_t E);
+cudaError_t launch_route(const RouteLaunch& L, cudaStream_t s);
+
+// Ragged products over the groups.
+struct RaggedLaunch {
+  const void* packed;
+  int fmt;
+  int64_t N, K, RT, KT, seg_split;
+  uint32_t layout;
+  int64_t expert_bytes;
+  int E;
+  const void* A;       // bf16 [tokens or pairs][lda]
+  int64_t lda;
+  const int32_t* order;
+  const int32_t* offsets;
+  int64_t pairs;
+  int topk;
+  int gather, scatter, silu;
+  void* C;
+  int64_t ldc;
+  int* status;
+};
+cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s);
+// out[m] = sum_j weights[m][j] * D[m * topk + j], pairs whose id is outside [0, E) left out.
+cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,
+                           const int32_t* ids, int E, const float* weights, void* out,
+                           int64_t ldo, cudaStream_t s);
+
+// Low-rank adapters.
+struct LoraLaunch {
+  const void* x;
+  int64_t M, ldx, K;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* ranks;
+  int L, R;
+  int64_t N;
+  const int32_t* order;
+  const int32_t* offsets;
+  const void* y;
+  int64_t ldy;
+  void* out;
+  int64_t ldo;
+};
+cudaError_t launch_lora(const LoraLaunch& L, cudaStream_t s);
+
 }  // namespace vt

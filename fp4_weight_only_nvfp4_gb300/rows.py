@@ -1,0 +1,264 @@
+"""Operators on rows grouped by an index chosen on the device: the mixture-of-experts router,
+the experts' ragged products, and low-rank adapters (the entry points of include/vt_fp4.h from
+vt_fp4_group_rows to vt_fp4_lora_add).  Argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import check, lib
+
+SCORING = {"softmax": 0, "sigmoid": 1}
+GATHER, SCATTER, SILU_MUL = 1, 2, 4
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need(t, name, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this GPU."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (got {t.device})")
+
+
+def _rows(t, name, rows, cols, device):
+    """A bf16 matrix with unit inner stride on this GPU; returns its row stride."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols \
+            or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a bf16 [{rows}, {cols}] tensor with unit inner stride")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (got {t.device})")
+    st = t.stride(0)
+    if rows > 1 and st < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return st if rows > 1 else max(st, cols)
+
+
+def _workspace(ws, device):
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or not ws.is_cuda or ws.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor on {device}")
+    return ws.data_ptr(), ws.numel()
+
+
+class RowGroups:
+    """(token, slot) pairs grouped by an index.  ids int32 [M, topk] (or [M], topk = 1), order
+    int32 [M * topk], offsets int32 [E + 1]: group e holds the pairs order[offsets[e]:offsets[e
+    + 1]], pair p being slot p % topk of token p // topk; pairs whose id is outside [0, E) come
+    last.  weights: fp32 [M, topk] where a router made them."""
+
+    def __init__(self, ids: torch.Tensor, order: torch.Tensor, offsets: torch.Tensor,
+                 weights: torch.Tensor | None = None):
+        if ids.dim() not in (1, 2):
+            raise ValueError("ids must be [M, topk] or [M]")
+        self.M, self.topk = ids.shape[0], (ids.shape[1] if ids.dim() == 2 else 1)
+        self.E, self.pairs = offsets.numel() - 1, ids.numel()
+        dev = self.device = ids.device
+        _need(ids, "ids", torch.int32, tuple(ids.shape), dev)
+        _need(order, "order", torch.int32, (self.pairs,), dev)
+        _need(offsets, "offsets", torch.int32, (self.E + 1,), dev)
+        if weights is not None:
+            _need(weights, "weights", torch.float32, (self.M, self.topk), dev)
+        self.ids, self.order, self.offsets, self.weights = ids, order, offsets, weights
+
+    @classmethod
+    def empty(cls, M: int, topk: int, E: int, device, weights: bool = False) -> "RowGroups":
+        """Uninitialised buffers for moe_route (weights=True) or group_rows to fill."""
+        ids = torch.empty((M, topk), dtype=torch.int32, device=device)
+        return cls(ids, torch.empty(M * topk, dtype=torch.int32, device=device),
+                   torch.empty(E + 1, dtype=torch.int32, device=device),
+                   torch.empty((M, topk), dtype=torch.float32, device=device) if weights else None)
+
+
+def group_workspace(M_max: int, topk: int, E: int, device) -> torch.Tensor:
+    """A zeroed workspace for moe_route and group_rows of up to M_max tokens of topk pairs."""
+    out = ctypes.c_size_t(0)
+    check(lib().vt_fp4_group_workspace_bytes(M_max * topk, E, ctypes.byref(out)),
+          "vt_fp4_group_workspace_bytes")
+    return torch.zeros(out.value, dtype=torch.uint8, device=device)
+
+
+def group_rows(ids: torch.Tensor, E: int, out: RowGroups | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> RowGroups:
+    """Groups the pairs of ids (int32 [M] or [M, topk]; outside [0, E): in no group)."""
+    if ids.dtype != torch.int32 or ids.dim() not in (1, 2) or not ids.is_contiguous() \
+            or not ids.is_cuda:
+        raise ValueError("ids must be a contiguous int32 CUDA tensor [M] or [M, topk]")
+    dev = ids.device
+    if out is None:
+        out = RowGroups(ids, torch.empty(ids.numel(), dtype=torch.int32, device=dev),
+                        torch.empty(E + 1, dtype=torch.int32, device=dev))
+    elif out.E != E or out.pairs != ids.numel() or out.device != dev:
+        raise ValueError("out does not have the shape of ids and E")
+    else:
+        out.ids = ids
+    if workspace is None:
+        workspace = group_workspace(ids.numel(), 1, E, dev)
+    wp, wn = _workspace(workspace, dev)
+    check(lib().vt_fp4_group_rows(ids.data_ptr(), ids.numel(), E, out.order.data_ptr(),
+                                  out.offsets.data_ptr(), wp, wn, _raw_stream(stream, dev)),
+          "vt_fp4_group_rows")
+    return out
+
+
+def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
+              bias: torch.Tensor | None = None, renormalize: bool = True, scale: float = 1.0,
+              out: RowGroups | None = None, workspace: torch.Tensor | None = None,
+              stream=None) -> RowGroups:
+    """The router: per token (row of logits, fp32 or bf16 [M, E]) the topk experts of largest
+    score, ties to the lowest index, with their weights, grouped by expert.  An expert masked
+    by a logit of -inf is never chosen (id -1, weight 0).  See vt_fp4_moe_route in
+    include/vt_fp4.h."""
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 \
+            or (logits.shape[1] > 1 and logits.stride(1) != 1) or not logits.is_cuda:
+        raise ValueError("logits must be an fp32 or bf16 CUDA [M, E] tensor with unit inner stride")
+    if scoring not in SCORING:
+        raise ValueError(f"scoring must be one of {sorted(SCORING)}")
+    M, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), dev)
+    if out is None:
+        out = RowGroups.empty(M, topk, E, dev, weights=True)
+    elif (out.M, out.topk, out.E, out.device) != (M, topk, E, dev) or out.weights is None:
+        raise ValueError("out must be RowGroups.empty(M, topk, E, device, weights=True)")
+    if workspace is None:
+        workspace = group_workspace(M, topk, E, dev)
+    wp, wn = _workspace(workspace, dev)
+    ld = logits.stride(0) if M > 1 else max(logits.stride(0), E)
+    check(lib().vt_fp4_moe_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), M, ld, E,
+                                 topk, SCORING[scoring], bias.data_ptr() if bias is not None else 0,
+                                 int(renormalize), scale, out.ids.data_ptr(),
+                                 out.weights.data_ptr(), out.order.data_ptr(),
+                                 out.offsets.data_ptr(), wp, wn, _raw_stream(stream, dev)),
+          "vt_fp4_moe_route")
+    return out
+
+
+def _check_groups(W, groups):
+    E = getattr(W, "E", 1)
+    if groups.E != E:
+        raise ValueError(f"the groups are of {groups.E} indices, the weight has {E} experts")
+    if groups.device != W.packed.device:
+        raise ValueError(f"groups must be on {W.packed.device}")
+
+
+def _ragged(A, W, groups, out, workspace, stream, flags, cols):
+    _check_groups(W, groups)
+    dev = W.packed.device
+    lda = _rows(A, "A", groups.M if flags & GATHER else groups.pairs, W.K, dev)
+    if out is None:
+        out = torch.empty((groups.pairs, cols), dtype=torch.bfloat16, device=dev)
+    ldc = _rows(out, "out", groups.pairs, cols, dev)
+    if workspace is None:
+        workspace = W.ragged_workspace(0, groups.topk)
+    wp, wn = _workspace(workspace, dev)
+    check(lib().vt_fp4_w4a16_gemm_ragged(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
+                                         groups.offsets.data_ptr(), groups.pairs, groups.topk,
+                                         flags, out.data_ptr(), ldc, wp, wn,
+                                         _raw_stream(stream, dev)), "vt_fp4_w4a16_gemm_ragged")
+    return out
+
+
+def w4a16_gemm_ragged(A: torch.Tensor, W, groups: RowGroups, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None, gather: bool = True,
+                      scatter: bool = False) -> torch.Tensor:
+    """Every grouped pair's row times its expert's weight, for any number of pairs: out
+    [pairs, N] (bf16).  gather: A holds one row per token, else one row per pair in group order.
+    scatter: pair p's output is row p, else the rows are in group order.  Rows of pairs in no
+    group are not written.  See vt_fp4_w4a16_gemm_ragged in include/vt_fp4.h."""
+    return _ragged(A, W, groups, out, workspace, stream,
+                   (GATHER if gather else 0) | (SCATTER if scatter else 0), W.N)
+
+
+def w4a16_gemm_ragged_silu_mul(A: torch.Tensor, W, groups: RowGroups,
+                               out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None, stream=None,
+                               gather: bool = True) -> torch.Tensor:
+    """The experts' gate and up products with silu(gate) * up as the output: out [pairs, I]
+    (bf16), rows in group order, for a weight from PackedWeight.grouped_gate_up."""
+    return _ragged(A, W, groups, out, workspace, stream, SILU_MUL | (GATHER if gather else 0),
+                   W.N // 2)
+
+
+def w4a16_gemm_ragged_combine(A: torch.Tensor, W, groups: RowGroups,
+                              out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts' second products (A [pairs, K], rows in group order) and each token's sum of
+    them by groups.weights: out [M, N] (bf16).  Pairs in no group count as zero."""
+    _check_groups(W, groups)
+    if groups.weights is None:
+        raise ValueError("the groups hold no weights")
+    dev = W.packed.device
+    lda = _rows(A, "A", groups.pairs, W.K, dev)
+    if out is None:
+        out = torch.empty((groups.M, W.N), dtype=torch.bfloat16, device=dev)
+    ldc = _rows(out, "out", groups.M, W.N, dev)
+    if workspace is None:
+        workspace = W.ragged_workspace(groups.M, groups.topk)
+    wp, wn = _workspace(workspace, dev)
+    check(lib().vt_fp4_w4a16_gemm_ragged_combine(
+        A.data_ptr(), lda, W.handle, groups.ids.data_ptr(), groups.order.data_ptr(),
+        groups.offsets.data_ptr(), groups.weights.data_ptr(), groups.M, groups.topk,
+        out.data_ptr(), ldc, wp, wn, _raw_stream(stream, dev)), "vt_fp4_w4a16_gemm_ragged_combine")
+    return out
+
+
+def moe_ffn(x: torch.Tensor, W_gate_up, W_down, groups: RowGroups, out: torch.Tensor | None = None,
+            h: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """A mixture-of-experts feed-forward block for any number of tokens: x [M, H] through the
+    chosen experts' gate_up (silu(gate) * up) and down weights, summed by the router's weights
+    into out [M, H].  h: optional bf16 [pairs, I] buffer of the inner activations; workspace:
+    W_down.ragged_workspace(M, topk)."""
+    if workspace is None:
+        workspace = W_down.ragged_workspace(groups.M, groups.topk)
+    h = w4a16_gemm_ragged_silu_mul(x, W_gate_up, groups, out=h, workspace=workspace, stream=stream)
+    return w4a16_gemm_ragged_combine(h, W_down, groups, out=out, workspace=workspace, stream=stream)
+
+
+class LoraAdapters:
+    """L low-rank adapters beside one projection: A bf16 [L, R, K], B bf16 [L, N, R], scale fp32
+    [L], ranks int32 [L] (the rank in use of each, at most R; None: R)."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                 ranks: torch.Tensor | None = None):
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A must be [L, R, K] and B [L, N, R]")
+        self.L, self.R, self.K = A.shape
+        self.N = B.shape[1]
+        dev = self.device = A.device
+        _need(A, "A", torch.bfloat16, tuple(A.shape), dev)
+        _need(B, "B", torch.bfloat16, (self.L, self.N, self.R), dev)
+        _need(scale, "scale", torch.float32, (self.L,), dev)
+        if ranks is not None:
+            _need(ranks, "ranks", torch.int32, (self.L,), dev)
+        self.A, self.B, self.scale, self.ranks = A, B, scale, ranks
+
+
+def lora_add(x: torch.Tensor, adapters: LoraAdapters, groups: RowGroups, y: torch.Tensor,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out = y + scale_a * B_a (A_a x) for every row's adapter a (groups of the rows' adapter
+    ids, topk = 1; rows in no group keep y).  y: the shared projection's output; out may be y."""
+    ad = adapters
+    if groups.topk != 1 or groups.E != ad.L:
+        raise ValueError("groups must hold one id of [0, L) per row")
+    dev = ad.device
+    if groups.device != dev:
+        raise ValueError(f"groups must be on {dev}")
+    M = groups.M
+    ldx, ldy = _rows(x, "x", M, ad.K, dev), _rows(y, "y", M, ad.N, dev)
+    if out is None:
+        out = torch.empty((M, ad.N), dtype=torch.bfloat16, device=dev)
+    ldo = _rows(out, "out", M, ad.N, dev)
+    check(lib().vt_fp4_lora_add(x.data_ptr(), M, ldx, ad.K, ad.A.data_ptr(), ad.B.data_ptr(),
+                                ad.scale.data_ptr(), 0 if ad.ranks is None else ad.ranks.data_ptr(),
+                                ad.L, ad.R, ad.N, groups.order.data_ptr(),
+                                groups.offsets.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo,
+                                _raw_stream(stream, dev)), "vt_fp4_lora_add")
+    return out

@@ -305,6 +305,111 @@ vt_status vt_fp4_workspace_status(void* workspace, vt_stream_t s, int* status);
 /* Host-side record of the last GEMM launched on W. */
 vt_status vt_fp4_stats(vt_fp4_handle W, vt_fp4_launch_info* info);
 
+/* ------------------------------------------- rows grouped by an index
+ *
+ * A mixture-of-experts block and low-rank adapters apply another weight to every row: an
+ * index (expert, adapter) chosen on the device says which.  The entry points below share one
+ * description of that choice:
+ *   ids     (device) int32 [pairs]: the index of each (token, slot) pair, pair p = m * topk + j
+ *           (topk = 1 where a row has one index); an id outside [0, E) puts the pair in no group.
+ *   order   (device) int32 [pairs]: the pairs in increasing index order, pairs of one index in
+ *           increasing pair order; the pairs in no group come last, in increasing order.
+ *   offsets (device) int32 [E + 1]: group e is order[offsets[e] .. offsets[e + 1]).
+ * Limits: 1 <= E <= 1024, 1 <= topk <= 32, fewer than 2^31 pairs.  Every result is
+ * deterministic and independent of the launch.  No counterpart on the pages beyond
+ * "re-verify 27B NVFP4 on the nvidia ModelOpt checkpoint" (PR #178), "Speed -- warp-shuffle
+ * MoE router top-k" (a top-k over the experts by a total order) and "Merge with origin/main"
+ * (the experts' products by the multi-expert route of the same GEMM). */
+
+/* Workspace of vt_fp4_group_rows and vt_fp4_moe_route for up to `pairs` pairs; 256-byte
+ * aligned, zeroed once by the caller, reusable afterwards in stream order. */
+vt_status vt_fp4_group_workspace_bytes(int64_t pairs, int64_t E, size_t* bytes);
+
+/* order and offsets from ids (see above).  pairs == 0 writes offsets (all 0) only. */
+vt_status vt_fp4_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_t* order,
+                            int32_t* offsets, void* workspace, size_t ws_bytes, vt_stream_t s);
+
+/* The router: per token the topk experts of largest score, their weights, and the grouping.
+ *   logits (device) [M][ld], ld >= E, fp32 (logits_bf16 == 0) or bf16 (1), aligned to its type.
+ *   scoring 0: the score is the logit and the weight softmax(logits)[e] over all experts;
+ *           1: the score and the weight are sigmoid(logit).
+ *   bias   (device, optional) fp32 [E]: added to the score for the choice alone (scoring 1).
+ *   renormalize: divide a token's weights by their sum; then every weight times `scale`.
+ *   ids (device) int32 [M][topk], weights (device) fp32 [M][topk], largest score first, equal
+ *   scores by the lowest index; a NaN score counts as larger than every number.  An expert
+ *   whose logit is -inf is never chosen: a token with fewer than topk others gets id -1 and
+ *   weight 0 in its last slots, and a token with none gets weight 0 in all of them.
+ * topk <= E.  M == 0 writes offsets (all 0) only. */
+vt_status vt_fp4_moe_route(const void* logits, int logits_bf16, int64_t M, int64_t ld, int64_t E,
+                           int64_t topk, int scoring, const float* bias, int renormalize,
+                           float scale, int32_t* ids, float* weights, int32_t* order,
+                           int32_t* offsets, void* workspace, size_t ws_bytes, vt_stream_t s);
+
+/* E experts' fused gate_up weights, each paired as vt_fp4_prepack_gate_up_paired does it, one
+ * after another as vt_fp4_prepack_grouped does: codes u8 [E][I][K/2], scales u8 [E][I][K/g]
+ * (device) and globals fp32 [E] (host) of gate and of up.  Size:
+ * vt_fp4_prepack_grouped_bytes with N = 2 * I.  unpack and dequant write each expert in
+ * gate-over-up row order. */
+vt_status vt_fp4_prepack_grouped_gate_up(const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                         const float* gate_globals, const uint8_t* up_codes,
+                                         const uint8_t* up_scales, const float* up_globals,
+                                         vt_fp4_format fmt, int64_t E, int64_t I, int64_t K,
+                                         void* packed_dst, size_t dst_bytes, vt_stream_t s,
+                                         vt_fp4_handle* out);
+
+/* Options of vt_fp4_w4a16_gemm_ragged. */
+enum {
+  VT_RAGGED_GATHER = 1,  /* A has one row per token: the i-th grouped pair p reads row p / topk;
+                            without it A has one row per grouped pair, row i */
+  VT_RAGGED_SCATTER = 2, /* the i-th grouped pair p writes row p of C; without it row i */
+  VT_RAGGED_SILU_MUL = 4 /* W from vt_fp4_prepack_grouped_gate_up: C = silu(gate) * up, I columns */
+};
+
+/* Workspace of the ragged products on W for up to M_max tokens of topk pairs each; 256-byte
+ * aligned, zeroed once by the caller, reusable afterwards in stream order.  Its first word is
+ * the status word (vt_fp4_workspace_status): VT_ERR_TIMEOUT after a wait that gave up, 6 after
+ * a call that skipped pairs because order or offsets hold values out of range. */
+vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t topk,
+                                        size_t* bytes);
+
+/* The products of ragged groups: for the i-th grouped pair, in group e,
+ *   C[row][n] = bf16( sum_k A[row'][k] * W_e[n][k] ),  fp32 accumulation,
+ * for any number of pairs, in one call; W a grouped weight of E experts (or a plain one, E = 1).
+ *   A  (device) bf16 [tokens or pairs][lda], 16-byte aligned, lda >= K, lda % 8 == 0.
+ *   C  (device) bf16 [pairs][ldc], ldc >= N (I with VT_RAGGED_SILU_MUL), 2-byte aligned; rows of
+ *      pairs in no group are not written.
+ * Asynchronous on `s`, no host synchronisation, capturable in a CUDA graph. */
+vt_status vt_fp4_w4a16_gemm_ragged(const void* A, int64_t lda, vt_fp4_handle W,
+                                   const int32_t* order, const int32_t* offsets, int64_t pairs,
+                                   int64_t topk, int flags, void* C, int64_t ldc, void* workspace,
+                                   size_t ws_bytes, vt_stream_t s);
+
+/* The experts' second products and each token's weighted sum of them:
+ *   C[m][n] = bf16( sum_j weights[m][j] * d[m][j][n] ),  d[m][j] = A[i] . W_e^T,
+ * with i the place of pair m * topk + j in order; the sum in fp32, in slot order.  A pair in no
+ * group (id outside [0, E)) counts as zero whatever its weight.
+ *   A  (device) bf16 [M * topk][lda], one row per grouped pair;  C (device) bf16 [M][ldc].
+ * Other arguments as above. */
+vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_handle W,
+                                           const int32_t* ids, const int32_t* order,
+                                           const int32_t* offsets, const float* weights,
+                                           int64_t M, int64_t topk, void* C, int64_t ldc,
+                                           void* workspace, size_t ws_bytes, vt_stream_t s);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[m][n] = bf16( y[m][n] + scale[a] * sum_r B_a[n][r] * sum_k A_a[r][k] * x[m][k] ),
+ * a = the group of row m (order and offsets over M rows, topk = 1, E = L adapters), both sums
+ * in fp32 over the adapter's own ranks[a] <= R; out[m] = y[m] for a row in no group.
+ *   x (device) bf16 [M][ldx], ldx >= K;  y, out (device) bf16 [M][ldy], [M][ldo], >= N;
+ *   A (device) bf16 [L][R][K];  B (device) bf16 [L][N][R];  scale (device) fp32 [L];
+ *   ranks (device, optional) int32 [L], clamped to [0, R]; NULL: R for each.
+ * out may be y itself (ldo == ldy).  Pointers need the alignment of their type.  1 <= R <= 128,
+ * 1 <= L <= 1024.  Asynchronous on `s`, capturable in a CUDA graph, deterministic. */
+vt_status vt_fp4_lora_add(const void* x, int64_t M, int64_t ldx, int64_t K, const void* A,
+                          const void* B, const float* scale, const int32_t* ranks, int64_t L,
+                          int64_t R, int64_t N, const int32_t* order, const int32_t* offsets,
+                          const void* y, int64_t ldy, void* out, int64_t ldo, vt_stream_t s);
+
 /* -------------------------------------------------------------------- W4A4 */
 
 /* The W4A4 arm: C = Q(A) . W^T with Q the activation quantiser below (activations in the
