@@ -368,7 +368,8 @@ enum {
 /* Workspace of the ragged products on W for up to M_max tokens of topk pairs each; 256-byte
  * aligned, zeroed once by the caller, reusable afterwards in stream order.  Its first word is
  * the status word (vt_fp4_workspace_status): VT_ERR_TIMEOUT after a wait that gave up, 6 after
- * a call that skipped pairs because order or offsets hold values out of range. */
+ * a call whose order or offsets held values out of range (such values are never used as
+ * addresses; the rows concerned are undefined). */
 vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t topk,
                                         size_t* bytes);
 
