@@ -12,38 +12,58 @@ namespace vt {
 
 namespace {
 
-// Roles of one persistent CTA per SM (15 warps):
+// Roles of one persistent CTA per SM:
 //   warp 0       weight producer: the packed 128 x 64 tiles of its items, one bulk copy per k step
-//   warp 1       token producer: up to 256 rows x 64 k of bf16 activations per k step by tiled
-//                TMA (128-byte swizzle), gathered four rows at a time where A is per token
+//   warp 1       token producer: up to TOK rows x 64 k of activations per k step by tiled TMA
+//                (128-byte swizzle), gathered four rows at a time where A is per token
 //   warp 2       TMEM, and one thread issuing tcgen05.mma: D[128 weight rows][tokens] (fp32,
 //                TMEM) += W . A^T with M = 128 and N = the tile's tokens rounded up to 16
-//   warps 3-10   dequantisers: packed tile -> bf16 K-major swizzled MMA operand
-//   warps 11-14  epilogue: lane = weight row, register = token
+//   kSets x 4    dequantisers: packed tile -> 16-bit K-major swizzled MMA operand; a set of four
+//   warps        warps takes every kSets-th k step, each warp 32 of its rows
+//   last 4 warps epilogue: lane = weight row, register = token
 // The weights are the MMA's M operand so that its cost follows the tokens a group really has
-// (N in steps of 16) and not a tile of 128 of them.  A weight value c * s (E2M1 times E4M3 or a
-// power of two) has at most 6 significant bits: exact in bf16, so the activations go to the
-// tensor core as they are, without a conversion pass.
+// (N in steps of 16) and not a tile of 128 of them.
+// Operands, per item: f16, with the activations converted by a pre-pass (A * 2^-p, one power of
+// two per row) and the weight value c * s one f16 multiply away from the E2M1 conversion; or
+// bf16, with the caller's activations as they are and three more operations per weight pair.
+// c * s has at most 6 significant bits and is exact in both; an expert whose E8M0 scales span
+// more exponents than f16 holds (`wide`) always takes bf16.
 // Items are (token tile, 128-row weight tile) pairs, weight tiles innermost; a group of n rows
-// is cut into ceil(n / 256) token tiles of nearly equal size.
-constexpr int kMaxTok = 256;
-constexpr int kDeqWarps = 8;
+// is cut into ceil(n / TOK) token tiles of nearly equal size.
+constexpr int kSets = 4;
+constexpr int kDeqWarps = kSets * 4;
 constexpr int kThreads = (3 + kDeqWarps + 4) * 32;
-constexpr int kNA = 3, kNB = 3, kNW = 13;    // ring depths: bf16 weights, tokens, packed weights
-constexpr int kABytes = 128 * 128, kBBytes = kMaxTok * 128;
+constexpr int kNA = 4;                       // ring of dequantised weight tiles
+constexpr int kABytes = 128 * 128;
 constexpr int kBoxRows = 16;                 // rows of one tiled activation load
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kOffB = kNA * kABytes;
-constexpr int kOffW = kOffB + kNB * kBBytes;
-__host__ __device__ constexpr int off_x(int fmt) { return kOffW + kNW * tile_bytes(fmt); }
-constexpr int kXBytes = 2 * 16 * 64 * 4;     // gate/up exchange of the SiLU epilogue
-constexpr int kNumBars = 2 * (kNA + kNB + kNW) + 4 + 1;
-__host__ __device__ constexpr int off_bar(int fmt) { return off_x(fmt) + kXBytes; }
-__host__ __device__ constexpr int off_tab(int fmt) { return off_bar(fmt) + (kNumBars + 1) * 8; }
-// prefix sums of the groups' token tiles, and their first rows
-inline int ragged_smem(int fmt, int E) { return off_tab(fmt) + 2 * (E + 1) * 4 + 1024; }
+constexpr int kXBytes = 2 * 2 * 8 * 64 * 4;  // gate/up exchange of the SiLU epilogue
 
-constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+// Shared-memory map (from a 1024-byte aligned base) for token tiles of up to TOK rows.
+template <int FMT, int TOK>
+struct Map {
+  static constexpr int NB = TOK == 256 ? 3 : 4;    // token stages
+  static constexpr int NW = TOK == 256 ? 10 : 14;  // packed weight stages
+  static constexpr int BBytes = TOK * 128;
+  static constexpr int OffB = kNA * kABytes;
+  static constexpr int OffW = OffB + NB * BBytes;
+  static constexpr int OffX = OffW + NW * tile_bytes(FMT);
+  static constexpr int OffBar = OffX + kXBytes;
+  static constexpr int NumBars = 2 * (kNA + NB + NW) + 4 + 1;
+  static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
+  // prefix sums of the groups' token tiles, and their first rows
+  static constexpr int smem(int E) { return OffTab + 2 * (E + 1) * 4 + 1024; }
+};
+static_assert(Map<FMT_NV, 256>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+static_assert(Map<FMT_NV, 128>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+
+constexpr uint32_t kIdescF16 = (1u << 4) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescBF16 = kIdescF16 | (1u << 7) | (1u << 10);
+
+struct RaggedParams {
+  RaggedLaunch L;
+  const float* rowscale;  // f16 operands: 2^p per row of A; NULL: bf16 operands
+};
 
 __device__ __forceinline__ float silu_f(float x) { return x / (1.0f + expf(-x)); }
 
@@ -59,6 +79,19 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
 // nothing crosses into the lower half).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2_m112(uint32_t h) {
   return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
+}
+
+// 16 columns of fp32 from TMEM.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 struct Item {
@@ -87,39 +120,108 @@ __device__ __forceinline__ Item item_at(int64_t it, const RaggedLaunch& L, const
   return q;
 }
 
-template <int FMT, bool GATHER, bool SILU>
+__device__ __forceinline__ const PackedHeader* header_of(const RaggedLaunch& L, int e) {
+  return reinterpret_cast<const PackedHeader*>(reinterpret_cast<const uint8_t*>(L.packed) +
+                                               e * L.expert_bytes);
+}
+
+// One row block (16 rows x 64 k; this lane: rows g and g + 8, 16 k each) of a packed tile to
+// 16-bit pairs in k order: og of row g, o8 of row g + 8.
+enum { kF16 = 0, kBF16 = 1, kWide = 2 };
+template <int FMT, int OP>
+__device__ __forceinline__ void dequant_block(const int4& cw, uint32_t sc, uint32_t (&og)[8],
+                                              uint32_t (&o8)[8]) {
+  const uint32_t words[4] = {(uint32_t)cw.x, (uint32_t)cw.y, (uint32_t)cw.z, (uint32_t)cw.w};
+  if constexpr (OP == kWide) {
+    // raw E8M0 bytes: c * 2^(e - 127) by fp32, exact in bf16 (subnormals included)
+    const float wg = e8m0_to_f32(sc & 0xFFu), w8 = e8m0_to_f32((sc >> 8) & 0xFFu);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t c4[4], o4[4];
+      e2m1x8_to_f16x8(words[q], c4[0], c4[1], c4[2], c4[3]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const __half2 hc = *reinterpret_cast<const __half2*>(&c4[b]);
+        const float s = (b & 1) ? w8 : wg;
+        o4[b] = as_u32(__floats2bfloat162_rn(__low2float(hc) * s, __high2float(hc) * s));
+      }
+      og[2 * q] = o4[0];
+      og[2 * q + 1] = o4[2];
+      o8[2 * q] = o4[1];
+      o8[2 * q + 1] = o4[3];
+    }
+  } else {
+    const uint32_t s2 = FMT == FMT_NV ? e4m3x2_to_f16x2(sc & 0xFFFFu) : mxenc2_to_f16x2(sc & 0xFFFFu);
+    if constexpr (OP == kF16) {
+      const uint32_t sg = bcast_lo(s2), s8 = bcast_hi(s2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r0, r1, r2, r3;
+        e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
+        og[2 * q] = hmul2_u32(r0, sg);
+        o8[2 * q] = hmul2_u32(r1, s8);
+        og[2 * q + 1] = hmul2_u32(r2, sg);
+        o8[2 * q + 1] = hmul2_u32(r3, s8);
+      }
+    } else {
+      const __half2 sh = *reinterpret_cast<const __half2*>(&s2);
+      const float fg = __low2float(sh) * 0x1p112f, f8 = __high2float(sh) * 0x1p112f;
+      const __nv_bfloat162 bg = __floats2bfloat162_rn(fg, fg), b8 = __floats2bfloat162_rn(f8, f8);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r0, r1, r2, r3;
+        e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
+        og[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r0)), bg));
+        o8[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r1)), b8));
+        og[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r2)), bg));
+        o8[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r3)), b8));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+template <int FMT, bool SILU, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_ragged(const __grid_constant__ CUtensorMap tmA, const RaggedLaunch L) {
-  constexpr int TB = tile_bytes(FMT);
+    k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmP,
+             const RaggedParams p) {
+  using S = Map<FMT, TOK>;
+  constexpr int TB = tile_bytes(FMT), NB = S::NB, NW = S::NW;
+  const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u - raw_u);
-  const uint32_t sA = base_u, sB = base_u + kOffB, sW = base_u + kOffW;
-  float* s_x = reinterpret_cast<float*>(base + off_x(FMT));
-  const uint32_t bars = base_u + off_bar(FMT);
+  const uint32_t sA = base_u, sB = base_u + S::OffB, sW = base_u + S::OffW;
+  float* s_x = reinterpret_cast<float*>(base + S::OffX);
+  const uint32_t bars = base_u + S::OffBar;
   const uint32_t a_full = bars, a_empty = a_full + 8 * kNA;
-  const uint32_t b_full = a_empty + 8 * kNA, b_empty = b_full + 8 * kNB;
-  const uint32_t w_full = b_empty + 8 * kNB, w_empty = w_full + 8 * kNW;
-  const uint32_t acc_full = w_empty + 8 * kNW, acc_empty = acc_full + 16, drain = acc_empty + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + off_bar(FMT) + kNumBars * 8);
+  const uint32_t b_full = a_empty + 8 * kNA, b_empty = b_full + 8 * NB;
+  const uint32_t w_full = b_empty + 8 * NB, w_empty = w_full + 8 * NW;
+  const uint32_t acc_full = w_empty + 8 * NW, acc_empty = acc_full + 16, drain = acc_empty + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OffBar + S::NumBars * 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* tstart = reinterpret_cast<int*>(base + off_tab(FMT));
+  int* tstart = reinterpret_cast<int*>(base + S::OffTab);
   int* first = tstart + L.E + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kNA; ++s) {
-      mbar_init(a_full + 8 * s, kDeqWarps);
+      mbar_init(a_full + 8 * s, 4);
       mbar_init(a_empty + 8 * s, 1);
     }
-    for (int s = 0; s < kNB; ++s) {
+    for (int s = 0; s < NB; ++s) {
       mbar_init(b_full + 8 * s, 1);
       mbar_init(b_empty + 8 * s, 1);
     }
-    for (int s = 0; s < kNW; ++s) {
+    for (int s = 0; s < NW; ++s) {
       mbar_init(w_full + 8 * s, 1);
-      mbar_init(w_empty + 8 * s, kDeqWarps);
+      mbar_init(w_empty + 8 * s, 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full + 8 * s, 1);
@@ -128,14 +230,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     *abort = 0;
   }
-  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), 2 * TOK);
   fence_mbar_init();
-  // everything above needs nothing of the kernel before this one
-  pdl_wait();
+  // The pre-pass lets this grid start only after its own wait for the kernels before it, so
+  // with a pre-pass the groups may be read (and the weights requested) at once; what the
+  // pre-pass writes is waited for by the roles that read it.
+  if (!p.rowscale) pdl_wait();
   pdl_launch_dependents();
   bool bad = false;  // offsets out of order or out of range
   for (int e = threadIdx.x; e <= L.E; e += kThreads) {
-    const int64_t v = L.offsets[e], c = v < 0 ? 0 : (v > L.pairs ? L.pairs : v);
+    const int64_t v = __ldcg(L.offsets + e), c = v < 0 ? 0 : (v > L.pairs ? L.pairs : v);
     bad |= v != c;
     first[e] = (int)c;
   }
@@ -146,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = lane * per; e < (lane + 1) * per && e < L.E; ++e) {
       const int n = first[e + 1] - first[e];
       bad |= n < 0;
-      sum += n > 0 ? (n + kMaxTok - 1) / kMaxTok : 0;
+      sum += n > 0 ? (n + TOK - 1) / TOK : 0;
     }
     int run = sum;
 #pragma unroll
@@ -158,11 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = lane * per; e < (lane + 1) * per && e < L.E; ++e) {
       tstart[e] = run;
       const int n = first[e + 1] - first[e];
-      run += n > 0 ? (n + kMaxTok - 1) / kMaxTok : 0;
+      run += n > 0 ? (n + TOK - 1) / TOK : 0;
     }
     if (lane == 31) tstart[L.E] = run;
-    if (blockIdx.x == 0 && bad) atomicExch(L.status, 6);
   }
+  if (blockIdx.x == 0 && bad) atomicExch(L.status, 6);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -186,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(w_full + 8 * iw, TB);
           bulk_g2s(sW + iw * TB, src + (int64_t)kt * TB, TB, w_full + 8 * iw, pol);
           ++issued;
-          if (++iw == kNW) { iw = 0; pw ^= 1u; }
+          if (++iw == NW) { iw = 0; pw ^= 1u; }
         }
       }
       if (!ok) {  // let the copies in flight land before shared memory is released
         atomicExch(L.status, 5);
-        for (int k = 0; k < kNW && k < issued; ++k) {
-          iw = iw == 0 ? kNW - 1 : iw - 1;
-          if (iw == kNW - 1) pw ^= 1u;
+        for (int k = 0; k < NW && k < issued; ++k) {
+          iw = iw == 0 ? NW - 1 : iw - 1;
+          if (iw == NW - 1) pw ^= 1u;
           const uint64_t t0 = globaltimer_ns();
           while (!mbar_try_wait(w_full + 8 * iw, pw) && globaltimer_ns() - t0 < kWaitNs) {}
         }
@@ -205,21 +309,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ib = 0, pb = 0;
     int issued = 0;
     bool ok = true;
+    pdl_wait();
     for (int64_t it = blockIdx.x; ok && it < items; it += G) {
       const Item q = item_at(it, L, tstart, first);
       const int n16 = (q.n + 15) & ~15;
+      const CUtensorMap* tm = p.rowscale && !(FMT == FMT_MX && header_of(L, q.e)->wide) ? &tmP : &tmA;
       // gathered: lane l fetches rows 4l .. 4l+3 and 128 + 4l ..; past the tile's tokens the
       // last one again (its products are not stored)
-      int4 y[2];
-      if constexpr (GATHER) {
-        for (int h = 0; h < 2; ++h) {
+      int4 y[TOK / 128];
+      if (L.gather) {
+#pragma unroll
+        for (int h = 0; h < TOK / 128; ++h) {
           int r[4];
           for (int c = 0; c < 4; ++c) {
             const int i = h * 128 + lane * 4 + c;
-            const int p = __ldg(L.order + q.i0 + (i < q.n ? i : q.n - 1));
-            const bool in = p >= 0 && p < L.pairs;
+            const int pr = __ldcg(L.order + q.i0 + (i < q.n ? i : q.n - 1));
+            const bool in = pr >= 0 && pr < L.pairs;
             if (!in) atomicExch(L.status, 6);
-            r[c] = in ? p / L.topk : 0;
+            r[c] = in ? pr / L.topk : 0;
           }
           y[h] = make_int4(r[0], r[1], r[2], r[3]);
         }
@@ -228,27 +335,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = lane != 0 || pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const uint32_t dst = sB + ib * kBBytes, bar = b_full + 8 * ib;
+        const uint32_t dst = sB + ib * S::BBytes, bar = b_full + 8 * ib;
         if (lane == 0) mbar_expect_tx(bar, (uint32_t)n16 * 128u);
         __syncwarp();
-        if constexpr (GATHER) {
-          if (lane * 4 < n16) tma_gather4(dst + lane * 512, &tmA, kt * kTileK, y[0], bar, pol);
-          if (128 + lane * 4 < n16)
-            tma_gather4(dst + 16384 + lane * 512, &tmA, kt * kTileK, y[1], bar, pol);
+        if (L.gather) {
+#pragma unroll
+          for (int h = 0; h < TOK / 128; ++h)
+            if (h * 128 + lane * 4 < n16)
+              tma_gather4(dst + h * 16384 + lane * 512, tm, kt * kTileK, y[h], bar, pol);
         } else {
           if (lane * kBoxRows < n16)
-            tma_load_2d(dst + lane * kBoxRows * 128, &tmA, kt * kTileK, (int)q.i0 + lane * kBoxRows,
+            tma_load_2d(dst + lane * kBoxRows * 128, tm, kt * kTileK, (int)q.i0 + lane * kBoxRows,
                         bar, pol);
         }
         ++issued;
-        if (++ib == kNB) { ib = 0; pb ^= 1u; }
+        if (++ib == NB) { ib = 0; pb ^= 1u; }
       }
     }
     if (!ok && lane == 0) {
       atomicExch(L.status, 5);
-      for (int k = 0; k < kNB && k < issued; ++k) {
-        ib = ib == 0 ? kNB - 1 : ib - 1;
-        if (ib == kNB - 1) pb ^= 1u;
+      for (int k = 0; k < NB && k < issued; ++k) {
+        ib = ib == 0 ? NB - 1 : ib - 1;
+        if (ib == NB - 1) pb ^= 1u;
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(b_full + 8 * ib, pb) && globaltimer_ns() - t0 < kWaitNs) {}
       }
@@ -261,22 +369,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int64_t it = blockIdx.x; ok && it < items; it += G) {
         const Item q = item_at(it, L, tstart, first);
-        const uint32_t idesc = kIdescBase | ((uint32_t)((q.n + 15) >> 4) << 18);
-        const uint32_t d = tmem + ic * kMaxTok;
+        const bool f16 = p.rowscale && !(FMT == FMT_MX && header_of(L, q.e)->wide);
+        const uint32_t idesc = (f16 ? kIdescF16 : kIdescBF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
+        const uint32_t d = tmem + ic * TOK;
         if (!(ok = pf_wait(acc_empty + 8 * ic, pc ^ 1u, abort, kWaitNs))) break;
         tc_fence_after();
         for (int kt = 0; kt < KT; ++kt) {
           if (!(ok = pf_wait(b_full + 8 * ib, pb, abort, kWaitNs))) break;
           if (!(ok = pf_wait(a_full + 8 * ia, pa, abort, kWaitNs))) break;
           tc_fence_after();
-          const uint64_t ad = desc_sw128(sA + ia * kABytes), bd = desc_sw128(sB + ib * kBBytes);
+          const uint64_t ad = desc_sw128(sA + ia * kABytes), bd = desc_sw128(sB + ib * S::BBytes);
 #pragma unroll
           for (int kk = 0; kk < kTileK / 16; ++kk)  // +32 bytes per 16-element k step
             mma_f16(d, ad + 2 * kk, bd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
           mma_commit(a_empty + 8 * ia);
           mma_commit(b_empty + 8 * ib);
           if (++ia == kNA) { ia = 0; pa ^= 1u; }
-          if (++ib == kNB) { ib = 0; pb ^= 1u; }
+          if (++ib == NB) { ib = 0; pb ^= 1u; }
         }
         if (!ok) break;
         mma_commit(acc_full + 8 * ic);
@@ -289,76 +398,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 3 + kDeqWarps) {
     // ------------------------------------------------------------- dequantisers
-    // Warp d owns row block d: lane (g, t) holds rows 16d + g and 16d + g + 8 for physical k
-    // [16t, 16t + 16) of the k tile (one NVFP4 scale each).
-    const int d = warp - 3, g = lane >> 2, t = lane & 3;
-    const int soff = scale_offset(FMT, d, g, t);
-    const int row = 16 * d + g;  // row & 7 == (row + 8) & 7 == g
+    // Set `set` takes the CTA's k steps set, set + kSets, ...; warp jp of the set the row blocks
+    // 2jp and 2jp + 1 (32 rows), whose four scale bytes per lane are one word.
+    const int set = (warp - 3) >> 2, jp = (warp - 3) & 3, g = lane >> 2, t = lane & 3;
+    const uint32_t soff = (uint32_t)scale_offset(FMT, 2 * jp, g, t);
+    const uint32_t roff = (uint32_t)(32 * jp + g) * 128;  // row & 7 == g for all four rows
     const uint32_t c0 = (uint32_t)(((2 * t) ^ g) << 4), c1 = (uint32_t)(((2 * t + 1) ^ g) << 4);
-    uint32_t iw = 0, pw = 0, ia = 0, pa = 0;
+    uint32_t iw = set, pw = 0, ia = set, pa = 0;
+    int kt = set;
     bool ok = true;
-    for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-      bool wide = false;
-      if constexpr (FMT == FMT_MX) {
-        const Item q = item_at(it, L, tstart, first);
-        wide = reinterpret_cast<const PackedHeader*>(reinterpret_cast<const uint8_t*>(L.packed) +
-                                                     q.e * L.expert_bytes)->wide != 0;
+    int64_t it = blockIdx.x;
+    while (it < items && kt >= KT) { kt -= KT; it += G; }
+    int op = p.rowscale ? kF16 : kBF16;
+    int64_t of = -1;  // the item `op` is of
+    while (it < items) {
+      if (FMT == FMT_MX && of != it) {
+        of = it;
+        op = header_of(L, item_at(it, L, tstart, first).e)->wide ? kWide : p.rowscale ? kF16 : kBF16;
       }
-      for (int kt = 0; kt < KT; ++kt) {
-        if (!(ok = pf_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
-        const uint32_t tb = sW + iw * TB;
-        const int4 cw = ld_shared_v4(tb + d * 512 + lane * 16);
-        const uint32_t sc = ld_shared_u16(tb + soff);
-        const uint32_t words[4] = {(uint32_t)cw.x, (uint32_t)cw.y, (uint32_t)cw.z, (uint32_t)cw.w};
-        uint32_t og[8], o8[8];  // rows g and g + 8, k order, bf16x2
-        if (FMT == FMT_MX && wide) {
-          // raw E8M0 bytes: c * 2^(e - 127) by fp32, exact in bf16 (subnormals included)
-          const float wg = e8m0_to_f32(sc & 0xFFu), w8 = e8m0_to_f32((sc >> 8) & 0xFFu);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t c4[4], o4[4];
-            e2m1x8_to_f16x8(words[q], c4[0], c4[1], c4[2], c4[3]);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const __half2 hc = *reinterpret_cast<const __half2*>(&c4[b]);
-              const float s = (b & 1) ? w8 : wg;
-              o4[b] = as_u32(__floats2bfloat162_rn(__low2float(hc) * s, __high2float(hc) * s));
-            }
-            og[2 * q] = o4[0];
-            og[2 * q + 1] = o4[2];
-            o8[2 * q] = o4[1];
-            o8[2 * q + 1] = o4[3];
-          }
-        } else {
-          const uint32_t s2 = FMT == FMT_NV ? e4m3x2_to_f16x2(sc) : mxenc2_to_f16x2(sc);
-          const __half2 sh = *reinterpret_cast<const __half2*>(&s2);
-          const float fg = __low2float(sh) * 0x1p112f, f8 = __high2float(sh) * 0x1p112f;
-          const __nv_bfloat162 bg = __floats2bfloat162_rn(fg, fg), b8 = __floats2bfloat162_rn(f8, f8);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t r0, r1, r2, r3;
-            e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
-            og[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r0)), bg));
-            o8[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r1)), b8));
-            og[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r2)), bg));
-            o8[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r3)), b8));
-          }
-        }
-        // every lane has used what it loaded: only now may the next copy overwrite the stage
-        __syncwarp();
-        if (lane == 0) mbar_arrive(w_empty + 8 * iw);
-        if (++iw == kNW) { iw = 0; pw ^= 1u; }
-        if (!(ok = pf_wait(a_empty + 8 * ia, pa ^ 1u, abort, kWaitNs))) break;
-        const uint32_t rg = sA + ia * kABytes + row * 128, r8 = rg + 8 * 128;
-        st_shared_v4(rg + c0, og[0], og[1], og[2], og[3]);
-        st_shared_v4(rg + c1, og[4], og[5], og[6], og[7]);
-        st_shared_v4(r8 + c0, o8[0], o8[1], o8[2], o8[3]);
-        st_shared_v4(r8 + c1, o8[4], o8[5], o8[6], o8[7]);
-        fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + 8 * ia);
-        if (++ia == kNA) { ia = 0; pa ^= 1u; }
+      if (!(ok = pf_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
+      const uint32_t tb = sW + iw * TB;
+      const int4 cw0 = ld_shared_v4(tb + (2 * jp) * 512 + lane * 16);
+      const int4 cw1 = ld_shared_v4(tb + (2 * jp + 1) * 512 + lane * 16);
+      const uint32_t sc = ld_shared_u32(tb + soff);
+      uint32_t og[2][8], o8[2][8];  // rows g and g + 8 of both row blocks
+      if (op == kF16) {
+        dequant_block<FMT, kF16>(cw0, sc, og[0], o8[0]);
+        dequant_block<FMT, kF16>(cw1, sc >> 16, og[1], o8[1]);
+      } else if (FMT == FMT_MX && op == kWide) {
+        dequant_block<FMT, kWide>(cw0, sc, og[0], o8[0]);
+        dequant_block<FMT, kWide>(cw1, sc >> 16, og[1], o8[1]);
+      } else {
+        dequant_block<FMT, kBF16>(cw0, sc, og[0], o8[0]);
+        dequant_block<FMT, kBF16>(cw1, sc >> 16, og[1], o8[1]);
       }
+      // every lane has used what it loaded: only now may the next copy overwrite the stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_empty + 8 * iw);
+      if (!(ok = pf_wait(a_empty + 8 * ia, pa ^ 1u, abort, kWaitNs))) break;
+      const uint32_t at = sA + ia * kABytes + roff;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        st_shared_v4(at + b * 2048 + c0, og[b][0], og[b][1], og[b][2], og[b][3]);
+        st_shared_v4(at + b * 2048 + c1, og[b][4], og[b][5], og[b][6], og[b][7]);
+        st_shared_v4(at + b * 2048 + 1024 + c0, o8[b][0], o8[b][1], o8[b][2], o8[b][3]);
+        st_shared_v4(at + b * 2048 + 1024 + c1, o8[b][4], o8[b][5], o8[b][6], o8[b][7]);
+      }
+      fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full + 8 * ia);
+      if ((iw += kSets) >= NW) { iw -= NW; pw ^= 1u; }
+      if ((ia += kSets) >= kNA) { ia -= kNA; pa ^= 1u; }
+      kt += kSets;
+      while (it < items && kt >= KT) { kt -= KT; it += G; }
     }
     if (!ok && lane == 0) atomicExch(L.status, 5);
   } else {
@@ -368,63 +460,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
     uint32_t ic = 0, pc = 0;
     bool ok = true;
+    pdl_wait();
     for (int64_t it = blockIdx.x; ok && it < items; it += G) {
       const Item q = item_at(it, L, tstart, first);
-      const PackedHeader* hdr = reinterpret_cast<const PackedHeader*>(
-          reinterpret_cast<const uint8_t*>(L.packed) + q.e * L.expert_bytes);
+      const PackedHeader* hdr = header_of(L, q.e);
+      const bool scaled = p.rowscale && !(FMT == FMT_MX && hdr->wide);
+      const int64_t n = SILU ? (int64_t)q.rt * 64 + (r & 63)
+                             : packed_to_row(L.layout, (int64_t)q.rt * kTileRows + r, L.N, L.seg_split);
+      const bool up = SILU && qd >= 2;
+      const bool live = SILU ? n < L.seg_split : n >= 0;
+      const float f = hdr->factor[SILU ? (up ? 1 : 0) : (n >= L.seg_split ? 1 : 0)];
       if (!(ok = pf_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
       tc_fence_after();
-      const uint32_t ta = tmem + ic * kMaxTok + ((uint32_t)(qd * 32) << 16);
-      if constexpr (SILU) {
-        // lanes 0-63 hold gate rows, 64-127 the matching up rows: for every 32 tokens the gate
-        // warps finish the first 16 and the up warps the others, trading the halves they lack
-        const float f = hdr->factor[qd >> 1];
-        const int64_t col = (int64_t)q.rt * 64 + (r & 63);
-        const bool live = col < L.seg_split, up = qd >= 2;
-        for (int c = 0; c * 32 < q.n; ++c) {
-          uint32_t v[32];
-          tmem_ld32(ta + c * 32, v);
-          const int64_t i = q.i0 + c * 32 + lane;
-          int64_t out = i;
-          if (L.scatter && c * 32 + lane < q.n) out = L.order[i];
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // the halves of the chunk before are read
-          float* mine = s_x + (up ? 0 : 16 * 64);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            mine[j * 64 + (r & 63)] = __uint_as_float(up ? v[j] : v[16 + j]) * f;
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          const float* other = s_x + (up ? 16 * 64 : 0);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int tok = c * 32 + (up ? 16 : 0) + j;
-            const int64_t ro = __shfl_sync(0xffffffffu, out, (up ? 16 : 0) + j);
-            const float x = __uint_as_float(up ? v[16 + j] : v[j]) * f;
-            const float z = other[j * 64 + (r & 63)];
-            const float h = up ? silu_f(z) * x : silu_f(x) * z;
-            if (tok < q.n && live && ro >= 0 && ro < L.pairs)
-              C[ro * L.ldc + col] = __float2bfloat16_rn(h);
+      const uint32_t ta = tmem + ic * TOK + ((uint32_t)(qd * 32) << 16);
+      for (int c = 0; c * 16 < q.n; ++c) {
+        uint32_t v[16];
+        tmem_ld16(ta + c * 16, v);
+        // lane j < 16: the output row and the activation scale of token j of the chunk
+        int64_t out = -1;
+        float rs = 1.0f;
+        const int64_t i = q.i0 + c * 16 + lane;
+        if (lane < 16 && c * 16 + lane < q.n) {
+          out = i;
+          if (L.scatter || (scaled && L.gather)) {
+            const int64_t pr = __ldcg(L.order + i);
+            const bool in = pr >= 0 && pr < L.pairs;
+            if (!in) atomicExch(L.status, 6);
+            if (L.scatter) out = in ? pr : -1;
+            if (scaled) rs = in ? __ldcg(p.rowscale + (L.gather ? pr / L.topk : i)) : 0.0f;
+          } else if (scaled) {
+            rs = __ldcg(p.rowscale + i);
           }
         }
-      } else {
-        const int64_t n = packed_to_row(L.layout, (int64_t)q.rt * kTileRows + r, L.N, L.seg_split);
-        const float f = hdr->factor[n >= L.seg_split ? 1 : 0];
-        for (int c = 0; c * 32 < q.n; ++c) {
-          uint32_t v[32];
-          tmem_ld32(ta + c * 32, v);
-          const int64_t i = q.i0 + c * 32 + lane;
-          int64_t out = i;
-          if (L.scatter && c * 32 + lane < q.n) {
-            out = L.order[i];
-            if ((out < 0 || out >= L.pairs) && q.rt == 0) atomicExch(L.status, 6);
-          }
+        if constexpr (SILU) {
+          // lanes 0-63 hold gate rows, 64-127 the matching up rows: of every 16 tokens the
+          // gate warps finish the first 8 and the up warps the others, trading what they lack
+          float* buf = s_x + (c & 1) * 1024;
+          float* mine = buf + (up ? 0 : 512);
+          float x[8];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < 8; ++j) {
+            const float a = __uint_as_float(v[j]), b = __uint_as_float(v[8 + j]);
+            const float ra = __shfl_sync(0xffffffffu, rs, j), rb = __shfl_sync(0xffffffffu, rs, 8 + j);
+            mine[j * 64 + (r & 63)] = up ? a * ra * f : b * rb * f;
+            x[j] = up ? b * rb * f : a * ra * f;
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          const float* other = buf + (up ? 512 : 0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int64_t ro = __shfl_sync(0xffffffffu, out, (up ? 8 : 0) + j);
+            const float z = other[j * 64 + (r & 63)];
+            const float h = up ? silu_f(z) * x[j] : silu_f(x[j]) * z;
+            if (live && ro >= 0) C[ro * L.ldc + n] = __float2bfloat16_rn(h);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
             const int64_t ro = __shfl_sync(0xffffffffu, out, j);
-            if (c * 32 + j < q.n && n >= 0 && ro >= 0 && ro < L.pairs)
-              C[ro * L.ldc + n] = __float2bfloat16_rn(__uint_as_float(v[j]) * f);
+            const float y = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, rs, j) * f;
+            if (live && ro >= 0) C[ro * L.ldc + n] = __float2bfloat16_rn(y);
           }
         }
       }
+      if constexpr (SILU) asm volatile("bar.sync 1, 128;" ::: "memory");  // the exchange is free again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + 8 * ic);
@@ -437,95 +536,190 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 2 * TOK);
   }
 }
 
-// Weighted sum of each token's pairs, in slot order, in fp32.
-__global__ void __launch_bounds__(256) k_combine(const __nv_bfloat16* D, int64_t M, int topk,
-                                                 int64_t N, int64_t ldd, const int32_t* ids, int E,
-                                                 const float* weights, __nv_bfloat16* out,
-                                                 int64_t ldo) {
-  const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  float acc = 0.0f;
+// Activation pre-pass of the f16 operands: A'[r][k] = A[r][k] * 2^-p in f16, p the power of two
+// of the row's largest magnitude (act_pow2), rowscale[r] = 2^p.  One block per row.
+constexpr int kPrepThreads = 128;
+__global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const __nv_bfloat16* __restrict__ A,
+                                                              int64_t lda, int64_t K, int64_t ldp,
+                                                              __half* __restrict__ Ap,
+                                                              float* __restrict__ rowscale) {
+  __shared__ int s_max[kPrepThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t m = blockIdx.x;
+  const uint4* row = reinterpret_cast<const uint4*>(A + m * lda);
+  const int64_t ng = K / 8;
+  int mx = 0;
+  for (int64_t i = threadIdx.x; i < ng; i += kPrepThreads) {
+    const uint4 v = row[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    mx = max(mx, act_maxmag8(w));
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPrepThreads / 32; ++i) mx = max(mx, s_max[i]);
+  const int p = act_pow2(mx);
+  uint4* dst = reinterpret_cast<uint4*>(Ap + m * ldp);
+  for (int64_t i = threadIdx.x; i < ng; i += kPrepThreads) {
+    const uint4 v = row[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    dst[i] = act_granule_f16(w, p);
+  }
+  if (threadIdx.x == 0) rowscale[m] = pow2f(p);
+}
+
+// Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.
+constexpr int kCombineThreads = 256;
+__global__ void __launch_bounds__(kCombineThreads) k_combine(
+    const __nv_bfloat16* __restrict__ D, int64_t M, int topk, int64_t N, int64_t ldd,
+    const int32_t* __restrict__ ids, int E, const float* __restrict__ weights,
+    __nv_bfloat16* __restrict__ out, int64_t ldo, int vec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t per = (N + 7) / 8, i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
+  if (i >= M * per) return;
+  const int64_t m = i / per, n0 = (i - m * per) * 8;
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
   for (int j = 0; j < topk; ++j) {
     const int64_t p = m * topk + j;
-    if (ids[p] >= 0 && ids[p] < E) acc += weights[p] * __bfloat162float(D[p * ldd + n]);
+    const int id = ids[p];
+    if (id < 0 || id >= E) continue;
+    const float w = weights[p];
+    // D's rows are padded to 8 columns (what lies in the padding is not stored)
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(D + p * ldd + n0));
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      acc[2 * c] += w * __uint_as_float(x[c] << 16);
+      acc[2 * c + 1] += w * __uint_as_float(x[c] & 0xFFFF0000u);
+    }
   }
-  out[m * ldo + n] = __float2bfloat16_rn(acc);
+  __nv_bfloat16* dst = out + m * ldo + n0;
+  if (vec && n0 + 8 <= N) {
+    uint4 o;
+    o.x = as_u32(__floats2bfloat162_rn(acc[0], acc[1]));
+    o.y = as_u32(__floats2bfloat162_rn(acc[2], acc[3]));
+    o.z = as_u32(__floats2bfloat162_rn(acc[4], acc[5]));
+    o.w = as_u32(__floats2bfloat162_rn(acc[6], acc[7]));
+    *reinterpret_cast<uint4*>(dst) = o;
+  } else {
+    for (int c = 0; c < 8 && n0 + c < N; ++c) dst[c] = __float2bfloat16_rn(acc[c]);
+  }
 }
 
 }  // namespace
 
 namespace {
 
-template <int FMT, bool GATHER, bool SILU>
-cudaError_t launch_main(const CUtensorMap& tm, const RaggedLaunch& L, int grid, cudaStream_t s) {
+cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* at, dim3 grid, int threads, int smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int FMT, bool SILU, int TOK>
+cudaError_t launch_main(const CUtensorMap& tmA, const CUtensorMap& tmP, const RaggedParams& p,
+                        int grid, cudaStream_t s) {
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_ragged<FMT, GATHER, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ragged_smem(FMT, kMaxGroups));
+    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Map<FMT, TOK>::smem(kMaxGroups));
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)ragged_smem(FMT, L.E);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, GATHER, SILU>, tm, L);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(&at, dim3((unsigned)grid), kThreads, Map<FMT, TOK>::smem(p.L.E), s);
+  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, TOK>, tmA, tmP, p);
 }
 
-template <int FMT>
-cudaError_t launch_fmt(const CUtensorMap& tm, const RaggedLaunch& L, int grid, cudaStream_t s) {
-  if (L.gather) return L.silu ? launch_main<FMT, true, true>(tm, L, grid, s)
-                              : launch_main<FMT, true, false>(tm, L, grid, s);
-  return L.silu ? launch_main<FMT, false, true>(tm, L, grid, s)
-                : launch_main<FMT, false, false>(tm, L, grid, s);
+template <int TOK>
+cudaError_t launch_tok(const CUtensorMap& tmA, const CUtensorMap& tmP, const RaggedParams& p,
+                       cudaStream_t s) {
+  const RaggedLaunch& L = p.L;
+  // at most one partial token tile per group in use
+  const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
+  const int64_t most = (groups + L.pairs / TOK) * L.RT;
+  const int grid = (int)(sm_count() < most ? sm_count() : most);
+  if (L.fmt == FMT_NV) return L.silu ? launch_main<FMT_NV, true, TOK>(tmA, tmP, p, grid, s)
+                                     : launch_main<FMT_NV, false, TOK>(tmA, tmP, p, grid, s);
+  return L.silu ? launch_main<FMT_MX, true, TOK>(tmA, tmP, p, grid, s)
+                : launch_main<FMT_MX, false, TOK>(tmA, tmP, p, grid, s);
 }
+
+inline int64_t ld_f16(int64_t KT) { return KT * kTileK; }
+
+bool use_f16(int64_t pairs, int64_t E) { return pairs <= 192 * E; }
 
 }  // namespace
+
+size_t ragged_act_bytes(int64_t pairs, int64_t E, int64_t KT) {
+  const int64_t most = 192 * E, rows = pairs < most ? pairs : most;
+  return (size_t)((rows * 4 + 255) / 256 * 256 + rows * ld_f16(KT) * 2);
+}
 
 cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  // A as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
-  CUtensorMap tm;
+  // the activations as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
   const int64_t rows = L.gather ? L.pairs / L.topk : L.pairs;
-  const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)L.lda * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)(L.gather ? 1 : kBoxRows)};
-  const cuuint32_t estr[2] = {1, 1};
-  if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(L.A), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  // at most one partial token tile per group in use
-  const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
-  const int64_t most = (groups + L.pairs / kMaxTok) * L.RT;
-  int64_t grid = sm_count();
-  if (grid > most) grid = most;
-  return L.fmt == FMT_NV ? launch_fmt<FMT_NV>(tm, L, (int)grid, s)
-                         : launch_fmt<FMT_MX>(tm, L, (int)grid, s);
+  auto encode = [&](CUtensorMap* tm, CUtensorMapDataType type, const void* at, int64_t ld) {
+    const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)(L.gather ? 1 : kBoxRows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(tm, type, 2, const_cast<void*>(at), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  CUtensorMap tmA, tmP;
+  if (!encode(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.A, L.lda)) return cudaErrorInvalidValue;
+  tmP = tmA;
+  RaggedParams p;
+  p.L = L;
+  p.rowscale = nullptr;
+  if (use_f16(L.pairs, L.E)) {
+    float* rowscale = reinterpret_cast<float*>(L.act);
+    __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (rows * 4 + 255) / 256 * 256);
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)rows), kPrepThreads, 0, s);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, reinterpret_cast<const __nv_bfloat16*>(L.A),
+                                       L.lda, L.K, ld_f16(L.KT), ap, rowscale);
+    if (e != cudaSuccess) return e;
+    if (!encode(&tmP, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ap, ld_f16(L.KT))) return cudaErrorInvalidValue;
+    p.rowscale = rowscale;
+    return launch_tok<128>(tmA, tmP, p, s);
+  }
+  return launch_tok<256>(tmA, tmP, p, s);
 }
 
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,
                            const int32_t* ids, int E, const float* weights, void* out,
                            int64_t ldo, cudaStream_t s) {
-  k_combine<<<dim3((unsigned)((N + 255) / 256), (unsigned)M), 256, 0, s>>>(
-      reinterpret_cast<const __nv_bfloat16*>(D), M, topk, N, ldd, ids, E, weights,
-      reinterpret_cast<__nv_bfloat16*>(out), ldo);
-  return cudaGetLastError();
+  const int64_t blocks = (M * ((N + 7) / 8) + kCombineThreads - 1) / kCombineThreads;
+  const int vec = (uintptr_t)out % 16 == 0 && ldo % 8 == 0;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)blocks), kCombineThreads, 0, s);
+  return cudaLaunchKernelEx(&cfg, k_combine, reinterpret_cast<const __nv_bfloat16*>(D), M, topk, N,
+                            ldd, ids, E, weights, reinterpret_cast<__nv_bfloat16*>(out), ldo, vec);
 }
 
 }  // namespace vt

@@ -46,13 +46,17 @@ vt_status check_workspace(const void* ws, size_t have, size_t need) {
   return VT_OK;
 }
 
-// Scratch of the combining product: the pairs' outputs [pairs][N] in bf16 behind the status.
-constexpr size_t kRaggedScratchOff = 256;
+// Workspace of the ragged products: the status, the converted activations and, for the
+// combining product, the pairs' outputs [pairs][N] in bf16.
+constexpr size_t kActOff = 256;
 inline int64_t scratch_ld(int64_t N) { return (N + 7) / 8 * 8; }
+size_t act_end(vt_fp4_handle W, int64_t pairs) {
+  return kActOff + up256(ragged_act_bytes(pairs, W->E, W->KT));
+}
 
 vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* order,
                  const int32_t* offsets, int64_t pairs, int64_t topk, int flags, void* C,
-                 int64_t ldc, void* ws, size_t ws_bytes, size_t need, vt_stream_t s) {
+                 int64_t ldc, void* ws, size_t ws_bytes, vt_stream_t s) {
   if (!W) return fail(VT_ERR_INVALID_ARG, "weight handle is NULL");
   if (vt_status st = check_groups(pairs, W->E)) return st;
   if (topk < 1 || topk > kMaxTopk) return fail(VT_ERR_INVALID_ARG, "topk must be in [1, %d]", kMaxTopk);
@@ -75,7 +79,7 @@ vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* ord
   if (!aligned(C, 2)) return fail(VT_ERR_MISALIGNED, "C must be 2-byte aligned");
   if (!aligned(order, 4) || !aligned(offsets, 4))
     return fail(VT_ERR_MISALIGNED, "order and offsets must be 4-byte aligned");
-  if (vt_status st = check_workspace(ws, ws_bytes, need)) return st;
+  if (vt_status st = check_workspace(ws, ws_bytes, act_end(W, pairs))) return st;
   RaggedLaunch L;
   L.packed = W->packed;
   L.fmt = W->fmt;
@@ -99,6 +103,7 @@ vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* ord
   L.C = C;
   L.ldc = ldc;
   L.status = reinterpret_cast<int*>(ws);
+  L.act = reinterpret_cast<uint8_t*>(ws) + kActOff;
   return done(launch_ragged(L, (cudaStream_t)s), "ragged product launch");
 }
 
@@ -180,7 +185,7 @@ vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t 
   if (vt_status st = check_groups(M_max * topk, W->E)) return st;
   // a paired weight's output is the caller's; only the combining product keeps scratch
   const size_t scratch = W->layout == (int)kLayoutPaired ? 0 : (size_t)(M_max * topk) * scratch_ld(W->N) * 2;
-  *bytes = kRaggedScratchOff + up256(scratch);
+  *bytes = act_end(W, M_max * topk) + up256(scratch);
   return VT_OK;
 }
 
@@ -188,8 +193,7 @@ vt_status vt_fp4_w4a16_gemm_ragged(const void* A, int64_t lda, vt_fp4_handle W,
                                    const int32_t* order, const int32_t* offsets, int64_t pairs,
                                    int64_t topk, int flags, void* C, int64_t ldc, void* workspace,
                                    size_t ws_bytes, vt_stream_t s) {
-  return ragged(A, lda, W, order, offsets, pairs, topk, flags, C, ldc, workspace, ws_bytes,
-                kRaggedScratchOff, s);
+  return ragged(A, lda, W, order, offsets, pairs, topk, flags, C, ldc, workspace, ws_bytes, s);
 }
 
 vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_handle W,
@@ -209,10 +213,10 @@ vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_ha
   if (ldc < W->N) return fail(VT_ERR_INVALID_ARG, "ldc (%lld) must be >= N", (long long)ldc);
   if (!aligned(C, 2)) return fail(VT_ERR_MISALIGNED, "C must be 2-byte aligned");
   if (vt_status st = check_workspace(workspace, ws_bytes, need)) return st;
-  void* D = reinterpret_cast<uint8_t*>(workspace) + kRaggedScratchOff;
+  void* D = reinterpret_cast<uint8_t*>(workspace) + act_end(W, M * topk);
   const int64_t ldd = scratch_ld(W->N);
   if (vt_status st = ragged(A, lda, W, order, offsets, M * topk, topk, VT_RAGGED_SCATTER, D, ldd,
-                            workspace, ws_bytes, need, s))
+                            workspace, ws_bytes, s))
     return st;
   return done(launch_combine(D, M, (int)topk, W->N, ldd, ids, (int)W->E, weights, C, ldc,
                              (cudaStream_t)s),

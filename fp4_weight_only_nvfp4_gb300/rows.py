@@ -156,7 +156,7 @@ def _ragged(A, W, groups, out, workspace, stream, flags, cols):
         out = torch.empty((groups.pairs, cols), dtype=torch.bfloat16, device=dev)
     ldc = _rows(out, "out", groups.pairs, cols, dev)
     if workspace is None:
-        workspace = W.ragged_workspace(0, groups.topk)
+        workspace = W.ragged_workspace(groups.M, groups.topk)
     wp, wn = _workspace(workspace, dev)
     check(lib().vt_fp4_w4a16_gemm_ragged(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
                                          groups.offsets.data_ptr(), groups.pairs, groups.topk,
