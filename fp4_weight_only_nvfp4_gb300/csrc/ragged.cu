@@ -12,48 +12,57 @@ namespace vt {
 
 namespace {
 
-// Roles of one persistent CTA per SM:
+// Roles of one persistent CTA per SM (23 warps):
 //   warp 0       weight producer: the packed 128 x 64 tiles of its items, one bulk copy per k step
 //   warp 1       token producer: up to TOK rows x 64 k of activations per k step by tiled TMA
-//                (128-byte swizzle), gathered four rows at a time where A is per token
+//                (128-byte swizzle), where an item's rows lie one after another
 //   warp 2       TMEM, and one thread issuing tcgen05.mma: D[128 weight rows][tokens] (fp32,
 //                TMEM) += W . A^T with M = 128 and N = the tile's tokens rounded up to 16
-//   kSets x 4    dequantisers: packed tile -> 16-bit K-major swizzled MMA operand; a set of four
-//   warps        warps takes every kSets-th k step, each warp 32 of its rows
-//   last 4 warps epilogue: lane = weight row, register = token
+//   Sets x 4     dequantisers: packed tile -> 16-bit K-major swizzled MMA operand; a set of four
+//   warps        warps takes every Sets-th k step, each warp 32 of its rows
+//   4 warps      (TOK = 256) loaders of gathered rows: 16-byte asynchronous copies to the same
+//                swizzled places
+//   last 4 warps epilogue
 // The weights are the MMA's M operand so that its cost follows the tokens a group really has
 // (N in steps of 16) and not a tile of 128 of them.
-// Operands, per item: f16, with the activations converted by a pre-pass (A * 2^-p, one power of
-// two per row) and the weight value c * s one f16 multiply away from the E2M1 conversion; or
-// bf16, with the caller's activations as they are and three more operations per weight pair.
+// Two operand types:
+//   f16, TOK = 128, for few rows per group, where the weights' dequantisation bounds the call: a
+//     pre-pass writes the rows in group order as A * 2^-p (one power of two per row), and a
+//     weight value c * s is one f16 multiply away from the E2M1 conversion;
+//   bf16, TOK = 256, for many, where the tensor core does: no pre-pass, the caller's rows go to
+//     the tensor core as they are, and a weight pair costs three more operations.
 // c * s has at most 6 significant bits and is exact in both; an expert whose E8M0 scales span
-// more exponents than f16 holds (`wide`) always takes bf16.
+// more exponents than f16 holds (`wide`) takes bf16 in either (the pre-pass copies its rows).
 // Items are (token tile, 128-row weight tile) pairs, weight tiles innermost; a group of n rows
 // is cut into ceil(n / TOK) token tiles of nearly equal size.
-constexpr int kSets = 4;
-constexpr int kDeqWarps = kSets * 4;
-constexpr int kThreads = (3 + kDeqWarps + 4) * 32;
+constexpr int kThreads = 23 * 32;
 constexpr int kNA = 4;                       // ring of dequantised weight tiles
 constexpr int kABytes = 128 * 128;
-constexpr int kBoxRows = 16;                 // rows of one tiled activation load
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kXBytes = 2 * 2 * 8 * 64 * 4;  // gate/up exchange of the SiLU epilogue
 
 // Shared-memory map (from a 1024-byte aligned base) for token tiles of up to TOK rows.
 template <int FMT, int TOK>
 struct Map {
-  static constexpr int NB = TOK == 256 ? 3 : 4;    // token stages
-  static constexpr int NW = TOK == 256 ? 10 : 14;  // packed weight stages
+  static constexpr bool Loaders = TOK == 256;
+  static constexpr int Sets = Loaders ? 3 : 4;
+  static constexpr int Box = TOK / 8;              // rows of one tiled activation load
+  static constexpr int NB = Loaders ? 3 : 4;       // token stages
+  static constexpr int NW = Loaders ? 8 : 14;      // packed weight stages
   static constexpr int BBytes = TOK * 128;
   static constexpr int OffB = kNA * kABytes;
   static constexpr int OffW = OffB + NB * BBytes;
   static constexpr int OffX = OffW + NW * tile_bytes(FMT);
-  static constexpr int OffBar = OffX + kXBytes;
+  // epilogue: 2 x 16 tokens x (128 columns, 16 bytes apart) of bf16; with SiLU 2 x 16 x 64
+  // columns behind the exchange of 2 x 4 warps x 8 registers
+  static constexpr int XBytes = 8192 + 2 * 16 * 144;
+  static constexpr int OffTok = OffX + XBytes;     // 2 x TOK x {output row, activation scale}
+  static constexpr int OffBar = OffTok + 2 * TOK * 8;
   static constexpr int NumBars = 2 * (kNA + NB + NW) + 4 + 1;
   static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
   // prefix sums of the groups' token tiles, and their first rows
   static constexpr int smem(int E) { return OffTab + 2 * (E + 1) * 4 + 1024; }
 };
+static_assert(2 * 16 * 272 <= Map<FMT_NV, 128>::XBytes, "plain epilogue");
 static_assert(Map<FMT_NV, 256>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 static_assert(Map<FMT_NV, 128>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 
@@ -81,17 +90,42 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2_m112(uint32_t h) {
   return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
 }
 
-// 16 columns of fp32 from TMEM.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+// 16 TMEM lanes x 16 columns of fp32 as MMA fragments: with lane = 4g + t, v[0..1] are row g,
+// columns 2t and 2t + 1, v[2..3] row g + 8, v[4..7] the same 8 columns on.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
+        "=r"(v[7])
       : "r"(taddr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_frags(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                 "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, transposed, to the rows whose addresses the lanes give.
+__device__ __forceinline__ void stmatrix_t4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// 16 bytes global -> shared, asynchronous; zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return as_u32(__floats2bfloat162_rn(a, b));
 }
 
 struct Item {
@@ -188,17 +222,16 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 
 template <int FMT, bool SILU, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmP,
-             const RaggedParams p) {
+    k_ragged(const __grid_constant__ CUtensorMap tm, const RaggedParams p) {
   using S = Map<FMT, TOK>;
-  constexpr int TB = tile_bytes(FMT), NB = S::NB, NW = S::NW;
+  constexpr int TB = tile_bytes(FMT), NB = S::NB, NW = S::NW, kSets = S::Sets;
+  constexpr bool kF16Mode = !S::Loaders;
   const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u - raw_u);
-  const uint32_t sA = base_u, sB = base_u + S::OffB, sW = base_u + S::OffW;
-  float* s_x = reinterpret_cast<float*>(base + S::OffX);
+  const uint32_t sA = base_u, sB = base_u + S::OffB, sW = base_u + S::OffW, sX = base_u + S::OffX;
   const uint32_t bars = base_u + S::OffBar;
   const uint32_t a_full = bars, a_empty = a_full + 8 * kNA;
   const uint32_t b_full = a_empty + 8 * kNA, b_empty = b_full + 8 * NB;
@@ -206,17 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t acc_full = w_empty + 8 * NW, acc_empty = acc_full + 16, drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OffBar + S::NumBars * 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int2* s_tok = reinterpret_cast<int2*>(base + S::OffTok);
   int* tstart = reinterpret_cast<int*>(base + S::OffTab);
   int* first = tstart + L.E + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const bool loaders = S::Loaders && L.gather;  // gathered rows: copied by the loader warps
   if (threadIdx.x == 0) {
     for (int s = 0; s < kNA; ++s) {
       mbar_init(a_full + 8 * s, 4);
       mbar_init(a_empty + 8 * s, 1);
     }
     for (int s = 0; s < NB; ++s) {
-      mbar_init(b_full + 8 * s, 1);
+      mbar_init(b_full + 8 * s, loaders ? 128 : 1);
       mbar_init(b_empty + 8 * s, 1);
     }
     for (int s = 0; s < NW; ++s) {
@@ -235,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The pre-pass lets this grid start only after its own wait for the kernels before it, so
   // with a pre-pass the groups may be read (and the weights requested) at once; what the
   // pre-pass writes is waited for by the roles that read it.
-  if (!p.rowscale) pdl_wait();
+  if (!kF16Mode) pdl_wait();
   pdl_launch_dependents();
   bool bad = false;  // offsets out of order or out of range
   for (int e = threadIdx.x; e <= L.E; e += kThreads) {
@@ -276,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- weight producer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pol = l2_evict_normal_policy();
       uint32_t iw = 0, pw = 0;
       int issued = 0;
@@ -305,71 +340,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- token producer
-    const uint64_t pol = l2_evict_last_policy();
-    uint32_t ib = 0, pb = 0;
-    int issued = 0;
-    bool ok = true;
-    pdl_wait();
-    for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-      const Item q = item_at(it, L, tstart, first);
-      const int n16 = (q.n + 15) & ~15;
-      const CUtensorMap* tm = p.rowscale && !(FMT == FMT_MX && header_of(L, q.e)->wide) ? &tmP : &tmA;
-      // gathered: lane l fetches rows 4l .. 4l+3 and 128 + 4l ..; past the tile's tokens the
-      // last one again (its products are not stored)
-      int4 y[TOK / 128];
-      if (L.gather) {
-#pragma unroll
-        for (int h = 0; h < TOK / 128; ++h) {
-          int r[4];
-          for (int c = 0; c < 4; ++c) {
-            const int i = h * 128 + lane * 4 + c;
-            const int pr = __ldcg(L.order + q.i0 + (i < q.n ? i : q.n - 1));
-            const bool in = pr >= 0 && pr < L.pairs;
-            if (!in) atomicExch(L.status, 6);
-            r[c] = in ? pr / L.topk : 0;
-          }
-          y[h] = make_int4(r[0], r[1], r[2], r[3]);
+    if (!loaders && elect_one()) {
+      const uint64_t pol = l2_evict_last_policy();
+      uint32_t ib = 0, pb = 0;
+      int issued = 0;
+      bool ok = true;
+      pdl_wait();
+      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
+        const Item q = item_at(it, L, tstart, first);
+        const int boxes = (q.n + S::Box - 1) / S::Box;
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs))) break;
+          const uint32_t dst = sB + ib * S::BBytes, bar = b_full + 8 * ib;
+          mbar_expect_tx(bar, (uint32_t)(boxes * S::Box * 128));
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(dst + b * S::Box * 128, &tm, kt * kTileK, (int)q.i0 + b * S::Box, bar, pol);
+          ++issued;
+          if (++ib == NB) { ib = 0; pb ^= 1u; }
         }
       }
-      for (int kt = 0; kt < KT; ++kt) {
-        ok = lane != 0 || pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const uint32_t dst = sB + ib * S::BBytes, bar = b_full + 8 * ib;
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)n16 * 128u);
-        __syncwarp();
-        if (L.gather) {
-#pragma unroll
-          for (int h = 0; h < TOK / 128; ++h)
-            if (h * 128 + lane * 4 < n16)
-              tma_gather4(dst + h * 16384 + lane * 512, tm, kt * kTileK, y[h], bar, pol);
-        } else {
-          if (lane * kBoxRows < n16)
-            tma_load_2d(dst + lane * kBoxRows * 128, tm, kt * kTileK, (int)q.i0 + lane * kBoxRows,
-                        bar, pol);
+      if (!ok) {
+        atomicExch(L.status, 5);
+        for (int k = 0; k < NB && k < issued; ++k) {
+          ib = ib == 0 ? NB - 1 : ib - 1;
+          if (ib == NB - 1) pb ^= 1u;
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(b_full + 8 * ib, pb) && globaltimer_ns() - t0 < kWaitNs) {}
         }
-        ++issued;
-        if (++ib == NB) { ib = 0; pb ^= 1u; }
       }
     }
-    if (!ok && lane == 0) {
-      atomicExch(L.status, 5);
-      for (int k = 0; k < NB && k < issued; ++k) {
-        ib = ib == 0 ? NB - 1 : ib - 1;
-        if (ib == NB - 1) pb ^= 1u;
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(b_full + 8 * ib, pb) && globaltimer_ns() - t0 < kWaitNs) {}
-      }
-    }
-    __syncwarp();
   } else if (warp == 2) {
     // --------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t ia = 0, pa = 0, ib = 0, pb = 0, ic = 0, pc = 0;
       bool ok = true;
       for (int64_t it = blockIdx.x; ok && it < items; it += G) {
         const Item q = item_at(it, L, tstart, first);
-        const bool f16 = p.rowscale && !(FMT == FMT_MX && header_of(L, q.e)->wide);
+        const bool f16 = kF16Mode && !(FMT == FMT_MX && header_of(L, q.e)->wide);
         const uint32_t idesc = (f16 ? kIdescF16 : kIdescBF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
         const uint32_t d = tmem + ic * TOK;
         if (!(ok = pf_wait(acc_empty + 8 * ic, pc ^ 1u, abort, kWaitNs))) break;
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kt = 0; kt < KT; ++kt) {
           if (!(ok = pf_wait(b_full + 8 * ib, pb, abort, kWaitNs))) break;
           if (!(ok = pf_wait(a_full + 8 * ia, pa, abort, kWaitNs))) break;
+          if (loaders) fence_proxy_async_smem();  // the loaders' copies -> visible to the tensor core
           tc_fence_after();
           const uint64_t ad = desc_sw128(sA + ia * kABytes), bd = desc_sw128(sB + ib * S::BBytes);
 #pragma unroll
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
     }
-  } else if (warp < 3 + kDeqWarps) {
+  } else if (warp < 3 + 4 * kSets) {
     // ------------------------------------------------------------- dequantisers
     // Set `set` takes the CTA's k steps set, set + kSets, ...; warp jp of the set the row blocks
     // 2jp and 2jp + 1 (32 rows), whose four scale bytes per lane are one word.
@@ -409,12 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int64_t it = blockIdx.x;
     while (it < items && kt >= KT) { kt -= KT; it += G; }
-    int op = p.rowscale ? kF16 : kBF16;
-    int64_t of = -1;  // the item `op` is of
+    bool wide = false;
+    int64_t of = -1;  // the item `wide` is of
     while (it < items) {
       if (FMT == FMT_MX && of != it) {
         of = it;
-        op = header_of(L, item_at(it, L, tstart, first).e)->wide ? kWide : p.rowscale ? kF16 : kBF16;
+        wide = header_of(L, item_at(it, L, tstart, first).e)->wide != 0;
       }
       if (!(ok = pf_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
       const uint32_t tb = sW + iw * TB;
@@ -422,15 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int4 cw1 = ld_shared_v4(tb + (2 * jp + 1) * 512 + lane * 16);
       const uint32_t sc = ld_shared_u32(tb + soff);
       uint32_t og[2][8], o8[2][8];  // rows g and g + 8 of both row blocks
-      if (op == kF16) {
-        dequant_block<FMT, kF16>(cw0, sc, og[0], o8[0]);
-        dequant_block<FMT, kF16>(cw1, sc >> 16, og[1], o8[1]);
-      } else if (FMT == FMT_MX && op == kWide) {
+      if (FMT == FMT_MX && wide) {
         dequant_block<FMT, kWide>(cw0, sc, og[0], o8[0]);
         dequant_block<FMT, kWide>(cw1, sc >> 16, og[1], o8[1]);
       } else {
-        dequant_block<FMT, kBF16>(cw0, sc, og[0], o8[0]);
-        dequant_block<FMT, kBF16>(cw1, sc >> 16, og[1], o8[1]);
+        dequant_block<FMT, kF16Mode ? kF16 : kBF16>(cw0, sc, og[0], o8[0]);
+        dequant_block<FMT, kF16Mode ? kF16 : kBF16>(cw1, sc >> 16, og[1], o8[1]);
       }
       // every lane has used what it loaded: only now may the next copy overwrite the stage
       __syncwarp();
@@ -453,77 +458,181 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (it < items && kt >= KT) { kt -= KT; it += G; }
     }
     if (!ok && lane == 0) atomicExch(L.status, 5);
+  } else if (S::Loaders && warp < 19) {
+    // ------------------------------------------------- loaders of gathered rows
+    // Thread: 16-byte chunk c of rows r0, r0 + 16, ...; a row past the tile's tokens reads the
+    // last one again (its products are not stored).
+    if (loaders) {
+      const int tid = (warp - 15) * 32 + lane, c = tid & 7, r0 = tid >> 3;
+      const uint32_t doff = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+      const uint8_t* A = reinterpret_cast<const uint8_t*>(L.A);
+      uint32_t ib = 0, pb = 0;
+      bool ok = true;
+      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
+        const Item q = item_at(it, L, tstart, first);
+        int row[TOK / 16];
+#pragma unroll
+        for (int i = 0; i < TOK / 16; ++i) {
+          row[i] = 0;
+          if (i * 16 < q.n) {
+            const int j = i * 16 + r0, pr = __ldcg(L.order + q.i0 + (j < q.n ? j : q.n - 1));
+            const bool in = pr >= 0 && pr < L.pairs;
+            if (!in) atomicExch(L.status, 6);
+            row[i] = in ? pr / L.topk : 0;
+          }
+        }
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs))) break;
+          const uint32_t dst = sB + ib * S::BBytes + doff;
+          const int64_t k = (int64_t)kt * kTileK + c * 8;
+          const uint32_t bytes = k < L.K ? 16u : 0u;  // K is a multiple of 16
+          const uint8_t* src = A + (k < L.K ? k * 2 : 0);
+#pragma unroll
+          for (int i = 0; i < TOK / 16; ++i)
+            if (i * 16 < q.n) cp_async16(dst + i * 2048, src + (int64_t)row[i] * L.lda * 2, bytes);
+          cp_async_arrive(b_full + 8 * ib);
+          if (++ib == NB) { ib = 0; pb ^= 1u; }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok && lane == 0) atomicExch(L.status, 5);
+    }
   } else {
     // ----------------------------------------------------------------- epilogue
-    const int qd = warp & 3;  // TMEM lane quarter this warp may access
-    const int r = qd * 32 + lane;  // packed row of the tile
+    // Four warps, warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16 tokens at a time:
+    // fragments from TMEM, scaled, rounded to bf16, transposed through shared memory and stored
+    // as rows of 128 (SiLU: 64) contiguous columns.
+    const int qd = warp & 3, tid = qd * 32 + lane, t = lane & 3;
+    constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16;
+    const uint32_t sT = sX + (SILU ? 8192 : 0);
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
-    uint32_t ic = 0, pc = 0;
+    const bool vec = (uintptr_t)L.C % 16 == 0 && L.ldc % 8 == 0;
+    const int64_t ncols = SILU ? L.seg_split : L.N;
+    uint32_t ic = 0, pc = 0, chunk = 0;
     bool ok = true;
     pdl_wait();
     for (int64_t it = blockIdx.x; ok && it < items; it += G) {
       const Item q = item_at(it, L, tstart, first);
       const PackedHeader* hdr = header_of(L, q.e);
-      const bool scaled = p.rowscale && !(FMT == FMT_MX && hdr->wide);
-      const int64_t n = SILU ? (int64_t)q.rt * 64 + (r & 63)
-                             : packed_to_row(L.layout, (int64_t)q.rt * kTileRows + r, L.N, L.seg_split);
       const bool up = SILU && qd >= 2;
-      const bool live = SILU ? n < L.seg_split : n >= 0;
-      const float f = hdr->factor[SILU ? (up ? 1 : 0) : (n >= L.seg_split ? 1 : 0)];
+      const float f0 = hdr->factor[up ? 1 : 0], f1 = hdr->factor[1];
+      const int64_t n0 = (int64_t)q.rt * kCols;
+      int2* tok = s_tok + ic * TOK;
+#pragma unroll
+      for (int h = 0; h < TOK / 128; ++h) {
+        const int j = h * 128 + tid;
+        int row = -1;
+        float rs = 1.0f;
+        if (j < q.n) {
+          row = (int)(q.i0 + j);
+          if (kF16Mode) rs = __ldcg(p.rowscale + row);
+          if (L.scatter) {
+            row = __ldcg(L.order + row);
+            if (row < 0 || row >= L.pairs) {
+              row = -1;
+              atomicExch(L.status, 6);
+            }
+          }
+        }
+        tok[j] = make_int2(row, __float_as_int(rs));
+      }
+      epilogue_sync();
       if (!(ok = pf_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
       tc_fence_after();
       const uint32_t ta = tmem + ic * TOK + ((uint32_t)(qd * 32) << 16);
-      for (int c = 0; c * 16 < q.n; ++c) {
-        uint32_t v[16];
-        tmem_ld16(ta + c * 16, v);
-        // lane j < 16: the output row and the activation scale of token j of the chunk
-        int64_t out = -1;
-        float rs = 1.0f;
-        const int64_t i = q.i0 + c * 16 + lane;
-        if (lane < 16 && c * 16 + lane < q.n) {
-          out = i;
-          if (L.scatter || (scaled && L.gather)) {
-            const int64_t pr = __ldcg(L.order + i);
-            const bool in = pr >= 0 && pr < L.pairs;
-            if (!in) atomicExch(L.status, 6);
-            if (L.scatter) out = in ? pr : -1;
-            if (scaled) rs = in ? __ldcg(p.rowscale + (L.gather ? pr / L.topk : i)) : 0.0f;
-          } else if (scaled) {
-            rs = __ldcg(p.rowscale + i);
-          }
+      for (int c = 0; c * 16 < q.n; ++c, ++chunk) {
+        uint32_t v[2][8];  // weight rows [0, 16) and [16, 32) of the warp's 32
+        tmem_ld_frag(ta + c * 16, v[0]);
+        tmem_ld_frag(ta + c * 16 + (16u << 16), v[1]);
+        // scales of this lane's tokens 2t, 2t + 1 and the same 8 on
+        float rs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (kF16Mode) {
+          const int4 a = *reinterpret_cast<const int4*>(tok + c * 16 + 2 * t);
+          const int4 b = *reinterpret_cast<const int4*>(tok + c * 16 + 8 + 2 * t);
+          rs[0] = __int_as_float(a.y);
+          rs[1] = __int_as_float(a.w);
+          rs[2] = __int_as_float(b.y);
+          rs[3] = __int_as_float(b.w);
         }
+        tmem_wait_frags(v[0], v[1]);
+        float x[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y = __uint_as_float(v[h][i]);
+            if (kF16Mode) y *= rs[(i & 1) + (i >> 2) * 2];
+            x[h][i] = y * f0;
+          }
+        const uint32_t buf = sT + (chunk & 1) * (16 * kRowB);
         if constexpr (SILU) {
-          // lanes 0-63 hold gate rows, 64-127 the matching up rows: of every 16 tokens the
-          // gate warps finish the first 8 and the up warps the others, trading what they lack
-          float* buf = s_x + (c & 1) * 1024;
-          float* mine = buf + (up ? 0 : 512);
-          float x[8];
+          // warps 0-1 hold gate rows, warps 2-3 the matching up rows in the same places: of
+          // every 16 tokens the gate warps finish the first 8 and the up warps the others
+          const uint32_t ex = sX + (chunk & 1) * 4096 + lane * 16;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = __uint_as_float(v[j]), b = __uint_as_float(v[8 + j]);
-            const float ra = __shfl_sync(0xffffffffu, rs, j), rb = __shfl_sync(0xffffffffu, rs, 8 + j);
-            mine[j * 64 + (r & 63)] = up ? a * ra * f : b * rb * f;
-            x[j] = up ? b * rb * f : a * ra * f;
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          const float* other = buf + (up ? 512 : 0);
+          for (int h = 0; h < 2; ++h)
+            st_shared_v4(ex + (qd * 2 + h) * 512, __float_as_uint(up ? x[h][0] : x[h][4]),
+                         __float_as_uint(up ? x[h][1] : x[h][5]), __float_as_uint(up ? x[h][2] : x[h][6]),
+                         __float_as_uint(up ? x[h][3] : x[h][7]));
+          epilogue_sync();
+          uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int64_t ro = __shfl_sync(0xffffffffu, out, (up ? 8 : 0) + j);
-            const float z = other[j * 64 + (r & 63)];
-            const float h = up ? silu_f(z) * x[j] : silu_f(x[j]) * z;
-            if (live && ro >= 0) C[ro * L.ldc + n] = __float2bfloat16_rn(h);
+          for (int h = 0; h < 2; ++h) {
+            const int4 z = ld_shared_v4(ex + ((qd ^ 2) * 2 + h) * 512);
+            const float zz[4] = {__int_as_float(z.x), __int_as_float(z.y), __int_as_float(z.z),
+                                 __int_as_float(z.w)};
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = up ? silu_f(zz[i]) * x[h][4 + i] : silu_f(x[h][i]) * zz[i];
+            o[2 * h] = pack_bf16(y[0], y[1]);
+            o[2 * h + 1] = pack_bf16(y[2], y[3]);
           }
+          stmatrix_t4(buf + ((up ? 8 : 0) + (lane & 7)) * kRowB + ((qd & 1) * 32 + (lane >> 3) * 8) * 2,
+                      o[0], o[1], o[2], o[3]);
         } else {
+          if (n0 + 128 > L.seg_split && L.seg_split < L.N) {
+            // the tile reaches into the second segment: its rows take that one's factor
+            const int64_t split = L.seg_split - n0 - qd * 32;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int64_t ro = __shfl_sync(0xffffffffu, out, j);
-            const float y = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, rs, j) * f;
-            if (live && ro >= 0) C[ro * L.ldc + n] = __float2bfloat16_rn(y);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (h * 16 + (lane >> 2) + ((i >> 1) & 1) * 8 >= split) {
+                  float y = __uint_as_float(v[h][i]);
+                  if (kF16Mode) y *= rs[(i & 1) + (i >> 2) * 2];
+                  x[h][i] = y * f1;
+                }
+          }
+#pragma unroll
+          for (int th = 0; th < 2; ++th)
+            stmatrix_t4(buf + (th * 8 + (lane & 7)) * kRowB + (qd * 32 + (lane >> 3) * 8) * 2,
+                        pack_bf16(x[0][4 * th], x[0][4 * th + 1]),
+                        pack_bf16(x[0][4 * th + 2], x[0][4 * th + 3]),
+                        pack_bf16(x[1][4 * th], x[1][4 * th + 1]),
+                        pack_bf16(x[1][4 * th + 2], x[1][4 * th + 3]));
+        }
+        epilogue_sync();
+        constexpr int kPieces = kCols / 8;  // 16-byte pieces of a token's columns
+#pragma unroll
+        for (int i = 0; i < 16 * kPieces / 128; ++i) {
+          const int j = (i * 128 + tid) / kPieces, pc8 = (i * 128 + tid) % kPieces;
+          const int row = tok[c * 16 + j].x;
+          const int64_t n = n0 + pc8 * 8;
+          if (row < 0 || n >= ncols) continue;
+          const int4 d = ld_shared_v4(buf + j * kRowB + pc8 * 16);
+          __nv_bfloat16* dst = C + (int64_t)row * L.ldc + n;
+          if (vec && n + 8 <= ncols) {
+            *reinterpret_cast<int4*>(dst) = d;
+          } else {
+            const uint32_t w[4] = {(uint32_t)d.x, (uint32_t)d.y, (uint32_t)d.z, (uint32_t)d.w};
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+              if (n + b < ncols)
+                reinterpret_cast<uint16_t*>(dst)[b] = (uint16_t)(w[b >> 1] >> ((b & 1) * 16));
           }
         }
       }
-      if constexpr (SILU) asm volatile("bar.sync 1, 128;" ::: "memory");  // the exchange is free again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + 8 * ic);
@@ -532,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) atomicExch(L.status, 5);
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
@@ -540,22 +650,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Activation pre-pass of the f16 operands: A'[r][k] = A[r][k] * 2^-p in f16, p the power of two
-// of the row's largest magnitude (act_pow2), rowscale[r] = 2^p.  One block per row.
+// Activation pre-pass of the f16 operands, rows in group order: A'[i][k] = A[row(i)][k] * 2^-p in
+// f16, p the power of two of the row's largest magnitude (act_pow2), rowscale[i] = 2^p; a row of
+// a `wide` expert is copied as bf16 with scale 1.  One block per grouped row.
 constexpr int kPrepThreads = 128;
-__global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const __nv_bfloat16* __restrict__ A,
-                                                              int64_t lda, int64_t K, int64_t ldp,
+__global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t ldp,
                                                               __half* __restrict__ Ap,
                                                               float* __restrict__ rowscale) {
-  __shared__ int s_max[kPrepThreads / 32];
+  __shared__ int s_max[kPrepThreads / 32], s_e;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t m = blockIdx.x;
-  const uint4* row = reinterpret_cast<const uint4*>(A + m * lda);
-  const int64_t ng = K / 8;
+  const int64_t i = blockIdx.x;
+  if (i >= __ldcg(L.offsets + L.E)) return;  // a pair in no group
+  int64_t m = i;
+  if (L.gather) {
+    const int pr = __ldcg(L.order + i);
+    const bool in = pr >= 0 && pr < L.pairs;
+    if (!in && threadIdx.x == 0) atomicExch(L.status, 6);
+    m = in ? pr / L.topk : 0;
+  }
+  const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(L.A) + m * L.lda);
+  uint4* dst = reinterpret_cast<uint4*>(Ap + i * ldp);
+  const int64_t ng = L.K / 8;
+  if (L.fmt == FMT_MX) {
+    if (threadIdx.x == 0) s_e = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < L.E; e += kPrepThreads)
+      if (__ldcg(L.offsets + e) <= i && i < __ldcg(L.offsets + e + 1)) s_e = e;
+    __syncthreads();
+    if (header_of(L, s_e)->wide) {
+      for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) dst[k] = row[k];
+      if (threadIdx.x == 0) rowscale[i] = 1.0f;
+      return;
+    }
+  }
   int mx = 0;
-  for (int64_t i = threadIdx.x; i < ng; i += kPrepThreads) {
-    const uint4 v = row[i];
+  for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) {
+    const uint4 v = row[k];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     mx = max(mx, act_maxmag8(w));
   }
@@ -563,15 +694,14 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const __nv_bfloat1
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPrepThreads / 32; ++i) mx = max(mx, s_max[i]);
+  for (int w = 0; w < kPrepThreads / 32; ++w) mx = max(mx, s_max[w]);
   const int p = act_pow2(mx);
-  uint4* dst = reinterpret_cast<uint4*>(Ap + m * ldp);
-  for (int64_t i = threadIdx.x; i < ng; i += kPrepThreads) {
-    const uint4 v = row[i];
+  for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) {
+    const uint4 v = row[k];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    dst[i] = act_granule_f16(w, p);
+    dst[k] = act_granule_f16(w, p);
   }
-  if (threadIdx.x == 0) rowscale[m] = pow2f(p);
+  if (threadIdx.x == 0) rowscale[i] = pow2f(p);
 }
 
 // Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.
@@ -632,7 +762,7 @@ cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* at, dim3 grid, int threads, i
 }
 
 template <int FMT, bool SILU, int TOK>
-cudaError_t launch_main(const CUtensorMap& tmA, const CUtensorMap& tmP, const RaggedParams& p,
+cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p,
                         int grid, cudaStream_t s) {
   static int done[64] = {0};
   int dev = 0;
@@ -648,21 +778,21 @@ cudaError_t launch_main(const CUtensorMap& tmA, const CUtensorMap& tmP, const Ra
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg =
       pdl_config(&at, dim3((unsigned)grid), kThreads, Map<FMT, TOK>::smem(p.L.E), s);
-  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, TOK>, tmA, tmP, p);
+  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, TOK>, tm, p);
 }
 
 template <int TOK>
-cudaError_t launch_tok(const CUtensorMap& tmA, const CUtensorMap& tmP, const RaggedParams& p,
+cudaError_t launch_tok(const CUtensorMap& tm, const RaggedParams& p,
                        cudaStream_t s) {
   const RaggedLaunch& L = p.L;
   // at most one partial token tile per group in use
   const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
   const int64_t most = (groups + L.pairs / TOK) * L.RT;
   const int grid = (int)(sm_count() < most ? sm_count() : most);
-  if (L.fmt == FMT_NV) return L.silu ? launch_main<FMT_NV, true, TOK>(tmA, tmP, p, grid, s)
-                                     : launch_main<FMT_NV, false, TOK>(tmA, tmP, p, grid, s);
-  return L.silu ? launch_main<FMT_MX, true, TOK>(tmA, tmP, p, grid, s)
-                : launch_main<FMT_MX, false, TOK>(tmA, tmP, p, grid, s);
+  if (L.fmt == FMT_NV) return L.silu ? launch_main<FMT_NV, true, TOK>(tm, p, grid, s)
+                                     : launch_main<FMT_NV, false, TOK>(tm, p, grid, s);
+  return L.silu ? launch_main<FMT_MX, true, TOK>(tm, p, grid, s)
+                : launch_main<FMT_MX, false, TOK>(tm, p, grid, s);
 }
 
 inline int64_t ld_f16(int64_t KT) { return KT * kTileK; }
@@ -679,36 +809,37 @@ size_t ragged_act_bytes(int64_t pairs, int64_t E, int64_t KT) {
 cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  // the activations as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
-  const int64_t rows = L.gather ? L.pairs / L.topk : L.pairs;
-  auto encode = [&](CUtensorMap* tm, CUtensorMapDataType type, const void* at, int64_t ld) {
-    const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)(L.gather ? 1 : kBoxRows)};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(tm, type, 2, const_cast<void*>(at), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  CUtensorMap tmA, tmP;
-  if (!encode(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.A, L.lda)) return cudaErrorInvalidValue;
-  tmP = tmA;
   RaggedParams p;
   p.L = L;
   p.rowscale = nullptr;
+  // the rows as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
+  auto encode = [&](CUtensorMap* tm, CUtensorMapDataType type, void* at, int64_t ld, int64_t rows,
+                    int rbox) {
+    const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)rbox};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(tm, type, 2, at, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  CUtensorMap tm;
   if (use_f16(L.pairs, L.E)) {
     float* rowscale = reinterpret_cast<float*>(L.act);
-    __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (rows * 4 + 255) / 256 * 256);
+    __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (L.pairs * 4 + 255) / 256 * 256);
+    if (!encode(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ap, ld_f16(L.KT), L.pairs, Map<FMT_NV, 128>::Box))
+      return cudaErrorInvalidValue;
     cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)rows), kPrepThreads, 0, s);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, reinterpret_cast<const __nv_bfloat16*>(L.A),
-                                       L.lda, L.K, ld_f16(L.KT), ap, rowscale);
+    const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)L.pairs), kPrepThreads, 0, s);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, ld_f16(L.KT), ap, rowscale);
     if (e != cudaSuccess) return e;
-    if (!encode(&tmP, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ap, ld_f16(L.KT))) return cudaErrorInvalidValue;
     p.rowscale = rowscale;
-    return launch_tok<128>(tmA, tmP, p, s);
+    return launch_tok<128>(tm, p, s);
   }
-  return launch_tok<256>(tmA, tmP, p, s);
+  if (!encode(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void*>(L.A), L.lda,
+              L.gather ? L.pairs / L.topk : L.pairs, Map<FMT_NV, 256>::Box))
+    return cudaErrorInvalidValue;
+  return launch_tok<256>(tm, p, s);
 }
 
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,

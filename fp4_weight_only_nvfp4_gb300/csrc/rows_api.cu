@@ -64,9 +64,9 @@ vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* ord
   if (flags & ~(VT_RAGGED_GATHER | VT_RAGGED_SCATTER | VT_RAGGED_SILU_MUL))
     return fail(VT_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   const bool silu = flags & VT_RAGGED_SILU_MUL;
-  if (silu && W->layout != (int)kLayoutPaired)
+  if (silu != (W->layout == (int)kLayoutPaired))
     return fail(VT_ERR_INVALID_ARG,
-                "the SiLU-and-multiply epilogue needs a weight packed as paired gate and up");
+                "the SiLU-and-multiply epilogue goes with a weight packed as paired gate and up");
   if (pairs == 0) return VT_OK;
   if (!A || !C || !order || !offsets)
     return fail(VT_ERR_INVALID_ARG, "A, C, order and offsets must be set");

@@ -105,16 +105,13 @@ __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   return v;
 }
 
-// Four rows y.x .. y.w of a 2-D tensor map whose box is one row high, to consecutive rows of
-// shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 y,
-                                            uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z),
-      "r"(y.w), "l"(policy)
-      : "memory");
+// True in one lane of the (converged) warp.  The tensor-core and TMA instructions take uniform
+// registers: under a branch on this the compiler knows that one thread issues them, under
+// `lane == 0` it does not and loops over the lanes (76 against some 10 cycles per MMA issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // Shared-memory matrix descriptor of a K-major operand tile whose rows are 128 bytes, stored

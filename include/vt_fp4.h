@@ -362,7 +362,8 @@ enum {
   VT_RAGGED_GATHER = 1,  /* A has one row per token: the i-th grouped pair p reads row p / topk;
                             without it A has one row per grouped pair, row i */
   VT_RAGGED_SCATTER = 2, /* the i-th grouped pair p writes row p of C; without it row i */
-  VT_RAGGED_SILU_MUL = 4 /* W from vt_fp4_prepack_grouped_gate_up: C = silu(gate) * up, I columns */
+  VT_RAGGED_SILU_MUL = 4 /* C = silu(gate) * up, I columns: set for a weight packed as paired gate
+                            and up (vt_fp4_prepack_grouped_gate_up), and for no other */
 };
 
 /* Workspace of the ragged products on W for up to M_max tokens of topk pairs each; 256-byte

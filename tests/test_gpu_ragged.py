@@ -312,6 +312,8 @@ def test_wrong_shapes_are_refused():
         vt.w4a16_gemm_ragged_combine(acts(rng, M * topk, K).cuda(), W, groups)
     with pytest.raises(_lib.VtError, match="paired"):
         vt.w4a16_gemm_ragged_silu_mul(x, W, groups)
+    with pytest.raises(_lib.VtError, match="paired"):
+        vt.w4a16_gemm_ragged(x, Wp, groups)
     with pytest.raises(_lib.VtError, match="MISALIGNED"):
         vt.w4a16_gemm_ragged(torch.zeros(M, K + 4, dtype=torch.bfloat16, device="cuda")[:, :K], W, groups)
     gw, _, _ = _groups(_ids(rng, M, topk, E), E, np.ones((M, topk)))
