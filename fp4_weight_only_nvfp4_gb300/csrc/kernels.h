@@ -160,7 +160,7 @@ struct RaggedLaunch {
   int* status;
   void* act;           // ragged_act_bytes of scratch for converted activations
 };
-size_t ragged_act_bytes(int64_t pairs, int64_t E, int64_t KT);
+size_t ragged_act_bytes(int64_t pairs, int64_t KT);
 cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s);
 // out[m] = sum_j weights[m][j] * D[m * topk + j], pairs whose id is outside [0, E) left out.
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,

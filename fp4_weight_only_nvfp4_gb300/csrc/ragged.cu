@@ -12,82 +12,81 @@ namespace vt {
 
 namespace {
 
+// Operands: f16.  A pre-pass writes the activations as A * 2^-p (one power of two per row), and a
+// weight value c * s (at most 6 significant bits) is exact in f16, one multiply away from the
+// E2M1 conversion.  An expert whose E8M0 scales span more exponents than f16 holds (`wide`) takes
+// bf16, in which its values and the caller's activations are exact.
+//
 // Roles of one persistent CTA per SM (23 warps):
-//   warp 0       weight producer: the packed 128 x 64 tiles of its items, one bulk copy per k step
-//   warp 1       token producer: up to TOK rows x 64 k of activations per k step by tiled TMA
-//                (128-byte swizzle), where an item's rows lie one after another
-//   warp 2       TMEM, and one thread issuing tcgen05.mma: D[128 weight rows][tokens] (fp32,
+//   warp 0       weight producer: R packed 128 x 64 tiles (one bulk copy each) per k step
+//   warp 1       token producer: up to 128 rows x 64 k of activations per k step by tiled TMA
+//                (128-byte swizzle), where the pre-pass has put the rows in group order
+//   warp 2       TMEM, and one thread issuing tcgen05.mma: D[R x 128 weight rows][tokens] (fp32,
 //                TMEM) += W . A^T with M = 128 and N = the tile's tokens rounded up to 16
-//   Sets x 4     dequantisers: packed tile -> 16-bit K-major swizzled MMA operand; a set of four
-//   warps        warps takes every Sets-th k step, each warp 32 of its rows
-//   4 warps      (TOK = 256) loaders of gathered rows: 16-byte asynchronous copies to the same
-//                swizzled places
+//   Sets x 4     dequantisers: packed tiles -> K-major swizzled MMA operand; a set of four warps
+//   warps        takes every Sets-th k step, each warp 32 rows of each tile
+//   4 warps      (LOAD) loaders: gathered rows by 16-byte asynchronous copies to the same places
 //   last 4 warps epilogue
 // The weights are the MMA's M operand so that its cost follows the tokens a group really has
 // (N in steps of 16) and not a tile of 128 of them.
-// Two operand types:
-//   f16, TOK = 128, for few rows per group, where the weights' dequantisation bounds the call: a
-//     pre-pass writes the rows in group order as A * 2^-p (one power of two per row), and a
-//     weight value c * s is one f16 multiply away from the E2M1 conversion;
-//   bf16, TOK = 256, for many, where the tensor core does: no pre-pass, the caller's rows go to
-//     the tensor core as they are, and a weight pair costs three more operations.
-// c * s has at most 6 significant bits and is exact in both; an expert whose E8M0 scales span
-// more exponents than f16 holds (`wide`) takes bf16 in either (the pre-pass copies its rows).
-// Items are (token tile, 128-row weight tile) pairs, weight tiles innermost; a group of n rows
-// is cut into ceil(n / TOK) token tiles of nearly equal size.
+// Items are (token tile, R x 128 weight rows) pairs, weight rows innermost; a group of n rows is
+// cut into ceil(n / 128) token tiles of nearly equal size.
+constexpr int kTok = 128;
 constexpr int kThreads = 23 * 32;
-constexpr int kNA = 4;                       // ring of dequantised weight tiles
+constexpr int kEpiWarp0 = 19;                // first of the four epilogue warps
 constexpr int kABytes = 128 * 128;
+constexpr int kBBytes = kTok * 128;
+constexpr int kBox = 16;                     // rows of one tiled activation load
+constexpr int kTileTable = 1024;             // token tiles whose group is looked up, not searched
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Shared-memory map (from a 1024-byte aligned base) for token tiles of up to TOK rows.
-template <int FMT, int TOK>
+// Shared-memory map (from a 1024-byte aligned base).
+template <int FMT, int R, bool LOAD>
 struct Map {
-  static constexpr bool Loaders = TOK == 256;
-  static constexpr int Sets = Loaders ? 3 : 4;
-  static constexpr int Box = TOK / 8;              // rows of one tiled activation load
-  static constexpr int NB = Loaders ? 3 : 4;       // token stages
-  static constexpr int NW = Loaders ? 8 : 14;      // packed weight stages
-  static constexpr int BBytes = TOK * 128;
-  static constexpr int OffB = kNA * kABytes;
-  static constexpr int OffW = OffB + NB * BBytes;
-  static constexpr int OffX = OffW + NW * tile_bytes(FMT);
-  // epilogue: 2 x 16 tokens x (128 columns, 16 bytes apart) of bf16; with SiLU 2 x 16 x 64
+  static constexpr int NS = R == 2 ? 3 : 4;        // stages of dequantised weights and tokens
+  static constexpr int Sets = NS;                  // sets of dequantisers
+  static constexpr int NW = R == 2 ? 6 : 14;       // stages of packed weights
+  // A wait on a phase's parity holds only if the phase before it is known to be over.  A set
+  // that waits for k step c has passed its wait of step c - Sets for a free stage, so the steps
+  // up to c - Sets - NS have been multiplied; the steps that used the same stage and the same
+  // packed stage before, c - NS and c - NW, have their phases before last over (Sets <= NS) and
+  // last over (the packed copies land in any order, so nothing less than consumption tells).
+  static_assert(Sets <= NS && NW >= NS + Sets, "barrier phases");
+  static constexpr int OffB = NS * R * kABytes;
+  static constexpr int OffW = OffB + NS * kBBytes;
+  static constexpr int OffX = OffW + NW * R * tile_bytes(FMT);
+  // epilogue: 2 x 16 tokens x 128 columns of bf16, rows 16 bytes apart; with SiLU 2 x 16 x 64
   // columns behind the exchange of 2 x 4 warps x 8 registers
   static constexpr int XBytes = 8192 + 2 * 16 * 144;
-  static constexpr int OffTok = OffX + XBytes;     // 2 x TOK x {output row, activation scale}
-  static constexpr int OffBar = OffTok + 2 * TOK * 8;
-  static constexpr int NumBars = 2 * (kNA + NB + NW) + 4 + 1;
+  static constexpr int OffTok = OffX + XBytes;     // 2 x kTok x {output row, activation scale}
+  static constexpr int OffBar = OffTok + 2 * kTok * 8;
+  static constexpr int NumBars = 2 * (NS + NW) + 4 + 1;
   static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
-  // prefix sums of the groups' token tiles, and their first rows
-  static constexpr int smem(int E) { return OffTab + 2 * (E + 1) * 4 + 1024; }
+  // per group: prefix sum of the token tiles, first row, rows per tile; group of a token tile
+  static constexpr int smem(int E) { return OffTab + (E + 1) * 10 + kTileTable * 2 + 16 + 1024; }
 };
-static_assert(2 * 16 * 272 <= Map<FMT_NV, 128>::XBytes, "plain epilogue");
-static_assert(Map<FMT_NV, 256>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
-static_assert(Map<FMT_NV, 128>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+static_assert(Map<FMT_NV, 1, false>::Sets <= 4 && Map<FMT_NV, 2, true>::Sets <= 3, "warps");
+static_assert(2 * 16 * 272 <= Map<FMT_NV, 1, false>::XBytes, "plain epilogue");
+static_assert(Map<FMT_NV, 1, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+static_assert(Map<FMT_NV, 2, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+static_assert(Map<FMT_NV, 2, true>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 
 constexpr uint32_t kIdescF16 = (1u << 4) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescBF16 = kIdescF16 | (1u << 7) | (1u << 10);
 
 struct RaggedParams {
   RaggedLaunch L;
-  const float* rowscale;  // f16 operands: 2^p per row of A; NULL: bf16 operands
+  const __half* Ap;       // converted activations [rows][ldp], in group order; LOAD: per token
+  int64_t ldp;
+  const float* rowscale;  // 2^p of each of their rows
 };
 
-__device__ __forceinline__ float silu_f(float x) { return x / (1.0f + expf(-x)); }
+// SiLU(x) = x / (1 + e^-x).  The quick divide is good to 2 units of 2^-24; from 1 + e^-x >= 2^126
+// on it gives 0 for a value below 2^-119.
+__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + expf(-x)); }
 
-__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
-  return *reinterpret_cast<__nv_bfloat162*>(&x);
-}
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
   return *reinterpret_cast<uint32_t*>(&x);
-}
-
-// f16x2 of two E2M1 values c -> bf16x2 of c * 2^-112: the sign stays, exponent and mantissa move
-// down by the 3 bits that the mantissas differ in (an E2M1 value's low 9 mantissa bits are 0, so
-// nothing crosses into the lower half).
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2_m112(uint32_t h) {
-  return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
 }
 
 // 16 TMEM lanes x 16 columns of fp32 as MMA fragments: with lane = 4g + t, v[0..1] are row g,
@@ -120,39 +119,63 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return as_u32(__floats2bfloat162_rn(a, b));
 }
 
-struct Item {
-  int e, rt, n;     // group, weight row tile, tokens
-  int64_t i0;       // first grouped row
+// The groups' token tiles, in shared memory.
+struct Tiles {
+  int* start;      // [E + 1] prefix sums of the token tiles
+  int* first;      // [E + 1] first grouped row
+  uint16_t* rows;  // [E] rows per token tile
+  uint16_t* of;    // [kTileTable] group of a token tile
+  int E;
 };
 
-// The item's group by bisection of the token tiles' prefix sums.
-__device__ __forceinline__ Item item_at(int64_t it, const RaggedLaunch& L, const int* tstart,
-                                        const int* first) {
+struct Item {
+  int e, n;      // group, tokens
+  int64_t i0;    // first grouped row
+};
+
+__device__ __forceinline__ Item item_of(const Tiles& T, int tile) {
   Item q;
-  const int tile = (int)(it / L.RT);
-  q.rt = (int)(it - (int64_t)tile * L.RT);
-  int lo = 0, hi = L.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tstart[mid] <= tile) lo = mid;
-    else hi = mid;
+  if (tile < kTileTable) {
+    q.e = T.of[tile];
+  } else {
+    int lo = 0, hi = T.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (T.start[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    q.e = lo;
   }
-  q.e = lo;
-  const int nt = tstart[lo + 1] - tstart[lo], t = tile - tstart[lo];
-  const int64_t n = first[lo + 1] - first[lo];
-  const int64_t b = n * t / nt;
-  q.n = (int)(n * (t + 1) / nt - b);
-  q.i0 = first[lo] + b;
+  const int per = T.rows[q.e], b = (tile - T.start[q.e]) * per;
+  const int left = T.first[q.e + 1] - T.first[q.e] - b;
+  q.n = left < per ? left : per;
+  q.i0 = T.first[q.e] + b;
   return q;
 }
+
+// A CTA's walk over its items: (token tile, group of R row tiles), G items apart.
+struct Walk {
+  int tile, rg, dtile, drg, RG;
+  __device__ __forceinline__ Walk(int64_t RGs) {
+    RG = (int)RGs;
+    tile = (int)blockIdx.x / RG;
+    rg = (int)blockIdx.x - tile * RG;
+    dtile = (int)gridDim.x / RG;
+    drg = (int)gridDim.x - dtile * RG;
+  }
+  __device__ __forceinline__ void next() {
+    tile += dtile;
+    if ((rg += drg) >= RG) {
+      rg -= RG;
+      ++tile;
+    }
+  }
+};
 
 __device__ __forceinline__ const PackedHeader* header_of(const RaggedLaunch& L, int e) {
   return reinterpret_cast<const PackedHeader*>(reinterpret_cast<const uint8_t*>(L.packed) +
@@ -161,12 +184,11 @@ __device__ __forceinline__ const PackedHeader* header_of(const RaggedLaunch& L, 
 
 // One row block (16 rows x 64 k; this lane: rows g and g + 8, 16 k each) of a packed tile to
 // 16-bit pairs in k order: og of row g, o8 of row g + 8.
-enum { kF16 = 0, kBF16 = 1, kWide = 2 };
-template <int FMT, int OP>
+template <int FMT, bool WIDE>
 __device__ __forceinline__ void dequant_block(const int4& cw, uint32_t sc, uint32_t (&og)[8],
                                               uint32_t (&o8)[8]) {
   const uint32_t words[4] = {(uint32_t)cw.x, (uint32_t)cw.y, (uint32_t)cw.z, (uint32_t)cw.w};
-  if constexpr (OP == kWide) {
+  if constexpr (WIDE) {
     // raw E8M0 bytes: c * 2^(e - 127) by fp32, exact in bf16 (subnormals included)
     const float wg = e8m0_to_f32(sc & 0xFFu), w8 = e8m0_to_f32((sc >> 8) & 0xFFu);
 #pragma unroll
@@ -186,30 +208,15 @@ __device__ __forceinline__ void dequant_block(const int4& cw, uint32_t sc, uint3
     }
   } else {
     const uint32_t s2 = FMT == FMT_NV ? e4m3x2_to_f16x2(sc & 0xFFFFu) : mxenc2_to_f16x2(sc & 0xFFFFu);
-    if constexpr (OP == kF16) {
-      const uint32_t sg = bcast_lo(s2), s8 = bcast_hi(s2);
+    const uint32_t sg = bcast_lo(s2), s8 = bcast_hi(s2);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r0, r1, r2, r3;
-        e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
-        og[2 * q] = hmul2_u32(r0, sg);
-        o8[2 * q] = hmul2_u32(r1, s8);
-        og[2 * q + 1] = hmul2_u32(r2, sg);
-        o8[2 * q + 1] = hmul2_u32(r3, s8);
-      }
-    } else {
-      const __half2 sh = *reinterpret_cast<const __half2*>(&s2);
-      const float fg = __low2float(sh) * 0x1p112f, f8 = __high2float(sh) * 0x1p112f;
-      const __nv_bfloat162 bg = __floats2bfloat162_rn(fg, fg), b8 = __floats2bfloat162_rn(f8, f8);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r0, r1, r2, r3;
-        e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
-        og[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r0)), bg));
-        o8[2 * q] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r1)), b8));
-        og[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r2)), bg));
-        o8[2 * q + 1] = as_u32(__hmul2(as_bf162(f16x2_to_bf16x2_m112(r3)), b8));
-      }
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r0, r1, r2, r3;
+      e2m1x8_to_f16x8(words[q], r0, r1, r2, r3);
+      og[2 * q] = hmul2_u32(r0, sg);
+      o8[2 * q] = hmul2_u32(r1, s8);
+      og[2 * q + 1] = hmul2_u32(r2, sg);
+      o8[2 * q + 1] = hmul2_u32(r3, s8);
     }
   }
 }
@@ -220,39 +227,36 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
-template <int FMT, bool SILU, int TOK>
+template <int FMT, bool SILU, int R, bool LOAD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ragged(const __grid_constant__ CUtensorMap tm, const RaggedParams p) {
-  using S = Map<FMT, TOK>;
-  constexpr int TB = tile_bytes(FMT), NB = S::NB, NW = S::NW, kSets = S::Sets;
-  constexpr bool kF16Mode = !S::Loaders;
+  using S = Map<FMT, R, LOAD>;
+  constexpr int TB = tile_bytes(FMT), NS = S::NS, NW = S::NW, kSets = S::Sets;
+  constexpr uint32_t kTmemCols = 2 * R * kTok;
   const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u - raw_u);
   const uint32_t sA = base_u, sB = base_u + S::OffB, sW = base_u + S::OffW, sX = base_u + S::OffX;
-  const uint32_t bars = base_u + S::OffBar;
-  const uint32_t a_full = bars, a_empty = a_full + 8 * kNA;
-  const uint32_t b_full = a_empty + 8 * kNA, b_empty = b_full + 8 * NB;
-  const uint32_t w_full = b_empty + 8 * NB, w_empty = w_full + 8 * NW;
+  const uint32_t full = base_u + S::OffBar, empty = full + 8 * NS;  // dequantised weights + tokens
+  const uint32_t w_full = empty + 8 * NS, w_empty = w_full + 8 * NW;
   const uint32_t acc_full = w_empty + 8 * NW, acc_empty = acc_full + 16, drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OffBar + S::NumBars * 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int2* s_tok = reinterpret_cast<int2*>(base + S::OffTok);
-  int* tstart = reinterpret_cast<int*>(base + S::OffTab);
-  int* first = tstart + L.E + 1;
+  Tiles T;
+  T.E = L.E;
+  T.start = reinterpret_cast<int*>(base + S::OffTab);
+  T.first = T.start + L.E + 1;
+  T.rows = reinterpret_cast<uint16_t*>(T.first + L.E + 1);
+  T.of = T.rows + L.E + 1;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const bool loaders = S::Loaders && L.gather;  // gathered rows: copied by the loader warps
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kNA; ++s) {
-      mbar_init(a_full + 8 * s, 4);
-      mbar_init(a_empty + 8 * s, 1);
-    }
-    for (int s = 0; s < NB; ++s) {
-      mbar_init(b_full + 8 * s, loaders ? 128 : 1);
-      mbar_init(b_empty + 8 * s, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full + 8 * s, 4 + (LOAD ? 128 : 1));  // a dequantiser set, the token copies
+      mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(w_full + 8 * s, 1);
@@ -265,27 +269,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     *abort = 0;
   }
-  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), 2 * TOK);
+  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   fence_mbar_init();
-  // The pre-pass lets this grid start only after its own wait for the kernels before it, so
-  // with a pre-pass the groups may be read (and the weights requested) at once; what the
-  // pre-pass writes is waited for by the roles that read it.
-  if (!kF16Mode) pdl_wait();
+  // The pre-pass lets this grid start only after its own wait for the kernels before it, so the
+  // groups may be read (and the weights requested) at once; what the pre-pass writes is waited
+  // for by the roles that read it.
   pdl_launch_dependents();
   bool bad = false;  // offsets out of order or out of range
   for (int e = threadIdx.x; e <= L.E; e += kThreads) {
     const int64_t v = __ldcg(L.offsets + e), c = v < 0 ? 0 : (v > L.pairs ? L.pairs : v);
     bad |= v != c;
-    first[e] = (int)c;
+    T.first[e] = (int)c;
   }
   __syncthreads();
   if (warp == 0) {  // token tiles of each group, summed up
-    const int per = (L.E + 31) / 32;
+    const int per = (L.E + 31) / 32, e0 = lane * per, e1 = min(e0 + per, L.E);
     int sum = 0;
-    for (int e = lane * per; e < (lane + 1) * per && e < L.E; ++e) {
-      const int n = first[e + 1] - first[e];
+    for (int e = e0; e < e1; ++e) {
+      const int n = T.first[e + 1] - T.first[e];
       bad |= n < 0;
-      sum += n > 0 ? (n + TOK - 1) / TOK : 0;
+      sum += n > 0 ? (n + kTok - 1) / kTok : 0;
     }
     int run = sum;
 #pragma unroll
@@ -293,21 +296,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int u = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += u;
     }
+    if (lane == 31) T.start[L.E] = run;
     run -= sum;
-    for (int e = lane * per; e < (lane + 1) * per && e < L.E; ++e) {
-      tstart[e] = run;
-      const int n = first[e + 1] - first[e];
-      run += n > 0 ? (n + TOK - 1) / TOK : 0;
+    for (int e = e0; e < e1; ++e) {
+      T.start[e] = run;
+      const int n = T.first[e + 1] - T.first[e];
+      const int nt = n > 0 ? (n + kTok - 1) / kTok : 0;
+      // nearly equal tiles, whole MMA column blocks; from 8 tiles on full ones (equal ones
+      // rounded up to 16 rows could leave the last tile empty)
+      T.rows[e] = (uint16_t)(nt == 0 || nt >= 8 ? kTok : ((n + nt - 1) / nt + 15) & ~15);
+      for (int t = run; t < run + nt && t < kTileTable; ++t) T.of[t] = (uint16_t)e;
+      run += nt;
     }
-    if (lane == 31) tstart[L.E] = run;
   }
   if (blockIdx.x == 0 && bad) atomicExch(L.status, 6);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t items = (int64_t)tstart[L.E] * L.RT, G = gridDim.x;
-  const int KT = (int)L.KT;
+  const int tiles = T.start[L.E], KT = (int)L.KT, RT = (int)L.RT;
+  const int64_t RGs = (RT + R - 1) / R;
 
   if (warp == 0) {
     // ---------------------------------------------------------- weight producer
@@ -316,14 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t iw = 0, pw = 0;
       int issued = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-        const Item q = item_at(it, L, tstart, first);
+      for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
+        const Item q = item_of(T, w.tile);
+        const int rt0 = w.rg * R, nrt = R == 1 ? 1 : min(R, RT - rt0);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(L.packed) + q.e * L.expert_bytes +
-                             kHeaderBytes + (int64_t)q.rt * KT * TB;
-        for (int kt = 0; kt < KT; ++kt) {
+                             kHeaderBytes + (int64_t)rt0 * KT * TB;
+        for (int kt = 0; kt < KT; ++kt, src += TB) {
           if (!(ok = pf_wait(w_empty + 8 * iw, pw ^ 1u, abort, kWaitNs))) break;
-          mbar_expect_tx(w_full + 8 * iw, TB);
-          bulk_g2s(sW + iw * TB, src + (int64_t)kt * TB, TB, w_full + 8 * iw, pol);
+          mbar_expect_tx(w_full + 8 * iw, nrt * TB);
+          for (int r = 0; r < nrt; ++r)
+            bulk_g2s(sW + (iw * R + r) * TB, src + (int64_t)r * KT * TB, TB, w_full + 8 * iw, pol);
           ++issued;
           if (++iw == NW) { iw = 0; pw ^= 1u; }
         }
@@ -340,60 +350,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- token producer
-    if (!loaders && elect_one()) {
+    if (!LOAD && elect_one()) {
       const uint64_t pol = l2_evict_last_policy();
-      uint32_t ib = 0, pb = 0;
-      int issued = 0;
+      uint32_t is = 0, ps = 0;
       bool ok = true;
       pdl_wait();
-      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-        const Item q = item_at(it, L, tstart, first);
-        const int boxes = (q.n + S::Box - 1) / S::Box;
+      for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
+        const Item q = item_of(T, w.tile);
+        const int boxes = (q.n + kBox - 1) / kBox;
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs))) break;
-          const uint32_t dst = sB + ib * S::BBytes, bar = b_full + 8 * ib;
-          mbar_expect_tx(bar, (uint32_t)(boxes * S::Box * 128));
+          if (!(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          const uint32_t dst = sB + is * kBBytes, bar = full + 8 * is;
+          mbar_expect_tx(bar, (uint32_t)(boxes * kBox * 128));
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(dst + b * S::Box * 128, &tm, kt * kTileK, (int)q.i0 + b * S::Box, bar, pol);
-          ++issued;
-          if (++ib == NB) { ib = 0; pb ^= 1u; }
+            tma_load_2d(dst + b * kBox * 128, &tm, kt * kTileK, (int)q.i0 + b * kBox, bar, pol);
+          if (++is == NS) { is = 0; ps ^= 1u; }
         }
       }
       if (!ok) {
+        // The stages' barriers also count the dequantisers, who may have given up, so there is no
+        // phase to wait for: give the last copies a millisecond, a thousand times what one takes.
         atomicExch(L.status, 5);
-        for (int k = 0; k < NB && k < issued; ++k) {
-          ib = ib == 0 ? NB - 1 : ib - 1;
-          if (ib == NB - 1) pb ^= 1u;
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(b_full + 8 * ib, pb) && globaltimer_ns() - t0 < kWaitNs) {}
-        }
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {}
       }
     }
   } else if (warp == 2) {
     // --------------------------------------------------------------- MMA issuer
     if (elect_one()) {
-      uint32_t ia = 0, pa = 0, ib = 0, pb = 0, ic = 0, pc = 0;
+      uint32_t is = 0, ps = 0, ic = 0, pc = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-        const Item q = item_at(it, L, tstart, first);
-        const bool f16 = kF16Mode && !(FMT == FMT_MX && header_of(L, q.e)->wide);
-        const uint32_t idesc = (f16 ? kIdescF16 : kIdescBF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
-        const uint32_t d = tmem + ic * TOK;
+      for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
+        const Item q = item_of(T, w.tile);
+        const bool two = R == 2 && w.rg * 2 + 1 < RT;
+        const bool wide = FMT == FMT_MX && header_of(L, q.e)->wide;
+        const uint32_t idesc = (wide ? kIdescBF16 : kIdescF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
+        const uint32_t d = tmem + ic * R * kTok;
         if (!(ok = pf_wait(acc_empty + 8 * ic, pc ^ 1u, abort, kWaitNs))) break;
         tc_fence_after();
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = pf_wait(b_full + 8 * ib, pb, abort, kWaitNs))) break;
-          if (!(ok = pf_wait(a_full + 8 * ia, pa, abort, kWaitNs))) break;
-          if (loaders) fence_proxy_async_smem();  // the loaders' copies -> visible to the tensor core
+          if (!(ok = pf_wait(full + 8 * is, ps, abort, kWaitNs))) break;
           tc_fence_after();
-          const uint64_t ad = desc_sw128(sA + ia * kABytes), bd = desc_sw128(sB + ib * S::BBytes);
+          const uint64_t ad = desc_sw128(sA + is * R * kABytes), bd = desc_sw128(sB + is * kBBytes);
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk)  // +32 bytes per 16-element k step
-            mma_f16(d, ad + 2 * kk, bd + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(a_empty + 8 * ia);
-          mma_commit(b_empty + 8 * ib);
-          if (++ia == kNA) { ia = 0; pa ^= 1u; }
-          if (++ib == NB) { ib = 0; pb ^= 1u; }
+          for (int kk = 0; kk < kTileK / 16; ++kk) {  // +32 bytes per 16-element k step
+            const uint32_t acc = (kt > 0 || kk > 0) ? 1u : 0u;
+            mma_f16(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
+            if (two) mma_f16(d + kTok, ad + (kABytes >> 4) + 2 * kk, bd + 2 * kk, idesc, acc);
+          }
+          mma_commit(empty + 8 * is);
+          if (++is == NS) { is = 0; ps ^= 1u; }
         }
         if (!ok) break;
         mma_commit(acc_full + 8 * ic);
@@ -407,229 +413,257 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 3 + 4 * kSets) {
     // ------------------------------------------------------------- dequantisers
     // Set `set` takes the CTA's k steps set, set + kSets, ...; warp jp of the set the row blocks
-    // 2jp and 2jp + 1 (32 rows), whose four scale bytes per lane are one word.
+    // 2jp and 2jp + 1 (32 rows) of each row tile, whose four scale bytes per lane are one word.
     const int set = (warp - 3) >> 2, jp = (warp - 3) & 3, g = lane >> 2, t = lane & 3;
     const uint32_t soff = (uint32_t)scale_offset(FMT, 2 * jp, g, t);
     const uint32_t roff = (uint32_t)(32 * jp + g) * 128;  // row & 7 == g for all four rows
     const uint32_t c0 = (uint32_t)(((2 * t) ^ g) << 4), c1 = (uint32_t)(((2 * t + 1) ^ g) << 4);
-    uint32_t iw = set, pw = 0, ia = set, pa = 0;
+    uint32_t iw = set, pw = 0, is = set, ps = 0;
     int kt = set;
-    bool ok = true;
-    int64_t it = blockIdx.x;
-    while (it < items && kt >= KT) { kt -= KT; it += G; }
-    bool wide = false;
-    int64_t of = -1;  // the item `wide` is of
-    while (it < items) {
-      if (FMT == FMT_MX && of != it) {
-        of = it;
-        wide = header_of(L, item_at(it, L, tstart, first).e)->wide != 0;
-      }
+    bool ok = true, wide = false, fresh = true;
+    Walk w(RGs);
+    while (w.tile < tiles && kt >= KT) { kt -= KT; w.next(); }
+    while (w.tile < tiles) {
+      if (FMT == FMT_MX && fresh) wide = header_of(L, item_of(T, w.tile).e)->wide != 0;
+      const int nrt = R == 1 ? 1 : min(R, RT - w.rg * R);
       if (!(ok = pf_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
-      const uint32_t tb = sW + iw * TB;
-      const int4 cw0 = ld_shared_v4(tb + (2 * jp) * 512 + lane * 16);
-      const int4 cw1 = ld_shared_v4(tb + (2 * jp + 1) * 512 + lane * 16);
-      const uint32_t sc = ld_shared_u32(tb + soff);
-      uint32_t og[2][8], o8[2][8];  // rows g and g + 8 of both row blocks
-      if (FMT == FMT_MX && wide) {
-        dequant_block<FMT, kWide>(cw0, sc, og[0], o8[0]);
-        dequant_block<FMT, kWide>(cw1, sc >> 16, og[1], o8[1]);
-      } else {
-        dequant_block<FMT, kF16Mode ? kF16 : kBF16>(cw0, sc, og[0], o8[0]);
-        dequant_block<FMT, kF16Mode ? kF16 : kBF16>(cw1, sc >> 16, og[1], o8[1]);
-      }
-      // every lane has used what it loaded: only now may the next copy overwrite the stage
-      __syncwarp();
-      if (lane == 0) mbar_arrive(w_empty + 8 * iw);
-      if (!(ok = pf_wait(a_empty + 8 * ia, pa ^ 1u, abort, kWaitNs))) break;
-      const uint32_t at = sA + ia * kABytes + roff;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        st_shared_v4(at + b * 2048 + c0, og[b][0], og[b][1], og[b][2], og[b][3]);
-        st_shared_v4(at + b * 2048 + c1, og[b][4], og[b][5], og[b][6], og[b][7]);
-        st_shared_v4(at + b * 2048 + 1024 + c0, o8[b][0], o8[b][1], o8[b][2], o8[b][3]);
-        st_shared_v4(at + b * 2048 + 1024 + c1, o8[b][4], o8[b][5], o8[b][6], o8[b][7]);
+      for (int r = 0; r < R; ++r) {
+        if (r >= nrt) break;  // warp-uniform
+        const uint32_t tb = sW + (iw * R + r) * TB;
+        const int4 cw0 = ld_shared_v4(tb + (2 * jp) * 512 + lane * 16);
+        const int4 cw1 = ld_shared_v4(tb + (2 * jp + 1) * 512 + lane * 16);
+        const uint32_t sc = ld_shared_u32(tb + soff);
+        uint32_t og[2][8], o8[2][8];  // rows g and g + 8 of both row blocks
+        if (FMT == FMT_MX && wide) {
+          dequant_block<FMT, true>(cw0, sc, og[0], o8[0]);
+          dequant_block<FMT, true>(cw1, sc >> 16, og[1], o8[1]);
+        } else {
+          dequant_block<FMT, false>(cw0, sc, og[0], o8[0]);
+          dequant_block<FMT, false>(cw1, sc >> 16, og[1], o8[1]);
+        }
+        if (r == nrt - 1) {
+          // every lane has used what it loaded: only now may the next copy overwrite the stage
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w_empty + 8 * iw);
+        }
+        if (r == 0 && !(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+        const uint32_t at = sA + (is * R + r) * kABytes + roff;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          st_shared_v4(at + b * 2048 + c0, og[b][0], og[b][1], og[b][2], og[b][3]);
+          st_shared_v4(at + b * 2048 + c1, og[b][4], og[b][5], og[b][6], og[b][7]);
+          st_shared_v4(at + b * 2048 + 1024 + c0, o8[b][0], o8[b][1], o8[b][2], o8[b][3]);
+          st_shared_v4(at + b * 2048 + 1024 + c1, o8[b][4], o8[b][5], o8[b][6], o8[b][7]);
+        }
       }
+      if (!ok) break;
       fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
       __syncwarp();
-      if (lane == 0) mbar_arrive(a_full + 8 * ia);
+      if (lane == 0) mbar_arrive(full + 8 * is);
       if ((iw += kSets) >= NW) { iw -= NW; pw ^= 1u; }
-      if ((ia += kSets) >= kNA) { ia -= kNA; pa ^= 1u; }
+      if ((is += kSets) >= NS) { is -= NS; ps ^= 1u; }
       kt += kSets;
-      while (it < items && kt >= KT) { kt -= KT; it += G; }
+      fresh = kt >= KT;
+      while (w.tile < tiles && kt >= KT) { kt -= KT; w.next(); }
     }
     if (!ok && lane == 0) atomicExch(L.status, 5);
-  } else if (S::Loaders && warp < 19) {
-    // ------------------------------------------------- loaders of gathered rows
-    // Thread: 16-byte chunk c of rows r0, r0 + 16, ...; a row past the tile's tokens reads the
-    // last one again (its products are not stored).
-    if (loaders) {
+  } else if (warp < kEpiWarp0) {
+    if constexpr (LOAD) {
+      // ------------------------------------------------- loaders of gathered rows
+      // Thread: 16-byte chunk c of rows r0, r0 + 16, ...; a row past the tile's tokens reads the
+      // last one again (its products are not stored).  A wide expert's rows come from the
+      // caller's bf16 activations.
       const int tid = (warp - 15) * 32 + lane, c = tid & 7, r0 = tid >> 3;
       const uint32_t doff = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
-      const uint8_t* A = reinterpret_cast<const uint8_t*>(L.A);
-      uint32_t ib = 0, pb = 0;
-      bool ok = true;
-      for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-        const Item q = item_at(it, L, tstart, first);
-        int row[TOK / 16];
+      uint32_t is = 0, ps = 0, last = 0;
+      bool ok = true, held = false;  // held: stage `last` is copied but not handed over
+      auto hand_over = [&](int newer) {
+        if (newer) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();  // this thread's copies -> visible to the tensor core
+        mbar_arrive(full + 8 * last);
+      };
+      pdl_wait();
+      for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
+        const Item q = item_of(T, w.tile);
+        const bool wide = FMT == FMT_MX && header_of(L, q.e)->wide;
+        const uint8_t* A = reinterpret_cast<const uint8_t*>(wide ? L.A : p.Ap);
+        const int64_t ld = (wide ? L.lda : p.ldp) * 2;
+        int row[kTok / 16];
 #pragma unroll
-        for (int i = 0; i < TOK / 16; ++i) {
-          row[i] = 0;
-          if (i * 16 < q.n) {
-            const int j = i * 16 + r0, pr = __ldcg(L.order + q.i0 + (j < q.n ? j : q.n - 1));
-            const bool in = pr >= 0 && pr < L.pairs;
-            if (!in) atomicExch(L.status, 6);
-            row[i] = in ? pr / L.topk : 0;
-          }
+        for (int i = 0; i < kTok / 16; ++i) {
+          const int j = i * 16 + r0;
+          row[i] = __ldcg(L.order + q.i0 + (j < q.n ? j : q.n - 1));
+        }
+#pragma unroll
+        for (int i = 0; i < kTok / 16; ++i) {
+          const bool in = row[i] >= 0 && row[i] < L.pairs;
+          if (!in) atomicExch(L.status, 6);
+          row[i] = in ? (int)((uint32_t)row[i] / (uint32_t)L.topk) : 0;
         }
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, kWaitNs))) break;
-          const uint32_t dst = sB + ib * S::BBytes + doff;
+          if (!mbar_try_wait(empty + 8 * is, ps ^ 1u)) {
+            // no free stage yet: hand over the last one before waiting for it
+            if (held) hand_over(0);
+            held = false;
+            if (!(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          }
+          const uint32_t dst = sB + is * kBBytes + doff;
           const int64_t k = (int64_t)kt * kTileK + c * 8;
           const uint32_t bytes = k < L.K ? 16u : 0u;  // K is a multiple of 16
           const uint8_t* src = A + (k < L.K ? k * 2 : 0);
 #pragma unroll
-          for (int i = 0; i < TOK / 16; ++i)
-            if (i * 16 < q.n) cp_async16(dst + i * 2048, src + (int64_t)row[i] * L.lda * 2, bytes);
-          cp_async_arrive(b_full + 8 * ib);
-          if (++ib == NB) { ib = 0; pb ^= 1u; }
+          for (int i = 0; i < kTok / 16; ++i)
+            if (i * 16 < q.n) cp_async16(dst + i * 2048, src + row[i] * ld, bytes);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (held) hand_over(1);
+          held = true;
+          last = is;
+          if (++is == NS) { is = 0; ps ^= 1u; }
         }
       }
+      if (ok && held) hand_over(0);
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) atomicExch(L.status, 5);
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    // Four warps, warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16 tokens at a time:
-    // fragments from TMEM, scaled, rounded to bf16, transposed through shared memory and stored
-    // as rows of 128 (SiLU: 64) contiguous columns.
+    // Four warps, warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16 tokens at a
+    // time: fragments from TMEM, scaled, rounded to bf16, transposed through shared memory
+    // and stored as rows of 128 (64) contiguous columns.
     const int qd = warp & 3, tid = qd * 32 + lane, t = lane & 3;
-    constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16;
+    constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16, kChunk = 16;
     const uint32_t sT = sX + (SILU ? 8192 : 0);
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
     const bool vec = (uintptr_t)L.C % 16 == 0 && L.ldc % 8 == 0;
+    const bool up = SILU && qd >= 2;
     const int64_t ncols = SILU ? L.seg_split : L.N;
     uint32_t ic = 0, pc = 0, chunk = 0;
     bool ok = true;
     pdl_wait();
-    for (int64_t it = blockIdx.x; ok && it < items; it += G) {
-      const Item q = item_at(it, L, tstart, first);
+    // this thread's token of the item: its pair, fetched an item ahead
+    Walk w(RGs);
+    int pair = 0;
+    auto fetch = [&]() {
+      if ((L.scatter || LOAD) && w.tile < tiles) {
+        const Item q = item_of(T, w.tile);
+        pair = tid < q.n ? __ldcg(L.order + q.i0 + tid) : 0;
+      }
+    };
+    fetch();
+    while (ok && w.tile < tiles) {
+      const Item q = item_of(T, w.tile);
+      const int rt0 = w.rg * R, nrt = R == 1 ? 1 : min(R, RT - rt0);
       const PackedHeader* hdr = header_of(L, q.e);
-      const bool up = SILU && qd >= 2;
       const float f0 = hdr->factor[up ? 1 : 0], f1 = hdr->factor[1];
-      const int64_t n0 = (int64_t)q.rt * kCols;
-      int2* tok = s_tok + ic * TOK;
-#pragma unroll
-      for (int h = 0; h < TOK / 128; ++h) {
-        const int j = h * 128 + tid;
+      const bool wide = FMT == FMT_MX && hdr->wide;
+      int2* tok = s_tok + ic * kTok;
+      {
         int row = -1;
         float rs = 1.0f;
-        if (j < q.n) {
-          row = (int)(q.i0 + j);
-          if (kF16Mode) rs = __ldcg(p.rowscale + row);
-          if (L.scatter) {
-            row = __ldcg(L.order + row);
-            if (row < 0 || row >= L.pairs) {
-              row = -1;
-              atomicExch(L.status, 6);
-            }
-          }
+        if (tid < q.n) {
+          row = (int)q.i0 + tid;
+          bool in = true;
+          if (L.scatter || LOAD) in = pair >= 0 && pair < L.pairs;
+          if (!in) atomicExch(L.status, 6);
+          if (!wide && in) rs = __ldcg(p.rowscale + (LOAD ? (int64_t)((uint32_t)pair / (uint32_t)L.topk) : row));
+          if (L.scatter) row = in ? pair : -1;
         }
-        tok[j] = make_int2(row, __float_as_int(rs));
+        tok[tid] = make_int2(row, __float_as_int(rs));
       }
+      w.next();
+      fetch();
       epilogue_sync();
       if (!(ok = pf_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
       tc_fence_after();
-      const uint32_t ta = tmem + ic * TOK + ((uint32_t)(qd * 32) << 16);
-      for (int c = 0; c * 16 < q.n; ++c, ++chunk) {
-        uint32_t v[2][8];  // weight rows [0, 16) and [16, 32) of the warp's 32
-        tmem_ld_frag(ta + c * 16, v[0]);
-        tmem_ld_frag(ta + c * 16 + (16u << 16), v[1]);
-        // scales of this lane's tokens 2t, 2t + 1 and the same 8 on
-        float rs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if (kF16Mode) {
-          const int4 a = *reinterpret_cast<const int4*>(tok + c * 16 + 2 * t);
-          const int4 b = *reinterpret_cast<const int4*>(tok + c * 16 + 8 + 2 * t);
-          rs[0] = __int_as_float(a.y);
-          rs[1] = __int_as_float(a.w);
-          rs[2] = __int_as_float(b.y);
-          rs[3] = __int_as_float(b.w);
-        }
-        tmem_wait_frags(v[0], v[1]);
-        float x[2][8];
+      for (int r = 0; r < nrt; ++r) {
+        const uint32_t ta = tmem + (ic * R + r) * kTok + ((uint32_t)(qd * 32) << 16);
+        const int64_t n0 = (int64_t)(rt0 + r) * kCols;
+        for (int c = 0; c * kChunk < q.n; ++c, ++chunk) {
+          const uint32_t buf = sT + (chunk & 1) * (kChunk * kRowB);
+          constexpr int kH = kChunk / 16;
+          uint32_t v[kH][2][8];  // 16 tokens x weight rows [0, 16), [16, 32) of the warp's 32
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float y = __uint_as_float(v[h][i]);
-            if (kF16Mode) y *= rs[(i & 1) + (i >> 2) * 2];
-            x[h][i] = y * f0;
+          for (int u = 0; u < kH; ++u) {
+            tmem_ld_frag(ta + c * kChunk + u * 16, v[u][0]);
+            tmem_ld_frag(ta + c * kChunk + u * 16 + (16u << 16), v[u][1]);
           }
-        const uint32_t buf = sT + (chunk & 1) * (16 * kRowB);
-        if constexpr (SILU) {
-          // warps 0-1 hold gate rows, warps 2-3 the matching up rows in the same places: of
-          // every 16 tokens the gate warps finish the first 8 and the up warps the others
-          const uint32_t ex = sX + (chunk & 1) * 4096 + lane * 16;
+          float x[kH][2][8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            st_shared_v4(ex + (qd * 2 + h) * 512, __float_as_uint(up ? x[h][0] : x[h][4]),
-                         __float_as_uint(up ? x[h][1] : x[h][5]), __float_as_uint(up ? x[h][2] : x[h][6]),
-                         __float_as_uint(up ? x[h][3] : x[h][7]));
-          epilogue_sync();
-          uint32_t o[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int4 z = ld_shared_v4(ex + ((qd ^ 2) * 2 + h) * 512);
-            const float zz[4] = {__int_as_float(z.x), __int_as_float(z.y), __int_as_float(z.z),
-                                 __int_as_float(z.w)};
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              y[i] = up ? silu_f(zz[i]) * x[h][4 + i] : silu_f(x[h][i]) * zz[i];
-            o[2 * h] = pack_bf16(y[0], y[1]);
-            o[2 * h + 1] = pack_bf16(y[2], y[3]);
-          }
-          stmatrix_t4(buf + ((up ? 8 : 0) + (lane & 7)) * kRowB + ((qd & 1) * 32 + (lane >> 3) * 8) * 2,
-                      o[0], o[1], o[2], o[3]);
-        } else {
-          if (n0 + 128 > L.seg_split && L.seg_split < L.N) {
-            // the tile reaches into the second segment: its rows take that one's factor
-            const int64_t split = L.seg_split - n0 - qd * 32;
+          for (int u = 0; u < kH; ++u) {
+            // scales of this lane's tokens 2t, 2t + 1 and the same 8 on
+            const int4 sa = *reinterpret_cast<const int4*>(tok + c * kChunk + u * 16 + 2 * t);
+            const int4 sb = *reinterpret_cast<const int4*>(tok + c * kChunk + u * 16 + 8 + 2 * t);
+            const float rs[4] = {__int_as_float(sa.y), __int_as_float(sa.w), __int_as_float(sb.y),
+                                 __int_as_float(sb.w)};
+            tmem_wait_frags(v[u][0], v[u][1]);
+            const int64_t split = L.seg_split - n0 - qd * 32;  // first row of the second factor
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (h * 16 + (lane >> 2) + ((i >> 1) & 1) * 8 >= split) {
-                  float y = __uint_as_float(v[h][i]);
-                  if (kF16Mode) y *= rs[(i & 1) + (i >> 2) * 2];
-                  x[h][i] = y * f1;
-                }
+              for (int i = 0; i < 8; ++i) {
+                const float f = SILU || h * 16 + (lane >> 2) + ((i >> 1) & 1) * 8 < split ? f0 : f1;
+                x[u][h][i] = __uint_as_float(v[u][h][i]) * rs[(i & 1) + (i >> 2) * 2] * f;
+              }
           }
+          if constexpr (SILU) {
+            // warps 0-1 hold gate rows, warps 2-3 the matching up rows in the same places: of
+            // every 16 tokens the gate warps finish the first 8 and the up warps the others
+            const uint32_t ex = sX + (chunk & 1) * 4096 + lane * 16;
+            const float (&y)[2][8] = x[0];
 #pragma unroll
-          for (int th = 0; th < 2; ++th)
-            stmatrix_t4(buf + (th * 8 + (lane & 7)) * kRowB + (qd * 32 + (lane >> 3) * 8) * 2,
-                        pack_bf16(x[0][4 * th], x[0][4 * th + 1]),
-                        pack_bf16(x[0][4 * th + 2], x[0][4 * th + 3]),
-                        pack_bf16(x[1][4 * th], x[1][4 * th + 1]),
-                        pack_bf16(x[1][4 * th + 2], x[1][4 * th + 3]));
-        }
-        epilogue_sync();
-        constexpr int kPieces = kCols / 8;  // 16-byte pieces of a token's columns
+            for (int h = 0; h < 2; ++h)
+              st_shared_v4(ex + (qd * 2 + h) * 512, __float_as_uint(up ? y[h][0] : y[h][4]),
+                           __float_as_uint(up ? y[h][1] : y[h][5]),
+                           __float_as_uint(up ? y[h][2] : y[h][6]),
+                           __float_as_uint(up ? y[h][3] : y[h][7]));
+            epilogue_sync();
+            uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 16 * kPieces / 128; ++i) {
-          const int j = (i * 128 + tid) / kPieces, pc8 = (i * 128 + tid) % kPieces;
-          const int row = tok[c * 16 + j].x;
-          const int64_t n = n0 + pc8 * 8;
-          if (row < 0 || n >= ncols) continue;
-          const int4 d = ld_shared_v4(buf + j * kRowB + pc8 * 16);
-          __nv_bfloat16* dst = C + (int64_t)row * L.ldc + n;
-          if (vec && n + 8 <= ncols) {
-            *reinterpret_cast<int4*>(dst) = d;
+            for (int h = 0; h < 2; ++h) {
+              const int4 z = ld_shared_v4(ex + ((qd ^ 2) * 2 + h) * 512);
+              const float zz[4] = {__int_as_float(z.x), __int_as_float(z.y), __int_as_float(z.z),
+                                   __int_as_float(z.w)};
+              float a[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                a[i] = up ? silu_f(zz[i]) * y[h][4 + i] : silu_f(y[h][i]) * zz[i];
+              o[2 * h] = pack_bf16(a[0], a[1]);
+              o[2 * h + 1] = pack_bf16(a[2], a[3]);
+            }
+            stmatrix_t4(buf + ((up ? 8 : 0) + (lane & 7)) * kRowB + ((qd & 1) * 32 + (lane >> 3) * 8) * 2,
+                        o[0], o[1], o[2], o[3]);
           } else {
-            const uint32_t w[4] = {(uint32_t)d.x, (uint32_t)d.y, (uint32_t)d.z, (uint32_t)d.w};
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (n + b < ncols)
-                reinterpret_cast<uint16_t*>(dst)[b] = (uint16_t)(w[b >> 1] >> ((b & 1) * 16));
+            for (int u = 0; u < kH; ++u)
+#pragma unroll
+              for (int th = 0; th < 2; ++th)
+                stmatrix_t4(buf + (u * 16 + th * 8 + (lane & 7)) * kRowB + (qd * 32 + (lane >> 3) * 8) * 2,
+                            pack_bf16(x[u][0][4 * th], x[u][0][4 * th + 1]),
+                            pack_bf16(x[u][0][4 * th + 2], x[u][0][4 * th + 3]),
+                            pack_bf16(x[u][1][4 * th], x[u][1][4 * th + 1]),
+                            pack_bf16(x[u][1][4 * th + 2], x[u][1][4 * th + 3]));
+          }
+          epilogue_sync();
+          constexpr int kPieces = kCols / 8;  // 16-byte pieces of a token's columns
+#pragma unroll
+          for (int i = 0; i < kChunk * kPieces / 128; ++i) {
+            const int j = (i * 128 + tid) / kPieces, pc8 = (i * 128 + tid) % kPieces;
+            const int row = tok[c * kChunk + j].x;
+            const int64_t n = n0 + pc8 * 8;
+            if (row < 0 || n >= ncols) continue;
+            const int4 d = ld_shared_v4(buf + j * kRowB + pc8 * 16);
+            __nv_bfloat16* dst = C + (int64_t)row * L.ldc + n;
+            if (vec && n + 8 <= ncols) {
+              *reinterpret_cast<int4*>(dst) = d;
+            } else {
+              const uint32_t w4[4] = {(uint32_t)d.x, (uint32_t)d.y, (uint32_t)d.z, (uint32_t)d.w};
+#pragma unroll
+              for (int b = 0; b < 8; ++b)
+                if (n + b < ncols)
+                  reinterpret_cast<uint16_t*>(dst)[b] = (uint16_t)(w4[b >> 1] >> ((b & 1) * 16));
+            }
           }
         }
       }
@@ -646,24 +680,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * TOK);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// Activation pre-pass of the f16 operands, rows in group order: A'[i][k] = A[row(i)][k] * 2^-p in
-// f16, p the power of two of the row's largest magnitude (act_pow2), rowscale[i] = 2^p; a row of
-// a `wide` expert is copied as bf16 with scale 1.  One block per grouped row.
+// Activation pre-pass: A'[i][k] = A[row(i)][k] * 2^-p in f16, p the power of two of the row's
+// largest magnitude (act_pow2), rowscale[i] = 2^p.  One block per row: grouped row i (a row of a
+// `wide` expert is copied as bf16 with scale 1), or, per_token, the caller's row i.
 constexpr int kPrepThreads = 128;
 __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t ldp,
+                                                              int per_token,
                                                               __half* __restrict__ Ap,
                                                               float* __restrict__ rowscale) {
   __shared__ int s_max[kPrepThreads / 32], s_e;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t i = blockIdx.x;
-  if (i >= __ldcg(L.offsets + L.E)) return;  // a pair in no group
+  if (!per_token && i >= __ldcg(L.offsets + L.E)) return;  // a pair in no group
   int64_t m = i;
-  if (L.gather) {
+  if (L.gather && !per_token) {
     const int pr = __ldcg(L.order + i);
     const bool in = pr >= 0 && pr < L.pairs;
     if (!in && threadIdx.x == 0) atomicExch(L.status, 6);
@@ -672,7 +707,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
   const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(L.A) + m * L.lda);
   uint4* dst = reinterpret_cast<uint4*>(Ap + i * ldp);
   const int64_t ng = L.K / 8;
-  if (L.fmt == FMT_MX) {
+  if (L.fmt == FMT_MX && !per_token) {
     if (threadIdx.x == 0) s_e = 0;
     __syncthreads();
     for (int e = threadIdx.x; e < L.E; e += kPrepThreads)
@@ -761,49 +796,40 @@ cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* at, dim3 grid, int threads, i
   return cfg;
 }
 
-template <int FMT, bool SILU, int TOK>
-cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p,
-                        int grid, cudaStream_t s) {
+template <int FMT, bool SILU, int R, bool LOAD>
+cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream_t s) {
+  using S = Map<FMT, R, LOAD>;
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Map<FMT, TOK>::smem(kMaxGroups));
+    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, R, LOAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::smem(kMaxGroups));
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
-  cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg =
-      pdl_config(&at, dim3((unsigned)grid), kThreads, Map<FMT, TOK>::smem(p.L.E), s);
-  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, TOK>, tm, p);
-}
-
-template <int TOK>
-cudaError_t launch_tok(const CUtensorMap& tm, const RaggedParams& p,
-                       cudaStream_t s) {
-  const RaggedLaunch& L = p.L;
   // at most one partial token tile per group in use
-  const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
-  const int64_t most = (groups + L.pairs / TOK) * L.RT;
+  const int64_t groups = p.L.pairs < p.L.E ? p.L.pairs : p.L.E;
+  const int64_t most = (groups + p.L.pairs / kTok) * ((p.L.RT + R - 1) / R);
   const int grid = (int)(sm_count() < most ? sm_count() : most);
-  if (L.fmt == FMT_NV) return L.silu ? launch_main<FMT_NV, true, TOK>(tm, p, grid, s)
-                                     : launch_main<FMT_NV, false, TOK>(tm, p, grid, s);
-  return L.silu ? launch_main<FMT_MX, true, TOK>(tm, p, grid, s)
-                : launch_main<FMT_MX, false, TOK>(tm, p, grid, s);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)grid), kThreads, S::smem(p.L.E), s);
+  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, R, LOAD>, tm, p);
 }
 
-inline int64_t ld_f16(int64_t KT) { return KT * kTileK; }
-
-bool use_f16(int64_t pairs, int64_t E) { return pairs <= 192 * E; }
+template <int FMT, bool SILU>
+cudaError_t launch_fmt(const CUtensorMap& tm, const RaggedParams& p, bool wide_items, bool load,
+                       cudaStream_t s) {
+  if (!wide_items) return launch_main<FMT, SILU, 1, false>(tm, p, s);
+  return load ? launch_main<FMT, SILU, 2, true>(tm, p, s) : launch_main<FMT, SILU, 2, false>(tm, p, s);
+}
 
 }  // namespace
 
-size_t ragged_act_bytes(int64_t pairs, int64_t E, int64_t KT) {
-  const int64_t most = 192 * E, rows = pairs < most ? pairs : most;
-  return (size_t)((rows * 4 + 255) / 256 * 256 + rows * ld_f16(KT) * 2);
+size_t ragged_act_bytes(int64_t pairs, int64_t KT) {
+  return (size_t)((pairs * 4 + 255) / 256 * 256 + pairs * KT * kTileK * 2);
 }
 
 cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
@@ -811,35 +837,36 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   if (!enc) return cudaErrorNotSupported;
   RaggedParams p;
   p.L = L;
-  p.rowscale = nullptr;
+  p.ldp = L.KT * kTileK;
+  float* rowscale = reinterpret_cast<float*>(L.act);
+  __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (L.pairs * 4 + 255) / 256 * 256);
+  p.rowscale = rowscale;
+  p.Ap = ap;
+  // One row tile per item while two would leave SMs without one.
+  const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
+  const bool two = groups * ((L.RT + 1) / 2) >= sm_count();
+  // Gathered rows: the pre-pass writes them in group order while that is little data, else it
+  // converts each token once and the loaders gather.
+  const bool load = L.gather && L.topk > 1 && two && L.pairs * L.K > (8 << 20);
+  const int64_t rows = load ? L.pairs / L.topk : L.pairs;
   // the rows as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
-  auto encode = [&](CUtensorMap* tm, CUtensorMapDataType type, void* at, int64_t ld, int64_t rows,
-                    int rbox) {
-    const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)rbox};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(tm, type, 2, at, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
   CUtensorMap tm;
-  if (use_f16(L.pairs, L.E)) {
-    float* rowscale = reinterpret_cast<float*>(L.act);
-    __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (L.pairs * 4 + 255) / 256 * 256);
-    if (!encode(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ap, ld_f16(L.KT), L.pairs, Map<FMT_NV, 128>::Box))
-      return cudaErrorInvalidValue;
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)L.pairs), kPrepThreads, 0, s);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, ld_f16(L.KT), ap, rowscale);
-    if (e != cudaSuccess) return e;
-    p.rowscale = rowscale;
-    return launch_tok<128>(tm, p, s);
-  }
-  if (!encode(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void*>(L.A), L.lda,
-              L.gather ? L.pairs / L.topk : L.pairs, Map<FMT_NV, 256>::Box))
+  const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.ldp * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)kBox};
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ap, dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  return launch_tok<256>(tm, p, s);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)rows), kPrepThreads, 0, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, p.ldp, load ? 1 : 0, ap, rowscale);
+  if (e != cudaSuccess) return e;
+  if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, load, s)
+                                     : launch_fmt<FMT_NV, false>(tm, p, two, load, s);
+  return L.silu ? launch_fmt<FMT_MX, true>(tm, p, two, load, s)
+                : launch_fmt<FMT_MX, false>(tm, p, two, load, s);
 }
 
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,

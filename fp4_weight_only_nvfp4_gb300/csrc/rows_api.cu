@@ -51,7 +51,7 @@ vt_status check_workspace(const void* ws, size_t have, size_t need) {
 constexpr size_t kActOff = 256;
 inline int64_t scratch_ld(int64_t N) { return (N + 7) / 8 * 8; }
 size_t act_end(vt_fp4_handle W, int64_t pairs) {
-  return kActOff + up256(ragged_act_bytes(pairs, W->E, W->KT));
+  return kActOff + up256(ragged_act_bytes(pairs, W->KT));
 }
 
 vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* order,

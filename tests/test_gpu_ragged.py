@@ -143,6 +143,28 @@ def test_combine(fmt, M, topk, E, N, K):
     assert vt.workspace_status(ws_) == 0
 
 
+@pytest.mark.parametrize("fmt", [vt.NVFP4, vt.MXFP4])
+@pytest.mark.parametrize("M,topk,E,N,K,wide", [
+    (60, 4, 200, 300, 96, False),      # enough groups for two weight row tiles per item, an odd one last
+    (500, 3, 170, 128, 352, True),     # a single row tile; mixed operand types
+    (2100, 8, 64, 640, 544, True)])    # more gathered rows than are written in group order first
+def test_many_items(fmt, M, topk, E, N, K, wide):
+    rng = np.random.default_rng(M)
+    wide = wide and fmt == vt.MXFP4
+    W, ws = _plain(rng, fmt, E, N, K, wide)
+    Wp, (wg, wu) = _paired(rng, fmt, E, N // 2 - 3, K, wide)
+    ids = _ids(rng, M, topk, E)
+    groups, order, offsets = _groups(ids, E)
+    x = acts(rng, M, K)
+    ref, err = _ref(f64(x), ws, order, offsets, topk, True)
+    assert_close(vt.w4a16_gemm_ragged(x.cuda(), W, groups), ref, err)
+    assert_close(f64(vt.w4a16_gemm_ragged(x.cuda(), W, groups, scatter=True))[order], ref, err)
+    h = f64(vt.w4a16_gemm_ragged_silu_mul(x.cuda(), Wp, groups))
+    for e in range(E):
+        i = np.arange(offsets[e], offsets[e + 1])
+        assert_close(h[i], *silu_mul64(f64(x)[order[i] // topk], wg[e], wu[e]))
+
+
 def test_wide_mx_scales():
     rng = np.random.default_rng(3)
     E, N, K, M = 3, 140, 256, 37
