@@ -25,50 +25,48 @@ __device__ __forceinline__ float load_logit(const void* p, int bf16, int64_t i) 
               : reinterpret_cast<const float*>(p)[i];
 }
 
-constexpr int kRouteWarps = 8;
-constexpr int kPerLane = kMaxGroups / 32;
-
-// One warp per token: every lane keeps its E / 32 keys in registers; topk times the warp takes
-// the largest key (lowest index among equals) and removes it.
-__global__ void __launch_bounds__(kRouteWarps * 32) k_topk(const RouteLaunch L) {
-  const int lane = threadIdx.x & 31;
-  const int64_t m = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (m >= L.M) return;
-  uint32_t key[kPerLane];
-  float mx = -INFINITY, sum = 0.0f;
+// One token per warp: lane j of the first topk returns its j-th choice and weight (id -1 where
+// no expert is left).  Every lane keeps PER keys, of experts lane, lane + 32, ...; topk times the
+// warp takes the largest (lowest index among equals) and removes it.
+template <int PER>
+__device__ __forceinline__ void topk_token(const RouteLaunch& L, int64_t m, int lane, int& id,
+                                           float& w) {
+  uint32_t key[PER];
+  float mx = -INFINITY;
+  auto logit = [&](int e) { return load_logit(L.logits, L.bf16, m * L.ld + e); };
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    key[i] = 0;
-    if (e < L.E) {
-      const float l = load_logit(L.logits, L.bf16, m * L.ld + e);
-      float sc = l;
-      if (L.scoring == 1) {
-        sc = 1.0f / (1.0f + expf(-l));
-        if (L.bias) sc += L.bias[e];
-      }
-      key[i] = l == -INFINITY ? 0u : score_key(sc);
-      mx = fmaxf(mx, l);
+    const float l = e < L.E ? logit(e) : -INFINITY;
+    float sc = l;
+    if (L.scoring == 1) {
+      sc = 1.0f / (1.0f + expf(-sc));
+      if (L.bias && e < L.E) sc += L.bias[e];
     }
+    key[i] = l == -INFINITY ? 0u : score_key(sc);
+    mx = fmaxf(mx, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (L.scoring == 0) {
+  // softmax over all experts: only where the weights are not divided by their own sum
+  float sum = 1.0f;
+  if (L.scoring == 0 && !L.renormalize) {
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = i * 32 + lane;
-      if (e < L.E && key[i]) sum += expf(load_logit(L.logits, L.bf16, m * L.ld + e) - mx);
-    }
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane < L.E) {
+        const float l = logit(i * 32 + lane);
+        if (l != -INFINITY) sum += expf(l - mx);
+      }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  int id = -1;        // lane j: the j-th choice
-  float w = 0.0f;
+  id = -1;
   for (int j = 0; j < L.topk; ++j) {
     uint32_t best = 0;
     int at = 0x7FFFFFFF;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
+    for (int i = 0; i < PER; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i * 32 + lane;
@@ -77,90 +75,272 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_topk(const RouteLaunch L) 
     if (top == 0) break;
     const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
+    for (int i = 0; i < PER; ++i)
       if (i * 32 + lane == e) key[i] = 0;
-    if (lane == j) {
-      id = e;
-      const float l = load_logit(L.logits, L.bf16, m * L.ld + e);
-      w = L.scoring == 1 ? 1.0f / (1.0f + expf(-l)) : expf(l - mx) / sum;
-    }
+    if (lane == j) id = e;
+  }
+  w = 0.0f;
+  if (id >= 0) {
+    const float l = logit(id);
+    w = L.scoring == 1 ? 1.0f / (1.0f + expf(-l)) : expf(l - mx) / sum;
   }
   if (L.renormalize) {
     float s = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (id >= 0) w /= s;
+    if (id >= 0 && s != 0.0f) w /= s;  // all weights 0 stay 0
   }
-  if (lane < L.topk) {
-    L.ids[m * L.topk + lane] = id;
-    L.weights[m * L.topk + lane] = id >= 0 ? w * L.scale : 0.0f;
-  }
+  w *= L.scale;
 }
 
-// Group e's pairs (block e; block E: the pairs in no group): counted, then, once every count
-// is known, written in pair order.
-constexpr int kGroupBlock = 256;
-__device__ __forceinline__ bool in_group(int id, int e, int E) {
-  return e < E ? id == e : (id < 0 || id >= E);
-}
+__device__ __forceinline__ int group_of_id(int id, int E) { return id >= 0 && id < E ? id : E; }
 
-__global__ void __launch_bounds__(kGroupBlock) k_count(const int32_t* ids, int64_t P, int E,
-                                                       int* counts) {
-  __shared__ int total;
-  if (threadIdx.x == 0) total = 0;
+// A block's exclusive scan of v[0 .. n) in shared memory, in place; T threads.
+template <int T>
+__device__ __forceinline__ void block_scan(int* v, int n, int* s_warp) {
+  const int per = (n + T - 1) / T, b = (int)threadIdx.x * per, lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int i = b; i < b + per && i < n; ++i) sum += v[i];
+  int run = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += u;
+  }
+  if (lane == 31) s_warp[threadIdx.x >> 5] = run;
   __syncthreads();
-  int n = 0;
-  for (int64_t i = threadIdx.x; i < P; i += kGroupBlock) n += in_group(ids[i], blockIdx.x, E);
-  atomicAdd(&total, n);
-  __syncthreads();
-  if (threadIdx.x == 0) counts[blockIdx.x] = total;
-}
-
-__global__ void __launch_bounds__(kGroupBlock) k_scatter(const int32_t* ids, int64_t P, int E,
-                                                         const int* counts, int32_t* order,
-                                                         int32_t* offsets) {
-  __shared__ int s_base, s_warp[kGroupBlock / 32];
-  const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    int b = 0;
-    for (int i = 0; i < e; ++i) b += counts[i];
-    s_base = b;
-    offsets[e] = b;  // block E: the number of grouped pairs
+  run -= sum;
+  for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) run += s_warp[w];
+  for (int i = b; i < b + per && i < n; ++i) {
+    const int x = v[i];
+    v[i] = run;
+    run += x;
   }
   __syncthreads();
-  int base = s_base;
-  for (int64_t i0 = 0; i0 < P; i0 += kGroupBlock) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool in = i < P && in_group(ids[i], e, E);
-    const uint32_t b = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) s_warp[warp] = __popc(b);
-    __syncthreads();
-    int before = __popc(b & ((1u << lane) - 1u)), all = 0;
-    for (int w = 0; w < kGroupBlock / 32; ++w) {
-      if (w < warp) before += s_warp[w];
-      all += s_warp[w];
+}
+
+// Stable places of a block's pairs [p0, p1): warp w takes a run of `run` pairs (a multiple of 32),
+// counts per group its own pairs in order, the warps' counts are summed in warp order behind
+// base[group], and each pair goes to base + earlier warps' + its rank in the warp.
+template <int T, typename Count>
+__device__ __forceinline__ void place_pairs(const int32_t* ids, int64_t p0, int64_t p1, int E,
+                                            const int* base, Count* wc, int32_t* order) {
+  constexpr int W = T / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, GE = E + 1;
+  const int64_t run = ((p1 - p0 + T - 1) / T) * 32;
+  const int64_t w0 = p0 + warp * run, w1 = w0 + run < p1 ? w0 + run : p1;
+  for (int i = threadIdx.x; i < W * GE; i += T) wc[i] = 0;
+  __syncthreads();
+  Count* mine = wc + warp * GE;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int64_t q = w0; q < w1; q += 32) {
+      const int64_t i = q + lane;
+      const int e = i < w1 ? group_of_id(ids[i], E) : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const int before = e >= 0 ? mine[e] : 0;
+      __syncwarp();
+      if (e >= 0) {
+        if (rank == 0) mine[e] = (Count)(before + __popc(same));
+        if (pass) order[base[e] + before + rank] = (int32_t)i;
+      }
+      __syncwarp();
     }
-    if (in) order[base + before] = (int32_t)i;
-    base += all;
-    __syncthreads();
+    if (pass == 0) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < GE; e += T) {
+        int sum = 0;
+        for (int w = 0; w < W; ++w) {
+          const int c = (int)wc[w * GE + e];
+          wc[w * GE + e] = (Count)sum;
+          sum += c;
+        }
+      }
+      __syncthreads();
+    }
   }
+}
+
+// Everything in one block: few pairs, where a launch costs more than the work.
+constexpr int kOneThreads = 1024;
+constexpr int64_t kOnePairs = 1024;
+inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + kOneThreads / 32 * 2) + 16; }
+
+template <int PER>
+__global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) {
+  extern __shared__ int s_dyn[];
+  __shared__ int s_warp[kOneThreads / 32], s_ids[kOnePairs];
+  int* total = s_dyn;  // [E + 1]
+  uint16_t* wc = reinterpret_cast<uint16_t*>(s_dyn + L.E + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = (int)L.M * L.topk;
+  for (int e = threadIdx.x; e <= L.E; e += kOneThreads) total[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  if (L.logits) {
+    for (int m = warp; m < L.M; m += kOneThreads / 32) {
+      int id;
+      float w;
+      topk_token<PER>(L, m, lane, id, w);
+      if (lane < L.topk) {
+        L.ids[m * L.topk + lane] = id;
+        L.weights[m * L.topk + lane] = w;
+        s_ids[m * L.topk + lane] = id;
+        atomicAdd(total + group_of_id(id, L.E), 1);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < P; i += kOneThreads) {
+      s_ids[i] = L.ids[i];
+      atomicAdd(total + group_of_id(s_ids[i], L.E), 1);
+    }
+  }
+  __syncthreads();
+  block_scan<kOneThreads>(total, L.E + 1, s_warp);
+  for (int e = threadIdx.x; e <= L.E; e += kOneThreads) L.offsets[e] = total[e];
+  place_pairs<kOneThreads>(s_ids, 0, P, L.E, total, wc, L.order);
+}
+
+// Many pairs: block c counts its run of pairs per group (after choosing them, where there are
+// logits); a second launch sums the blocks' counts and places the pairs.
+constexpr int kManyThreads = 512;
+constexpr int kManyBlocks = 152;
+
+__host__ __device__ inline int64_t block_pairs(int64_t P, int topk, int blocks) {
+  const int64_t M = P / topk;
+  return (M + blocks - 1) / blocks * topk;  // whole tokens
+}
+
+template <int PER>
+__global__ void __launch_bounds__(kManyThreads) k_route_count(const RouteLaunch L, int* hist) {
+  __shared__ int s_count[kMaxGroups + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = threadIdx.x; e <= L.E; e += kManyThreads) s_count[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
+  const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
+  if (L.logits) {
+    for (int64_t m = p0 / L.topk + warp; m * L.topk < p1; m += kManyThreads / 32) {
+      int id;
+      float w;
+      topk_token<PER>(L, m, lane, id, w);
+      if (lane < L.topk) {
+        L.ids[m * L.topk + lane] = id;
+        L.weights[m * L.topk + lane] = w;
+        atomicAdd(s_count + group_of_id(id, L.E), 1);
+      }
+    }
+  } else {
+    for (int64_t i = p0 + threadIdx.x; i < p1; i += kManyThreads)
+      atomicAdd(s_count + group_of_id(L.ids[i], L.E), 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= L.E; e += kManyThreads) hist[blockIdx.x * (L.E + 1) + e] = s_count[e];
+}
+
+inline size_t many_smem(int E) { return (size_t)(E + 1) * (8 + kManyThreads / 32 * 4); }
+
+__global__ void __launch_bounds__(kManyThreads) k_route_place(const RouteLaunch L, const int* hist) {
+  extern __shared__ int s_dyn[];
+  __shared__ int s_warp[kManyThreads / 32];
+  int* total = s_dyn;                // [E + 1]
+  int* before = total + L.E + 1;     // [E + 1] of the blocks before this one
+  uint32_t* wc = reinterpret_cast<uint32_t*>(before + L.E + 1);
+  const int GE = L.E + 1;
+  for (int e = threadIdx.x; e < GE; e += kManyThreads) total[e] = before[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int all = (int)gridDim.x * GE, mine = (int)blockIdx.x * GE;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < all; i += kManyThreads) {
+    const int v = __ldcg(hist + i), e = i % GE;
+    if (v) {
+      atomicAdd(total + e, v);
+      if (i < mine) atomicAdd(before + e, v);
+    }
+  }
+  __syncthreads();
+  block_scan<kManyThreads>(total, GE, s_warp);
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < GE; e += kManyThreads) L.offsets[e] = total[e];
+  for (int e = threadIdx.x; e < GE; e += kManyThreads) before[e] += total[e];
+  __syncthreads();
+  const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
+  const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
+  if (p0 < p1) place_pairs<kManyThreads>(L.ids, p0, p1, L.E, before, wc, L.order);
+}
+
+template <typename F>
+cudaError_t launch_pdl(F f, int grid, int threads, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return f(cfg);
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, int (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    done[dev] = 1;
+  }
+  return cudaSuccess;
+}
+
+template <int PER>
+cudaError_t route_per(const RouteLaunch& L, cudaStream_t s) {
+  const int64_t P = L.M * L.topk;
+  if (P <= kOnePairs) {
+    static int done[64] = {0};
+    const cudaError_t e = allow_smem(k_route_one<PER>, one_smem(kMaxGroups), done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl([&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_one<PER>, L); },
+                      1, kOneThreads, one_smem(L.E), s);
+  }
+  static int done[64] = {0};
+  cudaError_t e = allow_smem(k_route_place, many_smem(kMaxGroups), done);
+  if (e != cudaSuccess) return e;
+  int* hist = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(L.workspace) + 256);
+  const int64_t want = (P + 255) / 256;
+  const int blocks = (int)(want < kManyBlocks ? want : kManyBlocks);
+  e = launch_pdl(
+      [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_count<PER>, L, hist); },
+      blocks, kManyThreads, 0, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(
+      [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_place, L, (const int*)hist); },
+      blocks, kManyThreads, many_smem(L.E), s);
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t pairs, int64_t E) {
-  (void)pairs;
-  return 256 + ((size_t)(E + 1) * 4 + 255) / 256 * 256;
+  if (pairs <= kOnePairs) return 256;
+  return 256 + ((size_t)kManyBlocks * (E + 1) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_route(const RouteLaunch& L, cudaStream_t s) {
-  int* counts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(L.workspace) + 256);
-  const int64_t P = L.M * L.topk;
-  if (L.logits && L.M)
-    k_topk<<<(unsigned)((L.M + kRouteWarps - 1) / kRouteWarps), kRouteWarps * 32, 0, s>>>(L);
-  k_count<<<L.E + 1, kGroupBlock, 0, s>>>(L.ids, P, L.E, counts);
-  k_scatter<<<L.E + 1, kGroupBlock, 0, s>>>(L.ids, P, L.E, counts, L.order, L.offsets);
-  return cudaGetLastError();
+  if (L.E <= 32 || !L.logits) return route_per<1>(L, s);
+  if (L.E <= 128) return route_per<4>(L, s);
+  if (L.E <= 256) return route_per<8>(L, s);
+  return route_per<32>(L, s);
 }
 
 }  // namespace vt

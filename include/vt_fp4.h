@@ -337,8 +337,9 @@ vt_status vt_fp4_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_
  *   renormalize: divide a token's weights by their sum; then every weight times `scale`.
  *   ids (device) int32 [M][topk], weights (device) fp32 [M][topk], largest score first, equal
  *   scores by the lowest index; a NaN score counts as larger than every number.  An expert
- *   whose logit is -inf is never chosen: a token with fewer than topk others gets id -1 and
- *   weight 0 in its last slots, and a token with none gets weight 0 in all of them.
+ *   whose logit (or bias) is -inf is never chosen: a token with fewer than topk others gets id -1 and
+ *   weight 0 in its last slots, and a token with none gets weight 0 in all of them
+ *   (weights that are all 0 are not divided by their sum).
  * topk <= E.  M == 0 writes offsets (all 0) only. */
 vt_status vt_fp4_moe_route(const void* logits, int logits_bf16, int64_t M, int64_t ld, int64_t E,
                            int64_t topk, int scoring, const float* bias, int renormalize,
