@@ -17,59 +17,70 @@ namespace {
 // E2M1 conversion.  An expert whose E8M0 scales span more exponents than f16 holds (`wide`) takes
 // bf16, in which its values and the caller's activations are exact.
 //
-// Roles of one persistent CTA per SM (23 warps):
+// Roles of one persistent CTA per SM (27 warps):
 //   warp 0       weight producer: R packed 128 x 64 tiles (one bulk copy each) per k step
-//   warp 1       token producer: up to 128 rows x 64 k of activations per k step by tiled TMA
+//   warp 1       token producer: up to 64 rows x 64 k of activations per k step by tiled TMA
 //                (128-byte swizzle), where the pre-pass has put the rows in group order
 //   warp 2       TMEM, and one thread issuing tcgen05.mma: D[R x 128 weight rows][tokens] (fp32,
 //                TMEM) += W . A^T with M = 128 and N = the tile's tokens rounded up to 16
-//   Sets x 4     dequantisers: packed tiles -> K-major swizzled MMA operand; a set of four warps
-//   warps        takes every Sets-th k step, each warp 32 rows of each tile
-//   4 warps      (LOAD) loaders: gathered rows by 16-byte asynchronous copies to the same places
-//   last 4 warps epilogue
+//   Sets x 4     dequantisers: packed tiles -> 16-bit MMA operand in TMEM; a set of four warps
+//   warps        takes every Sets-th k step, each warp its TMEM quarter (32 rows) of each tile
+//   4 warps      (LOAD) loaders: gathered rows by asynchronous copies to the token stage
+//   last 8 warps epilogue, in two groups of four
 // The weights are the MMA's M operand so that its cost follows the tokens a group really has
-// (N in steps of 16) and not a tile of 128 of them.
+// (N in steps of 16), and they go to the tensor core through TMEM: a weight tile in shared memory
+// would be written and read once per 64 tokens or fewer, which alone took twice the time that its
+// packed form takes to arrive from HBM (77 tokens x top-8 over 128 experts of 1536 x 2048: 61 us).
 // Items are (token tile, R x 128 weight rows) pairs, weight rows innermost; a group of n rows is
-// cut into ceil(n / 128) token tiles of nearly equal size.
-constexpr int kTok = 128;
-constexpr int kThreads = 23 * 32;
-constexpr int kEpiWarp0 = 19;                // first of the four epilogue warps
-constexpr int kABytes = 128 * 128;
+// cut into ceil(n / 64) token tiles of nearly equal size.
+//
+// k order: a dequantiser's lane (g, t) holds 16 consecutive k of its rows, and the TMEM store that
+// takes them there gives it, of every 8 columns (k pairs), columns 2t and 2t + 1.  So pair
+// 8t + 2q + i of a 64-k tile is the MMA's pair 8q + 2t + i, and the activations are laid out in
+// that order (by the pre-pass).
+constexpr int kTok = 64;
+constexpr int kThreads = 27 * 32;
+constexpr int kEpiWarp0 = 19;                // first of the epilogue warps
 constexpr int kBBytes = kTok * 128;
 constexpr int kBox = 16;                     // rows of one tiled activation load
+constexpr int kNS = 4;                       // stages of dequantised weights (TMEM) and tokens
 constexpr int kTileTable = 1024;             // token tiles whose group is looked up, not searched
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Shared-memory map (from a 1024-byte aligned base).
 template <int FMT, int R, bool LOAD>
 struct Map {
-  static constexpr int NS = R == 2 ? 3 : 4;        // stages of dequantised weights and tokens
-  static constexpr int Sets = NS;                  // sets of dequantisers
-  static constexpr int NW = R == 2 ? 6 : 14;       // stages of packed weights
+  static constexpr int Sets = LOAD ? 3 : 4;        // sets of dequantisers
+  static constexpr int NW = R == 2 ? 14 : 16;      // stages of packed weights
   // A wait on a phase's parity holds only if the phase before it is known to be over.  A set
   // that waits for k step c has passed its wait of step c - Sets for a free stage, so the steps
   // up to c - Sets - NS have been multiplied; the steps that used the same stage and the same
   // packed stage before, c - NS and c - NW, have their phases before last over (Sets <= NS) and
   // last over (the packed copies land in any order, so nothing less than consumption tells).
-  static_assert(Sets <= NS && NW >= NS + Sets, "barrier phases");
-  static constexpr int OffB = NS * R * kABytes;
-  static constexpr int OffW = OffB + NS * kBBytes;
+  static_assert(Sets <= kNS && NW >= kNS + Sets, "barrier phases");
+  static constexpr int OffW = kNS * kBBytes;
   static constexpr int OffX = OffW + NW * R * tile_bytes(FMT);
-  // epilogue: 2 x 16 tokens x 128 columns of bf16, rows 16 bytes apart; with SiLU 2 x 16 x 64
-  // columns behind the exchange of 2 x 4 warps x 8 registers
+  // epilogue, per group of warps: 2 x 16 tokens x 128 columns of bf16, rows 16 bytes apart; with
+  // SiLU 2 x 16 x 64 columns behind the exchange of 2 x 4 warps x 8 registers
   static constexpr int XBytes = 8192 + 2 * 16 * 144;
-  static constexpr int OffTok = OffX + XBytes;     // 2 x kTok x {output row, activation scale}
-  static constexpr int OffBar = OffTok + 2 * kTok * 8;
-  static constexpr int NumBars = 2 * (NS + NW) + 4 + 1;
+  static constexpr int OffTok = OffX + 2 * XBytes;   // per group 2 x kTok x {output row, scale}
+  static constexpr int OffBar = OffTok + 2 * 2 * kTok * 8;
+  static constexpr int NumBars = 2 * (kNS + NW) + 4 + 1;
   static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
   // per group: prefix sum of the token tiles, first row, rows per tile; group of a token tile
   static constexpr int smem(int E) { return OffTab + (E + 1) * 10 + kTileTable * 2 + 16 + 1024; }
 };
-static_assert(Map<FMT_NV, 1, false>::Sets <= 4 && Map<FMT_NV, 2, true>::Sets <= 3, "warps");
 static_assert(2 * 16 * 272 <= Map<FMT_NV, 1, false>::XBytes, "plain epilogue");
 static_assert(Map<FMT_NV, 1, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 static_assert(Map<FMT_NV, 2, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 static_assert(Map<FMT_NV, 2, true>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
+
+// TMEM columns: accumulators [2][R][kTok] of fp32, then the weight stages [kNS][R][32] of pairs.
+template <int R>
+struct Tmem {
+  static constexpr uint32_t A = 2 * R * kTok, Cols = A + kNS * R * 32;
+  static_assert(Cols == 256 || Cols == 512, "a power of two");
+};
 
 constexpr uint32_t kIdescF16 = (1u << 4) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescBF16 = kIdescF16 | (1u << 7) | (1u << 10);
@@ -114,12 +125,46 @@ __device__ __forceinline__ void stmatrix_t4(uint32_t addr, uint32_t a, uint32_t 
                "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
-// 16 bytes global -> shared, asynchronous; zeros where `bytes` is 0.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+// 16 bytes global -> shared, asynchronous.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 8 bytes; zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] . B[smem desc]^T, kind::f16, one thread.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 lanes x 32 columns to TMEM in the layout of tmem_ld_frag (four times 8 columns): of columns
+// 8q .. 8q + 7 this lane gives 2t, 2t + 1 of row g (lo) and of row g + 8 (hi).
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&lo)[8],
+                                             const uint32_t (&hi)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(lo[0]), "r"(lo[1]), "r"(hi[0]), "r"(hi[1]), "r"(lo[2]), "r"(lo[3]), "r"(hi[2]), "r"(hi[3]),
+      "r"(lo[4]), "r"(lo[5]), "r"(hi[4]), "r"(hi[5]), "r"(lo[6]), "r"(lo[7]), "r"(hi[6]), "r"(hi[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// The byte in a 128-byte row of the first of the two MMA pairs that physical k pairs 4c + 2j and
+// 4c + 2j + 1 (16-byte chunk c, half j) become.
+__device__ __forceinline__ uint32_t pair_byte(int c, int j) {
+  return (uint32_t)(32 * (2 * (c & 1) + j) + 8 * (c >> 1));
+}
+__device__ __forceinline__ void epilogue_sync(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return as_u32(__floats2bfloat162_rn(a, b));
 }
@@ -231,14 +276,14 @@ template <int FMT, bool SILU, int R, bool LOAD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ragged(const __grid_constant__ CUtensorMap tm, const RaggedParams p) {
   using S = Map<FMT, R, LOAD>;
-  constexpr int TB = tile_bytes(FMT), NS = S::NS, NW = S::NW, kSets = S::Sets;
-  constexpr uint32_t kTmemCols = 2 * R * kTok;
+  constexpr int TB = tile_bytes(FMT), NS = kNS, NW = S::NW, kSets = S::Sets;
+  constexpr uint32_t kTmemCols = Tmem<R>::Cols;
   const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u - raw_u);
-  const uint32_t sA = base_u, sB = base_u + S::OffB, sW = base_u + S::OffW, sX = base_u + S::OffX;
+  const uint32_t sB = base_u, sW = base_u + S::OffW;
   const uint32_t full = base_u + S::OffBar, empty = full + 8 * NS;  // dequantised weights + tokens
   const uint32_t w_full = empty + 8 * NS, w_empty = w_full + 8 * NW;
   const uint32_t acc_full = w_empty + 8 * NW, acc_empty = acc_full + 16, drain = acc_empty + 16;
@@ -264,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full + 8 * s, 1);
-      mbar_init(acc_empty + 8 * s, 4);
+      mbar_init(acc_empty + 8 * s, 8);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -302,9 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       T.start[e] = run;
       const int n = T.first[e + 1] - T.first[e];
       const int nt = n > 0 ? (n + kTok - 1) / kTok : 0;
-      // nearly equal tiles, whole MMA column blocks; from 8 tiles on full ones (equal ones
-      // rounded up to 16 rows could leave the last tile empty)
-      T.rows[e] = (uint16_t)(nt == 0 || nt >= 8 ? kTok : ((n + nt - 1) / nt + 15) & ~15);
+      // nearly equal tiles of whole MMA column blocks (at most kTok rows, so none is left empty)
+      T.rows[e] = (uint16_t)(nt == 0 ? kTok : ((n + nt - 1) / nt + 15) & ~15);
       for (int t = run; t < run + nt && t < kTileTable; ++t) T.of[t] = (uint16_t)e;
       run += nt;
     }
@@ -391,12 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kt = 0; kt < KT; ++kt) {
           if (!(ok = pf_wait(full + 8 * is, ps, abort, kWaitNs))) break;
           tc_fence_after();
-          const uint64_t ad = desc_sw128(sA + is * R * kABytes), bd = desc_sw128(sB + is * kBBytes);
+          const uint32_t at = tmem + Tmem<R>::A + is * R * 32;
+          const uint64_t bd = desc_sw128(sB + is * kBBytes);
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk) {  // +32 bytes per 16-element k step
+          for (int kk = 0; kk < kTileK / 16; ++kk) {  // 8 columns, 32 bytes per 16-element k step
             const uint32_t acc = (kt > 0 || kk > 0) ? 1u : 0u;
-            mma_f16(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
-            if (two) mma_f16(d + kTok, ad + (kABytes >> 4) + 2 * kk, bd + 2 * kk, idesc, acc);
+            mma_f16_ts(d, at + 8 * kk, bd + 2 * kk, idesc, acc);
+            if (two) mma_f16_ts(d + kTok, at + 32 + 8 * kk, bd + 2 * kk, idesc, acc);
           }
           mma_commit(empty + 8 * is);
           if (++is == NS) { is = 0; ps ^= 1u; }
@@ -412,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 3 + 4 * kSets) {
     // ------------------------------------------------------------- dequantisers
-    // Set `set` takes the CTA's k steps set, set + kSets, ...; warp jp of the set the row blocks
-    // 2jp and 2jp + 1 (32 rows) of each row tile, whose four scale bytes per lane are one word.
-    const int set = (warp - 3) >> 2, jp = (warp - 3) & 3, g = lane >> 2, t = lane & 3;
+    // Set `set` takes the CTA's k steps set, set + kSets, ...; the warp of TMEM quarter jp the row
+    // blocks 2jp and 2jp + 1 (32 rows) of each row tile, whose four scale bytes per lane are one
+    // word.
+    const int set = (warp - 3) >> 2, jp = warp & 3, g = lane >> 2, t = lane & 3;
     const uint32_t soff = (uint32_t)scale_offset(FMT, 2 * jp, g, t);
-    const uint32_t roff = (uint32_t)(32 * jp + g) * 128;  // row & 7 == g for all four rows
-    const uint32_t c0 = (uint32_t)(((2 * t) ^ g) << 4), c1 = (uint32_t)(((2 * t + 1) ^ g) << 4);
+    const uint32_t ta = tmem + Tmem<R>::A + ((uint32_t)(32 * jp) << 16);
     uint32_t iw = set, pw = 0, is = set, ps = 0;
     int kt = set;
     bool ok = true, wide = false, fresh = true;
@@ -447,18 +492,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(w_empty + 8 * iw);
         }
-        if (r == 0 && !(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
-        const uint32_t at = sA + (is * R + r) * kABytes + roff;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          st_shared_v4(at + b * 2048 + c0, og[b][0], og[b][1], og[b][2], og[b][3]);
-          st_shared_v4(at + b * 2048 + c1, og[b][4], og[b][5], og[b][6], og[b][7]);
-          st_shared_v4(at + b * 2048 + 1024 + c0, o8[b][0], o8[b][1], o8[b][2], o8[b][3]);
-          st_shared_v4(at + b * 2048 + 1024 + c1, o8[b][4], o8[b][5], o8[b][6], o8[b][7]);
+        if (r == 0) {
+          if (!(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          tc_fence_after();
         }
+        const uint32_t at = ta + (is * R + r) * 32;
+        tmem_st_frag(at, og[0], o8[0]);
+        tmem_st_frag(at + (16u << 16), og[1], o8[1]);
       }
       if (!ok) break;
-      fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
+      tmem_st_wait();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * is);
       if ((iw += kSets) >= NW) { iw -= NW; pw ^= 1u; }
@@ -476,6 +520,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // caller's bf16 activations.
       const int tid = (warp - 15) * 32 + lane, c = tid & 7, r0 = tid >> 3;
       const uint32_t doff = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+      // where the two halves of a caller's chunk go (already in place in the pre-pass's rows)
+      uint32_t hoff[2];
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t o = pair_byte(c, j);
+        hoff[j] = (uint32_t)(r0 * 128) + ((((o >> 4) ^ (uint32_t)(r0 & 7)) << 4) | (o & 15u));
+      }
       uint32_t is = 0, ps = 0, last = 0;
       bool ok = true, held = false;  // held: stage `last` is copied but not handed over
       auto hand_over = [&](int newer) {
@@ -509,13 +559,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             held = false;
             if (!(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
           }
-          const uint32_t dst = sB + is * kBBytes + doff;
+          const uint32_t dst = sB + is * kBBytes;
           const int64_t k = (int64_t)kt * kTileK + c * 8;
-          const uint32_t bytes = k < L.K ? 16u : 0u;  // K is a multiple of 16
-          const uint8_t* src = A + (k < L.K ? k * 2 : 0);
+          if (FMT == FMT_MX && wide) {
+            const uint32_t bytes = k < L.K ? 8u : 0u;  // K is a multiple of 32
+            const uint8_t* src = A + (k < L.K ? k * 2 : 0);
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            if (i * 16 < q.n) cp_async16(dst + i * 2048, src + row[i] * ld, bytes);
+            for (int i = 0; i < kTok / 16; ++i)
+              if (i * 16 < q.n) {
+                cp_async8(dst + i * 2048 + hoff[0], src + row[i] * ld, bytes);
+                cp_async8(dst + i * 2048 + hoff[1], src + row[i] * ld + 8, bytes);
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kTok / 16; ++i)
+              if (i * 16 < q.n) cp_async16(dst + i * 2048 + doff, A + k * 2 + row[i] * ld);
+          }
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (held) hand_over(1);
           held = true;
@@ -529,12 +588,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    // Four warps, warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16 tokens at a
-    // time: fragments from TMEM, scaled, rounded to bf16, transposed through shared memory
-    // and stored as rows of 128 (64) contiguous columns.
-    const int qd = warp & 3, tid = qd * 32 + lane, t = lane & 3;
+    // Two groups of four warps: with R = 2 group eg takes row tile eg of every item, with R = 1
+    // every other chunk of its tokens.  Warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16
+    // tokens at a time: fragments from TMEM, scaled, rounded to bf16, transposed through shared
+    // memory and stored as rows of 128 (SiLU: 64) contiguous columns.
+    const int eg = (warp - kEpiWarp0) >> 2, qd = warp & 3, tid = qd * 32 + lane, t = lane & 3;
     constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16, kChunk = 16;
-    const uint32_t sT = sX + (SILU ? 8192 : 0);
+    const uint32_t sX = base_u + S::OffX + eg * S::XBytes, sT = sX + (SILU ? 8192 : 0);
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
     const bool vec = (uintptr_t)L.C % 16 == 0 && L.ldc % 8 == 0;
     const bool up = SILU && qd >= 2;
@@ -558,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const PackedHeader* hdr = header_of(L, q.e);
       const float f0 = hdr->factor[up ? 1 : 0], f1 = hdr->factor[1];
       const bool wide = FMT == FMT_MX && hdr->wide;
-      int2* tok = s_tok + ic * kTok;
-      {
+      int2* tok = s_tok + (eg * 2 + ic) * kTok;
+      if (tid < kTok) {
         int row = -1;
         float rs = 1.0f;
         if (tid < q.n) {
@@ -574,13 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       w.next();
       fetch();
-      epilogue_sync();
+      epilogue_sync(eg);
       if (!(ok = pf_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
       tc_fence_after();
-      for (int r = 0; r < nrt; ++r) {
+      const int r = R == 2 ? eg : 0;
+      if (r < nrt) {
         const uint32_t ta = tmem + (ic * R + r) * kTok + ((uint32_t)(qd * 32) << 16);
         const int64_t n0 = (int64_t)(rt0 + r) * kCols;
-        for (int c = 0; c * kChunk < q.n; ++c, ++chunk) {
+        for (int c = R == 2 ? 0 : eg; c * kChunk < q.n; c += R == 2 ? 1 : 2, ++chunk) {
           const uint32_t buf = sT + (chunk & 1) * (kChunk * kRowB);
           constexpr int kH = kChunk / 16;
           uint32_t v[kH][2][8];  // 16 tokens x weight rows [0, 16), [16, 32) of the warp's 32
@@ -618,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            __float_as_uint(up ? y[h][1] : y[h][5]),
                            __float_as_uint(up ? y[h][2] : y[h][6]),
                            __float_as_uint(up ? y[h][3] : y[h][7]));
-            epilogue_sync();
+            epilogue_sync(eg);
             uint32_t o[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -645,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pack_bf16(x[u][1][4 * th], x[u][1][4 * th + 1]),
                             pack_bf16(x[u][1][4 * th + 2], x[u][1][4 * th + 3]));
           }
-          epilogue_sync();
+          epilogue_sync(eg);
           constexpr int kPieces = kCols / 8;  // 16-byte pieces of a token's columns
 #pragma unroll
           for (int i = 0; i < kChunk * kPieces / 128; ++i) {
@@ -685,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Activation pre-pass: A'[i][k] = A[row(i)][k] * 2^-p in f16, p the power of two of the row's
-// largest magnitude (act_pow2), rowscale[i] = 2^p.  One block per row: grouped row i (a row of a
+// largest magnitude (act_pow2), rowscale[i] = 2^p, the k of each 64 in the MMA's order.  One block per row: grouped row i (a row of a
 // `wide` expert is copied as bf16 with scale 1), or, per_token, the caller's row i.
 constexpr int kPrepThreads = 128;
 __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t ldp,
@@ -705,8 +766,16 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
     m = in ? pr / L.topk : 0;
   }
   const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(L.A) + m * L.lda);
-  uint4* dst = reinterpret_cast<uint4*>(Ap + i * ldp);
-  const int64_t ng = L.K / 8;
+  // granule k (8 values) in the MMA's order, as two halves; granules past K are zeros
+  uint8_t* dst = reinterpret_cast<uint8_t*>(Ap + i * ldp);
+  auto put = [&](int64_t k, const uint4& v) {
+    uint8_t* tile = dst + (k >> 3) * 128;
+    const int c = (int)(k & 7);
+    *reinterpret_cast<uint2*>(tile + pair_byte(c, 0)) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(tile + pair_byte(c, 1)) = make_uint2(v.z, v.w);
+  };
+  const int64_t ng = L.K / 8, ngp = ldp / 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   if (L.fmt == FMT_MX && !per_token) {
     if (threadIdx.x == 0) s_e = 0;
     __syncthreads();
@@ -714,7 +783,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
       if (__ldcg(L.offsets + e) <= i && i < __ldcg(L.offsets + e + 1)) s_e = e;
     __syncthreads();
     if (header_of(L, s_e)->wide) {
-      for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) dst[k] = row[k];
+      for (int64_t k = threadIdx.x; k < ngp; k += kPrepThreads) put(k, k < ng ? row[k] : zero);
       if (threadIdx.x == 0) rowscale[i] = 1.0f;
       return;
     }
@@ -731,10 +800,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
 #pragma unroll
   for (int w = 0; w < kPrepThreads / 32; ++w) mx = max(mx, s_max[w]);
   const int p = act_pow2(mx);
-  for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) {
-    const uint4 v = row[k];
+  for (int64_t k = threadIdx.x; k < ngp; k += kPrepThreads) {
+    const uint4 v = k < ng ? row[k] : zero;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    dst[k] = act_granule_f16(w, p);
+    put(k, act_granule_f16(w, p));
   }
   if (threadIdx.x == 0) rowscale[i] = pow2f(p);
 }
@@ -849,9 +918,9 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   // converts each token once and the loaders gather.
   const bool load = L.gather && L.topk > 1 && two && L.pairs * L.K > (8 << 20);
   const int64_t rows = load ? L.pairs / L.topk : L.pairs;
-  // the rows as a 2-D tensor {K, rows}: reads past K or past the last row return zeros
+  // the converted rows as a 2-D tensor: reads past the last row return zeros
   CUtensorMap tm;
-  const cuuint64_t dims[2] = {(cuuint64_t)L.K, (cuuint64_t)rows};
+  const cuuint64_t dims[2] = {(cuuint64_t)p.ldp, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)p.ldp * 2};
   const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)kBox};
   const cuuint32_t estr[2] = {1, 1};
