@@ -17,68 +17,78 @@ namespace {
 // E2M1 conversion.  An expert whose E8M0 scales span more exponents than f16 holds (`wide`) takes
 // bf16, in which its values and the caller's activations are exact.
 //
-// Roles of one persistent CTA per SM (27 warps):
+// Roles of one persistent CTA per SM (28 warps):
 //   warp 0       weight producer: R packed 128 x 64 tiles (one bulk copy each) per k step
-//   warp 1       token producer: up to 64 rows x 64 k of activations per k step by tiled TMA
+//   warp 1       token producer: up to TOK rows x 64 k of activations per k step by tiled TMA
 //                (128-byte swizzle), where the pre-pass has put the rows in group order
-//   warp 2       TMEM, and one thread issuing tcgen05.mma: D[R x 128 weight rows][tokens] (fp32,
-//                TMEM) += W . A^T with M = 128 and N = the tile's tokens rounded up to 16
+//   warps 2, 3   one thread each issuing tcgen05.mma for row tile 0 and 1: D[128 weight rows]
+//                [tokens] (fp32, TMEM) += W . A^T, M = 128 and N = the tile's tokens rounded up to
+//                16 (one thread for both took 700 cycles per k step to issue 256 cycles of MMAs)
 //   Sets x 4     dequantisers: packed tiles -> 16-bit MMA operand in TMEM; a set of four warps
 //   warps        takes every Sets-th k step, each warp its TMEM quarter (32 rows) of each tile
 //   4 warps      (LOAD) loaders: gathered rows by asynchronous copies to the token stage
-//   last 8 warps epilogue, in two groups of four
+//   last 8 warps epilogue
 // The weights are the MMA's M operand so that its cost follows the tokens a group really has
 // (N in steps of 16), and they go to the tensor core through TMEM: a weight tile in shared memory
-// would be written and read once per 64 tokens or fewer, which alone took twice the time that its
-// packed form takes to arrive from HBM (77 tokens x top-8 over 128 experts of 1536 x 2048: 61 us).
+// would be written and read once per token tile, which alone took twice the time that its packed
+// form takes to arrive from HBM (77 tokens x top-8 over 128 experts of 1536 x 2048: 61 us; 47).
+// Token tiles: an M = 128 MMA takes the time of N = 128 even where N is smaller (some 70 cycles
+// measured at 16 and 64), so
+//   TOK = 64  for few rows per group, where that time hides behind the weights' arrival: two
+//             accumulators per row tile, the epilogue of an item beside the MMAs of the next;
+//   TOK = 128 for many: the accumulators of one item and the weight stages fill TMEM, so the
+//             epilogue first moves an item to shared memory as bf16 and then stores it.
+// With SiLU and two row tiles the dequantisers put the gate rows of both tiles in accumulator 0
+// and the up rows in accumulator 1, so that a thread finds its pairs in the same lane.
 // Items are (token tile, R x 128 weight rows) pairs, weight rows innermost; a group of n rows is
-// cut into ceil(n / 64) token tiles of nearly equal size.
+// cut into ceil(n / TOK) token tiles of nearly equal size.
 //
 // k order: a dequantiser's lane (g, t) holds 16 consecutive k of its rows, and the TMEM store that
 // takes them there gives it, of every 8 columns (k pairs), columns 2t and 2t + 1.  So pair
 // 8t + 2q + i of a 64-k tile is the MMA's pair 8q + 2t + i, and the activations are laid out in
 // that order (by the pre-pass).
-constexpr int kTok = 64;
-constexpr int kThreads = 27 * 32;
-constexpr int kEpiWarp0 = 19;                // first of the epilogue warps
-constexpr int kBBytes = kTok * 128;
+constexpr int kThreads = 28 * 32;
+constexpr int kDeqWarp0 = 4;                 // first of the dequantisers
+constexpr int kEpiWarp0 = 20;                // first of the epilogue warps
 constexpr int kBox = 16;                     // rows of one tiled activation load
 constexpr int kNS = 4;                       // stages of dequantised weights (TMEM) and tokens
 constexpr int kTileTable = 1024;             // token tiles whose group is looked up, not searched
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Shared-memory map (from a 1024-byte aligned base).
-template <int FMT, int R, bool LOAD>
+template <int FMT, int R, bool LOAD, int TOK>
 struct Map {
+  static constexpr int BBytes = TOK * 128;
   static constexpr int Sets = LOAD ? 3 : 4;        // sets of dequantisers
-  static constexpr int NW = R == 2 ? 14 : 16;      // stages of packed weights
+  static constexpr int NW = R == 1 ? 16 : TOK == 64 ? 14 : 8;  // stages of packed weights
   // A wait on a phase's parity holds only if the phase before it is known to be over.  A set
   // that waits for k step c has passed its wait of step c - Sets for a free stage, so the steps
   // up to c - Sets - NS have been multiplied; the steps that used the same stage and the same
   // packed stage before, c - NS and c - NW, have their phases before last over (Sets <= NS) and
   // last over (the packed copies land in any order, so nothing less than consumption tells).
   static_assert(Sets <= kNS && NW >= kNS + Sets, "barrier phases");
-  static constexpr int OffW = kNS * kBBytes;
+  static constexpr int OffW = kNS * BBytes;
   static constexpr int OffX = OffW + NW * R * tile_bytes(FMT);
-  // epilogue, per group of warps: 2 x 16 tokens x 128 columns of bf16, rows 16 bytes apart; with
-  // SiLU 2 x 16 x 64 columns behind the exchange of 2 x 4 warps x 8 registers
-  static constexpr int XBytes = 8192 + 2 * 16 * 144;
-  static constexpr int OffTok = OffX + 2 * XBytes;   // per group 2 x kTok x {output row, scale}
-  static constexpr int OffBar = OffTok + 2 * 2 * kTok * 8;
-  static constexpr int NumBars = 2 * (kNS + NW) + 4 + 1;
+  // epilogue.  R = 2: an item's TOK x 256 outputs in bf16, token rows 16 bytes apart (SiLU: x
+  // 128).  R = 1, per group of four warps: 2 x 16 tokens x 128 columns; with SiLU 2 x 16 x 64
+  // behind the exchange of 2 x 4 warps x 8 registers.
+  static constexpr int XGroup = 8192 + 2 * 16 * 144;
+  static constexpr int XBytes = R == 2 ? TOK * 528 : 2 * XGroup;
+  static constexpr int OffTok = OffX + XBytes;     // 2 (R = 1: per group) x TOK x {output row, scale}
+  static constexpr int OffBar = OffTok + 2 * (R == 2 ? 1 : 2) * TOK * 8;
+  static constexpr int NumBars = 2 * (kNS + NW) + 4 + 2;
   static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
   // per group: prefix sum of the token tiles, first row, rows per tile; group of a token tile
   static constexpr int smem(int E) { return OffTab + (E + 1) * 10 + kTileTable * 2 + 16 + 1024; }
+  static_assert(2 * 16 * 272 <= XGroup, "plain epilogue");
+  static_assert(OffTab + (kMaxGroups + 1) * 10 + kTileTable * 2 + 16 + 1024 <= 227 * 1024, "shared memory");
 };
-static_assert(2 * 16 * 272 <= Map<FMT_NV, 1, false>::XBytes, "plain epilogue");
-static_assert(Map<FMT_NV, 1, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
-static_assert(Map<FMT_NV, 2, false>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
-static_assert(Map<FMT_NV, 2, true>::smem(kMaxGroups) <= 227 * 1024, "shared memory");
 
-// TMEM columns: accumulators [2][R][kTok] of fp32, then the weight stages [kNS][R][32] of pairs.
-template <int R>
+// TMEM columns: accumulators [Bufs][R][TOK] of fp32, then the weight stages [kNS][R][32] of pairs.
+template <int R, int TOK>
 struct Tmem {
-  static constexpr uint32_t A = 2 * R * kTok, Cols = A + kNS * R * 32;
+  static constexpr uint32_t Bufs = TOK == 64 ? 2 : 1;
+  static constexpr uint32_t A = Bufs * R * TOK, Cols = A + kNS * R * 32;
   static_assert(Cols == 256 || Cols == 512, "a power of two");
 };
 
@@ -134,6 +144,16 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // D[tmem] (+)= A[tmem] . B[smem desc]^T, kind::f16, one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
@@ -161,9 +181,6 @@ __device__ __forceinline__ void tmem_st_wait() {
 // 4c + 2j + 1 (16-byte chunk c, half j) become.
 __device__ __forceinline__ uint32_t pair_byte(int c, int j) {
   return (uint32_t)(32 * (2 * (c & 1) + j) + 8 * (c >> 1));
-}
-__device__ __forceinline__ void epilogue_sync(int group) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return as_u32(__floats2bfloat162_rn(a, b));
@@ -272,12 +289,14 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
-template <int FMT, bool SILU, int R, bool LOAD>
+template <int FMT, bool SILU, int R, bool LOAD, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ragged(const __grid_constant__ CUtensorMap tm, const RaggedParams p) {
-  using S = Map<FMT, R, LOAD>;
+  using S = Map<FMT, R, LOAD, TOK>;
+  using TM = Tmem<R, TOK>;
   constexpr int TB = tile_bytes(FMT), NS = kNS, NW = S::NW, kSets = S::Sets;
-  constexpr uint32_t kTmemCols = Tmem<R>::Cols;
+  constexpr int kTok = TOK, kBBytes = S::BBytes;
+  constexpr uint32_t kTmemCols = TM::Cols, kBufs = TM::Bufs;
   const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
@@ -301,17 +320,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full + 8 * s, 4 + (LOAD ? 128 : 1));  // a dequantiser set, the token copies
-      mbar_init(empty + 8 * s, 1);
+      mbar_init(empty + 8 * s, R);                    // the MMA threads
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(w_full + 8 * s, 1);
       mbar_init(w_empty + 8 * s, 4);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(acc_full + 8 * s, 1);
+      mbar_init(acc_full + 8 * s, R);
       mbar_init(acc_empty + 8 * s, 8);
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
     *abort = 0;
   }
   if (warp == 2) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -419,50 +439,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (globaltimer_ns() - t0 < 1000000ull) {}
       }
     }
-  } else if (warp == 2) {
-    // --------------------------------------------------------------- MMA issuer
-    if (elect_one()) {
+  } else if (warp < kDeqWarp0) {
+    // -------------------------------------------------------------- MMA issuers
+    const int r = warp - 2;  // row tile
+    if (r < R && elect_one()) {
+      const uint32_t a0 = tmem + TM::A + r * 32, d0 = tmem + r * kTok;
+      const uint64_t b0 = desc_sw128(sB);
       uint32_t is = 0, ps = 0, ic = 0, pc = 0;
-      bool ok = true;
+      bool ok = true, ready = false;  // ready: the next stage was seen full
       for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
         const Item q = item_of(T, w.tile);
-        const bool two = R == 2 && w.rg * 2 + 1 < RT;
+        const bool live = SILU || r == 0 || w.rg * 2 + 1 < RT;  // not past an odd last row tile
         const bool wide = FMT == FMT_MX && header_of(L, q.e)->wide;
         const uint32_t idesc = (wide ? kIdescBF16 : kIdescF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
-        const uint32_t d = tmem + ic * R * kTok;
+        const uint32_t d = d0 + ic * R * kTok;  // ic: accumulator buffer
         if (!(ok = pf_wait(acc_empty + 8 * ic, pc ^ 1u, abort, kWaitNs))) break;
         tc_fence_after();
+        uint32_t acc = 0;
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = pf_wait(full + 8 * is, ps, abort, kWaitNs))) break;
+          if (!ready && !(ok = pf_wait(full + 8 * is, ps, abort, kWaitNs))) break;
           tc_fence_after();
-          const uint32_t at = tmem + Tmem<R>::A + is * R * 32;
-          const uint64_t bd = desc_sw128(sB + is * kBBytes);
-#pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk) {  // 8 columns, 32 bytes per 16-element k step
-            const uint32_t acc = (kt > 0 || kk > 0) ? 1u : 0u;
-            mma_f16_ts(d, at + 8 * kk, bd + 2 * kk, idesc, acc);
-            if (two) mma_f16_ts(d + kTok, at + 32 + 8 * kk, bd + 2 * kk, idesc, acc);
-          }
-          mma_commit(empty + 8 * is);
+          const uint32_t at = a0 + is * (R * 32), cur = empty + 8 * is;
+          const uint64_t bd = b0 + is * (kBBytes >> 4);
           if (++is == NS) { is = 0; ps ^= 1u; }
+          ready = mbar_test_wait(full + 8 * is, ps);  // answered while the MMAs are issued
+          if (live) {
+#pragma unroll
+            for (int kk = 0; kk < kTileK / 16; ++kk) {  // 8 columns, 32 bytes per 16-element k step
+              mma_f16_ts(d, at + 8 * kk, bd + 2 * kk, idesc, acc);
+              acc = 1;
+            }
+          }
+          mma_commit(cur);
         }
         if (!ok) break;
         mma_commit(acc_full + 8 * ic);
-        if (++ic == 2) { ic = 0; pc ^= 1u; }
+        if (++ic == kBufs) { ic = 0; pc ^= 1u; }
       }
       if (!ok) atomicExch(L.status, 5);
-      mma_commit(drain);  // every MMA issued has completed once this commit arrives
+      mma_commit(drain + 8 * r);  // every MMA issued has completed once this commit arrives
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
+      while (!mbar_try_wait(drain + 8 * r, 0) && globaltimer_ns() - t0 < kWaitNs) {}
     }
-  } else if (warp < 3 + 4 * kSets) {
+  } else if (warp < kDeqWarp0 + 4 * kSets) {
     // ------------------------------------------------------------- dequantisers
-    // Set `set` takes the CTA's k steps set, set + kSets, ...; the warp of TMEM quarter jp the row
-    // blocks 2jp and 2jp + 1 (32 rows) of each row tile, whose four scale bytes per lane are one
-    // word.
-    const int set = (warp - 3) >> 2, jp = warp & 3, g = lane >> 2, t = lane & 3;
-    const uint32_t soff = (uint32_t)scale_offset(FMT, 2 * jp, g, t);
-    const uint32_t ta = tmem + Tmem<R>::A + ((uint32_t)(32 * jp) << 16);
+    // Set `set` takes the CTA's k steps set, set + kSets, ...; the warp of TMEM quarter jp two row
+    // blocks (32 rows) for each accumulator, whose four scale bytes per lane are one word: blocks
+    // 2jp and 2jp + 1 of row tile r, or (SiLU, R = 2) of tile jp / 2 its gate (r = 0) or up rows.
+    const int set = (warp - kDeqWarp0) >> 2, jp = warp & 3, g = lane >> 2, t = lane & 3;
+    const uint32_t ta = tmem + TM::A + ((uint32_t)(32 * jp) << 16);
     uint32_t iw = set, pw = 0, is = set, ps = 0;
     int kt = set;
     bool ok = true, wide = false, fresh = true;
@@ -474,11 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = pf_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= nrt) break;  // warp-uniform
-        const uint32_t tb = sW + (iw * R + r) * TB;
-        const int4 cw0 = ld_shared_v4(tb + (2 * jp) * 512 + lane * 16);
-        const int4 cw1 = ld_shared_v4(tb + (2 * jp + 1) * 512 + lane * 16);
-        const uint32_t sc = ld_shared_u32(tb + soff);
+        constexpr bool kSplit = SILU && R == 2;
+        const int rt = kSplit ? jp >> 1 : r, j0 = kSplit ? r * 4 + (jp & 1) * 2 : 2 * jp;
+        // (warp-uniform) past an odd last row tile there is nothing to read
+        const bool live = rt < nrt;
+        const uint32_t tb = sW + (iw * R + (live ? rt : 0)) * TB;
+        const int4 cw0 = ld_shared_v4(tb + j0 * 512 + lane * 16);
+        const int4 cw1 = ld_shared_v4(tb + (j0 + 1) * 512 + lane * 16);
+        const uint32_t sc = ld_shared_u32(tb + scale_offset(FMT, j0, g, t));
         uint32_t og[2][8], o8[2][8];  // rows g and g + 8 of both row blocks
         if (FMT == FMT_MX && wide) {
           dequant_block<FMT, true>(cw0, sc, og[0], o8[0]);
@@ -486,11 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           dequant_block<FMT, false>(cw0, sc, og[0], o8[0]);
           dequant_block<FMT, false>(cw1, sc >> 16, og[1], o8[1]);
-        }
-        if (r == nrt - 1) {
-          // every lane has used what it loaded: only now may the next copy overwrite the stage
-          __syncwarp();
-          if (lane == 0) mbar_arrive(w_empty + 8 * iw);
         }
         if (r == 0) {
           if (!(ok = pf_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
@@ -501,6 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_frag(at + (16u << 16), og[1], o8[1]);
       }
       if (!ok) break;
+      // The stores have taken every value computed from the packed stage, so its loads are done:
+      // only now may the next copy overwrite it (an arrive placed after the conversions in the
+      // source can be executed before them, while loads are under way).
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_empty + 8 * iw);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -518,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Thread: 16-byte chunk c of rows r0, r0 + 16, ...; a row past the tile's tokens reads the
       // last one again (its products are not stored).  A wide expert's rows come from the
       // caller's bf16 activations.
-      const int tid = (warp - 15) * 32 + lane, c = tid & 7, r0 = tid >> 3;
+      const int tid = (warp - (kDeqWarp0 + 4 * kSets)) * 32 + lane, c = tid & 7, r0 = tid >> 3;
       const uint32_t doff = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
       // where the two halves of a caller's chunk go (already in place in the pre-pass's rows)
       uint32_t hoff[2];
@@ -588,18 +616,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    // Two groups of four warps: with R = 2 group eg takes row tile eg of every item, with R = 1
-    // every other chunk of its tokens.  Warp qd on TMEM lanes (weight rows) [32qd, 32qd + 32), 16
-    // tokens at a time: fragments from TMEM, scaled, rounded to bf16, transposed through shared
-    // memory and stored as rows of 128 (SiLU: 64) contiguous columns.
-    const int eg = (warp - kEpiWarp0) >> 2, qd = warp & 3, tid = qd * 32 + lane, t = lane & 3;
-    constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16, kChunk = 16;
-    const uint32_t sX = base_u + S::OffX + eg * S::XBytes, sT = sX + (SILU ? 8192 : 0);
+    // Warp qd of each group on TMEM lanes (weight rows) [32qd, 32qd + 32), 16 tokens at a time:
+    // fragments from TMEM, scaled, rounded to bf16 and transposed through shared memory, from
+    // where rows of contiguous columns are stored.
+    const int eg = (warp - kEpiWarp0) >> 2, qd = warp & 3, t = lane & 3;
+    constexpr int kTeam = R == 2 ? 256 : 128;  // threads that share a token table and a buffer
+    const int tid = (R == 2 ? eg * 128 : 0) + qd * 32 + lane;
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
     const bool vec = (uintptr_t)L.C % 16 == 0 && L.ldc % 8 == 0;
-    const bool up = SILU && qd >= 2;
     const int64_t ncols = SILU ? L.seg_split : L.N;
-    uint32_t ic = 0, pc = 0, chunk = 0;
+    auto team_sync = [&]() {
+      asm volatile("bar.sync %0, %1;" ::"r"(R == 2 ? 1 : 1 + eg), "n"(kTeam) : "memory");
+    };
+    // 16-byte piece of token j: 8 columns from column n on of its output row
+    auto store_piece = [&](const int2* tok, int j, int64_t n, uint32_t from) {
+      const int row = tok[j].x;
+      if (row < 0 || n >= ncols) return;
+      const int4 d = ld_shared_v4(from);
+      __nv_bfloat16* dst = C + (int64_t)row * L.ldc + n;
+      if (vec && n + 8 <= ncols) {
+        *reinterpret_cast<int4*>(dst) = d;
+      } else {
+        const uint32_t w4[4] = {(uint32_t)d.x, (uint32_t)d.y, (uint32_t)d.z, (uint32_t)d.w};
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          if (n + b < ncols)
+            reinterpret_cast<uint16_t*>(dst)[b] = (uint16_t)(w4[b >> 1] >> ((b & 1) * 16));
+      }
+    };
+    // scales of this lane's tokens 2t, 2t + 1 of a chunk and the same 8 on
+    auto scales = [&](const int2* tok, float (&rs)[4]) {
+      const int4 a = *reinterpret_cast<const int4*>(tok + 2 * t);
+      const int4 b = *reinterpret_cast<const int4*>(tok + 8 + 2 * t);
+      rs[0] = __int_as_float(a.y);
+      rs[1] = __int_as_float(a.w);
+      rs[2] = __int_as_float(b.y);
+      rs[3] = __int_as_float(b.w);
+    };
+    uint32_t ic = 0, pc = 0, chunk = 0, odd = 0;
     bool ok = true;
     pdl_wait();
     // this thread's token of the item: its pair, fetched an item ahead
@@ -616,9 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item q = item_of(T, w.tile);
       const int rt0 = w.rg * R, nrt = R == 1 ? 1 : min(R, RT - rt0);
       const PackedHeader* hdr = header_of(L, q.e);
-      const float f0 = hdr->factor[up ? 1 : 0], f1 = hdr->factor[1];
+      const float f0 = hdr->factor[0], f1 = hdr->factor[1];
       const bool wide = FMT == FMT_MX && hdr->wide;
-      int2* tok = s_tok + (eg * 2 + ic) * kTok;
+      int2* tok = s_tok + ((R == 2 ? 0 : eg * 2) + odd) * kTok;
+      odd ^= 1u;
       if (tid < kTok) {
         int row = -1;
         float rs = 1.0f;
@@ -634,52 +689,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       w.next();
       fetch();
-      epilogue_sync(eg);
+      team_sync();  // the table is written, and the buffer of the item before read
       if (!(ok = pf_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
       tc_fence_after();
-      const int r = R == 2 ? eg : 0;
-      if (r < nrt) {
-        const uint32_t ta = tmem + (ic * R + r) * kTok + ((uint32_t)(qd * 32) << 16);
-        const int64_t n0 = (int64_t)(rt0 + r) * kCols;
-        for (int c = R == 2 ? 0 : eg; c * kChunk < q.n; c += R == 2 ? 1 : 2, ++chunk) {
-          const uint32_t buf = sT + (chunk & 1) * (kChunk * kRowB);
-          constexpr int kH = kChunk / 16;
-          uint32_t v[kH][2][8];  // 16 tokens x weight rows [0, 16), [16, 32) of the warp's 32
-#pragma unroll
-          for (int u = 0; u < kH; ++u) {
-            tmem_ld_frag(ta + c * kChunk + u * 16, v[u][0]);
-            tmem_ld_frag(ta + c * kChunk + u * 16 + (16u << 16), v[u][1]);
-          }
-          float x[kH][2][8];
-#pragma unroll
-          for (int u = 0; u < kH; ++u) {
-            // scales of this lane's tokens 2t, 2t + 1 and the same 8 on
-            const int4 sa = *reinterpret_cast<const int4*>(tok + c * kChunk + u * 16 + 2 * t);
-            const int4 sb = *reinterpret_cast<const int4*>(tok + c * kChunk + u * 16 + 8 + 2 * t);
-            const float rs[4] = {__int_as_float(sa.y), __int_as_float(sa.w), __int_as_float(sb.y),
-                                 __int_as_float(sb.w)};
-            tmem_wait_frags(v[u][0], v[u][1]);
-            const int64_t split = L.seg_split - n0 - qd * 32;  // first row of the second factor
+      const uint32_t ta = tmem + ic * R * kTok + ((uint32_t)(qd * 32) << 16);
+      if constexpr (R == 2) {
+        // Group eg: row tile eg (SiLU: every other chunk, both accumulators of it).
+        constexpr int kCols = SILU ? 128 : 256, kRowB = kCols * 2 + 16;
+        const uint32_t sX = base_u + S::OffX;
+        if (SILU || eg < nrt) {
+          const int64_t split = SILU ? 0 : L.seg_split - (int64_t)(rt0 + eg) * 128 - qd * 32;
+          for (int c = SILU ? eg : 0; c * 16 < q.n; c += SILU ? 2 : 1) {
+            uint32_t v[2][8], u[2][8];  // weight rows [0, 16), [16, 32) of the warp's; SiLU: u of up
+            const uint32_t tc = ta + c * 16 + (SILU ? 0 : eg * kTok);
+            tmem_ld_frag(tc, v[0]);
+            tmem_ld_frag(tc + (16u << 16), v[1]);
+            if constexpr (SILU) {
+              tmem_ld_frag(tc + kTok, u[0]);
+              tmem_ld_frag(tc + kTok + (16u << 16), u[1]);
+            }
+            float rs[4];
+            scales(tok + c * 16, rs);
+            tmem_wait_frags(v[0], v[1]);
+            if constexpr (SILU) tmem_wait_frags(u[0], u[1]);
+            uint32_t o[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float f = SILU || h * 16 + (lane >> 2) + ((i >> 1) & 1) * 8 < split ? f0 : f1;
-                x[u][h][i] = __uint_as_float(v[u][h][i]) * rs[(i & 1) + (i >> 2) * 2] * f;
+              for (int i = 0; i < 4; ++i) {
+                float y[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float s = rs[z + (i >> 1) * 2];
+                  if constexpr (SILU) {
+                    y[z] = silu_f(__uint_as_float(v[h][2 * i + z]) * s * f0) *
+                           (__uint_as_float(u[h][2 * i + z]) * s * f1);
+                  } else {
+                    const float f = h * 16 + (lane >> 2) + (i & 1) * 8 < split ? f0 : f1;
+                    y[z] = __uint_as_float(v[h][2 * i + z]) * s * f;
+                  }
+                }
+                o[h][i] = pack_bf16(y[0], y[1]);
               }
+#pragma unroll
+            for (int th = 0; th < 2; ++th)
+              stmatrix_t4(sX + (c * 16 + th * 8 + (lane & 7)) * kRowB +
+                              ((SILU ? 0 : eg * 128) + qd * 32 + (lane >> 3) * 8) * 2,
+                          o[0][2 * th], o[0][2 * th + 1], o[1][2 * th], o[1][2 * th + 1]);
           }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * ic);  // the MMAs of the next item may begin
+        team_sync();
+        constexpr int kPieces = kCols / 8;
+        for (int i = tid; i < q.n * kPieces; i += kTeam) {
+          const int j = i / kPieces, c8 = i % kPieces;
+          store_piece(tok, j, (int64_t)rt0 * (kCols / 2) + c8 * 8, sX + j * kRowB + c8 * 16);
+        }
+      } else {
+        // Group eg: every other chunk of the item's tokens.
+        constexpr int kCols = SILU ? 64 : 128, kRowB = kCols * 2 + 16, kPieces = kCols / 8;
+        const uint32_t sX = base_u + S::OffX + eg * S::XGroup, sT = sX + (SILU ? 8192 : 0);
+        const bool up = SILU && qd >= 2;
+        const int64_t n0 = (int64_t)rt0 * kCols, split = L.seg_split - n0 - qd * 32;
+        for (int c = eg; c * 16 < q.n; c += 2, ++chunk) {
+          const uint32_t buf = sT + (chunk & 1) * (16 * kRowB);
+          uint32_t v[2][8];
+          tmem_ld_frag(ta + c * 16, v[0]);
+          tmem_ld_frag(ta + c * 16 + (16u << 16), v[1]);
+          float rs[4], x[2][8];
+          scales(tok + c * 16, rs);
+          tmem_wait_frags(v[0], v[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const bool second = SILU ? up : h * 16 + (lane >> 2) + ((i >> 1) & 1) * 8 >= split;
+              x[h][i] = __uint_as_float(v[h][i]) * rs[(i & 1) + (i >> 2) * 2] * (second ? f1 : f0);
+            }
           if constexpr (SILU) {
             // warps 0-1 hold gate rows, warps 2-3 the matching up rows in the same places: of
             // every 16 tokens the gate warps finish the first 8 and the up warps the others
             const uint32_t ex = sX + (chunk & 1) * 4096 + lane * 16;
-            const float (&y)[2][8] = x[0];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              st_shared_v4(ex + (qd * 2 + h) * 512, __float_as_uint(up ? y[h][0] : y[h][4]),
-                           __float_as_uint(up ? y[h][1] : y[h][5]),
-                           __float_as_uint(up ? y[h][2] : y[h][6]),
-                           __float_as_uint(up ? y[h][3] : y[h][7]));
-            epilogue_sync(eg);
+              st_shared_v4(ex + (qd * 2 + h) * 512, __float_as_uint(up ? x[h][0] : x[h][4]),
+                           __float_as_uint(up ? x[h][1] : x[h][5]),
+                           __float_as_uint(up ? x[h][2] : x[h][6]),
+                           __float_as_uint(up ? x[h][3] : x[h][7]));
+            team_sync();
             uint32_t o[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -689,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float a[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                a[i] = up ? silu_f(zz[i]) * y[h][4 + i] : silu_f(y[h][i]) * zz[i];
+                a[i] = up ? silu_f(zz[i]) * x[h][4 + i] : silu_f(x[h][i]) * zz[i];
               o[2 * h] = pack_bf16(a[0], a[1]);
               o[2 * h + 1] = pack_bf16(a[2], a[3]);
             }
@@ -697,41 +796,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[0], o[1], o[2], o[3]);
           } else {
 #pragma unroll
-            for (int u = 0; u < kH; ++u)
-#pragma unroll
-              for (int th = 0; th < 2; ++th)
-                stmatrix_t4(buf + (u * 16 + th * 8 + (lane & 7)) * kRowB + (qd * 32 + (lane >> 3) * 8) * 2,
-                            pack_bf16(x[u][0][4 * th], x[u][0][4 * th + 1]),
-                            pack_bf16(x[u][0][4 * th + 2], x[u][0][4 * th + 3]),
-                            pack_bf16(x[u][1][4 * th], x[u][1][4 * th + 1]),
-                            pack_bf16(x[u][1][4 * th + 2], x[u][1][4 * th + 3]));
+            for (int th = 0; th < 2; ++th)
+              stmatrix_t4(buf + (th * 8 + (lane & 7)) * kRowB + (qd * 32 + (lane >> 3) * 8) * 2,
+                          pack_bf16(x[0][4 * th], x[0][4 * th + 1]),
+                          pack_bf16(x[0][4 * th + 2], x[0][4 * th + 3]),
+                          pack_bf16(x[1][4 * th], x[1][4 * th + 1]),
+                          pack_bf16(x[1][4 * th + 2], x[1][4 * th + 3]));
           }
-          epilogue_sync(eg);
-          constexpr int kPieces = kCols / 8;  // 16-byte pieces of a token's columns
+          team_sync();
 #pragma unroll
-          for (int i = 0; i < kChunk * kPieces / 128; ++i) {
-            const int j = (i * 128 + tid) / kPieces, pc8 = (i * 128 + tid) % kPieces;
-            const int row = tok[c * kChunk + j].x;
-            const int64_t n = n0 + pc8 * 8;
-            if (row < 0 || n >= ncols) continue;
-            const int4 d = ld_shared_v4(buf + j * kRowB + pc8 * 16);
-            __nv_bfloat16* dst = C + (int64_t)row * L.ldc + n;
-            if (vec && n + 8 <= ncols) {
-              *reinterpret_cast<int4*>(dst) = d;
-            } else {
-              const uint32_t w4[4] = {(uint32_t)d.x, (uint32_t)d.y, (uint32_t)d.z, (uint32_t)d.w};
-#pragma unroll
-              for (int b = 0; b < 8; ++b)
-                if (n + b < ncols)
-                  reinterpret_cast<uint16_t*>(dst)[b] = (uint16_t)(w4[b >> 1] >> ((b & 1) * 16));
-            }
+          for (int i = 0; i < 16 * kPieces / 128; ++i) {
+            const int j = (i * 128 + tid) / kPieces, c8 = (i * 128 + tid) % kPieces;
+            store_piece(tok + c * 16, j, n0 + c8 * 8, buf + j * kRowB + c8 * 16);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * ic);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + 8 * ic);
-      if (++ic == 2) { ic = 0; pc ^= 1u; }
+      if (++ic == kBufs) { ic = 0; pc ^= 1u; }
     }
     if (!ok && lane == 0) atomicExch(L.status, 5);
   }
@@ -865,34 +948,36 @@ cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* at, dim3 grid, int threads, i
   return cfg;
 }
 
-template <int FMT, bool SILU, int R, bool LOAD>
+template <int FMT, bool SILU, int R, bool LOAD, int TOK>
 cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream_t s) {
-  using S = Map<FMT, R, LOAD>;
+  using S = Map<FMT, R, LOAD, TOK>;
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, R, LOAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, R, LOAD, TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::smem(kMaxGroups));
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
   // at most one partial token tile per group in use
   const int64_t groups = p.L.pairs < p.L.E ? p.L.pairs : p.L.E;
-  const int64_t most = (groups + p.L.pairs / kTok) * ((p.L.RT + R - 1) / R);
+  const int64_t most = (groups + p.L.pairs / TOK) * ((p.L.RT + R - 1) / R);
   const int grid = (int)(sm_count() < most ? sm_count() : most);
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)grid), kThreads, S::smem(p.L.E), s);
-  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, R, LOAD>, tm, p);
+  return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, R, LOAD, TOK>, tm, p);
 }
 
 template <int FMT, bool SILU>
-cudaError_t launch_fmt(const CUtensorMap& tm, const RaggedParams& p, bool wide_items, bool load,
+cudaError_t launch_fmt(const CUtensorMap& tm, const RaggedParams& p, bool two, bool many, bool load,
                        cudaStream_t s) {
-  if (!wide_items) return launch_main<FMT, SILU, 1, false>(tm, p, s);
-  return load ? launch_main<FMT, SILU, 2, true>(tm, p, s) : launch_main<FMT, SILU, 2, false>(tm, p, s);
+  if (!two) return launch_main<FMT, SILU, 1, false, 64>(tm, p, s);
+  if (!many) return launch_main<FMT, SILU, 2, false, 64>(tm, p, s);
+  return load ? launch_main<FMT, SILU, 2, true, 128>(tm, p, s)
+              : launch_main<FMT, SILU, 2, false, 128>(tm, p, s);
 }
 
 }  // namespace
@@ -916,7 +1001,8 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   const bool two = groups * ((L.RT + 1) / 2) >= sm_count();
   // Gathered rows: the pre-pass writes them in group order while that is little data, else it
   // converts each token once and the loaders gather.
-  const bool load = L.gather && L.topk > 1 && two && L.pairs * L.K > (8 << 20);
+  const bool many = two && L.pairs >= 64 * groups;  // rows per group
+  const bool load = L.gather && L.topk > 1 && many && L.pairs * L.K > (8 << 20);
   const int64_t rows = load ? L.pairs / L.topk : L.pairs;
   // the converted rows as a 2-D tensor: reads past the last row return zeros
   CUtensorMap tm;
@@ -932,10 +1018,10 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)rows), kPrepThreads, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, p.ldp, load ? 1 : 0, ap, rowscale);
   if (e != cudaSuccess) return e;
-  if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, load, s)
-                                     : launch_fmt<FMT_NV, false>(tm, p, two, load, s);
-  return L.silu ? launch_fmt<FMT_MX, true>(tm, p, two, load, s)
-                : launch_fmt<FMT_MX, false>(tm, p, two, load, s);
+  if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, many, load, s)
+                                     : launch_fmt<FMT_NV, false>(tm, p, two, many, load, s);
+  return L.silu ? launch_fmt<FMT_MX, true>(tm, p, two, many, load, s)
+                : launch_fmt<FMT_MX, false>(tm, p, two, many, load, s);
 }
 
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,
