@@ -50,7 +50,6 @@ namespace {
 constexpr int kThreads = 28 * 32;
 constexpr int kDeqWarp0 = 4;                 // first of the dequantisers
 constexpr int kEpiWarp0 = 20;                // first of the epilogue warps
-constexpr int kBox = 16;                     // rows of one tiled activation load
 constexpr int kNS = 4;                       // stages of dequantised weights (TMEM) and tokens
 constexpr int kTileTable = 1024;             // token tiles whose group is looked up, not searched
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -59,6 +58,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 template <int FMT, int R, bool LOAD, int TOK>
 struct Map {
   static constexpr int BBytes = TOK * 128;
+  static constexpr int Box = TOK / 4;              // rows of one tiled activation load
   static constexpr int Sets = LOAD ? 3 : 4;        // sets of dequantisers
   static constexpr int NW = R == 1 ? 16 : TOK == 64 ? 14 : 8;  // stages of packed weights
   // A wait on a phase's parity holds only if the phase before it is known to be over.  A set
@@ -102,9 +102,15 @@ struct RaggedParams {
   const float* rowscale;  // 2^p of each of their rows
 };
 
-// SiLU(x) = x / (1 + e^-x).  The quick divide is good to 2 units of 2^-24; from 1 + e^-x >= 2^126
-// on it gives 0 for a value below 2^-119.
-__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + expf(-x)); }
+// SiLU(x) = x / (1 + e^-x) by the hardware's 2^x and 1/x (each good to 2^-22; the product before
+// 2^x adds |x| 2^-24): far inside the rounding of the result to bf16.  From 1 + e^-x > 2^126 on
+// the reciprocal is 0, for a value below 2^-119.  With expf and a division the epilogue of 4096
+// tokens held up the MMAs for a sixth of the time.
+__device__ __forceinline__ float silu_f(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+  return x * r;
+}
 
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
   return *reinterpret_cast<uint32_t*>(&x);
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Map<FMT, R, LOAD, TOK>;
   using TM = Tmem<R, TOK>;
   constexpr int TB = tile_bytes(FMT), NS = kNS, NW = S::NW, kSets = S::Sets;
-  constexpr int kTok = TOK, kBBytes = S::BBytes;
+  constexpr int kTok = TOK, kBBytes = S::BBytes, kBox = S::Box;
   constexpr uint32_t kTmemCols = TM::Cols, kBufs = TM::Bufs;
   const RaggedLaunch& L = p.L;
   extern __shared__ uint8_t smem_raw[];
@@ -759,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(acc_empty + 8 * ic);  // the MMAs of the next item may begin
         team_sync();
         constexpr int kPieces = kCols / 8;
+#pragma unroll 4
         for (int i = tid; i < q.n * kPieces; i += kTeam) {
           const int j = i / kPieces, c8 = i % kPieces;
           store_piece(tok, j, (int64_t)rt0 * (kCols / 2) + c8 * 8, sX + j * kRowB + c8 * 16);
@@ -845,69 +852,79 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Activation pre-pass: A'[i][k] = A[row(i)][k] * 2^-p in f16, p the power of two of the row's
-// largest magnitude (act_pow2), rowscale[i] = 2^p, the k of each 64 in the MMA's order.  One block per row: grouped row i (a row of a
-// `wide` expert is copied as bf16 with scale 1), or, per_token, the caller's row i.
-constexpr int kPrepThreads = 128;
-__global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t ldp,
-                                                              int per_token,
+// largest magnitude (act_pow2), rowscale[i] = 2^p, the k of each 64 in the MMA's order.  One warp
+// per row: grouped row i (a row of a `wide` expert is copied as bf16 with scale 1), or, per_token,
+// the caller's row i.  Bound by memory: a row of up to 8 x 32 granules stays in registers between
+// its maximum and its conversion (a block of 128 threads per row took 38 us for 32768 rows of 768).
+constexpr int kPrepThreads = 256;
+constexpr int kPrepHeld = 8;  // granules of 8 values per lane
+__global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t rows,
+                                                              int64_t ldp, int per_token,
                                                               __half* __restrict__ Ap,
                                                               float* __restrict__ rowscale) {
-  __shared__ int s_max[kPrepThreads / 32], s_e;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i = blockIdx.x;
-  if (!per_token && i >= __ldcg(L.offsets + L.E)) return;  // a pair in no group
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  if (i >= (per_token ? rows : (int64_t)__ldcg(L.offsets + L.E))) return;  // a pair in no group
+  if (i >= rows) return;
   int64_t m = i;
   if (L.gather && !per_token) {
     const int pr = __ldcg(L.order + i);
     const bool in = pr >= 0 && pr < L.pairs;
-    if (!in && threadIdx.x == 0) atomicExch(L.status, 6);
+    if (!in && lane == 0) atomicExch(L.status, 6);
     m = in ? pr / L.topk : 0;
   }
   const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(L.A) + m * L.lda);
-  // granule k (8 values) in the MMA's order, as two halves; granules past K are zeros
+  // granule k in the MMA's order, as two halves; granules past K are zeros
   uint8_t* dst = reinterpret_cast<uint8_t*>(Ap + i * ldp);
-  auto put = [&](int64_t k, const uint4& v) {
-    uint8_t* tile = dst + (k >> 3) * 128;
-    const int c = (int)(k & 7);
-    *reinterpret_cast<uint2*>(tile + pair_byte(c, 0)) = make_uint2(v.x, v.y);
-    *reinterpret_cast<uint2*>(tile + pair_byte(c, 1)) = make_uint2(v.z, v.w);
+  auto put = [&](int k, const uint4& v) {
+    uint8_t* tile = dst + (int64_t)(k >> 3) * 128;
+    *reinterpret_cast<uint2*>(tile + pair_byte(k & 7, 0)) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(tile + pair_byte(k & 7, 1)) = make_uint2(v.z, v.w);
   };
-  const int64_t ng = L.K / 8, ngp = ldp / 8;
+  const int ng = (int)(L.K / 8), ngp = (int)(ldp / 8);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   if (L.fmt == FMT_MX && !per_token) {
-    if (threadIdx.x == 0) s_e = 0;
-    __syncthreads();
-    for (int e = threadIdx.x; e < L.E; e += kPrepThreads)
-      if (__ldcg(L.offsets + e) <= i && i < __ldcg(L.offsets + e + 1)) s_e = e;
-    __syncthreads();
-    if (header_of(L, s_e)->wide) {
-      for (int64_t k = threadIdx.x; k < ngp; k += kPrepThreads) put(k, k < ng ? row[k] : zero);
-      if (threadIdx.x == 0) rowscale[i] = 1.0f;
+    int e = 0;
+    for (int b = lane; b < L.E; b += 32)
+      if (__ldcg(L.offsets + b) <= i && i < __ldcg(L.offsets + b + 1)) e = b;
+    e = __reduce_max_sync(0xffffffffu, e);
+    if (header_of(L, e)->wide) {
+      for (int k = lane; k < ngp; k += 32) put(k, k < ng ? row[k] : zero);
+      if (lane == 0) rowscale[i] = 1.0f;
       return;
     }
   }
   int mx = 0;
-  for (int64_t k = threadIdx.x; k < ng; k += kPrepThreads) {
-    const uint4 v = row[k];
+  auto grow = [&](const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     mx = max(mx, act_maxmag8(w));
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
-  __syncthreads();
+  };
+  uint4 held[kPrepHeld];
 #pragma unroll
-  for (int w = 0; w < kPrepThreads / 32; ++w) mx = max(mx, s_max[w]);
+  for (int h = 0; h < kPrepHeld; ++h) held[h] = h * 32 + lane < ng ? row[h * 32 + lane] : zero;
+#pragma unroll
+  for (int h = 0; h < kPrepHeld; ++h) grow(held[h]);
+#pragma unroll 4
+  for (int k = kPrepHeld * 32 + lane; k < ng; k += 32) grow(row[k]);
+  mx = __reduce_max_sync(0xffffffffu, mx);
   const int p = act_pow2(mx);
-  for (int64_t k = threadIdx.x; k < ngp; k += kPrepThreads) {
-    const uint4 v = k < ng ? row[k] : zero;
+  auto convert = [&](int k, const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     put(k, act_granule_f16(w, p));
-  }
-  if (threadIdx.x == 0) rowscale[i] = pow2f(p);
+  };
+#pragma unroll
+  for (int h = 0; h < kPrepHeld; ++h)
+    if (h * 32 + lane < ngp) convert(h * 32 + lane, held[h]);
+#pragma unroll 4
+  for (int k = kPrepHeld * 32 + lane; k < ngp; k += 32) convert(k, k < ng ? row[k] : zero);
+  if (lane == 0) rowscale[i] = pow2f(p);
 }
 
-// Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.
+// Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.  Bound by
+// memory: the loads of 8 slots are in flight together (one after another, behind the test of each
+// slot's id, 4096 tokens x top-8 x 2048 columns took 39 us).
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_combine(
     const __nv_bfloat16* __restrict__ D, int64_t M, int topk, int64_t N, int64_t ldd,
@@ -919,29 +936,35 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(
   if (i >= M * per) return;
   const int64_t m = i / per, n0 = (i - m * per) * 8;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
-  for (int j = 0; j < topk; ++j) {
-    const int64_t p = m * topk + j;
-    const int id = ids[p];
-    if (id < 0 || id >= E) continue;
-    const float w = weights[p];
-    // D's rows are padded to 8 columns (what lies in the padding is not stored)
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(D + p * ldd + n0));
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  // D's rows are padded to 8 columns (what lies in the padding is not stored)
+  const __nv_bfloat16* src = D + m * topk * ldd + n0;
+  for (int j0 = 0; j0 < topk; j0 += 8) {
+    uint4 v[8];
+    float w[8];
+    bool in[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[2 * c] += w * __uint_as_float(x[c] << 16);
-      acc[2 * c + 1] += w * __uint_as_float(x[c] & 0xFFFF0000u);
+    for (int j = 0; j < 8; ++j) {
+      const int id = j0 + j < topk ? __ldg(ids + m * topk + j0 + j) : -1;
+      in[j] = id >= 0 && id < E;
+      w[j] = in[j] ? __ldg(weights + m * topk + j0 + j) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = in[j] ? __ldcs(reinterpret_cast<const uint4*>(src + (j0 + j) * ldd)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[2 * c] += w[j] * __uint_as_float(x[c] << 16);
+        acc[2 * c + 1] += w[j] * __uint_as_float(x[c] & 0xFFFF0000u);
+      }
     }
   }
   __nv_bfloat16* dst = out + m * ldo + n0;
   if (vec && n0 + 8 <= N) {
-    uint4 o;
-    o.x = as_u32(__floats2bfloat162_rn(acc[0], acc[1]));
-    o.y = as_u32(__floats2bfloat162_rn(acc[2], acc[3]));
-    o.z = as_u32(__floats2bfloat162_rn(acc[4], acc[5]));
-    o.w = as_u32(__floats2bfloat162_rn(acc[6], acc[7]));
-    *reinterpret_cast<uint4*>(dst) = o;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                                                pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
   } else {
     for (int c = 0; c < 8 && n0 + c < N; ++c) dst[c] = __float2bfloat16_rn(acc[c]);
   }
@@ -1024,15 +1047,17 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   CUtensorMap tm;
   const cuuint64_t dims[2] = {(cuuint64_t)p.ldp, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)p.ldp * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)kBox};
+  const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)(many ? 32 : 16)};
   const cuuint32_t estr[2] = {1, 1};
   if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ap, dims, strides, box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)rows), kPrepThreads, 0, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, p.ldp, load ? 1 : 0, ap, rowscale);
+  constexpr int kRows = kPrepThreads / 32;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(&at, dim3((unsigned)((rows + kRows - 1) / kRows)), kPrepThreads, 0, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, rows, p.ldp, load ? 1 : 0, ap, rowscale);
   if (e != cudaSuccess) return e;
   if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, many, load, s)
                                      : launch_fmt<FMT_NV, false>(tm, p, two, many, load, s);
