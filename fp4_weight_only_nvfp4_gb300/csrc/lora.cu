@@ -10,26 +10,49 @@ namespace vt {
 namespace {
 
 // One cluster of kCluster CTAs per tile of up to TM rows of one adapter.  First each CTA sums its
-// share of K (v = A x, ranks as the MMA's rows, tokens as its columns) and the cluster adds the
-// shares through distributed shared memory, in CTA order; then each CTA does its share of N
-// (tokens as rows, columns of B as columns) and adds it to y.  x, y and out cross the memory bus
-// once, an adapter once per tile (from L2 after the first).  v is fp32; as an MMA operand it is
-// the sum of two bf16 values (16 significant bits).
-// Within a block of 32 k (or ranks) lane t of a quad holds the 8 physical positions 8t .. 8t + 7,
-// one 16-byte load, in the MMA's k columns {2t, 2t+1, 2t+8, 2t+9} of two steps; both operands use
-// the same order, so the products are those of the physical order.
+// share of K (v = A x: ranks are the MMA's rows, tokens its columns) and the cluster adds the
+// shares through distributed shared memory, in CTA order; then each CTA adds v B^T to its share of
+// y's columns (tokens are rows).  x, y and out cross the memory bus once, an adapter once per tile
+// (from L2 after the first), no workspace, one launch.  v is fp32; as an MMA operand it is the sum
+// of two bf16 values (16 significant bits).
+// Memory bounds it, so everything streams through a ring of shared-memory chunks filled by
+// asynchronous 16-byte copies, the columns' chunks already under way while v is exchanged (with
+// loads to registers too few bytes were in flight: 53 us against NOW us for 5003 rows, 4096 -> 5120,
+// rank 32).  Rows that are not 16-byte aligned are copied to the same chunks value by value.
 constexpr int kCluster = 8;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 128;             // k, or columns, per chunk
+constexpr int kStride = kChunk * 2 + 16;  // bytes per row of a chunk of x, A or y (no bank conflicts)
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+// TM: rows per tile; RM: ranks held.
+template <int TM, int RM>
+struct LoraSmem {
+  static constexpr int WT = TM / 16, WK = kWarps / WT;      // token groups, shares of a chunk's k
+  static constexpr int BStride = RM * 2 + 16;               // bytes per column of B, per row of v
+  static constexpr int ChunkA = (RM + TM) * kStride, ChunkB = kChunk * BStride + TM * kStride;
+  static constexpr int Stage = ChunkA > ChunkB ? ChunkA : ChunkB;
+  static constexpr int Stages = RM == 128 && TM == 64 ? 2 : 3;
+  static constexpr int VStride = RM + 4;                    // floats per token of the partial sums
+  static constexpr int Partial = WK * TM * VStride * 4;
+  static constexpr int OffPart = Stages * Stage, OffV = OffPart + Partial;
+  static constexpr int Bytes = OffV + 2 * TM * BStride;
+  static_assert(Bytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -41,7 +64,7 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The float at shared-memory address `addr` of CTA `rank` of the cluster.
+// Four floats at shared-memory address `addr` of CTA `rank` of the cluster.
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
   uint32_t a;
   float4 v;
@@ -52,42 +75,32 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// 8 consecutive 16-bit values, the first `n` of them valid (the others 0); `vec`: 16-byte aligned.
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int64_t n, bool vec) {
-  if (vec && n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4] = {0, 0, 0, 0};
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+// 8 consecutive values to shared memory, the first n of them valid (the others zeros).  VEC: one
+// asynchronous copy (src 16-byte aligned); else value by value.
+template <bool VEC>
+__device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int n) {
+  n = n < 0 ? 0 : (n > 8 ? 8 : n);
+  if constexpr (VEC) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n * 2)
+                 : "memory");
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(src);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i >> 1] |= (uint32_t)__ldg(q + i) << ((i & 1) * 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i >> 1] |= (uint32_t)q[i] << ((i & 1) * 16);
+    st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+  }
 }
 
-struct LoraParams {
-  LoraLaunch L;
-  int vec_x, vec_a, vec_b, vec_y;  // 16-byte aligned rows
-};
-
-// RM: ranks held (16 .. RM per adapter).
-template <int TM, int RM>
-struct LoraSmem {
-  static constexpr int WT = TM / 16, WK = kWarps / WT;      // token groups, shares of the CTA's k
-  static constexpr int VStride = RM + 4;                    // floats per token of the partial sums
-  static constexpr int HStride = RM + 8;                    // bf16 per token of v's two terms
-  static constexpr int Partial = WK * TM * VStride * 4;
-  static constexpr int Halves = 2 * TM * HStride * 2;
-  static constexpr int Bytes = Partial + Halves;
-};
-
-template <int TM, int RM>
-__global__ void __launch_bounds__(kThreads) k_lora(const LoraParams p) {
+template <int TM, int RM, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
   using S = LoraSmem<TM, RM>;
-  const LoraLaunch& L = p.L;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* s_part = reinterpret_cast<float*>(smem);                        // [WK][TM][VStride]
-  __nv_bfloat16* s_hi = reinterpret_cast<__nv_bfloat16*>(smem + S::Partial);  // [TM][HStride]
-  __nv_bfloat16* s_lo = s_hi + TM * S::HStride;
   __shared__ int s_warp[kWarps], s_e, s_i0, s_n, s_row[TM];
+  const uint32_t ring = smem_u32(smem);
+  float* s_part = reinterpret_cast<float*>(smem + S::OffPart);  // [WK][TM][VStride]
+  const uint32_t v_hi = ring + S::OffV, v_lo = v_hi + TM * S::BStride;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int rank = (int)cluster_rank();
   const int tile = (int)(blockIdx.x / kCluster);
@@ -147,43 +160,96 @@ __global__ void __launch_bounds__(kThreads) k_lora(const LoraParams p) {
   int R = 0;
   if (e < L.L) R = L.ranks ? min(max(__ldg(L.ranks + e), 0), L.R) : L.R;
   __syncthreads();
+
+  // this CTA's k and columns, in blocks of 32
+  const int K = (int)L.K, N = (int)L.N, R16 = (R + 15) & ~15;
+  const int kb = (K + 31) / 32, nb = (N + 31) / 32;
+  const int k0 = kb * rank / kCluster * 32, k1 = R ? min(kb * (rank + 1) / kCluster * 32, K) : k0;
+  const int c0 = nb * rank / kCluster * 32, c1 = min(nb * (rank + 1) / kCluster * 32, N);
+  const int nk = (k1 - k0 + kChunk - 1) / kChunk, chunks = nk + (c1 - c0 + kChunk - 1) / kChunk;
+  const __nv_bfloat16* A = reinterpret_cast<const __nv_bfloat16*>(L.A) + (R ? (int64_t)e * L.R * K : 0);
+  const __nv_bfloat16* B = reinterpret_cast<const __nv_bfloat16*>(L.B) + (R ? (int64_t)e * N * L.R : 0);
+  const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(L.x);
   const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(L.y);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(L.out);
 
-  if (R > 0) {
-    // ---------------------------------------------------------- v = A x, this CTA's k
-    const int wt = warp % S::WT, wk = warp / S::WT;
-    const int64_t kb = (L.K + 31) / 32;
-    const int64_t k0 = kb * rank / kCluster, k1 = kb * (rank + 1) / kCluster;
-    const __nv_bfloat16* A = reinterpret_cast<const __nv_bfloat16*>(L.A) + (int64_t)e * L.R * L.K;
-    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(L.x);
-    float acc[RM / 16][2][4] = {};
-    int row[2];
+  // Chunk c of the CTA's work: nk of x [TM] over A [R16] (rows of 128 k), then y [TM] over B
+  // [128 columns] (rows of ranks).  A thread copies piece `pc` of rows r0, r0 + 16, ... of x, y and
+  // A, and piece bp of columns bc0, bc0 + bstep, ... of B, 2^sh >= R16 / 8 threads to a column.
+  // Sources of zeros point at valid memory all the same.
+  constexpr int P = kChunk / 8;  // pieces per row
+  const int pc = tid % P, r0 = tid / P;
+  int rows[TM / 16];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) row[j] = s_row[wt * 16 + j * 8 + g];
-    if (wt * 16 < n) {
-#pragma unroll 2
-      for (int64_t b = k0 + wk; b < k1; b += S::WK) {
-        const int64_t k = b * 32 + t * 8, left = L.K - k;
-        uint4 xv[2];
+  for (int i = 0; i < TM / 16; ++i) rows[i] = s_row[r0 + i * 16];
+  const int sh = R16 <= 16 ? 1 : R16 <= 32 ? 2 : R16 <= 64 ? 3 : 4;
+  const int bp = tid & ((1 << sh) - 1), bc0 = tid >> sh, bstep = kThreads >> sh;
+  auto fetch = [&](int c) {
+    if (c < chunks) {
+      const uint32_t st = ring + (uint32_t)(c % S::Stages) * S::Stage;
+      const bool first = c < nk;
+      const int b0 = first ? k0 + c * kChunk : c0 + (c - nk) * kChunk, end = first ? k1 : c1;
+      const int q = b0 + pc * 8, left = end - q;
+      const __nv_bfloat16* src = (first ? x : y) + (left > 0 ? q : 0);
+      const int64_t ld = first ? L.ldx : L.ldy;
+      const uint32_t to = st + r0 * kStride + pc * 16;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          xv[j] = row[j] >= 0 ? load8(x + row[j] * L.ldx + k, left, p.vec_x) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < TM / 16; ++i)
+        if (i * 16 < n) copy8<VEC>(to + i * 16 * kStride, src + (rows[i] >= 0 ? rows[i] * ld : 0), rows[i] >= 0 ? left : 0);
+      if (first) {
+        const __nv_bfloat16* a = A + (left > 0 ? q : 0);
 #pragma unroll
-        for (int m = 0; m < RM / 16; ++m) {
-          if (m * 16 >= R) break;
-          uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0;
-          if (m * 16 + g < R) a0 = load8(A + (int64_t)(m * 16 + g) * L.K + k, left, p.vec_a);
-          if (m * 16 + g + 8 < R) a1 = load8(A + (int64_t)(m * 16 + g + 8) * L.K + k, left, p.vec_a);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            mma_bf16(acc[m][j], a0.x, a1.x, a0.y, a1.y, xv[j].x, xv[j].y);
-            mma_bf16(acc[m][j], a0.z, a1.z, a0.w, a1.w, xv[j].z, xv[j].w);
+        for (int i = 0; i < RM / 16; ++i)
+          if (i * 16 < R) {
+            const int j = r0 + i * 16;
+            copy8<VEC>(to + (TM + i * 16) * kStride, a + (j < R ? (int64_t)j * K : 0), j < R ? left : 0);
           }
+      } else if (bp * 8 < R16) {
+        const uint32_t tb = st + TM * kStride + bp * 16;
+        const int have = R - bp * 8;  // of this piece's ranks
+        for (int j = bc0; j < kChunk; j += bstep) {
+          const bool on = b0 + j < end && have > 0;
+          copy8<VEC>(tb + j * S::BStride, B + (on ? (int64_t)(b0 + j) * L.R + bp * 8 : 0), on ? have : 0);
         }
       }
     }
-    // rows of the MMA are ranks, columns tokens
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int c = 0; c < S::Stages - 1; ++c) fetch(c);
+  // the ring's next chunk: landed for every thread, and the one before it used by every thread
+  auto next = [&](int c) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::Stages - 2) : "memory");
+    __syncthreads();
+    fetch(c + S::Stages - 1);
+    return ring + (uint32_t)(c % S::Stages) * S::Stage;
+  };
+  // rows of tokens past n in a chunk hold what earlier chunks left: finite or not, they are
+  // columns (then rows) of their own that are not stored
+  const int lrow = lane & 7, lmat = lane >> 3;  // this lane's row and matrix of an ldmatrix
+
+  if (R > 0) {
+    // ---------------------------------------------------------------- v = A x
+    const int wt = warp % S::WT, wk = warp / S::WT;
+    float acc[RM / 16][2][4] = {};
+    for (int c = 0; c < nk; ++c) {
+      const uint32_t st = next(c);
+      if (wt * 16 >= n) continue;
+#pragma unroll
+      for (int s = 0; s < kChunk / 16 / S::WK; ++s) {
+        const int ks = (s * S::WK + wk) * 32;  // byte of the 16-k step in a row
+        uint32_t xv[4];  // tokens 0-7 (k low, high), 8-15
+        ldmatrix4(st + (wt * 16 + (lmat >> 1) * 8 + lrow) * kStride + ks + (lmat & 1) * 16, xv);
+#pragma unroll
+        for (int m = 0; m < RM / 16; ++m) {
+          if (m * 16 >= R) break;
+          uint32_t av[4];
+          ldmatrix4(st + (TM + m * 16 + (lmat & 1) * 8 + lrow) * kStride + ks + (lmat >> 1) * 16, av);
+          mma_bf16(acc[m][0], av, xv[0], xv[1]);
+          mma_bf16(acc[m][1], av, xv[2], xv[3]);
+        }
+      }
+    }
 #pragma unroll
     for (int m = 0; m < RM / 16; ++m)
 #pragma unroll
@@ -194,130 +260,110 @@ __global__ void __launch_bounds__(kThreads) k_lora(const LoraParams p) {
               acc[m][j][i];
     __syncthreads();
     // the CTA's share of v, over its warps' shares of k
-    for (int i = tid; i < TM * RM / 4; i += kThreads) {
-      const int tok = i / (RM / 4), r4 = i % (RM / 4) * 4;
-      float4 v = *reinterpret_cast<float4*>(s_part + tok * S::VStride + r4);
+    const int r4s = R16 / 4;
+    for (int i = tid; i < n * r4s; i += kThreads) {
+      float* at = s_part + i / r4s * S::VStride + i % r4s * 4;
+      float4 v = *reinterpret_cast<float4*>(at);
 #pragma unroll
       for (int w = 1; w < S::WK; ++w) {
-        const float4 u = *reinterpret_cast<float4*>(s_part + (w * TM + tok) * S::VStride + r4);
+        const float4 u = *reinterpret_cast<float4*>(at + w * TM * S::VStride);
         v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
       }
-      *reinterpret_cast<float4*>(s_part + tok * S::VStride + r4) = v;
+      *reinterpret_cast<float4*>(at) = v;
     }
     cluster_arrive();
     cluster_wait();
     // v over the cluster's CTAs, times the adapter's scale, as two bf16 terms
     const float scale = __ldg(L.scale + e);
-    for (int i = tid; i < TM * RM / 4; i += kThreads) {
-      const int tok = i / (RM / 4), r4 = i % (RM / 4) * 4;
-      float4 v = make_float4(0, 0, 0, 0);
-      if (tok < n && r4 < R) {
-        const uint32_t at = smem_u32(s_part + tok * S::VStride + r4);
+    for (int i = tid; i < n * r4s; i += kThreads) {
+      const int tok = i / r4s, r4 = i % r4s * 4;
+      const uint32_t at = smem_u32(s_part + tok * S::VStride + r4);
+      float4 u[kCluster], v = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < kCluster; ++c) {
-          const float4 u = ld_cluster_v4(at, c);
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
+      for (int c = 0; c < kCluster; ++c) u[c] = ld_cluster_v4(at, c);
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        v.x += u[c].x; v.y += u[c].y; v.z += u[c].z; v.w += u[c].w;
       }
       const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+      uint32_t h[4], l[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(f[c]);
-        s_hi[tok * S::HStride + r4 + c] = h;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(f[c]);
         // an infinite or NaN v is all in its first term
-        const float d = f[c] - __bfloat162float(h);
-        s_lo[tok * S::HStride + r4 + c] = __float2bfloat16_rn(isfinite(f[c]) ? d : 0.0f);
+        const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(f[c]) ? f[c] - __bfloat162float(hi) : 0.0f);
+        h[c] = __bfloat16_as_ushort(hi);
+        l[c] = __bfloat16_as_ushort(lo);
       }
+      const uint32_t to = tok * S::BStride + r4 * 2;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(v_hi + to), "r"(h[0] | h[1] << 16), "r"(h[2] | h[3] << 16) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(v_lo + to), "r"(l[0] | l[1] << 16), "r"(l[2] | l[3] << 16) : "memory");
     }
     cluster_arrive();  // no CTA may leave while another reads its shared memory: waited for below
-    __syncthreads();
   }
 
-  // -------------------------------------------------------- out = y + v B^T, this CTA's columns
-  const int64_t nb = (L.N + 31) / 32;
-  const int64_t n0 = nb * rank / kCluster, n1 = nb * (rank + 1) / kCluster;
-  const __nv_bfloat16* B = reinterpret_cast<const __nv_bfloat16*>(L.B) + (int64_t)(R > 0 ? e : 0) * L.N * L.R;
-  for (int64_t b = n0 + warp; b < n1; b += kWarps) {
-    // tile j of four, MMA column c: physical column 32b + 8 (c / 2) + 2j + c % 2, so that lane t
-    // ends with the 8 columns from 32b + 8t on
-    uint4 bv[RM / 32 > 0 ? RM / 32 : 1][4];
+  // ------------------------------------------------------------- out = y + v B^T
+  // Warp: 16 columns of the chunk.  MMA column i of its n8 tile j is column 4 (i / 2) + 2j + i % 2,
+  // so that lane t ends with the four columns from 4t on.
+  int orow[TM / 16][2];  // output rows of this lane's fragments
 #pragma unroll
-    for (int q = 0; q < RM / 32; ++q)
+  for (int m = 0; m < TM / 16; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t col = b * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-        bv[q][j] = make_uint4(0, 0, 0, 0);
-        if (col < L.N && q * 32 + t * 8 < R)
-          bv[q][j] = load8(B + col * L.R + q * 32 + t * 8, R - (q * 32 + t * 8), p.vec_b);
+    for (int h = 0; h < 2; ++h) orow[m][h] = s_row[m * 16 + h * 8 + g];
+  for (int c = nk; c < chunks; ++c) {
+    const uint32_t st = next(c);
+    const int col = c0 + (c - nk) * kChunk + warp * 16;
+    if (col >= c1) continue;
+    float d[TM / 16][2][4] = {};
+#pragma unroll
+    for (int q = 0; q < RM / 16; ++q) {
+      if (q * 16 >= R) break;
+      uint32_t bv[4];  // tile 0 (ranks low, high), tile 1
+      const int bc = warp * 16 + 4 * (lrow >> 1) + 2 * (lmat >> 1) + (lrow & 1);
+      ldmatrix4(st + TM * kStride + bc * S::BStride + q * 32 + (lmat & 1) * 16, bv);
+#pragma unroll
+      for (int m = 0; m < TM / 16; ++m) {
+        if (m * 16 >= n) break;
+        const uint32_t at = (m * 16 + (lmat & 1) * 8 + lrow) * S::BStride + q * 32 + (lmat >> 1) * 16;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t vv[4];
+          ldmatrix4((part ? v_lo : v_hi) + at, vv);
+          mma_bf16(d[m][0], vv, bv[0], bv[1]);
+          mma_bf16(d[m][1], vv, bv[2], bv[3]);
+        }
       }
-    const int64_t c0 = b * 32 + t * 8, left = L.N - c0;
-#pragma unroll 1
-    for (int m = 0; m * 16 < n; ++m) {
-      float d[4][4] = {};
-      uint4 yv[2];
-      int row[2];
+    }
+#pragma unroll
+    for (int m = 0; m < TM / 16; ++m) {
+      if (m * 16 >= n) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        row[h] = s_row[m * 16 + h * 8 + g];
-        yv[h] = make_uint4(0, 0, 0, 0);
-        if (row[h] >= 0 && left > 0) {
-          // out may be y itself: not the read-only path
-          const __nv_bfloat16* src = y + row[h] * L.ldy + c0;
-          if (p.vec_y && left >= 8) {
-            yv[h] = *reinterpret_cast<const uint4*>(src);
-          } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < left) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(src)[i] << ((i & 1) * 16);
-            yv[h] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      if (R > 0) {
-#pragma unroll
-        for (int q = 0; q < RM / 32; ++q) {
-          if (q * 32 >= R) break;
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const __nv_bfloat16* s = (part ? s_lo : s_hi) + (m * 16 + g) * S::HStride + q * 32 + t * 8;
-            const uint4 v0 = *reinterpret_cast<const uint4*>(s);
-            const uint4 v1 = *reinterpret_cast<const uint4*>(s + 8 * S::HStride);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(d[j], v0.x, v1.x, v0.y, v1.y, bv[q][j].x, bv[q][j].y);
-              mma_bf16(d[j], v0.z, v1.z, v0.w, v1.w, bv[q][j].z, bv[q][j].w);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (row[h] < 0 || left <= 0) continue;
-        const uint32_t w[4] = {yv[h].x, yv[h].y, yv[h].z, yv[h].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(w[j] << 16) + d[j][2 * h],
-                                                         __uint_as_float(w[j] & 0xFFFF0000u) + d[j][2 * h + 1]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-        __nv_bfloat16* dst = out + row[h] * L.ldo + c0;
-        if (p.vec_y && left >= 8) {
-          *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        const int j = m * 16 + h * 8 + g, row = orow[m][h], left = c1 - (col + 4 * t);
+        if (row < 0 || left <= 0) continue;
+        const uint2 w = ld_shared_v2(st + j * kStride + (warp * 16 + 4 * t) * 2);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(w.x << 16) + d[m][0][2 * h],
+                                                        __uint_as_float(w.x & 0xFFFF0000u) + d[m][0][2 * h + 1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[m][1][2 * h],
+                                                        __uint_as_float(w.y & 0xFFFF0000u) + d[m][1][2 * h + 1]);
+        const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
+        __nv_bfloat16* dst = out + (int64_t)row * L.ldo + col + 4 * t;
+        if constexpr (VEC) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 4; ++i)
             if (i < left) reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(o[i >> 1] >> ((i & 1) * 16));
         }
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (R > 0) cluster_wait();
 }
 
-template <int TM, int RM>
-cudaError_t launch(const LoraParams& p, cudaStream_t s) {
+template <int TM, int RM, bool VEC>
+cudaError_t launch(const LoraLaunch& L, cudaStream_t s) {
   constexpr int bytes = LoraSmem<TM, RM>::Bytes;
   static int done[64] = {0};
   int dev = 0;
@@ -325,13 +371,13 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_lora<TM, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(k_lora<TM, RM, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
   // at most one partial tile per group in use, the rows without adapter a group too
-  const int64_t groups = p.L.M < p.L.L + 1 ? p.L.M : p.L.L + 1;
-  const int64_t tiles = groups + p.L.M / TM;
+  const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1;
+  const int64_t tiles = groups + L.M / TM;
   if (tiles * kCluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * kCluster));
@@ -347,27 +393,29 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM>, p);
+  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM, VEC>, L);
+}
+
+template <int TM, int RM>
+cudaError_t launch_vec(const LoraLaunch& L, cudaStream_t s) {
+  // 16-byte copies need every row aligned and whole groups of 8
+  const bool vec = ((uintptr_t)L.x | (uintptr_t)L.A | (uintptr_t)L.B | (uintptr_t)L.y | (uintptr_t)L.out) % 16 == 0 &&
+                   (L.ldx | L.K | (int64_t)L.R | L.ldy | L.ldo | L.N) % 8 == 0;
+  return vec ? launch<TM, RM, true>(L, s) : launch<TM, RM, false>(L, s);
 }
 
 template <int RM>
-cudaError_t launch_rank(const LoraParams& p, cudaStream_t s) {
+cudaError_t launch_rank(const LoraLaunch& L, cudaStream_t s) {
   // long runs of one adapter: tiles of 64 rows read the adapter a quarter as often
-  return p.L.M >= 24 * (int64_t)p.L.L ? launch<64, RM>(p, s) : launch<16, RM>(p, s);
+  return L.M >= 24 * (int64_t)L.L ? launch_vec<64, RM>(L, s) : launch_vec<16, RM>(L, s);
 }
 
 }  // namespace
 
 cudaError_t launch_lora(const LoraLaunch& L, cudaStream_t s) {
-  LoraParams p;
-  p.L = L;
-  p.vec_x = (uintptr_t)L.x % 16 == 0 && L.ldx % 8 == 0;
-  p.vec_a = (uintptr_t)L.A % 16 == 0 && L.K % 8 == 0;
-  p.vec_b = (uintptr_t)L.B % 16 == 0 && L.R % 8 == 0;
-  p.vec_y = (uintptr_t)L.y % 16 == 0 && L.ldy % 8 == 0 && (uintptr_t)L.out % 16 == 0 && L.ldo % 8 == 0;
-  if (L.R <= 32) return launch_rank<32>(p, s);
-  if (L.R <= 64) return launch_rank<64>(p, s);
-  return launch_rank<128>(p, s);
+  if (L.R <= 32) return launch_rank<32>(L, s);
+  if (L.R <= 64) return launch_rank<64>(L, s);
+  return launch_rank<128>(L, s);
 }
 
 }  // namespace vt
