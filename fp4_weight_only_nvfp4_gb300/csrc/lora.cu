@@ -75,6 +75,12 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t rank, uint2 v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // 8 consecutive values to shared memory, the first n of them valid (the others zeros).  VEC: one
 // asynchronous copy (src 16-byte aligned); else value by value.
 template <bool VEC>
@@ -171,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
   const __nv_bfloat16* B = reinterpret_cast<const __nv_bfloat16*>(L.B) + (R ? (int64_t)e * N * L.R : 0);
   const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(L.x);
   const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(L.y);
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(L.out);
 
   // Chunk c of the CTA's work: nk of x [TM] over A [R16] (rows of 128 k), then y [TM] over B
   // [128 columns] (rows of ranks).  A thread copies piece `pc` of rows r0, r0 + 16, ... of x, y and
@@ -228,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
   // columns (then rows) of their own that are not stored
   const int lrow = lane & 7, lmat = lane >> 3;  // this lane's row and matrix of an ldmatrix
 
+  bool late_wait = false;
   if (R > 0) {
     // ---------------------------------------------------------------- v = A x
     const int wt = warp % S::WT, wk = warp / S::WT;
@@ -235,19 +241,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
     for (int c = 0; c < nk; ++c) {
       const uint32_t st = next(c);
       if (wt * 16 >= n) continue;
+      // k steps wk, wk + WK, ...: the fragments of kS of them are loaded before their products
+      constexpr int kSteps = kChunk / 16 / S::WK, kS = kSteps < 2 ? 1 : 2;
 #pragma unroll
-      for (int s = 0; s < kChunk / 16 / S::WK; ++s) {
-        const int ks = (s * S::WK + wk) * 32;  // byte of the 16-k step in a row
-        uint32_t xv[4];  // tokens 0-7 (k low, high), 8-15
-        ldmatrix4(st + (wt * 16 + (lmat >> 1) * 8 + lrow) * kStride + ks + (lmat & 1) * 16, xv);
+      for (int s0 = 0; s0 < kSteps; s0 += kS) {
+        uint32_t xv[kS][4], av[kS][RM / 16][4];
 #pragma unroll
-        for (int m = 0; m < RM / 16; ++m) {
-          if (m * 16 >= R) break;
-          uint32_t av[4];
-          ldmatrix4(st + (TM + m * 16 + (lmat & 1) * 8 + lrow) * kStride + ks + (lmat >> 1) * 16, av);
-          mma_bf16(acc[m][0], av, xv[0], xv[1]);
-          mma_bf16(acc[m][1], av, xv[2], xv[3]);
+        for (int s = 0; s < kS; ++s) {
+          const int ks = ((s0 + s) * S::WK + wk) * 32;  // byte of the 16-k step in a row
+          // tokens 0-7 (k low, high), 8-15
+          ldmatrix4(st + (wt * 16 + (lmat >> 1) * 8 + lrow) * kStride + ks + (lmat & 1) * 16, xv[s]);
+#pragma unroll
+          for (int m = 0; m < RM / 16; ++m)
+            if (m * 16 < R)
+              ldmatrix4(st + (TM + m * 16 + (lmat & 1) * 8 + lrow) * kStride + ks + (lmat >> 1) * 16, av[s][m]);
         }
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+#pragma unroll
+          for (int m = 0; m < RM / 16; ++m)
+            if (m * 16 < R) {
+              mma_bf16(acc[m][0], av[s][m], xv[s][0], xv[s][1]);
+              mma_bf16(acc[m][1], av[s][m], xv[s][2], xv[s][3]);
+            }
       }
     }
 #pragma unroll
@@ -273,9 +289,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
     }
     cluster_arrive();
     cluster_wait();
-    // v over the cluster's CTAs, times the adapter's scale, as two bf16 terms
+    // v over the cluster's CTAs, times the adapter's scale, as two bf16 terms.  Large tiles: each
+    // CTA sums its share of the values and writes it to all (one more barrier, an eighth of the
+    // reads); small ones: each sums them all.
     const float scale = __ldg(L.scale + e);
-    for (int i = tid; i < n * r4s; i += kThreads) {
+    const int entries = n * r4s;
+    const bool share = entries >= 2 * kThreads;
+    const int i0 = share ? entries * rank / kCluster : 0, i1 = share ? entries * (rank + 1) / kCluster : entries;
+    for (int i = i0 + tid; i < i1; i += kThreads) {
       const int tok = i / r4s, r4 = i % r4s * 4;
       const uint32_t at = smem_u32(s_part + tok * S::VStride + r4);
       float4 u[kCluster], v = make_float4(0, 0, 0, 0);
@@ -296,70 +317,98 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
         l[c] = __bfloat16_as_ushort(lo);
       }
       const uint32_t to = tok * S::BStride + r4 * 2;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(v_hi + to), "r"(h[0] | h[1] << 16), "r"(h[2] | h[3] << 16) : "memory");
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(v_lo + to), "r"(l[0] | l[1] << 16), "r"(l[2] | l[3] << 16) : "memory");
+      const uint2 hv = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      const uint2 lv = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+      if (share) {
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+          st_cluster_v2(v_hi + to, c, hv);
+          st_cluster_v2(v_lo + to, c, lv);
+        }
+      } else {
+        st_cluster_v2(v_hi + to, rank, hv);
+        st_cluster_v2(v_lo + to, rank, lv);
+      }
     }
-    cluster_arrive();  // no CTA may leave while another reads its shared memory: waited for below
+    // Shared: every CTA's values are here after the barrier.  Otherwise it only keeps a CTA from
+    // leaving while another reads its shared memory, and is waited for at the end.
+    cluster_arrive();
+    if (share) cluster_wait();
+    late_wait = !share;
   }
 
   // ------------------------------------------------------------- out = y + v B^T
-  // Warp: 16 columns of the chunk.  MMA column i of its n8 tile j is column 4 (i / 2) + 2j + i % 2,
-  // so that lane t ends with the four columns from 4t on.
-  int orow[TM / 16][2];  // output rows of this lane's fragments
+  // Warp: rows [16 wm, 16 wm + 16) and kCW columns of the chunk; v's fragments stay in registers
+  // where they fit.  MMA column i of n8 tile 2a + b is column 16a + 4 (i / 2) + 2b + i % 2, so that
+  // lane t ends with the four columns from 16a + 4t on and a quad stores whole 32-byte sectors.
+  constexpr int WM = TM / 16, WN = kWarps / WM, kCW = kChunk / WN, kTiles = kCW / 8;
+  constexpr bool kHold = RM <= 64;
+  const int wm = warp % WM, wn = warp / WM;
+  uint32_t vv[kHold ? RM / 16 : 1][2][4];
+  const uint32_t vat = (uint32_t)((wm * 16 + (lmat & 1) * 8 + lrow) * S::BStride + (lmat >> 1) * 16);
+  int orow[2];  // output rows of this lane's fragments
 #pragma unroll
-  for (int m = 0; m < TM / 16; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) orow[m][h] = s_row[m * 16 + h * 8 + g];
+  for (int h = 0; h < 2; ++h) orow[h] = s_row[wm * 16 + h * 8 + g];
   for (int c = nk; c < chunks; ++c) {
     const uint32_t st = next(c);
-    const int col = c0 + (c - nk) * kChunk + warp * 16;
-    if (col >= c1) continue;
-    float d[TM / 16][2][4] = {};
+    if (kHold && c == nk) {  // v is written by now for every thread
+#pragma unroll
+      for (int q = 0; q < RM / 16; ++q)
+        if (q * 16 < R) {
+          ldmatrix4(v_hi + vat + q * 32, vv[q][0]);
+          ldmatrix4(v_lo + vat + q * 32, vv[q][1]);
+        }
+    }
+    const int col = c0 + (c - nk) * kChunk + wn * kCW;
+    if (col >= c1 || wm * 16 >= n) continue;
+    float d[kTiles][4] = {};
 #pragma unroll
     for (int q = 0; q < RM / 16; ++q) {
       if (q * 16 >= R) break;
-      uint32_t bv[4];  // tile 0 (ranks low, high), tile 1
-      const int bc = warp * 16 + 4 * (lrow >> 1) + 2 * (lmat >> 1) + (lrow & 1);
-      ldmatrix4(st + TM * kStride + bc * S::BStride + q * 32 + (lmat & 1) * 16, bv);
-#pragma unroll
-      for (int m = 0; m < TM / 16; ++m) {
-        if (m * 16 >= n) break;
-        const uint32_t at = (m * 16 + (lmat & 1) * 8 + lrow) * S::BStride + q * 32 + (lmat >> 1) * 16;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t vv[4];
-          ldmatrix4((part ? v_lo : v_hi) + at, vv);
-          mma_bf16(d[m][0], vv, bv[0], bv[1]);
-          mma_bf16(d[m][1], vv, bv[2], bv[3]);
-        }
+      if (!kHold) {
+        ldmatrix4(v_hi + vat + q * 32, vv[0][0]);
+        ldmatrix4(v_lo + vat + q * 32, vv[0][1]);
       }
+      const uint32_t (&v)[2][4] = vv[kHold ? q : 0];
+      uint32_t bv[kTiles / 2][4];  // tile 2j (ranks low, high), tile 2j + 1
+#pragma unroll
+      for (int j = 0; j < kTiles / 2; ++j) {
+        const int bc = wn * kCW + 16 * j + 4 * (lrow >> 1) + 2 * (lmat >> 1) + (lrow & 1);
+        ldmatrix4(st + TM * kStride + bc * S::BStride + q * 32 + (lmat & 1) * 16, bv[j]);
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+          mma_bf16(d[j], v[part], bv[j >> 1][2 * (j & 1)], bv[j >> 1][2 * (j & 1) + 1]);
     }
+    const int left = c1 - (col + 4 * t);
 #pragma unroll
-    for (int m = 0; m < TM / 16; ++m) {
-      if (m * 16 >= n) break;
+    for (int h = 0; h < 2; ++h) {
+      if (orow[h] < 0 || left <= 0) continue;
+      const uint32_t from = st + (wm * 16 + h * 8 + g) * kStride + (wn * kCW + 4 * t) * 2;
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(L.out) + orow[h] * L.ldo + col + 4 * t;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = m * 16 + h * 8 + g, row = orow[m][h], left = c1 - (col + 4 * t);
-        if (row < 0 || left <= 0) continue;
-        const uint2 w = ld_shared_v2(st + j * kStride + (warp * 16 + 4 * t) * 2);
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(w.x << 16) + d[m][0][2 * h],
-                                                        __uint_as_float(w.x & 0xFFFF0000u) + d[m][0][2 * h + 1]);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[m][1][2 * h],
-                                                        __uint_as_float(w.y & 0xFFFF0000u) + d[m][1][2 * h + 1]);
+      for (int j = 0; j < kTiles; j += 2) {
+        const uint2 w = ld_shared_v2(from + j * 16);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(w.x << 16) + d[j][2 * h],
+                                                        __uint_as_float(w.x & 0xFFFF0000u) + d[j][2 * h + 1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[j + 1][2 * h],
+                                                        __uint_as_float(w.y & 0xFFFF0000u) + d[j + 1][2 * h + 1]);
         const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
-        __nv_bfloat16* dst = out + (int64_t)row * L.ldo + col + 4 * t;
         if constexpr (VEC) {
-          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+          if (j * 8 < left) *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(o[0], o[1]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < left) reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(o[i >> 1] >> ((i & 1) * 16));
+            if (j * 8 + i < left)
+              reinterpret_cast<uint16_t*>(dst)[j * 8 + i] = (uint16_t)(o[i >> 1] >> ((i & 1) * 16));
         }
       }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (R > 0) cluster_wait();
+  if (late_wait) cluster_wait();
 }
 
 template <int TM, int RM, bool VEC>
