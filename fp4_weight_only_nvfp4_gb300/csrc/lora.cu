@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
     // reads); small ones: each sums them all.
     const float scale = __ldg(L.scale + e);
     const int entries = n * r4s;
-    const bool share = entries >= 2 * kThreads;
+    const bool share = entries >= kThreads / 2;
     const int i0 = share ? entries * rank / kCluster : 0, i1 = share ? entries * (rank + 1) / kCluster : entries;
     for (int i = i0 + tid; i < i1; i += kThreads) {
       const int tok = i / r4s, r4 = i % r4s * 4;
