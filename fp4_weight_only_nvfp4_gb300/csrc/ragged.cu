@@ -854,10 +854,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Activation pre-pass: A'[i][k] = A[row(i)][k] * 2^-p in f16, p the power of two of the row's
 // largest magnitude (act_pow2), rowscale[i] = 2^p, the k of each 64 in the MMA's order.  One warp
 // per row: grouped row i (a row of a `wide` expert is copied as bf16 with scale 1), or, per_token,
-// the caller's row i.  Bound by memory: a row of up to 8 x 32 granules stays in registers between
-// its maximum and its conversion (a block of 128 threads per row took 38 us for 32768 rows of 768).
+// the caller's row i.  Bound by memory: a row of up to HELD x 32 granules of 8 values stays in
+// registers between its maximum and its conversion (a block of 128 threads per row took 38 us for
+// 32768 rows of 768).
 constexpr int kPrepThreads = 256;
-constexpr int kPrepHeld = 8;  // granules of 8 values per lane
+template <int HELD>
 __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch L, int64_t rows,
                                                               int64_t ldp, int per_token,
                                                               __half* __restrict__ Ap,
@@ -866,8 +867,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-  if (i >= (per_token ? rows : (int64_t)__ldcg(L.offsets + L.E))) return;  // a pair in no group
   if (i >= rows) return;
+  const int64_t grouped = per_token ? rows : (int64_t)__ldcg(L.offsets + L.E);
   int64_t m = i;
   if (L.gather && !per_token) {
     const int pr = __ldcg(L.order + i);
@@ -885,6 +886,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
   };
   const int ng = (int)(L.K / 8), ngp = (int)(ldp / 8);
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 held[HELD];
+#pragma unroll
+  for (int h = 0; h < HELD; ++h) held[h] = h * 32 + lane < ng ? row[h * 32 + lane] : zero;
+  if (i >= grouped) return;  // a pair in no group
   if (L.fmt == FMT_MX && !per_token) {
     int e = 0;
     for (int b = lane; b < L.E; b += 32)
@@ -901,13 +906,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     mx = max(mx, act_maxmag8(w));
   };
-  uint4 held[kPrepHeld];
 #pragma unroll
-  for (int h = 0; h < kPrepHeld; ++h) held[h] = h * 32 + lane < ng ? row[h * 32 + lane] : zero;
-#pragma unroll
-  for (int h = 0; h < kPrepHeld; ++h) grow(held[h]);
+  for (int h = 0; h < HELD; ++h) grow(held[h]);
 #pragma unroll 4
-  for (int k = kPrepHeld * 32 + lane; k < ng; k += 32) grow(row[k]);
+  for (int k = HELD * 32 + lane; k < ng; k += 32) grow(row[k]);
   mx = __reduce_max_sync(0xffffffffu, mx);
   const int p = act_pow2(mx);
   auto convert = [&](int k, const uint4& v) {
@@ -915,16 +917,17 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
     put(k, act_granule_f16(w, p));
   };
 #pragma unroll
-  for (int h = 0; h < kPrepHeld; ++h)
+  for (int h = 0; h < HELD; ++h)
     if (h * 32 + lane < ngp) convert(h * 32 + lane, held[h]);
 #pragma unroll 4
-  for (int k = kPrepHeld * 32 + lane; k < ngp; k += 32) convert(k, k < ng ? row[k] : zero);
+  for (int k = HELD * 32 + lane; k < ngp; k += 32) convert(k, k < ng ? row[k] : zero);
   if (lane == 0) rowscale[i] = pow2f(p);
 }
 
 // Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.  Bound by
-// memory: the loads of 8 slots are in flight together (one after another, behind the test of each
-// slot's id, 4096 tokens x top-8 x 2048 columns took 39 us).
+// memory: the loads of 8 slots are in flight together, those of pairs in no group too (what their
+// rows hold is masked); one after another, behind the test of each slot's id, 4096 tokens x top-8
+// x 2048 columns took 39 us.
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_combine(
     const __nv_bfloat16* __restrict__ D, int64_t M, int topk, int64_t N, int64_t ldd,
@@ -940,24 +943,20 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(
   const __nv_bfloat16* src = D + m * topk * ldd + n0;
   for (int j0 = 0; j0 < topk; j0 += 8) {
     uint4 v[8];
-    float w[8];
-    bool in[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = j0 + j < topk ? __ldcs(reinterpret_cast<const uint4*>(src + (j0 + j) * ldd)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int id = j0 + j < topk ? __ldg(ids + m * topk + j0 + j) : -1;
-      in[j] = id >= 0 && id < E;
-      w[j] = in[j] ? __ldg(weights + m * topk + j0 + j) : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = in[j] ? __ldcs(reinterpret_cast<const uint4*>(src + (j0 + j) * ldd)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      const bool in = id >= 0 && id < E;
+      const float w = in ? __ldg(weights + m * topk + j0 + j) : 0.0f;
+      const uint32_t mask = in ? 0xFFFFFFFFu : 0u;
+      const uint32_t x[4] = {v[j].x & mask, v[j].y & mask, v[j].z & mask, v[j].w & mask};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        acc[2 * c] += w[j] * __uint_as_float(x[c] << 16);
-        acc[2 * c + 1] += w[j] * __uint_as_float(x[c] & 0xFFFF0000u);
+        acc[2 * c] += w * __uint_as_float(x[c] << 16);
+        acc[2 * c + 1] += w * __uint_as_float(x[c] & 0xFFFF0000u);
       }
     }
   }
@@ -1057,7 +1056,9 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   constexpr int kRows = kPrepThreads / 32;
   const cudaLaunchConfig_t cfg =
       pdl_config(&at, dim3((unsigned)((rows + kRows - 1) / kRows)), kPrepThreads, 0, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ragged_prep, L, rows, p.ldp, load ? 1 : 0, ap, rowscale);
+  cudaError_t e = L.K <= 1024
+                      ? cudaLaunchKernelEx(&cfg, k_ragged_prep<4>, L, rows, p.ldp, load ? 1 : 0, ap, rowscale)
+                      : cudaLaunchKernelEx(&cfg, k_ragged_prep<8>, L, rows, p.ldp, load ? 1 : 0, ap, rowscale);
   if (e != cudaSuccess) return e;
   if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, many, load, s)
                                      : launch_fmt<FMT_NV, false>(tm, p, two, many, load, s);
