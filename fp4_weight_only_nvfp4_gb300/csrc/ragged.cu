@@ -924,42 +924,50 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
   if (lane == 0) rowscale[i] = pow2f(p);
 }
 
-// Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread.  Bound by
-// memory: the loads of 8 slots are in flight together, those of pairs in no group too (what their
-// rows hold is masked); one after another, behind the test of each slot's id, 4096 tokens x top-8
-// x 2048 columns took 39 us.
+// Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread, a block per
+// token and 2048 columns.  The loads of 8 slots are in flight together, those of pairs in no group
+// too (what their rows hold is not used): one after another, behind the test of each slot's id,
+// 4096 tokens x top-8 x 2048 columns took 39 us.  Bound by memory and its instructions about alike.
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_combine(
-    const __nv_bfloat16* __restrict__ D, int64_t M, int topk, int64_t N, int64_t ldd,
+    const __nv_bfloat16* __restrict__ D, int topk, int N, int64_t ldd,
     const int32_t* __restrict__ ids, int E, const float* __restrict__ weights,
     __nv_bfloat16* __restrict__ out, int64_t ldo, int vec) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t per = (N + 7) / 8, i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
-  if (i >= M * per) return;
-  const int64_t m = i / per, n0 = (i - m * per) * 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t m = blockIdx.x;
+  const int n0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  const bool live = n0 < N;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   // D's rows are padded to 8 columns (what lies in the padding is not stored)
-  const __nv_bfloat16* src = D + m * topk * ldd + n0;
+  const __nv_bfloat16* src = D + m * topk * ldd + (live ? n0 : 0);
+  ids += m * topk;
+  weights += m * topk;
   for (int j0 = 0; j0 < topk; j0 += 8) {
+    // lane j: slot j0 + j
+    const bool slot = lane < 8 && j0 + lane < topk;
+    const int id = slot ? __ldg(ids + j0 + lane) : -1;
+    const float wl = slot ? __ldg(weights + j0 + lane) : 0.0f;
     uint4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       v[j] = j0 + j < topk ? __ldcs(reinterpret_cast<const uint4*>(src + (j0 + j) * ldd)) : make_uint4(0, 0, 0, 0);
+    const uint32_t in = __ballot_sync(0xffffffffu, id >= 0 && id < E);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int id = j0 + j < topk ? __ldg(ids + m * topk + j0 + j) : -1;
-      const bool in = id >= 0 && id < E;
-      const float w = in ? __ldg(weights + m * topk + j0 + j) : 0.0f;
-      const uint32_t mask = in ? 0xFFFFFFFFu : 0u;
-      const uint32_t x[4] = {v[j].x & mask, v[j].y & mask, v[j].z & mask, v[j].w & mask};
+      const float w = __shfl_sync(0xffffffffu, wl, j);
+      if (in >> j & 1) {
+        const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        acc[2 * c] += w * __uint_as_float(x[c] << 16);
-        acc[2 * c + 1] += w * __uint_as_float(x[c] & 0xFFFF0000u);
+        for (int c = 0; c < 4; ++c) {
+          acc[2 * c] += w * __uint_as_float(x[c] << 16);
+          acc[2 * c + 1] += w * __uint_as_float(x[c] & 0xFFFF0000u);
+        }
       }
     }
   }
+  if (!live) return;
   __nv_bfloat16* dst = out + m * ldo + n0;
   if (vec && n0 + 8 <= N) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
@@ -1069,11 +1077,13 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,
                            const int32_t* ids, int E, const float* weights, void* out,
                            int64_t ldo, cudaStream_t s) {
-  const int64_t blocks = (M * ((N + 7) / 8) + kCombineThreads - 1) / kCombineThreads;
+  const int64_t pieces = (N + 7) / 8;
+  const int threads = (int)(pieces < kCombineThreads ? (pieces + 31) / 32 * 32 : kCombineThreads);
+  const dim3 grid((unsigned)M, (unsigned)((pieces + threads - 1) / threads));
   const int vec = (uintptr_t)out % 16 == 0 && ldo % 8 == 0;
   cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)blocks), kCombineThreads, 0, s);
-  return cudaLaunchKernelEx(&cfg, k_combine, reinterpret_cast<const __nv_bfloat16*>(D), M, topk, N,
+  const cudaLaunchConfig_t cfg = pdl_config(&at, grid, threads, 0, s);
+  return cudaLaunchKernelEx(&cfg, k_combine, reinterpret_cast<const __nv_bfloat16*>(D), topk, (int)N,
                             ldd, ids, E, weights, reinterpret_cast<__nv_bfloat16*>(out), ldo, vec);
 }
 
