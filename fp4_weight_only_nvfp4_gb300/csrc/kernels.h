@@ -186,4 +186,19 @@ struct LoraLaunch {
 };
 cudaError_t launch_lora(const LoraLaunch& L, cudaStream_t s);
 
+// Raises a kernel's limit of dynamic shared memory, once per device.
+template <typename K>
+inline cudaError_t set_up_kernel(K kernel, size_t bytes, int (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    done[dev] = 1;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace vt

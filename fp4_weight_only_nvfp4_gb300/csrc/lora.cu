@@ -415,15 +415,8 @@ template <int TM, int RM, bool VEC>
 cudaError_t launch(const LoraLaunch& L, cudaStream_t s) {
   constexpr int bytes = LoraSmem<TM, RM>::Bytes;
   static int done[64] = {0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = set_up_kernel(k_lora<TM, RM, VEC>, bytes, done);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_lora<TM, RM, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    done[dev] = 1;
-  }
   // at most one partial tile per group in use, the rows without adapter a group too
   const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1;
   const int64_t tiles = groups + L.M / TM;

@@ -998,16 +998,9 @@ template <int FMT, bool SILU, int R, bool LOAD, int TOK>
 cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream_t s) {
   using S = Map<FMT, R, LOAD, TOK>;
   static int done[64] = {0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e =
+      set_up_kernel(k_ragged<FMT, SILU, R, LOAD, TOK>, (size_t)S::smem(kMaxGroups), done);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(k_ragged<FMT, SILU, R, LOAD, TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::smem(kMaxGroups));
-    if (e != cudaSuccess) return e;
-    done[dev] = 1;
-  }
   // at most one partial token tile per group in use
   const int64_t groups = p.L.pairs < p.L.E ? p.L.pairs : p.L.E;
   const int64_t most = (groups + p.L.pairs / TOK) * ((p.L.RT + R - 1) / R);

@@ -163,11 +163,13 @@ __device__ __forceinline__ void place_pairs(const int32_t* ids, int64_t p0, int6
 }
 
 // Everything in one block: few pairs, where a launch costs more than the work.
-constexpr int kOneThreads = 1024;
 constexpr int64_t kOnePairs = 1024;
-inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + kOneThreads / 32 * 2) + 16; }
+template <int T>
+inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + T / 32 * 2) + 16; }
 
-template <int PER>
+// T = 256 up to 8 tokens (a warp each) or 256 given ids, where the barriers and the sum over the
+// warps' counts of 1024 threads are most of the time (8 tokens: 4.7 us, 5.3 with 1024); 1024 above.
+template <int PER, int kOneThreads>
 __global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) {
   extern __shared__ int s_dyn[];
   __shared__ int s_warp[kOneThreads / 32], s_ids[kOnePairs];
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) 
 
 // Many pairs: block c counts its run of pairs per group (after choosing them, where there are
 // logits); a second launch sums the blocks' counts and places the pairs.
-constexpr int kManyThreads = 512;
+constexpr int kPlaceThreads = 512;
 constexpr int kManyBlocks = 152;
 
 __host__ __device__ inline int64_t block_pairs(int64_t P, int topk, int blocks) {
@@ -212,18 +214,18 @@ __host__ __device__ inline int64_t block_pairs(int64_t P, int topk, int blocks) 
   return (M + blocks - 1) / blocks * topk;  // whole tokens
 }
 
-template <int PER>
-__global__ void __launch_bounds__(kManyThreads) k_route_count(const RouteLaunch L, int* hist) {
+template <int PER, int T>
+__global__ void __launch_bounds__(T) k_route_count(const RouteLaunch L, int* hist) {
   __shared__ int s_count[kMaxGroups + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e <= L.E; e += kManyThreads) s_count[e] = 0;
+  for (int e = threadIdx.x; e <= L.E; e += T) s_count[e] = 0;
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
   const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
   const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
   if (L.logits) {
-    for (int64_t m = p0 / L.topk + warp; m * L.topk < p1; m += kManyThreads / 32) {
+    for (int64_t m = p0 / L.topk + warp; m * L.topk < p1; m += T / 32) {
       int id;
       float w;
       topk_token<PER>(L, m, lane, id, w);
@@ -234,29 +236,33 @@ __global__ void __launch_bounds__(kManyThreads) k_route_count(const RouteLaunch 
       }
     }
   } else {
-    for (int64_t i = p0 + threadIdx.x; i < p1; i += kManyThreads)
+    for (int64_t i = p0 + threadIdx.x; i < p1; i += T)
       atomicAdd(s_count + group_of_id(L.ids[i], L.E), 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e <= L.E; e += kManyThreads) hist[blockIdx.x * (L.E + 1) + e] = s_count[e];
+  for (int e = threadIdx.x; e <= L.E; e += T) hist[blockIdx.x * (L.E + 1) + e] = s_count[e];
 }
 
-inline size_t many_smem(int E) { return (size_t)(E + 1) * (8 + kManyThreads / 32 * 4); }
+// More than half of an SM's shared memory, so that the placing blocks spread over the SMs: as they
+// launch while the counting blocks run, four of them would go to the first SM that frees up (8192
+// tokens, 8 of 128 experts: 25.0 us, 17.4 us spread out).
+constexpr size_t kManySmem = 116 * 1024;
+static_assert((kMaxGroups + 1) * (8 + kPlaceThreads / 32 * 4) <= kManySmem);
 
-__global__ void __launch_bounds__(kManyThreads) k_route_place(const RouteLaunch L, const int* hist) {
+__global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteLaunch L, const int* hist) {
   extern __shared__ int s_dyn[];
-  __shared__ int s_warp[kManyThreads / 32];
+  __shared__ int s_warp[kPlaceThreads / 32];
   int* total = s_dyn;                // [E + 1]
   int* before = total + L.E + 1;     // [E + 1] of the blocks before this one
   uint32_t* wc = reinterpret_cast<uint32_t*>(before + L.E + 1);
   const int GE = L.E + 1;
-  for (int e = threadIdx.x; e < GE; e += kManyThreads) total[e] = before[e] = 0;
+  for (int e = threadIdx.x; e < GE; e += kPlaceThreads) total[e] = before[e] = 0;
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
   const int all = (int)gridDim.x * GE, mine = (int)blockIdx.x * GE;
 #pragma unroll 8
-  for (int i = threadIdx.x; i < all; i += kManyThreads) {
+  for (int i = threadIdx.x; i < all; i += kPlaceThreads) {
     const int v = __ldcg(hist + i), e = i % GE;
     if (v) {
       atomicAdd(total + e, v);
@@ -264,14 +270,14 @@ __global__ void __launch_bounds__(kManyThreads) k_route_place(const RouteLaunch 
     }
   }
   __syncthreads();
-  block_scan<kManyThreads>(total, GE, s_warp);
+  block_scan<kPlaceThreads>(total, GE, s_warp);
   if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e < GE; e += kManyThreads) L.offsets[e] = total[e];
-  for (int e = threadIdx.x; e < GE; e += kManyThreads) before[e] += total[e];
+    for (int e = threadIdx.x; e < GE; e += kPlaceThreads) L.offsets[e] = total[e];
+  for (int e = threadIdx.x; e < GE; e += kPlaceThreads) before[e] += total[e];
   __syncthreads();
   const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
   const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
-  if (p0 < p1) place_pairs<kManyThreads>(L.ids, p0, p1, L.E, before, wc, L.order);
+  if (p0 < p1) place_pairs<kPlaceThreads>(L.ids, p0, p1, L.E, before, wc, L.order);
 }
 
 template <typename F>
@@ -289,44 +295,34 @@ cudaError_t launch_pdl(F f, int grid, int threads, size_t smem, cudaStream_t s) 
   return f(cfg);
 }
 
-// Raises a kernel's shared-memory limit once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, int (&done)[64]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+template <int PER, int T>
+cudaError_t route_one(const RouteLaunch& L, cudaStream_t s) {
+  static int done[64] = {0};
+  const cudaError_t e = set_up_kernel(k_route_one<PER, T>, one_smem<T>(kMaxGroups), done);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    done[dev] = 1;
-  }
-  return cudaSuccess;
+  return launch_pdl([&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_one<PER, T>, L); },
+                    1, T, one_smem<T>(L.E), s);
 }
 
 template <int PER>
 cudaError_t route_per(const RouteLaunch& L, cudaStream_t s) {
   const int64_t P = L.M * L.topk;
-  if (P <= kOnePairs) {
-    static int done[64] = {0};
-    const cudaError_t e = allow_smem(k_route_one<PER>, one_smem(kMaxGroups), done);
-    if (e != cudaSuccess) return e;
-    return launch_pdl([&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_one<PER>, L); },
-                      1, kOneThreads, one_smem(L.E), s);
-  }
+  if (P <= kOnePairs)
+    return (L.logits ? L.M <= 8 : P <= 256) ? route_one<PER, 256>(L, s) : route_one<PER, 1024>(L, s);
   static int done[64] = {0};
-  cudaError_t e = allow_smem(k_route_place, many_smem(kMaxGroups), done);
+  cudaError_t e = set_up_kernel(k_route_place, kManySmem, done);
   if (e != cudaSuccess) return e;
   int* hist = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(L.workspace) + 256);
   const int64_t want = (P + 255) / 256;
   const int blocks = (int)(want < kManyBlocks ? want : kManyBlocks);
+  constexpr int T = PER > 8 ? 512 : 1024;  // registers for the keys (8192 tokens: 9.0 us, 11.7 with 512)
   e = launch_pdl(
-      [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_count<PER>, L, hist); },
-      blocks, kManyThreads, 0, s);
+      [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_count<PER, T>, L, hist); },
+      blocks, T, 0, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(
       [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_place, L, (const int*)hist); },
-      blocks, kManyThreads, many_smem(L.E), s);
+      blocks, kPlaceThreads, kManySmem, s);
 }
 
 }  // namespace

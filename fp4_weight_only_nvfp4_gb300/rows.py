@@ -13,10 +13,8 @@ SCORING = {"softmax": 0, "sigmoid": 1}
 GATHER, SCATTER, SILU_MUL = 1, 2, 4
 
 
-def _raw_stream(stream, device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_current_stream = torch._C._cuda_getCurrentRawStream
+_BF16 = torch.bfloat16
 
 
 def _need(t, name, dtype, shape, device):
@@ -27,22 +25,26 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a CUDA tensor on {device} (got {t.device})")
 
 
-def _rows(t, name, rows, cols, device):
-    """A bf16 matrix with unit inner stride on this GPU; returns its row stride."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols \
-            or (cols > 1 and t.stride(1) != 1):
+def _rows(t, name, rows, cols, gpu):
+    """A bf16 matrix with unit inner stride on GPU number gpu; returns its row stride."""
+    if t.dtype is not _BF16 or t.shape != (rows, cols):
         raise ValueError(f"{name} must be a bf16 [{rows}, {cols}] tensor with unit inner stride")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device} (got {t.device})")
-    st = t.stride(0)
-    if rows > 1 and st < cols:
-        raise ValueError(f"{name} must not have overlapping rows")
-    return st if rows > 1 else max(st, cols)
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must be a bf16 [{rows}, {cols}] tensor with unit inner stride")
+    if t.get_device() != gpu or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name} must not have overlapping rows")
+        ld = cols
+    return ld
 
 
-def _workspace(ws, device):
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or not ws.is_cuda or ws.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor on {device}")
+def _workspace(ws, gpu):
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != gpu \
+            or not ws.is_cuda:
+        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor on cuda:{gpu}")
     return ws.data_ptr(), ws.numel()
 
 
@@ -59,6 +61,7 @@ class RowGroups:
         self.M, self.topk = ids.shape[0], (ids.shape[1] if ids.dim() == 2 else 1)
         self.E, self.pairs = offsets.numel() - 1, ids.numel()
         dev = self.device = ids.device
+        self.gpu = ids.get_device()
         _need(ids, "ids", torch.int32, tuple(ids.shape), dev)
         _need(order, "order", torch.int32, (self.pairs,), dev)
         _need(offsets, "offsets", torch.int32, (self.E + 1,), dev)
@@ -89,7 +92,7 @@ def group_rows(ids: torch.Tensor, E: int, out: RowGroups | None = None,
     if ids.dtype != torch.int32 or ids.dim() not in (1, 2) or not ids.is_contiguous() \
             or not ids.is_cuda:
         raise ValueError("ids must be a contiguous int32 CUDA tensor [M] or [M, topk]")
-    dev = ids.device
+    dev, gpu = ids.device, ids.get_device()
     if out is None:
         out = RowGroups(ids, torch.empty(ids.numel(), dtype=torch.int32, device=dev),
                         torch.empty(E + 1, dtype=torch.int32, device=dev))
@@ -99,9 +102,9 @@ def group_rows(ids: torch.Tensor, E: int, out: RowGroups | None = None,
         out.ids = ids
     if workspace is None:
         workspace = group_workspace(ids.numel(), 1, E, dev)
-    wp, wn = _workspace(workspace, dev)
+    wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_group_rows(ids.data_ptr(), ids.numel(), E, out.order.data_ptr(),
-                                  out.offsets.data_ptr(), wp, wn, _raw_stream(stream, dev)),
+                                  out.offsets.data_ptr(), wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)),
           "vt_fp4_group_rows")
     return out
 
@@ -120,22 +123,22 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
     if scoring not in SCORING:
         raise ValueError(f"scoring must be one of {sorted(SCORING)}")
     M, E = logits.shape
-    dev = logits.device
+    dev, gpu = logits.device, logits.get_device()
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,), dev)
     if out is None:
         out = RowGroups.empty(M, topk, E, dev, weights=True)
-    elif (out.M, out.topk, out.E, out.device) != (M, topk, E, dev) or out.weights is None:
+    elif (out.M, out.topk, out.E, out.gpu) != (M, topk, E, gpu) or out.weights is None:
         raise ValueError("out must be RowGroups.empty(M, topk, E, device, weights=True)")
     if workspace is None:
         workspace = group_workspace(M, topk, E, dev)
-    wp, wn = _workspace(workspace, dev)
+    wp, wn = _workspace(workspace, gpu)
     ld = logits.stride(0) if M > 1 else max(logits.stride(0), E)
     check(lib().vt_fp4_moe_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), M, ld, E,
                                  topk, SCORING[scoring], bias.data_ptr() if bias is not None else 0,
                                  int(renormalize), scale, out.ids.data_ptr(),
                                  out.weights.data_ptr(), out.order.data_ptr(),
-                                 out.offsets.data_ptr(), wp, wn, _raw_stream(stream, dev)),
+                                 out.offsets.data_ptr(), wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)),
           "vt_fp4_moe_route")
     return out
 
@@ -144,24 +147,25 @@ def _check_groups(W, groups):
     E = getattr(W, "E", 1)
     if groups.E != E:
         raise ValueError(f"the groups are of {groups.E} indices, the weight has {E} experts")
-    if groups.device != W.packed.device:
+    gpu = W.packed.get_device()
+    if groups.gpu != gpu:
         raise ValueError(f"groups must be on {W.packed.device}")
+    return gpu
 
 
 def _ragged(A, W, groups, out, workspace, stream, flags, cols):
-    _check_groups(W, groups)
-    dev = W.packed.device
-    lda = _rows(A, "A", groups.M if flags & GATHER else groups.pairs, W.K, dev)
+    gpu = _check_groups(W, groups)
+    lda = _rows(A, "A", groups.M if flags & GATHER else groups.pairs, W.K, gpu)
     if out is None:
-        out = torch.empty((groups.pairs, cols), dtype=torch.bfloat16, device=dev)
-    ldc = _rows(out, "out", groups.pairs, cols, dev)
+        out = torch.empty((groups.pairs, cols), dtype=torch.bfloat16, device=A.device)
+    ldc = _rows(out, "out", groups.pairs, cols, gpu)
     if workspace is None:
         workspace = W.ragged_workspace(groups.M, groups.topk)
-    wp, wn = _workspace(workspace, dev)
+    wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_w4a16_gemm_ragged(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
                                          groups.offsets.data_ptr(), groups.pairs, groups.topk,
                                          flags, out.data_ptr(), ldc, wp, wn,
-                                         _raw_stream(stream, dev)), "vt_fp4_w4a16_gemm_ragged")
+                                         stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_w4a16_gemm_ragged")
     return out
 
 
@@ -191,21 +195,20 @@ def w4a16_gemm_ragged_combine(A: torch.Tensor, W, groups: RowGroups,
                               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The experts' second products (A [pairs, K], rows in group order) and each token's sum of
     them by groups.weights: out [M, N] (bf16).  Pairs in no group count as zero."""
-    _check_groups(W, groups)
+    gpu = _check_groups(W, groups)
     if groups.weights is None:
         raise ValueError("the groups hold no weights")
-    dev = W.packed.device
-    lda = _rows(A, "A", groups.pairs, W.K, dev)
+    lda = _rows(A, "A", groups.pairs, W.K, gpu)
     if out is None:
-        out = torch.empty((groups.M, W.N), dtype=torch.bfloat16, device=dev)
-    ldc = _rows(out, "out", groups.M, W.N, dev)
+        out = torch.empty((groups.M, W.N), dtype=torch.bfloat16, device=A.device)
+    ldc = _rows(out, "out", groups.M, W.N, gpu)
     if workspace is None:
         workspace = W.ragged_workspace(groups.M, groups.topk)
-    wp, wn = _workspace(workspace, dev)
+    wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_w4a16_gemm_ragged_combine(
         A.data_ptr(), lda, W.handle, groups.ids.data_ptr(), groups.order.data_ptr(),
         groups.offsets.data_ptr(), groups.weights.data_ptr(), groups.M, groups.topk,
-        out.data_ptr(), ldc, wp, wn, _raw_stream(stream, dev)), "vt_fp4_w4a16_gemm_ragged_combine")
+        out.data_ptr(), ldc, wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_w4a16_gemm_ragged_combine")
     return out
 
 
@@ -239,6 +242,7 @@ class LoraAdapters:
         if ranks is not None:
             _need(ranks, "ranks", torch.int32, (self.L,), dev)
         self.A, self.B, self.scale, self.ranks = A, B, scale, ranks
+        self.gpu = A.get_device()
 
 
 def lora_add(x: torch.Tensor, adapters: LoraAdapters, groups: RowGroups, y: torch.Tensor,
@@ -248,17 +252,16 @@ def lora_add(x: torch.Tensor, adapters: LoraAdapters, groups: RowGroups, y: torc
     ad = adapters
     if groups.topk != 1 or groups.E != ad.L:
         raise ValueError("groups must hold one id of [0, L) per row")
-    dev = ad.device
-    if groups.device != dev:
-        raise ValueError(f"groups must be on {dev}")
-    M = groups.M
-    ldx, ldy = _rows(x, "x", M, ad.K, dev), _rows(y, "y", M, ad.N, dev)
+    gpu, M = ad.gpu, groups.M
+    if groups.gpu != gpu:
+        raise ValueError(f"groups must be on {ad.device}")
+    ldx, ldy = _rows(x, "x", M, ad.K, gpu), _rows(y, "y", M, ad.N, gpu)
     if out is None:
-        out = torch.empty((M, ad.N), dtype=torch.bfloat16, device=dev)
-    ldo = _rows(out, "out", M, ad.N, dev)
+        out = torch.empty((M, ad.N), dtype=torch.bfloat16, device=ad.device)
+    ldo = _rows(out, "out", M, ad.N, gpu)
     check(lib().vt_fp4_lora_add(x.data_ptr(), M, ldx, ad.K, ad.A.data_ptr(), ad.B.data_ptr(),
                                 ad.scale.data_ptr(), 0 if ad.ranks is None else ad.ranks.data_ptr(),
                                 ad.L, ad.R, ad.N, groups.order.data_ptr(),
                                 groups.offsets.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo,
-                                _raw_stream(stream, dev)), "vt_fp4_lora_add")
+                                stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_lora_add")
     return out
