@@ -186,15 +186,18 @@ struct LoraLaunch {
 };
 cudaError_t launch_lora(const LoraLaunch& L, cudaStream_t s);
 
-// Raises a kernel's limit of dynamic shared memory, once per device.
+// Raises a kernel's limits of dynamic shared memory and (large) cluster size, once per device.
 template <typename K>
-inline cudaError_t set_up_kernel(K kernel, size_t bytes, int (&done)[64]) {
+inline cudaError_t set_up_kernel(K kernel, size_t bytes, int (&done)[64],
+                                 bool large_cluster = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && large_cluster)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }

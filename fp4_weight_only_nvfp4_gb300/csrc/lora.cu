@@ -3,13 +3,14 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "handle.h"
 #include "kernels.h"
 
 namespace vt {
 
 namespace {
 
-// One cluster of kCluster CTAs per tile of up to TM rows of one adapter.  First each CTA sums its
+// One cluster of 8 or 16 CTAs per tile of up to TM rows of one adapter.  First each CTA sums its
 // share of K (v = A x: ranks are the MMA's rows, tokens its columns) and the cluster adds the
 // shares through distributed shared memory, in CTA order; then each CTA adds v B^T to its share of
 // y's columns (tokens are rows).  x, y and out cross the memory bus once, an adapter once per tile
@@ -19,7 +20,6 @@ namespace {
 // asynchronous 16-byte copies, the columns' chunks already under way while v is exchanged (with
 // loads to registers too few bytes were in flight: 53 us against NOW us for 5003 rows, 4096 -> 5120,
 // rank 32).  Rows that are not 16-byte aligned are copied to the same chunks value by value.
-constexpr int kCluster = 8;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 128;             // k, or columns, per chunk
@@ -28,16 +28,21 @@ constexpr int kStride = kChunk * 2 + 16;  // bytes per row of a chunk of x, A or
 // TM: rows per tile; RM: ranks held.
 template <int TM, int RM>
 struct LoraSmem {
-  static constexpr int WT = TM / 16, WK = kWarps / WT;      // token groups, shares of a chunk's k
+  // v's warps: WT groups of 16 tokens, WR of rank tiles (each takes every WR-th), WK shares of k
+  static constexpr int WT = TM / 16, WR = RM / 16 < kWarps / WT ? RM / 16 : kWarps / WT;
+  static constexpr int WK = kWarps / WT / WR;
   static constexpr int BStride = RM * 2 + 16;               // bytes per column of B, per row of v
   static constexpr int ChunkA = (RM + TM) * kStride, ChunkB = kChunk * BStride + TM * kStride;
   static constexpr int Stage = ChunkA > ChunkB ? ChunkA : ChunkB;
-  static constexpr int Stages = RM == 128 && TM == 64 ? 2 : 3;
   static constexpr int VStride = RM + 4;                    // floats per token of the partial sums
-  static constexpr int Partial = WK * TM * VStride * 4;
+  static constexpr int Partial = WK * TM * VStride * 4, V = 2 * TM * BStride;
+  // as many stages as two CTAs of an SM hold, or one CTA where that were fewer than three
+  static constexpr int Half = (113 * 1024 - Partial - V) / Stage, All = (226 * 1024 - Partial - V) / Stage;
+  static constexpr int Ctas = Half >= 3 ? 2 : 1, Most = Ctas == 2 ? Half : All;
+  static constexpr int Stages = Most < 6 ? Most : 6;
   static constexpr int OffPart = Stages * Stage, OffV = OffPart + Partial;
-  static constexpr int Bytes = OffV + 2 * TM * BStride;
-  static_assert(Bytes <= 227 * 1024, "shared memory");
+  static constexpr int Bytes = OffV + V;
+  static_assert(Stages >= 2, "shared memory");
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -99,8 +104,8 @@ __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, in
   }
 }
 
-template <int TM, int RM, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
+template <int TM, int RM, int kCluster, bool VEC>
+__global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const LoraLaunch L) {
   using S = LoraSmem<TM, RM>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_warp[kWarps], s_e, s_i0, s_n, s_row[TM];
@@ -236,56 +241,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
   bool late_wait = false;
   if (R > 0) {
     // ---------------------------------------------------------------- v = A x
-    const int wt = warp % S::WT, wk = warp / S::WT;
-    float acc[RM / 16][2][4] = {};
+    const int wt = warp % S::WT, wr = warp / S::WT % S::WR, wk = warp / S::WT / S::WR;
+    constexpr int MT = RM / 16 / S::WR;  // rank tiles wr, wr + WR, ... of the warp
+    float acc[MT][2][4] = {};
     for (int c = 0; c < nk; ++c) {
       const uint32_t st = next(c);
-      if (wt * 16 >= n) continue;
+      if (wt * 16 >= n || wr * 16 >= R) continue;
       // k steps wk, wk + WK, ...: the fragments of kS of them are loaded before their products
-      constexpr int kSteps = kChunk / 16 / S::WK, kS = kSteps < 2 ? 1 : 2;
+      constexpr int kSteps = kChunk / 16 / S::WK, kS = kSteps < 4 / MT ? kSteps : MT < 4 ? 4 / MT : 1;
 #pragma unroll
       for (int s0 = 0; s0 < kSteps; s0 += kS) {
-        uint32_t xv[kS][4], av[kS][RM / 16][4];
+        uint32_t xv[kS][4], av[kS][MT][4];
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
           const int ks = ((s0 + s) * S::WK + wk) * 32;  // byte of the 16-k step in a row
           // tokens 0-7 (k low, high), 8-15
           ldmatrix4(st + (wt * 16 + (lmat >> 1) * 8 + lrow) * kStride + ks + (lmat & 1) * 16, xv[s]);
 #pragma unroll
-          for (int m = 0; m < RM / 16; ++m)
+          for (int i = 0; i < MT; ++i) {
+            const int m = i * S::WR + wr;
             if (m * 16 < R)
-              ldmatrix4(st + (TM + m * 16 + (lmat & 1) * 8 + lrow) * kStride + ks + (lmat >> 1) * 16, av[s][m]);
+              ldmatrix4(st + (TM + m * 16 + (lmat & 1) * 8 + lrow) * kStride + ks + (lmat >> 1) * 16, av[s][i]);
+          }
         }
 #pragma unroll
         for (int s = 0; s < kS; ++s)
 #pragma unroll
-          for (int m = 0; m < RM / 16; ++m)
-            if (m * 16 < R) {
-              mma_bf16(acc[m][0], av[s][m], xv[s][0], xv[s][1]);
-              mma_bf16(acc[m][1], av[s][m], xv[s][2], xv[s][3]);
+          for (int i = 0; i < MT; ++i)
+            if ((i * S::WR + wr) * 16 < R) {
+              mma_bf16(acc[i][0], av[s][i], xv[s][0], xv[s][1]);
+              mma_bf16(acc[i][1], av[s][i], xv[s][2], xv[s][3]);
             }
       }
     }
 #pragma unroll
-    for (int m = 0; m < RM / 16; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s_part[(wk * TM + wt * 16 + j * 8 + 2 * t + (i & 1)) * S::VStride + m * 16 + g + (i >> 1) * 8] =
-              acc[m][j][i];
-    __syncthreads();
-    // the CTA's share of v, over its warps' shares of k
+          s_part[(wk * TM + wt * 16 + j * 8 + 2 * t + (i & 1)) * S::VStride + (m * S::WR + wr) * 16 + g +
+                 (i >> 1) * 8] = acc[m][j][i];
     const int r4s = R16 / 4;
-    for (int i = tid; i < n * r4s; i += kThreads) {
-      float* at = s_part + i / r4s * S::VStride + i % r4s * 4;
-      float4 v = *reinterpret_cast<float4*>(at);
-#pragma unroll
-      for (int w = 1; w < S::WK; ++w) {
-        const float4 u = *reinterpret_cast<float4*>(at + w * TM * S::VStride);
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    if constexpr (S::WK > 1) {  // the CTA's share of v, over its warps' shares of k
+      __syncthreads();
+      for (int i = tid; i < n * r4s; i += kThreads) {
+        float* at = s_part + i / r4s * S::VStride + i % r4s * 4;
+        float4 v = *reinterpret_cast<float4*>(at);
+  #pragma unroll
+        for (int w = 1; w < S::WK; ++w) {
+          const float4 u = *reinterpret_cast<float4*>(at + w * TM * S::VStride);
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        *reinterpret_cast<float4*>(at) = v;
       }
-      *reinterpret_cast<float4*>(at) = v;
     }
     cluster_arrive();
     cluster_wait();
@@ -411,15 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora(const LoraLaunch L) {
   if (late_wait) cluster_wait();
 }
 
-template <int TM, int RM, bool VEC>
-cudaError_t launch(const LoraLaunch& L, cudaStream_t s) {
+template <int TM, int RM, int kCluster, bool VEC>
+cudaError_t launch(const LoraLaunch& L, int64_t tiles, cudaStream_t s) {
   constexpr int bytes = LoraSmem<TM, RM>::Bytes;
   static int done[64] = {0};
-  const cudaError_t e = set_up_kernel(k_lora<TM, RM, VEC>, bytes, done);
+  const cudaError_t e = set_up_kernel(k_lora<TM, RM, kCluster, VEC>, bytes, done, kCluster > 8);
   if (e != cudaSuccess) return e;
-  // at most one partial tile per group in use, the rows without adapter a group too
-  const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1;
-  const int64_t tiles = groups + L.M / TM;
   if (tiles * kCluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * kCluster));
@@ -435,7 +441,7 @@ cudaError_t launch(const LoraLaunch& L, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM, VEC>, L);
+  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM, kCluster, VEC>, L);
 }
 
 template <int TM, int RM>
@@ -443,7 +449,15 @@ cudaError_t launch_vec(const LoraLaunch& L, cudaStream_t s) {
   // 16-byte copies need every row aligned and whole groups of 8
   const bool vec = ((uintptr_t)L.x | (uintptr_t)L.A | (uintptr_t)L.B | (uintptr_t)L.y | (uintptr_t)L.out) % 16 == 0 &&
                    (L.ldx | L.K | (int64_t)L.R | L.ldy | L.ldo | L.N) % 8 == 0;
-  return vec ? launch<TM, RM, true>(L, s) : launch<TM, RM, false>(L, s);
+  // at most one partial tile per group in use, the rows without adapter a group too
+  const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1, tiles = groups + L.M / TM;
+  if (!vec) return launch<TM, RM, 8, false>(L, tiles, s);
+  // While clusters of 16 find an SM for each CTA, they halve what a CTA reads one after another
+  // (1 row, 4096 -> 4096, rank 16: 5.0 us, 6.3 with 8); beyond, 8 (96 rows of 64 adapters: NOW
+  // us, 30 with 16, 22 with 4).
+  if constexpr (TM == 16)
+    if (tiles * 16 <= sm_count()) return launch<TM, RM, 16, true>(L, tiles, s);
+  return launch<TM, RM, 8, true>(L, tiles, s);
 }
 
 template <int RM>
