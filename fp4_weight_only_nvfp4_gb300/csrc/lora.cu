@@ -86,11 +86,10 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t rank, uint
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// 8 consecutive values to shared memory, the first n of them valid (the others zeros).  VEC: one
+// 8 consecutive values to shared memory, the first n (0 to 8) of them valid (the others zeros).  VEC: one
 // asynchronous copy (src 16-byte aligned); else value by value.
 template <bool VEC>
 __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int n) {
-  n = n < 0 ? 0 : (n > 8 ? 8 : n);
   if constexpr (VEC) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n * 2)
                  : "memory");
@@ -184,55 +183,83 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const
   const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(L.y);
 
   // Chunk c of the CTA's work: nk of x [TM] over A [R16] (rows of 128 k), then y [TM] over B
-  // [128 columns] (rows of ranks).  A thread copies piece `pc` of rows r0, r0 + 16, ... of x, y and
-  // A, and piece bp of columns bc0, bc0 + bstep, ... of B, 2^sh >= R16 / 8 threads to a column.
+  // [128 columns] (rows of ranks).  A thread copies piece `pc` of rows r0, r0 + RP, ... of x, y and
+  // A, and piece bp of columns bc0, bc0 + bstep, ... of B, 2^sh >= R16 / 8 threads to a column; its
+  // pointers move on by a chunk per fetch (issuing the copies is a good part of a chunk's time).
   // Sources of zeros point at valid memory all the same.
-  constexpr int P = kChunk / 8;  // pieces per row
+  constexpr int P = kChunk / 8, RP = kThreads / P, XP = TM / RP;  // pieces per row, rows per pass
   const int pc = tid % P, r0 = tid / P;
-  int rows[TM / 16];
+  const __nv_bfloat16* px[XP];  // this thread's pieces of x, then of y
+  int xrow[XP];
 #pragma unroll
-  for (int i = 0; i < TM / 16; ++i) rows[i] = s_row[r0 + i * 16];
+  for (int i = 0; i < XP; ++i) {
+    xrow[i] = s_row[r0 + i * RP];
+    px[i] = x + max(xrow[i], 0) * L.ldx + k0 + pc * 8;
+  }
   const int sh = R16 <= 16 ? 1 : R16 <= 32 ? 2 : R16 <= 64 ? 3 : 4;
   const int bp = tid & ((1 << sh) - 1), bc0 = tid >> sh, bstep = kThreads >> sh;
-  auto fetch = [&](int c) {
-    if (c < chunks) {
-      const uint32_t st = ring + (uint32_t)(c % S::Stages) * S::Stage;
-      const bool first = c < nk;
-      const int b0 = first ? k0 + c * kChunk : c0 + (c - nk) * kChunk, end = first ? k1 : c1;
-      const int q = b0 + pc * 8, left = end - q;
-      const __nv_bfloat16* src = (first ? x : y) + (left > 0 ? q : 0);
-      const int64_t ld = first ? L.ldx : L.ldy;
-      const uint32_t to = st + r0 * kStride + pc * 16;
+  const int have = min(max(R - bp * 8, 0), 8);  // ranks of this thread's piece of a column
+  const int64_t stepA = (int64_t)RP * K, stepB = (int64_t)bstep * L.R;
+  const __nv_bfloat16* pa = A + (int64_t)r0 * K + k0 + pc * 8;
+  const __nv_bfloat16* pb = B + (int64_t)(c0 + bc0) * L.R + bp * 8;
+  const uint32_t to_row = ring + r0 * kStride + pc * 16, to_b = ring + TM * kStride + bc0 * S::BStride + bp * 16;
+  int fetched = 0;
+  uint32_t slot = 0;  // byte offset of the next chunk's stage
+  auto fetch = [&] {
+    const int c = fetched++;
+    if (c < nk) {
+      const int left = min(max(k1 - (k0 + c * kChunk + pc * 8), 0), 8);
+      const uint32_t to = to_row + slot;
 #pragma unroll
-      for (int i = 0; i < TM / 16; ++i)
-        if (i * 16 < n) copy8<VEC>(to + i * 16 * kStride, src + (rows[i] >= 0 ? rows[i] * ld : 0), rows[i] >= 0 ? left : 0);
-      if (first) {
-        const __nv_bfloat16* a = A + (left > 0 ? q : 0);
+      for (int i = 0; i < XP; ++i) {
+        if (i * RP < n) copy8<VEC>(to + i * RP * kStride, left > 0 ? px[i] : x, xrow[i] >= 0 ? left : 0);
+        px[i] += kChunk;
+      }
+      const __nv_bfloat16* a = pa;
 #pragma unroll
-        for (int i = 0; i < RM / 16; ++i)
-          if (i * 16 < R) {
-            const int j = r0 + i * 16;
-            copy8<VEC>(to + (TM + i * 16) * kStride, a + (j < R ? (int64_t)j * K : 0), j < R ? left : 0);
-          }
-      } else if (bp * 8 < R16) {
-        const uint32_t tb = st + TM * kStride + bp * 16;
-        const int have = R - bp * 8;  // of this piece's ranks
+      for (int i = 0; i < RM / RP; ++i) {
+        if (i * RP < R) copy8<VEC>(to + (TM + i * RP) * kStride, left > 0 && r0 + i * RP < R ? a : A, r0 + i * RP < R ? left : 0);
+        a += stepA;
+      }
+      pa += kChunk;
+    } else if (c < chunks) {
+      if (c == nk) {
+#pragma unroll
+        for (int i = 0; i < XP; ++i) px[i] = y + max(xrow[i], 0) * L.ldy + c0 + pc * 8;
+      }
+      const int b0 = c0 + (c - nk) * kChunk, left = min(max(c1 - (b0 + pc * 8), 0), 8);
+      const uint32_t to = to_row + slot;
+#pragma unroll
+      for (int i = 0; i < XP; ++i) {
+        if (i * RP < n) copy8<VEC>(to + i * RP * kStride, left > 0 ? px[i] : y, xrow[i] >= 0 ? left : 0);
+        px[i] += kChunk;
+      }
+      if (bp * 8 < R16) {
+        uint32_t tb = to_b + slot;
+        const __nv_bfloat16* b = pb;
         for (int j = bc0; j < kChunk; j += bstep) {
-          const bool on = b0 + j < end && have > 0;
-          copy8<VEC>(tb + j * S::BStride, B + (on ? (int64_t)(b0 + j) * L.R + bp * 8 : 0), on ? have : 0);
+          const bool on = b0 + j < c1 && have > 0;
+          copy8<VEC>(tb, on ? b : B, on ? have : 0);
+          tb += bstep * S::BStride;
+          b += stepB;
         }
+        pb += (int64_t)kChunk * L.R;
       }
     }
+    slot = slot + S::Stage == S::Stages * S::Stage ? 0 : slot + S::Stage;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int c = 0; c < S::Stages - 1; ++c) fetch(c);
+  for (int c = 0; c < S::Stages - 1; ++c) fetch();
   // the ring's next chunk: landed for every thread, and the one before it used by every thread
-  auto next = [&](int c) {
+  uint32_t used = 0;
+  auto next = [&] {
     asm volatile("cp.async.wait_group %0;" ::"n"(S::Stages - 2) : "memory");
     __syncthreads();
-    fetch(c + S::Stages - 1);
-    return ring + (uint32_t)(c % S::Stages) * S::Stage;
+    fetch();
+    const uint32_t st = ring + used;
+    used = used + S::Stage == S::Stages * S::Stage ? 0 : used + S::Stage;
+    return st;
   };
   // rows of tokens past n in a chunk hold what earlier chunks left: finite or not, they are
   // columns (then rows) of their own that are not stored
@@ -245,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const
     constexpr int MT = RM / 16 / S::WR;  // rank tiles wr, wr + WR, ... of the warp
     float acc[MT][2][4] = {};
     for (int c = 0; c < nk; ++c) {
-      const uint32_t st = next(c);
+      const uint32_t st = next();
       if (wt * 16 >= n || wr * 16 >= R) continue;
       // k steps wk, wk + WK, ...: the fragments of kS of them are loaded before their products
       constexpr int kSteps = kChunk / 16 / S::WK, kS = kSteps < 4 / MT ? kSteps : MT < 4 ? 4 / MT : 1;
@@ -359,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const
 #pragma unroll
   for (int h = 0; h < 2; ++h) orow[h] = s_row[wm * 16 + h * 8 + g];
   for (int c = nk; c < chunks; ++c) {
-    const uint32_t st = next(c);
+    const uint32_t st = next();
     if (kHold && c == nk) {  // v is written by now for every thread
 #pragma unroll
       for (int q = 0; q < RM / 16; ++q)
