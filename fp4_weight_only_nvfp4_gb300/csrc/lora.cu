@@ -18,16 +18,19 @@ namespace {
 // of two bf16 values (16 significant bits).
 // Memory bounds it, so everything streams through a ring of shared-memory chunks filled by
 // asynchronous 16-byte copies, the columns' chunks already under way while v is exchanged (with
-// loads to registers too few bytes were in flight: 53 us against NOW us for 5003 rows, 4096 -> 5120,
-// rank 32).  Rows that are not 16-byte aligned are copied to the same chunks value by value.
+// loads to registers too few bytes were in flight: 53 us for 5003 rows, 4096 -> 5120, rank 32,
+// 46 with them).  Rows that are not 16-byte aligned are copied to the same chunks value by value.
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 128;             // k, or columns, per chunk
-constexpr int kStride = kChunk * 2 + 16;  // bytes per row of a chunk of x, A or y (no bank conflicts)
 
-// TM: rows per tile; RM: ranks held.
-template <int TM, int RM>
+// TM: rows per tile; RM: ranks held.  A chunk has a fixed cost of barriers and copies to issue:
+// 256 wide where a CTA has an SM for itself (1 row: 4.6 us, 5.3 with 128); else 128 and as many CTAs
+// per SM as hold two chunks each, with 80 registers a thread for three (96 rows of 64 adapters:
+// 19.2 us; two CTAs of four chunks 20.5; three of five chunks of 64 22.3).
+template <int TM, int RM, int kCluster>
 struct LoraSmem {
+  static constexpr int kChunk = kCluster == 16 ? 256 : 128;  // k, or columns, per chunk
+  static constexpr int kStride = kChunk * 2 + 16;           // bytes per row of x, A or y (no bank conflicts)
   // v's warps: WT groups of 16 tokens, WR of rank tiles (each takes every WR-th), WK shares of k
   static constexpr int WT = TM / 16, WR = RM / 16 < kWarps / WT ? RM / 16 : kWarps / WT;
   static constexpr int WK = kWarps / WT / WR;
@@ -36,10 +39,11 @@ struct LoraSmem {
   static constexpr int Stage = ChunkA > ChunkB ? ChunkA : ChunkB;
   static constexpr int VStride = RM + 4;                    // floats per token of the partial sums
   static constexpr int Partial = WK * TM * VStride * 4, V = 2 * TM * BStride;
-  // as many stages as two CTAs of an SM hold, or one CTA where that were fewer than three
-  static constexpr int Half = (113 * 1024 - Partial - V) / Stage, All = (226 * 1024 - Partial - V) / Stage;
-  static constexpr int Ctas = Half >= 3 ? 2 : 1, Most = Ctas == 2 ? Half : All;
-  static constexpr int Stages = Most < 6 ? Most : 6;
+  static constexpr int stages(int ctas) { return ((228 / ctas - 1) * 1024 - 512 - Partial - V) / Stage; }
+  static constexpr int Ctas = kCluster == 16 ? 1
+                              : TM == 16     ? (stages(3) >= 2 ? 3 : stages(2) >= 2 ? 2 : 1)
+                                             : (stages(2) >= 3 ? 2 : 1);
+  static constexpr int Stages = stages(Ctas) < 6 ? stages(Ctas) : 6;
   static constexpr int OffPart = Stages * Stage, OffV = OffPart + Partial;
   static constexpr int Bytes = OffV + V;
   static_assert(Stages >= 2, "shared memory");
@@ -104,8 +108,9 @@ __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, in
 }
 
 template <int TM, int RM, int kCluster, bool VEC>
-__global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const LoraLaunch L) {
-  using S = LoraSmem<TM, RM>;
+__global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_lora(const LoraLaunch L) {
+  using S = LoraSmem<TM, RM, kCluster>;
+  constexpr int kChunk = S::kChunk, kStride = S::kStride;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_warp[kWarps], s_e, s_i0, s_n, s_row[TM];
   const uint32_t ring = smem_u32(smem);
@@ -217,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const
       }
       const __nv_bfloat16* a = pa;
 #pragma unroll
-      for (int i = 0; i < RM / RP; ++i) {
-        if (i * RP < R) copy8<VEC>(to + (TM + i * RP) * kStride, left > 0 && r0 + i * RP < R ? a : A, r0 + i * RP < R ? left : 0);
+      for (int i = 0; i < (RM + RP - 1) / RP; ++i) {
+        if (i * RP < R16) copy8<VEC>(to + (TM + i * RP) * kStride, left > 0 && r0 + i * RP < R ? a : A, r0 + i * RP < R ? left : 0);
         a += stepA;
       }
       pa += kChunk;
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM>::Ctas) k_lora(const
 
 template <int TM, int RM, int kCluster, bool VEC>
 cudaError_t launch(const LoraLaunch& L, int64_t tiles, cudaStream_t s) {
-  constexpr int bytes = LoraSmem<TM, RM>::Bytes;
+  constexpr int bytes = LoraSmem<TM, RM, kCluster>::Bytes;
   static int done[64] = {0};
   const cudaError_t e = set_up_kernel(k_lora<TM, RM, kCluster, VEC>, bytes, done, kCluster > 8);
   if (e != cudaSuccess) return e;
@@ -480,8 +485,8 @@ cudaError_t launch_vec(const LoraLaunch& L, cudaStream_t s) {
   const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1, tiles = groups + L.M / TM;
   if (!vec) return launch<TM, RM, 8, false>(L, tiles, s);
   // While clusters of 16 find an SM for each CTA, they halve what a CTA reads one after another
-  // (1 row, 4096 -> 4096, rank 16: 5.0 us, 6.3 with 8); beyond, 8 (96 rows of 64 adapters: NOW
-  // us, 30 with 16, 22 with 4).
+  // (1 row, 4096 -> 4096, rank 16: 5.1 us, 6.4 with 8, both with chunks of 128); beyond, 8 (96 rows
+  // of 64 adapters, two CTAs per SM: 22.3 us, 30 with 16; 22.0 with 4, but then 1 row 9.5).
   if constexpr (TM == 16)
     if (tiles * 16 <= sm_count()) return launch<TM, RM, 16, true>(L, tiles, s);
   return launch<TM, RM, 8, true>(L, tiles, s);
@@ -489,8 +494,10 @@ cudaError_t launch_vec(const LoraLaunch& L, cudaStream_t s) {
 
 template <int RM>
 cudaError_t launch_rank(const LoraLaunch& L, cudaStream_t s) {
-  // long runs of one adapter: tiles of 64 rows read the adapter a quarter as often
-  return L.M >= 24 * (int64_t)L.L ? launch_vec<64, RM>(L, s) : launch_vec<16, RM>(L, s);
+  // Long runs of one adapter: tiles of 64 rows read the adapter a quarter as often.  4096 -> 4096,
+  // rank 64, 4 adapters, 32 rows each: 9.6 us with 16 rows, 11.5 with 64; 96 rows: 14.7 and 13.8;
+  // 5003 rows of 8 adapters, 4096 -> 5120, rank 32: 66 and 45.
+  return L.M >= 64 * (int64_t)L.L ? launch_vec<64, RM>(L, s) : launch_vec<16, RM>(L, s);
 }
 
 }  // namespace

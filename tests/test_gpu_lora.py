@@ -66,6 +66,21 @@ def test_ranks_missing_adapters_and_unused_storage():
     assert torch.equal(out.cpu()[none], y[none])
 
 
+@pytest.mark.parametrize("R", [24, 64, 128])
+@pytest.mark.parametrize("M", [1, 4])
+def test_few_rows_with_ranks_and_unused_storage(M, R):
+    rng = np.random.default_rng(R + M)
+    L, K, N = 4, 2056, 1032
+    A, B, scale, ranks = _adapters(rng, L, R, K, N, [R - 8, 3, 17, R])
+    for a in range(L):
+        A[a, ranks[a]:], B[a, :, ranks[a]:] = float("nan"), float("inf")
+    x, y = acts(rng, M, K), acts(rng, M, N)
+    for first in range(L):
+        ids = (first + np.arange(M)) % L
+        out = _run(x, y, ids, A, B, scale, ranks)
+        assert_close(out, *_ref(x, y, ids, A, B, scale, ranks))
+
+
 @pytest.mark.parametrize("K,N,padx,pady", [(128, 128, 0, 0), (128, 128, 8, 8), (129, 127, 1, 1),
                                            (132, 130, 4, 2), (136, 133, 3, 5)])
 def test_strides_in_place_and_canaries(K, N, padx, pady):
