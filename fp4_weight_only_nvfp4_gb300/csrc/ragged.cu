@@ -386,11 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {  // token tiles of each group, summed up
     const int per = (L.E + 31) / 32, e0 = lane * per, e1 = min(e0 + per, L.E);
     int sum = 0;
+    bool down = false;
     for (int e = e0; e < e1; ++e) {
       const int n = T.first[e + 1] - T.first[e];
-      bad |= n < 0;
-      sum += n > 0 ? (n + kTok - 1) / kTok : 0;
+      down |= n < 0;
+      sum += (n + kTok - 1) / kTok;
     }
+    down = __any_sync(0xffffffffu, down);  // then no tile at all: their number is bounded by order
+    if (down) sum = 0;
+    bad |= down;
     int run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = e0; e < e1; ++e) {
       T.start[e] = run;
       const int n = T.first[e + 1] - T.first[e];
-      const int nt = n > 0 ? (n + kTok - 1) / kTok : 0;
+      const int nt = down ? 0 : (n + kTok - 1) / kTok;
       // nearly equal tiles of whole MMA column blocks (at most kTok rows, so none is left empty)
       T.rows[e] = (uint16_t)(nt == 0 ? kTok : ((n + nt - 1) / nt + 15) & ~15);
       for (int t = run; t < run + nt && t < kTileTable; ++t) T.of[t] = (uint16_t)e;
@@ -1035,12 +1039,19 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (L.pairs * 4 + 255) / 256 * 256);
   p.rowscale = rowscale;
   p.Ap = ap;
-  // One row tile per item while two would leave SMs without one.
+  // The rules below were measured on 128 experts, top-8, gate_up 1536 x 2048 NVFP4 ("A") and 24
+  // experts, top-3, gate_up 2880 x 2592 MXFP4 ("B"), us:
+  // One row tile per item while every item gets an SM of its own, so that an SM's share of the
+  // weights is the least (1 token, A: 10.9, 12.1 with two; B: 12.9 and 14.2); else two, which share
+  // the token tile (2 tokens, A: 12.4, 16.0 with one; 77: 48.6 and 66.2).
   const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
-  const bool two = groups * ((L.RT + 1) / 2) >= sm_count();
-  // Gathered rows: the pre-pass writes them in group order while that is little data, else it
-  // converts each token once and the loaders gather.
-  const bool many = two && L.pairs >= 64 * groups;  // rows per group
+  const bool two = groups * L.RT > sm_count();
+  // Tiles of 128 rows from 64 rows per group on (64 rows, A: 69.8, 85.6 with tiles of 64; B: 35.3
+  // and 41.6; 32 rows, A: 55.5 and 54.2; 19 rows, B: 30.2 and 29.0).
+  const bool many = two && L.pairs >= 64 * groups;
+  // Gathered rows: the pre-pass writes them in group order while that is little data (3063 rows, B:
+  // 53.6, 54.7 by loaders), else it converts each token once and the loaders gather (6144 rows, B:
+  // 82.1, 83.3 in group order; 32768 rows, A: 157 and 186).
   const bool load = L.gather && L.topk > 1 && many && L.pairs * L.K > (8 << 20);
   const int64_t rows = load ? L.pairs / L.topk : L.pairs;
   // the converted rows as a 2-D tensor: reads past the last row return zeros

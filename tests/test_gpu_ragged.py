@@ -344,3 +344,69 @@ def test_wrong_shapes_are_refused():
                                      workspace=W.ragged_workspace(0, 1))
     with pytest.raises(_lib.VtError, match="plain grouped"):
         vt.w4a16_gemm_ragged_combine(acts(rng, M * topk, K).cuda(), Wp, gw)
+
+
+def test_more_token_tiles_than_the_lookup_table_holds():
+    rng = np.random.default_rng(14)
+    E, N, K = 1024, 72, 32
+    counts = [1] * 600 + [40000] + [3] * (E - 601)
+    W, ws = _plain(rng, vt.NVFP4, E, N, K)
+    ids = np.repeat(np.arange(E, dtype=np.int32), counts).reshape(-1, 1)
+    groups, order, offsets = _groups(ids, E)
+    x = acts(rng, len(ids), K)
+    assert_close(vt.w4a16_gemm_ragged(x.cuda(), W, groups), *_ref(f64(x), ws, order, offsets, 1, True))
+
+
+def test_smallest_mx_scales():
+    """Scale byte 0 (2^-127) beside scales near 1, and rows that hold nothing else."""
+    rng = np.random.default_rng(15)
+    E, N, K, M = 2, 130, 96, 20
+    c, s, g = random_weight(rng, vt.MXFP4, E, N, K)
+    s[:, ::2, 1] = 0
+    s[:, 1::4] = 0
+    W = vt.PackedWeight.grouped(_dev(c), _dev(s), g, vt.MXFP4, E, N, K)
+    ws = [weight64(vt.MXFP4, c[e], s[e]) for e in range(E)]
+    groups, order, offsets = _groups(_ids(rng, M, 1, E), E)
+    x = acts(rng, M, K)
+    assert_close(vt.w4a16_gemm_ragged(x.cuda(), W, groups), *_ref(f64(x), ws, order, offsets, 1, True))
+
+
+@pytest.mark.parametrize("M,topk,E,N,K", [(6, 2, 4, 136, 96), (2100, 8, 64, 320, 544)])
+def test_pairs_out_of_range_are_reported_and_not_followed(M, topk, E, N, K):
+    rng = np.random.default_rng(M)
+    W, ws = _plain(rng, vt.NVFP4, E, N, K)
+    groups, order, offsets = _groups(_ids(rng, M, topk, E), E)
+    x, xg = acts(rng, M, K), acts(rng, M * topk, K)
+    wild = order.copy()
+    at = rng.choice(M * topk, 4, replace=False)
+    wild[at] = [-1, M * topk, 2 ** 31 - 1, -2 ** 31]
+    bad = vt.RowGroups(groups.ids, _dev(wild), groups.offsets)
+    right = np.setdiff1d(np.arange(M * topk), at)
+    for gather, scatter in ((True, False), (True, True), (False, True)):
+        ws_ = W.ragged_workspace(M, topk)
+        out = torch.zeros(M * topk, N, dtype=torch.bfloat16, device="cuda")
+        a = x if gather else xg
+        vt.w4a16_gemm_ragged(a.cuda(), W, bad, out=out, workspace=ws_, gather=gather, scatter=scatter)
+        assert vt.workspace_status(ws_) == 6
+        ref, err = _ref(f64(a), ws, order, offsets, topk, gather)
+        got = f64(out)[order] if scatter else f64(out)
+        assert_close(got[right], ref[right], err[right])
+        if scatter:
+            assert not got[at].any()  # no such row
+
+
+@pytest.mark.parametrize("change", [lambda o, P: o.__setitem__(1, P + 5), lambda o, P: o.__setitem__(2, -3),
+                                    lambda o, P: o.__setitem__(3, 0), lambda o, P: o.fill(2 ** 31 - 1)])
+def test_offsets_out_of_range_are_reported(change):
+    rng = np.random.default_rng(17)
+    M, topk, E, N, K = 50, 2, 6, 136, 96
+    W, _ = _plain(rng, vt.NVFP4, E, N, K)
+    groups, order, offsets = _groups(_ids(rng, M, topk, E), E)
+    wild = offsets.copy()
+    change(wild, M * topk)
+    ws = W.ragged_workspace(M, topk)
+    guard = torch.full((M * topk + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    vt.w4a16_gemm_ragged(acts(rng, M, K).cuda(), W, vt.RowGroups(groups.ids, groups.order, _dev(wild)),
+                         out=guard[1:-1], workspace=ws)
+    assert vt.workspace_status(ws) == 6
+    assert (guard[0] == 7).all() and (guard[-1] == 7).all()
