@@ -14,7 +14,7 @@ import torch
 
 from ._lib import GemmOpts, LaunchInfo, VtError, check, lib
 from .rows import (LoraAdapters, RowGroups, group_rows, group_workspace, lora_add, moe_ffn,
-                   moe_route, w4a16_gemm_ragged, w4a16_gemm_ragged_combine,
+                   moe_ffn_workspace, moe_route, w4a16_gemm_ragged, w4a16_gemm_ragged_combine,
                    w4a16_gemm_ragged_silu_mul)
 
 NVFP4, MXFP4 = 0, 1
@@ -25,7 +25,7 @@ __all__ = ["NVFP4", "MXFP4", "GROUP", "PackedWeight", "w4a16_gemm", "w4a16_gemm_
            "quantize_act", "quantize", "prepack_bytes", "workspace_status", "noalloc_status", "VtError",
            "algorithmic_bytes", "RowGroups", "group_rows", "group_workspace", "moe_route",
            "w4a16_gemm_ragged", "w4a16_gemm_ragged_silu_mul", "w4a16_gemm_ragged_combine",
-           "moe_ffn", "LoraAdapters", "lora_add"]
+           "moe_ffn", "moe_ffn_workspace", "LoraAdapters", "lora_add"]
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -166,10 +166,14 @@ class PackedWeight:
     def ragged_workspace(self, M_max: int, topk: int) -> torch.Tensor:
         """A zeroed workspace for the ragged products on this weight of up to M_max tokens of
         topk pairs each (zero once; any smaller call may share it in stream order)."""
+        return torch.zeros(self.ragged_workspace_bytes(M_max, topk), dtype=torch.uint8,
+                           device=self.packed.device)
+
+    def ragged_workspace_bytes(self, M_max: int, topk: int) -> int:
         out = ctypes.c_size_t(0)
         check(lib().vt_fp4_ragged_workspace_bytes(self.handle, M_max, topk, ctypes.byref(out)),
               "vt_fp4_ragged_workspace_bytes")
-        return torch.zeros(out.value, dtype=torch.uint8, device=self.packed.device)
+        return out.value
 
     def moe_workspace(self, M_max: int, topk: int) -> torch.Tensor:
         out = ctypes.c_size_t(0)

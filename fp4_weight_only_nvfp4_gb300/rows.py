@@ -3,6 +3,7 @@ the experts' ragged products, and low-rank adapters (the entry points of include
 vt_fp4_group_rows to vt_fp4_lora_add).  Argument checks and marshalling only."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -15,6 +16,23 @@ GATHER, SCATTER, SILU_MUL = 1, 2, 4
 
 _current_stream = torch._C._cuda_getCurrentRawStream
 _BF16 = torch.bfloat16
+
+
+def _raw(stream, gpu):
+    return stream.cuda_stream if stream is not None else _current_stream(gpu)
+
+
+def _made_on(stream):
+    """Buffers made for a call belong to the stream it runs on: they are zeroed there, and the
+    allocator hands them out again in that stream's order."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _made_on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _need(t, name, dtype, shape, device):
@@ -94,17 +112,18 @@ def group_rows(ids: torch.Tensor, E: int, out: RowGroups | None = None,
         raise ValueError("ids must be a contiguous int32 CUDA tensor [M] or [M, topk]")
     dev, gpu = ids.device, ids.get_device()
     if out is None:
-        out = RowGroups(ids, torch.empty(ids.numel(), dtype=torch.int32, device=dev),
-                        torch.empty(E + 1, dtype=torch.int32, device=dev))
+        out = RowGroups(ids, _empty(ids.numel(), torch.int32, dev, stream),
+                        _empty(E + 1, torch.int32, dev, stream))
     elif out.E != E or out.pairs != ids.numel() or out.device != dev:
         raise ValueError("out does not have the shape of ids and E")
     else:
         out.ids = ids
     if workspace is None:
-        workspace = group_workspace(ids.numel(), 1, E, dev)
+        with _made_on(stream):
+            workspace = group_workspace(ids.numel(), 1, E, dev)
     wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_group_rows(ids.data_ptr(), ids.numel(), E, out.order.data_ptr(),
-                                  out.offsets.data_ptr(), wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)),
+                                  out.offsets.data_ptr(), wp, wn, _raw(stream, gpu)),
           "vt_fp4_group_rows")
     return out
 
@@ -127,18 +146,20 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,), dev)
     if out is None:
-        out = RowGroups.empty(M, topk, E, dev, weights=True)
+        with _made_on(stream):
+            out = RowGroups.empty(M, topk, E, dev, weights=True)
     elif (out.M, out.topk, out.E, out.gpu) != (M, topk, E, gpu) or out.weights is None:
         raise ValueError("out must be RowGroups.empty(M, topk, E, device, weights=True)")
     if workspace is None:
-        workspace = group_workspace(M, topk, E, dev)
+        with _made_on(stream):
+            workspace = group_workspace(M, topk, E, dev)
     wp, wn = _workspace(workspace, gpu)
     ld = logits.stride(0) if M > 1 else max(logits.stride(0), E)
     check(lib().vt_fp4_moe_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), M, ld, E,
                                  topk, SCORING[scoring], bias.data_ptr() if bias is not None else 0,
                                  int(renormalize), scale, out.ids.data_ptr(),
                                  out.weights.data_ptr(), out.order.data_ptr(),
-                                 out.offsets.data_ptr(), wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)),
+                                 out.offsets.data_ptr(), wp, wn, _raw(stream, gpu)),
           "vt_fp4_moe_route")
     return out
 
@@ -157,15 +178,17 @@ def _ragged(A, W, groups, out, workspace, stream, flags, cols):
     gpu = _check_groups(W, groups)
     lda = _rows(A, "A", groups.M if flags & GATHER else groups.pairs, W.K, gpu)
     if out is None:
-        out = torch.empty((groups.pairs, cols), dtype=torch.bfloat16, device=A.device)
+        out = _empty((groups.pairs, cols), _BF16, A.device, stream)
     ldc = _rows(out, "out", groups.pairs, cols, gpu)
     if workspace is None:
-        workspace = W.ragged_workspace(groups.M, groups.topk)
+        with _made_on(stream):
+            workspace = W.ragged_workspace(groups.M, groups.topk)
     wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_w4a16_gemm_ragged(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
                                          groups.offsets.data_ptr(), groups.pairs, groups.topk,
                                          flags, out.data_ptr(), ldc, wp, wn,
-                                         stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_w4a16_gemm_ragged")
+                                         _raw(stream, gpu)),
+          "vt_fp4_w4a16_gemm_ragged")
     return out
 
 
@@ -200,16 +223,24 @@ def w4a16_gemm_ragged_combine(A: torch.Tensor, W, groups: RowGroups,
         raise ValueError("the groups hold no weights")
     lda = _rows(A, "A", groups.pairs, W.K, gpu)
     if out is None:
-        out = torch.empty((groups.M, W.N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((groups.M, W.N), _BF16, A.device, stream)
     ldc = _rows(out, "out", groups.M, W.N, gpu)
     if workspace is None:
-        workspace = W.ragged_workspace(groups.M, groups.topk)
+        with _made_on(stream):
+            workspace = W.ragged_workspace(groups.M, groups.topk)
     wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_w4a16_gemm_ragged_combine(
         A.data_ptr(), lda, W.handle, groups.ids.data_ptr(), groups.order.data_ptr(),
         groups.offsets.data_ptr(), groups.weights.data_ptr(), groups.M, groups.topk,
-        out.data_ptr(), ldc, wp, wn, stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_w4a16_gemm_ragged_combine")
+        out.data_ptr(), ldc, wp, wn, _raw(stream, gpu)), "vt_fp4_w4a16_gemm_ragged_combine")
     return out
+
+
+def moe_ffn_workspace(W_gate_up, W_down, M_max: int, topk: int) -> torch.Tensor:
+    """A zeroed workspace for moe_ffn of up to M_max tokens of topk pairs each: one that serves
+    the ragged products on either weight."""
+    n = max(W.ragged_workspace_bytes(M_max, topk) for W in (W_gate_up, W_down))
+    return torch.zeros(n, dtype=torch.uint8, device=W_down.packed.device)
 
 
 def moe_ffn(x: torch.Tensor, W_gate_up, W_down, groups: RowGroups, out: torch.Tensor | None = None,
@@ -218,9 +249,10 @@ def moe_ffn(x: torch.Tensor, W_gate_up, W_down, groups: RowGroups, out: torch.Te
     """A mixture-of-experts feed-forward block for any number of tokens: x [M, H] through the
     chosen experts' gate_up (silu(gate) * up) and down weights, summed by the router's weights
     into out [M, H].  h: optional bf16 [pairs, I] buffer of the inner activations; workspace:
-    W_down.ragged_workspace(M, topk)."""
+    moe_ffn_workspace(W_gate_up, W_down, M_max, topk)."""
     if workspace is None:
-        workspace = W_down.ragged_workspace(groups.M, groups.topk)
+        with _made_on(stream):
+            workspace = moe_ffn_workspace(W_gate_up, W_down, groups.M, groups.topk)
     h = w4a16_gemm_ragged_silu_mul(x, W_gate_up, groups, out=h, workspace=workspace, stream=stream)
     return w4a16_gemm_ragged_combine(h, W_down, groups, out=out, workspace=workspace, stream=stream)
 
@@ -257,11 +289,11 @@ def lora_add(x: torch.Tensor, adapters: LoraAdapters, groups: RowGroups, y: torc
         raise ValueError(f"groups must be on {ad.device}")
     ldx, ldy = _rows(x, "x", M, ad.K, gpu), _rows(y, "y", M, ad.N, gpu)
     if out is None:
-        out = torch.empty((M, ad.N), dtype=torch.bfloat16, device=ad.device)
+        out = _empty((M, ad.N), _BF16, ad.device, stream)
     ldo = _rows(out, "out", M, ad.N, gpu)
     check(lib().vt_fp4_lora_add(x.data_ptr(), M, ldx, ad.K, ad.A.data_ptr(), ad.B.data_ptr(),
                                 ad.scale.data_ptr(), 0 if ad.ranks is None else ad.ranks.data_ptr(),
                                 ad.L, ad.R, ad.N, groups.order.data_ptr(),
                                 groups.offsets.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo,
-                                stream.cuda_stream if stream is not None else _current_stream(gpu)), "vt_fp4_lora_add")
+                                _raw(stream, gpu)), "vt_fp4_lora_add")
     return out
