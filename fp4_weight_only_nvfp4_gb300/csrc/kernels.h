@@ -136,6 +136,7 @@ struct RouteLaunch {
   int32_t* order;      // [M * topk]
   int32_t* offsets;    // [E + 1]
   void* workspace;
+  int64_t block_tokens;   // tokens per block, set by the launch (many pairs)
 };
 size_t route_workspace_bytes(int64_t pairs, int64_t E);
 cudaError_t launch_route(const RouteLaunch& L, cudaStream_t s);

@@ -25,9 +25,30 @@ __device__ __forceinline__ float load_logit(const void* p, int bf16, int64_t i) 
               : reinterpret_cast<const float*>(p)[i];
 }
 
+// Sorts a lane's PER keys, largest first, equal ones in their order; at[i]: 32 times the i-th's
+// place before.
+template <int PER>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[PER], uint32_t (&at)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) at[i] = i * 32;
+  // odd-even transposition: neighbours only, so equal keys never pass one another
+#pragma unroll
+  for (int r = 0; r < PER; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < PER; i += 2) {
+      const bool swap = key[i] < key[i + 1];
+      const uint32_t k = key[i], a = at[i];
+      key[i] = swap ? key[i + 1] : k;
+      key[i + 1] = swap ? k : key[i + 1];
+      at[i] = swap ? at[i + 1] : a;
+      at[i + 1] = swap ? a : at[i + 1];
+    }
+}
+
 // One token per warp: lane j of the first topk returns its j-th choice and weight (id -1 where
 // no expert is left).  Every lane keeps PER keys, of experts lane, lane + 32, ...; topk times the
-// warp takes the largest (lowest index among equals) and removes it.
+// warp takes the largest (lowest index among equals) and removes it, up to 4 keys per lane from
+// sorted lists.
 template <int PER>
 __device__ __forceinline__ void topk_token(const RouteLaunch& L, int64_t m, int lane, int& id,
                                            float& w) {
@@ -62,21 +83,38 @@ __device__ __forceinline__ void topk_token(const RouteLaunch& L, int64_t m, int 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
   id = -1;
+  constexpr bool kSorted = PER <= 4;
+  uint32_t place[PER];
+  if constexpr (kSorted) sort_keys<PER>(key, place);
   for (int j = 0; j < L.topk; ++j) {
     uint32_t best = 0;
     int at = 0x7FFFFFFF;
+    if constexpr (kSorted) {
+      best = key[0];
+      at = (int)place[0] + lane;
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i * 32 + lane;
-      }
+      for (int i = 0; i < PER; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = i * 32 + lane;
+        }
+    }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     if (top == 0) break;
     const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
+    if constexpr (kSorted) {
+      const bool mine = at == e;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i * 32 + lane == e) key[i] = 0;
+      for (int i = 0; i < PER; ++i) {
+        key[i] = !mine ? key[i] : i + 1 < PER ? key[i + 1] : 0u;
+        if (i + 1 < PER) place[i] = mine ? place[i + 1] : place[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i * 32 + lane == e) key[i] = 0;
+    }
     if (lane == j) id = e;
   }
   w = 0.0f;
@@ -209,11 +247,6 @@ __global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) 
 constexpr int kPlaceThreads = 512;
 constexpr int kManyBlocks = 152;
 
-__host__ __device__ inline int64_t block_pairs(int64_t P, int topk, int blocks) {
-  const int64_t M = P / topk;
-  return (M + blocks - 1) / blocks * topk;  // whole tokens
-}
-
 template <int PER, int T>
 __global__ void __launch_bounds__(T) k_route_count(const RouteLaunch L, int* hist) {
   __shared__ int s_count[kMaxGroups + 1];
@@ -222,10 +255,9 @@ __global__ void __launch_bounds__(T) k_route_count(const RouteLaunch L, int* his
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
-  const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
+  const int64_t m0 = blockIdx.x * L.block_tokens, m1 = min(m0 + L.block_tokens, L.M);
   if (L.logits) {
-    for (int64_t m = p0 / L.topk + warp; m * L.topk < p1; m += T / 32) {
+    for (int64_t m = m0 + warp; m < m1; m += T / 32) {
       int id;
       float w;
       topk_token<PER>(L, m, lane, id, w);
@@ -236,7 +268,7 @@ __global__ void __launch_bounds__(T) k_route_count(const RouteLaunch L, int* his
       }
     }
   } else {
-    for (int64_t i = p0 + threadIdx.x; i < p1; i += T)
+    for (int64_t i = m0 * L.topk + threadIdx.x; i < m1 * L.topk; i += T)
       atomicAdd(s_count + group_of_id(L.ids[i], L.E), 1);
   }
   __syncthreads();
@@ -261,13 +293,17 @@ __global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteLaunch
   pdl_launch_dependents();
   __syncthreads();
   const int all = (int)gridDim.x * GE, mine = (int)blockIdx.x * GE;
+  int e = (int)threadIdx.x % GE;
+  const int step = kPlaceThreads % GE;
 #pragma unroll 8
   for (int i = threadIdx.x; i < all; i += kPlaceThreads) {
-    const int v = __ldcg(hist + i), e = i % GE;
+    const int v = __ldcg(hist + i);
     if (v) {
       atomicAdd(total + e, v);
       if (i < mine) atomicAdd(before + e, v);
     }
+    e += step;
+    if (e >= GE) e -= GE;
   }
   __syncthreads();
   block_scan<kPlaceThreads>(total, GE, s_warp);
@@ -275,9 +311,8 @@ __global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteLaunch
     for (int e = threadIdx.x; e < GE; e += kPlaceThreads) L.offsets[e] = total[e];
   for (int e = threadIdx.x; e < GE; e += kPlaceThreads) before[e] += total[e];
   __syncthreads();
-  const int64_t P = L.M * L.topk, per = block_pairs(P, L.topk, gridDim.x);
-  const int64_t p0 = blockIdx.x * per, p1 = p0 + per < P ? p0 + per : P;
-  if (p0 < p1) place_pairs<kPlaceThreads>(L.ids, p0, p1, L.E, before, wc, L.order);
+  const int64_t m0 = blockIdx.x * L.block_tokens, m1 = min(m0 + L.block_tokens, L.M);
+  if (m0 < m1) place_pairs<kPlaceThreads>(L.ids, m0 * L.topk, m1 * L.topk, L.E, before, wc, L.order);
 }
 
 template <typename F>
@@ -305,7 +340,7 @@ cudaError_t route_one(const RouteLaunch& L, cudaStream_t s) {
 }
 
 template <int PER>
-cudaError_t route_per(const RouteLaunch& L, cudaStream_t s) {
+cudaError_t route_per(RouteLaunch L, cudaStream_t s) {
   const int64_t P = L.M * L.topk;
   if (P <= kOnePairs)
     return (L.logits ? L.M <= 8 : P <= 256) ? route_one<PER, 256>(L, s) : route_one<PER, 1024>(L, s);
@@ -315,6 +350,7 @@ cudaError_t route_per(const RouteLaunch& L, cudaStream_t s) {
   int* hist = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(L.workspace) + 256);
   const int64_t want = (P + 255) / 256;
   const int blocks = (int)(want < kManyBlocks ? want : kManyBlocks);
+  L.block_tokens = (L.M + blocks - 1) / blocks;
   constexpr int T = PER > 8 ? 512 : 1024;  // registers for the keys (8192 tokens: 9.0 us, 11.7 with 512)
   e = launch_pdl(
       [&](const cudaLaunchConfig_t& c) { return cudaLaunchKernelEx(&c, k_route_count<PER, T>, L, hist); },
