@@ -32,12 +32,18 @@ namespace {
 // (N in steps of 16), and they go to the tensor core through TMEM: a weight tile in shared memory
 // would be written and read once per token tile, which alone took twice the time that its packed
 // form takes to arrive from HBM (77 tokens x top-8 over 128 experts of 1536 x 2048: 61 us; 47).
-// Token tiles: an M = 128 MMA takes the time of N = 128 even where N is smaller (some 70 cycles
-// measured at 16 and 64), so
+// Token tiles: an M = 128, K = 16 MMA takes N / 2 cycles and some 27 more (58 measured at N = 64, 89
+// at 128), and no less than 60 to 70 where N is small, so
 //   TOK = 64  for few rows per group, where that time hides behind the weights' arrival: two
 //             accumulators per row tile, the epilogue of an item beside the MMAs of the next;
 //   TOK = 128 for many: the accumulators of one item and the weight stages fill TMEM, so the
-//             epilogue first moves an item to shared memory as bf16 and then stores it.
+//             epilogue first moves an item to shared memory as bf16 and then stores it.  (160 rows
+//             leave room for three stages only, which cost 8 %: 168 us for 4096 tokens of top-8, 155
+//             with 128 and four.)
+// Bound: with few rows per group by that least time of an MMA, 270 cycles per packed tile of 4.6 KB
+// or 5.3 TB/s over 152 SMs (77 tokens: 43 us, 5.3 TB/s of packed weights); with many by the MMAs and
+// by the drains, in which an item's SiLU (two special-function operations per output) holds up the
+// next item's MMAs for 2000 of its 20000 cycles (4096 tokens: 155 us, 1.33 PFLOP/s).
 // With SiLU and two row tiles the dequantisers put the gate rows of both tiles in accumulator 0
 // and the up rows in accumulator 1, so that a thread finds its pairs in the same lane.
 // Items are (token tile, R x 128 weight rows) pairs, weight rows innermost; a group of n rows is
@@ -931,7 +937,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_ragged_prep(const RaggedLaunch
 // Weighted sum of each token's pairs, in slot order, in fp32; 8 columns per thread, a block per
 // token and 2048 columns.  The loads of 8 slots are in flight together, those of pairs in no group
 // too (what their rows hold is not used): one after another, behind the test of each slot's id,
-// 4096 tokens x top-8 x 2048 columns took 39 us.  Bound by memory and its instructions about alike.
+// 4096 tokens x top-8 x 2048 columns took 39 us, 25 now (5.5 TB/s).  Bound by memory.  D is bf16: each
+// pair's output is rounded once as a product of its own would be (in fp32 its 134 MB written and
+// read there would be twice that), and the sum is rounded once more.
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_combine(
     const __nv_bfloat16* __restrict__ D, int topk, int N, int64_t ldd,
