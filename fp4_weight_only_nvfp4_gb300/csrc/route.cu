@@ -200,13 +200,18 @@ __device__ __forceinline__ void place_pairs(const int32_t* ids, int64_t p0, int6
   }
 }
 
-// Everything in one block: few pairs, where a launch costs more than the work.
-constexpr int64_t kOnePairs = 1024;
+// Everything in one block: few pairs, where a launch costs more than the work.  With logits while
+// every token has a warp of its own (32 tokens: 6.6 us; 64 tokens, two rounds: 10.1, 8.0 in two launches;
+// 128: 17.2 and 8.2), given ids up to 1024 pairs (1024: 5.0 us and 5.2; 2048: 7.1 and 5.5).
+constexpr int64_t kOnePairs = 1024, kOneTokens = 32;
+inline bool one_block(bool logits, int64_t M, int64_t pairs) {
+  return pairs <= kOnePairs && (!logits || M <= kOneTokens);
+}
 template <int T>
 inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + T / 32 * 2) + 16; }
 
-// T = 256 up to 8 tokens (a warp each) or 256 given ids, where the barriers and the sum over the
-// warps' counts of 1024 threads are most of the time (8 tokens: 4.7 us, 5.3 with 1024); 1024 above.
+// T = 256 up to 8 tokens (a warp each; 4.7 us, 5.3 with 1024 threads, whose barriers and sum over the
+// warps' counts cost more) and given ids; 1024 for more tokens (16: 5.5 us, 6.7 with 256).
 template <int PER, int kOneThreads>
 __global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) {
   extern __shared__ int s_dyn[];
@@ -342,13 +347,13 @@ cudaError_t route_one(const RouteLaunch& L, cudaStream_t s) {
 template <int PER>
 cudaError_t route_per(RouteLaunch L, cudaStream_t s) {
   const int64_t P = L.M * L.topk;
-  if (P <= kOnePairs)
-    return (L.logits ? L.M <= 8 : P <= 256) ? route_one<PER, 256>(L, s) : route_one<PER, 1024>(L, s);
+  if (one_block(L.logits != nullptr, L.M, P))
+    return !L.logits || L.M <= 8 ? route_one<PER, 256>(L, s) : route_one<PER, 1024>(L, s);
   static int done[64] = {0};
   cudaError_t e = set_up_kernel(k_route_place, kManySmem, done);
   if (e != cudaSuccess) return e;
   int* hist = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(L.workspace) + 256);
-  const int64_t want = (P + 255) / 256;
+  const int64_t want = L.logits ? (L.M + 31) / 32 : (P + 255) / 256;
   const int blocks = (int)(want < kManyBlocks ? want : kManyBlocks);
   L.block_tokens = (L.M + blocks - 1) / blocks;
   constexpr int T = PER > 8 ? 512 : 1024;  // registers for the keys (8192 tokens: 9.0 us, 11.7 with 512)
@@ -364,7 +369,7 @@ cudaError_t route_per(RouteLaunch L, cudaStream_t s) {
 }  // namespace
 
 size_t route_workspace_bytes(int64_t pairs, int64_t E) {
-  if (pairs <= kOnePairs) return 256;
+  if (pairs <= kOneTokens) return 256;  // one block with logits too, whatever topk
   return 256 + ((size_t)kManyBlocks * (E + 1) * 4 + 255) / 256 * 256;
 }
 
