@@ -316,10 +316,11 @@ vt_status vt_fp4_stats(vt_fp4_handle W, vt_fp4_launch_info* info);
  *           increasing pair order; the pairs in no group come last, in increasing order.
  *   offsets (device) int32 [E + 1]: group e is order[offsets[e] .. offsets[e + 1]).
  * Limits: 1 <= E <= 1024, 1 <= topk <= 32, fewer than 2^31 pairs.  Every result is
- * deterministic: the order of its sums follows from the call's sizes alone.  No counterpart on the pages beyond
- * "re-verify 27B NVFP4 on the nvidia ModelOpt checkpoint" (PR #178), "Speed -- warp-shuffle
- * MoE router top-k" (a top-k over the experts by a total order) and "dense projections take
- * vLLM's own dense marlin" (the multi-expert route of the same W4A16 GEMM). */
+ * deterministic: the order of its sums follows from the call's sizes and alignment alone.  No
+ * counterpart on the pages beyond "re-verify 27B NVFP4 on the nvidia ModelOpt checkpoint" (PR
+ * #178), "Speed -- warp-shuffle MoE router top-k" (a top-k over the experts by a total order) and
+ * "dense projections take vLLM's own dense marlin" (the multi-expert route of the same W4A16
+ * GEMM). */
 
 /* Workspace of vt_fp4_group_rows and vt_fp4_moe_route for up to `pairs` pairs; 256-byte
  * aligned, zeroed once by the caller, reusable afterwards in stream order. */
