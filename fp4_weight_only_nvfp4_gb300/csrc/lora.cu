@@ -19,7 +19,9 @@ namespace {
 // Memory bounds it, so everything streams through a ring of shared-memory chunks filled by
 // asynchronous 16-byte copies, the columns' chunks already under way while v is exchanged (with
 // loads to registers too few bytes were in flight: 53 us for 5003 rows, 4096 -> 5120, rank 32,
-// 46 with them).  Rows that are not 16-byte aligned are copied to the same chunks value by value.
+// 46 with them).  Rows of y that are not whole 16-byte pieces (odd N) are copied from the boundary
+// before them on (3000 rows, 4096 -> 4095: 49 us, 92 value by value; 30 for 4096 columns); such rows of
+// x, A and B value by value.
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
@@ -90,6 +92,15 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t rank, uint
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
+// Four 16-bit values from any place in shared memory.
+__device__ __forceinline__ uint2 ld_shared_4h(uint32_t addr) {
+  uint16_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[i]) : "r"(addr + 2 * i) : "memory");
+  return make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+}
+
 // 8 consecutive values to shared memory, the first n (0 to 8) of them valid (the others zeros).  VEC: one
 // asynchronous copy (src 16-byte aligned); else value by value.
 template <bool VEC>
@@ -107,7 +118,8 @@ __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, in
   }
 }
 
-template <int TM, int RM, int kCluster, bool VEC>
+// VEC: the rows of x, A and B are whole 16-byte pieces; VECY: those of y and out too.
+template <int TM, int RM, int kCluster, bool VEC, bool VECY>
 __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_lora(const LoraLaunch L) {
   using S = LoraSmem<TM, RM, kCluster>;
   constexpr int kChunk = S::kChunk, kStride = S::kStride;
@@ -208,6 +220,11 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
   const __nv_bfloat16* pa = A + (int64_t)r0 * K + k0 + pc * 8;
   const __nv_bfloat16* pb = B + (int64_t)(c0 + bc0) * L.R + bp * 8;
   const uint32_t to_row = ring + r0 * kStride + pc * 16, to_b = ring + TM * kStride + bc0 * S::BStride + bp * 16;
+  // y's rows without VECY, where VEC: the 16-byte pieces from the boundary before the row's first
+  // column on, one more than the columns need (a row of a chunk has room for it; what lies beside the
+  // columns is not used); y8: that column's place in the first piece
+  constexpr bool kWindow = VEC && !VECY;
+  int y8[kWindow ? XP : 1];
   int fetched = 0;
   uint32_t slot = 0;  // byte offset of the next chunk's stage
   auto fetch = [&] {
@@ -230,13 +247,29 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
     } else if (c < chunks) {
       if (c == nk) {
 #pragma unroll
-        for (int i = 0; i < XP; ++i) px[i] = y + max(xrow[i], 0) * L.ldy + c0 + pc * 8;
+        for (int i = 0; i < XP; ++i) {
+          px[i] = y + max(xrow[i], 0) * L.ldy + c0;
+          if constexpr (kWindow) {
+            y8[i] = (int)((uintptr_t)px[i] >> 1) & 7;
+            px[i] -= y8[i];
+          }
+          px[i] += pc * 8;
+        }
       }
       const int b0 = c0 + (c - nk) * kChunk, left = min(max(c1 - (b0 + pc * 8), 0), 8);
       const uint32_t to = to_row + slot;
 #pragma unroll
       for (int i = 0; i < XP; ++i) {
-        if (i * RP < n) copy8<VEC>(to + i * RP * kStride, left > 0 ? px[i] : y, xrow[i] >= 0 ? left : 0);
+        if (i * RP < n) {
+          const uint32_t dst = to + i * RP * kStride;
+          if constexpr (kWindow) {
+            const int ends = xrow[i] >= 0 ? min(kChunk, c1 - b0) + y8[i] - pc * 8 : 0;
+            copy8<true>(dst, ends > 0 ? px[i] : A, min(max(ends, 0), 8));
+            if (pc == P - 1) copy8<true>(dst + 16, ends > 8 ? px[i] + 8 : A, min(max(ends - 8, 0), 8));
+          } else {
+            copy8<VECY>(dst, left > 0 ? px[i] : y, xrow[i] >= 0 ? left : 0);
+          }
+        }
         px[i] += kChunk;
       }
       if (bp * 8 < R16) {
@@ -391,6 +424,11 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
   int orow[2];  // output rows of this lane's fragments
 #pragma unroll
   for (int h = 0; h < 2; ++h) orow[h] = s_row[wm * 16 + h * 8 + g];
+  int shift[2] = {0, 0};  // bytes by which their y lies behind the start of the chunk's rows
+  if constexpr (kWindow) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) shift[h] = (int)(uintptr_t)(y + max(orow[h], 0) * L.ldy + c0) & 14;
+  }
   for (int c = nk; c < chunks; ++c) {
     const uint32_t st = next();
     if (kHold && c == nk) {  // v is written by now for every thread
@@ -428,18 +466,28 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (orow[h] < 0 || left <= 0) continue;
-      const uint32_t from = st + (wm * 16 + h * 8 + g) * kStride + (wn * kCW + 4 * t) * 2;
+      const uint32_t from = st + (wm * 16 + h * 8 + g) * kStride + (wn * kCW + 4 * t) * 2 + shift[h];
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(L.out) + orow[h] * L.ldo + col + 4 * t;
 #pragma unroll
       for (int j = 0; j < kTiles; j += 2) {
-        const uint2 w = ld_shared_v2(from + j * 16);
+        const uint2 w = kWindow ? ld_shared_4h(from + j * 16) : ld_shared_v2(from + j * 16);
         const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(w.x << 16) + d[j][2 * h],
                                                         __uint_as_float(w.x & 0xFFFF0000u) + d[j][2 * h + 1]);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[j + 1][2 * h],
                                                         __uint_as_float(w.y & 0xFFFF0000u) + d[j + 1][2 * h + 1]);
         const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
-        if constexpr (VEC) {
+        if constexpr (VECY) {
           if (j * 8 < left) *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(o[0], o[1]);
+        } else if (j * 8 + 4 <= left) {
+          uint16_t* to = reinterpret_cast<uint16_t*>(dst + j * 8);
+          if ((uintptr_t)to & 2) {
+            to[0] = (uint16_t)o[0];
+            *reinterpret_cast<uint32_t*>(to + 1) = __funnelshift_r(o[0], o[1], 16);
+            to[3] = (uint16_t)(o[1] >> 16);
+          } else {
+            *reinterpret_cast<uint32_t*>(to) = o[0];
+            *reinterpret_cast<uint32_t*>(to + 2) = o[1];
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -453,11 +501,11 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
   if (late_wait) cluster_wait();
 }
 
-template <int TM, int RM, int kCluster, bool VEC>
+template <int TM, int RM, int kCluster, bool VEC, bool VECY>
 cudaError_t launch(const LoraLaunch& L, int64_t tiles, cudaStream_t s) {
   constexpr int bytes = LoraSmem<TM, RM, kCluster>::Bytes;
   static int done[64] = {0};
-  const cudaError_t e = set_up_kernel(k_lora<TM, RM, kCluster, VEC>, bytes, done, kCluster > 8);
+  const cudaError_t e = set_up_kernel(k_lora<TM, RM, kCluster, VEC, VECY>, bytes, done, kCluster > 8);
   if (e != cudaSuccess) return e;
   if (tiles * kCluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -474,23 +522,25 @@ cudaError_t launch(const LoraLaunch& L, int64_t tiles, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM, kCluster, VEC>, L);
+  return cudaLaunchKernelEx(&cfg, k_lora<TM, RM, kCluster, VEC, VECY>, L);
 }
 
 template <int TM, int RM>
 cudaError_t launch_vec(const LoraLaunch& L, cudaStream_t s) {
   // 16-byte copies need every row aligned and whole groups of 8
-  const bool vec = ((uintptr_t)L.x | (uintptr_t)L.A | (uintptr_t)L.B | (uintptr_t)L.y | (uintptr_t)L.out) % 16 == 0 &&
-                   (L.ldx | L.K | (int64_t)L.R | L.ldy | L.ldo | L.N) % 8 == 0;
+  const bool vec = ((uintptr_t)L.x | (uintptr_t)L.A | (uintptr_t)L.B) % 16 == 0 &&
+                   (L.ldx | L.K | (int64_t)L.R) % 8 == 0;
+  const bool vecy = ((uintptr_t)L.y | (uintptr_t)L.out) % 16 == 0 && (L.ldy | L.ldo | L.N) % 8 == 0;
   // at most one partial tile per group in use, the rows without adapter a group too
   const int64_t groups = L.M < L.L + 1 ? L.M : L.L + 1, tiles = groups + L.M / TM;
-  if (!vec) return launch<TM, RM, 8, false>(L, tiles, s);
+  if (!vec) return launch<TM, RM, 8, false, false>(L, tiles, s);
   // While clusters of 16 find an SM for each CTA, they halve what a CTA reads one after another
   // (1 row, 4096 -> 4096, rank 16: 5.1 us, 6.4 with 8, both with chunks of 128); beyond, 8 (96 rows
   // of 64 adapters, two CTAs per SM: 22.3 us, 30 with 16; 22.0 with 4, but then 1 row 9.5).
   if constexpr (TM == 16)
-    if (tiles * 16 <= sm_count()) return launch<TM, RM, 16, true>(L, tiles, s);
-  return launch<TM, RM, 8, true>(L, tiles, s);
+    if (tiles * 16 <= sm_count())
+      return vecy ? launch<TM, RM, 16, true, true>(L, tiles, s) : launch<TM, RM, 16, true, false>(L, tiles, s);
+  return vecy ? launch<TM, RM, 8, true, true>(L, tiles, s) : launch<TM, RM, 8, true, false>(L, tiles, s);
 }
 
 template <int RM>

@@ -174,3 +174,28 @@ def test_repeats_are_bit_equal():
     ids = np.array([0] * 200 + [1] * 100)
     a = _run(x, y, ids, A, B, scale, None)
     assert torch.equal(a, _run(x, y, ids, A, B, scale, None))
+
+
+@pytest.mark.parametrize("M,L,R,K,N", [
+    (1, 2, 16, 512, 1027), (2, 1, 64, 264, 513), (50, 9, 32, 256, 130), (90, 6, 64, 136, 1285),
+    (90, 30, 128, 128, 301), (1025, 2, 32, 128, 131), (400, 2, 64, 256, 333), (300, 1, 128, 72, 259)])
+def test_outputs_of_any_width_and_place(M, L, R, K, N):
+    """Columns, row strides and bases of y and out that are not whole 16-byte pieces, apart and in
+    place; what lies around them stays."""
+    rng = np.random.default_rng(N)
+    A, B, scale, _ = _adapters(rng, L, R, K, N)
+    x, y = acts(rng, M, K), acts(rng, M, N)
+    ids = rng.integers(-1, L, M)
+    ref, err = _ref(x, y, ids, A, B, scale, None)
+    assert_close(_run(x, y, ids, A, B, scale, None), ref, err)
+    for pad, first in ((1, 0), (3, 1), (2, 2), (8, 5)):
+        wide_y = torch.full((M, N + pad + first), 9.0, dtype=torch.bfloat16, device="cuda")
+        wide_o = torch.full((M, N + 2 * pad + first), 7.0, dtype=torch.bfloat16, device="cuda")
+        sy, so = wide_y[:, first:first + N], wide_o[:, first:first + N]
+        sy.copy_(y)
+        _run(x, sy, ids, A, B, scale, None, out=so)
+        assert_close(so, ref, err)
+        assert (wide_o[:, :first] == 7).all() and (wide_o[:, first + N:] == 7).all()
+        _run(x, sy, ids, A, B, scale, None, out=sy)  # in place
+        assert torch.equal(sy, so)
+        assert (wide_y[:, :first] == 9).all() and (wide_y[:, first + N:] == 9).all()
