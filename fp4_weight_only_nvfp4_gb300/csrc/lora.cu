@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
           if (j * 8 < left) *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(o[0], o[1]);
         } else if (j * 8 + 4 <= left) {
           uint16_t* to = reinterpret_cast<uint16_t*>(dst + j * 8);
-          if ((uintptr_t)to & 2) {
+          if (!((uintptr_t)to & 7)) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
+          } else if ((uintptr_t)to & 2) {
             to[0] = (uint16_t)o[0];
             *reinterpret_cast<uint32_t*>(to + 1) = __funnelshift_r(o[0], o[1], 16);
             to[3] = (uint16_t)(o[1] >> 16);
