@@ -76,6 +76,8 @@ SIGNATURES = {
     "vt_fp4_ragged_workspace_bytes": (_ST, [_P, _I64, _I64, ctypes.POINTER(_SZ)]),
     "vt_fp4_w4a16_gemm_ragged": (_ST, [_P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_int, _P, _I64,
                                        _P, _SZ, _P]),
+    "vt_fp4_w4a16_gemm_ragged_ex": (_ST, [_P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_int, _P, _I64,
+                                          _P, _SZ, _P, ctypes.POINTER(GemmOpts)]),
     "vt_fp4_w4a16_gemm_ragged_combine": (_ST, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _I64,
                                                _P, _SZ, _P]),
     "vt_fp4_lora_add": (_ST, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P,

@@ -160,6 +160,8 @@ struct RaggedLaunch {
   int64_t ldc;
   int* status;
   void* act;           // ragged_act_bytes of scratch for converted activations
+  uint64_t wait_ns;    // limit of the waits (0: the kernel's own)
+  int withhold;        // n > 0: each weight producer stops before its n-th k step; -n: pauses there
 };
 size_t ragged_act_bytes(int64_t pairs, int64_t KT);
 cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s);

@@ -58,7 +58,9 @@ constexpr int kDeqWarp0 = 4;                 // first of the dequantisers
 constexpr int kEpiWarp0 = 20;                // first of the epilogue warps
 constexpr int kNS = 4;                       // stages of dequantised weights (TMEM) and tokens
 constexpr int kTileTable = 1024;             // token tiles whose group is looked up, not searched
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull;   // limit of a wait (of the roles: unless the call sets one)
+constexpr int kNoHold = 1 << 30;
+constexpr uint64_t kPauseNs = 1000000ull;     // of a producer that is asked to pause
 
 // Shared-memory map (from a 1024-byte aligned base).
 template <int FMT, int R, bool LOAD, int TOK>
@@ -83,7 +85,7 @@ struct Map {
   static constexpr int OffTok = OffX + XBytes;     // 2 (R = 1: per group) x TOK x {output row, scale}
   static constexpr int OffBar = OffTok + 2 * (R == 2 ? 1 : 2) * TOK * 8;
   static constexpr int NumBars = 2 * (kNS + NW) + 4 + 2;
-  static constexpr int OffTab = OffBar + (NumBars + 1) * 8;
+  static constexpr int OffTab = OffBar + (NumBars + 2) * 8;  // behind TMEM's address, abort and issued
   // per group: prefix sum of the token tiles, first row, rows per tile; group of a token tile
   static constexpr int smem(int E) { return OffTab + (E + 1) * 10 + kTileTable * 2 + 16 + 1024; }
   static_assert(2 * 16 * 272 <= XGroup, "plain epilogue");
@@ -106,6 +108,8 @@ struct RaggedParams {
   const __half* Ap;       // converted activations [rows][ldp], in group order; LOAD: per token
   int64_t ldp;
   const float* rowscale;  // 2^p of each of their rows
+  uint64_t wait_ns;       // limit of the roles' waits
+  int hold;               // k steps after which each weight producer stops, or pauses
 };
 
 // SiLU(x) = x / (1 + e^-x) by the hardware's 2^x and 1/x (each good to 2^-22; the product before
@@ -156,9 +160,22 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait that also gives up when another role has.  The thread sleeps on the barrier for up
 // to 0.1 ms at a time: two dozen warps asking again and again slowed the others' barrier
-// operations (77 tokens x top-8 over 128 experts: 48 -> 43 us).
+// operations (77 tokens x top-8 over 128 experts: 48 -> 43 us).  Each thread gets an answer of its
+// own: with the limit running out while the barrier completes, one thread may be told to give up
+// and its neighbour to go on.  Whoever shares a warp-wide instruction or a named barrier first agrees
+// on one answer (warp_wait, team_wait).
 __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -170,27 +187,38 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                           uint64_t limit_ns) {
+                                           const RaggedParams& p) {
   if (mbar_sleep_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (*abort) return false;
     if (mbar_sleep_wait(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > limit_ns) {
+    if (globaltimer_ns() - t0 > p.wait_ns) {
       *abort = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
+// stage_wait with one answer for the warp: false if it is for any lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          const RaggedParams& p) {
+  return __all_sync(0xffffffffu, stage_wait(bar, parity, abort, p));
+}
+// stage_wait with one answer for the `Threads` threads of named barrier `id`, which also
+// synchronises them: a thread that gives up still arrives, so none is waited for in vain.
+template <int Threads>
+__device__ __forceinline__ bool team_wait(int id, uint32_t bar, uint32_t parity, volatile int* abort,
+                                          const RaggedParams& p) {
+  const uint32_t mine = stage_wait(bar, parity, abort, p) ? 1u : 0u;
+  uint32_t all;
+  __syncwarp();
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"(mine), "r"(id), "n"(Threads)
       : "memory");
-  return ok != 0;
+  return all != 0;
 }
 // D[tmem] (+)= A[tmem] . B[smem desc]^T, kind::f16, one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -350,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t acc_full = w_empty + 8 * NW, acc_empty = acc_full + 16, drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OffBar + S::NumBars * 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued = abort + 1;  // packed stages requested, once the producer is done
   int2* s_tok = reinterpret_cast<int2*>(base + S::OffTok);
   Tiles T;
   T.E = L.E;
@@ -374,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     mbar_init(drain + 8, 1);
-    *abort = 0;
+    *abort = *issued = 0;
   }
   if (warp == 2) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   fence_mbar_init();
@@ -432,31 +461,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       const uint64_t pol = l2_evict_normal_policy();
       uint32_t iw = 0, pw = 0;
-      int issued = 0;
+      int n = 0, hold = p.hold;
       bool ok = true;
       for (Walk w(RGs); ok && w.tile < tiles; w.next()) {
         const Item q = item_of(T, w.tile);
         const int rt0 = w.rg * R, nrt = R == 1 ? 1 : min(R, RT - rt0);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(L.packed) + q.e * L.expert_bytes +
                              kHeaderBytes + (int64_t)rt0 * KT * TB;
-        for (int kt = 0; kt < KT; ++kt, src += TB) {
-          if (!(ok = stage_wait(w_empty + 8 * iw, pw ^ 1u, abort, kWaitNs))) break;
-          mbar_expect_tx(w_full + 8 * iw, nrt * TB);
-          for (int r = 0; r < nrt; ++r)
-            bulk_g2s(sW + (iw * R + r) * TB, src + (int64_t)r * KT * TB, TB, w_full + 8 * iw, pol);
-          ++issued;
-          if (++iw == NW) { iw = 0; pw ^= 1u; }
-        }
+        int kt = 0;
+        do {
+          // (the test hook outside the loop: a compare per step cost 2 of 43 us at 77 tokens)
+          for (const int end = min(KT, kt + hold); kt < end; ++kt, src += TB) {
+            if (!(ok = stage_wait(w_empty + 8 * iw, pw ^ 1u, abort, p))) break;
+            mbar_expect_tx(w_full + 8 * iw, nrt * TB);
+            for (int r = 0; r < nrt; ++r)
+              bulk_g2s(sW + (iw * R + r) * TB, src + (int64_t)r * KT * TB, TB, w_full + 8 * iw, pol);
+            if (++iw == NW) { iw = 0; pw ^= 1u; }
+          }
+          if (ok && kt < KT) {
+            ok = L.withhold < 0;
+            hold = kNoHold;
+            const uint64_t t0 = globaltimer_ns();
+            while (ok && globaltimer_ns() - t0 < kPauseNs) {}
+          }
+        } while (ok && kt < KT);
+        n += kt;
+        if (L.withhold) hold -= kt;
       }
-      if (!ok) {  // let the copies in flight land before shared memory is released
-        atomicExch(L.status, 5);
-        for (int k = 0; k < NW && k < issued; ++k) {
-          iw = iw == 0 ? NW - 1 : iw - 1;
-          if (iw == NW - 1) pw ^= 1u;
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(w_full + 8 * iw, pw) && globaltimer_ns() - t0 < kWaitNs) {}
-        }
-      }
+      *issued = n;
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- token producer
@@ -469,20 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item q = item_of(T, w.tile);
         const int boxes = (q.n + kBox - 1) / kBox;
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = stage_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          if (!(ok = stage_wait(empty + 8 * is, ps ^ 1u, abort, p))) break;
           const uint32_t dst = sB + is * kBBytes, bar = full + 8 * is;
           mbar_expect_tx(bar, (uint32_t)(boxes * kBox * 128));
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(dst + b * kBox * 128, &tm, kt * kTileK, (int)q.i0 + b * kBox, bar, pol);
           if (++is == NS) { is = 0; ps ^= 1u; }
         }
-      }
-      if (!ok) {
-        // The stages' barriers also count the dequantisers, who may have given up, so there is no
-        // phase to wait for: give the last copies a millisecond, a thousand times what one takes.
-        atomicExch(L.status, 5);
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) {}
       }
     }
   } else if (warp < kDeqWarp0) {
@@ -499,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = FMT == FMT_MX && header_of(L, q.e)->wide;
         const uint32_t idesc = (wide ? kIdescBF16 : kIdescF16) | ((uint32_t)((q.n + 15) >> 4) << 18);
         const uint32_t d = d0 + ic * R * kTok;  // ic: accumulator buffer
-        if (!(ok = stage_wait(acc_empty + 8 * ic, pc ^ 1u, abort, kWaitNs))) break;
+        if (!(ok = stage_wait(acc_empty + 8 * ic, pc ^ 1u, abort, p))) break;
         tc_fence_after();
         uint32_t acc = 0;
         for (int kt = 0; kt < KT; ++kt) {
-          if (!ready && !(ok = stage_wait(full + 8 * is, ps, abort, kWaitNs))) break;
+          if (!ready && !(ok = stage_wait(full + 8 * is, ps, abort, p))) break;
           if (LOAD) fence_proxy_async_smem();  // the loaders' copies -> visible to the tensor core
           tc_fence_after();
           const uint32_t at = a0 + is * (R * 32), cur = empty + 8 * is;
@@ -523,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(acc_full + 8 * ic);
         if (++ic == kBufs) { ic = 0; pc ^= 1u; }
       }
-      if (!ok) atomicExch(L.status, 5);
       mma_commit(drain + 8 * r);  // every MMA issued has completed once this commit arrives
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(drain + 8 * r, 0) && globaltimer_ns() - t0 < kWaitNs) {}
@@ -543,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (w.tile < tiles) {
       if (FMT == FMT_MX && fresh) wide = header_of(L, item_of(T, w.tile).e)->wide != 0;
       const int nrt = R == 1 ? 1 : min(R, RT - w.rg * R);
-      if (!(ok = stage_wait(w_full + 8 * iw, pw, abort, kWaitNs))) break;
+      if (!(ok = warp_wait(w_full + 8 * iw, pw, abort, p))) break;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         constexpr bool kSplit = SILU && R == 2;
@@ -563,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dequant_block<FMT, false>(cw1, sc >> 16, og[1], o8[1]);
         }
         if (r == 0) {
-          if (!(ok = stage_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          if (!(ok = warp_wait(empty + 8 * is, ps ^ 1u, abort, p))) break;
           tc_fence_after();
         }
         const uint32_t at = ta + (is * R + r) * 32;
@@ -586,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       fresh = kt >= KT;
       while (w.tile < tiles && kt >= KT) { kt -= KT; w.next(); }
     }
-    if (!ok && lane == 0) atomicExch(L.status, 5);
   } else if (warp < kEpiWarp0) {
     if constexpr (LOAD) {
       // ------------------------------------------------- loaders of gathered rows
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           row[i] = in ? (int)((uint32_t)row[i] / (uint32_t)L.topk) : 0;
         }
         for (int kt = 0; kt < KT; ++kt) {
-          if (!(ok = stage_wait(empty + 8 * is, ps ^ 1u, abort, kWaitNs))) break;
+          if (!(ok = stage_wait(empty + 8 * is, ps ^ 1u, abort, p))) break;
           const uint32_t dst = sB + is * kBBytes;
           const int64_t k = (int64_t)kt * kTileK + c * 8;
           if (FMT == FMT_MX && wide) {
@@ -644,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!ok && lane == 0) atomicExch(L.status, 5);
     }
   } else {
     // ----------------------------------------------------------------- epilogue
@@ -657,9 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* C = reinterpret_cast<__nv_bfloat16*>(L.C);
     const bool vec = (uintptr_t)L.C % 16 == 0 && L.ldc % 8 == 0;
     const int64_t ncols = SILU ? L.seg_split : L.N;
-    auto team_sync = [&]() {
-      asm volatile("bar.sync %0, %1;" ::"r"(R == 2 ? 1 : 1 + eg), "n"(kTeam) : "memory");
-    };
+    const int team = R == 2 ? 1 : 1 + eg;  // its named barrier
+    auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(team), "n"(kTeam) : "memory"); };
     // 16-byte piece of token j: 8 columns from column n on of its output row
     auto store_piece = [&](const int2* tok, int j, int64_t n, uint32_t from) {
       const int row = tok[j].x;
@@ -721,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       w.next();
       fetch();
-      team_sync();  // the table is written, and the buffer of the item before read
-      if (!(ok = stage_wait(acc_full + 8 * ic, pc, abort, kWaitNs))) break;
+      // behind it the table is written, and the buffer of the item before read
+      if (!(ok = team_wait<kTeam>(team, acc_full + 8 * ic, pc, abort, p))) break;
       tc_fence_after();
       const uint32_t ta = tmem + ic * R * kTok + ((uint32_t)(qd * 32) << 16);
       if constexpr (R == 2) {
@@ -849,7 +870,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (++ic == kBufs) { ic = 0; pc ^= 1u; }
     }
-    if (!ok && lane == 0) atomicExch(L.status, 5);
   }
 
   __syncwarp();
@@ -858,6 +878,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort) {
+    // Some role gave up, perhaps not the producers: shared memory is kept until the copies under way
+    // have landed.  The packed stages have a barrier of their own each; the token stages' barriers
+    // also count the dequantisers, who may have left, so the last of those copies get a
+    // millisecond, a thousand times what one takes.
+    atomicExch(L.status, 5);
+    const int n = *issued;
+    for (int k = n > NW ? n - NW : 0; k < n; ++k)
+      mbar_wait_bounded(w_full + 8 * (k % NW), (uint32_t)(k / NW) & 1u, kWaitNs);
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {}
   }
 }
 
@@ -1047,6 +1079,8 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
   __half* ap = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(L.act) + (L.pairs * 4 + 255) / 256 * 256);
   p.rowscale = rowscale;
   p.Ap = ap;
+  p.wait_ns = L.wait_ns ? L.wait_ns : kWaitNs;
+  p.hold = L.withhold == 0 ? kNoHold : L.withhold > 0 ? L.withhold - 1 : -1 - L.withhold;
   // The rules below were measured on 128 experts, top-8, gate_up 1536 x 2048 NVFP4 ("A") and 24
   // experts, top-3, gate_up 2880 x 2592 MXFP4 ("B"), us:
   // One row tile per item while every item gets an SM of its own, so that an SM's share of the

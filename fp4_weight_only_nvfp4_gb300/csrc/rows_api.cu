@@ -1,6 +1,7 @@
 // C entry points of the operators on rows grouped by an index (declared in include/vt_fp4.h):
 // the router, the grouping, the ragged products and the low-rank adapters.  Argument checks
 // run before any CUDA call.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -56,8 +57,12 @@ size_t act_end(vt_fp4_handle W, int64_t pairs) {
 
 vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* order,
                  const int32_t* offsets, int64_t pairs, int64_t topk, int flags, void* C,
-                 int64_t ldc, void* ws, size_t ws_bytes, vt_stream_t s) {
+                 int64_t ldc, void* ws, size_t ws_bytes, vt_stream_t s,
+                 const vt_fp4_gemm_opts* opts) {
   if (!W) return fail(VT_ERR_INVALID_ARG, "weight handle is NULL");
+  if (opts && (opts->grid || opts->warps || opts->stages || opts->force_path ||
+               opts->wait_limit_us < 0 || opts->withhold_weights == INT_MIN))
+    return fail(VT_ERR_INVALID_ARG, "only wait_limit_us (>= 0) and withhold_weights may be set");
   if (vt_status st = check_groups(pairs, W->E)) return st;
   if (topk < 1 || topk > kMaxTopk) return fail(VT_ERR_INVALID_ARG, "topk must be in [1, %d]", kMaxTopk);
   if (pairs % topk) return fail(VT_ERR_INVALID_ARG, "pairs must be a multiple of topk");
@@ -104,6 +109,8 @@ vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* ord
   L.ldc = ldc;
   L.status = reinterpret_cast<int*>(ws);
   L.act = reinterpret_cast<uint8_t*>(ws) + kActOff;
+  L.wait_ns = opts ? (uint64_t)opts->wait_limit_us * 1000ull : 0;
+  L.withhold = opts ? opts->withhold_weights : 0;
   return done(launch_ragged(L, (cudaStream_t)s), "ragged product launch");
 }
 
@@ -193,7 +200,16 @@ vt_status vt_fp4_w4a16_gemm_ragged(const void* A, int64_t lda, vt_fp4_handle W,
                                    const int32_t* order, const int32_t* offsets, int64_t pairs,
                                    int64_t topk, int flags, void* C, int64_t ldc, void* workspace,
                                    size_t ws_bytes, vt_stream_t s) {
-  return ragged(A, lda, W, order, offsets, pairs, topk, flags, C, ldc, workspace, ws_bytes, s);
+  return vt_fp4_w4a16_gemm_ragged_ex(A, lda, W, order, offsets, pairs, topk, flags, C, ldc, workspace,
+                                     ws_bytes, s, nullptr);
+}
+
+vt_status vt_fp4_w4a16_gemm_ragged_ex(const void* A, int64_t lda, vt_fp4_handle W,
+                                      const int32_t* order, const int32_t* offsets, int64_t pairs,
+                                      int64_t topk, int flags, void* C, int64_t ldc,
+                                      void* workspace, size_t ws_bytes, vt_stream_t s,
+                                      const vt_fp4_gemm_opts* opts) {
+  return ragged(A, lda, W, order, offsets, pairs, topk, flags, C, ldc, workspace, ws_bytes, s, opts);
 }
 
 vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_handle W,
@@ -216,7 +232,7 @@ vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_ha
   void* D = reinterpret_cast<uint8_t*>(workspace) + act_end(W, M * topk);
   const int64_t ldd = scratch_ld(W->N);
   if (vt_status st = ragged(A, lda, W, order, offsets, M * topk, topk, VT_RAGGED_SCATTER, D, ldd,
-                            workspace, ws_bytes, s))
+                            workspace, ws_bytes, s, nullptr))
     return st;
   return done(launch_combine(D, M, (int)topk, W->N, ldd, ids, (int)W->E, weights, C, ldc,
                              (cudaStream_t)s),

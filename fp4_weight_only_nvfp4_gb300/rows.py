@@ -8,7 +8,7 @@ import ctypes
 
 import torch
 
-from ._lib import check, lib
+from ._lib import GemmOpts, check, lib
 
 SCORING = {"softmax": 0, "sigmoid": 1}
 GATHER, SCATTER, SILU_MUL = 1, 2, 4
@@ -174,7 +174,14 @@ def _check_groups(W, groups):
     return gpu
 
 
-def _ragged(A, W, groups, out, workspace, stream, flags, cols):
+def _options(opts):
+    unknown = set(opts) - {name for name, _ in GemmOpts._fields_}
+    if unknown:
+        raise TypeError(f"unknown options {sorted(unknown)}")
+    return ctypes.byref(GemmOpts(**opts))
+
+
+def _ragged(A, W, groups, out, workspace, stream, flags, cols, opts=None):
     gpu = _check_groups(W, groups)
     lda = _rows(A, "A", groups.M if flags & GATHER else groups.pairs, W.K, gpu)
     if out is None:
@@ -184,33 +191,35 @@ def _ragged(A, W, groups, out, workspace, stream, flags, cols):
         with _made_on(stream):
             workspace = W.ragged_workspace(groups.M, groups.topk)
     wp, wn = _workspace(workspace, gpu)
-    check(lib().vt_fp4_w4a16_gemm_ragged(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
-                                         groups.offsets.data_ptr(), groups.pairs, groups.topk,
-                                         flags, out.data_ptr(), ldc, wp, wn,
-                                         _raw(stream, gpu)),
+    check(lib().vt_fp4_w4a16_gemm_ragged_ex(A.data_ptr(), lda, W.handle, groups.order.data_ptr(),
+                                            groups.offsets.data_ptr(), groups.pairs, groups.topk,
+                                            flags, out.data_ptr(), ldc, wp, wn,
+                                            _raw(stream, gpu),
+                                            _options(opts) if opts else None),
           "vt_fp4_w4a16_gemm_ragged")
     return out
 
 
 def w4a16_gemm_ragged(A: torch.Tensor, W, groups: RowGroups, out: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, stream=None, gather: bool = True,
-                      scatter: bool = False) -> torch.Tensor:
+                      scatter: bool = False, opts: dict | None = None) -> torch.Tensor:
     """Every grouped pair's row times its expert's weight, for any number of pairs: out
     [pairs, N] (bf16).  gather: A holds one row per token, else one row per pair in group order.
     scatter: pair p's output is row p, else the rows are in group order.  Rows of pairs in no
-    group are not written.  See vt_fp4_w4a16_gemm_ragged in include/vt_fp4.h."""
+    group are not written.  opts: wait_limit_us, withhold_weights.  See vt_fp4_w4a16_gemm_ragged
+    and vt_fp4_w4a16_gemm_ragged_ex in include/vt_fp4.h."""
     return _ragged(A, W, groups, out, workspace, stream,
-                   (GATHER if gather else 0) | (SCATTER if scatter else 0), W.N)
+                   (GATHER if gather else 0) | (SCATTER if scatter else 0), W.N, opts)
 
 
 def w4a16_gemm_ragged_silu_mul(A: torch.Tensor, W, groups: RowGroups,
                                out: torch.Tensor | None = None,
                                workspace: torch.Tensor | None = None, stream=None,
-                               gather: bool = True) -> torch.Tensor:
+                               gather: bool = True, opts: dict | None = None) -> torch.Tensor:
     """The experts' gate and up products with silu(gate) * up as the output: out [pairs, I]
     (bf16), rows in group order, for a weight from PackedWeight.grouped_gate_up."""
     return _ragged(A, W, groups, out, workspace, stream, SILU_MUL | (GATHER if gather else 0),
-                   W.N // 2)
+                   W.N // 2, opts)
 
 
 def w4a16_gemm_ragged_combine(A: torch.Tensor, W, groups: RowGroups,

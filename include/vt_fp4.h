@@ -388,6 +388,17 @@ vt_status vt_fp4_w4a16_gemm_ragged(const void* A, int64_t lda, vt_fp4_handle W,
                                    int64_t topk, int flags, void* C, int64_t ldc, void* workspace,
                                    size_t ws_bytes, vt_stream_t s);
 
+/* As vt_fp4_w4a16_gemm_ragged with the wait options of vt_fp4_gemm_opts (NULL: defaults; every other
+ * field must be 0): wait_limit_us bounds each device-side wait; withhold_weights = n > 0 makes each
+ * CTA's weight producer stop before its n-th k step, so that the waits run out, and -n makes it
+ * pause there for a millisecond.  A call that gave up sets VT_ERR_TIMEOUT in the status word and its
+ * output is undefined; the workspace stays usable. */
+vt_status vt_fp4_w4a16_gemm_ragged_ex(const void* A, int64_t lda, vt_fp4_handle W,
+                                      const int32_t* order, const int32_t* offsets, int64_t pairs,
+                                      int64_t topk, int flags, void* C, int64_t ldc,
+                                      void* workspace, size_t ws_bytes, vt_stream_t s,
+                                      const vt_fp4_gemm_opts* opts);
+
 /* The experts' second products and each token's weighted sum of them:
  *   C[m][n] = bf16( sum_j weights[m][j] * d[m][j][n] ),  d[m][j] = A[i] . W_e^T,
  * with i the place of pair m * topk + j in order; the sum in fp32, in slot order.  A pair in no
