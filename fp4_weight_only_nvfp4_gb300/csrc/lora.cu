@@ -381,7 +381,9 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
       for (int c = 0; c < kCluster; ++c) {
         v.x += u[c].x; v.y += u[c].y; v.z += u[c].z; v.w += u[c].w;
       }
-      const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+      // ranks past R are zeros whatever x holds (an infinity times A's zeros there is NaN)
+      const float f[4] = {r4 < R ? v.x * scale : 0.0f, r4 + 1 < R ? v.y * scale : 0.0f,
+                          r4 + 2 < R ? v.z * scale : 0.0f, r4 + 3 < R ? v.w * scale : 0.0f};
       uint32_t h[4], l[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
