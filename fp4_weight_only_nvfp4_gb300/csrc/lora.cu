@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
       uint32_t h[4], l[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(f[c]);
+        const __nv_bfloat16 hi = __float2bfloat16_rz(f[c]);  // (a rounded one could overflow)
         // an infinite or NaN v is all in its first term
         const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(f[c]) ? f[c] - __bfloat162float(hi) : 0.0f);
         h[c] = __bfloat16_as_ushort(hi);

@@ -34,3 +34,19 @@ def test_an_infinite_activation_meets_its_adapters_own_ranks_only(M, K, N, R, ra
     out = f64(_run(x, y, ids, A, B, scale, ranks))
     assert (out[rows] == np.inf).all()
     assert np.isfinite(np.delete(out, rows, 0)).all()
+
+
+@pytest.mark.parametrize("R", [1, 16])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_a_finite_v_beyond_the_largest_bf16(R, sign):
+    """v = 2^128 (1 - 2^-10), an fp32 number that rounds to infinity in bf16; B = 2^-100."""
+    K, N = 8, 24
+    x, A = torch.zeros(2, K), torch.zeros(1, R, K)
+    x[:, 0], x[:, 1] = 255 / 128 * 2.0 ** 63, 2.0 ** 63
+    A[0, R - 1, 0], A[0, R - 1, 1] = sign * 2.0 ** 64, sign * 3 * 2.0 ** 55
+    B = torch.zeros(1, N, R)
+    B[0, :, R - 1] = 2.0 ** -100
+    bf = torch.bfloat16
+    out = f64(_run(x.to(bf), torch.zeros(2, N, dtype=bf), [0, 0], A.to(bf), B.to(bf), torch.ones(1)))
+    want = sign * 2.0 ** 28 * (1 - 2.0 ** -10)
+    assert (np.abs(out - want) <= 2.0 ** -8 * abs(want)).all(), out
