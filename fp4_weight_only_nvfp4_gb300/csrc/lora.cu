@@ -388,10 +388,13 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const __nv_bfloat16 hi = __float2bfloat16_rz(f[c]);  // (a rounded one could overflow)
-        // an infinite or NaN v is all in its first term
-        const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(f[c]) ? f[c] - __bfloat162float(hi) : 0.0f);
+        // Both terms have v's sign and neither is 0 unless v is, so that an infinite entry of B
+        // gives infinities of one sign: an infinite v is in both terms, and the second term of a v
+        // that the first one holds whole is 2^-24 of it (0 times infinity would be NaN).
         h[c] = __bfloat16_as_ushort(hi);
-        l[c] = __bfloat16_as_ushort(lo);
+        l[c] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(f[c]) ? f[c] - __bfloat162float(hi) : f[c]));
+        if (!(l[c] & 0x7FFFu) && f[c] != 0.0f)
+          l[c] = __bfloat16_as_ushort(__float2bfloat16_rn(copysignf(fmaxf(fabsf(f[c]) * 0x1p-24f, 0x1p-133f), f[c])));
       }
       const uint32_t to = tok * S::BStride + r4 * 2;
       const uint2 hv = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);

@@ -50,3 +50,31 @@ def test_a_finite_v_beyond_the_largest_bf16(R, sign):
     out = f64(_run(x.to(bf), torch.zeros(2, N, dtype=bf), [0, 0], A.to(bf), B.to(bf), torch.ones(1)))
     want = sign * 2.0 ** 28 * (1 - 2.0 ** -10)
     assert (np.abs(out - want) <= 2.0 ** -8 * abs(want)).all(), out
+
+
+@pytest.mark.parametrize("M,R", [(1, 1), (5, 16), (70, 24)])
+def test_an_infinite_entry_of_b(M, R):
+    """B[n][r] = Inf makes column n infinite with v_r's sign, whether or not v_r is a bf16 number."""
+    rng = np.random.default_rng(R)
+    K, N = 64, 40
+    A, B, scale = acts(rng, 1, R, K), acts(rng, 1, N, R), torch.ones(1)
+    x, y = acts(rng, M, K), acts(rng, M, N)
+    x[0] = 0
+    x[0, 0], A[0, :, 0] = 1.0, torch.arange(1, R + 1).to(torch.bfloat16)  # small integers: v exact in bf16
+    B[0, 3, R - 1], B[0, 30, 0] = float("inf"), float("-inf")
+    out = f64(_run(x, y, np.zeros(M), A, B, scale))
+    v = f64(x) @ f64(A[0]).T
+    assert (v[:, [0, R - 1]] != 0).all()
+    assert np.array_equal(out[:, 3], np.sign(v[:, R - 1]) * np.inf)
+    assert np.array_equal(out[:, 30], -np.sign(v[:, 0]) * np.inf)
+    assert np.isfinite(np.delete(out, [3, 30], 1)).all()
+
+
+def test_an_infinite_v_meets_an_infinite_entry_of_b():
+    K, N, bf = 16, 24, torch.bfloat16
+    A, B = torch.ones(1, 1, K, dtype=bf), torch.ones(1, N, 1, dtype=bf)
+    x, y = torch.ones(2, K, dtype=bf), torch.zeros(2, N, dtype=bf)
+    x[0, 2], B[0, 5, 0], B[0, 6, 0] = float("inf"), float("inf"), float("-inf")
+    out = f64(_run(x, y, [0, 0], A, B, torch.ones(1)))
+    assert (out[:, 5] == np.inf).all() and (out[:, 6] == -np.inf).all()
+    assert (np.delete(out[0], [5, 6]) == np.inf).all() and (np.delete(out[1], [5, 6]) == K).all()
