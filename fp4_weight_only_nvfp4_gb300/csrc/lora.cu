@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, LoraSmem<TM, RM, kCluster>::Ctas) k_
                                                         __uint_as_float(w.x & 0xFFFF0000u) + d[j][2 * h + 1]);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[j + 1][2 * h],
                                                         __uint_as_float(w.y & 0xFFFF0000u) + d[j + 1][2 * h + 1]);
-        const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)};
+        // without an adapter y's own bits (y + 0 would change -0 and NaNs)
+        const uint32_t o[2] = {R ? *reinterpret_cast<const uint32_t*>(&lo) : w.x,
+                               R ? *reinterpret_cast<const uint32_t*>(&hi) : w.y};
         if constexpr (VECY) {
           if (j * 8 < left) *reinterpret_cast<uint2*>(dst + j * 8) = make_uint2(o[0], o[1]);
         } else if (j * 8 + 4 <= left) {

@@ -78,3 +78,18 @@ def test_an_infinite_v_meets_an_infinite_entry_of_b():
     out = f64(_run(x, y, [0, 0], A, B, torch.ones(1)))
     assert (out[:, 5] == np.inf).all() and (out[:, 6] == -np.inf).all()
     assert (np.delete(out[0], [5, 6]) == np.inf).all() and (np.delete(out[1], [5, 6]) == K).all()
+
+
+@pytest.mark.parametrize("N", [64, 77])
+def test_rows_without_an_adapter_keep_every_bit(N):
+    """-0, subnormals and NaNs of any payload, for rows in no group and for an adapter of rank 0."""
+    rng = np.random.default_rng(N)
+    M, K, L, R = 40, 32, 3, 8
+    A, B, scale = acts(rng, L, R, K), acts(rng, L, N, R), torch.ones(L)
+    bits = torch.from_numpy(rng.integers(-2 ** 15, 2 ** 15, size=(M, N)).astype(np.int16))
+    bits[:, :6] = torch.tensor([-32768, 0, 0x7FC1, 0x7F81, 1, -32767], dtype=torch.int16)
+    x, y = acts(rng, M, K), bits.view(torch.bfloat16)
+    ids = np.arange(M) % 4 - 1                          # -1, 0, 1, 2
+    out = _run(x, y, ids, A, B, scale, [8, 0, -2]).cpu().view(torch.int16)
+    kept = torch.from_numpy(ids != 0)
+    assert torch.equal(out[kept], bits[kept])
