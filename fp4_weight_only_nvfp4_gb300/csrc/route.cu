@@ -59,10 +59,12 @@ __device__ __forceinline__ void topk_token(const RouteLaunch& L, int64_t m, int 
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
     const float l = e < L.E ? logit(e) : -INFINITY;
+    // the sigmoid grows with the logit, so without a bias the logits give the order (in fp32 the
+    // sigmoids of different logits may be equal)
     float sc = l;
-    if (L.scoring == 1) {
+    if (L.scoring == 1 && L.bias) {
       sc = 1.0f / (1.0f + expf(-sc));
-      if (L.bias && e < L.E) sc += L.bias[e];
+      if (e < L.E) sc += L.bias[e];
     }
     key[i] = l == -INFINITY ? 0u : score_key(sc);
     mx = fmaxf(mx, l);
@@ -213,7 +215,7 @@ inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + T / 32 * 2) + 16; 
 // T = 256 up to 8 tokens (a warp each; 4.7 us, 5.3 with 1024 threads, whose barriers and sum over the
 // warps' counts cost more) and given ids; 1024 for more tokens (16: 5.5 us, 6.7 with 256).
 template <int PER, int kOneThreads>
-__global__ void __launch_bounds__(kOneThreads) k_route_one(const RouteLaunch L) {
+__global__ void __launch_bounds__(kOneThreads, 1) k_route_one(const RouteLaunch L) {
   extern __shared__ int s_dyn[];
   __shared__ int s_warp[kOneThreads / 32], s_ids[kOnePairs];
   int* total = s_dyn;  // [E + 1]

@@ -333,8 +333,10 @@ vt_status vt_fp4_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_
 /* The router: per token the topk experts of largest score, their weights, and the grouping.
  *   logits (device) [M][ld], ld >= E, fp32 (logits_bf16 == 0) or bf16 (1), aligned to its type.
  *   scoring 0: the score is the logit and the weight softmax(logits)[e] over all experts;
- *           1: the score and the weight are sigmoid(logit).
- *   bias   (device, optional) fp32 [E]: added to the score for the choice alone (scoring 1).
+ *           1: the score and the weight are sigmoid(logit); without a bias the choice is made by the
+ *              logits themselves, which are in the same order and never rounded to equal scores.
+ *   bias   (device, optional) fp32 [E]: added to the score for the choice alone (scoring 1), the
+ *          sum rounded to fp32.
  *   renormalize: divide a token's weights by their sum; then every weight times `scale`.
  *   ids (device) int32 [M][topk], weights (device) fp32 [M][topk], largest score first, equal
  *   scores by the lowest index; a NaN score counts as larger than every number.  An expert
