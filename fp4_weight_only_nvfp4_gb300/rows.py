@@ -15,11 +15,20 @@ GATHER, SCATTER, SILU_MUL = 1, 2, 4
 
 
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _BF16 = torch.bfloat16
 
 
 def _raw(stream, gpu):
-    return stream.cuda_stream if stream is not None else _current_stream(gpu)
+    """The handle of the call's stream.  The kernels launch on the current GPU: the operands (on GPU
+    number gpu) and the stream must be its own."""
+    if _current_device() != gpu:
+        raise ValueError(f"the operands are on cuda:{gpu}, the current GPU is cuda:{_current_device()}")
+    if stream is None:
+        return _current_stream(gpu)
+    if getattr(stream, "device_index", gpu) != gpu:
+        raise ValueError(f"the stream must be on cuda:{gpu}")
+    return stream.cuda_stream
 
 
 def _made_on(stream):

@@ -1,0 +1,97 @@
+"""CPU: the binding of the operators on grouped rows, on stand-ins for GPU tensors and a stand-in
+for the library.  No CUDA call is made."""
+import types
+
+import pytest
+import torch
+
+from fp4_weight_only_nvfp4_gb300 import rows
+
+
+class Fake:
+    """What the binding asks of a contiguous tensor on GPU number gpu."""
+    is_cuda = True
+
+    def __init__(self, dtype, *shape, gpu=1):
+        self.dtype, self.shape, self.gpu = dtype, torch.Size(shape), gpu
+        self.device = torch.device("cuda", gpu)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i=None):
+        st = [1] * len(self.shape)
+        for k in range(len(st) - 2, -1, -1):
+            st[k] = st[k + 1] * self.shape[k + 1]
+        return tuple(st) if i is None else st[i]
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.gpu
+
+    def data_ptr(self):
+        return 0x10000
+
+
+class Library:
+    """Records the entry points called; each succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append(name) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    L = Library()
+    monkeypatch.setattr(rows, "lib", lambda: L)
+    monkeypatch.setattr(rows, "_current_stream", lambda gpu: 0x77)
+    return L
+
+
+def _calls(gpu):
+    """Every entry point that launches, on operands of one GPU: name -> call(stream)."""
+    f = lambda dt, *s: Fake(dt, *s, gpu=gpu)
+    i32, bf, f32, u8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+    M, topk, E, N, K = 6, 2, 4, 64, 32
+    groups = rows.RowGroups(f(i32, M, topk), f(i32, M * topk), f(i32, E + 1), f(f32, M, topk))
+    one = rows.RowGroups(f(i32, M), f(i32, M), f(i32, E + 1))
+    W = types.SimpleNamespace(E=E, N=N, K=K, packed=f(u8, 100), handle=0x5)
+    ad = rows.LoraAdapters(f(bf, E, 8, K), f(bf, E, N, 8), f(f32, E))
+    ws, x, h = f(u8, 1 << 20), f(bf, M, K), f(bf, M * topk, K)
+    kw = lambda out: dict(out=out, workspace=ws)
+    return {
+        "vt_fp4_group_rows": lambda s: rows.group_rows(f(i32, M), E, stream=s, **kw(one)),
+        "vt_fp4_moe_route": lambda s: rows.moe_route(f(f32, M, E), topk, stream=s, **kw(groups)),
+        "vt_fp4_w4a16_gemm_ragged_ex": lambda s: rows.w4a16_gemm_ragged(
+            x, W, groups, stream=s, **kw(f(bf, M * topk, N))),
+        "silu_mul": lambda s: rows.w4a16_gemm_ragged_silu_mul(x, W, groups, stream=s, **kw(f(bf, M * topk, N // 2))),
+        "vt_fp4_w4a16_gemm_ragged_combine": lambda s: rows.w4a16_gemm_ragged_combine(
+            h, W, groups, stream=s, **kw(f(bf, M, N))),
+        "vt_fp4_lora_add": lambda s: rows.lora_add(x, ad, one, f(bf, M, N), out=f(bf, M, N), stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls(0)))
+def test_operands_of_another_gpu_than_the_current_one_are_refused(lib, monkeypatch, name):
+    """The kernels launch on the current GPU: another one's memory would reach them as a wild address."""
+    monkeypatch.setattr(rows, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current"):
+        _calls(1)[name](None)
+    with pytest.raises(ValueError, match="current"):
+        _calls(1)[name](types.SimpleNamespace(cuda_stream=5, device_index=1))
+    with pytest.raises(ValueError, match="stream"):
+        _calls(0)[name](types.SimpleNamespace(cuda_stream=5, device_index=1))
+    assert lib.calls == []
+    _calls(0)[name](None)
+    _calls(0)[name](types.SimpleNamespace(cuda_stream=5, device_index=0))
+    monkeypatch.setattr(rows, "_current_device", lambda: 1)
+    _calls(1)[name](None)
+    assert len(lib.calls) == 3
