@@ -14,8 +14,9 @@ SCORING = {"softmax": 0, "sigmoid": 1}
 GATHER, SCATTER, SILU_MUL = 1, 2, 4
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a torch without CUDA has neither, and no tensor that gets as far as their use)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _BF16 = torch.bfloat16
 
 

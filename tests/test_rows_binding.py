@@ -1,5 +1,8 @@
 """CPU: the binding of the operators on grouped rows, on stand-ins for GPU tensors and a stand-in
 for the library.  No CUDA call is made."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -95,3 +98,14 @@ def test_operands_of_another_gpu_than_the_current_one_are_refused(lib, monkeypat
     monkeypatch.setattr(rows, "_current_device", lambda: 1)
     _calls(1)[name](None)
     assert len(lib.calls) == 3
+
+
+def test_the_package_imports_where_torch_has_no_cuda():
+    """A torch built without CUDA has none of its private stream and device functions."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_get')]: delattr(torch._C, name)\n"
+            "import fp4_weight_only_nvfp4_gb300 as vt\n"
+            "assert vt.algorithmic_bytes(vt.NVFP4, 16, 16, 1) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-800:]
