@@ -116,15 +116,17 @@ def group_workspace(M_max: int, topk: int, E: int, device) -> torch.Tensor:
 
 def group_rows(ids: torch.Tensor, E: int, out: RowGroups | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> RowGroups:
-    """Groups the pairs of ids (int32 [M] or [M, topk]; outside [0, E): in no group)."""
+    """Groups the pairs of ids (int32 [M] or [M, topk]; outside [0, E): in no group).  out: of the
+    same [M, topk]; it takes ids as its own, and its weights, if any, stay the caller's business."""
     if ids.dtype != torch.int32 or ids.dim() not in (1, 2) or not ids.is_contiguous() \
             or not ids.is_cuda:
         raise ValueError("ids must be a contiguous int32 CUDA tensor [M] or [M, topk]")
     dev, gpu = ids.device, ids.get_device()
+    shape = (ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1)
     if out is None:
         out = RowGroups(ids, _empty(ids.numel(), torch.int32, dev, stream),
                         _empty(E + 1, torch.int32, dev, stream))
-    elif out.E != E or out.pairs != ids.numel() or out.device != dev:
+    elif out.E != E or (out.M, out.topk) != shape or out.device != dev:
         raise ValueError("out does not have the shape of ids and E")
     else:
         out.ids = ids

@@ -1,0 +1,43 @@
+"""GPU: what the calls on grouped rows accept, refuse and report."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_weight_only_nvfp4_gb300 as vt
+from fp4_weight_only_nvfp4_gb300 import _lib
+from rows_helpers import acts, group64, random_weight
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _grouped(rng, E, N, K):
+    c, s, g = random_weight(rng, vt.NVFP4, E, N, K)
+    return vt.PackedWeight.grouped(_dev(c), _dev(s), g, vt.NVFP4, E, N, K)
+
+
+def _paired(rng, E, I, K):
+    parts = [random_weight(rng, vt.NVFP4, E, I, K) for _ in range(2)]
+    return vt.PackedWeight.grouped_gate_up(*((_dev(c), _dev(s), g) for c, s, g in parts), vt.NVFP4, E, I, K)
+
+
+def _groups(rng, M, topk, E):
+    ids = np.stack([rng.permutation(E)[:topk] for _ in range(M)]).astype(np.int32)
+    order, offsets = group64(ids, E)
+    return vt.RowGroups(_dev(ids), _dev(order), _dev(offsets), torch.rand(M, topk, device="cuda"))
+
+
+def test_groups_out_has_the_shape_of_ids():
+    ids = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    for M, topk in ((4, 2), (8, 1), (1, 8)):
+        with pytest.raises(ValueError, match="shape"):
+            vt.group_rows(ids, 3, out=vt.RowGroups.empty(M, topk, 3, "cuda"))
+        with pytest.raises(ValueError, match="shape"):
+            vt.group_rows(ids, 3, out=vt.RowGroups.empty(M, topk, 3, "cuda", weights=True))
+    out = vt.RowGroups.empty(2, 4, 3, "cuda")
+    assert vt.group_rows(ids, 3, out=out) is out
+    flat = vt.RowGroups.empty(8, 1, 3, "cuda")
+    assert vt.group_rows(ids.view(8), 3, out=flat) is flat  # [M] and [M, 1] are one shape
