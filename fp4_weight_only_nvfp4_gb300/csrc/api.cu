@@ -404,7 +404,11 @@ vt_status gemm_impl(const void* A, int64_t M, int64_t lda, vt_fp4_handle W, void
                     const vt_fp4_gemm_opts* opts, int32_t* g_idx, float* g_val,
                     bool silu = false, bool w4a4 = false, float alpha = 1.0f) {
   if (vt_status st = check_handle(W)) return st;
-  if (W->E > 1) return fail(VT_ERR_INVALID_ARG, "a grouped weight serves vt_fp4_w4a16_gemm_moe");
+  if (W->E > 1)
+    return fail(VT_ERR_INVALID_ARG,
+                W->layout == (int)kLayoutPaired
+                    ? "a grouped gate and up weight serves vt_fp4_w4a16_gemm_ragged"
+                    : "a grouped weight serves vt_fp4_w4a16_gemm_moe and vt_fp4_w4a16_gemm_ragged");
   if (M < 0) return fail(VT_ERR_INVALID_ARG, "M must be >= 0 (got %lld)", (long long)M);
   if (M == 0) return VT_OK;
   if (!A || !workspace || !(C || g_idx))

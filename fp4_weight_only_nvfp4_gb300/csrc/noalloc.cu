@@ -61,7 +61,11 @@ extern "C" vt_status vt_fp4_w4a16_gemm_noalloc(const void* A, int64_t M, int64_t
                                                vt_stream_t s) {
   char msg[256];
   if (!W) return err(VT_ERR_INVALID_ARG, "weight handle is NULL");
-  if (W->E > 1) return err(VT_ERR_INVALID_ARG, "a grouped weight serves vt_fp4_w4a16_gemm_moe");
+  if (W->E > 1)
+    return err(VT_ERR_INVALID_ARG,
+               W->layout == (int)kLayoutPaired
+                   ? "a grouped gate and up weight serves vt_fp4_w4a16_gemm_ragged"
+                   : "a grouped weight serves vt_fp4_w4a16_gemm_moe and vt_fp4_w4a16_gemm_ragged");
   if (M < 0) return err(VT_ERR_INVALID_ARG, "M must be >= 0");
   if (M == 0) return VT_OK;
   if (M > 16) return err(VT_ERR_UNSUPPORTED, "the no-alloc GEMM serves M <= 16 only");

@@ -41,3 +41,17 @@ def test_groups_out_has_the_shape_of_ids():
     assert vt.group_rows(ids, 3, out=out) is out
     flat = vt.RowGroups.empty(8, 1, 3, "cuda")
     assert vt.group_rows(ids.view(8), 3, out=flat) is flat  # [M] and [M, 1] are one shape
+
+
+def test_a_plain_gemm_names_the_entry_that_serves_a_grouped_weight():
+    rng = np.random.default_rng(1)
+    Wp, W = _paired(rng, 3, 64, 64), _grouped(rng, 3, 64, 64)
+    x = acts(rng, 2, 64).cuda()
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    for call, kw in ((vt.w4a16_gemm, dict(workspace=ws)), (vt.w4a16_gemm_silu_mul, dict(workspace=ws)),
+                     (vt.w4a16_gemm_noalloc, {})):
+        with pytest.raises(_lib.VtError, match="vt_fp4_w4a16_gemm_ragged") as err:
+            call(x, Wp, **kw)
+        assert "_moe" not in str(err.value)
+    with pytest.raises(_lib.VtError, match="vt_fp4_w4a16_gemm_moe"):
+        vt.w4a16_gemm(x, W, workspace=ws)
