@@ -163,8 +163,12 @@ struct RaggedLaunch {
   uint64_t wait_ns;    // limit of the waits (0: the kernel's own)
   int withhold;        // n > 0: each weight producer stops before its n-th k step; -n: pauses there
 };
+struct RaggedShape {   // of the product's launch
+  int grid, warps, tokens;  // CTAs, warps of each, rows per token tile
+  int64_t items;            // (token tile, weight rows) pairs, an upper bound
+};
 size_t ragged_act_bytes(int64_t pairs, int64_t KT);
-cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s);
+cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s, RaggedShape* shape);
 // out[m] = sum_j weights[m][j] * D[m * topk + j], pairs whose id is outside [0, E) left out.
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,
                            const int32_t* ids, int E, const float* weights, void* out,

@@ -1039,7 +1039,7 @@ cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* at, dim3 grid, int threads, i
 }
 
 template <int FMT, bool SILU, int R, bool LOAD, int TOK>
-cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream_t s) {
+cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream_t s, RaggedShape* shape) {
   using S = Map<FMT, R, LOAD, TOK>;
   static int done[64] = {0};
   const cudaError_t e =
@@ -1049,6 +1049,7 @@ cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream
   const int64_t groups = p.L.pairs < p.L.E ? p.L.pairs : p.L.E;
   const int64_t most = (groups + p.L.pairs / TOK) * ((p.L.RT + R - 1) / R);
   const int grid = (int)(sm_count() < most ? sm_count() : most);
+  *shape = {grid, kThreads / 32, TOK, most};
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(&at, dim3((unsigned)grid), kThreads, S::smem(p.L.E), s);
   return cudaLaunchKernelEx(&cfg, k_ragged<FMT, SILU, R, LOAD, TOK>, tm, p);
@@ -1056,11 +1057,11 @@ cudaError_t launch_main(const CUtensorMap& tm, const RaggedParams& p, cudaStream
 
 template <int FMT, bool SILU>
 cudaError_t launch_fmt(const CUtensorMap& tm, const RaggedParams& p, bool two, bool many, bool load,
-                       cudaStream_t s) {
-  if (!two) return launch_main<FMT, SILU, 1, false, 64>(tm, p, s);
-  if (!many) return launch_main<FMT, SILU, 2, false, 64>(tm, p, s);
-  return load ? launch_main<FMT, SILU, 2, true, 128>(tm, p, s)
-              : launch_main<FMT, SILU, 2, false, 128>(tm, p, s);
+                       cudaStream_t s, RaggedShape* shape) {
+  if (!two) return launch_main<FMT, SILU, 1, false, 64>(tm, p, s, shape);
+  if (!many) return launch_main<FMT, SILU, 2, false, 64>(tm, p, s, shape);
+  return load ? launch_main<FMT, SILU, 2, true, 128>(tm, p, s, shape)
+              : launch_main<FMT, SILU, 2, false, 128>(tm, p, s, shape);
 }
 
 }  // namespace
@@ -1069,7 +1070,7 @@ size_t ragged_act_bytes(int64_t pairs, int64_t KT) {
   return (size_t)((pairs * 4 + 255) / 256 * 256 + pairs * KT * kTileK * 2);
 }
 
-cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
+cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s, RaggedShape* shape) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   RaggedParams p;
@@ -1114,10 +1115,10 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s) {
                       ? cudaLaunchKernelEx(&cfg, k_ragged_prep<4>, L, rows, p.ldp, load ? 1 : 0, ap, rowscale)
                       : cudaLaunchKernelEx(&cfg, k_ragged_prep<8>, L, rows, p.ldp, load ? 1 : 0, ap, rowscale);
   if (e != cudaSuccess) return e;
-  if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, many, load, s)
-                                     : launch_fmt<FMT_NV, false>(tm, p, two, many, load, s);
-  return L.silu ? launch_fmt<FMT_MX, true>(tm, p, two, many, load, s)
-                : launch_fmt<FMT_MX, false>(tm, p, two, many, load, s);
+  if (L.fmt == FMT_NV) return L.silu ? launch_fmt<FMT_NV, true>(tm, p, two, many, load, s, shape)
+                                     : launch_fmt<FMT_NV, false>(tm, p, two, many, load, s, shape);
+  return L.silu ? launch_fmt<FMT_MX, true>(tm, p, two, many, load, s, shape)
+                : launch_fmt<FMT_MX, false>(tm, p, two, many, load, s, shape);
 }
 
 cudaError_t launch_combine(const void* D, int64_t M, int topk, int64_t N, int64_t ldd,

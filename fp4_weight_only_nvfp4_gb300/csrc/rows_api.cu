@@ -111,7 +111,18 @@ vt_status ragged(const void* A, int64_t lda, vt_fp4_handle W, const int32_t* ord
   L.act = reinterpret_cast<uint8_t*>(ws) + kActOff;
   L.wait_ns = opts ? (uint64_t)opts->wait_limit_us * 1000ull : 0;
   L.withhold = opts ? opts->withhold_weights : 0;
-  return done(launch_ragged(L, (cudaStream_t)s), "ragged product launch");
+  RaggedShape shape = {};
+  if (vt_status st = done(launch_ragged(L, (cudaStream_t)s, &shape), "ragged product launch")) return st;
+  W->info.path = 4;
+  W->info.tile_epilogue = 0;
+  W->info.stage_k_tiles = 1;
+  W->info.grid = shape.grid;
+  W->info.warps_per_cta = shape.warps;
+  W->info.m_tile = shape.tokens;
+  W->info.items = shape.items;
+  W->info.launches = 2;  // the activation pre-pass and the product
+  W->info.calls += 1;
+  return VT_OK;
 }
 
 }  // namespace
@@ -234,9 +245,12 @@ vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_ha
   if (vt_status st = ragged(A, lda, W, order, offsets, M * topk, topk, VT_RAGGED_SCATTER, D, ldd,
                             workspace, ws_bytes, s, nullptr))
     return st;
-  return done(launch_combine(D, M, (int)topk, W->N, ldd, ids, (int)W->E, weights, C, ldc,
-                             (cudaStream_t)s),
-              "combine launch");
+  if (vt_status st = done(launch_combine(D, M, (int)topk, W->N, ldd, ids, (int)W->E, weights, C, ldc,
+                                         (cudaStream_t)s),
+                          "combine launch"))
+    return st;
+  W->info.launches += 1;
+  return VT_OK;
 }
 
 vt_status vt_fp4_lora_add(const void* x, int64_t M, int64_t ldx, int64_t K, const void* A,

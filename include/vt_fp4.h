@@ -64,13 +64,14 @@ typedef struct vt_fp4_weight_s* vt_fp4_handle;
 /* What the last GEMM call on a handle launched (host-side record). */
 typedef struct {
   int path;           /* 0 none yet, 1 decode (M <= 16), 2 prefill tile path,
-                         3 grouped mixture-of-experts decode */
+                         3 grouped mixture-of-experts decode, 4 ragged product */
   int grid;           /* CTAs of the main kernel */
   int warps_per_cta;  /* warps per CTA of the main kernel */
   int m_tile;         /* decode and grouped: tokens per MMA column block (8 or 16);
-                         prefill: 128 */
+                         prefill: 128; ragged: rows per token tile (64 or 128) */
   int64_t items;      /* decode: (row tile, k tile) work items; grouped: an upper bound on
-                         them (the routing is read on the device); prefill: output tiles */
+                         them (the routing is read on the device); prefill: output tiles;
+                         ragged: an upper bound on (token tile, weight rows) items */
   int64_t launches;   /* kernels enqueued by that call */
   int64_t calls;      /* GEMM calls made on this handle so far */
   int tile_epilogue;  /* decode: 1 when complete row tiles were summed per row-block group
@@ -81,7 +82,7 @@ typedef struct {
                          for up to 8 tokens and more than 4096 activation elements on a call
                          of at least three row tiles per CTA; grouped: 16 in the one-launch
                          mode when min(M * topk, E) experts give at least three row tiles
-                         per CTA); prefill: 1 (one 64-wide k step per stage) */
+                         per CTA); prefill and ragged: 1 (one 64-wide k step per stage) */
 } vt_fp4_launch_info;
 
 /* Optional overrides for vt_fp4_w4a16_gemm_ex (0 = library choice). */

@@ -55,3 +55,29 @@ def test_a_plain_gemm_names_the_entry_that_serves_a_grouped_weight():
         assert "_moe" not in str(err.value)
     with pytest.raises(_lib.VtError, match="vt_fp4_w4a16_gemm_moe"):
         vt.w4a16_gemm(x, W, workspace=ws)
+
+
+def test_stats_report_the_ragged_calls():
+    rng = np.random.default_rng(2)
+    E, N, K = 4, 300, 64
+    W, Wp = _grouped(rng, E, N, K), _paired(rng, E, N // 2, K)
+    M, topk = 6, 2
+    g = _groups(rng, M, topk, E)
+    vt.w4a16_gemm_ragged(acts(rng, M, K).cuda(), W, g)
+    s = W.stats()
+    assert (s["path"], s["calls"], s["launches"], s["m_tile"], s["stage_k_tiles"]) == (4, 1, 2, 64, 1)
+    assert s["grid"] >= 1 and s["items"] >= 4 * 3 and s["warps_per_cta"] == 28
+    vt.w4a16_gemm_ragged_combine(acts(rng, M * topk, K).cuda(), W, g)
+    s = W.stats()
+    assert (s["path"], s["calls"], s["launches"]) == (4, 2, 3)
+    vt.w4a16_gemm_ragged_silu_mul(acts(rng, M, K).cuda(), Wp, g)
+    assert (Wp.stats()["path"], Wp.stats()["calls"], Wp.stats()["launches"]) == (4, 1, 2)
+    big = _groups(rng, 4000, 1, E)
+    W2 = _grouped(rng, E, 128 * 40, K)
+    vt.w4a16_gemm_ragged(acts(rng, 4000, K).cuda(), W2, big)
+    assert W2.stats()["m_tile"] == 128
+    none = vt.RowGroups(torch.zeros(0, 2, dtype=torch.int32, device="cuda"),
+                        torch.zeros(0, dtype=torch.int32, device="cuda"),
+                        torch.zeros(E + 1, dtype=torch.int32, device="cuda"))
+    vt.w4a16_gemm_ragged(acts(rng, 1, K).cuda()[:0], W, none)
+    assert W.stats()["calls"] == 2  # no pair, no call recorded
