@@ -14,8 +14,8 @@ import torch
 
 from ._lib import GemmOpts, LaunchInfo, VtError, check, lib
 from .rows import (LoraAdapters, RowGroups, group_rows, group_workspace, lora_add, moe_ffn,
-                   moe_ffn_workspace, moe_route, w4a16_gemm_ragged, w4a16_gemm_ragged_combine,
-                   w4a16_gemm_ragged_silu_mul)
+                   moe_ffn_workspace, moe_route, status_workspace, w4a16_gemm_ragged,
+                   w4a16_gemm_ragged_combine, w4a16_gemm_ragged_silu_mul)
 
 NVFP4, MXFP4 = 0, 1
 GROUP = {NVFP4: 16, MXFP4: 32}
@@ -164,10 +164,9 @@ class PackedWeight:
         return W
 
     def ragged_workspace(self, M_max: int, topk: int) -> torch.Tensor:
-        """A zeroed workspace for the ragged products on this weight of up to M_max tokens of
-        topk pairs each (zero once; any smaller call may share it in stream order)."""
-        return torch.zeros(self.ragged_workspace_bytes(M_max, topk), dtype=torch.uint8,
-                           device=self.packed.device)
+        """A workspace for the ragged products on this weight of up to M_max tokens of topk pairs
+        each, its status word cleared (any smaller call may share it in stream order)."""
+        return status_workspace(self.ragged_workspace_bytes(M_max, topk), self.packed.device)
 
     def ragged_workspace_bytes(self, M_max: int, topk: int) -> int:
         out = ctypes.c_size_t(0)

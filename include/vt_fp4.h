@@ -324,7 +324,7 @@ vt_status vt_fp4_stats(vt_fp4_handle W, vt_fp4_launch_info* info);
  * GEMM). */
 
 /* Workspace of vt_fp4_group_rows and vt_fp4_moe_route for up to `pairs` pairs; 256-byte
- * aligned, zeroed once by the caller, reusable afterwards in stream order. */
+ * aligned, reusable in stream order; it need not be cleared. */
 vt_status vt_fp4_group_workspace_bytes(int64_t pairs, int64_t E, size_t* bytes);
 
 /* order and offsets from ids (see above).  pairs == 0 writes offsets (all 0) only. */
@@ -372,8 +372,8 @@ enum {
 };
 
 /* Workspace of the ragged products on W for up to M_max tokens of topk pairs each; 256-byte
- * aligned, zeroed once by the caller, reusable afterwards in stream order.  Its first word is
- * the status word (vt_fp4_workspace_status): VT_ERR_TIMEOUT after a wait that gave up, 6 after
+ * aligned, its first 256 bytes zeroed once by the caller (the rest need not be), reusable afterwards
+ * in stream order.  Its first word is the status word (vt_fp4_workspace_status): VT_ERR_TIMEOUT after a wait that gave up, 6 after
  * a call whose order or offsets held values out of range (such values are never used as
  * addresses; the rows concerned are undefined). */
 vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t topk,

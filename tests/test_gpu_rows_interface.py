@@ -81,3 +81,26 @@ def test_stats_report_the_ragged_calls():
                         torch.zeros(E + 1, dtype=torch.int32, device="cuda"))
     vt.w4a16_gemm_ragged(acts(rng, 1, K).cuda()[:0], W, none)
     assert W.stats()["calls"] == 2  # no pair, no call recorded
+
+
+def test_calls_without_a_workspace_on_memory_used_before():
+    """What an earlier tensor left in the memory of a workspace changes nothing."""
+    rng = np.random.default_rng(4)
+    E, I, H, M, topk = 6, 96, 160, 50, 3
+    Wgu, Wd = _paired(rng, E, I, H), _grouped(rng, E, H, I)
+    x, logits = acts(rng, M, H).cuda(), torch.randn(M, E, device="cuda")
+    zeroed = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")
+    routes = vt.moe_route(logits, topk, workspace=zeroed(1 << 20))
+    want = vt.moe_ffn(x, Wgu, Wd, routes, workspace=zeroed(1 << 22))
+    for byte in (0x7F, 0xFF, 0x01):
+        used = [torch.full((n,), byte, dtype=torch.uint8, device="cuda") for n in [1 << 12, 1 << 17, 1 << 21, 1 << 24] * 3]
+        torch.cuda.synchronize()
+        del used
+        r = vt.moe_route(logits, topk)
+        assert torch.equal(r.order, routes.order) and torch.equal(r.offsets, routes.offsets)
+        g = vt.group_rows(r.ids, E)
+        assert torch.equal(g.order, routes.order) and torch.equal(g.offsets, routes.offsets)
+        assert torch.equal(vt.moe_ffn(x, Wgu, Wd, r), want)
+        ws = vt.moe_ffn_workspace(Wgu, Wd, M, topk)
+        assert torch.equal(vt.moe_ffn(x, Wgu, Wd, r, workspace=ws), want)
+        assert vt.workspace_status(ws) == 0

@@ -7,7 +7,9 @@ import types
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
+import fp4_weight_only_nvfp4_gb300 as vt
 from fp4_weight_only_nvfp4_gb300 import rows
 
 
@@ -109,3 +111,36 @@ def test_the_package_imports_where_torch_has_no_cuda():
             "assert vt.algorithmic_bytes(vt.NVFP4, 16, 16, 1) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-800:]
+
+
+class Cleared(TorchDispatchMode):
+    """The elements that each clearing operation writes."""
+
+    def __init__(self):
+        super().__init__()
+        self.sizes = []
+
+    def __torch_dispatch__(self, func, types_, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if any(word in func.__name__ for word in ("zero", "fill", "full", "ones")):
+            self.sizes.append(out.numel())
+        return out
+
+
+def test_a_workspace_is_cleared_where_it_has_to_be_only(monkeypatch):
+    """The status word's 256 bytes; the rest of a workspace, which may be hundreds of megabytes, is
+    scratch that every call writes before it reads it."""
+    W = types.SimpleNamespace(ragged_workspace_bytes=lambda M, topk: 1 << 20, packed=torch.empty(1))
+
+    class Sizes:
+        def vt_fp4_group_workspace_bytes(self, pairs, E, out):
+            out._obj.value = 1 << 20
+            return 0
+
+    monkeypatch.setattr(rows, "lib", lambda: Sizes())
+    with Cleared() as c:
+        made = [vt.PackedWeight.ragged_workspace(W, 100, 8), rows.moe_ffn_workspace(W, W, 100, 8)]
+        scratch = rows.group_workspace(100, 8, 16, "cpu")
+    assert all(w.numel() == 1 << 20 and w.dtype == torch.uint8 for w in made + [scratch])
+    assert all(not w[:256].any() for w in made)
+    assert sum(c.sizes) <= 2 * 256
