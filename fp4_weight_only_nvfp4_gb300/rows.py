@@ -54,7 +54,8 @@ def _need(t, name, dtype, shape, device):
 
 
 def _rows(t, name, rows, cols, gpu):
-    """A bf16 matrix with unit inner stride on GPU number gpu; returns its row stride."""
+    """A bf16 matrix with unit inner stride on GPU number gpu; returns its row stride (one row: its
+    columns)."""
     if t.dtype is not _BF16 or t.shape != (rows, cols):
         raise ValueError(f"{name} must be a bf16 [{rows}, {cols}] tensor with unit inner stride")
     ld, inner = t.stride()
@@ -62,10 +63,10 @@ def _rows(t, name, rows, cols, gpu):
         raise ValueError(f"{name} must be a bf16 [{rows}, {cols}] tensor with unit inner stride")
     if t.get_device() != gpu or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+    if rows <= 1:  # no second row for the stride to lead to
+        return cols
     if ld < cols:
-        if rows > 1:
-            raise ValueError(f"{name} must not have overlapping rows")
-        ld = cols
+        raise ValueError(f"{name} must not have overlapping rows")
     return ld
 
 

@@ -83,6 +83,21 @@ def test_stats_report_the_ragged_calls():
     assert W.stats()["calls"] == 2  # no pair, no call recorded
 
 
+def test_a_single_row_may_have_any_row_stride():
+    rng = np.random.default_rng(3)
+    E, N, K = 3, 72, 64
+    W, g = _grouped(rng, E, N, K), _groups(rng, 1, 1, E)
+    x = acts(rng, 1, K).cuda()
+    wide = torch.zeros(1, K + 5, dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = x
+    view = wide[:, :K]
+    assert view.stride(0) % 8
+    want = vt.w4a16_gemm_ragged(x, W, g)
+    assert torch.equal(vt.w4a16_gemm_ragged(view, W, g), want)
+    assert torch.equal(vt.w4a16_gemm_ragged(view, W, g, gather=False), want)
+    assert torch.equal(vt.w4a16_gemm_ragged_combine(view, W, g), vt.w4a16_gemm_ragged_combine(x, W, g))
+
+
 def test_calls_without_a_workspace_on_memory_used_before():
     """What an earlier tensor left in the memory of a workspace changes nothing."""
     rng = np.random.default_rng(4)
