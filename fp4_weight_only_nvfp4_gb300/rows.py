@@ -247,7 +247,8 @@ def w4a16_gemm_ragged_combine(A: torch.Tensor, W, groups: RowGroups,
                               out: torch.Tensor | None = None,
                               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The experts' second products (A [pairs, K], rows in group order) and each token's sum of
-    them by groups.weights: out [M, N] (bf16).  Pairs in no group count as zero."""
+    them by groups.weights: out [M, N] (bf16).  The products are rounded to bf16 first, as
+    w4a16_gemm_ragged writes them; the sum is fp32.  Pairs in no group count as zero."""
     gpu = _check_groups(W, groups)
     if groups.weights is None:
         raise ValueError("the groups hold no weights")

@@ -403,9 +403,11 @@ vt_status vt_fp4_w4a16_gemm_ragged_ex(const void* A, int64_t lda, vt_fp4_handle 
                                       const vt_fp4_gemm_opts* opts);
 
 /* The experts' second products and each token's weighted sum of them:
- *   C[m][n] = bf16( sum_j weights[m][j] * d[m][j][n] ),  d[m][j] = A[i] . W_e^T,
- * with i the place of pair m * topk + j in order; the sum in fp32, in slot order.  A pair in no
- * group (id outside [0, E)) counts as zero whatever its weight.
+ *   C[m][n] = bf16( sum_j weights[m][j] * d[m][j][n] ),  d[m][j] = bf16( A[i] . W_e^T ),
+ * with i the place of pair m * topk + j in order; the sum in fp32, in slot order.  The products are
+ * rounded to bf16 as vt_fp4_w4a16_gemm_ragged writes them, before the sum and its own rounding:
+ * together 1.4 times the rms error of a single rounding (0.0023 and 0.0017 of the outputs' rms).  A
+ * pair in no group (id outside [0, E)) counts as zero whatever its weight.
  *   A  (device) bf16 [M * topk][lda], one row per grouped pair;  C (device) bf16 [M][ldc].
  * Other arguments as above. */
 vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_handle W,
