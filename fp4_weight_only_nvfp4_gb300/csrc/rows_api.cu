@@ -31,12 +31,13 @@ vt_status done(cudaError_t e, const char* where) {
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-constexpr int64_t kMaxPairs = 0x7FFFFFFF;
+// A group of n rows is cut into nt tiles of 16 rows or more, and the kernels' n + nt + 128 stays an int.
+constexpr int64_t kMaxPairs = ((int64_t)1 << 31) - ((int64_t)1 << 27);
 
 vt_status check_groups(int64_t pairs, int64_t E) {
   if (E < 1 || E > kMaxGroups) return fail(VT_ERR_INVALID_ARG, "E must be in [1, %d]", kMaxGroups);
   if (pairs < 0 || pairs >= kMaxPairs)
-    return fail(VT_ERR_INVALID_ARG, "pairs must be in [0, 2^31 - 1) (got %lld)", (long long)pairs);
+    return fail(VT_ERR_INVALID_ARG, "pairs must be in [0, 2^31 - 2^27) (got %lld)", (long long)pairs);
   return VT_OK;
 }
 
@@ -159,7 +160,7 @@ vt_status vt_fp4_moe_route(const void* logits, int logits_bf16, int64_t M, int64
                            int64_t topk, int scoring, const float* bias, int renormalize,
                            float scale, int32_t* ids, float* weights, int32_t* order,
                            int32_t* offsets, void* workspace, size_t ws_bytes, vt_stream_t s) {
-  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 1)");
+  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 2^27)");
   if (topk < 1 || topk > kMaxTopk) return fail(VT_ERR_INVALID_ARG, "topk must be in [1, %d]", kMaxTopk);
   if (vt_status st = check_groups(M * topk, E)) return st;
   if (topk > E) return fail(VT_ERR_INVALID_ARG, "topk (%lld) exceeds E (%lld)", (long long)topk, (long long)E);
@@ -199,7 +200,7 @@ vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t 
   if (!W) return fail(VT_ERR_INVALID_ARG, "weight handle is NULL");
   if (!bytes) return fail(VT_ERR_INVALID_ARG, "bytes is NULL");
   if (topk < 1 || topk > kMaxTopk) return fail(VT_ERR_INVALID_ARG, "topk must be in [1, %d]", kMaxTopk);
-  if (M_max < 0 || M_max >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M_max must be in [0, 2^31 - 1)");
+  if (M_max < 0 || M_max >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M_max must be in [0, 2^31 - 2^27)");
   if (vt_status st = check_groups(M_max * topk, W->E)) return st;
   // a paired weight's output is the caller's; only the combining product keeps scratch
   const size_t scratch = W->layout == (int)kLayoutPaired ? 0 : (size_t)(M_max * topk) * scratch_ld(W->N) * 2;
@@ -228,7 +229,7 @@ vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_ha
                                            const int32_t* offsets, const float* weights,
                                            int64_t M, int64_t topk, void* C, int64_t ldc,
                                            void* workspace, size_t ws_bytes, vt_stream_t s) {
-  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 1)");
+  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 2^27)");
   size_t need = 0;
   if (vt_status st = vt_fp4_ragged_workspace_bytes(W, M, topk, &need)) return st;
   if (W->layout != (int)kLayoutRows)
@@ -259,7 +260,7 @@ vt_status vt_fp4_lora_add(const void* x, int64_t M, int64_t ldx, int64_t K, cons
                           const void* y, int64_t ldy, void* out, int64_t ldo, vt_stream_t s) {
   if (L < 1 || L > kMaxGroups) return fail(VT_ERR_INVALID_ARG, "L must be in [1, %d]", kMaxGroups);
   if (R < 1 || R > kMaxRank) return fail(VT_ERR_INVALID_ARG, "R must be in [1, %d]", kMaxRank);
-  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 1)");
+  if (M < 0 || M >= kMaxPairs) return fail(VT_ERR_INVALID_ARG, "M must be in [0, 2^31 - 2^27)");
   if (K < 1 || N < 1 || K > (int64_t)1 << 24 || N > (int64_t)1 << 24)
     return fail(VT_ERR_INVALID_ARG, "K and N must be in [1, 2^24]");
   if (ldx < K || ldy < N || ldo < N)

@@ -316,7 +316,7 @@ vt_status vt_fp4_stats(vt_fp4_handle W, vt_fp4_launch_info* info);
  *   order   (device) int32 [pairs]: the pairs in increasing index order, pairs of one index in
  *           increasing pair order; the pairs in no group come last, in increasing order.
  *   offsets (device) int32 [E + 1]: group e is order[offsets[e] .. offsets[e + 1]).
- * Limits: 1 <= E <= 1024, 1 <= topk <= 32, fewer than 2^31 pairs.  Every result is
+ * Limits: 1 <= E <= 1024, 1 <= topk <= 32, fewer than 2^31 - 2^27 pairs.  Every result is
  * deterministic: the order of its sums follows from the call's sizes and alignment alone.  No
  * counterpart on the pages beyond "re-verify 27B NVFP4 on the nvidia ModelOpt checkpoint" (PR
  * #178), "Speed -- warp-shuffle MoE router top-k" (a top-k over the experts by a total order) and
