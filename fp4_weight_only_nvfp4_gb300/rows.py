@@ -281,6 +281,14 @@ def moe_ffn(x: torch.Tensor, W_gate_up, W_down, groups: RowGroups, out: torch.Te
     chosen experts' gate_up (silu(gate) * up) and down weights, summed by the router's weights
     into out [M, H].  h: optional bf16 [pairs, I] buffer of the inner activations; workspace:
     moe_ffn_workspace(W_gate_up, W_down, M_max, topk)."""
+    # what the second product would refuse after the first is under way
+    gpu = _check_groups(W_down, groups)
+    if groups.weights is None:
+        raise ValueError("the groups hold no weights")
+    if W_gate_up.N != 2 * W_down.K:
+        raise ValueError(f"W_down must take the {W_gate_up.N // 2} columns of gate and up (it takes {W_down.K})")
+    if out is not None:
+        _rows(out, "out", groups.M, W_down.N, gpu)
     if workspace is None:
         with _made_on(stream):
             workspace = moe_ffn_workspace(W_gate_up, W_down, groups.M, groups.topk)

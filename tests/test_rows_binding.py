@@ -144,3 +144,21 @@ def test_a_workspace_is_cleared_where_it_has_to_be_only(monkeypatch):
     assert all(w.numel() == 1 << 20 and w.dtype == torch.uint8 for w in made + [scratch])
     assert all(not w[:256].any() for w in made)
     assert sum(c.sizes) <= 2 * 256
+
+
+def test_the_block_refuses_before_its_first_launch(lib, monkeypatch):
+    monkeypatch.setattr(rows, "_current_device", lambda: 1)
+    i32, bf, f32, u8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+    M, topk, E, I, H = 6, 2, 4, 64, 32
+    part = (Fake(i32, M, topk), Fake(i32, M * topk), Fake(i32, E + 1))
+    weight = lambda N, K: types.SimpleNamespace(E=E, N=N, K=K, packed=Fake(u8, 100), handle=0x5)
+    x, ws, h = Fake(bf, M, H), Fake(u8, 1 << 20), Fake(bf, M * topk, I)
+    call = lambda groups=rows.RowGroups(*part, Fake(f32, M, topk)), down=weight(H, I), out=Fake(bf, M, H): \
+        rows.moe_ffn(x, weight(2 * I, H), down, groups, out=out, h=h, workspace=ws)
+    for kw, match in ((dict(groups=rows.RowGroups(*part)), "weights"), (dict(down=weight(H, I + 32)), "W_down"),
+                      (dict(out=Fake(bf, M, H + 8)), "out must be"), (dict(out=Fake(bf, M, H, gpu=0)), "out must be")):
+        with pytest.raises(ValueError, match=match):
+            call(**kw)
+    assert lib.calls == []
+    call()
+    assert lib.calls == ["vt_fp4_w4a16_gemm_ragged_ex", "vt_fp4_w4a16_gemm_ragged_combine"]
