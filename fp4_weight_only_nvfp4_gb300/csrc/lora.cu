@@ -19,7 +19,7 @@ namespace {
 // Memory bounds it, so everything streams through a ring of shared-memory chunks filled by
 // asynchronous 16-byte copies, the columns' chunks already under way while v is exchanged (with
 // loads to registers too few bytes were in flight: 53 us for 5003 rows, 4096 -> 5120, rank 32,
-// 46 with them).  Rows of y that are not whole 16-byte pieces (odd N) are copied from the boundary
+// 44 to 49 with them, from card to card).  Rows of y that are not whole 16-byte pieces (odd N) are copied from the boundary
 // before them on (3000 rows, 4096 -> 4095: 49 us, 92 value by value; 30 for 4096 columns); such rows of
 // x, A and B value by value.
 constexpr int kWarps = 8;
@@ -28,7 +28,7 @@ constexpr int kThreads = kWarps * 32;
 // TM: rows per tile; RM: ranks held.  A chunk has a fixed cost of barriers and copies to issue:
 // 256 wide where a CTA has an SM for itself (1 row: 4.6 us, 5.3 with 128); else 128 and as many CTAs
 // per SM as hold two chunks each, with 80 registers a thread for three (96 rows of 64 adapters:
-// 19.2 us; two CTAs of four chunks 20.5; three of five chunks of 64 22.3).
+// 19.8 us; two CTAs of four chunks 20.5; three of five chunks of 64 22.3).
 template <int TM, int RM, int kCluster>
 struct LoraSmem {
   static constexpr int kChunk = kCluster == 16 ? 256 : 128;  // k, or columns, per chunk

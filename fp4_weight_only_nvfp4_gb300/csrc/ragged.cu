@@ -38,12 +38,11 @@ namespace {
 //             accumulators per row tile, the epilogue of an item beside the MMAs of the next;
 //   TOK = 128 for many: the accumulators of one item and the weight stages fill TMEM, so the
 //             epilogue first moves an item to shared memory as bf16 and then stores it.  (160 rows
-//             leave room for three stages only, which cost 8 %: 168 us for 4096 tokens of top-8, 155
-//             with 128 and four.)
+//             leave room for three stages only, which cost 8 % at 4096 tokens of top-8.)
 // Bound: with few rows per group by that least time of an MMA, 270 cycles per packed tile of 4.6 KB
 // or 5.3 TB/s over 152 SMs (77 tokens: 43 us, 5.3 TB/s of packed weights); with many by the MMAs and
 // by the drains, in which an item's SiLU (two special-function operations per output) holds up the
-// next item's MMAs for 2000 of its 20000 cycles (4096 tokens: 155 us, 1.33 PFLOP/s).
+// next item's MMAs for 2000 of its 20000 cycles (4096 tokens: 155 us, 1.33 PFLOP/s, of a call's 166).
 // With SiLU and two row tiles the dequantisers put the gate rows of both tiles in accumulator 0
 // and the up rows in accumulator 1, so that a thread finds its pairs in the same lane.
 // Items are (token tile, R x 128 weight rows) pairs, weight rows innermost; a group of n rows is
@@ -1085,16 +1084,16 @@ cudaError_t launch_ragged(const RaggedLaunch& L, cudaStream_t s, RaggedShape* sh
   // The rules below were measured on 128 experts, top-8, gate_up 1536 x 2048 NVFP4 ("A") and 24
   // experts, top-3, gate_up 2880 x 2592 MXFP4 ("B"), us:
   // One row tile per item while every item gets an SM of its own, so that an SM's share of the
-  // weights is the least (1 token, A: 10.9, 12.1 with two; B: 12.9 and 14.2); else two, which share
-  // the token tile (2 tokens, A: 12.4, 16.0 with one; 77: 48.6 and 66.2).
+  // weights is the least (1 token, A: 10.6, 12.2 with two; B: 12.5 and 14.1); else two, which share
+  // the token tile (2 tokens, A: 13.0, 16.6 with one; 77: 44 and 62).
   const int64_t groups = L.pairs < L.E ? L.pairs : L.E;
   const bool two = groups * L.RT > sm_count();
-  // Tiles of 128 rows from 64 rows per group on (64 rows, A: 69.8, 85.6 with tiles of 64; B: 35.3
-  // and 41.6; 32 rows, A: 55.5 and 54.2; 19 rows, B: 30.2 and 29.0).
+  // Tiles of 128 rows from 64 rows per group on (64 rows, A: 70, 85 with tiles of 64; B: 38 and 43;
+  // 32 rows, A: 62.6 and 63.8; 19 rows, B: 31.3 and 30.2).
   const bool many = two && L.pairs >= 64 * groups;
   // Gathered rows: the pre-pass writes them in group order while that is little data (3063 rows, B:
-  // 53.6, 54.7 by loaders), else it converts each token once and the loaders gather (6144 rows, B:
-  // 82.1, 83.3 in group order; 32768 rows, A: 157 and 186).
+  // 52.2 either way; 4096 rows, A: 64), else it converts each token once and the loaders gather (6144
+  // rows, B: 83.1, 84.6 in group order; 8192 rows, A: 69 and 78; 32768: 166 and 189).
   const bool load = L.gather && L.topk > 1 && many && L.pairs * L.K > (8 << 20);
   const int64_t rows = load ? L.pairs / L.topk : L.pairs;
   // the converted rows as a 2-D tensor: reads past the last row return zeros

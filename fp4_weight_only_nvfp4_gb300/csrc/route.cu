@@ -213,7 +213,9 @@ template <int T>
 inline size_t one_smem(int E) { return (size_t)(E + 1) * (4 + T / 32 * 2) + 16; }
 
 // T = 256 up to 8 tokens (a warp each; 4.7 us, 5.3 with 1024 threads, whose barriers and sum over the
-// warps' counts cost more) and given ids; 1024 for more tokens (16: 5.5 us, 6.7 with 256).
+// warps' counts cost more) and given ids; 1024 for more tokens (16: 5.5 us, 6.7 with 256).  One block
+// per SM is all there is, and saying so lets the compiler take the registers that it needs (16
+// tokens, 256 experts, replayed from a graph: 7.4 us, 7.8 where it spilled some instead).
 template <int PER, int kOneThreads>
 __global__ void __launch_bounds__(kOneThreads, 1) k_route_one(const RouteLaunch L) {
   extern __shared__ int s_dyn[];

@@ -382,6 +382,8 @@ vt_status vt_fp4_ragged_workspace_bytes(vt_fp4_handle W, int64_t M_max, int64_t 
 /* The products of ragged groups: for the i-th grouped pair, in group e,
  *   C[row][n] = bf16( sum_k A[row'][k] * W_e[n][k] ),  fp32 accumulation,
  * for any number of pairs, in one call; W a grouped weight of E experts (or a plain one, E = 1).
+ * The activations enter the products in f16, each row times a power of two: values below 2^-28 of
+ * the row's largest are rounded, by at most 2^-39 of it.
  *   A  (device) bf16 [tokens or pairs][lda], 16-byte aligned, lda >= K, lda % 8 == 0.
  *   C  (device) bf16 [pairs][ldc], ldc >= N (I with VT_RAGGED_SILU_MUL), 2-byte aligned; rows of
  *      pairs in no group are not written.
@@ -419,7 +421,8 @@ vt_status vt_fp4_w4a16_gemm_ragged_combine(const void* A, int64_t lda, vt_fp4_ha
 /* Low-rank adapters of many requests beside a shared projection:
  *   out[m][n] = bf16( y[m][n] + scale[a] * sum_r B_a[n][r] * sum_k A_a[r][k] * x[m][k] ),
  * a = the group of row m (order and offsets over M rows, topk = 1, E = L adapters), both sums
- * in fp32 over the adapter's own ranks[a] <= R; out[m] = y[m] for a row in no group.
+ * in fp32 over the adapter's own ranks[a] <= R, with scale * (A x) held to 16 significant bits (two
+ * bf16 terms) as an operand of the second; out[m] = y[m], bit for bit, for a row in no group.
  *   x (device) bf16 [M][ldx], ldx >= K;  y, out (device) bf16 [M][ldy], [M][ldo], >= N;
  *   A (device) bf16 [L][R][K];  B (device) bf16 [L][N][R];  scale (device) fp32 [L];
  *   ranks (device, optional) int32 [L], clamped to [0, R]; NULL: R for each.
