@@ -35,6 +35,7 @@ namespace vt {
 namespace {
 
 constexpr uint64_t kPfWaitNs = 2000000000ull;  // drains of copies and MMAs in flight
+constexpr uint64_t kPauseNs = 1000000ull;      // of a producer that is asked to start late
 constexpr int kBM = 128;          // tokens per tile (MMA M)
 constexpr int kBN = 256;          // weight rows per tile (MMA N): two packed row tiles
 // A tile is 256 weight rows x 2 token tiles of 128: one dequantised B tile serves two MMAs
@@ -86,7 +87,7 @@ struct PrefillParams {
   int vec32_store;   // C 32-byte aligned and ldc % 16 == 0
   int pair_store;    // C 4-byte aligned and ldc even: two outputs per 32-bit store
   uint64_t wait_ns;  // limit of every bounded wait
-  int withhold;      // test hook: issue no copies (the waits then run out)
+  int withhold;      // test hook: > 0 issue no copies (the waits then run out), < 0 start a millisecond late
   uint32_t layout;   // packed row order (kLayoutRows / kLayoutPaired)
   int silu;          // paired gate_up: C[M][I] = silu(gate) * up
 };
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const uint32_t drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + off_bar(FMT) + kNumBars * 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued = abort + 1;  // copies of activation and of weight stages, once the producer is done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(acc_empty + 8 * s, kEpiWarps);
     }
     mbar_init(drain, 1);
-    *abort = 0;
+    *abort = issued[0] = issued[1] = 0;
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   fence_mbar_init();
@@ -145,13 +147,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && !p.withhold) {
+    if (lane == 0 && p.withhold < 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < kPauseNs) {}
+    }
+    if (lane == 0 && p.withhold <= 0) {
       // a weight tile serves the token tiles running beside it; an activation tile serves
       // every weight tile over the whole run
       const uint64_t pol_w = l2_evict_normal_policy();
       const uint64_t pol_a = l2_evict_last_policy();
       uint32_t ia = 0, pa = 0, ip = 0, pp = 0;
-      int a_issued = 0, p_issued = 0;  // copies issued (for the drain after a timeout)
+      int a_issued = 0, p_issued = 0;
       bool ok = true;
       for (int64_t tile = blockIdx.x; ok && tile < T; tile += G) {
         const int64_t nt = tile / mptiles, mt0 = 2 * (tile % mptiles);
@@ -177,23 +183,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (++ip == kPStages) { ip = 0; pp ^= 1u; }
         }
       }
-      if (!ok) {
-        atomicExch(p.status, 5);
-        // Let the copies already issued land before the CTA's shared memory is released:
-        // the most recent issue on each slot completes that slot's current phase.
-        for (int k = 0; k < kAStages && k < a_issued; ++k) {
-          ia = ia == 0 ? kAStages - 1 : ia - 1;
-          if (ia == kAStages - 1) pa ^= 1u;
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(a_full + 8 * ia, pa) && globaltimer_ns() - t0 < kPfWaitNs) {}
-        }
-        for (int k = 0; k < kPStages && k < p_issued; ++k) {
-          ip = ip == 0 ? kPStages - 1 : ip - 1;
-          if (ip == kPStages - 1) pp ^= 1u;
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(p_full + 8 * ip, pp) && globaltimer_ns() - t0 < kPfWaitNs) {}
-        }
-      }
+      issued[0] = a_issued;
+      issued[1] = p_issued;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -244,11 +235,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const bool wide = FMT == FMT_MX && p.hdr->wide != 0;
     uint32_t ip = 0, pp = 0, ib = 0, pb = 0;
     bool ok = true;
+    // Each lane learns for itself that a wait has run out.  One that gives up keeps step with the
+    // warp: it passes the two __syncwarp of every k step still to come, so that no lane that goes on
+    // waits there for ever.  (A vote at each wait would do too: 2048 tokens 484 us, 475 without.)
+    int64_t left = 0;
+    auto steps_left = [&](int64_t tile, int64_t kt) { return 2 * ((T - 1 - tile) / G * KT + KT - kt); };
     for (int64_t tile = blockIdx.x; ok && tile < T; tile += G) {
       const int64_t nt = tile / mptiles;
       const int nrt = (RT - 2 * nt) >= 2 ? 2 : 1;
       for (int64_t kt = 0; kt < KT; ++kt) {
-        if (!(ok = pf_wait(p_full + 8 * ip, pp, abort, p.wait_ns))) break;
+        if (!(ok = pf_wait(p_full + 8 * ip, pp, abort, p.wait_ns))) { left = steps_left(tile, kt); break; }
         int4 cw[2];
         uint32_t sc[2];
 #pragma unroll
@@ -318,7 +314,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_empty + 8 * ip);
         if (++ip == kPStages) { ip = 0; pp ^= 1u; }
-        if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, p.wait_ns))) break;
+        if (!(ok = pf_wait(b_empty + 8 * ib, pb ^ 1u, abort, p.wait_ns))) { left = steps_left(tile, kt) - 1; break; }
         const uint32_t bt = sB + ib * kBBytes;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -338,6 +334,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (++ib == kBStages) { ib = 0; pb ^= 1u; }
       }
     }
+    for (; left > 0; --left) __syncwarp();
     if (!ok && lane == 0) atomicExch(p.status, 5);
   } else {
     // ------------------------------------------------------------ epilogue
@@ -347,7 +344,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     bool ok = true;
     for (int64_t tile = blockIdx.x; ok && tile < T; tile += G) {
       const int64_t nt = tile / mptiles, mp = tile % mptiles;
-      if (!(ok = pf_wait(acc_full, pab, abort, p.wait_ns))) break;
+      if (!(ok = pf_warp_wait(acc_full, pab, abort, p.wait_ns))) break;
       tc_fence_after();
       for (int h = 0; h < kPair; ++h) {  // the tile's two token tiles, accumulator h
       const int64_t mt = 2 * mp + h;
@@ -519,6 +516,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort) {
+    // Some role gave up, perhaps not the producer: shared memory is kept until the copies that it
+    // issued have landed (the last one on each stage completes that stage's current phase).
+    atomicExch(p.status, 5);
+    const int na = issued[0], np = issued[1];
+    for (int k = na > kAStages ? na - kAStages : 0; k < na; ++k)
+      mbar_wait_bounded(a_full + 8 * (k % kAStages), (uint32_t)(k / kAStages) & 1u, kPfWaitNs);
+    for (int k = np > kPStages ? np - kPStages : 0; k < np; ++k)
+      mbar_wait_bounded(p_full + 8 * (k % kPStages), (uint32_t)(k / kPStages) & 1u, kPfWaitNs);
   }
 }
 

@@ -140,5 +140,12 @@ __device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, volatile 
     }
   }
 }
+// pf_wait with one answer for the (converged) warp: false if it is for any lane.  With the limit
+// running out as the barrier completes, lanes left to themselves could part before a warp-wide
+// instruction.
+__device__ __forceinline__ bool pf_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, pf_wait(bar, parity, abort, limit_ns));
+}
 
 }  // namespace vt

@@ -101,7 +101,9 @@ typedef struct {
   int withhold_weights;/* test hook for the failure path: when nonzero the kernels' weight
                         * producer issues no copies, so the bounded waits run out; the call
                         * completes, the status word reads VT_ERR_TIMEOUT and the output is
-                        * undefined.  The workspace stays reusable. */
+                        * undefined.  The workspace stays reusable.  Negative, on the prefill
+                        * path: the producer starts a millisecond late instead, so that with a
+                        * wait limit of about that the copies land as the waits run out. */
 } vt_fp4_gemm_opts;
 
 /* ---------------------------------------------------------------------- sizes */
