@@ -13,6 +13,8 @@ import ctypes
 import torch
 
 from ._lib import GemmOpts, LaunchInfo, VtError, check, lib
+from .layer import (KVCache, attention_workspace, kv_append, kv_read, paged_attention, residual_norm,
+                    rope_table)
 from .rows import (LoraAdapters, RowGroups, group_rows, group_workspace, lora_add, moe_ffn,
                    moe_ffn_workspace, moe_route, status_workspace, w4a16_gemm_ragged,
                    w4a16_gemm_ragged_combine, w4a16_gemm_ragged_silu_mul)
@@ -25,7 +27,8 @@ __all__ = ["NVFP4", "MXFP4", "GROUP", "PackedWeight", "w4a16_gemm", "w4a16_gemm_
            "quantize_act", "quantize", "prepack_bytes", "workspace_status", "noalloc_status", "VtError",
            "algorithmic_bytes", "RowGroups", "group_rows", "group_workspace", "moe_route",
            "w4a16_gemm_ragged", "w4a16_gemm_ragged_silu_mul", "w4a16_gemm_ragged_combine",
-           "moe_ffn", "moe_ffn_workspace", "LoraAdapters", "lora_add"]
+           "moe_ffn", "moe_ffn_workspace", "LoraAdapters", "lora_add", "KVCache", "rope_table",
+           "kv_append", "kv_read", "paged_attention", "attention_workspace", "residual_norm"]
 
 
 def _stream(stream) -> ctypes.c_void_p:

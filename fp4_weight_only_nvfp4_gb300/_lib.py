@@ -31,6 +31,15 @@ class GemmOpts(ctypes.Structure):
                 ("withhold_weights", ctypes.c_int)]
 
 
+class KvCacheView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+_F32 = ctypes.c_float
+_KV = ctypes.POINTER(KvCacheView)
+
 SIGNATURES = {
     "vt_fp4_prepack_bytes": (_ST, [ctypes.c_int, _I64, _I64, ctypes.POINTER(_SZ)]),
     "vt_fp4_prepack": (_ST, [_P, _P, ctypes.c_float, ctypes.c_int, _I64, _I64, _P, _SZ, _P,
@@ -82,6 +91,17 @@ SIGNATURES = {
                                                _P, _SZ, _P]),
     "vt_fp4_lora_add": (_ST, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P,
                               _I64, _P, _I64, _P]),
+    "vt_fp4_kv_page_bytes": (_ST, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "vt_fp4_kv_append": (_ST, [_KV, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64,
+                               ctypes.c_int, _P, _P, ctypes.c_int, _F32, _P, _I64, _P]),
+    "vt_fp4_kv_read": (_ST, [_KV, _I64, _P, _P, _P, _P]),
+    "vt_fp4_kv_put": (_ST, [_KV, _I64, _P, _P, _P, _P, _P, _P]),
+    "vt_fp4_kv_get": (_ST, [_KV, _I64, _P, _P, _P, _P, _P, _P]),
+    "vt_fp4_attention_workspace_bytes": (_ST, [_KV, _I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "vt_fp4_paged_attention": (_ST, [_KV, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _F32, _I64, _P,
+                                     _P, _I64, _P, _SZ, _P]),
+    "vt_fp4_residual_norm": (_ST, [_P, _I64, _I64, _I64, _P, _I64, ctypes.c_int, _P, _P, _I64, _F32, _P,
+                                   ctypes.c_int, _F32, _P, _I64, _P, _I64, _P]),
     "vt_fp4_last_error": (ctypes.c_char_p, []),
 }
 

@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kv.cuh"
+
 namespace vt {
 
 cudaError_t launch_prepack(const uint8_t* const codes[2], const uint8_t* const scales[2],
@@ -192,6 +194,89 @@ struct LoraLaunch {
   int64_t ldo;
 };
 cudaError_t launch_lora(const LoraLaunch& L, cudaStream_t s);
+
+// ------------------------------------------------- cache, attention and norms
+constexpr int kMaxNormWidth = 16384;
+constexpr int kMaxGroupHeads = 64;  // query heads of one key/value head
+
+struct AppendLaunch {
+  KvCache cache;
+  int64_t T;
+  const void* q;           // NULL: none (q_heads 0)
+  int q_heads;
+  int64_t ldq;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+  const int64_t* slots;
+  const int32_t* positions;
+  const float* table;      // [table_rows][rot]
+  int64_t table_rows;
+  int rot, interleaved;
+  const void* q_norm;
+  const void* k_norm;      // NULL: no norms
+  int norms_fp32;
+  float eps;
+  void* q_out;
+  int64_t ldo;
+};
+cudaError_t launch_append(const AppendLaunch& L, int head_dim, cudaStream_t s);
+
+struct KvMoveLaunch {
+  KvCache cache;
+  int64_t T;
+  const int64_t* slots;
+  uint8_t* k_codes;        // put, get
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  void* k;                 // read: bf16
+  void* v;
+};
+// dir 0 put, 1 get, 2 read
+cudaError_t launch_kv_move(const KvMoveLaunch& L, int head_dim, int dir, cudaStream_t s);
+
+struct AttendLaunch {
+  KvCache cache;
+  int64_t T;
+  const void* q;
+  int64_t ldq;
+  int q_heads, group;      // group: query heads per key/value head
+  const int32_t* tables;
+  int64_t ldt;
+  const int32_t* lens;
+  const int32_t* starts;   // NULL: one row per sequence
+  int64_t B;
+  float scale;
+  int64_t window;          // 0: none
+  const float* sinks;
+  void* out;
+  int64_t ldo;
+  uint8_t* workspace;
+};
+size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int head_dim);
+cudaError_t launch_attend(const AttendLaunch& L, int head_dim, cudaStream_t s);
+
+struct NormLaunch {
+  const void* x;
+  int64_t T, H, ldx;
+  const void* residual;    // NULL: none
+  int64_t ldr;
+  int residual_fp32;
+  const void* post_weight;
+  const void* gate;
+  int64_t ldg;             // 0: one row for all
+  float scale;
+  const void* weight;
+  int weights_fp32;
+  float eps;
+  void* h;
+  int64_t ldh;
+  void* y;
+  int64_t ldy;
+};
+cudaError_t launch_norm(const NormLaunch& L, cudaStream_t s);
 
 // Raises a kernel's limits of dynamic shared memory and (large) cluster size, once per device.
 template <typename K>

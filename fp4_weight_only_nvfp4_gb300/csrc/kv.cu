@@ -1,0 +1,247 @@
+// The paged NVFP4 cache: appending tokens (per-head norm, rotation and quantisation on the way),
+// reading values back, and moving raw tokens in and out.
+#include <cuda_bf16.h>
+
+#include "actq.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "kv.cuh"
+
+namespace vt {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    x[2 * q] = bf16_lo(w[q]);
+    x[2 * q + 1] = bf16_hi(w[q]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+    w[q] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void load_norm8(const void* w, int fp32, int d, float (&x)[8]) {
+  if (fp32) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + d);
+    const float4 a = p[0], b = p[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(w) + d), x);
+  }
+}
+
+// (hi, lo) += v, hi + lo the exact sum but for the rounding of lo (Knuth's two-sum).
+__device__ __forceinline__ void two_add(float& hi, float& lo, float v) {
+  const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b));
+  hi = s;
+  lo = __fadd_rn(lo, e);
+}
+
+// D / 8 lanes take one head's vector of one token, 8 values each.  The decisions of the quantiser
+// follow the vector's values, so each operation is rounded on its own: the result is that of the
+// formulas in fp32 whatever the layout.  Bound by memory: 2 bytes in per value, 2 (q) or 9/16 (k, v) out.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendLaunch p) {
+  constexpr int LANES = D / 8;
+  const int sub = threadIdx.x % LANES, d = sub * 8;
+  const int per_token = p.q_heads + 2 * p.cache.heads;
+  const int64_t items = p.T * per_token;
+  const int64_t item = (blockIdx.x * (int64_t)kAppendThreads + threadIdx.x) / LANES;
+  // every lane stays for the shuffles; one past the end repeats the last item and stores nothing
+  const bool live = item < items;
+  const int64_t it = live ? item : items - 1;
+  const int64_t t = it / per_token;
+  const int h = (int)(it - t * per_token);
+  const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.cache.heads;
+  const int kvh = is_q ? 0 : (is_k ? h - p.q_heads : h - p.q_heads - p.cache.heads);
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_q ? p.q : is_k ? p.k : p.v) +
+                             t * (is_q ? p.ldq : is_k ? p.ldk : p.ldv) + (int64_t)(is_q ? h : kvh) * D + d;
+  float x[8];
+  unpack8(*reinterpret_cast<const uint4*>(src), x);
+  const bool turned = is_q || is_k;
+
+  if (p.k_norm) {  // uniform over the grid: every lane takes part in the shuffles
+    // squares of bf16 values are exact in fp32; their sum is held in two words and rounded once
+    float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) two_add(hi, lo, __fmul_rn(x[i], x[i]));
+#pragma unroll
+    for (int m = 1; m < LANES; m <<= 1) {
+      const float ohi = __shfl_xor_sync(0xffffffffu, hi, m), olo = __shfl_xor_sync(0xffffffffu, lo, m);
+      two_add(hi, lo, ohi);
+      lo = __fadd_rn(lo, olo);
+    }
+    const float ms = __fmul_rn(__fadd_rn(hi, lo), 1.0f / D);
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
+    if (turned) {
+      float w[8];
+      load_norm8(is_q ? p.q_norm : p.k_norm, p.norms_fp32, d, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+    }
+  }
+
+  if (p.rot) {
+    const int half = p.rot >> 1;
+    const int pos = turned ? p.positions[t] : 0;
+    const bool known = pos >= 0 && pos < p.table_rows;
+    const float* row = p.table + (known ? (int64_t)pos * p.rot : 0);
+    const bool inside = turned && d < p.rot;
+    if (p.interleaved) {
+      if (inside) {
+        const float4 c4 = *reinterpret_cast<const float4*>(row + (d >> 1));
+        const float4 s4 = *reinterpret_cast<const float4*>(row + half + (d >> 1));
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[2 * i], b = x[2 * i + 1];
+          x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+          x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+        }
+      }
+    } else {
+      // the other of each pair is half / 8 lanes away (rot is a multiple of 16)
+      const bool low = d < half;
+      const int lane = threadIdx.x & 31;
+      const int from = d < p.rot ? (low ? lane + half / 8 : lane - half / 8) : lane;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], from);
+      if (inside) {
+        const int at = low ? d : d - half;
+        const float4* cp = reinterpret_cast<const float4*>(row + at);
+        const float4* sp = reinterpret_cast<const float4*>(row + half + at);
+        const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = __fmul_rn(x[i], c[i]), b = __fmul_rn(o[i], s[i]);
+          x[i] = low ? __fsub_rn(a, b) : __fadd_rn(a, b);
+        }
+      }
+    }
+    if (inside && !known) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(0x7FC00000u);
+    }
+  }
+
+  // a scale group is two lanes; an inf or NaN in it shows in its exponent bits
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (!live) return;
+  if (is_q) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.q_out) + t * p.ldo + (int64_t)h * D + d) = pack8(x);
+    return;
+  }
+  const int64_t slot = p.slots[t];
+  if (slot < 0 || slot >= p.cache.slots) return;
+  const float g = (is_k ? p.cache.k_scale : p.cache.v_scale)[kvh];
+  const bool bad = top >= 0x7F800000u;
+  const AqNvGroup q = aq_nv_group(bad ? 0.0f : __uint_as_float(top), g, __fmul_rn(6.0f, g));
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __fdiv_rn(x[i], q.d);
+  const uint32_t codes = bad || q.step == 0.0f ? 0u : aq_e2m1x8(c);
+  const int64_t page = slot >> p.cache.page_shift;
+  const int in = (int)(slot & (p.cache.page_size - 1)), r = in % kKvTile;
+  uint8_t* tile = kv_tile<D>(p.cache, page, kvh, in);
+  *reinterpret_cast<uint32_t*>(tile + (is_k ? kv_k_code(D, r, d / 2) : kv_v_code(D, r, d / 2))) = codes;
+  if ((sub & 1) == 0)
+    tile[is_k ? kv_k_scale(D, r, d / 16) : kv_v_scale(D, r, d / 16)] = (uint8_t)(bad ? 0x7Fu : q.sbyte);
+}
+
+// One thread per (token, head, 16 values): their 8 code bytes and scale byte of K and of V.
+template <int D, int DIR>  // 0 put, 1 get, 2 read
+__global__ void __launch_bounds__(256) k_kv_move(const KvMoveLaunch p) {
+  constexpr int GROUPS = D / 16;
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (i >= p.T * p.cache.heads * GROUPS) return;
+  const int g = (int)(i % GROUPS);
+  const int64_t th = i / GROUPS, t = th / p.cache.heads;
+  const int h = (int)(th - t * p.cache.heads);
+  const int64_t slot = p.slots[t];
+  const bool there = slot >= 0 && slot < p.cache.slots;
+  const int in = there ? (int)(slot & (p.cache.page_size - 1)) : 0, r = in % kKvTile;
+  uint8_t* tile = kv_tile<D>(p.cache, there ? slot >> p.cache.page_shift : 0, h, in);
+  const int code_at[2] = {kv_k_code(D, r, g * 8), kv_v_code(D, r, g * 8)};
+  const int scale_at[2] = {kv_k_scale(D, r, g), kv_v_scale(D, r, g)};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint2* codes = reinterpret_cast<uint2*>(tile + code_at[w]);
+    if constexpr (DIR == 0) {
+      if (there) {
+        *codes = reinterpret_cast<const uint2*>(w ? p.v_codes : p.k_codes)[i];
+        tile[scale_at[w]] = (w ? p.v_scales : p.k_scales)[i];
+      }
+    } else {
+      const uint2 c = there ? *codes : make_uint2(0, 0);
+      const uint32_t sb = there ? tile[scale_at[w]] : 0;
+      if constexpr (DIR == 1) {
+        reinterpret_cast<uint2*>(w ? p.v_codes : p.k_codes)[i] = c;
+        (w ? p.v_scales : p.k_scales)[i] = (uint8_t)sb;
+      } else {
+        const float global = (w ? p.cache.v_scale : p.cache.k_scale)[h];
+        const float step = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(sb)));
+        uint32_t f[8];
+        e2m1x8_to_f16x8(c.x, f[0], f[1], f[2], f[3]);
+        e2m1x8_to_f16x8(c.y, f[4], f[5], f[6], f[7]);
+        float x[16];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float2 v = __half22float2(bits_h2(f[q]));
+          x[2 * q] = there ? v.x * step * global : 0.0f;
+          x[2 * q + 1] = there ? v.y * step * global : 0.0f;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(w ? p.v : p.k) + i * 16);
+        dst[0] = pack8(reinterpret_cast<float(&)[8]>(x[0]));
+        dst[1] = pack8(reinterpret_cast<float(&)[8]>(x[8]));
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t move(const KvMoveLaunch& L, int dir, cudaStream_t s) {
+  const int64_t items = L.T * L.cache.heads * (D / 16);
+  const unsigned blocks = (unsigned)((items + 255) / 256);
+  if (dir == 0) k_kv_move<D, 0><<<blocks, 256, 0, s>>>(L);
+  else if (dir == 1) k_kv_move<D, 1><<<blocks, 256, 0, s>>>(L);
+  else k_kv_move<D, 2><<<blocks, 256, 0, s>>>(L);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t append(const AppendLaunch& L, cudaStream_t s) {
+  const int64_t threads = L.T * (L.q_heads + 2 * L.cache.heads) * (D / 8);
+  k_kv_append<D><<<(unsigned)((threads + kAppendThreads - 1) / kAppendThreads), kAppendThreads, 0, s>>>(L);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendLaunch& L, int head_dim, cudaStream_t s) {
+  return head_dim == 64 ? append<64>(L, s) : head_dim == 128 ? append<128>(L, s) : append<256>(L, s);
+}
+
+cudaError_t launch_kv_move(const KvMoveLaunch& L, int head_dim, int dir, cudaStream_t s) {
+  return head_dim == 64 ? move<64>(L, dir, s) : head_dim == 128 ? move<128>(L, dir, s) : move<256>(L, dir, s);
+}
+
+}  // namespace vt

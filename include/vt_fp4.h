@@ -435,6 +435,116 @@ vt_status vt_fp4_lora_add(const void* x, int64_t M, int64_t ldx, int64_t K, cons
                           int64_t R, int64_t N, const int32_t* order, const int32_t* offsets,
                           const void* y, int64_t ldy, void* out, int64_t ldo, vt_stream_t s);
 
+/* ------------------------------------------- between a layer's products
+ *
+ * What a decoder layer runs between its products: a paged cache of keys and values held in NVFP4, the
+ * attention over it, and the norms around the blocks.  No counterpart on the pages beyond
+ * "re-verify 27B NVFP4 on the nvidia ModelOpt checkpoint" (PR #178), "Where decode time goes"
+ * (the step's other kernels beside its GEMMs); the formats are those of the weights.
+ *
+ * The cache: keys and values of `pages` pages of `page_size` tokens.  A slot p names token
+ * p % page_size of page p / page_size.  Each head's vector of a token is head_dim E2M1 codes, an E4M3 scale
+ * per 16 of them and the head's global: k[d] = e2m1 * e4m3 * k_scale[head].  Inside a page the bytes
+ * are in the order that the attention's matrix instructions take them (vt_fp4_kv_put and
+ * vt_fp4_kv_get convert); page i is at data + i * page_stride. */
+typedef struct {
+  void* data;            /* (device), 128-byte aligned; it need not be cleared */
+  int64_t pages;         /* 1 <= pages * page_size < 2^31 */
+  int64_t page_stride;   /* bytes, a multiple of 128, >= vt_fp4_kv_page_bytes */
+  int64_t page_size;     /* 16, 32, 64, 128 or 256 tokens */
+  int64_t heads;         /* key/value heads, 1 to 1024 */
+  int64_t head_dim;      /* 64, 128 or 256 */
+  const float* k_scale;  /* (device) fp32 [heads]: positive normal numbers */
+  const float* v_scale;  /* (device) fp32 [heads] */
+} vt_fp4_kv_cache;
+
+/* Bytes of one page: heads * page_size * head_dim * 9 / 8. */
+vt_status vt_fp4_kv_page_bytes(int64_t page_size, int64_t heads, int64_t head_dim, size_t* bytes);
+
+/* Appends T tokens: q and k normalised per head and rotated by position, k and v quantised into
+ * the cache, q written as bf16.
+ *   q (optional) bf16 [T][ldq] holding q_heads * head_dim columns, k, v bf16 [T][ldk], [T][ldv] of heads *
+ *     head_dim; q_out bf16 [T][ldo] (may be q itself, ldo == ldq).  All (device), 16-byte aligned,
+ *     row strides multiples of 8.
+ *   slots (device) int64 [T]: where token t goes; a slot outside [0, pages * page_size) is not
+ *     written.  Slots are distinct (two tokens of one slot leave a mixture of both).
+ *   norms (optional, both or neither; k_norm alone without q): bf16 (norms_fp32 == 0) or fp32 [head_dim], 16-byte aligned:
+ *     x[d] * r * w[d], r = 1 / sqrt(sum_d x[d]^2 / head_dim + eps).
+ *   positions (device) int32 [T] and table (device) fp32 [table_rows][rot], 16-byte aligned: rot / 2
+ *     cosines and rot / 2 sines per position; both NULL with rot == 0: no rotation.  rot is a multiple
+ *     of 16, at most head_dim.  Of each pair (a, b): a cos - b sin, b cos + a sin; the pairs are (x[i], x[i + rot/2]), or
+ *     (x[2i], x[2i + 1]) if interleaved.  A position outside the table gives NaN.
+ * Quantisation as vt_fp4_quantize_act, with the head's global as the activation global and without
+ * a rounding of k' to bf16 before it: s = E4M3(amax_g / fl32(6 global)), code = E2M1(x / fl32(s
+ * global)); a group holding an inf or NaN gets the NaN scale byte.  Every operation above is rounded to fp32
+ * on its own (no contraction; the sum of squares is held to 2^-44 and rounded once), so that the
+ * result does not depend on how the work is laid out. */
+vt_status vt_fp4_kv_append(const vt_fp4_kv_cache* cache, int64_t T, const void* q, int64_t q_heads,
+                           int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                           const int64_t* slots, const int32_t* positions, const float* table,
+                           int64_t table_rows, int64_t rot, int interleaved, const void* q_norm,
+                           const void* k_norm, int norms_fp32, float eps, void* q_out, int64_t ldo,
+                           vt_stream_t s);
+
+/* The values of T slots: k, v (device) bf16 [T][heads][head_dim], 16-byte aligned,
+ * bf16(fl32(e2m1 * e4m3 * global)); zeros for a slot outside the cache. */
+vt_status vt_fp4_kv_read(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* slots, void* k, void* v,
+                         vt_stream_t s);
+
+/* Raw tokens into and out of the cache: codes u8 [T][heads][head_dim / 2] (low nibble = even d, 8-byte
+ * aligned) and scales u8 [T][heads][head_dim / 16] of keys and of values.  put skips a slot outside
+ * the cache, get writes zeros for it. */
+vt_status vt_fp4_kv_put(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* slots,
+                        const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, vt_stream_t s);
+vt_status vt_fp4_kv_get(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* slots, uint8_t* k_codes,
+                        uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, vt_stream_t s);
+
+/* Workspace of vt_fp4_paged_attention for up to T_max rows of q_heads heads and B_max sequences over
+ * the cache; 256-byte aligned, its first VT_ATTENTION_CLEARED bytes zeroed once by the caller, reusable afterwards in stream order.
+ * Its first word is the status word (vt_fp4_workspace_status). */
+#define VT_ATTENTION_CLEARED 4096
+vt_status vt_fp4_attention_workspace_bytes(const vt_fp4_kv_cache* cache, int64_t T_max, int64_t B_max,
+                                           int64_t q_heads, size_t* bytes);
+
+/* Causal attention of T rows over the cache, the rows' own keys and values being in it already:
+ *   out[t][h] = sum_j p_j v_j / (sum_j p_j + [sinks] exp(sinks[h])),  p_j = exp(scale * q[t][h] . k_j),
+ * over the keys j that row t sees; head h reads key/value head h / (q_heads / heads).
+ *   tables (device) int32 [B][ldt]: sequence b's key j is token j % page_size of page
+ *     tables[b][j / page_size]; entries behind its last key are not read.  A key on a page
+ *     outside [0, pages) is left out.
+ *   lens   (device) int32 [B]: its number of keys (at most ldt * page_size are used).
+ *   starts (device, optional) int32 [B + 1], ascending: rows starts[b] .. starts[b + 1] of q are its
+ *     last ones, in order (the last row sees the last key, the one before it all but that, ...); NULL: one row each, T == B.
+ *     Rows from starts[B] on are left as they were.
+ *   window > 0: row at position p sees the keys (p - window, p]; 0: all up to p.
+ *   sinks  (device, optional) fp32 [q_heads].
+ * A row that sees no key gets zeros.  q, out (device) bf16 [T][ldq], [T][ldo], 16-byte aligned, strides
+ * multiples of 8, q_heads a multiple of heads, at most 64 times as many.  The scores, the softmax's sums and the output accumulate in
+ * fp32; q enters the products in f16 times a power of two per row and head (values below 2^-28 of the row's largest are
+ * rounded, by at most 2^-39 of it), p in f16.  Deterministic: the order of its sums follows from the call's sizes, lens and
+ * the GPU alone.  Asynchronous on `s`, capturable in a CUDA graph; lens, starts and tables are
+ * read on the device. */
+vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const void* q, int64_t q_heads,
+                                 int64_t ldq, const int32_t* tables, int64_t ldt, const int32_t* lens,
+                                 const int32_t* starts, int64_t B, float scale, int64_t window,
+                                 const float* sinks, void* out, int64_t ldo, void* workspace,
+                                 size_t ws_bytes, vt_stream_t s);
+
+/* The norms around a block, with its gate and the residual sum:
+ *   a = x, or norm(x) * post_weight;   h = residual + scale * gate * a;   y = norm(h) * weight,
+ *   norm(x) = x / sqrt(sum x^2 / H + eps).
+ *   x bf16 [T][ldx], residual and h [T][ldr], [T][ldh] of one type (bf16, or fp32 with residual_fp32),
+ *   gate (optional) bf16 [T][ldg], or one row for all with ldg == 0; y bf16 [T][ldy]; weight and
+ *   post_weight (optional) [H], bf16 or fp32 (weights_fp32).  All (device), aligned to their type.
+ *   residual and h NULL: h = scale * gate * a is not written.
+ * Everything in fp32, h and y rounded once (y from the unrounded h).  h may be residual itself, and y may be x, with the same strides.
+ * 1 <= H <= 16384. */
+vt_status vt_fp4_residual_norm(const void* x, int64_t T, int64_t H, int64_t ldx, const void* residual,
+                               int64_t ldr, int residual_fp32, const void* post_weight, const void* gate,
+                               int64_t ldg, float scale, const void* weight, int weights_fp32,
+                               float eps, void* h, int64_t ldh, void* y, int64_t ldy, vt_stream_t s);
+
 /* -------------------------------------------------------------------- W4A4 */
 
 /* The W4A4 arm: C = Q(A) . W^T with Q the activation quantiser below (activations in the

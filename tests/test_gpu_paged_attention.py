@@ -1,0 +1,248 @@
+"""GPU: causal attention over the paged NVFP4 cache, against fp64."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_weight_only_nvfp4_gb300 as vt
+from layer_helpers import F, attention, gpu, random_tokens, values
+from rows_helpers import acts, assert_close, f64
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    """A cache of random tokens and sequences of the given lengths on shuffled pages."""
+
+    def __init__(self, rng, lens, Hq, Hkv, D, page, rows=None, spare=2):
+        self.rng, self.Hq, self.Hkv, self.D, self.page = rng, Hq, Hkv, D, page
+        self.lens = np.array(lens, dtype=np.int32)
+        need = [-(-max(n, 0) // page) for n in lens]
+        self.pages = sum(need) + spare
+        g = lambda: torch.from_numpy(rng.uniform(0.01, 0.03, Hkv).astype(F)).cuda()
+        self.cache = vt.KVCache.empty(self.pages, page, Hkv, D, g(), g())
+        self.cache.data.fill_(0xFF)  # unused places hold NaN scales
+        self.tables = np.full((len(lens), max(need + [1])), -1, dtype=np.int32)
+        order, at = rng.permutation(self.pages), 0
+        for b, n in enumerate(need):
+            self.tables[b, :n] = order[at:at + n]
+            at += n
+        slots = np.concatenate([self.slots(b) for b in range(len(lens))] + [np.zeros(0, dtype=np.int64)])
+        self.raw = random_tokens(rng, self.pages * page, Hkv, D)
+        if slots.size:
+            self.cache.put(gpu(slots), *(gpu(a[slots]) for a in self.raw))
+        if rows is None:
+            self.starts, T = None, len(lens)
+        else:
+            self.starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+            T = int(self.starts[-1])
+        self.q = acts(rng, T, Hq, D)
+
+    def slots(self, b):
+        j = np.arange(max(int(self.lens[b]), 0))
+        return self.tables[b][j // self.page].astype(np.int64) * self.page + j % self.page
+
+    def kv(self):
+        kc, ks, vc, vs = self.raw
+        wide = lambda t: f64(t)[None, :, None]
+        return values(kc, ks, wide(self.cache.k_scale)), values(vc, vs, wide(self.cache.v_scale))
+
+    def run(self, **kw):
+        more = {} if self.starts is None else {"starts": gpu(self.starts)}
+        return vt.paged_attention(self.q.cuda(), self.cache, gpu(self.tables), gpu(self.lens), **more, **kw)
+
+    def check(self, scale=None, window=0, sinks=None):
+        got = self.run(scale=scale, window=window, sinks=None if sinks is None else gpu(sinks))
+        ref, err = attention(f64(self.q), *self.kv(), self.tables, self.lens, self.starts, self.page,
+                             self.D ** -0.5 if scale is None else scale, window, sinks)
+        assert_close(got, ref, err)
+        return got
+
+
+HEADS = [(1, 1), (8, 1), (4, 4), (6, 2), (14, 2), (16, 1), (24, 2), (64, 1), (5, 5), (33, 3)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", HEADS)
+def test_one_row_per_sequence(Hq, Hkv, D):
+    rng = np.random.default_rng(Hq * 300 + D)
+    Case(rng, [1, 77, 0, 16, 300, 33], Hq, Hkv, D, 16 << (Hq % 3)).check()
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 256), (128, 16), (256, 64)])
+@pytest.mark.parametrize("lens", [[0], [1], [15, 16, 17], [63, 64, 65, 127, 128, 129], [0, 0, 5, 0], [2000], [1] * 90])
+def test_lengths(lens, D, page):
+    rng = np.random.default_rng(len(lens) + D)
+    Case(rng, lens, 4, 2, D, page).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", HEADS)
+def test_rows_of_a_prompt(Hq, Hkv, D):
+    rng = np.random.default_rng(Hq * 301 + D)
+    Case(rng, [50, 40, 7, 150], Hq, Hkv, D, 16 << (Hq % 3), rows=[1, 40, 0, 70]).check()
+
+
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 64), (256, 16)])
+@pytest.mark.parametrize("lens,rows", [([1], [1]), ([300], [300]), ([0, 3], [0, 3]), ([129, 400, 5], [129, 2, 5]),
+                                       ([1000], [3]), ([128, 128], [128, 64]), ([520, 130], [17, 130])])
+def test_chunks(lens, rows, D, page):
+    rng = np.random.default_rng(sum(lens) + D)
+    Case(rng, lens, 8, 2, D, page, rows=rows).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 100, 129, 5000])
+def test_windows_and_sinks(window, D):
+    rng = np.random.default_rng(window + D)
+    sinks = rng.standard_normal(8).astype(F)
+    sinks[2], sinks[3] = -np.inf, 30.0
+    Case(rng, [1, 64, 200, 333, 0], 8, 2, D, 16).check(window=window, sinks=sinks)
+    Case(rng, [150, 64, 290], 8, 2, D, 32, rows=[150, 5, 130]).check(window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("rows", [None, [3, 40, 9]])
+def test_more_rows_than_keys_and_rows_behind_the_last(rows):
+    """Rows that see no key are zeros; rows of no sequence are left as they were."""
+    rng = np.random.default_rng(9)
+    c = Case(rng, [10, 20, 0], 4, 2, 64, 16, rows=rows)
+    if rows is None:
+        c.check(sinks=np.ones(4, dtype=F))
+        return
+    c.check()
+    c.check(sinks=np.ones(4, dtype=F), window=3)
+    T = c.q.shape[0]
+    wide = torch.full((T + 5, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.cat([c.q, torch.full((5, 4, 64), float("nan"), dtype=torch.bfloat16)]).cuda()
+    vt.paged_attention(q, c.cache, gpu(c.tables), gpu(c.lens), starts=gpu(c.starts), out=wide)
+    assert torch.equal(wide[:T], c.run()) and (wide[T:] == 7).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [None, [70, 3, 130]])
+def test_not_a_number_in_keys_values_and_queries(rows, D):
+    """A NaN scale of a key makes the rows that see it NaN, one of a value the 16 columns it scales
+    of those rows; rows that do not see the token keep their numbers."""
+    rng = np.random.default_rng(D)
+    c = Case(rng, [90, 200, 130], 6, 2, D, 16, rows=rows)
+    kc, ks, vc, vs = c.raw
+    first = lambda j, b: c.slots(b)[j]
+    vs[first(60, 0), 1, 2], vs[first(150, 1), 0, 0], vs[first(199, 1), 0, 3] = 0x7F, 0xFF, 0x7F
+    vs[first(129, 2), 1, 1], ks[first(128, 2), 0, 1], ks[first(5, 0), 0, 0] = 0x7F, 0x7F, 0xFF
+    everything = np.arange(c.pages * c.page)
+    c.cache.put(gpu(everything), *(gpu(a) for a in c.raw))
+    c.q[-1, 5, 3] = float("nan")
+    for window in (0, 20):
+        got = f64(c.run(window=window))
+        ref, err = attention(f64(c.q), *c.kv(), c.tables, c.lens, c.starts, c.page, D ** -0.5, window)
+        lost = np.isnan(ref)
+        assert lost.any() and np.array_equal(np.isnan(got), lost)
+        assert_close(got[~lost], ref[~lost], err[~lost])
+
+
+@pytest.mark.parametrize("rows", [None, [2, 60]])
+def test_large_and_small_scores(rows):
+    """Scores of thousands, of one sign, and q from tiny to huge: the largest score alone counts."""
+    rng = np.random.default_rng(11)
+    for size in (1e-30, 1e-4, 300.0):
+        c = Case(rng, [100, 190], 4, 2, 128, 16, rows=rows)
+        c.q *= size
+        c.check(scale=1.0 if size < 1 else 0.3)
+    c = Case(rng, [100, 190], 4, 2, 128, 16, rows=rows)
+    c.q *= 1e30
+    got = f64(c.run(scale=1e-30))
+    assert np.isfinite(got).all()
+    c.check(scale=-0.1e-30)
+    c.check(scale=0.0)
+
+
+@pytest.mark.parametrize("rows", [None, [2, 60]])
+def test_pages_outside_the_cache_are_left_out(rows):
+    rng = np.random.default_rng(12)
+    c = Case(rng, [100, 190], 4, 2, 128, 16, rows=rows)
+    c.tables[0, 2], c.tables[1, 0], c.tables[1, 11] = -7, c.pages, 2 ** 31 - 1
+    c.check()
+    c.tables[1, :] = -1
+    c.check()
+    assert (c.run()[-1] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [None, [2, 60]])
+def test_lens_beyond_the_table_and_below_zero(rows):
+    rng = np.random.default_rng(13)
+    c = Case(rng, [96, 192], 4, 2, 64, 16, rows=rows)
+    keep = c.lens.copy()
+    want = c.run()
+    c.tables = np.ascontiguousarray(c.tables)
+    c.lens = np.array([keep[0], 2 ** 31 - 1], dtype=np.int32)  # the table holds 192 for the second
+    got = c.run()
+    assert torch.equal(got, want)
+    c.lens = np.array([-5, -2 ** 31], dtype=np.int32)
+    assert (c.run() == 0).all()
+
+
+def test_starts_out_of_range_touch_nothing_else():
+    rng = np.random.default_rng(14)
+    c = Case(rng, [96, 192, 50], 4, 2, 64, 16, rows=[5, 6, 7])
+    q = c.q.cuda()
+    wide = torch.full((18 + 40, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for s in ([0, 5, 11, 2 ** 31 - 1], [-2 ** 31, 5, 11, 18], [18, 11, 5, 0], [0, 40, 3, 18], [-1, -1, -1, -1],
+              [2 ** 31 - 1] * 4):
+        vt.paged_attention(q, c.cache, gpu(c.tables), gpu(c.lens), starts=gpu(np.array(s, dtype=np.int32)), out=wide[20:38])
+        assert (wide[:20] == 7).all() and (wide[38:] == 7).all()
+
+
+@pytest.mark.parametrize("rows", [None, [2, 60]])
+def test_strides_another_stream_and_the_same_workspace_again(rows):
+    rng = np.random.default_rng(15)
+    c = Case(rng, [100, 190], 4, 2, 128, 16, rows=rows)
+    T = c.q.shape[0]
+    want = c.run()
+    qkv = torch.full((T, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    qkv[:, :4] = c.q.cuda()
+    out = torch.full((T, 6, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    more = {} if rows is None else {"starts": gpu(c.starts)}
+    ws = vt.attention_workspace(T, 2, 4, c.cache)
+    tables, lens = gpu(c.tables), gpu(c.lens)
+    vt.paged_attention(qkv[:, :4], c.cache, tables, lens, out=out[:, 1:5], workspace=ws, **more)
+    assert torch.equal(out[:, 1:5], want) and (out[:, 0] == 7).all() and (out[:, 5] == 7).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        got = vt.paged_attention(qkv[:, :4], c.cache, tables, lens, workspace=ws, stream=side, **more)
+    side.synchronize()
+    assert torch.equal(got, want)
+    assert vt.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("rows", [None, [2, 60]])
+def test_a_captured_call_follows_lens_and_tables(rows):
+    rng = np.random.default_rng(16)
+    c = Case(rng, [100, 190], 4, 2, 128, 16, rows=rows)
+    more = {} if rows is None else {"starts": gpu(c.starts)}
+    q, tables, lens = c.q.cuda(), gpu(c.tables), gpu(c.lens)
+    out, ws = torch.empty_like(q), vt.attention_workspace(q.shape[0], 2, 4, c.cache)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vt.paged_attention(q, c.cache, tables, lens, out=out, workspace=ws, **more)
+    for n in ([100, 190], [64, 3], [100, 77]):
+        c.lens = np.array(n, dtype=np.int32)
+        c.q = acts(rng, *c.q.shape)
+        lens.copy_(gpu(c.lens)), q.copy_(c.q)
+        graph.replay()
+        assert torch.equal(out, c.run())
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,lens,rows", [(128, 8, 1, [40000], None), (256, 6, 1, [30000], [5]),
+                                               (64, 16, 2, [20001, 5, 9000], [40, 1, 3])])
+def test_long_sequences(D, Hq, Hkv, lens, rows):
+    rng = np.random.default_rng(D)
+    Case(rng, lens, Hq, Hkv, D, 64, rows=rows).check()
+
+
+def test_two_runs_are_bit_for_bit_alike():
+    rng = np.random.default_rng(17)
+    for rows in (None, [30, 200, 1]):
+        c = Case(rng, [3000, 500, 9000], 8, 2, 128, 16, rows=rows)
+        want = c.run()
+        for _ in range(5):
+            assert torch.equal(c.run(), want)
