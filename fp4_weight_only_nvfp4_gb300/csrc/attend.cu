@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include "actq.cuh"
+#include "attend.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.cuh"
@@ -84,9 +85,12 @@ __global__ void __launch_bounds__(128) k_attend_simple(const AttendLaunch p) {
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int head_dim) { return 4096; }
+size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int head_dim) {
+  return kAttendCleared + attend_row_parts_bytes(head_dim);
+}
 
 cudaError_t launch_attend(const AttendLaunch& L, int head_dim, cudaStream_t s) {
+  if (!L.starts) return launch_attend_row(L, head_dim, s);
   const unsigned blocks = (unsigned)((L.T * L.q_heads + 3) / 4);
   if (head_dim == 64) k_attend_simple<64><<<blocks, 128, 0, s>>>(L);
   else if (head_dim == 128) k_attend_simple<128><<<blocks, 128, 0, s>>>(L);

@@ -1,0 +1,77 @@
+// Shared by the kernels of attention over the paged NVFP4 cache.
+#pragma once
+#include "kernels.h"
+
+namespace vt {
+
+constexpr int kAttendCleared = 4096;  // status word and arrival counts, zeros between calls
+constexpr int kMaxAttendGrid = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+// Probabilities are held as 2^(s - m + kPBias): in f16 those down to 2^-26 of the row's largest
+// then keep all their bits (2^-36: the last bit), and their sum over a long row what they add.
+constexpr float kPBias = 12.0f;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_wait_all_if(bool yes) {
+  if (yes) asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Keys of sequence b, and the first that its last row sees.
+__device__ __forceinline__ int seq_len(const AttendLaunch& a, int64_t b) {
+  const int64_t most = a.ldt << a.cache.page_shift, n = __ldg(a.lens + b);
+  return (int)(n < 0 ? 0 : n > most ? most : n);
+}
+__device__ __forceinline__ int first_key(const AttendLaunch& a, int len) {
+  return a.window > 0 && a.window < len ? len - (int)a.window : 0;
+}
+
+// What a row's sum of p v is multiplied by: the values' global over the sum of p and the sink's
+// share (m in log2 units; p as above).
+__device__ __forceinline__ float out_factor(const AttendLaunch& a, int head, int kvh, float m, float l) {
+  float f = a.cache.v_scale[kvh];
+  if (a.sinks) {
+    const float s = a.sinks[head] * kLog2e, top = fmaxf(m, s), ts = top == -INFINITY ? 0.0f : top;
+    const float w = fast_exp2(m - ts);  // the row's sums are re-based where the sink is larger
+    l = l * w + fast_exp2(s - ts + kPBias);
+    f *= w;
+  }
+  return f / l;
+}
+
+// Sum over the CTA's threads, and the sum over the threads before this one.
+template <int WARPS>
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* scan, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += scan[w];
+    all += scan[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+template <int WARPS>
+__device__ __forceinline__ int64_t block_total(int64_t v, int64_t* scan) {
+  int64_t all;
+  block_prefix<WARPS>(v, scan, &all);
+  return all;
+}
+
+size_t attend_row_parts_bytes(int head_dim);
+cudaError_t launch_attend_row(const AttendLaunch& L, int head_dim, cudaStream_t s);
+
+}  // namespace vt

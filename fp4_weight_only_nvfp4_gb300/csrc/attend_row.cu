@@ -1,0 +1,682 @@
+// Attention of one row per sequence over the paged NVFP4 cache (the decode step).
+//
+//   S^T = K Q^T,  p = 2^(s - m),  O^T = V^T P^T,  out = O / sum p
+// with 16 tokens x 8 query heads of one key/value head as one m16n8k16 product's rows and columns.
+// Bound by the cache's bytes (9/16 per value) and close behind by the instructions that turn them into f16: a
+// conversion and a product for every two values (c * s is exact in f16).  So the cache is read once
+// for up to 8 query heads, every lane's codes are fragments as they lie (see kv.cuh), and the
+// probabilities go from the first product's result to the second's operand by a transpose of
+// registers.
+//
+// The work is cut over the keys: all sequences' chunks of kChunk tokens, times the heads, stand in one line
+// that is shared out evenly over the CTAs and inside a CTA over its warps.  A warp has its own ring of
+// asynchronous copies, running maximum, sum and output, and meets the others only at its range's ends:
+// parts of one (sequence, head) in one CTA are joined in shared memory, those of several CTAs in the
+// workspace by the CTA that comes last, in the order of the line.  No wait for another CTA.
+#include <cuda_bf16.h>
+
+#include "actq.cuh"
+#include "attend.cuh"
+#include "common.cuh"
+#include "handle.h"
+#include "kernels.h"
+#include "kv.cuh"
+
+namespace vt {
+
+namespace {
+
+constexpr int kHeads = 8;    // query heads of a work item: the columns of the MMA
+constexpr int kStages = 2;   // chunks of a warp's ring
+
+template <int D>
+struct RowCfg {
+  static constexpr int kChunk = D == 64 ? 64 : 32;          // tokens
+  static constexpr int kTiles = kChunk / kKvTile;
+  static constexpr int kWarps = D == 256 ? 8 : 16;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTile = kv_tile_bytes(D);
+  static constexpr int kStageBytes = kTiles * kTile;        // 4608, 4608, 9216
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kPartFloats = kHeads * (D + 2) + 16; // O [8][D], m [8], l [8], any
+  static constexpr int kPartBytes = kPartFloats * 4;
+  static_assert(kPartBytes <= kRing && kPartBytes % 16 == 0, "a part fits a warp's ring");
+  static constexpr int kOffPart = kWarps * kRing;           // the parts that end inside a warp's range
+  static constexpr int kOffMeta = kOffPart + kWarps * kPartBytes;
+};
+
+// What a warp leaves for the CTA's join: a run of chunks of one (sequence, head) line.
+struct PartMeta {
+  int64_t seg0;   // first chunk of the (sequence, head) on the line
+  int64_t u0, u1; // chunks covered
+  int nb;         // its chunks
+  int b, hu;
+  int used;
+};
+struct RowShared {
+  PartMeta part[32];       // [warp][0: ended inside the range, 1: the last]
+  int64_t scan[32];
+  int64_t start_prefix[16];
+  int start_b[16];
+  int runs, run_first[33];
+  int last;
+};
+
+struct RowParams {
+  AttendLaunch a;
+  int G;         // CTAs
+  int subs;      // sets of 8 query heads per key/value head
+};
+
+// A chunk of the line.
+template <int D>
+struct Cursor {
+  int b, hu, c, nb, c0, len, lo;
+  int64_t seg0;
+  __device__ __forceinline__ void sequence(const RowParams& p) {
+    len = seq_len(p.a, b);
+    lo = first_key(p.a, len);
+    c0 = lo / RowCfg<D>::kChunk;
+    nb = (len + RowCfg<D>::kChunk - 1) / RowCfg<D>::kChunk - c0;
+  }
+  __device__ __forceinline__ void advance(const RowParams& p, int HU) {
+    if (++c < nb) return;
+    c = 0;
+    seg0 += nb;
+    if (++hu < HU) return;
+    hu = 0;
+    do {
+      if (++b >= p.a.B) { nb = 0; return; }
+      sequence(p);
+    } while (nb == 0);
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16x(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+
+// Four A fragments' worth of codes (two words of 8) of rows g and g + 8, times their scales,
+// against four k steps of Q.
+__device__ __forceinline__ void k_words(float (&s)[4], uint32_t lo, uint32_t hi, uint32_t sl, uint32_t sh,
+                                        const uint32_t* q) {
+  uint32_t a[4], b[4];
+  e2m1x8_to_f16x8(lo, a[0], a[1], a[2], a[3]);
+  e2m1x8_to_f16x8(hi, b[0], b[1], b[2], b[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = hmul2_u32(a[i], sl);
+    b[i] = hmul2_u32(b[i], sh);
+  }
+  mma_f16_16816(s, a[0], b[0], a[1], b[1], q[0], q[1]);
+  mma_f16_16816(s, a[2], b[2], a[3], b[3], q[2], q[3]);
+}
+
+// Words of codes of tokens a, b, c, d (8 columns each) and their scales, against P of a tile: four
+// output tiles.
+__device__ __forceinline__ void v_words(float (*o)[4], uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                        uint32_t sab, uint32_t scd, uint32_t p0, uint32_t p1) {
+  constexpr uint32_t M = 0x0F0F0F0Fu;
+  uint32_t e[4], f[4], g[4], h[4];
+  e2m1x8_to_f16x8((a & M) | ((b << 4) & ~M), e[0], e[1], e[2], e[3]);         // even columns
+  e2m1x8_to_f16x8(((a >> 4) & M) | (b & ~M), f[0], f[1], f[2], f[3]);         // odd ones
+  e2m1x8_to_f16x8((c & M) | ((d << 4) & ~M), g[0], g[1], g[2], g[3]);
+  e2m1x8_to_f16x8(((c >> 4) & M) | (d & ~M), h[0], h[1], h[2], h[3]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    mma_f16_16816(o[j], hmul2_u32(e[j], sab), hmul2_u32(f[j], sab), hmul2_u32(g[j], scd),
+                  hmul2_u32(h[j], scd), p0, p1);
+}
+
+// Joins the parts at `parts` (n of them, `stride` floats apart) for head h: lane's D / 32 values of
+// O, and m, l.  The weights 2^(m_i - m) are taken once, 32 parts at a time.
+template <int D, bool GLOBAL>
+__device__ __forceinline__ void join_head(const float* parts, int64_t stride, int n, int h, float (&o)[D / 32],
+                                          float& m, float& l, bool& any) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  auto ld = [](const float* q) { return GLOBAL ? __ldcg(q) : *q; };
+  m = -INFINITY;
+  any = false;
+  for (int i = lane; i < n; i += 32) {
+    const float* q = parts + i * stride + kHeads * D;
+    m = fmaxf(m, ld(q + h));
+    any |= ld(q + 2 * kHeads) != 0.0f;
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  any = __any_sync(0xffffffffu, any);
+  const float ms = m == -INFINITY ? 0.0f : m;
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.0f;
+    if (i0 + lane < n) {
+      const float* q = parts + (i0 + lane) * stride + kHeads * D;
+      w = fast_exp2(ld(q + h) - ms);
+      l += w * ld(q + kHeads + h);
+    }
+    const int k = min(32, n - i0);
+#pragma unroll 4
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* q = parts + (i0 + i) * stride + h * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = GLOBAL ? __ldcg(reinterpret_cast<const float2*>(q + e)) : *reinterpret_cast<const float2*>(q + e);
+        o[e] += wi * v.x;
+        o[e + 1] += wi * v.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const RowParams& p, int b, int hu, int h, float (&o)[D / 32], float m,
+                                          float l, bool any) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, kvh = hu / p.subs, inner = (hu % p.subs) * kHeads + h;
+  if (inner >= p.a.group) return;
+  const int head = kvh * p.a.group + inner;
+  float f = 0.0f;
+  if (any) f = out_factor(p.a, head, kvh, m, l);
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + b * p.a.ldo + (int64_t)head * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+        any ? __floats2bfloat162_rn(o[e] * f, o[e + 1] * f) : __floats2bfloat162_rn(0.0f, 0.0f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const RowParams p) {
+  using C = RowCfg<D>;
+  constexpr int NB = D == 256 ? 2 : 1;         // column blocks of a tile
+  constexpr int KS = D / 16;                   // k steps of S, output tiles of O
+  extern __shared__ __align__(128) uint8_t smem[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem + C::kOffMeta);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int B = (int)p.a.B, HU = p.a.cache.heads * p.subs;
+
+  // ---- the line: chunks of every sequence, and where this CTA's warps begin
+  auto chunks = [&](int b) {
+    const int len = seq_len(p.a, b), lo = first_key(p.a, len);
+    return (len + C::kChunk - 1) / C::kChunk - lo / C::kChunk;
+  };
+  // a sequence without keys has no chunk: its row is zeros
+  for (int b = blockIdx.x * C::kWarps + warp; b < B; b += p.G * C::kWarps)
+    if (seq_len(p.a, b) == 0) {
+      uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + b * p.a.ldo);
+      for (int i = lane; i < p.a.q_heads * D / 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+    }
+  int64_t sum = 0;
+  for (int b = tid; b < B; b += C::kThreads) sum += chunks(b);
+  const int64_t total = block_total<C::kWarps>(sum, sh.scan);
+  const int64_t U = total * HU;
+  if (U == 0) return;
+  const int64_t G = min((int64_t)p.G, (U + C::kWarps - 1) / C::kWarps);
+  if (blockIdx.x >= G) return;
+  const int64_t cta0 = blockIdx.x * U / G, cta1 = (blockIdx.x + 1) * U / G, mine = cta1 - cta0;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < B; b0 += C::kThreads) {
+    const int b = b0 + tid;
+    const int n = b < B ? chunks(b) : 0;
+    int64_t round;
+    const int64_t before = base + block_prefix<C::kWarps>(n, sh.scan, &round);
+#pragma unroll 1
+    for (int w = 0; w < C::kWarps; ++w) {
+      const int64_t u = cta0 + mine * w / C::kWarps;
+      if (u >= before * HU && u < (before + n) * HU) {
+        sh.start_b[w] = b;
+        sh.start_prefix[w] = before;
+      }
+    }
+    base += round;
+  }
+  if (tid < 32) sh.part[tid].used = 0;
+  __syncthreads();
+
+  const int64_t u0 = cta0 + mine * warp / C::kWarps, u1 = cta0 + mine * (warp + 1) / C::kWarps;
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+  if (u0 < u1) {
+    Cursor<D> cur;
+    cur.b = sh.start_b[warp];
+    cur.sequence(p);
+    const int64_t r = u0 - sh.start_prefix[warp] * HU;
+    cur.hu = (int)(r / cur.nb);
+    cur.c = (int)(r - (int64_t)cur.hu * cur.nb);
+    cur.seg0 = u0 - cur.c;
+    Cursor<D> ld = cur;
+    const int total_chunks = (int)(u1 - u0);
+    int issued = 0;
+    uint32_t valid_fifo = 0;  // 4 bits per chunk in the ring: tiles that are there
+    // the page of lane's tile of the chunk to be issued next, fetched ahead
+    auto page_of = [&]() -> int {
+      if (lane >= C::kTiles) return -1;
+      const int tok = (ld.c0 + ld.c) * C::kChunk + lane * kKvTile;
+      return tok < ld.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (tok >> p.a.cache.page_shift)) : -1;
+    };
+    int page = page_of();
+    auto issue = [&]() {
+      const bool ok = page >= 0 && page < p.a.cache.pages;
+      const int tok = (ld.c0 + ld.c) * C::kChunk + lane * kKvTile;
+      const uint8_t* src = kv_tile<D>(p.a.cache, ok ? page : 0, ld.hu / p.subs, tok & (p.a.cache.page_size - 1));
+      const uint32_t there = __ballot_sync(0xffffffffu, ok) & ((1u << C::kTiles) - 1);
+      valid_fifo |= there << (4 * (issued < kStages ? issued : kStages - 1));
+      const uint32_t dst = ring + (issued % kStages) * C::kStageBytes;
+      constexpr int PT = C::kTile / 16;  // 16-byte pieces of a tile
+#pragma unroll
+      for (int j = 0; j < C::kStageBytes / 512; ++j) {
+        const int piece = j * 32 + lane, tile = piece / PT;
+        const uint64_t from = __shfl_sync(0xffffffffu, (uint64_t)(uintptr_t)src, tile);
+        if ((there >> tile) & 1)
+          cp_async16(dst + piece * 16, reinterpret_cast<const uint8_t*>((uintptr_t)from) + (piece - tile * PT) * 16);
+      }
+      ++issued;
+      if (issued < total_chunks) {
+        ld.advance(p, HU);
+        page = page_of();
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (issued < total_chunks) issue();
+      cp_commit();
+    }
+
+    uint32_t q[KS][2];       // B fragments: column g (a head), k = the lane's own columns
+    float mul[2];            // of heads 2t and 2t + 1: raw products to log2 units
+    float o[KS][4], m[2], l[2];
+    bool any = false;
+    int first_c = cur.c;
+    auto begin = [&]() {
+      const int kvh = cur.hu / p.subs, sub = cur.hu % p.subs, inner = sub * kHeads + g;
+      uint4 w[KS / 2];
+      int mx = 0;
+      if (inner < p.a.group) {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + cur.b * p.a.ldq +
+                                   (int64_t)(kvh * p.a.group + inner) * D + (D == 64 ? 16 : 32) * t;
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(src + (D == 256 ? (i >> 2) * 128 + (i & 3) * 8 : i * 8));
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) w[i] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) mx = max(mx, act_maxmag8(reinterpret_cast<const uint32_t*>(&w[i])));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int pw = act_pow2(mx);
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&w[i]), pw);
+        q[2 * i][0] = f.x, q[2 * i][1] = f.y, q[2 * i + 1][0] = f.z, q[2 * i + 1][1] = f.w;
+      }
+      const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[kvh];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mul[i] = unit * pow2f(__shfl_sync(0xffffffffu, pw, 4 * (2 * t + i)));
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+      any = false;
+      first_c = cur.c;
+    };
+    begin();
+
+#pragma unroll 1
+    for (int n = 0; n < total_chunks; ++n) {
+      if (issued < total_chunks) issue();
+      cp_commit();
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t st = ring + (n % kStages) * C::kStageBytes;
+      const uint32_t there = valid_fifo & 15u;
+      valid_fifo >>= 4;
+      const int tok0 = (cur.c0 + cur.c) * C::kChunk;
+      const bool edge = tok0 < cur.lo || tok0 + C::kChunk > cur.len || there != (1u << C::kTiles) - 1;
+
+      // ---- S^T = K Q^T
+      float s[C::kTiles][4];
+#pragma unroll
+      for (int i = 0; i < C::kTiles; ++i) {
+        const uint32_t tb = st + i * C::kTile;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
+        if constexpr (D == 64) {
+          const uint2 lo = ld_shared_v2(tb + g * 32 + t * 8), hi = ld_shared_v2(tb + 256 + g * 32 + t * 8);
+          const uint32_t sc = e4m3x2_to_f16x2(ld_shared_u16x(tb + 8 * D + g * 8 + t * 2));
+          const uint32_t sl = bcast_lo(sc), sr = bcast_hi(sc);
+          k_words(s[i], lo.x, hi.x, sl, sr, q[0]);
+          k_words(s[i], lo.y, hi.y, sl, sr, q[2]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            const int4 lo = ld_shared_v4(tb + c * 1024 + g * 64 + t * 16);
+            const int4 hi = ld_shared_v4(tb + c * 1024 + 512 + g * 64 + t * 16);
+            const uint32_t sw = ld_shared_u32(tb + 8 * D + c * 128 + g * 16 + t * 4);
+            const uint32_t s0 = e4m3x2_to_f16x2(sw), s1 = e4m3x2_to_f16x2(sw >> 16);
+            k_words(s[i], lo.x, hi.x, bcast_lo(s0), bcast_lo(s1), q[8 * c]);
+            k_words(s[i], lo.y, hi.y, bcast_lo(s0), bcast_lo(s1), q[8 * c + 2]);
+            k_words(s[i], lo.z, hi.z, bcast_hi(s0), bcast_hi(s1), q[8 * c + 4]);
+            k_words(s[i], lo.w, hi.w, bcast_hi(s0), bcast_hi(s1), q[8 * c + 6]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] *= mul[e & 1];
+      }
+      // ---- keys that the row does not see; what their places hold may be anything
+      uint32_t seen = 0xFFFFFFFFu;  // bit 4 i + k: token t + 4 k of tile i
+      if (edge) {
+        seen = 0;
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < C::kTiles; ++i) {
+          auto sees = [&](int r) {
+            const int tok = tok0 + i * kKvTile + r;
+            return ((there >> i) & 1) && tok >= cur.lo && tok < cur.len;
+          };
+          const bool a = sees(kv_mma_token(g)), b = sees(kv_mma_token(g + 8));
+          some |= a | b;
+          s[i][0] = a ? s[i][0] : -INFINITY;
+          s[i][1] = a ? s[i][1] : -INFINITY;
+          s[i][2] = b ? s[i][2] : -INFINITY;
+          s[i][3] = b ? s[i][3] : -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) seen |= (uint32_t)sees(t + 4 * k) << (4 * i + k);
+        }
+        any |= __any_sync(0xffffffffu, some);
+      } else {
+        any = true;
+      }
+      // ---- running maximum; the output is scaled only where one rose
+      float ms[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = fmaxf(s[0][i], s[0][i + 2]);
+#pragma unroll
+        for (int j = 1; j < C::kTiles; ++j) x = fmaxf(x, fmaxf(s[j][i], s[j][i + 2]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        ms[i] = fmaxf(m[i], x);
+      }
+      if (__any_sync(0xffffffffu, ms[0] > m[0] || ms[1] > m[1])) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f[i] = ms[i] > m[i] ? fast_exp2(m[i] - ms[i]) : 1.0f;
+          l[i] *= f[i];
+          m[i] = ms[i];
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] *= f[e & 1];
+      }
+      const float off[2] = {kPBias - (m[0] == -INFINITY ? 0.0f : m[0]), kPBias - (m[1] == -INFINITY ? 0.0f : m[1])};
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int i = 0; i < C::kTiles; ++i) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pr[e] = fast_exp2(s[i][e] + off[e & 1]);
+          l[e & 1] += pr[e];
+        }
+        const uint32_t p0 = transpose8x8(pack_half2(pr[0], pr[1])), p1 = transpose8x8(pack_half2(pr[2], pr[3]));
+        const uint32_t tb = st + i * C::kTile + 9 * D;
+        auto scales = [&](int group) {
+          uint32_t w = ld_shared_u32(tb + 8 * D + group * 16 + t * 4);
+          if (edge) {  // a place that is not seen may hold a NaN scale
+            const uint32_t k = seen >> (4 * i);
+            w &= ((k & 1) ? 0xFFu : 0u) | ((k & 2) ? 0xFF00u : 0u) | ((k & 4) ? 0xFF0000u : 0u) | ((k & 8) ? 0xFF000000u : 0u);
+          }
+          return w;
+        };
+        if constexpr (D == 64) {
+          const uint32_t at = tb + t * 32 + g * 4;
+          const uint32_t sw = scales(g >> 1);
+          v_words(o, ld_shared_u32(at), ld_shared_u32(at + 128), ld_shared_u32(at + 256), ld_shared_u32(at + 384),
+                  e4m3x2_to_f16x2(sw), e4m3x2_to_f16x2(sw >> 16), p0, p1);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            const uint32_t at = tb + c * 1024 + t * 64 + ((g * 8) ^ ((t >> 1) * 32));
+            const uint2 a = ld_shared_v2(at), b = ld_shared_v2(at + 256), cc = ld_shared_v2(at + 512), d = ld_shared_v2(at + 768);
+            const uint32_t sw = scales(8 * c + g);
+            const uint32_t sab = e4m3x2_to_f16x2(sw), scd = e4m3x2_to_f16x2(sw >> 16);
+            v_words(o + 8 * c, a.x, b.x, cc.x, d.x, sab, scd, p0, p1);
+            v_words(o + 8 * c + 4, a.y, b.y, cc.y, d.y, sab, scd, p0, p1);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage before it is filled again
+
+      // ---- the end of this (sequence, head), or of the warp's range
+      const bool ends = cur.c + 1 == cur.nb, last = n + 1 == total_chunks;
+      if (ends || last) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+        }
+        constexpr int EJ = D == 64 ? 4 : 8;   // output tiles of a column block
+        if (ends && first_c == 0) {           // all of it
+          const int kvh = cur.hu / p.subs;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int inner = (cur.hu % p.subs) * kHeads + 2 * t + i;
+            if (inner < p.a.group) {
+              const int head = kvh * p.a.group + inner;
+              const float f = any ? out_factor(p.a, head, kvh, m[i], l[i]) : 0.0f;
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + cur.b * p.a.ldo + (int64_t)head * D;
+#pragma unroll
+              for (int c = 0; c < NB; ++c) {
+                uint32_t w[EJ];
+#pragma unroll
+                for (int j = 0; j < EJ; ++j) {
+                  const float x = any ? o[8 * c + j][i] * f : 0.0f, y = any ? o[8 * c + j][i + 2] * f : 0.0f;
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                  w[j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+#pragma unroll
+                for (int j = 0; j < EJ; j += 4)
+                  *reinterpret_cast<uint4*>(dst + c * 128 + (2 * EJ) * g + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+              }
+            }
+          }
+        } else {
+          // ends inside the range (it began before it): a place of its own; else the warp's ring,
+          // which no copy is under way to any more
+          const int kind = ends && !last ? 0 : 1;
+          float* part = reinterpret_cast<float*>(smem + (kind ? warp * C::kRing : C::kOffPart + warp * C::kPartBytes));
+          cp_wait_all_if(kind);
+#pragma unroll
+          for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int j = 0; j < EJ; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float2*>(part + (2 * t + i) * D + c * 128 + 2 * EJ * g + 2 * j) =
+                    make_float2(o[8 * c + j][i], o[8 * c + j][i + 2]);
+          if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              part[kHeads * D + 2 * t + i] = m[i];
+              part[kHeads * D + kHeads + 2 * t + i] = l[i];
+            }
+          }
+          if (lane == 0) {
+            part[kHeads * D + 2 * kHeads] = any ? 1.0f : 0.0f;
+            PartMeta& pm = sh.part[2 * warp + kind];
+            pm.seg0 = cur.seg0;
+            pm.u0 = cur.seg0 + first_c;
+            pm.u1 = cur.seg0 + cur.c + 1;
+            pm.nb = cur.nb;
+            pm.b = cur.b;
+            pm.hu = cur.hu;
+            pm.used = 1;
+          }
+        }
+        if (!last) {
+          cur.advance(p, HU);
+          begin();
+        }
+      } else {
+        ++cur.c;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- join the parts of each (sequence, head): runs of neighbours in the order of the line
+  if (tid == 0) {
+    int n = 0;
+    int64_t seg = -1;
+    for (int i = 0; i < 2 * C::kWarps; ++i)
+      if (sh.part[i].used && sh.part[i].seg0 != seg) {
+        seg = sh.part[i].seg0;
+        sh.run_first[n++] = i;
+      }
+    sh.runs = n;
+    sh.run_first[n] = 2 * C::kWarps;
+  }
+  __syncthreads();
+  const int runs = sh.runs;
+  float* parts = reinterpret_cast<float*>(p.a.workspace + kAttendCleared);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + 256);
+  auto part_at = [&](int i) {
+    return reinterpret_cast<const float*>(smem + ((i & 1) ? (i >> 1) * C::kRing : C::kOffPart + (i >> 1) * C::kPartBytes));
+  };
+  for (int task = warp; task < runs * kHeads; task += C::kWarps) {
+    const int run = task / kHeads, h = task % kHeads, i0 = sh.run_first[run], i1 = sh.run_first[run + 1];
+    const PartMeta& first = sh.part[i0];
+    constexpr int E = D / 32;
+    float o[E], m = -INFINITY, l = 0.0f;
+    bool any = false;
+    int64_t upto = first.u0;
+    for (int i = i0; i < i1; ++i)
+      if (sh.part[i].used) {
+        const float* q = part_at(i) + kHeads * D;
+        m = fmaxf(m, q[h]);
+        any |= q[2 * kHeads] != 0.0f;
+        upto = sh.part[i].u1;
+      }
+    const float ms = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int i = i0; i < i1; ++i)
+      if (sh.part[i].used) {
+        const float* q = part_at(i);
+        const float w = fast_exp2(q[kHeads * D + h] - ms);
+        l += w * q[kHeads * D + kHeads + h];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += w * q[h * D + lane * E + e];
+      }
+    if (first.u0 == first.seg0 && upto == first.seg0 + first.nb) {
+      store_row<D>(p, first.b, first.hu, h, o, m, l, any);
+    } else {
+      // slot 0: what began in an earlier CTA, slot 1: what begins here and goes on
+      float* dst = parts + ((int64_t)blockIdx.x * 2 + (first.u0 == first.seg0)) * C::kPartFloats;
+#pragma unroll
+      for (int e = 0; e < E; ++e) __stcg(dst + h * D + lane * E + e, o[e]);
+      if (lane == 0) {
+        __stcg(dst + kHeads * D + h, m);
+        __stcg(dst + kHeads * D + kHeads + h, l);
+        if (h == 0) __stcg(dst + kHeads * D + 2 * kHeads, any ? 1.0f : 0.0f);
+      }
+    }
+  }
+  // ---- parts that other CTAs hold too: the last one to come joins them
+  for (int run = 0; run < runs; ++run) {
+    if (run != 0 && run != runs - 1) continue;
+    const PartMeta& first = sh.part[sh.run_first[run]];
+    int64_t upto = 0;
+    for (int i = sh.run_first[run]; i < sh.run_first[run + 1]; ++i)
+      if (sh.part[i].used) upto = sh.part[i].u1;
+    const int64_t seg1 = first.seg0 + first.nb;
+    if (first.u0 == first.seg0 && upto == seg1) continue;
+    // CTAs from c0 to c1 share it: CTA i holds [i U / G, (i + 1) U / G)
+    const int64_t c0 = ((first.seg0 + 1) * G - 1) / U, c1 = (seg1 * G - 1) / U;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t before = atomicAdd(counters + c0, 1u);
+      sh.last = before == (uint32_t)(c1 - c0);
+      if (sh.last) counters[c0] = 0;  // for the next call
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh.last) {
+      // CTA c0's part is in its slot 1, the others' in their slot 0
+      for (int h = warp; h < kHeads; h += C::kWarps) {
+        float o[D / 32], m, l, o2[D / 32], m2, l2;
+        bool any, any2;
+        join_head<D, true>(parts + (2 * c0 + 1) * C::kPartFloats, 0, 1, h, o, m, l, any);
+        join_head<D, true>(parts + 2 * (c0 + 1) * C::kPartFloats, 2 * C::kPartFloats, (int)(c1 - c0), h, o2, m2, l2, any2);
+        const float top = fmaxf(m, m2), ts = top == -INFINITY ? 0.0f : top;
+        const float a = fast_exp2(m - ts), b = fast_exp2(m2 - ts);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = o[e] * a + o2[e] * b;
+        store_row<D>(p, first.b, first.hu, h, o, top, l * a + l2 * b, any || any2);
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t go(const RowParams& p, cudaStream_t s) {
+  using C = RowCfg<D>;
+  static int done[64];
+  constexpr size_t bytes = C::kOffMeta + sizeof(RowShared);
+  static_assert(bytes <= 232448, "shared memory");
+  if (cudaError_t e = set_up_kernel(k_attend_row<D>, bytes, done)) return e;
+  k_attend_row<D><<<p.G, C::kThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_row_parts_bytes(int head_dim) {
+  const size_t f = head_dim == 64 ? RowCfg<64>::kPartBytes : head_dim == 128 ? RowCfg<128>::kPartBytes : RowCfg<256>::kPartBytes;
+  return 2 * (size_t)kMaxAttendGrid * f;
+}
+
+cudaError_t launch_attend_row(const AttendLaunch& L, int head_dim, cudaStream_t s) {
+  RowParams p;
+  p.a = L;
+  p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
+  p.subs = (L.group + kHeads - 1) / kHeads;
+  return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
+}
+
+}  // namespace vt
