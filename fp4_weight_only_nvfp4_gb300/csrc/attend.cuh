@@ -5,7 +5,7 @@
 namespace vt {
 
 constexpr int kAttendCleared = 4096;  // status word and arrival counts, zeros between calls
-constexpr int kMaxAttendGrid = 256;
+constexpr int kMaxAttendGrid = 160;
 constexpr float kLog2e = 1.4426950408889634f;
 // Probabilities are held as 2^(s - m + kPBias): in f16 those down to 2^-26 of the row's largest
 // then keep all their bits (2^-36: the last bit), and their sum over a long row what they add.
@@ -30,13 +30,13 @@ __device__ __forceinline__ int first_key(const AttendLaunch& a, int len) {
 }
 
 // What a row's sum of p v is multiplied by: the values' global over the sum of p and the sink's
-// share (m in log2 units; p as above).
-__device__ __forceinline__ float out_factor(const AttendLaunch& a, int head, int kvh, float m, float l) {
+// share (m in log2 units; p and l hold 2^bias).
+__device__ __forceinline__ float out_factor(const AttendLaunch& a, int head, int kvh, float m, float l, float bias) {
   float f = a.cache.v_scale[kvh];
   if (a.sinks) {
     const float s = a.sinks[head] * kLog2e, top = fmaxf(m, s), ts = top == -INFINITY ? 0.0f : top;
     const float w = fast_exp2(m - ts);  // the row's sums are re-based where the sink is larger
-    l = l * w + fast_exp2(s - ts + kPBias);
+    l = l * w + fast_exp2(s - ts + bias);
     f *= w;
   }
   return f / l;
@@ -71,7 +71,10 @@ __device__ __forceinline__ int64_t block_total(int64_t v, int64_t* scan) {
   return all;
 }
 
+// Bytes of the parts that CTAs hand to one another.
 size_t attend_row_parts_bytes(int head_dim);
+size_t attend_tile_parts_bytes(int head_dim);
 cudaError_t launch_attend_row(const AttendLaunch& L, int head_dim, cudaStream_t s);
+cudaError_t launch_attend_tile(const AttendLaunch& L, int head_dim, cudaStream_t s);
 
 }  // namespace vt

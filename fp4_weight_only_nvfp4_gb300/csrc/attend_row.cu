@@ -202,7 +202,7 @@ __device__ __forceinline__ void store_row(const RowParams& p, int b, int hu, int
   if (inner >= p.a.group) return;
   const int head = kvh * p.a.group + inner;
   float f = 0.0f;
-  if (any) f = out_factor(p.a, head, kvh, m, l);
+  if (any) f = out_factor(p.a, head, kvh, m, l, kPBias);
   __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + b * p.a.ldo + (int64_t)head * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
             const int inner = (cur.hu % p.subs) * kHeads + 2 * t + i;
             if (inner < p.a.group) {
               const int head = kvh * p.a.group + inner;
-              const float f = any ? out_factor(p.a, head, kvh, m[i], l[i]) : 0.0f;
+              const float f = any ? out_factor(p.a, head, kvh, m[i], l[i], kPBias) : 0.0f;
               __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + cur.b * p.a.ldo + (int64_t)head * D;
 #pragma unroll
               for (int c = 0; c < NB; ++c) {

@@ -1,0 +1,868 @@
+// Causal attention of chunks of rows over the paged NVFP4 cache, on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(S - m),  O = O + P V,  out = O / sum P
+// A tile is the rows of one key/value head: tokens x its query heads, 128 rows an MMA; two such row
+// tiles (one at head_dim 256) share each block of keys, so that a block is turned into f16 once for 256
+// rows and one row tile's softmax runs beside the other's products.  Bound by the tensor cores for
+// long chunks; for a few rows by the cache's bytes and their conversion.
+//
+// One persistent CTA per SM:
+//   softmax warps  4 per row tile, a thread per row: Q to shared memory (f16, times a power of two per
+//                  row), then per block the row's maximum, the probabilities (written over the
+//                  scores in TMEM as the A operand of the second product) and their sum; at the end
+//                  O to the output.  O is scaled only where a row's maximum rose by more than 2^8: until then the
+//                  sums stay on the older one, which f16 has room for.
+//   K, V warps     4 each: codes and scales straight from the pages to registers a block ahead,
+//                  then f16 (c * s, exact) into shared memory, K as [token][d], V as [d][token]
+//                  (both K-major, 128-byte swizzle).
+//   MMA warp       one thread issues every product.
+// The tiles' blocks of keys, times the heads, stand in one line that is shared out evenly over the
+// CTAs; the parts of a tile that CTAs share are joined by the CTA that comes last.
+//
+// Every wait inside the CTA is bounded (2 s); one that gives up sets the status word and ends every role.
+#include <cuda_bf16.h>
+
+#include "actq.cuh"
+#include "attend.cuh"
+#include "common.cuh"
+#include "handle.h"
+#include "kernels.h"
+#include "kv.cuh"
+#include "tc.cuh"
+
+namespace vt {
+
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kTileBias = 7.0f;   // P = 2^(s - m + 7): below 2^15 while s - m <= 8
+constexpr float kSlack = 8.0f;
+
+template <int D>
+struct TileCfg {
+  static constexpr int kRowTiles = D == 256 ? 1 : 2;
+  static constexpr int kSBufs = D == 256 ? 2 : 1;         // score buffers of a row tile
+  static constexpr int kKeys = D == 256 ? 64 : 128;       // keys of a block
+  static constexpr int kSoftWarps = 4 * kRowTiles;
+  static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + 4;
+  static constexpr int kThreads = (kWarpMma + 1) * 32;
+  static constexpr int kQBytes = 128 * D * 2;             // a row tile
+  static constexpr int kKvBytes = kKeys * D * 2;          // a block of K or V
+  static constexpr int kStages = 2;
+  static constexpr int kOffK = kRowTiles * kQBytes;
+  static constexpr int kOffV = kOffK + kStages * kKvBytes;
+  static constexpr int kOffMeta = kOffV + kStages * kKvBytes;
+  static constexpr int kJobs = D == 64 ? 1 : 2;           // 64 values per lane each, of a K or V warp and block
+  // TMEM columns: scores (P over them), then O
+  static constexpr int kTmemO = 256;
+  static constexpr int kRows = 128 * kRowTiles;
+  static constexpr int kPartFloats = kRows * (D + 4);     // O in columns of 4, then m, l, any
+};
+
+struct TileShared {
+  int64_t scan[32];
+  int64_t seq_first[32 * 17 + 1];
+  int64_t u0, before;  // this CTA's first unit; the units before its tile
+  int b, i;            // its tile
+  int last;
+  int nan_seg[8];
+  uint32_t tmem;
+  int abort;
+  alignas(8) uint64_t bars[24];
+};
+
+struct TileParams {
+  AttendLaunch a;
+  int G;
+  int tokens;     // of a row tile: 128 / group
+  float* parts;
+  uint64_t wait_ns;
+};
+
+struct Seq {
+  int s0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const AttendLaunch& a, int64_t b) {
+  Seq q;
+  const int T = (int)a.T, s = __ldg(a.starts + b), e = __ldg(a.starts + b + 1);
+  q.s0 = s < 0 ? 0 : s > T ? T : s;
+  q.n = (e < q.s0 ? q.s0 : e > T ? T : e) - q.s0;
+  q.len = seq_len(a, b);
+  return q;
+}
+
+// Blocks of keys of a sequence's i-th tile: [first, first + count).
+template <int D>
+__device__ __forceinline__ void tile_blocks(const AttendLaunch& a, const Seq& q, int i, int per_tile, int* first, int* count) {
+  constexpr int KB = TileCfg<D>::kKeys;
+  const int r0 = i * per_tile, r1 = min(q.n, r0 + per_tile);
+  const int64_t past = (int64_t)q.len - q.n;
+  const int64_t hi = past + r1;                                // keys that its last row sees
+  int64_t lo = a.window > 0 ? past + r0 - a.window + 1 : 0;    // the first key that its first row sees
+  if (lo < 0) lo = 0;
+  *first = (int)(lo / KB);
+  *count = hi > 0 && hi > lo ? (int)((hi + KB - 1) / KB) - *first : 0;
+}
+
+// A run of blocks of one (tile, head), walked by every role on its own.
+template <int D>
+struct Walk {
+  Seq q;
+  int b, i, h;
+  int first, count;   // the tile's blocks
+  int at, end;        // this segment: blocks [at, end) of them, counted from first
+  int64_t seg0;       // unit of block 0
+  int64_t left;       // units of the CTA from `at` on
+  int no;             // segments before this one
+  __device__ __forceinline__ void start(const TileParams& p, const TileShared& sh, int64_t u0, int64_t u1) {
+    b = sh.b;
+    i = sh.i;
+    q = load_seq(p.a, b);
+    tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
+    const int64_t r = u0 - sh.before;
+    h = (int)(r / count);
+    at = (int)(r - (int64_t)h * count);
+    seg0 = u0 - at;
+    left = u1 - u0;
+    no = 0;
+    end = (int)min((int64_t)count, at + left);
+  }
+  static __device__ __forceinline__ int per_tile(const TileParams& p) { return p.tokens * TileCfg<D>::kRowTiles; }
+  // To the CTA's next segment; false at its end.
+  __device__ __forceinline__ bool next(const TileParams& p) {
+    left -= end - at;
+    if (left <= 0) return false;
+    ++no;
+    seg0 += count;
+    at = 0;
+    if (++h == p.a.cache.heads) {
+      h = 0;
+      do {
+        ++i;
+        while ((int64_t)i * per_tile(p) >= q.n) {
+          if (++b >= p.a.B) { left = 0; return false; }
+          q = load_seq(p.a, b);
+          i = 0;
+        }
+        tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
+      } while (count == 0);
+    }
+    end = (int)min((int64_t)count, left);
+    return true;
+  }
+  __device__ __forceinline__ int row_tiles(const TileParams& p) const {
+    return TileCfg<D>::kRowTiles == 2 && q.n - i * per_tile(p) > p.tokens ? 2 : 1;
+  }
+  __device__ __forceinline__ bool whole() const { return at == 0 && end == count; }
+};
+
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+      "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = v[i], b[i] = v[16 + i];
+  tmem_st16(taddr, a);
+  tmem_st16(taddr + 16, b);
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
+
+// NaN scales of the values that a row sees in this segment, read from the pages: a bit per 16
+// columns.  Only where a V warp met one: the products themselves take such a scale as zero, since
+// their other rows may not see it.
+template <int D>
+__device__ __noinline__ uint32_t nan_columns(const AttendLaunch& a, int b, int h, int k0, int k1) {
+  uint32_t bits = 0;
+  for (int j = k0; j < k1; ++j) {
+    const int page = __ldg(a.tables + b * a.ldt + (j >> a.cache.page_shift));
+    if (page < 0 || page >= a.cache.pages) continue;
+    const int in = j & (a.cache.page_size - 1);
+    const uint8_t* tile = kv_tile<D>(a.cache, page, h, in);
+    for (int s = 0; s < D / 16; ++s)
+      if ((tile[kv_v_scale(D, in % kKvTile, s)] & 0x7F) == 0x7F) bits |= 1u << s;
+  }
+  return bits;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const TileParams p) {
+  using C = TileCfg<D>;
+  constexpr int KB = C::kKeys, SB = C::kSBufs, W = C::kThreads / 32;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u = smem_u32(smem_raw), base = (raw_u + 1023u) & ~1023u;
+  TileShared& sh = *reinterpret_cast<TileShared*>(smem_raw + (base - raw_u) + C::kOffMeta);
+  const uint32_t sQ = base, sK = base + C::kOffK, sV = base + C::kOffV;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sh.abort;
+  const uint32_t bar0 = smem_u32(sh.bars);
+  const uint32_t q_full = bar0, k_full = q_full + 16, k_empty = k_full + 16, v_full = k_empty + 16, v_empty = v_full + 16;
+  const uint32_t s_full = v_empty + 16;                  // [row tile or buffer]
+  const uint32_t p_full = s_full + 16, pv_done = p_full + 16, joined = pv_done + 16, told = joined + 8, drain = told + 8;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 4);
+      mbar_init(k_full + 8 * i, 4);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 4);
+      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(pv_done + 8 * i, 1);
+    }
+    mbar_init(joined, C::kSoftWarps);
+    mbar_init(told, 1);
+    mbar_init(drain, 1);
+    sh.abort = 0;
+    for (int i = 0; i < 8; ++i) sh.nan_seg[i] = 0;
+  }
+  if (warp == C::kWarpMma) tmem_alloc(smem_u32(&sh.tmem), 512);
+  fence_mbar_init();
+
+  // ---- the line: twice over the tiles, for their units' number and for this CTA's first
+  const int per_tile = p.tokens * C::kRowTiles, Hkv = p.a.cache.heads;
+  int64_t total = 0, cta0 = 0, cta1 = 0, G = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t done = 0;
+    for (int64_t b0 = 0; b0 < p.a.B; b0 += C::kThreads) {
+      const int64_t b = b0 + tid;
+      int64_t tiles = 0, round;
+      if (b < p.a.B) tiles = (load_seq(p.a, b).n + per_tile - 1) / per_tile;
+      const int64_t mine = block_prefix<W>(tiles, sh.scan, &round);
+      sh.seq_first[tid] = mine;
+      if (tid == 0) sh.seq_first[C::kThreads] = round;
+      __syncthreads();
+      for (int64_t f0 = 0; f0 < round; f0 += C::kThreads) {
+        const int64_t f = f0 + tid;
+        int count = 0, first, at = 0, i = 0;
+        Seq q = {};
+        if (f < round) {
+          int hi = C::kThreads;  // the last sequence of the round whose first tile is at or before f
+          while (hi - at > 1) {
+            const int mid = (at + hi) >> 1;
+            if (sh.seq_first[mid] <= f) at = mid;
+            else hi = mid;
+          }
+          i = (int)(f - sh.seq_first[at]);
+          q = load_seq(p.a, b0 + at);
+          tile_blocks<D>(p.a, q, i, per_tile, &first, &count);
+          if (pass == 0 && count == 0 && f % gridDim.x == blockIdx.x) {  // no key: its rows are zeros
+            const int r1 = min(q.n, (i + 1) * per_tile);
+            for (int r = i * per_tile; r < r1; ++r) {
+              uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + r) * p.a.ldo);
+              for (int e = 0; e < p.a.q_heads * D / 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        int64_t all;
+        const int64_t before = (done + block_prefix<W>(count, sh.scan, &all)) * Hkv;
+        if (pass == 1 && cta0 >= before && cta0 < before + (int64_t)count * Hkv) {
+          sh.b = (int)(b0 + at);
+          sh.i = i;
+          sh.before = before;
+        }
+        done += all;
+      }
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = done * Hkv;
+      G = min((int64_t)p.G, total);
+      if (blockIdx.x < G) {
+        cta0 = blockIdx.x * total / G;
+        cta1 = (blockIdx.x + 1) * total / G;
+      } else {
+        break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  bool ok = true;
+
+  if (cta0 < cta1) {
+    Walk<D> w;
+    w.start(p, sh, cta0, cta1);
+    if (warp < C::kSoftWarps) {
+      // ------------------------------------------------------------ softmax
+      const int X = warp >> 2, r = tid & 127;           // row tile, row of it
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tO = tmem + lanes + C::kTmemO + X * D;
+      const uint32_t qrow = sQ + X * C::kQBytes + r * 128;
+      uint32_t it = 0, segs = 0, joins = 0;             // blocks, segments, joins of this row tile
+      do {
+        const bool mine_seg = X < w.row_tiles(p);
+        const int inner = r % p.a.group, tok = X * p.tokens + r / p.a.group, idx = w.i * per_tile + tok;
+        const bool live = mine_seg && r < p.tokens * p.a.group && idx < w.q.n;
+        const int head = w.h * p.a.group + inner;
+        const int64_t t = (int64_t)w.q.s0 + idx;
+        const int64_t pos = (int64_t)w.q.len - w.q.n + idx;
+        // keys [row_lo, row_hi) are those that the row sees
+        const int row_hi = live ? (int)max(pos + 1, (int64_t)0) : 0x7FFFFFFF;
+        const int row_lo = live && p.a.window > 0 ? (int)max(pos + 1 - p.a.window, (int64_t)0) : 0;
+        float m = -INFINITY, l = 0.0f;
+        bool any = false;
+        if (mine_seg) {
+          // ---- Q
+          float mul;
+          const bool negative = p.a.scale * p.a.cache.k_scale[w.h] < 0.0f;
+          {
+            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.a.q) +
+                                                              (live ? t * p.a.ldq + (int64_t)head * D : 0));
+            int mx = 0;
+            if (live) {
+#pragma unroll 8
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = src[c];
+                mx = max(mx, act_maxmag8(reinterpret_cast<const uint32_t*>(&v)));
+              }
+            }
+            const int pw = act_pow2(mx);
+            mul = p.a.scale * kLog2e * p.a.cache.k_scale[w.h] * pow2f(pw);
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (live) v = src[c];
+              const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&v), pw);
+              st_shared_v4(qrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), f.x, f.y, f.z, f.w);
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full + 8 * X);
+          const bool idle = !__any_sync(0xffffffffu, live);  // no row of this warp counts
+          // pages of the block's tiles that are not there, a block ahead
+          auto pages_of = [&](int blk) -> bool {
+            if (lane >= KB / 16) return true;
+            const int64_t k = (int64_t)(w.first + blk) * KB + lane * 16;
+            if (k >= w.q.len) return true;
+            const int page = __ldg(p.a.tables + w.b * p.a.ldt + (k >> p.a.cache.page_shift));
+            return page >= 0 && page < p.a.cache.pages;
+          };
+          bool page_ok = pages_of(w.at);
+          for (int blk = w.at; blk < w.end; ++blk, ++it) {
+            const uint32_t sbuf = SB == 2 ? (it & 1) : X, sphase = SB == 2 ? (it >> 1) & 1 : it & 1;
+            const uint32_t tS = tmem + lanes + sbuf * KB;
+            const uint32_t gone = ~__ballot_sync(0xffffffffu, page_ok) & ((1u << (KB / 16)) - 1);
+            if (blk + 1 < w.end) page_ok = pages_of(blk + 1);
+            const int64_t k0 = (int64_t)(w.first + blk) * KB;
+            // columns [lo, hi) that the row sees
+            const int hi = (int)min((int64_t)KB, max((int64_t)row_hi - k0, (int64_t)0));
+            const int lo = (int)min((int64_t)KB, max((int64_t)row_lo - k0, (int64_t)0));
+            const bool edge = __any_sync(0xffffffffu, hi < KB || lo > 0) || gone;
+            if (!(ok = pf_warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
+            tc_fence_after();
+            if (!idle) {
+              auto mask = [&](uint32_t (&v)[32], int c) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int col = c * 32 + e;
+                  if (col < lo || col >= hi || ((gone >> (col >> 4)) & 1)) v[e] = 0xFF800000u;
+                }
+              };
+              float top = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < KB / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tS + c * 32, v);
+                if (edge) mask(v, c);
+                if (!negative) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                } else {  // the largest score is the least product (a masked one stays out)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    top = fmaxf(top, v[e] == 0xFF800000u ? -INFINITY : -__uint_as_float(v[e]));
+                }
+              }
+              any |= lo < hi && !gone;
+              if (gone) {
+                for (int g = 0; g < KB / 16; ++g)
+                  any |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
+              }
+              const float mx = top == -INFINITY ? top : top * fabsf(mul);
+              const float mn = (m == -INFINITY || mx > m + kSlack) ? fmaxf(m, mx) : m;
+              if (blk > w.at && __any_sync(0xffffffffu, mn > m)) {
+                if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+                tc_fence_after();
+                const float f = mn > m ? fast_exp2(m - mn) : 1.0f;
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t v[32];
+                  tmem_ld32(tO + c * 32, v);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                  tmem_st32(tO + c * 32, v);
+                }
+              }
+              m = mn;
+              const float off = kTileBias - (m == -INFINITY ? 0.0f : m);
+#pragma unroll
+              for (int c = 0; c < KB / 32; ++c) {
+                uint32_t v[32], pk[16];
+                tmem_ld32(tS + c * 32, v);
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float a = fast_exp2(fmaf(__uint_as_float(v[e]), mul, off));
+                  float b = fast_exp2(fmaf(__uint_as_float(v[e + 1]), mul, off));
+                  if (edge) {
+                    const int col = c * 32 + e;
+                    const bool g = (gone >> (col >> 4)) & 1;
+                    if (col < lo || col >= hi || g) a = 0.0f;
+                    if (col + 1 < lo || col + 1 >= hi || g) b = 0.0f;
+                  }
+                  sum0 += a;
+                  sum1 += b;
+                  pk[e >> 1] = pack_half2(a, b);
+                }
+                l += sum0 + sum1;
+                tmem_st16(tS + c * 16, pk);
+              }
+              tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 8 * sbuf);
+          }
+          if (!ok) break;
+          if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+          tc_fence_after();
+          ++segs;
+        }
+        const bool whole = w.whole();
+        float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w.at == 0)) * C::kPartFloats;
+        uint32_t lost = 0;
+        if (live && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
+          lost = nan_columns<D>(p.a, w.b, w.h, max(row_lo, (w.first + w.at) * KB),
+                                (int)min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB));
+        auto value = [&](uint32_t v, int col) {
+          return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
+        };
+        if (mine_seg) {
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (live ? t * p.a.ldo + (int64_t)head * D : 0);
+          const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kTileBias) : 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tO + c * 32, v);
+            if (live && whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int col = c * 32 + e + 2 * k;
+                  const float x = any ? value(v[e + 2 * k], col) * f : 0.0f, y = any ? value(v[e + 2 * k + 1], col) * f : 0.0f;
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(x, y);
+                  o[k] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+                *reinterpret_cast<uint4*>(dst + c * 32 + e) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            } else if (live) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const int col = c * 32 + e;
+                __stcg(reinterpret_cast<float4*>(part) + (int64_t)(col / 4) * C::kRows + X * 128 + r,
+                       make_float4(value(v[e], col), value(v[e + 1], col), value(v[e + 2], col), value(v[e + 3], col)));
+              }
+            }
+            __syncwarp();  // the next load from TMEM takes the whole warp
+          }
+          if (live && !whole) {
+            float* st = part + C::kRows * D + X * 128 + r;
+            __stcg(st, m);
+            __stcg(st + C::kRows, l);
+            __stcg(st + 2 * C::kRows, any ? 1.0f : 0.0f);
+          }
+        }
+        if (!whole) {
+          // ---- a part: the last of the tile's CTAs joins them, in the order of the line
+          const int64_t seg1 = w.seg0 + w.count;
+          const int64_t c0 = ((w.seg0 + 1) * G - 1) / total, c1 = (seg1 * G - 1) / total;
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(joined);
+          if (warp == 0) {
+            if (!(ok = pf_warp_wait(joined, joins & 1, abort, p.wait_ns))) break;
+            if (lane == 0) {
+              uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + 256) + c0;
+              __threadfence();
+              const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
+              if (last) *count = 0;  // for the next call
+              __threadfence();
+              *reinterpret_cast<volatile int*>(&sh.last) = last;
+              mbar_arrive(told);
+            }
+            __syncwarp();
+          }
+          if (!(ok = pf_warp_wait(told, joins & 1, abort, p.wait_ns))) break;
+          ++joins;
+          if (*reinterpret_cast<volatile int*>(&sh.last)) {
+            const int n = (int)(c1 - c0) + 1;
+            // CTA c0's part is in its slot 1, the others' in their slot 0
+            auto part_of = [&](int k) { return p.parts + (2 * (c0 + k) + (k == 0)) * (int64_t)C::kPartFloats; };
+            if (live) {
+              float mt = -INFINITY, lt = 0.0f;
+              bool at = false;
+              for (int k = 0; k < n; ++k) {
+                const float* st = part_of(k) + C::kRows * D + X * 128 + r;
+                mt = fmaxf(mt, __ldcg(st));
+                at |= __ldcg(st + 2 * C::kRows) != 0.0f;
+              }
+              const float ms = mt == -INFINITY ? 0.0f : mt;
+              for (int k = 0; k < n; ++k) {
+                const float* st = part_of(k) + C::kRows * D + X * 128 + r;
+                lt += fast_exp2(__ldcg(st) - ms) * __ldcg(st + C::kRows);
+              }
+              const float f = at ? out_factor(p.a, head, w.h, mt, lt, kTileBias) : 0.0f;
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + t * p.a.ldo + (int64_t)head * D;
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                float4 o[4] = {};
+                for (int k = 0; k < n; ++k) {
+                  const float* q = part_of(k);
+                  const float wk = fast_exp2(__ldcg(q + C::kRows * D + X * 128 + r) - ms);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + (int64_t)(c * 4 + e) * C::kRows + X * 128 + r);
+                    o[e].x += wk * v.x, o[e].y += wk * v.y, o[e].z += wk * v.z, o[e].w += wk * v.w;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  float x[8] = {o[e].x, o[e].y, o[e].z, o[e].w, o[e + 1].x, o[e + 1].y, o[e + 1].z, o[e + 1].w};
+                  uint32_t b[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(at ? x[2 * k] * f : 0.0f, at ? x[2 * k + 1] * f : 0.0f);
+                    b[k] = *reinterpret_cast<const uint32_t*>(&h2);
+                  }
+                  *reinterpret_cast<uint4*>(dst + c * 16 + e * 4) = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+              }
+            }
+          }
+        }
+      } while (w.next(p));
+    } else if (warp < C::kWarpV) {
+      // ------------------------------------------------------------ K to f16
+      const int kw = warp - C::kWarpK, mu = lane & 15, half = lane >> 4;
+      const int tok = kv_mma_token(mu);
+      uint4 code[2][C::kJobs][2];
+      uint2 sc[2][C::kJobs];
+      // the tile (of 16 tokens) of job j and this lane, counted in the block
+      auto tile_of = [&](int j) { return D == 64 ? 2 * kw + half : D == 128 ? kw + 4 * j : kw; };
+      Walk<D> ld = w;
+      int lblk = ld.at;
+      bool more = true;
+      int page[C::kJobs];
+      auto fetch = [&]() {  // pages of the block to be loaded next
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
+          page[j] = k < ld.q.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (k >> p.a.cache.page_shift)) : -1;
+        }
+      };
+      auto load = [&](int set) {
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          code[set][j][0] = code[set][j][1] = make_uint4(0, 0, 0, 0);
+          sc[set][j] = make_uint2(0, 0);
+          if (page[j] >= 0 && page[j] < p.a.cache.pages) {
+            const int in = (int)(((int64_t)(ld.first + lblk) * KB + tile_of(j) * 16) & (p.a.cache.page_size - 1));
+            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, in);
+            const int at = D == 64 ? mu * 32 : (D == 256 ? j * 1024 : 0) + mu * 64 + half * 32;
+            const int sat = 8 * D + (D == 64 ? (mu & 7) * 8 : (D == 256 ? j * 128 : 0) + (mu & 7) * 16 + half * 8);
+            code[set][j][0] = *reinterpret_cast<const uint4*>(tile + at);
+            code[set][j][1] = *reinterpret_cast<const uint4*>(tile + at + 16);
+            sc[set][j] = *reinterpret_cast<const uint2*>(tile + sat);
+          }
+        }
+        if (++lblk == ld.end) {
+          more = ld.next(p);
+          lblk = ld.at;
+        }
+        if (more) fetch();
+      };
+      fetch();
+      load(0);
+      uint32_t it = 0;
+      const int64_t blocks = cta1 - cta0;
+      auto step = [&](int set) -> bool {
+        if (more) load(set ^ 1);
+        const uint32_t stage = it & 1;
+        if (!pf_warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          const uint32_t s4 = D == 64 ? __byte_perm(sc[set][j].x, sc[set][j].y, mu >> 3 ? 0x7531 : 0x6420)
+                                      : __byte_perm(sc[set][j].x, sc[set][j].y, mu >> 3 ? 0x7632 : 0x5410);
+          const uint32_t s01 = e4m3x2_to_f16x2(s4), s23 = e4m3x2_to_f16x2(s4 >> 16);
+          const uint32_t s[4] = {bcast_lo(s01), bcast_hi(s01), bcast_lo(s23), bcast_hi(s23)};
+          const int n = tile_of(j) * 16 + tok, sub = D == 64 ? 0 : D == 128 ? half : 2 * j + half;
+          const uint32_t row = sK + stage * C::kKvBytes + sub * (KB * 128) + n * 128;
+          const uint32_t wd[8] = {code[set][j][0].x, code[set][j][0].y, code[set][j][0].z, code[set][j][0].w,
+                                  code[set][j][1].x, code[set][j][1].y, code[set][j][1].z, code[set][j][1].w};
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t f[4];
+            e2m1x8_to_f16x8(wd[c], f[0], f[1], f[2], f[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = hmul2_u32(f[e], s[c >> 1]);
+            st_shared_v4(row + ((c ^ (n & 7)) << 4), f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + 8 * stage);
+        ++it;
+        return true;
+      };
+      for (int64_t n = 0; n < blocks; n += 2) {  // two steps: the register sets are named, not indexed
+        if (!(ok = step(0))) break;
+        if (n + 1 < blocks && !(ok = step(1))) break;
+      }
+    } else if (warp < C::kWarpMma) {
+      // ------------------------------------------------------------ V to f16, turned
+      const int vw = warp - C::kWarpV;
+      const int half = D == 64 ? (lane >> 3) & 1 : lane >> 4, o = D == 64 ? lane & 7 : lane & 15;
+      uint32_t code[2][C::kJobs][8];
+      uint4 sc[2][C::kJobs];
+      int nvalid[2][C::kJobs];   // of the lane's 8 tokens
+      int segno[2];
+      auto tile_of = [&](int j) { return D == 64 ? 2 * vw + (lane >> 4) : D == 128 ? vw + 4 * j : vw; };
+      Walk<D> ld = w;
+      int lblk = ld.at;
+      bool more = true;
+      int page[C::kJobs];
+      auto fetch = [&]() {
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
+          page[j] = k < ld.q.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (k >> p.a.cache.page_shift)) : -1;
+        }
+      };
+      auto load = [&](int set) {
+        segno[set] = ld.no;
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
+          sc[set][j] = make_uint4(0, 0, 0, 0);
+          nvalid[set][j] = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) code[set][j][i] = 0;
+          if (page[j] >= 0 && page[j] < p.a.cache.pages) {
+            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, (int)(k & (p.a.cache.page_size - 1)));
+            const uint8_t* at = tile + 9 * D + (D == 256 ? j * 1024 : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 8 * half + i;
+              code[set][j][i] = *reinterpret_cast<const uint32_t*>(at + (D == 64 ? r * 32 + o * 4 : r * 64 + ((o * 4) ^ (((i >> 1) & 1) * 32))));
+            }
+            sc[set][j] = *reinterpret_cast<const uint4*>(tile + 17 * D + ((D == 256 ? j * 8 : 0) + (o >> 1)) * 16);
+            nvalid[set][j] = (int)min((int64_t)8, max((int64_t)ld.q.len - k - 8 * half, (int64_t)0));
+          }
+        }
+        if (++lblk == ld.end) {
+          more = ld.next(p);
+          lblk = ld.at;
+        }
+        if (more) fetch();
+      };
+      fetch();
+      load(0);
+      const int rot = o & 3, odd = (o >> 2) & 1;
+      const uint32_t rsel = rot == 0 ? 0x3210 : rot == 1 ? 0x0321 : rot == 2 ? 0x1032 : 0x2103;
+      uint32_t it = 0;
+      const int64_t blocks = cta1 - cta0;
+      auto step = [&](int set) -> bool {
+        if (more) load(set ^ 1);
+        const uint32_t stage = it & 1;
+        if (!pf_warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
+#pragma unroll
+        for (int j = 0; j < C::kJobs; ++j) {
+          // scales of the lane's tokens 0..3 and 4..7, a byte each
+          const uint4 sw = sc[set][j];
+          const uint32_t s0 = half ? 0x62 : 0x40, s1 = half ? 0x73 : 0x51;
+          uint32_t q[2] = {__byte_perm(__byte_perm(sw.x, sw.y, s0), __byte_perm(sw.z, sw.w, s0), 0x5410),
+                           __byte_perm(__byte_perm(sw.x, sw.y, s1), __byte_perm(sw.z, sw.w, s1), 0x5410)};
+          const int nv = nvalid[set][j];
+          if (nv < 8) {  // places behind the last key hold anything
+            q[1] = nv > 4 ? q[1] & ((1u << (8 * (nv - 4))) - 1) : 0u;
+            if (nv < 4) q[0] &= (1u << (8 * nv)) - 1;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t bad = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            if (bad) {
+              q[k] &= ~((bad >> 7) * 0xFFu);
+              *reinterpret_cast<volatile int*>(&sh.nan_seg[segno[set] & 7]) = segno[set] + 1;
+            }
+          }
+          uint32_t x[4][4], y[4][4];  // [d][pair of tokens]
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            constexpr uint32_t M = 0x0F0F0F0Fu;
+            const uint32_t a = code[set][j][2 * i], b = code[set][j][2 * i + 1];
+            const uint32_t even = __byte_perm((a & M) | ((b << 4) & ~M), 0, rsel);
+            const uint32_t oddw = __byte_perm(((a >> 4) & M) | (b & ~M), 0, rsel);
+            const uint32_t u = odd ? oddw : even, v = odd ? even : oddw;
+            const uint32_t s = e4m3x2_to_f16x2(q[i >> 1] >> (16 * (i & 1)));
+            uint32_t f[4], g[4];
+            e2m1x8_to_f16x8(u, f[0], f[1], f[2], f[3]);
+            e2m1x8_to_f16x8(v, g[0], g[1], g[2], g[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e][i] = hmul2_u32(f[e], s);
+              y[e][i] = hmul2_u32(g[e], s);
+            }
+          }
+          const int ti = tile_of(j), chunk = (ti & 3) * 2 + half;
+          const uint32_t at = sV + stage * C::kKvBytes + (ti >> 2) * (D * 128) + (D == 256 ? j * 128 * 128 : 0) + o * 1024;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d0 = 2 * ((e + rot) & 3) + odd, d1 = 2 * ((e + rot) & 3) + 1 - odd;
+            st_shared_v4(at + d0 * 128 + ((chunk ^ d0) << 4), x[e][0], x[e][1], x[e][2], x[e][3]);
+            st_shared_v4(at + d1 * 128 + ((chunk ^ d1) << 4), y[e][0], y[e][1], y[e][2], y[e][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + 8 * stage);
+        ++it;
+        return true;
+      };
+      for (int64_t n = 0; n < blocks; n += 2) {
+        if (!(ok = step(0))) break;
+        if (n + 1 < blocks && !(ok = step(1))) break;
+      }
+    } else if (elect_one()) {
+      // ------------------------------------------------------------ the products
+      constexpr uint32_t ids = idesc_f16(KB), ido = idesc_f16(D);
+      uint32_t it = 0, done[2] = {0, 0}, segs[2] = {0, 0};
+      auto qk = [&](int X, uint32_t n, uint32_t sbuf) {  // scores of block n (of the CTA's)
+        const uint32_t ks = sK + (n & 1) * C::kKvBytes;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint64_t a = desc_sw128(sQ + X * C::kQBytes + c * 16384), b = desc_sw128(ks + c * (KB * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f16(tmem + sbuf * KB, a + 2 * kk, b + 2 * kk, ids, c > 0 || kk > 0);
+        }
+        mma_commit(s_full + 8 * sbuf);
+      };
+      auto pv = [&](int X, uint32_t n, uint32_t sbuf, bool add) {
+        const uint32_t vs = sV + (n & 1) * C::kKvBytes;
+#pragma unroll
+        for (int c = 0; c < KB / 64; ++c) {
+          const uint64_t b = desc_sw128(vs + c * (D * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ta(tmem + C::kTmemO + X * D, tmem + sbuf * KB + (c * 4 + kk) * 8, b + 2 * kk, ido, add || c > 0 || kk > 0);
+        }
+        mma_commit(pv_done + 8 * X);
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && pf_wait(bar, parity, abort, p.wait_ns);
+        return ok;
+      };
+      do {
+        const int rt = w.row_tiles(p), n = w.end - w.at;
+        if (!wait(k_full + 8 * (it & 1), (it >> 1) & 1)) break;
+        for (int X = 0; X < rt; ++X) {
+          if (!wait(q_full + 8 * X, segs[X] & 1)) break;
+          ++segs[X];
+          tc_fence_after();
+          qk(X, it, SB == 2 ? (done[0] & 1) : X);
+        }
+        if (!ok) break;
+        mma_commit(k_empty + 8 * (it & 1));
+        for (int j = 0; j < n; ++j, ++it) {
+          const bool on = j + 1 < n;
+          const uint32_t nx = it + 1;
+          if (SB == 2 && on) {
+            if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
+            tc_fence_after();
+            qk(0, nx, (done[0] + 1) & 1);
+            mma_commit(k_empty + 8 * (nx & 1));
+          }
+          for (int X = 0; X < rt; ++X) {
+            const uint32_t sbuf = SB == 2 ? (done[0] & 1) : X;
+            if (!wait(p_full + 8 * sbuf, (SB == 2 ? done[0] >> 1 : done[X]) & 1)) break;
+            if (X == 0 && !wait(v_full + 8 * (it & 1), (it >> 1) & 1)) break;
+            tc_fence_after();
+            pv(X, it, sbuf, j > 0);
+            ++done[X];
+            if (SB == 1 && on) {
+              if (X == 0 && !wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
+              tc_fence_after();
+              qk(X, nx, X);
+            }
+          }
+          if (!ok) break;
+          mma_commit(v_empty + 8 * (it & 1));
+          if (SB == 1 && on) mma_commit(k_empty + 8 * (nx & 1));
+        }
+        if (!ok) break;
+      } while (w.next(p));
+      // every product issued has completed once this arrives
+      mma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
+    }
+    if (!ok && (lane == 0 || warp == C::kWarpMma)) atomicExch(reinterpret_cast<int*>(p.a.workspace), 5);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == C::kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t go(TileParams p, cudaStream_t s) {
+  using C = TileCfg<D>;
+  static int done[64];
+  constexpr size_t bytes = C::kOffMeta + sizeof(TileShared) + 1024;
+  static_assert(bytes <= 232448, "shared memory");
+  if (cudaError_t e = set_up_kernel(k_attend_tile<D>, bytes, done)) return e;
+  k_attend_tile<D><<<p.G, C::kThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_tile_parts_bytes(int head_dim) {
+  const size_t f = head_dim == 64 ? TileCfg<64>::kPartFloats : head_dim == 128 ? TileCfg<128>::kPartFloats : TileCfg<256>::kPartFloats;
+  return 2 * (size_t)kMaxAttendGrid * f * 4;
+}
+
+cudaError_t launch_attend_tile(const AttendLaunch& L, int head_dim, cudaStream_t s) {
+  TileParams p;
+  p.a = L;
+  p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
+  p.tokens = 128 / L.group;
+  p.parts = reinterpret_cast<float*>(L.workspace + kAttendCleared);
+  p.wait_ns = kWaitNs;
+  return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
+}
+
+}  // namespace vt
