@@ -44,7 +44,10 @@ struct TileCfg {
   static constexpr int kSBufs = D == 256 ? 2 : 1;         // score buffers of a row tile
   static constexpr int kKeys = D == 256 ? 64 : 128;       // keys of a block
   static constexpr int kSoftWarps = 4 * kRowTiles;
-  static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + 4;
+  // 16 warps for two row tiles: a 17th would leave every thread 96 registers, and the softmax
+  // spills with fewer than 128 (into an L1 that the shared memory leaves next to nothing).
+  static constexpr int kVWarps = kRowTiles == 2 ? 3 : 4;
+  static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kVWarps;
   static constexpr int kThreads = (kWarpMma + 1) * 32;
   static constexpr int kQBytes = 128 * D * 2;             // a row tile
   static constexpr int kKvBytes = kKeys * D * 2;          // a block of K or V
@@ -52,7 +55,9 @@ struct TileCfg {
   static constexpr int kOffK = kRowTiles * kQBytes;
   static constexpr int kOffV = kOffK + kStages * kKvBytes;
   static constexpr int kOffMeta = kOffV + kStages * kKvBytes;
-  static constexpr int kJobs = D == 64 ? 1 : 2;           // 64 values per lane each, of a K or V warp and block
+  // Conversion goes in jobs of 64 values per lane: 16 tokens of 128 columns, or 32 of 64.
+  static constexpr int kAllJobs = kKeys * D / 2048;       // of a block of K or V
+  static constexpr int kKJobs = kAllJobs / 4, kVJobs = (kAllJobs + kVWarps - 1) / kVWarps;
   // TMEM columns: scores (P over them), then O
   static constexpr int kTmemO = 256;
   static constexpr int kRows = 128 * kRowTiles;
@@ -61,8 +66,9 @@ struct TileCfg {
 
 struct TileShared {
   int64_t scan[32];
-  int64_t seq_first[32 * 17 + 1];
-  int64_t u0, before;  // this CTA's first unit; the units before its tile
+  int64_t seq_first[32 * 16 + 1];
+  int64_t before;      // the units before this CTA's first tile
+  int64_t G, total;    // CTAs in use, units in all
   int b, i;            // its tile
   int last;
   int nan_seg[8];
@@ -178,6 +184,30 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
   tmem_st16(taddr, a);
   tmem_st16(taddr + 16, b);
 }
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
@@ -219,7 +249,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       mbar_init(q_full + 8 * i, 4);
       mbar_init(k_full + 8 * i, 4);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, 4);
+      mbar_init(v_full + 8 * i, C::kVWarps);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
@@ -291,6 +321,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       }
     }
   }
+  if (tid == 0) {
+    sh.G = G;
+    sh.total = total;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -305,45 +339,51 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       const int X = warp >> 2, r = tid & 127;           // row tile, row of it
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t tO = tmem + lanes + C::kTmemO + X * D;
-      const uint32_t qrow = sQ + X * C::kQBytes + r * 128;
+      const uint32_t qwarp = sQ + X * C::kQBytes + (warp & 3) * 4096;  // this warp's 32 rows
+      constexpr int LR = D / 8, RI = 32 / LR;           // lanes a row takes, rows a load takes
       uint32_t it = 0, segs = 0, joins = 0;             // blocks, segments, joins of this row tile
       do {
         const bool mine_seg = X < w.row_tiles(p);
         const int inner = r % p.a.group, tok = X * p.tokens + r / p.a.group, idx = w.i * per_tile + tok;
         const bool live = mine_seg && r < p.tokens * p.a.group && idx < w.q.n;
         const int head = w.h * p.a.group + inner;
-        const int64_t t = (int64_t)w.q.s0 + idx;
-        const int64_t pos = (int64_t)w.q.len - w.q.n + idx;
+        const int64_t t = w.q.s0 + idx;
+        const int seen = w.q.len - w.q.n + idx + 1;       // keys up to the row's own
         // keys [row_lo, row_hi) are those that the row sees
-        const int row_hi = live ? (int)max(pos + 1, (int64_t)0) : 0x7FFFFFFF;
-        const int row_lo = live && p.a.window > 0 ? (int)max(pos + 1 - p.a.window, (int64_t)0) : 0;
+        const int row_hi = live ? max(seen, 0) : 0x7FFFFFFF;
+        const int row_lo = live && p.a.window > 0 && p.a.window < row_hi ? row_hi - (int)p.a.window : 0;
         float m = -INFINITY, l = 0.0f;
         bool any = false;
         if (mine_seg) {
           // ---- Q
-          float mul;
+          // LR lanes take a row 16 bytes each, so that a load meets few lines; a lane keeps the power of
+          // two of its own row
           const bool negative = p.a.scale * p.a.cache.k_scale[w.h] < 0.0f;
-          {
-            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.a.q) +
-                                                              (live ? t * p.a.ldq + (int64_t)head * D : 0));
-            int mx = 0;
-            if (live) {
-#pragma unroll 8
-              for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = src[c];
-                mx = max(mx, act_maxmag8(reinterpret_cast<const uint32_t*>(&v)));
-              }
+          const int64_t from = live ? t * p.a.ldq + (int64_t)head * D : -1;
+          int pw = 0;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 8 * RI) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t f = __shfl_sync(0xffffffffu, from, i0 + i * RI + lane / LR);
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (f >= 0) v[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.a.q) + f + (lane % LR) * 8);
             }
-            const int pw = act_pow2(mx);
-            mul = p.a.scale * kLog2e * p.a.cache.k_scale[w.h] * pow2f(pw);
-#pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (live) v = src[c];
-              const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&v), pw);
-              st_shared_v4(qrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), f.x, f.y, f.z, f.w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              int mx = act_maxmag8(reinterpret_cast<const uint32_t*>(&v[i]));
+#pragma unroll
+              for (int k = 1; k < LR; k <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+              const int pr = act_pow2(mx), row = i0 + i * RI + lane / LR, c = lane % LR;
+              const int mine = __shfl_sync(0xffffffffu, pr, (lane % RI) * LR);
+              if (lane / RI == i0 / RI + i) pw = mine;
+              const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&v[i]), pr);
+              st_shared_v4(qwarp + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), f.x, f.y, f.z, f.w);
             }
           }
+          float mul = p.a.scale * kLog2e * p.a.cache.k_scale[w.h] * pow2f(pw);
+          if (mul == 0.0f) mul = 1e-38f;  // every score 0, a masked one (-inf) stays out
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -352,7 +392,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           // pages of the block's tiles that are not there, a block ahead
           auto pages_of = [&](int blk) -> bool {
             if (lane >= KB / 16) return true;
-            const int64_t k = (int64_t)(w.first + blk) * KB + lane * 16;
+            const int k = (w.first + blk) * KB + lane * 16;
             if (k >= w.q.len) return true;
             const int page = __ldg(p.a.tables + w.b * p.a.ldt + (k >> p.a.cache.page_shift));
             return page >= 0 && page < p.a.cache.pages;
@@ -363,42 +403,53 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             const uint32_t tS = tmem + lanes + sbuf * KB;
             const uint32_t gone = ~__ballot_sync(0xffffffffu, page_ok) & ((1u << (KB / 16)) - 1);
             if (blk + 1 < w.end) page_ok = pages_of(blk + 1);
-            const int64_t k0 = (int64_t)(w.first + blk) * KB;
+            const int k0 = (w.first + blk) * KB;
             // columns [lo, hi) that the row sees
-            const int hi = (int)min((int64_t)KB, max((int64_t)row_hi - k0, (int64_t)0));
-            const int lo = (int)min((int64_t)KB, max((int64_t)row_lo - k0, (int64_t)0));
+            const int hi = min(KB, max(row_hi - k0, 0));
+            const int lo = min(KB, max(row_lo - k0, 0));
             const bool edge = __any_sync(0xffffffffu, hi < KB || lo > 0) || gone;
             if (!(ok = pf_warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
             tc_fence_after();
             if (!idle) {
+              // Masked scores become -inf (of the sign that the products take).
+              const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
               auto mask = [&](uint32_t (&v)[32], int c) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   const int col = c * 32 + e;
-                  if (col < lo || col >= hi || ((gone >> (col >> 4)) & 1)) v[e] = 0xFF800000u;
+                  if (col < lo || col >= hi || ((gone >> (col >> 4)) & 1)) v[e] = out;
                 }
               };
-              float top = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < KB / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(tS + c * 32, v);
-                if (edge) mask(v, c);
+              uint32_t v[2][32];
+              float top[2] = {-INFINITY, -INFINITY};
+              auto highest = [&](uint32_t (&x)[32], int c) {
+                if (edge) mask(x, c);
                 if (!negative) {
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
-                } else {  // the largest score is the least product (a masked one stays out)
+                  for (int e = 0; e < 32; e += 4) {
+                    top[0] = max3(top[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    top[1] = max3(top[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                  }
+                } else {
 #pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    top = fmaxf(top, v[e] == 0xFF800000u ? -INFINITY : -__uint_as_float(v[e]));
+                  for (int e = 0; e < 32; ++e) top[0] = fmaxf(top[0], -__uint_as_float(x[e]));
                 }
+              };
+              tmem_ld32_issue(tS, v[0]);
+#pragma unroll
+              for (int c = 0; c < KB / 32; ++c) {
+                tmem_ld_wait(v[c & 1]);
+                if (c + 1 < KB / 32) tmem_ld32_issue(tS + (c + 1) * 32, v[(c + 1) & 1]);
+                highest(v[c & 1], c);
               }
+              tmem_ld32_issue(tS, v[0]);  // again, for the probabilities
+              const float best = fmaxf(top[0], top[1]);
               any |= lo < hi && !gone;
               if (gone) {
                 for (int g = 0; g < KB / 16; ++g)
                   any |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
               }
-              const float mx = top == -INFINITY ? top : top * fabsf(mul);
+              const float mx = best == -INFINITY ? best : best * fabsf(mul);
               const float mn = (m == -INFINITY || mx > m + kSlack) ? fmaxf(m, mx) : m;
               if (blk > w.at && __any_sync(0xffffffffu, mn > m)) {
                 if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
@@ -416,28 +467,29 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               }
               m = mn;
               const float off = kTileBias - (m == -INFINITY ? 0.0f : m);
+              const uint64_t mul2 = pair(mul, mul), off2 = pair(off, off);
+              uint64_t sum[2] = {0, 0};
 #pragma unroll
               for (int c = 0; c < KB / 32; ++c) {
-                uint32_t v[32], pk[16];
-                tmem_ld32(tS + c * 32, v);
-                float sum0 = 0.0f, sum1 = 0.0f;
+                uint32_t(&x)[32] = v[c & 1];
+                tmem_ld_wait(x);
+                if (c + 1 < KB / 32) tmem_ld32_issue(tS + (c + 1) * 32, v[(c + 1) & 1]);
+                if (edge) mask(x, c);
+                uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                  float a = fast_exp2(fmaf(__uint_as_float(v[e]), mul, off));
-                  float b = fast_exp2(fmaf(__uint_as_float(v[e + 1]), mul, off));
-                  if (edge) {
-                    const int col = c * 32 + e;
-                    const bool g = (gone >> (col >> 4)) & 1;
-                    if (col < lo || col >= hi || g) a = 0.0f;
-                    if (col + 1 < lo || col + 1 >= hi || g) b = 0.0f;
-                  }
-                  sum0 += a;
-                  sum1 += b;
+                  float a, b;
+                  split(fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2, off2), a, b);
+                  a = fast_exp2(a);
+                  b = fast_exp2(b);
+                  sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, b));
                   pk[e >> 1] = pack_half2(a, b);
                 }
-                l += sum0 + sum1;
                 tmem_st16(tS + c * 16, pk);
               }
+              float la, lb;
+              split(add2(sum[0], sum[1]), la, lb);
+              l += la + lb;
               tmem_st_wait();
             }
             tc_fence_before();
@@ -459,13 +511,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
         };
         if (mine_seg) {
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (live ? t * p.a.ldo + (int64_t)head * D : 0);
           const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kTileBias) : 0.0f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(tO + c * 32, v);
-            if (live && whole) {
+            if (whole) {  // to the place of Q, whose products are done
 #pragma unroll
               for (int e = 0; e < 32; e += 8) {
                 uint32_t o[4];
@@ -476,7 +527,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                   const __nv_bfloat162 h2 = __floats2bfloat162_rn(x, y);
                   o[k] = *reinterpret_cast<const uint32_t*>(&h2);
                 }
-                *reinterpret_cast<uint4*>(dst + c * 32 + e) = make_uint4(o[0], o[1], o[2], o[3]);
+                const int chunk = c * 4 + e / 8;
+                st_shared_v4(qwarp + (chunk >> 3) * 16384 + lane * 128 + (((chunk & 7) ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
               }
             } else if (live) {
 #pragma unroll
@@ -488,6 +540,17 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             __syncwarp();  // the next load from TMEM takes the whole warp
           }
+          if (whole) {
+            const int64_t to = live ? t * p.a.ldo + (int64_t)head * D : -1;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += RI) {
+              const int row = i + lane / LR, c = lane % LR;
+              const int64_t at = __shfl_sync(0xffffffffu, to, row);
+              const int4 o = ld_shared_v4(qwarp + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+              if (at >= 0) *reinterpret_cast<int4*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + at + c * 8) = o;
+            }
+            __syncwarp();
+          }
           if (live && !whole) {
             float* st = part + C::kRows * D + X * 128 + r;
             __stcg(st, m);
@@ -498,7 +561,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         if (!whole) {
           // ---- a part: the last of the tile's CTAs joins them, in the order of the line
           const int64_t seg1 = w.seg0 + w.count;
-          const int64_t c0 = ((w.seg0 + 1) * G - 1) / total, c1 = (seg1 * G - 1) / total;
+          const int64_t total_units = *reinterpret_cast<volatile int64_t*>(&sh.total), ctas = *reinterpret_cast<volatile int64_t*>(&sh.G);
+          const int64_t c0 = ((w.seg0 + 1) * ctas - 1) / total_units, c1 = (seg1 * ctas - 1) / total_units;
           __threadfence();
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
@@ -568,34 +632,34 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       // ------------------------------------------------------------ K to f16
       const int kw = warp - C::kWarpK, mu = lane & 15, half = lane >> 4;
       const int tok = kv_mma_token(mu);
-      uint4 code[2][C::kJobs][2];
-      uint2 sc[2][C::kJobs];
+      uint4 code[C::kKJobs][2];
+      uint2 sc[C::kKJobs];
       // the tile (of 16 tokens) of job j and this lane, counted in the block
       auto tile_of = [&](int j) { return D == 64 ? 2 * kw + half : D == 128 ? kw + 4 * j : kw; };
       Walk<D> ld = w;
       int lblk = ld.at;
       bool more = true;
-      int page[C::kJobs];
+      int page[C::kKJobs];
       auto fetch = [&]() {  // pages of the block to be loaded next
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
-          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
+        for (int j = 0; j < C::kKJobs; ++j) {
+          const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
           page[j] = k < ld.q.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (k >> p.a.cache.page_shift)) : -1;
         }
       };
-      auto load = [&](int set) {
+      auto load = [&]() {
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
-          code[set][j][0] = code[set][j][1] = make_uint4(0, 0, 0, 0);
-          sc[set][j] = make_uint2(0, 0);
+        for (int j = 0; j < C::kKJobs; ++j) {
+          code[j][0] = code[j][1] = make_uint4(0, 0, 0, 0);
+          sc[j] = make_uint2(0, 0);
           if (page[j] >= 0 && page[j] < p.a.cache.pages) {
-            const int in = (int)(((int64_t)(ld.first + lblk) * KB + tile_of(j) * 16) & (p.a.cache.page_size - 1));
+            const int in = ((ld.first + lblk) * KB + tile_of(j) * 16) & (p.a.cache.page_size - 1);
             const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, in);
             const int at = D == 64 ? mu * 32 : (D == 256 ? j * 1024 : 0) + mu * 64 + half * 32;
             const int sat = 8 * D + (D == 64 ? (mu & 7) * 8 : (D == 256 ? j * 128 : 0) + (mu & 7) * 16 + half * 8);
-            code[set][j][0] = *reinterpret_cast<const uint4*>(tile + at);
-            code[set][j][1] = *reinterpret_cast<const uint4*>(tile + at + 16);
-            sc[set][j] = *reinterpret_cast<const uint2*>(tile + sat);
+            code[j][0] = *reinterpret_cast<const uint4*>(tile + at);
+            code[j][1] = *reinterpret_cast<const uint4*>(tile + at + 16);
+            sc[j] = *reinterpret_cast<const uint2*>(tile + sat);
           }
         }
         if (++lblk == ld.end) {
@@ -605,23 +669,22 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         if (more) fetch();
       };
       fetch();
-      load(0);
+      load();
       uint32_t it = 0;
       const int64_t blocks = cta1 - cta0;
-      auto step = [&](int set) -> bool {
-        if (more) load(set ^ 1);
+      auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
         if (!pf_warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
-          const uint32_t s4 = D == 64 ? __byte_perm(sc[set][j].x, sc[set][j].y, mu >> 3 ? 0x7531 : 0x6420)
-                                      : __byte_perm(sc[set][j].x, sc[set][j].y, mu >> 3 ? 0x7632 : 0x5410);
+        for (int j = 0; j < C::kKJobs; ++j) {
+          const uint32_t s4 = D == 64 ? __byte_perm(sc[j].x, sc[j].y, mu >> 3 ? 0x7531 : 0x6420)
+                                      : __byte_perm(sc[j].x, sc[j].y, mu >> 3 ? 0x7632 : 0x5410);
           const uint32_t s01 = e4m3x2_to_f16x2(s4), s23 = e4m3x2_to_f16x2(s4 >> 16);
           const uint32_t s[4] = {bcast_lo(s01), bcast_hi(s01), bcast_lo(s23), bcast_hi(s23)};
           const int n = tile_of(j) * 16 + tok, sub = D == 64 ? 0 : D == 128 ? half : 2 * j + half;
           const uint32_t row = sK + stage * C::kKvBytes + sub * (KB * 128) + n * 128;
-          const uint32_t wd[8] = {code[set][j][0].x, code[set][j][0].y, code[set][j][0].z, code[set][j][0].w,
-                                  code[set][j][1].x, code[set][j][1].y, code[set][j][1].z, code[set][j][1].w};
+          const uint32_t wd[8] = {code[j][0].x, code[j][0].y, code[j][0].z, code[j][0].w,
+                                  code[j][1].x, code[j][1].y, code[j][1].z, code[j][1].w};
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t f[4];
@@ -635,51 +698,53 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + 8 * stage);
         ++it;
+        if (more) load();  // in flight while the stages are full
         return true;
       };
-      for (int64_t n = 0; n < blocks; n += 2) {  // two steps: the register sets are named, not indexed
-        if (!(ok = step(0))) break;
-        if (n + 1 < blocks && !(ok = step(1))) break;
-      }
+      for (int64_t n = 0; n < blocks; ++n)
+        if (!(ok = step())) break;
     } else if (warp < C::kWarpMma) {
       // ------------------------------------------------------------ V to f16, turned
       const int vw = warp - C::kWarpV;
       const int half = D == 64 ? (lane >> 3) & 1 : lane >> 4, o = D == 64 ? lane & 7 : lane & 15;
-      uint32_t code[2][C::kJobs][8];
-      uint4 sc[2][C::kJobs];
-      int nvalid[2][C::kJobs];   // of the lane's 8 tokens
-      int segno[2];
-      auto tile_of = [&](int j) { return D == 64 ? 2 * vw + (lane >> 4) : D == 128 ? vw + 4 * j : vw; };
+      uint32_t code[C::kVJobs][8];
+      uint4 sc[C::kVJobs];
+      int nvalid[C::kVJobs];   // of the lane's 8 tokens
+      int segno;
+      // job vw + j * kVWarps: its tile (of 16 tokens) and, at head_dim 256, column block
+      auto job_of = [&](int j) { return vw + j * C::kVWarps; };
+      auto tile_of = [&](int j) { return D == 64 ? 2 * job_of(j) + (lane >> 4) : D == 128 ? job_of(j) : job_of(j) & 3; };
+      auto block_of = [&](int j) { return D == 256 ? job_of(j) >> 2 : 0; };
       Walk<D> ld = w;
       int lblk = ld.at;
       bool more = true;
-      int page[C::kJobs];
+      int page[C::kVJobs];
       auto fetch = [&]() {
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
-          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
-          page[j] = k < ld.q.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (k >> p.a.cache.page_shift)) : -1;
+        for (int j = 0; j < C::kVJobs; ++j) {
+          const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
+          page[j] = job_of(j) < C::kAllJobs && k < ld.q.len ? __ldg(p.a.tables + ld.b * p.a.ldt + (k >> p.a.cache.page_shift)) : -1;
         }
       };
-      auto load = [&](int set) {
-        segno[set] = ld.no;
+      auto load = [&]() {
+        segno = ld.no;
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
-          const int64_t k = (int64_t)(ld.first + lblk) * KB + tile_of(j) * 16;
-          sc[set][j] = make_uint4(0, 0, 0, 0);
-          nvalid[set][j] = 0;
+        for (int j = 0; j < C::kVJobs; ++j) {
+          const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
+          sc[j] = make_uint4(0, 0, 0, 0);
+          nvalid[j] = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) code[set][j][i] = 0;
+          for (int i = 0; i < 8; ++i) code[j][i] = 0;
           if (page[j] >= 0 && page[j] < p.a.cache.pages) {
-            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, (int)(k & (p.a.cache.page_size - 1)));
-            const uint8_t* at = tile + 9 * D + (D == 256 ? j * 1024 : 0);
+            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, k & (p.a.cache.page_size - 1));
+            const uint8_t* at = tile + 9 * D + block_of(j) * 1024;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = 8 * half + i;
-              code[set][j][i] = *reinterpret_cast<const uint32_t*>(at + (D == 64 ? r * 32 + o * 4 : r * 64 + ((o * 4) ^ (((i >> 1) & 1) * 32))));
+              code[j][i] = *reinterpret_cast<const uint32_t*>(at + (D == 64 ? r * 32 + o * 4 : r * 64 + ((o * 4) ^ (((i >> 1) & 1) * 32))));
             }
-            sc[set][j] = *reinterpret_cast<const uint4*>(tile + 17 * D + ((D == 256 ? j * 8 : 0) + (o >> 1)) * 16);
-            nvalid[set][j] = (int)min((int64_t)8, max((int64_t)ld.q.len - k - 8 * half, (int64_t)0));
+            sc[j] = *reinterpret_cast<const uint4*>(tile + 17 * D + (block_of(j) * 8 + (o >> 1)) * 16);
+            nvalid[j] = min(8, max(ld.q.len - k - 8 * half, 0));
           }
         }
         if (++lblk == ld.end) {
@@ -689,23 +754,23 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         if (more) fetch();
       };
       fetch();
-      load(0);
+      load();
       const int rot = o & 3, odd = (o >> 2) & 1;
       const uint32_t rsel = rot == 0 ? 0x3210 : rot == 1 ? 0x0321 : rot == 2 ? 0x1032 : 0x2103;
       uint32_t it = 0;
       const int64_t blocks = cta1 - cta0;
-      auto step = [&](int set) -> bool {
-        if (more) load(set ^ 1);
+      auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
         if (!pf_warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
 #pragma unroll
-        for (int j = 0; j < C::kJobs; ++j) {
+        for (int j = 0; j < C::kVJobs; ++j) {
+          if (job_of(j) >= C::kAllJobs) break;
           // scales of the lane's tokens 0..3 and 4..7, a byte each
-          const uint4 sw = sc[set][j];
+          const uint4 sw = sc[j];
           const uint32_t s0 = half ? 0x62 : 0x40, s1 = half ? 0x73 : 0x51;
           uint32_t q[2] = {__byte_perm(__byte_perm(sw.x, sw.y, s0), __byte_perm(sw.z, sw.w, s0), 0x5410),
                            __byte_perm(__byte_perm(sw.x, sw.y, s1), __byte_perm(sw.z, sw.w, s1), 0x5410)};
-          const int nv = nvalid[set][j];
+          const int nv = nvalid[j];
           if (nv < 8) {  // places behind the last key hold anything
             q[1] = nv > 4 ? q[1] & ((1u << (8 * (nv - 4))) - 1) : 0u;
             if (nv < 4) q[0] &= (1u << (8 * nv)) - 1;
@@ -715,14 +780,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             const uint32_t bad = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
             if (bad) {
               q[k] &= ~((bad >> 7) * 0xFFu);
-              *reinterpret_cast<volatile int*>(&sh.nan_seg[segno[set] & 7]) = segno[set] + 1;
+              *reinterpret_cast<volatile int*>(&sh.nan_seg[segno & 7]) = segno + 1;
             }
           }
           uint32_t x[4][4], y[4][4];  // [d][pair of tokens]
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             constexpr uint32_t M = 0x0F0F0F0Fu;
-            const uint32_t a = code[set][j][2 * i], b = code[set][j][2 * i + 1];
+            const uint32_t a = code[j][2 * i], b = code[j][2 * i + 1];
             const uint32_t even = __byte_perm((a & M) | ((b << 4) & ~M), 0, rsel);
             const uint32_t oddw = __byte_perm(((a >> 4) & M) | (b & ~M), 0, rsel);
             const uint32_t u = odd ? oddw : even, v = odd ? even : oddw;
@@ -737,7 +802,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
           }
           const int ti = tile_of(j), chunk = (ti & 3) * 2 + half;
-          const uint32_t at = sV + stage * C::kKvBytes + (ti >> 2) * (D * 128) + (D == 256 ? j * 128 * 128 : 0) + o * 1024;
+          const uint32_t at = sV + stage * C::kKvBytes + (ti >> 2) * (D * 128) + block_of(j) * 16384 + o * 1024;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int d0 = 2 * ((e + rot) & 3) + odd, d1 = 2 * ((e + rot) & 3) + 1 - odd;
@@ -749,14 +814,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + 8 * stage);
         ++it;
+        if (more) load();
         return true;
       };
-      for (int64_t n = 0; n < blocks; n += 2) {
-        if (!(ok = step(0))) break;
-        if (n + 1 < blocks && !(ok = step(1))) break;
-      }
-    } else if (elect_one()) {
+      for (int64_t n = 0; n < blocks; ++n)
+        if (!(ok = step())) break;
+    } else {
       // ------------------------------------------------------------ the products
+      if (elect_one()) {
       constexpr uint32_t ids = idesc_f16(KB), ido = idesc_f16(D);
       uint32_t it = 0, done[2] = {0, 0}, segs[2] = {0, 0};
       auto qk = [&](int X, uint32_t n, uint32_t sbuf) {  // scores of block n (of the CTA's)
@@ -827,6 +892,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       mma_commit(drain);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
+      }
     }
     if (!ok && (lane == 0 || warp == C::kWarpMma)) atomicExch(reinterpret_cast<int*>(p.a.workspace), 5);
   }
