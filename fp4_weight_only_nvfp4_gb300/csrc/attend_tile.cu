@@ -17,7 +17,8 @@
 //                  (both K-major, 128-byte swizzle).
 //   MMA warp       one thread issues every product.
 // The tiles' blocks of keys, times the heads, stand in one line that is shared out evenly over the
-// CTAs; the parts of a tile that CTAs share are joined by the CTA that comes last.
+// CTAs; the parts of a tile that CTAs share are joined by the CTA that comes last.  Each (tile,
+// head) stands there with kLead units more than its blocks, for its start and end.
 //
 // Every wait inside the CTA is bounded (2 s); one that gives up sets the status word and ends every role.
 #include <cuda_bf16.h>
@@ -37,6 +38,7 @@ namespace {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kTileBias = 7.0f;   // P = 2^(s - m + 7): below 2^15 while s - m <= 8
 constexpr float kSlack = 8.0f;
+constexpr int kLead = 3;
 
 template <int D>
 struct TileCfg {
@@ -72,9 +74,12 @@ struct TileShared {
   int b, i;            // its tile
   int last;
   int nan_seg[8];
+  float half_m[128], half_l[128];  // of the row tile's second half of blocks
+  int half_any[128];
   uint32_t tmem;
   int abort;
   alignas(8) uint64_t bars[24];
+  alignas(16) uint8_t walk[8 * 96];  // of each softmax warp
 };
 
 struct TileParams {
@@ -118,29 +123,34 @@ struct Walk {
   int first, count;   // the tile's blocks
   int at, end;        // this segment: blocks [at, end) of them, counted from first
   int64_t seg0;       // unit of block 0
-  int64_t left;       // units of the CTA from `at` on
+  int64_t left;       // units of the CTA from the (tile, head)'s first, or the CTA's own first, on
   int no;             // segments before this one
-  __device__ __forceinline__ void start(const TileParams& p, const TileShared& sh, int64_t u0, int64_t u1) {
+  static __device__ __forceinline__ int per_tile(const TileParams& p) { return p.tokens * TileCfg<D>::kRowTiles; }
+  // The CTA's first segment; false if there is no block in its units.
+  __device__ __forceinline__ bool start(const TileParams& p, const TileShared& sh, int64_t u0, int64_t u1) {
     b = sh.b;
     i = sh.i;
     q = load_seq(p.a, b);
     tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
     const int64_t r = u0 - sh.before;
-    h = (int)(r / count);
-    at = (int)(r - (int64_t)h * count);
-    seg0 = u0 - at;
-    left = u1 - u0;
+    h = (int)(r / (count + kLead));
+    const int off = (int)(r - (int64_t)h * (count + kLead));
+    seg0 = u0 - off + kLead;
+    left = u1 - u0 + off;
     no = 0;
-    end = (int)min((int64_t)count, at + left);
+    return cut(off);
   }
-  static __device__ __forceinline__ int per_tile(const TileParams& p) { return p.tokens * TileCfg<D>::kRowTiles; }
+  __device__ __forceinline__ bool cut(int off) {
+    at = max(off - kLead, 0);
+    end = (int)min((int64_t)count, left - kLead);
+    return end > at;
+  }
   // To the CTA's next segment; false at its end.
   __device__ __forceinline__ bool next(const TileParams& p) {
-    left -= end - at;
+    left -= count + kLead;
     if (left <= 0) return false;
     ++no;
-    seg0 += count;
-    at = 0;
+    seg0 += count + kLead;
     if (++h == p.a.cache.heads) {
       h = 0;
       do {
@@ -153,11 +163,14 @@ struct Walk {
         tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
       } while (count == 0);
     }
-    end = (int)min((int64_t)count, left);
-    return true;
+    return cut(0);
   }
   __device__ __forceinline__ int row_tiles(const TileParams& p) const {
     return TileCfg<D>::kRowTiles == 2 && q.n - i * per_tile(p) > p.tokens ? 2 : 1;
+  }
+  // One row tile of the two: its blocks go to both in turn, and their halves are joined at the end.
+  __device__ __forceinline__ bool halved(const TileParams& p) const {
+    return TileCfg<D>::kRowTiles == 2 && row_tiles(p) == 1;
   }
   __device__ __forceinline__ bool whole() const { return at == 0 && end == count; }
 };
@@ -175,6 +188,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
       "%12, %13, %14, %15};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
       "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -242,7 +269,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
   const uint32_t bar0 = smem_u32(sh.bars);
   const uint32_t q_full = bar0, k_full = q_full + 16, k_empty = k_full + 16, v_full = k_empty + 16, v_empty = v_full + 16;
   const uint32_t s_full = v_empty + 16;                  // [row tile or buffer]
-  const uint32_t p_full = s_full + 16, pv_done = p_full + 16, joined = pv_done + 16, told = joined + 8, drain = told + 8;
+  const uint32_t p_full = s_full + 16, pv_done = p_full + 16, joined = pv_done + 16, told = joined + 8;
+  const uint32_t half_full = told + 8, half_read = half_full + 8, drain = half_read + 8;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -257,6 +285,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
     }
     mbar_init(joined, C::kSoftWarps);
     mbar_init(told, 1);
+    mbar_init(half_full, 4);
+    mbar_init(half_read, 4);
     mbar_init(drain, 1);
     sh.abort = 0;
     for (int i = 0; i < 8; ++i) sh.nan_seg[i] = 0;
@@ -300,8 +330,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           }
         }
         int64_t all;
-        const int64_t before = (done + block_prefix<W>(count, sh.scan, &all)) * Hkv;
-        if (pass == 1 && cta0 >= before && cta0 < before + (int64_t)count * Hkv) {
+        const int units = count ? count + kLead : 0;
+        const int64_t before = (done + block_prefix<W>(units, sh.scan, &all)) * Hkv;
+        if (pass == 1 && cta0 >= before && cta0 < before + (int64_t)units * Hkv) {
           sh.b = (int)(b0 + at);
           sh.i = i;
           sh.before = before;
@@ -332,8 +363,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
   bool ok = true;
 
   if (cta0 < cta1) {
-    Walk<D> w;
-    w.start(p, sh, cta0, cta1);
     if (warp < C::kSoftWarps) {
       // ------------------------------------------------------------ softmax
       const int X = warp >> 2, r = tid & 127;           // row tile, row of it
@@ -341,13 +370,26 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       const uint32_t tO = tmem + lanes + C::kTmemO + X * D;
       const uint32_t qwarp = sQ + X * C::kQBytes + (warp & 3) * 4096;  // this warp's 32 rows
       constexpr int LR = D / 8, RI = 32 / LR;           // lanes a row takes, rows a load takes
-      uint32_t it = 0, segs = 0, joins = 0;             // blocks, segments, joins of this row tile
-      do {
-        const bool mine_seg = X < w.row_tiles(p);
-        const int inner = r % p.a.group, tok = X * p.tokens + r / p.a.group, idx = w.i * per_tile + tok;
-        const bool live = mine_seg && r < p.tokens * p.a.group && idx < w.q.n;
-        const int head = w.h * p.a.group + inner;
-        const int64_t t = w.q.s0 + idx;
+      // the walk stays in shared memory: the block loop needs the registers
+      static_assert(sizeof(Walk<D>) <= 96, "a warp's walk");
+      Walk<D>& w = *reinterpret_cast<Walk<D>*>(sh.walk + warp * 96);
+      int more = 0;
+      if (lane == 0) more = w.start(p, sh, cta0, cta1);
+      more = __shfl_sync(0xffffffffu, more, 0);
+      uint32_t it = 0, turns = 0;                       // blocks of this row tile; bit 0: halves joined, bit 1: parts joined
+      while (more) {
+        __syncwarp();
+        const bool halved = w.halved(p);
+        // blocks from `b0` on, every `step`-th; the second half of one block is empty
+        const int b0 = w.at + (halved ? X : 0), step = halved ? 2 : 1, b1 = w.end;
+        const bool mine_seg = b0 < b1;
+        const int XR = halved ? 0 : X;                  // whose rows
+        const int idx = w.i * per_tile + XR * p.tokens + r / p.a.group;
+        const bool live = mine_seg && r / p.a.group < p.tokens && idx < w.q.n;
+        auto at_row = [&](int64_t ld) {                 // of q or out, in elements
+          const int tok = r / p.a.group, inner = r - tok * p.a.group, row = halved ? 0 : X;
+          return (int64_t)(w.q.s0 + w.i * per_tile + row * p.tokens + tok) * ld + (int64_t)(w.h * p.a.group + inner) * D;
+        };
         const int seen = w.q.len - w.q.n + idx + 1;       // keys up to the row's own
         // keys [row_lo, row_hi) are those that the row sees
         const int row_hi = live ? max(seen, 0) : 0x7FFFFFFF;
@@ -358,8 +400,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           // ---- Q
           // LR lanes take a row 16 bytes each, so that a load meets few lines; a lane keeps the power of
           // two of its own row
-          const bool negative = p.a.scale * p.a.cache.k_scale[w.h] < 0.0f;
-          const int64_t from = live ? t * p.a.ldq + (int64_t)head * D : -1;
+          const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[w.h];
+          const uint32_t sign = unit < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q: the largest product is the largest score
+          const int64_t from = live ? at_row(p.a.ldq) : -1;
           int pw = 0;
 #pragma unroll 1
           for (int i0 = 0; i0 < 32; i0 += 8 * RI) {
@@ -379,10 +422,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               const int mine = __shfl_sync(0xffffffffu, pr, (lane % RI) * LR);
               if (lane / RI == i0 / RI + i) pw = mine;
               const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&v[i]), pr);
-              st_shared_v4(qwarp + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), f.x, f.y, f.z, f.w);
+              st_shared_v4(qwarp + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), f.x ^ sign, f.y ^ sign, f.z ^ sign, f.w ^ sign);
             }
           }
-          float mul = p.a.scale * kLog2e * p.a.cache.k_scale[w.h] * pow2f(pw);
+          float mul = fabsf(unit) * pow2f(pw);
           if (mul == 0.0f) mul = 1e-38f;  // every score 0, a masked one (-inf) stays out
           fence_proxy_async_smem();
           tc_fence_before();
@@ -397,13 +440,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             const int page = __ldg(p.a.tables + w.b * p.a.ldt + (k >> p.a.cache.page_shift));
             return page >= 0 && page < p.a.cache.pages;
           };
-          bool page_ok = pages_of(w.at);
-          for (int blk = w.at; blk < w.end; ++blk, ++it) {
+          bool page_ok = pages_of(b0);
+          const int key0 = w.first * KB;
+          for (int blk = b0; blk < b1; blk += step, ++it) {
             const uint32_t sbuf = SB == 2 ? (it & 1) : X, sphase = SB == 2 ? (it >> 1) & 1 : it & 1;
             const uint32_t tS = tmem + lanes + sbuf * KB;
             const uint32_t gone = ~__ballot_sync(0xffffffffu, page_ok) & ((1u << (KB / 16)) - 1);
-            if (blk + 1 < w.end) page_ok = pages_of(blk + 1);
-            const int k0 = (w.first + blk) * KB;
+            if (blk + step < b1) page_ok = pages_of(blk + step);
+            const int k0 = key0 + blk * KB;
             // columns [lo, hi) that the row sees
             const int hi = min(KB, max(row_hi - k0, 0));
             const int lo = min(KB, max(row_lo - k0, 0));
@@ -411,87 +455,98 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             if (!(ok = pf_warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
             tc_fence_after();
             if (!idle) {
-              // Masked scores become -inf (of the sign that the products take).
-              const uint32_t out = negative ? 0x7F800000u : 0xFF800000u;
-              auto mask = [&](uint32_t (&v)[32], int c) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int col = c * 32 + e;
-                  if (col < lo || col >= hi || ((gone >> (col >> 4)) & 1)) v[e] = out;
-                }
-              };
               uint32_t v[2][32];
-              float top[2] = {-INFINITY, -INFINITY};
-              auto highest = [&](uint32_t (&x)[32], int c) {
-                if (edge) mask(x, c);
-                if (!negative) {
+              if (edge) {  // scores that a row does not see become -inf in their place
+#pragma unroll 1
+                for (int c = 0; c < KB; c += 32) {
+                  tmem_ld32(tS + c, v[0]);
 #pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    top[0] = max3(top[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                    top[1] = max3(top[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) top[0] = fmaxf(top[0], -__uint_as_float(x[e]));
+                  for (int e = 0; e < 32; ++e)
+                    if (c + e < lo || c + e >= hi || ((gone >> ((c + e) >> 4)) & 1)) v[0][e] = 0xFF800000u;
+                  tmem_st32(tS + c, v[0]);
                 }
-              };
-              tmem_ld32_issue(tS, v[0]);
+                tmem_st_wait();
+                any |= lo < hi && !gone;
+                if (gone) {
+                  for (int g = 0; g < KB / 16; ++g)
+                    any |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
+                }
+              } else {
+                any = true;
+              }
+              // the maximum; the last 64 scores stay in registers
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int c = 0; c < KB / 32; ++c) {
-                tmem_ld_wait(v[c & 1]);
-                if (c + 1 < KB / 32) tmem_ld32_issue(tS + (c + 1) * 32, v[(c + 1) & 1]);
-                highest(v[c & 1], c);
+              for (int c = 0; c < KB; c += 64) {
+                tmem_ld32_issue(tS + c, v[0]);
+                tmem_ld32_issue(tS + c + 32, v[1]);
+                tmem_ld_wait(v[0]);
+                tmem_ld_wait(v[1]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    top[2 * k] = max3(top[2 * k], __uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1]));
+                    top[2 * k + 1] = max3(top[2 * k + 1], __uint_as_float(v[k][e + 2]), __uint_as_float(v[k][e + 3]));
+                  }
+                }
               }
-              tmem_ld32_issue(tS, v[0]);  // again, for the probabilities
-              const float best = fmaxf(top[0], top[1]);
-              any |= lo < hi && !gone;
-              if (gone) {
-                for (int g = 0; g < KB / 16; ++g)
-                  any |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
-              }
-              const float mx = best == -INFINITY ? best : best * fabsf(mul);
+              const float best = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+              const float mx = best == -INFINITY ? best : best * mul;
               const float mn = (m == -INFINITY || mx > m + kSlack) ? fmaxf(m, mx) : m;
-              if (blk > w.at && __any_sync(0xffffffffu, mn > m)) {
+              if (blk > b0 && __any_sync(0xffffffffu, mn > m)) {
                 if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
                 tc_fence_after();
                 const float f = mn > m ? fast_exp2(m - mn) : 1.0f;
                 l *= f;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t v[32];
-                  tmem_ld32(tO + c * 32, v);
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + c, o);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                  tmem_st32(tO + c * 32, v);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(tO + c, o);
                 }
               }
               m = mn;
               const float off = kTileBias - (m == -INFINITY ? 0.0f : m);
               const uint64_t mul2 = pair(mul, mul), off2 = pair(off, off);
               uint64_t sum[2] = {0, 0};
+              // P, two f16 a column, over the second half of the scores: those are in registers
+              auto probabilities = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
-              for (int c = 0; c < KB / 32; ++c) {
-                uint32_t(&x)[32] = v[c & 1];
-                tmem_ld_wait(x);
-                if (c + 1 < KB / 32) tmem_ld32_issue(tS + (c + 1) * 32, v[(c + 1) & 1]);
-                if (edge) mask(x, c);
-                uint32_t pk[16];
+                for (int h = 0; h < 32; h += 16) {
+                  uint32_t pk[8];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  float a, b;
-                  split(fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2, off2), a, b);
-                  a = fast_exp2(a);
-                  b = fast_exp2(b);
-                  sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, b));
-                  pk[e >> 1] = pack_half2(a, b);
+                  for (int e = 0; e < 16; e += 2) {
+                    float a, b;
+                    split(fma2(pair(__uint_as_float(x[h + e]), __uint_as_float(x[h + e + 1])), mul2, off2), a, b);
+                    a = fast_exp2(a);
+                    b = fast_exp2(b);
+                    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(a, b));
+                    pk[e >> 1] = pack_half2(a, b);
+                  }
+                  tmem_st8(tS + KB / 2 + (c + h) / 2, pk);
                 }
-                tmem_st16(tS + c * 16, pk);
+              };
+              probabilities(v[0], KB - 64);
+              if (KB == 128) tmem_ld32_issue(tS, v[0]);
+              probabilities(v[1], KB - 32);
+              if (KB == 128) {
+                tmem_ld32_issue(tS + 32, v[1]);
+                tmem_ld_wait(v[0]);
+                tmem_ld_wait(v[1]);
+                probabilities(v[0], 0);
+                probabilities(v[1], 32);
               }
               float la, lb;
               split(add2(sum[0], sum[1]), la, lb);
               l += la + lb;
               tmem_st_wait();
             }
+            // With two score buffers this block's scores do not say that the last block's P V is done.  It is
+            // waited for here, one phase at a time: a wait on a phase takes the one before it for done.
+            if (SB == 2 && blk > b0 && !(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * sbuf);
@@ -499,23 +554,53 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           if (!ok) break;
           if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
           tc_fence_after();
-          ++segs;
         }
+        // ---- the two halves of a single row tile: the second's sums to the first
+        const bool other = halved && w.end - w.at > 1;
+        float f0 = 1.0f, f1 = 0.0f;
+        if (other) {
+          if (X == 1) {
+            sh.half_m[r] = m;
+            sh.half_l[r] = l;
+            sh.half_any[r] = any;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(half_full);
+            if (!(ok = pf_warp_wait(half_read, turns & 1, abort, p.wait_ns))) break;
+          } else {
+            if (!(ok = pf_warp_wait(half_full, turns & 1, abort, p.wait_ns))) break;
+            tc_fence_after();
+            const float m1 = sh.half_m[r], mt = fmaxf(m, m1), ms = mt == -INFINITY ? 0.0f : mt;
+            f0 = fast_exp2(m - ms);
+            f1 = fast_exp2(m1 - ms);
+            l = l * f0 + sh.half_l[r] * f1;
+            any |= sh.half_any[r] != 0;
+            m = mt;
+          }
+          turns ^= 1;
+        }
+        const bool out = mine_seg && !(halved && X == 1);
         const bool whole = w.whole();
+        const int head = w.h * p.a.group + r % p.a.group;
         float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w.at == 0)) * C::kPartFloats;
         uint32_t lost = 0;
-        if (live && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
+        if (live && out && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
           lost = nan_columns<D>(p.a, w.b, w.h, max(row_lo, (w.first + w.at) * KB),
                                 (int)min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB));
         auto value = [&](uint32_t v, int col) {
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
         };
-        if (mine_seg) {
+        if (out) {
           const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kTileBias) : 0.0f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(tO + c * 32, v);
+            if (other) {
+              uint32_t u[32];
+              tmem_ld32(tO + D + c * 32, u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0 + __uint_as_float(u[e]) * f1);
+            }
             if (whole) {  // to the place of Q, whose products are done
 #pragma unroll
               for (int e = 0; e < 32; e += 8) {
@@ -540,8 +625,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             __syncwarp();  // the next load from TMEM takes the whole warp
           }
+          if (other) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(half_read);
+          }
           if (whole) {
-            const int64_t to = live ? t * p.a.ldo + (int64_t)head * D : -1;
+            const int64_t to = live ? at_row(p.a.ldo) : -1;
 #pragma unroll 4
             for (int i = 0; i < 32; i += RI) {
               const int row = i + lane / LR, c = lane % LR;
@@ -567,7 +657,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
           if (warp == 0) {
-            if (!(ok = pf_warp_wait(joined, joins & 1, abort, p.wait_ns))) break;
+            if (!(ok = pf_warp_wait(joined, (turns >> 1) & 1, abort, p.wait_ns))) break;
             if (lane == 0) {
               uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + 256) + c0;
               __threadfence();
@@ -579,13 +669,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             __syncwarp();
           }
-          if (!(ok = pf_warp_wait(told, joins & 1, abort, p.wait_ns))) break;
-          ++joins;
+          if (!(ok = pf_warp_wait(told, (turns >> 1) & 1, abort, p.wait_ns))) break;
+          turns ^= 2;
           if (*reinterpret_cast<volatile int*>(&sh.last)) {
             const int n = (int)(c1 - c0) + 1;
             // CTA c0's part is in its slot 1, the others' in their slot 0
             auto part_of = [&](int k) { return p.parts + (2 * (c0 + k) + (k == 0)) * (int64_t)C::kPartFloats; };
-            if (live) {
+            if (live && out) {
               float mt = -INFINITY, lt = 0.0f;
               bool at = false;
               for (int k = 0; k < n; ++k) {
@@ -599,7 +689,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 lt += fast_exp2(__ldcg(st) - ms) * __ldcg(st + C::kRows);
               }
               const float f = at ? out_factor(p.a, head, w.h, mt, lt, kTileBias) : 0.0f;
-              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + t * p.a.ldo + (int64_t)head * D;
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + at_row(p.a.ldo);
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 float4 o[4] = {};
@@ -627,7 +717,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
           }
         }
-      } while (w.next(p));
+        __syncwarp();
+        if (lane == 0) more = w.next(p);
+        more = __shfl_sync(0xffffffffu, more, 0);
+      }
     } else if (warp < C::kWarpV) {
       // ------------------------------------------------------------ K to f16
       const int kw = warp - C::kWarpK, mu = lane & 15, half = lane >> 4;
@@ -636,9 +729,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       uint2 sc[C::kKJobs];
       // the tile (of 16 tokens) of job j and this lane, counted in the block
       auto tile_of = [&](int j) { return D == 64 ? 2 * kw + half : D == 128 ? kw + 4 * j : kw; };
-      Walk<D> ld = w;
+      Walk<D> ld;
+      bool more = ld.start(p, sh, cta0, cta1), pending = more;   // a block to load; one loaded
       int lblk = ld.at;
-      bool more = true;
       int page[C::kKJobs];
       auto fetch = [&]() {  // pages of the block to be loaded next
 #pragma unroll
@@ -668,10 +761,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         }
         if (more) fetch();
       };
-      fetch();
-      load();
+      if (more) {
+        fetch();
+        load();
+      }
       uint32_t it = 0;
-      const int64_t blocks = cta1 - cta0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
         if (!pf_warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
@@ -698,11 +792,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + 8 * stage);
         ++it;
+        pending = more;
         if (more) load();  // in flight while the stages are full
         return true;
       };
-      for (int64_t n = 0; n < blocks; ++n)
-        if (!(ok = step())) break;
+      while (pending && (ok = step())) {}
     } else if (warp < C::kWarpMma) {
       // ------------------------------------------------------------ V to f16, turned
       const int vw = warp - C::kWarpV;
@@ -715,9 +809,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       auto job_of = [&](int j) { return vw + j * C::kVWarps; };
       auto tile_of = [&](int j) { return D == 64 ? 2 * job_of(j) + (lane >> 4) : D == 128 ? job_of(j) : job_of(j) & 3; };
       auto block_of = [&](int j) { return D == 256 ? job_of(j) >> 2 : 0; };
-      Walk<D> ld = w;
+      Walk<D> ld;
+      bool more = ld.start(p, sh, cta0, cta1), pending = more;   // a block to load; one loaded
       int lblk = ld.at;
-      bool more = true;
       int page[C::kVJobs];
       auto fetch = [&]() {
 #pragma unroll
@@ -753,12 +847,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         }
         if (more) fetch();
       };
-      fetch();
-      load();
+      if (more) {
+        fetch();
+        load();
+      }
       const int rot = o & 3, odd = (o >> 2) & 1;
       const uint32_t rsel = rot == 0 ? 0x3210 : rot == 1 ? 0x0321 : rot == 2 ? 0x1032 : 0x2103;
       uint32_t it = 0;
-      const int64_t blocks = cta1 - cta0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
         if (!pf_warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
@@ -814,15 +909,17 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + 8 * stage);
         ++it;
+        pending = more;
         if (more) load();
         return true;
       };
-      for (int64_t n = 0; n < blocks; ++n)
-        if (!(ok = step())) break;
+      while (pending && (ok = step())) {}
     } else {
       // ------------------------------------------------------------ the products
       if (elect_one()) {
       constexpr uint32_t ids = idesc_f16(KB), ido = idesc_f16(D);
+      Walk<D> w;
+      bool more = w.start(p, sh, cta0, cta1);
       uint32_t it = 0, done[2] = {0, 0}, segs[2] = {0, 0};
       auto qk = [&](int X, uint32_t n, uint32_t sbuf) {  // scores of block n (of the CTA's)
         const uint32_t ks = sK + (n & 1) * C::kKvBytes;
@@ -841,7 +938,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           const uint64_t b = desc_sw128(vs + c * (D * 128));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ta(tmem + C::kTmemO + X * D, tmem + sbuf * KB + (c * 4 + kk) * 8, b + 2 * kk, ido, add || c > 0 || kk > 0);
+            mma_f16_ta(tmem + C::kTmemO + X * D, tmem + sbuf * KB + KB / 2 + (c * 4 + kk) * 8, b + 2 * kk, ido, add || c > 0 || kk > 0);
         }
         mma_commit(pv_done + 8 * X);
       };
@@ -849,8 +946,36 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         ok = ok && pf_wait(bar, parity, abort, p.wait_ns);
         return ok;
       };
-      do {
+      for (; more; more = w.next(p)) {
         const int rt = w.row_tiles(p), n = w.end - w.at;
+        if (w.halved(p)) {  // blocks to the two in turn
+          const int ahead = n < 2 ? n : 2;
+          for (int X = 0; X < ahead; ++X) {
+            const uint32_t nx = it + X;
+            if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1) || !wait(q_full + 8 * X, segs[X] & 1)) break;
+            ++segs[X];
+            tc_fence_after();
+            qk(X, nx, X);
+            mma_commit(k_empty + 8 * (nx & 1));
+          }
+          for (int j = 0; ok && j < n; ++j, ++it) {
+            const int X = j & 1;
+            const uint32_t nx = it + 2;
+            if (!wait(p_full + 8 * X, done[X] & 1) || !wait(v_full + 8 * (it & 1), (it >> 1) & 1)) break;
+            tc_fence_after();
+            pv(X, it, X, j > 1);
+            ++done[X];
+            mma_commit(v_empty + 8 * (it & 1));
+            if (j + 2 < n) {
+              if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
+              tc_fence_after();
+              qk(X, nx, X);
+              mma_commit(k_empty + 8 * (nx & 1));
+            }
+          }
+          if (!ok) break;
+          continue;
+        }
         if (!wait(k_full + 8 * (it & 1), (it >> 1) & 1)) break;
         for (int X = 0; X < rt; ++X) {
           if (!wait(q_full + 8 * X, segs[X] & 1)) break;
@@ -887,7 +1012,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           if (SB == 1 && on) mma_commit(k_empty + 8 * (nx & 1));
         }
         if (!ok) break;
-      } while (w.next(p));
+      }
       // every product issued has completed once this arrives
       mma_commit(drain);
       const uint64_t t0 = globaltimer_ns();

@@ -246,3 +246,14 @@ def test_two_runs_are_bit_for_bit_alike():
         want = c.run()
         for _ in range(5):
             assert torch.equal(c.run(), want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_short_calls_again_and_again(D):
+    """Tiles of two or three blocks shared between CTAs, many times over: a part handed on too early
+    shows in some runs only."""
+    rng = np.random.default_rng(D + 1)
+    c = Case(rng, [50, 40, 7, 150], 64, 1, D, 16, rows=[1, 40, 0, 70])
+    want = c.check()
+    for _ in range(60):
+        assert torch.equal(c.run(), want)
