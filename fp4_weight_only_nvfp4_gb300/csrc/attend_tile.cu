@@ -211,6 +211,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
   tmem_st16(taddr, a);
   tmem_st16(taddr + 16, b);
 }
+// Bounded wait; the warp sleeps in the barrier for up to 20 us at a time, so that those that wait take
+// no issue slots from those that work.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (try_wait_long(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (try_wait_long(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// One answer for the warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort, limit_ns));
+}
 // Two fp32 at a time.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -254,6 +282,15 @@ __device__ __noinline__ uint32_t nan_columns(const AttendLaunch& a, int b, int h
       if ((tile[kv_v_scale(D, in % kKvTile, s)] & 0x7F) == 0x7F) bits |= 1u << s;
   }
   return bits;
+}
+
+// Tile holding key k of a sequence, on page `page` (page 0 if that is none).
+template <int D>
+__device__ __forceinline__ const uint8_t* tile_at(const KvCache& c, int page, int h, int k) {
+  const uint32_t pg = page >= 0 && page < c.pages ? page : 0;
+  const uint32_t stride = (uint32_t)(c.page_stride >> 7), tiles = (uint32_t)c.page_size / kKvTile;
+  return c.data + (((uint64_t)pg * stride) << 7) +
+         (h * tiles + (((uint32_t)k & (c.page_size - 1)) / kKvTile)) * (uint64_t)kv_tile_bytes(D);
 }
 
 template <int D>
@@ -452,7 +489,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             const int hi = min(KB, max(row_hi - k0, 0));
             const int lo = min(KB, max(row_lo - k0, 0));
             const bool edge = __any_sync(0xffffffffu, hi < KB || lo > 0) || gone;
-            if (!(ok = pf_warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
             tc_fence_after();
             if (!idle) {
               uint32_t v[2][32];
@@ -495,7 +532,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               const float mx = best == -INFINITY ? best : best * mul;
               const float mn = (m == -INFINITY || mx > m + kSlack) ? fmaxf(m, mx) : m;
               if (blk > b0 && __any_sync(0xffffffffu, mn > m)) {
-                if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+                if (!(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
                 tc_fence_after();
                 const float f = mn > m ? fast_exp2(m - mn) : 1.0f;
                 l *= f;
@@ -546,13 +583,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             // With two score buffers this block's scores do not say that the last block's P V is done.  It is
             // waited for here, one phase at a time: a wait on a phase takes the one before it for done.
-            if (SB == 2 && blk > b0 && !(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+            if (SB == 2 && blk > b0 && !(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * sbuf);
           }
           if (!ok) break;
-          if (!(ok = pf_warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+          if (!(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
           tc_fence_after();
         }
         // ---- the two halves of a single row tile: the second's sums to the first
@@ -565,9 +602,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             sh.half_any[r] = any;
             __syncwarp();
             if (lane == 0) mbar_arrive(half_full);
-            if (!(ok = pf_warp_wait(half_read, turns & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(half_read, turns & 1, abort, p.wait_ns))) break;
           } else {
-            if (!(ok = pf_warp_wait(half_full, turns & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(half_full, turns & 1, abort, p.wait_ns))) break;
             tc_fence_after();
             const float m1 = sh.half_m[r], mt = fmaxf(m, m1), ms = mt == -INFINITY ? 0.0f : mt;
             f0 = fast_exp2(m - ms);
@@ -657,7 +694,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
           if (warp == 0) {
-            if (!(ok = pf_warp_wait(joined, (turns >> 1) & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(joined, (turns >> 1) & 1, abort, p.wait_ns))) break;
             if (lane == 0) {
               uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + 256) + c0;
               __threadfence();
@@ -669,7 +706,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             __syncwarp();
           }
-          if (!(ok = pf_warp_wait(told, (turns >> 1) & 1, abort, p.wait_ns))) break;
+          if (!(ok = warp_wait(told, (turns >> 1) & 1, abort, p.wait_ns))) break;
           turns ^= 2;
           if (*reinterpret_cast<volatile int*>(&sh.last)) {
             const int n = (int)(c1 - c0) + 1;
@@ -725,6 +762,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       // ------------------------------------------------------------ K to f16
       const int kw = warp - C::kWarpK, mu = lane & 15, half = lane >> 4;
       const int tok = kv_mma_token(mu);
+      // the lane's codes and scales in a tile: 64 values of row mu
+      const int at = D == 64 ? mu * 32 : mu * 64 + half * 32;
+      const int sat = 8 * D + (D == 64 ? (mu & 7) * 8 : (mu & 7) * 16 + half * 8) - at;
       uint4 code[C::kKJobs][2];
       uint2 sc[C::kKJobs];
       // the tile (of 16 tokens) of job j and this lane, counted in the block
@@ -743,17 +783,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       auto load = [&]() {
 #pragma unroll
         for (int j = 0; j < C::kKJobs; ++j) {
-          code[j][0] = code[j][1] = make_uint4(0, 0, 0, 0);
-          sc[j] = make_uint2(0, 0);
-          if (page[j] >= 0 && page[j] < p.a.cache.pages) {
-            const int in = ((ld.first + lblk) * KB + tile_of(j) * 16) & (p.a.cache.page_size - 1);
-            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, in);
-            const int at = D == 64 ? mu * 32 : (D == 256 ? j * 1024 : 0) + mu * 64 + half * 32;
-            const int sat = 8 * D + (D == 64 ? (mu & 7) * 8 : (D == 256 ? j * 128 : 0) + (mu & 7) * 16 + half * 8);
-            code[j][0] = *reinterpret_cast<const uint4*>(tile + at);
-            code[j][1] = *reinterpret_cast<const uint4*>(tile + at + 16);
-            sc[j] = *reinterpret_cast<const uint2*>(tile + sat);
-          }
+          // (a page that is not there: page 0's, whose scores are masked)
+          const uint8_t* tile = tile_at<D>(p.a.cache, page[j], ld.h, (ld.first + lblk) * KB + tile_of(j) * 16) +
+                                (D == 256 ? j * 1024 : 0) + at;
+          code[j][0] = *reinterpret_cast<const uint4*>(tile);
+          code[j][1] = *reinterpret_cast<const uint4*>(tile + 16);
+          sc[j] = *reinterpret_cast<const uint2*>(tile + (D == 256 ? j * (128 - 1024) : 0) + sat);
         }
         if (++lblk == ld.end) {
           more = ld.next(p);
@@ -768,7 +803,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       uint32_t it = 0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
-        if (!pf_warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
+        if (!warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
 #pragma unroll
         for (int j = 0; j < C::kKJobs; ++j) {
           const uint32_t s4 = D == 64 ? __byte_perm(sc[j].x, sc[j].y, mu >> 3 ? 0x7531 : 0x6420)
@@ -801,6 +836,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       // ------------------------------------------------------------ V to f16, turned
       const int vw = warp - C::kWarpV;
       const int half = D == 64 ? (lane >> 3) & 1 : lane >> 4, o = D == 64 ? lane & 7 : lane & 15;
+      // the lane's codes in a tile: 8 columns of tokens 8 half + i; their scales
+      const int at0 = 9 * D + (D == 64 ? half * 256 : half * 512) + o * 4, at1 = 9 * D + half * 512 + ((o * 4) ^ 32);
+      const int sat = 17 * D + (o >> 1) * 16;
       uint32_t code[C::kVJobs][8];
       uint4 sc[C::kVJobs];
       int nvalid[C::kVJobs];   // of the lane's 8 tokens
@@ -825,21 +863,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
           const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
-          sc[j] = make_uint4(0, 0, 0, 0);
-          nvalid[j] = 0;
+          // (a page that is not there: page 0's, with scales taken as zero)
+          const uint8_t* tile = tile_at<D>(p.a.cache, page[j], ld.h, k) + block_of(j) * 1024;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) code[j][i] = 0;
-          if (page[j] >= 0 && page[j] < p.a.cache.pages) {
-            const uint8_t* tile = kv_tile<D>(p.a.cache, page[j], ld.h, k & (p.a.cache.page_size - 1));
-            const uint8_t* at = tile + 9 * D + block_of(j) * 1024;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 8 * half + i;
-              code[j][i] = *reinterpret_cast<const uint32_t*>(at + (D == 64 ? r * 32 + o * 4 : r * 64 + ((o * 4) ^ (((i >> 1) & 1) * 32))));
-            }
-            sc[j] = *reinterpret_cast<const uint4*>(tile + 17 * D + (block_of(j) * 8 + (o >> 1)) * 16);
-            nvalid[j] = min(8, max(ld.q.len - k - 8 * half, 0));
-          }
+          for (int i = 0; i < 8; ++i)
+            code[j][i] = *reinterpret_cast<const uint32_t*>(tile + ((i & 2) && D > 64 ? at1 : at0) + i * (D == 64 ? 32 : 64));
+          sc[j] = *reinterpret_cast<const uint4*>(tile + sat + block_of(j) * (128 - 1024));
+          nvalid[j] = page[j] >= 0 && page[j] < p.a.cache.pages ? min(8, max(ld.q.len - k - 8 * half, 0)) : 0;
         }
         if (++lblk == ld.end) {
           more = ld.next(p);
@@ -852,11 +882,17 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         load();
       }
       const int rot = o & 3, odd = (o >> 2) & 1;
+      uint32_t place[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d0 = 2 * ((e + rot) & 3) + odd;
+        place[e] = d0 * 128 + ((half ^ d0) << 4);
+      }
       const uint32_t rsel = rot == 0 ? 0x3210 : rot == 1 ? 0x0321 : rot == 2 ? 0x1032 : 0x2103;
       uint32_t it = 0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
-        if (!pf_warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
+        if (!warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
           if (job_of(j) >= C::kAllJobs) break;
@@ -870,13 +906,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             q[1] = nv > 4 ? q[1] & ((1u << (8 * (nv - 4))) - 1) : 0u;
             if (nv < 4) q[0] &= (1u << (8 * nv)) - 1;
           }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t bad = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            if (bad) {
-              q[k] &= ~((bad >> 7) * 0xFFu);
-              *reinterpret_cast<volatile int*>(&sh.nan_seg[segno & 7]) = segno + 1;
-            }
+          const uint32_t nan0 = ((q[0] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          const uint32_t nan1 = ((q[1] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          if (nan0 | nan1) {
+            q[0] &= ~((nan0 >> 7) * 0xFFu);
+            q[1] &= ~((nan1 >> 7) * 0xFFu);
+            *reinterpret_cast<volatile int*>(&sh.nan_seg[segno & 7]) = segno + 1;
           }
           uint32_t x[4][4], y[4][4];  // [d][pair of tokens]
 #pragma unroll
@@ -896,13 +931,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               y[e][i] = hmul2_u32(g[e], s);
             }
           }
-          const int ti = tile_of(j), chunk = (ti & 3) * 2 + half;
-          const uint32_t at = sV + stage * C::kKvBytes + (ti >> 2) * (D * 128) + block_of(j) * 16384 + o * 1024;
+          const int ti = tile_of(j);
+          const uint32_t to = sV + stage * C::kKvBytes + (ti >> 2) * (D * 128) + block_of(j) * 16384 + o * 1024;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int d0 = 2 * ((e + rot) & 3) + odd, d1 = 2 * ((e + rot) & 3) + 1 - odd;
-            st_shared_v4(at + d0 * 128 + ((chunk ^ d0) << 4), x[e][0], x[e][1], x[e][2], x[e][3]);
-            st_shared_v4(at + d1 * 128 + ((chunk ^ d1) << 4), y[e][0], y[e][1], y[e][2], y[e][3]);
+            // row d0 of the octet and its neighbour d0 ^ 1; 16-byte place (2 (ti & 3) + half) ^ row
+            const uint32_t at = place[e] ^ ((ti & 3) << 5);
+            st_shared_v4(to | at, x[e][0], x[e][1], x[e][2], x[e][3]);
+            st_shared_v4(to | (at ^ (128 + 16)), y[e][0], y[e][1], y[e][2], y[e][3]);
           }
         }
         fence_proxy_async_smem();
@@ -943,7 +979,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         mma_commit(pv_done + 8 * X);
       };
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && pf_wait(bar, parity, abort, p.wait_ns);
+        ok = ok && wait_for(bar, parity, abort, p.wait_ns);
         return ok;
       };
       for (; more; more = w.next(p)) {
