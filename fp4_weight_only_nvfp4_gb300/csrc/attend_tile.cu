@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       int more = 0;
       if (lane == 0) more = w.start(p, sh, cta0, cta1);
       more = __shfl_sync(0xffffffffu, more, 0);
-      uint32_t it = 0, turns = 0;                       // blocks of this row tile; bit 0: halves joined, bit 1: parts joined
+      uint32_t it = 0, s_turn = 0, turns = 0;           // blocks of this row tile; phases: of the score buffers; bit 0 halves joined, bit 1 parts joined
       while (more) {
         __syncwarp();
         const bool halved = w.halved(p);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           bool page_ok = pages_of(b0);
           const int key0 = w.first * KB;
           for (int blk = b0; blk < b1; blk += step, ++it) {
-            const uint32_t sbuf = SB == 2 ? (it & 1) : X, sphase = SB == 2 ? (it >> 1) & 1 : it & 1;
+            const uint32_t sbuf = SB == 2 ? (blk - b0) & 1 : X;
             const uint32_t tS = tmem + lanes + sbuf * KB;
             const uint32_t gone = ~__ballot_sync(0xffffffffu, page_ok) & ((1u << (KB / 16)) - 1);
             if (blk + step < b1) page_ok = pages_of(blk + step);
@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             const int hi = min(KB, max(row_hi - k0, 0));
             const int lo = min(KB, max(row_lo - k0, 0));
             const bool edge = __any_sync(0xffffffffu, hi < KB || lo > 0) || gone;
-            if (!(ok = warp_wait(s_full + 8 * sbuf, sphase, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(s_full + 8 * sbuf, (s_turn >> sbuf) & 1, abort, p.wait_ns))) break;
+            s_turn ^= 1u << sbuf;
             tc_fence_after();
             if (!idle) {
               uint32_t v[2][32];
@@ -566,15 +567,15 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                   tmem_st8(tS + KB / 2 + (c + h) / 2, pk);
                 }
               };
-              probabilities(v[0], KB - 64);
-              if (KB == 128) tmem_ld32_issue(tS, v[0]);
-              probabilities(v[1], KB - 32);
-              if (KB == 128) {
+#pragma unroll 1
+              for (int c = KB - 64;; c -= 64) {
+                probabilities(v[0], c);
+                if (c) tmem_ld32_issue(tS, v[0]);
+                probabilities(v[1], c + 32);
+                if (!c) break;
                 tmem_ld32_issue(tS + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_wait(v[1]);
-                probabilities(v[0], 0);
-                probabilities(v[1], 32);
               }
               float la, lb;
               split(add2(sum[0], sum[1]), la, lb);
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       // the tile (of 16 tokens) of job j and this lane, counted in the block
       auto tile_of = [&](int j) { return D == 64 ? 2 * kw + half : D == 128 ? kw + 4 * j : kw; };
       Walk<D> ld;
-      bool more = ld.start(p, sh, cta0, cta1), pending = more;   // a block to load; one loaded
+      bool more = ld.start(p, sh, cta0, cta1), pending = false;  // a block to load; one loaded
       int lblk = ld.at;
       int page[C::kKJobs];
       auto fetch = [&]() {  // pages of the block to be loaded next
@@ -796,10 +797,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         }
         if (more) fetch();
       };
-      if (more) {
-        fetch();
-        load();
-      }
+      if (more) fetch();
       uint32_t it = 0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
@@ -827,11 +825,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + 8 * stage);
         ++it;
-        pending = more;
-        if (more) load();  // in flight while the stages are full
         return true;
       };
-      while (pending && (ok = step())) {}
+      while ((!pending || (ok = step())) && more) {
+        load();  // in flight while the stages are full
+        pending = true;
+      }
+      
     } else if (warp < C::kWarpMma) {
       // ------------------------------------------------------------ V to f16, turned
       const int vw = warp - C::kWarpV;
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       auto tile_of = [&](int j) { return D == 64 ? 2 * job_of(j) + (lane >> 4) : D == 128 ? job_of(j) : job_of(j) & 3; };
       auto block_of = [&](int j) { return D == 256 ? job_of(j) >> 2 : 0; };
       Walk<D> ld;
-      bool more = ld.start(p, sh, cta0, cta1), pending = more;   // a block to load; one loaded
+      bool more = ld.start(p, sh, cta0, cta1), pending = false;  // a block to load; one loaded
       int lblk = ld.at;
       int page[C::kVJobs];
       auto fetch = [&]() {
@@ -877,10 +877,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         }
         if (more) fetch();
       };
-      if (more) {
-        fetch();
-        load();
-      }
+      if (more) fetch();
       const int rot = o & 3, odd = (o >> 2) & 1;
       uint32_t place[4];
 #pragma unroll
@@ -945,114 +942,77 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + 8 * stage);
         ++it;
-        pending = more;
-        if (more) load();
         return true;
       };
-      while (pending && (ok = step())) {}
+      while ((!pending || (ok = step())) && more) {
+        load();
+        pending = true;
+      }
+      
     } else {
       // ------------------------------------------------------------ the products
       if (elect_one()) {
-      constexpr uint32_t ids = idesc_f16(KB), ido = idesc_f16(D);
-      Walk<D> w;
-      bool more = w.start(p, sh, cta0, cta1);
-      uint32_t it = 0, done[2] = {0, 0}, segs[2] = {0, 0};
-      auto qk = [&](int X, uint32_t n, uint32_t sbuf) {  // scores of block n (of the CTA's)
-        const uint32_t ks = sK + (n & 1) * C::kKvBytes;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint64_t a = desc_sw128(sQ + X * C::kQBytes + c * 16384), b = desc_sw128(ks + c * (KB * 128));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f16(tmem + sbuf * KB, a + 2 * kk, b + 2 * kk, ids, c > 0 || kk > 0);
-        }
-        mma_commit(s_full + 8 * sbuf);
-      };
-      auto pv = [&](int X, uint32_t n, uint32_t sbuf, bool add) {
-        const uint32_t vs = sV + (n & 1) * C::kKvBytes;
-#pragma unroll
-        for (int c = 0; c < KB / 64; ++c) {
-          const uint64_t b = desc_sw128(vs + c * (D * 128));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ta(tmem + C::kTmemO + X * D, tmem + sbuf * KB + KB / 2 + (c * 4 + kk) * 8, b + 2 * kk, ido, add || c > 0 || kk > 0);
-        }
-        mma_commit(pv_done + 8 * X);
-      };
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && wait_for(bar, parity, abort, p.wait_ns);
-        return ok;
-      };
-      for (; more; more = w.next(p)) {
-        const int rt = w.row_tiles(p), n = w.end - w.at;
-        if (w.halved(p)) {  // blocks to the two in turn
-          const int ahead = n < 2 ? n : 2;
-          for (int X = 0; X < ahead; ++X) {
-            const uint32_t nx = it + X;
-            if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1) || !wait(q_full + 8 * X, segs[X] & 1)) break;
-            ++segs[X];
-            tc_fence_after();
-            qk(X, nx, X);
-            mma_commit(k_empty + 8 * (nx & 1));
-          }
-          for (int j = 0; ok && j < n; ++j, ++it) {
-            const int X = j & 1;
-            const uint32_t nx = it + 2;
-            if (!wait(p_full + 8 * X, done[X] & 1) || !wait(v_full + 8 * (it & 1), (it >> 1) & 1)) break;
-            tc_fence_after();
-            pv(X, it, X, j > 1);
-            ++done[X];
-            mma_commit(v_empty + 8 * (it & 1));
-            if (j + 2 < n) {
-              if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
+        constexpr uint32_t ids = idesc_f16(KB), ido = idesc_f16(D);
+        uint32_t it = 0, q_turn = 0, p_turn = 0;  // blocks before this segment; phases, a bit per row tile or buffer
+        auto wait = [&](uint32_t bar, uint32_t parity) { return ok = ok && wait_for(bar, parity, abort, p.wait_ns); };
+        Walk<D> w;
+        for (bool more = w.start(p, sh, cta0, cta1); more && ok; more = w.next(p)) {
+          // A task is the two products of one row tile with one block: (block, row tile) in turn, or
+          // the blocks alone where there is one row tile.  Task t takes score buffer t & 1; its
+          // scores are issued two tasks ahead of its P V, behind the P V that read the buffer last.
+          const bool both = w.row_tiles(p) == 2, halved = w.halved(p);
+          const int tasks = (w.end - w.at) << (both ? 1 : 0);
+#pragma unroll 1
+          for (int u = 0; u < tasks + 2 && ok; ++u) {
+            if (u >= 2) {
+              const int t = u - 2, blk = both ? t >> 1 : t;
+              const uint32_t n = it + blk, sbuf = t & 1, X = C::kRowTiles == 2 ? sbuf : 0;
+              if (!wait(p_full + 8 * sbuf, (p_turn >> sbuf) & 1)) break;
+              if (!(both && sbuf) && !wait(v_full + 8 * (n & 1), (n >> 1) & 1)) break;
+              p_turn ^= 1u << sbuf;
               tc_fence_after();
-              qk(X, nx, X);
-              mma_commit(k_empty + 8 * (nx & 1));
+              uint32_t add = blk > (halved ? 1 : 0);
+              const uint64_t vd = desc_sw128(sV + (n & 1) * C::kKvBytes);
+              const uint32_t pt = tmem + sbuf * KB + KB / 2;
+#pragma unroll 1
+              for (int c = 0; c < KB / 64; ++c) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  mma_f16_ta(tmem + C::kTmemO + X * D, pt + (c * 4 + kk) * 8, vd + c * (D * 8) + 2 * kk, ido, add);
+                  add = 1;
+                }
+              }
+              mma_commit(pv_done + 8 * X);
+              if (!both || sbuf) mma_commit(v_empty + 8 * (n & 1));
+            }
+            if (u < tasks) {
+              const uint32_t n = it + (both ? u >> 1 : u), sbuf = u & 1, X = both || halved ? sbuf : 0;
+              if (!(both && sbuf) && !wait(k_full + 8 * (n & 1), (n >> 1) & 1)) break;
+              if (u < (both || halved ? 2 : 1)) {
+                if (!wait(q_full + 8 * X, (q_turn >> X) & 1)) break;
+                q_turn ^= 1u << X;
+              }
+              tc_fence_after();
+              const uint64_t qd = desc_sw128(sQ + X * C::kQBytes), kd = desc_sw128(sK + (n & 1) * C::kKvBytes);
+              uint32_t add = 0;
+#pragma unroll 1
+              for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  mma_f16(tmem + sbuf * KB, qd + c * 1024 + 2 * kk, kd + c * (KB * 8) + 2 * kk, ids, add);
+                  add = 1;
+                }
+              }
+              mma_commit(s_full + 8 * sbuf);
+              if (!both || sbuf) mma_commit(k_empty + 8 * (n & 1));
             }
           }
-          if (!ok) break;
-          continue;
+          it += w.end - w.at;
         }
-        if (!wait(k_full + 8 * (it & 1), (it >> 1) & 1)) break;
-        for (int X = 0; X < rt; ++X) {
-          if (!wait(q_full + 8 * X, segs[X] & 1)) break;
-          ++segs[X];
-          tc_fence_after();
-          qk(X, it, SB == 2 ? (done[0] & 1) : X);
-        }
-        if (!ok) break;
-        mma_commit(k_empty + 8 * (it & 1));
-        for (int j = 0; j < n; ++j, ++it) {
-          const bool on = j + 1 < n;
-          const uint32_t nx = it + 1;
-          if (SB == 2 && on) {
-            if (!wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
-            tc_fence_after();
-            qk(0, nx, (done[0] + 1) & 1);
-            mma_commit(k_empty + 8 * (nx & 1));
-          }
-          for (int X = 0; X < rt; ++X) {
-            const uint32_t sbuf = SB == 2 ? (done[0] & 1) : X;
-            if (!wait(p_full + 8 * sbuf, (SB == 2 ? done[0] >> 1 : done[X]) & 1)) break;
-            if (X == 0 && !wait(v_full + 8 * (it & 1), (it >> 1) & 1)) break;
-            tc_fence_after();
-            pv(X, it, sbuf, j > 0);
-            ++done[X];
-            if (SB == 1 && on) {
-              if (X == 0 && !wait(k_full + 8 * (nx & 1), (nx >> 1) & 1)) break;
-              tc_fence_after();
-              qk(X, nx, X);
-            }
-          }
-          if (!ok) break;
-          mma_commit(v_empty + 8 * (it & 1));
-          if (SB == 1 && on) mma_commit(k_empty + 8 * (nx & 1));
-        }
-        if (!ok) break;
-      }
-      // every product issued has completed once this arrives
-      mma_commit(drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
+        // every product issued has completed once this arrives
+        mma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs) {}
       }
     }
     if (!ok && (lane == 0 || warp == C::kWarpMma)) atomicExch(reinterpret_cast<int*>(p.a.workspace), 5);
