@@ -38,7 +38,7 @@ namespace {
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kTileBias = 7.0f;   // P = 2^(s - m + 7): below 2^15 while s - m <= 8
 constexpr float kSlack = 8.0f;
-constexpr int kLead = 3;
+constexpr int kLead = 6;
 
 template <int D>
 struct TileCfg {
@@ -80,6 +80,7 @@ struct TileShared {
   int abort;
   alignas(8) uint64_t bars[24];
   alignas(16) uint8_t walk[8 * 96];  // of each softmax warp
+  alignas(16) int row[256][4];       // of each softmax thread: first key, end of the keys, factor of the scores
 };
 
 struct TileParams {
@@ -413,13 +414,18 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       int more = 0;
       if (lane == 0) more = w.start(p, sh, cta0, cta1);
       more = __shfl_sync(0xffffffffu, more, 0);
-      uint32_t it = 0, s_turn = 0, turns = 0;           // blocks of this row tile; phases: of the score buffers; bit 0 halves joined, bit 1 parts joined
+      // Phases and flags in one register: bits 0, 1 the score buffers, 2 P V done, 3 halves joined, 4 parts
+      // joined, 5 some key seen, 6 a block before this one in the segment.  What else the block loop
+      // does not need in registers is in shared memory (a spill would go through an L1 of a few KB).
+      constexpr uint32_t kPv = 4, kHalf = 8, kPart = 16, kAny = 32, kLater = 64;
+      uint32_t st = 0;
+      const uint32_t row_at = smem_u32(sh.row[tid]);
       while (more) {
         __syncwarp();
         const bool halved = w.halved(p);
         // blocks from `b0` on, every `step`-th; the second half of one block is empty
-        const int b0 = w.at + (halved ? X : 0), step = halved ? 2 : 1, b1 = w.end;
-        const bool mine_seg = b0 < b1;
+        const int b0 = w.at + (halved ? X : 0);
+        const bool mine_seg = b0 < w.end;
         const int XR = halved ? 0 : X;                  // whose rows
         const int idx = w.i * per_tile + XR * p.tokens + r / p.a.group;
         const bool live = mine_seg && r / p.a.group < p.tokens && idx < w.q.n;
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         const int row_hi = live ? max(seen, 0) : 0x7FFFFFFF;
         const int row_lo = live && p.a.window > 0 && p.a.window < row_hi ? row_hi - (int)p.a.window : 0;
         float m = -INFINITY, l = 0.0f;
-        bool any = false;
+        st &= ~(kAny | kLater);
         if (mine_seg) {
           // ---- Q
           // LR lanes take a row 16 bytes each, so that a load meets few lines; a lane keeps the power of
@@ -462,8 +468,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               st_shared_v4(qwarp + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), f.x ^ sign, f.y ^ sign, f.z ^ sign, f.w ^ sign);
             }
           }
-          float mul = fabsf(unit) * pow2f(pw);
-          if (mul == 0.0f) mul = 1e-38f;  // every score 0, a masked one (-inf) stays out
+          float factor = fabsf(unit) * pow2f(pw);
+          if (factor == 0.0f) factor = 1e-38f;  // every score 0, a masked one (-inf) stays out
+          st_shared_v4(row_at, row_lo, row_hi, __float_as_uint(factor), 0);
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -478,19 +485,20 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             return page >= 0 && page < p.a.cache.pages;
           };
           bool page_ok = pages_of(b0);
-          const int key0 = w.first * KB;
-          for (int blk = b0; blk < b1; blk += step, ++it) {
-            const uint32_t sbuf = SB == 2 ? (blk - b0) & 1 : X;
+#pragma unroll 1
+          for (int blk = b0; blk < w.end; blk += halved ? 2 : 1) {
+            const uint32_t sbuf = SB == 2 ? (blk - w.at) & 1 : X;
             const uint32_t tS = tmem + lanes + sbuf * KB;
             const uint32_t gone = ~__ballot_sync(0xffffffffu, page_ok) & ((1u << (KB / 16)) - 1);
-            if (blk + step < b1) page_ok = pages_of(blk + step);
-            const int k0 = key0 + blk * KB;
+            if (blk + (halved ? 2 : 1) < w.end) page_ok = pages_of(blk + (halved ? 2 : 1));
+            const int k0 = (w.first + blk) * KB;
             // columns [lo, hi) that the row sees
-            const int hi = min(KB, max(row_hi - k0, 0));
-            const int lo = min(KB, max(row_lo - k0, 0));
+            const uint2 sees = ld_shared_v2(row_at);
+            const int hi = min(KB, max((int)sees.y - k0, 0));
+            const int lo = min(KB, max((int)sees.x - k0, 0));
             const bool edge = __any_sync(0xffffffffu, hi < KB || lo > 0) || gone;
-            if (!(ok = warp_wait(s_full + 8 * sbuf, (s_turn >> sbuf) & 1, abort, p.wait_ns))) break;
-            s_turn ^= 1u << sbuf;
+            if (!(ok = warp_wait(s_full + 8 * sbuf, (st >> sbuf) & 1, abort, p.wait_ns))) break;
+            st ^= 1u << sbuf;
             tc_fence_after();
             if (!idle) {
               uint32_t v[2][32];
@@ -504,13 +512,15 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                   tmem_st32(tS + c, v[0]);
                 }
                 tmem_st_wait();
-                any |= lo < hi && !gone;
+                bool some = lo < hi;
                 if (gone) {
+                  some = false;
                   for (int g = 0; g < KB / 16; ++g)
-                    any |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
+                    some |= !((gone >> g) & 1) && max(lo, g * 16) < min(hi, g * 16 + 16);
                 }
+                if (some) st |= kAny;
               } else {
-                any = true;
+                st |= kAny;
               }
               // the maximum; the last 64 scores stay in registers
               float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -530,10 +540,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 }
               }
               const float best = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+              const float mul = __uint_as_float(ld_shared_v2(row_at + 8).x);
               const float mx = best == -INFINITY ? best : best * mul;
               const float mn = (m == -INFINITY || mx > m + kSlack) ? fmaxf(m, mx) : m;
-              if (blk > b0 && __any_sync(0xffffffffu, mn > m)) {
-                if (!(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+              if ((st & kLater) && __any_sync(0xffffffffu, mn > m)) {
+                if (!(ok = warp_wait(pv_done + 8 * X, !(st & kPv), abort, p.wait_ns))) break;
                 tc_fence_after();
                 const float f = mn > m ? fast_exp2(m - mn) : 1.0f;
                 l *= f;
@@ -584,17 +595,19 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             // With two score buffers this block's scores do not say that the last block's P V is done.  It is
             // waited for here, one phase at a time: a wait on a phase takes the one before it for done.
-            if (SB == 2 && blk > b0 && !(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+            if (SB == 2 && (st & kLater) && !(ok = warp_wait(pv_done + 8 * X, !(st & kPv), abort, p.wait_ns))) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + 8 * sbuf);
+            st = (st ^ kPv) | kLater;
           }
           if (!ok) break;
-          if (!(ok = warp_wait(pv_done + 8 * X, (it - 1) & 1, abort, p.wait_ns))) break;
+          if (!(ok = warp_wait(pv_done + 8 * X, !(st & kPv), abort, p.wait_ns))) break;
           tc_fence_after();
         }
         // ---- the two halves of a single row tile: the second's sums to the first
         const bool other = halved && w.end - w.at > 1;
+        bool any = st & kAny;
         float f0 = 1.0f, f1 = 0.0f;
         if (other) {
           if (X == 1) {
@@ -603,9 +616,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             sh.half_any[r] = any;
             __syncwarp();
             if (lane == 0) mbar_arrive(half_full);
-            if (!(ok = warp_wait(half_read, turns & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(half_read, (st & kHalf) != 0, abort, p.wait_ns))) break;
           } else {
-            if (!(ok = warp_wait(half_full, turns & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(half_full, (st & kHalf) != 0, abort, p.wait_ns))) break;
             tc_fence_after();
             const float m1 = sh.half_m[r], mt = fmaxf(m, m1), ms = mt == -INFINITY ? 0.0f : mt;
             f0 = fast_exp2(m - ms);
@@ -614,7 +627,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             any |= sh.half_any[r] != 0;
             m = mt;
           }
-          turns ^= 1;
+          st ^= kHalf;
         }
         const bool out = mine_seg && !(halved && X == 1);
         const bool whole = w.whole();
@@ -695,7 +708,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
           if (warp == 0) {
-            if (!(ok = warp_wait(joined, (turns >> 1) & 1, abort, p.wait_ns))) break;
+            if (!(ok = warp_wait(joined, (st & kPart) != 0, abort, p.wait_ns))) break;
             if (lane == 0) {
               uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + 256) + c0;
               __threadfence();
@@ -707,8 +720,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             }
             __syncwarp();
           }
-          if (!(ok = warp_wait(told, (turns >> 1) & 1, abort, p.wait_ns))) break;
-          turns ^= 2;
+          if (!(ok = warp_wait(told, (st & kPart) != 0, abort, p.wait_ns))) break;
+          st ^= kPart;
           if (*reinterpret_cast<volatile int*>(&sh.last)) {
             const int n = (int)(c1 - c0) + 1;
             // CTA c0's part is in its slot 1, the others' in their slot 0
