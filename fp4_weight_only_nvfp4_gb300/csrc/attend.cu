@@ -3,13 +3,14 @@
 
 namespace vt {
 
+// Each kernel has its parts and its arrival counts.
 size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int head_dim) {
-  const size_t row = attend_row_parts_bytes(head_dim), tile = attend_tile_parts_bytes(head_dim);
-  return kAttendCleared + (row > tile ? row : tile);
+  return kAttendCleared + attend_row_parts_bytes(head_dim) + attend_tile_parts_bytes(head_dim);
 }
 
 cudaError_t launch_attend(const AttendLaunch& L, int head_dim, cudaStream_t s) {
-  return L.starts ? launch_attend_tile(L, head_dim, s) : launch_attend_row(L, head_dim, s);
+  if (cudaError_t e = launch_attend_row(L, head_dim, s)) return e;
+  return L.starts ? launch_attend_tile(L, head_dim, s) : cudaSuccess;
 }
 
 }  // namespace vt

@@ -6,6 +6,8 @@ namespace vt {
 
 constexpr int kAttendCleared = 4096;  // status word and arrival counts, zeros between calls
 constexpr int kMaxAttendGrid = 160;
+constexpr int kRowCounts = 256, kTileCounts = 2048;  // of the arrival counts, bytes
+static_assert(kRowCounts + 4 * kMaxAttendGrid <= kTileCounts && kTileCounts + 4 * kMaxAttendGrid <= kAttendCleared, "counts");
 constexpr float kLog2e = 1.4426950408889634f;
 // Probabilities are held as 2^(s - m + kPBias): in f16 those down to 2^-26 of the row's largest
 // then keep all their bits (2^-36: the last bit), and their sum over a long row what they add.
@@ -25,9 +27,22 @@ __device__ __forceinline__ int seq_len(const AttendLaunch& a, int64_t b) {
   const int64_t most = a.ldt << a.cache.page_shift, n = __ldg(a.lens + b);
   return (int)(n < 0 ? 0 : n > most ? most : n);
 }
-__device__ __forceinline__ int first_key(const AttendLaunch& a, int len) {
-  return a.window > 0 && a.window < len ? len - (int)a.window : 0;
+// Its rows and keys, whatever starts and lens hold.
+struct AttendSeq {
+  int s0, n, len;
+};
+__device__ __forceinline__ AttendSeq load_seq(const AttendLaunch& a, int64_t b) {
+  AttendSeq q;
+  const int T = (int)a.T, s = __ldg(a.starts + b), e = __ldg(a.starts + b + 1);
+  q.s0 = s < 0 ? 0 : s > T ? T : s;
+  q.n = (e < q.s0 ? q.s0 : e > T ? T : e) - q.s0;
+  q.len = seq_len(a, b);
+  return q;
 }
+// Which kernel takes a sequence of n rows (with starts): up to kFewColumns rows x query heads of a
+// key/value head go 8 at a time through the row kernel, more as tiles of 128 rows.
+constexpr int kFewColumns = 32;
+__device__ __forceinline__ bool few_rows(const AttendLaunch& a, int n) { return (int64_t)n * a.group <= kFewColumns; }
 
 // What a row's sum of p v is multiplied by: the values' global over the sum of p and the sink's
 // share (m in log2 units; p and l hold 2^bias).

@@ -1,10 +1,11 @@
-// Attention of one row per sequence over the paged NVFP4 cache (the decode step).
+// Attention of few rows per sequence over the paged NVFP4 cache (the decode step, drafted tokens).
 //
 //   S^T = K Q^T,  p = 2^(s - m),  O^T = V^T P^T,  out = O / sum p
-// with 16 tokens x 8 query heads of one key/value head as one m16n8k16 product's rows and columns.
+// with 16 tokens x 8 columns of one key/value head as one m16n8k16 product's rows and columns; a column is
+// a query head of a row, and a sequence's rows x heads go in sets of 8.
 // Bound by the cache's bytes (9/16 per value) and close behind by the instructions that turn them into f16: a
 // conversion and a product for every two values (c * s is exact in f16).  So the cache is read once
-// for up to 8 query heads, every lane's codes are fragments as they lie (see kv.cuh), and the
+// for up to 8 columns, every lane's codes are fragments as they lie (see kv.cuh), and the
 // probabilities go from the first product's result to the second's operand by a transpose of
 // registers.
 //
@@ -38,7 +39,7 @@ struct RowCfg {
   static constexpr int kTile = kv_tile_bytes(D);
   static constexpr int kStageBytes = kTiles * kTile;        // 4608, 4608, 9216
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kPartFloats = kHeads * (D + 2) + 16; // O [8][D], m [8], l [8], any
+  static constexpr int kPartFloats = kHeads * (D + 3) + 8; // O [8][D], m [8], l [8], any [8]
   static constexpr int kPartBytes = kPartFloats * 4;
   static_assert(kPartBytes <= kRing && kPartBytes % 16 == 0, "a part fits a warp's ring");
   static constexpr int kOffPart = kWarps * kRing;           // the parts that end inside a warp's range
@@ -53,6 +54,7 @@ struct PartMeta {
   int b, hu;
   int used;
 };
+static_assert(sizeof(PartMeta) == 40, "meta");
 struct RowShared {
   PartMeta part[32];       // [warp][0: ended inside the range, 1: the last]
   int64_t scan[32];
@@ -60,37 +62,69 @@ struct RowShared {
   int start_b[16];
   int runs, run_first[33];
   int last;
+  uint32_t lost[16 * 32];  // of each lane: columns whose sums a NaN scale reaches, 8 bits a column block
 };
 
 struct RowParams {
   AttendLaunch a;
   int G;         // CTAs
-  int subs;      // sets of 8 query heads per key/value head
 };
+
+// A sequence as this kernel takes it: n = 0 where the other kernel does.
+struct RowSeq {
+  int s0, n, len;
+};
+__device__ __forceinline__ RowSeq row_seq(const AttendLaunch& a, int b) {
+  if (!a.starts) return {b, 1, seq_len(a, b)};
+  const AttendSeq q = load_seq(a, b);
+  return {q.s0, few_rows(a, q.n) ? q.n : 0, q.len};
+}
+// Sets of 8 columns per key/value head.
+__device__ __forceinline__ int row_sets(const AttendLaunch& a, int n) { return (n * a.group + kHeads - 1) / kHeads; }
+template <int D>
+__device__ __forceinline__ void row_chunks(const AttendLaunch& a, const RowSeq& q, int* c0, int* nb) {
+  // keys from the first that the first row sees to the last row's own
+  const int64_t first = a.window > 0 ? (int64_t)q.len - q.n + 1 - a.window : 0;
+  *c0 = first > 0 ? (int)(first / RowCfg<D>::kChunk) : 0;
+  *nb = q.n > 0 ? (int)(((int64_t)q.len + RowCfg<D>::kChunk - 1) / RowCfg<D>::kChunk) - *c0 : 0;
+}
 
 // A chunk of the line.
 template <int D>
 struct Cursor {
-  int b, hu, c, nb, c0, len, lo;
-  int64_t seg0;
+  int b, hu, c, nb, c0, len;
+  int sets, kvh;   // hu: kvh * sets + the set
   __device__ __forceinline__ void sequence(const RowParams& p) {
-    len = seq_len(p.a, b);
-    lo = first_key(p.a, len);
-    c0 = lo / RowCfg<D>::kChunk;
-    nb = (len + RowCfg<D>::kChunk - 1) / RowCfg<D>::kChunk - c0;
+    const RowSeq q = row_seq(p.a, b);
+    len = q.len;
+    row_chunks<D>(p.a, q, &c0, &nb);
+    sets = row_sets(p.a, q.n);
   }
-  __device__ __forceinline__ void advance(const RowParams& p, int HU) {
-    if (++c < nb) return;
+  // To the next (sequence, head, set).
+  __device__ __forceinline__ void next(const RowParams& p) {
     c = 0;
-    seg0 += nb;
-    if (++hu < HU) return;
-    hu = 0;
+    kvh = ++hu / sets;
+    if (kvh < p.a.cache.heads) return;
+    hu = kvh = 0;
     do {
       if (++b >= p.a.B) { nb = 0; return; }
       sequence(p);
     } while (nb == 0);
   }
 };
+
+// Column i of a set: its row of the sequence and its query head; false past the last.
+__device__ __forceinline__ bool column_of(const RowParams& p, const RowSeq& q, int hu, int i, int* row, int* head) {
+  const int sets = row_sets(p.a, q.n), kvh = hu / sets, at = (hu - kvh * sets) * kHeads + i;
+  *row = at / p.a.group;
+  *head = kvh * p.a.group + at - *row * p.a.group;
+  return *row < q.n;
+}
+// Keys [lo, hi) that a row of the sequence sees.
+__device__ __forceinline__ int row_hi(const RowSeq& q, int row) { return max(q.len - q.n + row + 1, 0); }
+__device__ __forceinline__ int row_lo(const AttendLaunch& a, int hi) {
+  return a.window > 0 && a.window < hi ? hi - (int)a.window : 0;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -161,7 +195,7 @@ __device__ __forceinline__ void join_head(const float* parts, int64_t stride, in
   for (int i = lane; i < n; i += 32) {
     const float* q = parts + i * stride + kHeads * D;
     m = fmaxf(m, ld(q + h));
-    any |= ld(q + 2 * kHeads) != 0.0f;
+    any |= ld(q + 2 * kHeads + h) != 0.0f;
   }
 #pragma unroll
   for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -198,16 +232,45 @@ template <int D>
 __device__ __forceinline__ void store_row(const RowParams& p, int b, int hu, int h, float (&o)[D / 32], float m,
                                           float l, bool any) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, kvh = hu / p.subs, inner = (hu % p.subs) * kHeads + h;
-  if (inner >= p.a.group) return;
-  const int head = kvh * p.a.group + inner;
+  const int lane = threadIdx.x & 31;
+  const RowSeq q = row_seq(p.a, b);
+  int row, head;
+  if (!column_of(p, q, hu, h, &row, &head)) return;
   float f = 0.0f;
-  if (any) f = out_factor(p.a, head, kvh, m, l, kPBias);
-  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + b * p.a.ldo + (int64_t)head * D + lane * E;
+  if (any) f = out_factor(p.a, head, head / p.a.group, m, l, kPBias);
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + row) * p.a.ldo + (int64_t)head * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(dst + e) =
         any ? __floats2bfloat162_rn(o[e] * f, o[e + 1] * f) : __floats2bfloat162_rn(0.0f, 0.0f);
+}
+
+// Tokens of `partly` (bit 4 i + k: token t + 4 k of tile i) whose value scales, of the lane's columns,
+// hold a NaN: they leave the product, where it would reach columns that do not see them, and those that do
+// are noted in *lost.  Returns them, those of a second column block 16 bits up.
+template <int D>
+__device__ __noinline__ uint32_t nan_partly(const RowParams& p, const RowSeq& q, int hu, uint32_t st, int tok0, uint32_t partly,
+                                            uint32_t* lost) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint32_t out = 0;
+  for (int i = 0; i < 4 * RowCfg<D>::kTiles; ++i) {
+    if (!((partly >> i) & 1)) continue;
+    const int tok = tok0 + (i >> 2) * kKvTile + t + 4 * (i & 3);
+    for (int c = 0; c < (D == 256 ? 2 : 1); ++c) {
+      const int group = D == 64 ? g >> 1 : 8 * c + g;
+      uint32_t w;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(st + (i >> 2) * kv_tile_bytes(D) + 17 * D + group * 16 + t * 4));
+      if (((w >> (8 * (i & 3))) & 0x7F) != 0x7F) continue;
+      out |= 1u << (16 * c + i);
+      for (int k = 0; k < kHeads; ++k) {
+        int row, head;
+        if (!column_of(p, q, hu, k, &row, &head)) continue;
+        const int hi = row_hi(q, row);
+        if (tok >= row_lo(p.a, hi) && tok < hi) *lost |= 1u << (8 * c + k);
+      }
+    }
+  }
+  return out;
 }
 
 template <int D>
@@ -218,42 +281,59 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   extern __shared__ __align__(128) uint8_t smem[];
   RowShared& sh = *reinterpret_cast<RowShared*>(smem + C::kOffMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int B = (int)p.a.B, HU = p.a.cache.heads * p.subs;
+  const int B = (int)p.a.B;
 
-  // ---- the line: chunks of every sequence, and where this CTA's warps begin
-  auto chunks = [&](int b) {
-    const int len = seq_len(p.a, b), lo = first_key(p.a, len);
-    return (len + C::kChunk - 1) / C::kChunk - lo / C::kChunk;
-  };
-  // a sequence without keys has no chunk: its row is zeros
-  for (int b = blockIdx.x * C::kWarps + warp; b < B; b += p.G * C::kWarps)
-    if (seq_len(p.a, b) == 0) {
-      uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + b * p.a.ldo);
-      for (int i = lane; i < p.a.q_heads * D / 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+  // ---- the line: chunks of every sequence times its heads and sets, and where this CTA's warps begin
+  auto units = [&](int b) -> int64_t {
+    if (b >= B) return 0;
+    const RowSeq q = row_seq(p.a, b);
+    int c0, nb;
+    row_chunks<D>(p.a, q, &c0, &nb);
+    if (q.n > 0 && q.len == 0) {  // no key: its rows are zeros
+      for (int i = blockIdx.x; i < q.n; i += gridDim.x) {
+        uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + i) * p.a.ldo);
+        for (int e = 0; e < p.a.q_heads * D / 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+      }
     }
-  int64_t sum = 0;
-  for (int b = tid; b < B; b += C::kThreads) sum += chunks(b);
-  const int64_t total = block_total<C::kWarps>(sum, sh.scan);
-  const int64_t U = total * HU;
+    return (int64_t)nb * (p.a.cache.heads * row_sets(p.a, q.n));
+  };
+  int64_t U = 0, n = 0, before = 0;
+  if (B <= C::kThreads) {
+    n = units(tid);
+    before = block_prefix<C::kWarps>(n, sh.scan, &U);
+  } else {
+    for (int b = tid; b < B; b += C::kThreads) n += units(b);
+    U = block_total<C::kWarps>(n, sh.scan);
+  }
   if (U == 0) return;
-  const int64_t G = min((int64_t)p.G, (U + C::kWarps - 1) / C::kWarps);
+  // a CTA has a chunk for every warp; as a multiple of the (head, set) lines, where there is room,
+  // equal lines end where CTAs end
+  int64_t G = min((int64_t)p.G, (U + C::kWarps - 1) / C::kWarps);
+  const int64_t lines = (int64_t)B * p.a.cache.heads * row_sets(p.a, 1);
+  if (lines <= p.G) G = min(U, min((G + lines - 1) / lines, (int64_t)p.G / lines) * lines);
   if (blockIdx.x >= G) return;
   const int64_t cta0 = blockIdx.x * U / G, cta1 = (blockIdx.x + 1) * U / G, mine = cta1 - cta0;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < B; b0 += C::kThreads) {
-    const int b = b0 + tid;
-    const int n = b < B ? chunks(b) : 0;
-    int64_t round;
-    const int64_t before = base + block_prefix<C::kWarps>(n, sh.scan, &round);
+  auto starts_in = [&](int b) {  // warps whose first chunk is one of sequence b's
+    if (before + n <= cta0 || before >= cta1) return;
 #pragma unroll 1
     for (int w = 0; w < C::kWarps; ++w) {
       const int64_t u = cta0 + mine * w / C::kWarps;
-      if (u >= before * HU && u < (before + n) * HU) {
+      if (u >= before && u < before + n) {
         sh.start_b[w] = b;
         sh.start_prefix[w] = before;
       }
     }
-    base += round;
+  };
+  if (B <= C::kThreads) {
+    starts_in(tid);
+  } else {
+    int64_t base = 0, round;
+    for (int b0 = 0; b0 < B; b0 += C::kThreads) {
+      n = units(b0 + tid);
+      before = base + block_prefix<C::kWarps>(n, sh.scan, &round);
+      starts_in(b0 + tid);
+      base += round;
+    }
   }
   if (tid < 32) sh.part[tid].used = 0;
   __syncthreads();
@@ -264,10 +344,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     Cursor<D> cur;
     cur.b = sh.start_b[warp];
     cur.sequence(p);
-    const int64_t r = u0 - sh.start_prefix[warp] * HU;
+    const int64_t r = u0 - sh.start_prefix[warp];
     cur.hu = (int)(r / cur.nb);
+    cur.kvh = cur.hu / cur.sets;
     cur.c = (int)(r - (int64_t)cur.hu * cur.nb);
-    cur.seg0 = u0 - cur.c;
     Cursor<D> ld = cur;
     const int total_chunks = (int)(u1 - u0);
     int issued = 0;
@@ -282,21 +362,26 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     auto issue = [&]() {
       const bool ok = page >= 0 && page < p.a.cache.pages;
       const int tok = (ld.c0 + ld.c) * C::kChunk + lane * kKvTile;
-      const uint8_t* src = kv_tile<D>(p.a.cache, ok ? page : 0, ld.hu / p.subs, tok & (p.a.cache.page_size - 1));
+      const uint8_t* src = kv_tile<D>(p.a.cache, ok ? page : 0, ld.kvh, tok & (p.a.cache.page_size - 1));
       const uint32_t there = __ballot_sync(0xffffffffu, ok) & ((1u << C::kTiles) - 1);
       valid_fifo |= there << (4 * (issued < kStages ? issued : kStages - 1));
-      const uint32_t dst = ring + (issued % kStages) * C::kStageBytes;
-      constexpr int PT = C::kTile / 16;  // 16-byte pieces of a tile
+      const uint32_t dst = ring + (issued % kStages) * C::kStageBytes + lane * 16;
+      constexpr int PT = C::kTile / 16;  // 16-byte pieces of a tile, 32 at a time
+      const uint8_t* from[C::kTiles];
+#pragma unroll
+      for (int i = 0; i < C::kTiles; ++i)
+        from[i] = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(0xffffffffu, (uint64_t)(uintptr_t)src, i)) +
+                  lane * 16 - i * C::kTile;
 #pragma unroll
       for (int j = 0; j < C::kStageBytes / 512; ++j) {
-        const int piece = j * 32 + lane, tile = piece / PT;
-        const uint64_t from = __shfl_sync(0xffffffffu, (uint64_t)(uintptr_t)src, tile);
-        if ((there >> tile) & 1)
-          cp_async16(dst + piece * 16, reinterpret_cast<const uint8_t*>((uintptr_t)from) + (piece - tile * PT) * 16);
+        constexpr int last = C::kTiles - 1;
+        const int t0 = j * 32 / PT, t1 = (j * 32 + 31) / PT < last ? (j * 32 + 31) / PT : last;
+        const bool second = t1 > t0 && lane >= t1 * PT - j * 32;
+        if ((there >> (second ? t1 : t0)) & 1) cp_async16(dst + j * 512, (second ? from[t1] : from[t0]) + j * 512);
       }
       ++issued;
       if (issued < total_chunks) {
-        ld.advance(p, HU);
+        if (++ld.c == ld.nb) ld.next(p);
         page = page_of();
       }
     };
@@ -309,15 +394,17 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     uint32_t q[KS][2];       // B fragments: column g (a head), k = the lane's own columns
     float mul[2];            // of heads 2t and 2t + 1: raw products to log2 units
     float o[KS][4], m[2], l[2];
-    bool any = false;
-    int first_c = cur.c;
+    uint32_t any = 0;         // bit i: column 2t + i has seen a key
+    int first_c = cur.c, all_lo, all_hi;   // keys [all_lo, all_hi) are seen by every column
     auto begin = [&]() {
-      const int kvh = cur.hu / p.subs, sub = cur.hu % p.subs, inner = sub * kHeads + g;
+      const RowSeq sq = row_seq(p.a, cur.b);
+      int row, head;
+      const bool on = column_of(p, sq, cur.hu, g, &row, &head);
       uint4 w[KS / 2];
       int mx = 0;
-      if (inner < p.a.group) {
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + cur.b * p.a.ldq +
-                                   (int64_t)(kvh * p.a.group + inner) * D + (D == 64 ? 16 : 32) * t;
+      if (on) {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(sq.s0 + row) * p.a.ldq +
+                                   (int64_t)head * D + (D == 64 ? 16 : 32) * t;
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i)
           w[i] = *reinterpret_cast<const uint4*>(src + (D == 256 ? (i >> 2) * 128 + (i & 3) * 8 : i * 8));
@@ -335,7 +422,15 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         const uint4 f = act_granule_f16(reinterpret_cast<const uint32_t*>(&w[i]), pw);
         q[2 * i][0] = f.x, q[2 * i][1] = f.y, q[2 * i + 1][0] = f.z, q[2 * i + 1][1] = f.w;
       }
-      const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[kvh];
+      int h0, r0, r1;
+      column_of(p, sq, cur.hu, 0, &r0, &h0);
+      const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[h0 / p.a.group];
+      // the set's first and last row bound what all of them see
+      column_of(p, sq, cur.hu, kHeads - 1, &r1, &h0);
+      r1 = min(r1, sq.n - 1);
+      all_hi = row_hi(sq, r0);
+      all_lo = row_lo(p.a, row_hi(sq, r1));
+      sh.lost[tid] = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         mul[i] = unit * pow2f(__shfl_sync(0xffffffffu, pw, 4 * (2 * t + i)));
@@ -346,7 +441,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       for (int j = 0; j < KS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-      any = false;
+      any = 0;
       first_c = cur.c;
     };
     begin();
@@ -361,7 +456,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       const uint32_t there = valid_fifo & 15u;
       valid_fifo >>= 4;
       const int tok0 = (cur.c0 + cur.c) * C::kChunk;
-      const bool edge = tok0 < cur.lo || tok0 + C::kChunk > cur.len || there != (1u << C::kTiles) - 1;
+      const bool edge = tok0 < all_lo || tok0 + C::kChunk > all_hi || there != (1u << C::kTiles) - 1;
 
       // ---- S^T = K Q^T
       float s[C::kTiles][4];
@@ -392,29 +487,53 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[i][e] *= mul[e & 1];
       }
-      // ---- keys that the row does not see; what their places hold may be anything
-      uint32_t seen = 0xFFFFFFFFu;  // bit 4 i + k: token t + 4 k of tile i
+      // ---- keys that a column does not see; what their places hold may be anything
+      uint32_t seen = 0xFFFFFFFFu;  // bit 16 c + 4 i + k: token t + 4 k of tile i, column block c, by some column
       if (edge) {
-        seen = 0;
-        bool some = false;
+        const RowSeq sq = row_seq(p.a, cur.b);
+        int row, head, lo[2], hi[2];
+        column_of(p, sq, cur.hu, 2 * t, &row, &head);
+        hi[0] = row < sq.n ? row_hi(sq, row) : 0;
+        lo[0] = row_lo(p.a, hi[0]);
+        column_of(p, sq, cur.hu, 2 * t + 1, &row, &head);
+        hi[1] = row < sq.n ? row_hi(sq, row) : 0;
+        lo[1] = row_lo(p.a, hi[1]);
+        bool some[2] = {false, false};
 #pragma unroll
         for (int i = 0; i < C::kTiles; ++i) {
-          auto sees = [&](int r) {
-            const int tok = tok0 + i * kKvTile + r;
-            return ((there >> i) & 1) && tok >= cur.lo && tok < cur.len;
-          };
-          const bool a = sees(kv_mma_token(g)), b = sees(kv_mma_token(g + 8));
-          some |= a | b;
-          s[i][0] = a ? s[i][0] : -INFINITY;
-          s[i][1] = a ? s[i][1] : -INFINITY;
-          s[i][2] = b ? s[i][2] : -INFINITY;
-          s[i][3] = b ? s[i][3] : -INFINITY;
+          const int a = tok0 + i * kKvTile + kv_mma_token(g), b = tok0 + i * kKvTile + kv_mma_token(g + 8);
+          const bool in = (there >> i) & 1;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) seen |= (uint32_t)sees(t + 4 * k) << (4 * i + k);
+          for (int k = 0; k < 2; ++k) {
+            const bool sa = in && a >= lo[k] && a < hi[k], sb = in && b >= lo[k] && b < hi[k];
+            some[k] |= sa || sb;
+            s[i][k] = sa ? s[i][k] : -INFINITY;
+            s[i][2 + k] = sb ? s[i][2 + k] : -INFINITY;
+          }
         }
-        any |= __any_sync(0xffffffffu, some);
+        seen = 0;
+        const int last = row_hi(sq, sq.n - 1), first = row_lo(p.a, row_hi(sq, 0));
+        uint32_t partly = 0;           // of those, not by all of the set
+#pragma unroll
+        for (int i = 0; i < C::kTiles; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = tok0 + i * kKvTile + t + 4 * k;
+            if (((there >> i) & 1) && tok >= first && tok < last) {
+              seen |= 1u << (4 * i + k);
+              if (tok < all_lo || tok >= all_hi) partly |= 1u << (4 * i + k);
+            }
+          }
+        // a column has seen a key: bits 2 t, 2 t + 1 of its lanes, for all of them
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t who = __ballot_sync(0xffffffffu, some[k]);
+          if (who & (0x11111111u << t)) any |= 1u << k;
+        }
+        if (NB == 2) seen |= seen << 16;
+        if (__any_sync(0xffffffffu, partly != 0)) seen &= ~nan_partly<D>(p, sq, cur.hu, st, tok0, partly, &sh.lost[tid]);
       } else {
-        any = true;
+        any = 3;
       }
       // ---- running maximum; the output is scaled only where one rose
       float ms[2];
@@ -453,17 +572,17 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         }
         const uint32_t p0 = transpose8x8(pack_half2(pr[0], pr[1])), p1 = transpose8x8(pack_half2(pr[2], pr[3]));
         const uint32_t tb = st + i * C::kTile + 9 * D;
-        auto scales = [&](int group) {
+        auto scales = [&](int group, int c) {
           uint32_t w = ld_shared_u32(tb + 8 * D + group * 16 + t * 4);
           if (edge) {  // a place that is not seen may hold a NaN scale
-            const uint32_t k = seen >> (4 * i);
+            const uint32_t k = seen >> (16 * c + 4 * i);
             w &= ((k & 1) ? 0xFFu : 0u) | ((k & 2) ? 0xFF00u : 0u) | ((k & 4) ? 0xFF0000u : 0u) | ((k & 8) ? 0xFF000000u : 0u);
           }
           return w;
         };
         if constexpr (D == 64) {
           const uint32_t at = tb + t * 32 + g * 4;
-          const uint32_t sw = scales(g >> 1);
+          const uint32_t sw = scales(g >> 1, 0);
           v_words(o, ld_shared_u32(at), ld_shared_u32(at + 128), ld_shared_u32(at + 256), ld_shared_u32(at + 384),
                   e4m3x2_to_f16x2(sw), e4m3x2_to_f16x2(sw >> 16), p0, p1);
         } else {
@@ -471,7 +590,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
           for (int c = 0; c < NB; ++c) {
             const uint32_t at = tb + c * 1024 + t * 64 + ((g * 8) ^ ((t >> 1) * 32));
             const uint2 a = ld_shared_v2(at), b = ld_shared_v2(at + 256), cc = ld_shared_v2(at + 512), d = ld_shared_v2(at + 768);
-            const uint32_t sw = scales(8 * c + g);
+            const uint32_t sw = scales(8 * c + g, c);
             const uint32_t sab = e4m3x2_to_f16x2(sw), scd = e4m3x2_to_f16x2(sw >> 16);
             v_words(o + 8 * c, a.x, b.x, cc.x, d.x, sab, scd, p0, p1);
             v_words(o + 8 * c + 4, a.y, b.y, cc.y, d.y, sab, scd, p0, p1);
@@ -490,21 +609,31 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
           l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
         }
         constexpr int EJ = D == 64 ? 4 : 8;   // output tiles of a column block
+        uint32_t lost = sh.lost[tid];         // met by the lanes of this column group
+        lost |= __shfl_xor_sync(0xffffffffu, lost, 1);
+        lost |= __shfl_xor_sync(0xffffffffu, lost, 2);
+        if (lost) {
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((lost >> (8 * (j >> 3) + 2 * t + (e & 1))) & 1) o[j][e] = __uint_as_float(0x7FC00000u);
+        }
         if (ends && first_c == 0) {           // all of it
-          const int kvh = cur.hu / p.subs;
+          const RowSeq sq = row_seq(p.a, cur.b);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int inner = (cur.hu % p.subs) * kHeads + 2 * t + i;
-            if (inner < p.a.group) {
-              const int head = kvh * p.a.group + inner;
-              const float f = any ? out_factor(p.a, head, kvh, m[i], l[i], kPBias) : 0.0f;
-              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + cur.b * p.a.ldo + (int64_t)head * D;
+            int row, head;
+            if (column_of(p, sq, cur.hu, 2 * t + i, &row, &head)) {
+              const bool some = (any >> i) & 1;
+              const float f = some ? out_factor(p.a, head, head / p.a.group, m[i], l[i], kPBias) : 0.0f;
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(sq.s0 + row) * p.a.ldo + (int64_t)head * D;
 #pragma unroll
               for (int c = 0; c < NB; ++c) {
                 uint32_t w[EJ];
 #pragma unroll
                 for (int j = 0; j < EJ; ++j) {
-                  const float x = any ? o[8 * c + j][i] * f : 0.0f, y = any ? o[8 * c + j][i + 2] * f : 0.0f;
+                  const float x = some ? o[8 * c + j][i] * f : 0.0f, y = some ? o[8 * c + j][i + 2] * f : 0.0f;
                   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
                   w[j] = *reinterpret_cast<const uint32_t*>(&v);
                 }
@@ -535,12 +664,15 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
               part[kHeads * D + kHeads + 2 * t + i] = l[i];
             }
           }
+          if (g == 0) {
+            part[kHeads * D + 2 * kHeads + 2 * t] = any & 1 ? 1.0f : 0.0f;
+            part[kHeads * D + 2 * kHeads + 2 * t + 1] = any & 2 ? 1.0f : 0.0f;
+          }
           if (lane == 0) {
-            part[kHeads * D + 2 * kHeads] = any ? 1.0f : 0.0f;
             PartMeta& pm = sh.part[2 * warp + kind];
-            pm.seg0 = cur.seg0;
-            pm.u0 = cur.seg0 + first_c;
-            pm.u1 = cur.seg0 + cur.c + 1;
+            pm.seg0 = u0 + n - cur.c;
+            pm.u0 = u0 + n - cur.c + first_c;
+            pm.u1 = u0 + n + 1;
             pm.nb = cur.nb;
             pm.b = cur.b;
             pm.hu = cur.hu;
@@ -548,7 +680,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
           }
         }
         if (!last) {
-          cur.advance(p, HU);
+          cur.next(p);
           begin();
         }
       } else {
@@ -559,21 +691,21 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   __syncthreads();
 
   // ---- join the parts of each (sequence, head): runs of neighbours in the order of the line
-  if (tid == 0) {
-    int n = 0;
-    int64_t seg = -1;
-    for (int i = 0; i < 2 * C::kWarps; ++i)
-      if (sh.part[i].used && sh.part[i].seg0 != seg) {
-        seg = sh.part[i].seg0;
-        sh.run_first[n++] = i;
-      }
-    sh.runs = n;
-    sh.run_first[n] = 2 * C::kWarps;
+  if (warp == 0) {
+    const bool used = lane < 2 * C::kWarps && sh.part[lane].used;
+    const uint32_t all = __ballot_sync(0xffffffffu, used), below = all & ((1u << lane) - 1);
+    const bool first = used && (!below || sh.part[31 - __clz(below)].seg0 != sh.part[lane].seg0);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    if (first) sh.run_first[__popc(firsts & ((1u << lane) - 1))] = lane;
+    if (lane == 0) {
+      sh.runs = __popc(firsts);
+      sh.run_first[__popc(firsts)] = 2 * C::kWarps;
+    }
   }
   __syncthreads();
   const int runs = sh.runs;
   float* parts = reinterpret_cast<float*>(p.a.workspace + kAttendCleared);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + 256);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + kRowCounts);
   auto part_at = [&](int i) {
     return reinterpret_cast<const float*>(smem + ((i & 1) ? (i >> 1) * C::kRing : C::kOffPart + (i >> 1) * C::kPartBytes));
   };
@@ -588,7 +720,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       if (sh.part[i].used) {
         const float* q = part_at(i) + kHeads * D;
         m = fmaxf(m, q[h]);
-        any |= q[2 * kHeads] != 0.0f;
+        any |= q[2 * kHeads + h] != 0.0f;
         upto = sh.part[i].u1;
       }
     const float ms = m == -INFINITY ? 0.0f : m;
@@ -612,7 +744,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       if (lane == 0) {
         __stcg(dst + kHeads * D + h, m);
         __stcg(dst + kHeads * D + kHeads + h, l);
-        if (h == 0) __stcg(dst + kHeads * D + 2 * kHeads, any ? 1.0f : 0.0f);
+        __stcg(dst + kHeads * D + 2 * kHeads + h, any ? 1.0f : 0.0f);
       }
     }
   }
@@ -675,7 +807,6 @@ cudaError_t launch_attend_row(const AttendLaunch& L, int head_dim, cudaStream_t 
   RowParams p;
   p.a = L;
   p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
-  p.subs = (L.group + kHeads - 1) / kHeads;
   return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
 }
 

@@ -91,21 +91,16 @@ struct TileParams {
   uint64_t wait_ns;
 };
 
-struct Seq {
-  int s0, n, len;
-};
-__device__ __forceinline__ Seq load_seq(const AttendLaunch& a, int64_t b) {
-  Seq q;
-  const int T = (int)a.T, s = __ldg(a.starts + b), e = __ldg(a.starts + b + 1);
-  q.s0 = s < 0 ? 0 : s > T ? T : s;
-  q.n = (e < q.s0 ? q.s0 : e > T ? T : e) - q.s0;
-  q.len = seq_len(a, b);
+// A sequence as this kernel takes it: n = 0 where the row kernel does.
+__device__ __forceinline__ AttendSeq tile_seq(const AttendLaunch& a, int64_t b) {
+  AttendSeq q = load_seq(a, b);
+  if (few_rows(a, q.n)) q.n = 0;
   return q;
 }
 
 // Blocks of keys of a sequence's i-th tile: [first, first + count).
 template <int D>
-__device__ __forceinline__ void tile_blocks(const AttendLaunch& a, const Seq& q, int i, int per_tile, int* first, int* count) {
+__device__ __forceinline__ void tile_blocks(const AttendLaunch& a, const AttendSeq& q, int i, int per_tile, int* first, int* count) {
   constexpr int KB = TileCfg<D>::kKeys;
   const int r0 = i * per_tile, r1 = min(q.n, r0 + per_tile);
   const int64_t past = (int64_t)q.len - q.n;
@@ -119,7 +114,7 @@ __device__ __forceinline__ void tile_blocks(const AttendLaunch& a, const Seq& q,
 // A run of blocks of one (tile, head), walked by every role on its own.
 template <int D>
 struct Walk {
-  Seq q;
+  AttendSeq q;
   int b, i, h;
   int first, count;   // the tile's blocks
   int at, end;        // this segment: blocks [at, end) of them, counted from first
@@ -131,7 +126,7 @@ struct Walk {
   __device__ __forceinline__ bool start(const TileParams& p, const TileShared& sh, int64_t u0, int64_t u1) {
     b = sh.b;
     i = sh.i;
-    q = load_seq(p.a, b);
+    q = tile_seq(p.a, b);
     tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
     const int64_t r = u0 - sh.before;
     h = (int)(r / (count + kLead));
@@ -158,7 +153,7 @@ struct Walk {
         ++i;
         while ((int64_t)i * per_tile(p) >= q.n) {
           if (++b >= p.a.B) { left = 0; return false; }
-          q = load_seq(p.a, b);
+          q = tile_seq(p.a, b);
           i = 0;
         }
         tile_blocks<D>(p.a, q, i, per_tile(p), &first, &count);
@@ -340,7 +335,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
     for (int64_t b0 = 0; b0 < p.a.B; b0 += C::kThreads) {
       const int64_t b = b0 + tid;
       int64_t tiles = 0, round;
-      if (b < p.a.B) tiles = (load_seq(p.a, b).n + per_tile - 1) / per_tile;
+      if (b < p.a.B) tiles = (tile_seq(p.a, b).n + per_tile - 1) / per_tile;
       const int64_t mine = block_prefix<W>(tiles, sh.scan, &round);
       sh.seq_first[tid] = mine;
       if (tid == 0) sh.seq_first[C::kThreads] = round;
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       for (int64_t f0 = 0; f0 < round; f0 += C::kThreads) {
         const int64_t f = f0 + tid;
         int count = 0, first, at = 0, i = 0;
-        Seq q = {};
+        AttendSeq q = {};
         if (f < round) {
           int hi = C::kThreads;  // the last sequence of the round whose first tile is at or before f
           while (hi - at > 1) {
@@ -357,7 +352,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             else hi = mid;
           }
           i = (int)(f - sh.seq_first[at]);
-          q = load_seq(p.a, b0 + at);
+          q = tile_seq(p.a, b0 + at);
           tile_blocks<D>(p.a, q, i, per_tile, &first, &count);
           if (pass == 0 && count == 0 && f % gridDim.x == blockIdx.x) {  // no key: its rows are zeros
             const int r1 = min(q.n, (i + 1) * per_tile);
@@ -710,7 +705,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           if (warp == 0) {
             if (!(ok = warp_wait(joined, (st & kPart) != 0, abort, p.wait_ns))) break;
             if (lane == 0) {
-              uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + 256) + c0;
+              uint32_t* count = reinterpret_cast<uint32_t*>(p.a.workspace + kTileCounts) + c0;
               __threadfence();
               const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
               if (last) *count = 0;  // for the next call
@@ -1060,7 +1055,7 @@ cudaError_t launch_attend_tile(const AttendLaunch& L, int head_dim, cudaStream_t
   p.a = L;
   p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
   p.tokens = 128 / L.group;
-  p.parts = reinterpret_cast<float*>(L.workspace + kAttendCleared);
+  p.parts = reinterpret_cast<float*>(L.workspace + kAttendCleared + attend_row_parts_bytes(head_dim));
   p.wait_ns = kWaitNs;
   return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
 }
