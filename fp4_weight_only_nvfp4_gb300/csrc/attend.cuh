@@ -9,9 +9,10 @@ constexpr int kMaxAttendGrid = 160;
 constexpr int kRowCounts = 256, kTileCounts = 2048;  // of the arrival counts, bytes
 static_assert(kRowCounts + 4 * kMaxAttendGrid <= kTileCounts && kTileCounts + 4 * kMaxAttendGrid <= kAttendCleared, "counts");
 constexpr float kLog2e = 1.4426950408889634f;
-// Probabilities are held as 2^(s - m + kPBias): in f16 those down to 2^-26 of the row's largest
-// then keep all their bits (2^-36: the last bit), and their sum over a long row what they add.
-constexpr float kPBias = 12.0f;
+// Probabilities are held as 2^(s - m + kPBias) with m the row's maximum or an older one that it passes
+// by kSlack at most: below 2^15 in f16, and those down to 2^-21 of the largest keep all their
+// bits (2^-31: the last bit), so that a long row's sum keeps what many small ones add.
+constexpr float kPBias = 7.0f, kSlack = 8.0f;
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;

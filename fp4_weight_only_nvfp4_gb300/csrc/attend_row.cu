@@ -151,8 +151,8 @@ __device__ __forceinline__ uint32_t ld_shared_u16x(uint32_t addr) {
 }
 
 // Four A fragments' worth of codes (two words of 8) of rows g and g + 8, times their scales,
-// against four k steps of Q.
-__device__ __forceinline__ void k_words(float (&s)[4], uint32_t lo, uint32_t hi, uint32_t sl, uint32_t sh,
+// against two k steps of Q; each has a sum of its own, so that two products run beside one another.
+__device__ __forceinline__ void k_words(float (&s)[4], float (&s2)[4], uint32_t lo, uint32_t hi, uint32_t sl, uint32_t sh,
                                         const uint32_t* q) {
   uint32_t a[4], b[4];
   e2m1x8_to_f16x8(lo, a[0], a[1], a[2], a[3]);
@@ -163,7 +163,7 @@ __device__ __forceinline__ void k_words(float (&s)[4], uint32_t lo, uint32_t hi,
     b[i] = hmul2_u32(b[i], sh);
   }
   mma_f16_16816(s, a[0], b[0], a[1], b[1], q[0], q[1]);
-  mma_f16_16816(s, a[2], b[2], a[3], b[3], q[2], q[3]);
+  mma_f16_16816(s2, a[2], b[2], a[3], b[3], q[2], q[3]);
 }
 
 // Words of codes of tokens a, b, c, d (8 columns each) and their scales, against P of a tile: four
@@ -465,12 +465,13 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         const uint32_t tb = st + i * C::kTile;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
+        float s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (D == 64) {
           const uint2 lo = ld_shared_v2(tb + g * 32 + t * 8), hi = ld_shared_v2(tb + 256 + g * 32 + t * 8);
           const uint32_t sc = e4m3x2_to_f16x2(ld_shared_u16x(tb + 8 * D + g * 8 + t * 2));
           const uint32_t sl = bcast_lo(sc), sr = bcast_hi(sc);
-          k_words(s[i], lo.x, hi.x, sl, sr, q[0]);
-          k_words(s[i], lo.y, hi.y, sl, sr, q[2]);
+          k_words(s[i], s2, lo.x, hi.x, sl, sr, q[0]);
+          k_words(s[i], s2, lo.y, hi.y, sl, sr, q[2]);
         } else {
 #pragma unroll
           for (int c = 0; c < NB; ++c) {
@@ -478,14 +479,14 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
             const int4 hi = ld_shared_v4(tb + c * 1024 + 512 + g * 64 + t * 16);
             const uint32_t sw = ld_shared_u32(tb + 8 * D + c * 128 + g * 16 + t * 4);
             const uint32_t s0 = e4m3x2_to_f16x2(sw), s1 = e4m3x2_to_f16x2(sw >> 16);
-            k_words(s[i], lo.x, hi.x, bcast_lo(s0), bcast_lo(s1), q[8 * c]);
-            k_words(s[i], lo.y, hi.y, bcast_lo(s0), bcast_lo(s1), q[8 * c + 2]);
-            k_words(s[i], lo.z, hi.z, bcast_hi(s0), bcast_hi(s1), q[8 * c + 4]);
-            k_words(s[i], lo.w, hi.w, bcast_hi(s0), bcast_hi(s1), q[8 * c + 6]);
+            k_words(s[i], s2, lo.x, hi.x, bcast_lo(s0), bcast_lo(s1), q[8 * c]);
+            k_words(s[i], s2, lo.y, hi.y, bcast_lo(s0), bcast_lo(s1), q[8 * c + 2]);
+            k_words(s[i], s2, lo.z, hi.z, bcast_hi(s0), bcast_hi(s1), q[8 * c + 4]);
+            k_words(s[i], s2, lo.w, hi.w, bcast_hi(s0), bcast_hi(s1), q[8 * c + 6]);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] *= mul[e & 1];
+        for (int e = 0; e < 4; ++e) s[i][e] = (s[i][e] + s2[e]) * mul[e & 1];
       }
       // ---- keys that a column does not see; what their places hold may be anything
       uint32_t seen = 0xFFFFFFFFu;  // bit 16 c + 4 i + k: token t + 4 k of tile i, column block c, by some column
@@ -535,25 +536,26 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       } else {
         any = 3;
       }
-      // ---- running maximum; the output is scaled only where one rose
-      float ms[2];
+      // ---- running maximum: the sums stay on an older one while no lane has a score more than kSlack
+      // above it, so that the maximum over the lanes and the scaling are rare
+      float top[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(s[0][i], s[0][i + 2]);
+        top[i] = fmaxf(s[0][i], s[0][i + 2]);
 #pragma unroll
-        for (int j = 1; j < C::kTiles; ++j) x = fmaxf(x, fmaxf(s[j][i], s[j][i + 2]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        ms[i] = fmaxf(m[i], x);
+        for (int j = 1; j < C::kTiles; ++j) top[i] = fmaxf(top[i], fmaxf(s[j][i], s[j][i + 2]));
       }
-      if (__any_sync(0xffffffffu, ms[0] > m[0] || ms[1] > m[1])) {
+      if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          f[i] = ms[i] > m[i] ? fast_exp2(m[i] - ms[i]) : 1.0f;
+          float x = top[i];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          f[i] = x > m[i] ? fast_exp2(m[i] - x) : 1.0f;
           l[i] *= f[i];
-          m[i] = ms[i];
+          m[i] = fmaxf(m[i], x);
         }
 #pragma unroll
         for (int j = 0; j < KS; ++j)

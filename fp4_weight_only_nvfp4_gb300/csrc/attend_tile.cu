@@ -36,8 +36,6 @@ namespace vt {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kTileBias = 7.0f;   // P = 2^(s - m + 7): below 2^15 while s - m <= 8
-constexpr float kSlack = 8.0f;
 constexpr int kLead = 6;
 
 template <int D>
@@ -553,7 +551,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 }
               }
               m = mn;
-              const float off = kTileBias - (m == -INFINITY ? 0.0f : m);
+              const float off = kPBias - (m == -INFINITY ? 0.0f : m);
               const uint64_t mul2 = pair(mul, mul), off2 = pair(off, off);
               uint64_t sum[2] = {0, 0};
               // P, two f16 a column, over the second half of the scores: those are in registers
@@ -636,7 +634,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
         };
         if (out) {
-          const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kTileBias) : 0.0f;
+          const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kPBias) : 0.0f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -734,7 +732,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 const float* st = part_of(k) + C::kRows * D + X * 128 + r;
                 lt += fast_exp2(__ldcg(st) - ms) * __ldcg(st + C::kRows);
               }
-              const float f = at ? out_factor(p.a, head, w.h, mt, lt, kTileBias) : 0.0f;
+              const float f = at ? out_factor(p.a, head, w.h, mt, lt, kPBias) : 0.0f;
               __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + at_row(p.a.ldo);
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
