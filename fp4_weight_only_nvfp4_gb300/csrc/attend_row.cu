@@ -60,8 +60,12 @@ struct RowShared {
   int64_t scan[32];
   int64_t start_prefix[16];
   int start_b[16];
-  int runs, run_first[33];
-  int last;
+  int parts, runs;         // in use, in the order of the line
+  int list[32], run_of[32], run_first[33];
+  float weight[32][kHeads];
+  float run_m[32][kHeads], run_l[32][kHeads];
+  int run_any[32][kHeads];
+  int last[2];
   uint32_t lost[16 * 32];  // of each lane: columns whose sums a NaN scale reaches, 8 bits a column block
 };
 
@@ -182,67 +186,15 @@ __device__ __forceinline__ void v_words(float (*o)[4], uint32_t a, uint32_t b, u
                   hmul2_u32(h[j], scd), p0, p1);
 }
 
-// Joins the parts at `parts` (n of them, `stride` floats apart) for head h: lane's D / 32 values of
-// O, and m, l.  The weights 2^(m_i - m) are taken once, 32 parts at a time.
-template <int D, bool GLOBAL>
-__device__ __forceinline__ void join_head(const float* parts, int64_t stride, int n, int h, float (&o)[D / 32],
-                                          float& m, float& l, bool& any) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  auto ld = [](const float* q) { return GLOBAL ? __ldcg(q) : *q; };
-  m = -INFINITY;
-  any = false;
-  for (int i = lane; i < n; i += 32) {
-    const float* q = parts + i * stride + kHeads * D;
-    m = fmaxf(m, ld(q + h));
-    any |= ld(q + 2 * kHeads + h) != 0.0f;
-  }
-#pragma unroll
-  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-  any = __any_sync(0xffffffffu, any);
-  const float ms = m == -INFINITY ? 0.0f : m;
-  l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.0f;
-    if (i0 + lane < n) {
-      const float* q = parts + (i0 + lane) * stride + kHeads * D;
-      w = fast_exp2(ld(q + h) - ms);
-      l += w * ld(q + kHeads + h);
-    }
-    const int k = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* q = parts + (i0 + i) * stride + h * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = GLOBAL ? __ldcg(reinterpret_cast<const float2*>(q + e)) : *reinterpret_cast<const float2*>(q + e);
-        o[e] += wi * v.x;
-        o[e + 1] += wi * v.y;
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-}
-
+// Columns d, d + 1 of column h of a (sequence, head, set), from its sums.
 template <int D>
-__device__ __forceinline__ void store_row(const RowParams& p, int b, int hu, int h, float (&o)[D / 32], float m,
-                                          float l, bool any) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void store_pair(const RowParams& p, int b, int hu, int h, int d, float2 o, float m, float l, bool any) {
   const RowSeq q = row_seq(p.a, b);
   int row, head;
   if (!column_of(p, q, hu, h, &row, &head)) return;
-  float f = 0.0f;
-  if (any) f = out_factor(p.a, head, head / p.a.group, m, l, kPBias);
-  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + row) * p.a.ldo + (int64_t)head * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + e) =
-        any ? __floats2bfloat162_rn(o[e] * f, o[e + 1] * f) : __floats2bfloat162_rn(0.0f, 0.0f);
+  const float f = any ? out_factor(p.a, head, head / p.a.group, m, l, kPBias) : 0.0f;
+  *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + row) * p.a.ldo + (int64_t)head * D + d) =
+      any ? __floats2bfloat162_rn(o.x * f, o.y * f) : __floats2bfloat162_rn(0.0f, 0.0f);
 }
 
 // Tokens of `partly` (bit 4 i + k: token t + 4 k of tile i) whose value scales, of the lane's columns,
@@ -345,7 +297,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     cur.b = sh.start_b[warp];
     cur.sequence(p);
     const int64_t r = u0 - sh.start_prefix[warp];
-    cur.hu = (int)(r / cur.nb);
+    cur.hu = r >> 31 ? (int)(r / cur.nb) : (int)((uint32_t)r / (uint32_t)cur.nb);
     cur.kvh = cur.hu / cur.sets;
     cur.c = (int)(r - (int64_t)cur.hu * cur.nb);
     Cursor<D> ld = cur;
@@ -385,33 +337,27 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         page = page_of();
       }
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (issued < total_chunks) issue();
-      cp_commit();
-    }
 
     uint32_t q[KS][2];       // B fragments: column g (a head), k = the lane's own columns
     float mul[2];            // of heads 2t and 2t + 1: raw products to log2 units
     float o[KS][4], m[2], l[2];
     uint32_t any = 0;         // bit i: column 2t + i has seen a key
     int first_c = cur.c, all_lo, all_hi;   // keys [all_lo, all_hi) are seen by every column
-    auto begin = [&]() {
+    auto load_q = [&](uint4 (&w)[KS / 2]) {
       const RowSeq sq = row_seq(p.a, cur.b);
       int row, head;
       const bool on = column_of(p, sq, cur.hu, g, &row, &head);
-      uint4 w[KS / 2];
-      int mx = 0;
-      if (on) {
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(sq.s0 + row) * p.a.ldq +
-                                   (int64_t)head * D + (D == 64 ? 16 : 32) * t;
+      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + (on ? (int64_t)(sq.s0 + row) * p.a.ldq + (int64_t)head * D : 0) +
+                                 (D == 64 ? 16 : 32) * t;
 #pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-          w[i] = *reinterpret_cast<const uint4*>(src + (D == 256 ? (i >> 2) * 128 + (i & 3) * 8 : i * 8));
-      } else {
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) w[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < KS / 2; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (on) w[i] = *reinterpret_cast<const uint4*>(src + (D == 256 ? (i >> 2) * 128 + (i & 3) * 8 : i * 8));
       }
+    };
+    auto begin = [&](uint4 (&w)[KS / 2]) {
+      const RowSeq sq = row_seq(p.a, cur.b);
+      int mx = 0;
 #pragma unroll
       for (int i = 0; i < KS / 2; ++i) mx = max(mx, act_maxmag8(reinterpret_cast<const uint32_t*>(&w[i])));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -424,7 +370,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       }
       int h0, r0, r1;
       column_of(p, sq, cur.hu, 0, &r0, &h0);
-      const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[h0 / p.a.group];
+      const float unit = p.a.scale * kLog2e * __ldg(p.a.cache.k_scale + h0 / p.a.group);
       // the set's first and last row bound what all of them see
       column_of(p, sq, cur.hu, kHeads - 1, &r1, &h0);
       r1 = min(r1, sq.n - 1);
@@ -444,7 +390,15 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       any = 0;
       first_c = cur.c;
     };
-    begin();
+    // loads of q and of the first page's entry are in flight together
+    uint4 w0[KS / 2];
+    load_q(w0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (issued < total_chunks) issue();
+      cp_commit();
+    }
+    begin(w0);
 
 #pragma unroll 1
     for (int n = 0; n < total_chunks; ++n) {
@@ -683,7 +637,9 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         }
         if (!last) {
           cur.next(p);
-          begin();
+          uint4 w[KS / 2];
+          load_q(w);
+          begin(w);
         }
       } else {
         ++cur.c;
@@ -692,98 +648,146 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   }
   __syncthreads();
 
-  // ---- join the parts of each (sequence, head): runs of neighbours in the order of the line
+  // ---- join the parts of each (sequence, head, set): runs of neighbours in the order of the line
   if (warp == 0) {
     const bool used = lane < 2 * C::kWarps && sh.part[lane].used;
     const uint32_t all = __ballot_sync(0xffffffffu, used), below = all & ((1u << lane) - 1);
     const bool first = used && (!below || sh.part[31 - __clz(below)].seg0 != sh.part[lane].seg0);
     const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-    if (first) sh.run_first[__popc(firsts & ((1u << lane) - 1))] = lane;
+    const int k = __popc(below), run = __popc(firsts & ((2u << lane) - 1)) - 1;
+    if (used) {
+      sh.list[k] = lane;
+      sh.run_of[k] = run;
+    }
+    if (first) sh.run_first[run] = k;
     if (lane == 0) {
+      sh.parts = __popc(all);
       sh.runs = __popc(firsts);
-      sh.run_first[__popc(firsts)] = 2 * C::kWarps;
+      sh.run_first[__popc(firsts)] = __popc(all);
     }
   }
   __syncthreads();
   const int runs = sh.runs;
-  float* parts = reinterpret_cast<float*>(p.a.workspace + kAttendCleared);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + kRowCounts);
-  auto part_at = [&](int i) {
+  auto part_at = [&](int k) {
+    const int i = sh.list[k];
     return reinterpret_cast<const float*>(smem + ((i & 1) ? (i >> 1) * C::kRing : C::kOffPart + (i >> 1) * C::kPartBytes));
   };
-  for (int task = warp; task < runs * kHeads; task += C::kWarps) {
-    const int run = task / kHeads, h = task % kHeads, i0 = sh.run_first[run], i1 = sh.run_first[run + 1];
-    const PartMeta& first = sh.part[i0];
-    constexpr int E = D / 32;
-    float o[E], m = -INFINITY, l = 0.0f;
-    bool any = false;
-    int64_t upto = first.u0;
-    for (int i = i0; i < i1; ++i)
-      if (sh.part[i].used) {
-        const float* q = part_at(i) + kHeads * D;
-        m = fmaxf(m, q[h]);
-        any |= q[2 * kHeads + h] != 0.0f;
-        upto = sh.part[i].u1;
-      }
+  for (int i = tid; i < sh.parts * kHeads; i += C::kThreads) {
+    const int k = i / kHeads, h = i % kHeads, run = sh.run_of[k], k0 = sh.run_first[run], k1 = sh.run_first[run + 1];
+    float m = -INFINITY;
+    for (int j = k0; j < k1; ++j) m = fmaxf(m, part_at(j)[kHeads * D + h]);
     const float ms = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int i = i0; i < i1; ++i)
-      if (sh.part[i].used) {
-        const float* q = part_at(i);
-        const float w = fast_exp2(q[kHeads * D + h] - ms);
-        l += w * q[kHeads * D + kHeads + h];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += w * q[h * D + lane * E + e];
+    sh.weight[k][h] = fast_exp2(part_at(k)[kHeads * D + h] - ms);
+    if (k == k0) {
+      float l = 0.0f;
+      int any = 0;
+      for (int j = k0; j < k1; ++j) {
+        const float* q = part_at(j) + kHeads * D;
+        l += fast_exp2(q[h] - ms) * q[kHeads + h];
+        any |= q[2 * kHeads + h] != 0.0f;
       }
-    if (first.u0 == first.seg0 && upto == first.seg0 + first.nb) {
-      store_row<D>(p, first.b, first.hu, h, o, m, l, any);
+      sh.run_m[run][h] = m;
+      sh.run_l[run][h] = l;
+      sh.run_any[run][h] = any;
+    }
+  }
+  __syncthreads();
+  float* parts = reinterpret_cast<float*>(p.a.workspace + kAttendCleared);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + kRowCounts);
+  constexpr int kPairs = kHeads * D / 2;  // of a run's sums
+  auto whole = [&](int run) {
+    const PartMeta &f = sh.part[sh.list[sh.run_first[run]]], &e = sh.part[sh.list[sh.run_first[run + 1] - 1]];
+    return f.u0 == f.seg0 && e.u1 == f.seg0 + f.nb;
+  };
+  for (int i = tid; i < runs * kPairs; i += C::kThreads) {
+    const int run = i / kPairs, at = (i % kPairs) * 2, h = at / D;
+    float2 o = make_float2(0.0f, 0.0f);
+    for (int k = sh.run_first[run]; k < sh.run_first[run + 1]; ++k) {
+      const float w = sh.weight[k][h];
+      const float2 v = *reinterpret_cast<const float2*>(part_at(k) + at);
+      o.x += w * v.x;
+      o.y += w * v.y;
+    }
+    const PartMeta& first = sh.part[sh.list[sh.run_first[run]]];
+    if (whole(run)) {
+      store_pair<D>(p, first.b, first.hu, h, at % D, o, sh.run_m[run][h], sh.run_l[run][h], sh.run_any[run][h]);
     } else {
       // slot 0: what began in an earlier CTA, slot 1: what begins here and goes on
       float* dst = parts + ((int64_t)blockIdx.x * 2 + (first.u0 == first.seg0)) * C::kPartFloats;
-#pragma unroll
-      for (int e = 0; e < E; ++e) __stcg(dst + h * D + lane * E + e, o[e]);
-      if (lane == 0) {
-        __stcg(dst + kHeads * D + h, m);
-        __stcg(dst + kHeads * D + kHeads + h, l);
-        __stcg(dst + kHeads * D + 2 * kHeads + h, any ? 1.0f : 0.0f);
+      __stcg(reinterpret_cast<float2*>(dst + at), o);
+      if (at % D == 0) {
+        __stcg(dst + kHeads * D + h, sh.run_m[run][h]);
+        __stcg(dst + kHeads * D + kHeads + h, sh.run_l[run][h]);
+        __stcg(dst + kHeads * D + 2 * kHeads + h, sh.run_any[run][h] ? 1.0f : 0.0f);
       }
     }
   }
-  // ---- parts that other CTAs hold too: the last one to come joins them
-  for (int run = 0; run < runs; ++run) {
-    if (run != 0 && run != runs - 1) continue;
-    const PartMeta& first = sh.part[sh.run_first[run]];
-    int64_t upto = 0;
-    for (int i = sh.run_first[run]; i < sh.run_first[run + 1]; ++i)
-      if (sh.part[i].used) upto = sh.part[i].u1;
-    const int64_t seg1 = first.seg0 + first.nb;
-    if (first.u0 == first.seg0 && upto == seg1) continue;
-    // CTAs from c0 to c1 share it: CTA i holds [i U / G, (i + 1) U / G)
-    const int64_t c0 = ((first.seg0 + 1) * G - 1) / U, c1 = (seg1 * G - 1) / U;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t before = atomicAdd(counters + c0, 1u);
-      sh.last = before == (uint32_t)(c1 - c0);
-      if (sh.last) counters[c0] = 0;  // for the next call
+  // ---- parts that other CTAs hold too (of the first run, of the last): the last one to come joins them
+  const bool shared0 = runs > 0 && !whole(0), shared1 = runs > 1 && !whole(runs - 1);
+  if (!shared0 && !shared1) return;
+  // CTAs from c0 to c1 share a run: CTA i holds [i U / G, (i + 1) U / G)
+  auto first_cta = [&](const PartMeta& f) { return ((f.seg0 + 1) * G - 1) / U; };
+  auto last_cta = [&](const PartMeta& f) { return ((f.seg0 + f.nb) * G - 1) / U; };
+  __threadfence();
+  __syncthreads();
+  if (lane == 0 && warp < 2) {
+    sh.last[warp] = 0;
+    if (warp ? shared1 : shared0) {
+      const PartMeta& f = sh.part[sh.list[sh.run_first[warp ? runs - 1 : 0]]];
+      uint32_t* count = counters + first_cta(f);
       __threadfence();
+      const bool last = atomicAdd(count, 1u) == (uint32_t)(last_cta(f) - first_cta(f));
+      if (last) *count = 0;  // for the next call
+      __threadfence();
+      sh.last[warp] = last;
     }
-    __syncthreads();
-    if (sh.last) {
-      // CTA c0's part is in its slot 1, the others' in their slot 0
-      for (int h = warp; h < kHeads; h += C::kWarps) {
-        float o[D / 32], m, l, o2[D / 32], m2, l2;
-        bool any, any2;
-        join_head<D, true>(parts + (2 * c0 + 1) * C::kPartFloats, 0, 1, h, o, m, l, any);
-        join_head<D, true>(parts + 2 * (c0 + 1) * C::kPartFloats, 2 * C::kPartFloats, (int)(c1 - c0), h, o2, m2, l2, any2);
-        const float top = fmaxf(m, m2), ts = top == -INFINITY ? 0.0f : top;
-        const float a = fast_exp2(m - ts), b = fast_exp2(m2 - ts);
+  }
+  __syncthreads();
+  float* weight = reinterpret_cast<float*>(smem);  // [parts][8], in the place of the rings
+  for (int which = 0; which < 2; ++which) {
+    if (!sh.last[which]) continue;
+    const PartMeta& f = sh.part[sh.list[sh.run_first[which ? runs - 1 : 0]]];
+    const int64_t c0 = first_cta(f);
+    const int n = (int)(last_cta(f) - c0) + 1;
+    // CTA c0's part is in its slot 1, the others' in their slot 0
+    auto part_of = [&](int k) { return parts + (2 * (c0 + k) + (k == 0)) * (int64_t)C::kPartFloats; };
+    for (int h = warp; h < kHeads; h += C::kWarps) {
+      float m = -INFINITY, l = 0.0f;
+      bool any = false;
+      for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(part_of(k) + kHeads * D + h));
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = o[e] * a + o2[e] * b;
-        store_row<D>(p, first.b, first.hu, h, o, top, l * a + l2 * b, any || any2);
+      for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const float ms = m == -INFINITY ? 0.0f : m;
+      for (int k = lane; k < n; k += 32) {
+        const float* q = part_of(k) + kHeads * D + h;
+        const float w = fast_exp2(__ldcg(q) - ms);
+        weight[k * kHeads + h] = w;
+        l += w * __ldcg(q + kHeads);
+        any |= __ldcg(q + 2 * kHeads) != 0.0f;
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      any = __any_sync(0xffffffffu, any);
+      if (lane == 0) {
+        sh.run_m[which][h] = m;
+        sh.run_l[which][h] = l;
+        sh.run_any[which][h] = any;
       }
     }
+    __syncthreads();
+    for (int i = tid; i < kPairs; i += C::kThreads) {
+      const int at = i * 2, h = at / D;
+      float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(part_of(k) + at));
+        const float w = weight[k * kHeads + h];
+        o.x += w * v.x;
+        o.y += w * v.y;
+      }
+      store_pair<D>(p, f.b, f.hu, h, at % D, o, sh.run_m[which][h], sh.run_l[which][h], sh.run_any[which][h]);
+    }
+    __syncthreads();
   }
 }
 
