@@ -46,16 +46,14 @@ constexpr int kFewColumns = 32;
 __device__ __forceinline__ bool few_rows(const AttendLaunch& a, int n) { return (int64_t)n * a.group <= kFewColumns; }
 
 // What a row's sum of p v is multiplied by: the values' global over the sum of p and the sink's
-// share (m in log2 units; p and l hold 2^bias).
+// share (m in log2 units; p and l hold 2^bias; a sink of -inf is none).
+__device__ __forceinline__ float out_factor(float value, float sink, float m, float l, float bias) {
+  const float s = sink * kLog2e, top = fmaxf(m, s), ts = top == -INFINITY ? 0.0f : top;
+  const float w = fast_exp2(m - ts);  // the row's sums are re-based where the sink is larger
+  return value * w / (l * w + fast_exp2(s - ts + bias));
+}
 __device__ __forceinline__ float out_factor(const AttendLaunch& a, int head, int kvh, float m, float l, float bias) {
-  float f = a.cache.v_scale[kvh];
-  if (a.sinks) {
-    const float s = a.sinks[head] * kLog2e, top = fmaxf(m, s), ts = top == -INFINITY ? 0.0f : top;
-    const float w = fast_exp2(m - ts);  // the row's sums are re-based where the sink is larger
-    l = l * w + fast_exp2(s - ts + bias);
-    f *= w;
-  }
-  return f / l;
+  return out_factor(a.cache.v_scale[kvh], a.sinks ? a.sinks[head] : -INFINITY, m, l, bias);
 }
 
 // Sum over the CTA's threads, and the sum over the threads before this one.

@@ -46,24 +46,32 @@ struct RowCfg {
   static constexpr int kOffMeta = kOffPart + kWarps * kPartBytes;
 };
 
+// Where a column goes in out, in elements (-1: nowhere), with its sink (-inf: none) and the global of its
+// values: fetched with q, so that no join waits for them.
+struct Place {
+  int64_t to;
+  float sink, value;
+  // What the column's sums are multiplied by.
+  __device__ __forceinline__ float factor(float m, float l) const { return out_factor(value, sink, m, l, kPBias); }
+};
 // What a warp leaves for the CTA's join: a run of chunks of one (sequence, head) line.
 struct PartMeta {
   int64_t seg0;   // first chunk of the (sequence, head) on the line
   int64_t u0, u1; // chunks covered
   int nb;         // its chunks
-  int b, hu;
   int used;
+  const Place* place;
 };
-static_assert(sizeof(PartMeta) == 40, "meta");
 struct RowShared {
+  Place place[16][2][kHeads];  // [warp][0: of its first (sequence, head, set), 1: of the one it is at]
   PartMeta part[32];       // [warp][0: ended inside the range, 1: the last]
   int64_t scan[32];
   int64_t start_prefix[16];
   int start_b[16];
   int parts, runs;         // in use, in the order of the line
-  int list[32], run_of[32], run_first[33];
+  int slot[32], list[32], run_first[33];  // of each part: its place in part[], in shared memory
   float weight[32][kHeads];
-  float run_m[32][kHeads], run_l[32][kHeads];
+  float run_m[32][kHeads], run_l[32][kHeads], run_factor[32][kHeads];
   int run_any[32][kHeads];
   int last[2];
   uint32_t lost[16 * 32];  // of each lane: columns whose sums a NaN scale reaches, 8 bits a column block
@@ -71,7 +79,8 @@ struct RowShared {
 
 struct RowParams {
   AttendLaunch a;
-  int G;         // CTAs
+  int G;              // CTAs
+  uint32_t by_group;  // floor(2^32 / group) + 1: quotients of small numbers by it
 };
 
 // A sequence as this kernel takes it: n = 0 where the other kernel does.
@@ -98,6 +107,7 @@ template <int D>
 struct Cursor {
   int b, hu, c, nb, c0, len;
   int sets, kvh;   // hu: kvh * sets + the set
+  __device__ __forceinline__ int set() const { return hu - kvh * sets; }
   __device__ __forceinline__ void sequence(const RowParams& p) {
     const RowSeq q = row_seq(p.a, b);
     len = q.len;
@@ -117,12 +127,13 @@ struct Cursor {
   }
 };
 
-// Column i of a set: its row of the sequence and its query head; false past the last.
-__device__ __forceinline__ bool column_of(const RowParams& p, const RowSeq& q, int hu, int i, int* row, int* head) {
-  const int sets = row_sets(p.a, q.n), kvh = hu / sets, at = (hu - kvh * sets) * kHeads + i;
-  *row = at / p.a.group;
+// Column i of a set (the kvh-th head's): its row of the sequence and its query head; false past the last.
+// A set's columns are below 2^7: the quotient is exact.
+__device__ __forceinline__ bool column_of(const RowParams& p, int n, int kvh, int set, int i, int* row, int* head) {
+  const uint32_t at = set * kHeads + i;
+  *row = p.a.group == 1 ? at : __umulhi(at, p.by_group);
   *head = kvh * p.a.group + at - *row * p.a.group;
-  return *row < q.n;
+  return *row < n;
 }
 // Keys [lo, hi) that a row of the sequence sees.
 __device__ __forceinline__ int row_hi(const RowSeq& q, int row) { return max(q.len - q.n + row + 1, 0); }
@@ -186,22 +197,11 @@ __device__ __forceinline__ void v_words(float (*o)[4], uint32_t a, uint32_t b, u
                   hmul2_u32(h[j], scd), p0, p1);
 }
 
-// Columns d, d + 1 of column h of a (sequence, head, set), from its sums.
-template <int D>
-__device__ __forceinline__ void store_pair(const RowParams& p, int b, int hu, int h, int d, float2 o, float m, float l, bool any) {
-  const RowSeq q = row_seq(p.a, b);
-  int row, head;
-  if (!column_of(p, q, hu, h, &row, &head)) return;
-  const float f = any ? out_factor(p.a, head, head / p.a.group, m, l, kPBias) : 0.0f;
-  *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(q.s0 + row) * p.a.ldo + (int64_t)head * D + d) =
-      any ? __floats2bfloat162_rn(o.x * f, o.y * f) : __floats2bfloat162_rn(0.0f, 0.0f);
-}
-
 // Tokens of `partly` (bit 4 i + k: token t + 4 k of tile i) whose value scales, of the lane's columns,
 // hold a NaN: they leave the product, where it would reach columns that do not see them, and those that do
 // are noted in *lost.  Returns them, those of a second column block 16 bits up.
 template <int D>
-__device__ __noinline__ uint32_t nan_partly(const RowParams& p, const RowSeq& q, int hu, uint32_t st, int tok0, uint32_t partly,
+__device__ __noinline__ uint32_t nan_partly(const RowParams& p, const RowSeq& q, int kvh, int set, uint32_t st, int tok0, uint32_t partly,
                                             uint32_t* lost) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t out = 0;
@@ -216,7 +216,7 @@ __device__ __noinline__ uint32_t nan_partly(const RowParams& p, const RowSeq& q,
       out |= 1u << (16 * c + i);
       for (int k = 0; k < kHeads; ++k) {
         int row, head;
-        if (!column_of(p, q, hu, k, &row, &head)) continue;
+        if (!column_of(p, q.n, kvh, set, k, &row, &head)) continue;
         const int hi = row_hi(q, row);
         if (tok >= row_lo(p.a, hi) && tok < hi) *lost |= 1u << (8 * c + k);
       }
@@ -343,10 +343,17 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     float o[KS][4], m[2], l[2];
     uint32_t any = 0;         // bit i: column 2t + i has seen a key
     int first_c = cur.c, all_lo, all_hi;   // keys [all_lo, all_hi) are seen by every column
+    int later = 0;            // past the warp's first (sequence, head, set)
     auto load_q = [&](uint4 (&w)[KS / 2]) {
       const RowSeq sq = row_seq(p.a, cur.b);
       int row, head;
-      const bool on = column_of(p, sq, cur.hu, g, &row, &head);
+      const bool on = column_of(p, sq.n, cur.kvh, cur.set(), g, &row, &head);
+      if (t == 0) {
+        Place& to = sh.place[warp][later][g];
+        to.to = on ? (int64_t)(sq.s0 + row) * p.a.ldo + (int64_t)head * D : -1;
+        to.sink = on && p.a.sinks ? __ldg(p.a.sinks + head) : -INFINITY;
+        to.value = __ldg(p.a.cache.v_scale + cur.kvh);
+      }
       const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.a.q) + (on ? (int64_t)(sq.s0 + row) * p.a.ldq + (int64_t)head * D : 0) +
                                  (D == 64 ? 16 : 32) * t;
 #pragma unroll
@@ -369,10 +376,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
         q[2 * i][0] = f.x, q[2 * i][1] = f.y, q[2 * i + 1][0] = f.z, q[2 * i + 1][1] = f.w;
       }
       int h0, r0, r1;
-      column_of(p, sq, cur.hu, 0, &r0, &h0);
-      const float unit = p.a.scale * kLog2e * __ldg(p.a.cache.k_scale + h0 / p.a.group);
+      column_of(p, sq.n, cur.kvh, cur.set(), 0, &r0, &h0);
+      const float unit = p.a.scale * kLog2e * __ldg(p.a.cache.k_scale + cur.kvh);
       // the set's first and last row bound what all of them see
-      column_of(p, sq, cur.hu, kHeads - 1, &r1, &h0);
+      column_of(p, sq.n, cur.kvh, cur.set(), kHeads - 1, &r1, &h0);
       r1 = min(r1, sq.n - 1);
       all_hi = row_hi(sq, r0);
       all_lo = row_lo(p.a, row_hi(sq, r1));
@@ -447,10 +454,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       if (edge) {
         const RowSeq sq = row_seq(p.a, cur.b);
         int row, head, lo[2], hi[2];
-        column_of(p, sq, cur.hu, 2 * t, &row, &head);
+        column_of(p, sq.n, cur.kvh, cur.set(), 2 * t, &row, &head);
         hi[0] = row < sq.n ? row_hi(sq, row) : 0;
         lo[0] = row_lo(p.a, hi[0]);
-        column_of(p, sq, cur.hu, 2 * t + 1, &row, &head);
+        column_of(p, sq.n, cur.kvh, cur.set(), 2 * t + 1, &row, &head);
         hi[1] = row < sq.n ? row_hi(sq, row) : 0;
         lo[1] = row_lo(p.a, hi[1]);
         bool some[2] = {false, false};
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
           if (who & (0x11111111u << t)) any |= 1u << k;
         }
         if (NB == 2) seen |= seen << 16;
-        if (__any_sync(0xffffffffu, partly != 0)) seen &= ~nan_partly<D>(p, sq, cur.hu, st, tok0, partly, &sh.lost[tid]);
+        if (__any_sync(0xffffffffu, partly != 0)) seen &= ~nan_partly<D>(p, sq, cur.kvh, cur.set(), st, tok0, partly, &sh.lost[tid]);
       } else {
         any = 3;
       }
@@ -576,14 +583,13 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
               if ((lost >> (8 * (j >> 3) + 2 * t + (e & 1))) & 1) o[j][e] = __uint_as_float(0x7FC00000u);
         }
         if (ends && first_c == 0) {           // all of it
-          const RowSeq sq = row_seq(p.a, cur.b);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            int row, head;
-            if (column_of(p, sq, cur.hu, 2 * t + i, &row, &head)) {
-              const bool some = (any >> i) & 1;
-              const float f = some ? out_factor(p.a, head, head / p.a.group, m[i], l[i], kPBias) : 0.0f;
-              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + (int64_t)(sq.s0 + row) * p.a.ldo + (int64_t)head * D;
+            const bool some = (any >> i) & 1;
+            const Place at = sh.place[warp][later][2 * t + i];
+            const float f = at.factor(m[i], l[i]);
+            if (at.to >= 0) {
+              __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + at.to;
 #pragma unroll
               for (int c = 0; c < NB; ++c) {
                 uint32_t w[EJ];
@@ -630,13 +636,14 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
             pm.u0 = u0 + n - cur.c + first_c;
             pm.u1 = u0 + n + 1;
             pm.nb = cur.nb;
-            pm.b = cur.b;
-            pm.hu = cur.hu;
+            pm.place = sh.place[warp][later];
             pm.used = 1;
           }
         }
         if (!last) {
           cur.next(p);
+          later = 1;
+          __syncwarp();  // every lane has read the places that are filled again
           uint4 w[KS / 2];
           load_q(w);
           begin(w);
@@ -656,8 +663,8 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     const uint32_t firsts = __ballot_sync(0xffffffffu, first);
     const int k = __popc(below), run = __popc(firsts & ((2u << lane) - 1)) - 1;
     if (used) {
-      sh.list[k] = lane;
-      sh.run_of[k] = run;
+      sh.slot[k] = lane;
+      sh.list[k] = (lane & 1) ? (lane >> 1) * C::kRing : C::kOffPart + (lane >> 1) * C::kPartBytes;
     }
     if (first) sh.run_first[run] = k;
     if (lane == 0) {
@@ -668,49 +675,61 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   }
   __syncthreads();
   const int runs = sh.runs;
-  auto part_at = [&](int k) {
-    const int i = sh.list[k];
-    return reinterpret_cast<const float*>(smem + ((i & 1) ? (i >> 1) * C::kRing : C::kOffPart + (i >> 1) * C::kPartBytes));
-  };
-  for (int i = tid; i < sh.parts * kHeads; i += C::kThreads) {
-    const int k = i / kHeads, h = i % kHeads, run = sh.run_of[k], k0 = sh.run_first[run], k1 = sh.run_first[run + 1];
-    float m = -INFINITY;
-    for (int j = k0; j < k1; ++j) m = fmaxf(m, part_at(j)[kHeads * D + h]);
-    const float ms = m == -INFINITY ? 0.0f : m;
-    sh.weight[k][h] = fast_exp2(part_at(k)[kHeads * D + h] - ms);
-    if (k == k0) {
-      float l = 0.0f;
-      int any = 0;
-      for (int j = k0; j < k1; ++j) {
-        const float* q = part_at(j) + kHeads * D;
-        l += fast_exp2(q[h] - ms) * q[kHeads + h];
-        any |= q[2 * kHeads + h] != 0.0f;
-      }
+  auto part_at = [&](int k) { return reinterpret_cast<const float*>(smem + sh.list[k]); };
+  // a warp takes one column of a run: its parts side by side in the lanes
+#pragma unroll 1
+  for (int task = warp; task < runs * kHeads; task += C::kWarps) {
+    const int run = task / kHeads, h = task % kHeads, k0 = sh.run_first[run], n = sh.run_first[run + 1] - k0;
+    const Place& at = sh.part[sh.slot[k0]].place[h];
+    const float* q = part_at(k0 + (lane < n ? lane : 0)) + kHeads * D + h;
+    const float mine = q[0];
+    float m = mine;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float w = fast_exp2(mine - (m == -INFINITY ? 0.0f : m));
+    float l = lane < n ? w * q[kHeads] : 0.0f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    const bool any = __any_sync(0xffffffffu, q[2 * kHeads] != 0.0f);
+    if (lane < n) sh.weight[k0 + lane][h] = w;
+    if (lane == 0) {
       sh.run_m[run][h] = m;
       sh.run_l[run][h] = l;
       sh.run_any[run][h] = any;
+      sh.run_factor[run][h] = at.factor(m, l);
     }
   }
   __syncthreads();
+  auto store_pair = [&](const PartMeta& first, int at, float2 o, const float* factor, const int* some) {
+    const int h = at / D;
+    const int64_t to = first.place[h].to;
+    const float f = factor[h];
+    const bool any = some[h];
+    if (to >= 0)
+      *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.a.out) + to + at % D) =
+          any ? __floats2bfloat162_rn(o.x * f, o.y * f) : __floats2bfloat162_rn(0.0f, 0.0f);
+  };
   float* parts = reinterpret_cast<float*>(p.a.workspace + kAttendCleared);
   uint32_t* counters = reinterpret_cast<uint32_t*>(p.a.workspace + kRowCounts);
   constexpr int kPairs = kHeads * D / 2;  // of a run's sums
   auto whole = [&](int run) {
-    const PartMeta &f = sh.part[sh.list[sh.run_first[run]]], &e = sh.part[sh.list[sh.run_first[run + 1] - 1]];
+    const PartMeta &f = sh.part[sh.slot[sh.run_first[run]]], &e = sh.part[sh.slot[sh.run_first[run + 1] - 1]];
     return f.u0 == f.seg0 && e.u1 == f.seg0 + f.nb;
   };
+#pragma unroll 1
   for (int i = tid; i < runs * kPairs; i += C::kThreads) {
     const int run = i / kPairs, at = (i % kPairs) * 2, h = at / D;
     float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
     for (int k = sh.run_first[run]; k < sh.run_first[run + 1]; ++k) {
       const float w = sh.weight[k][h];
       const float2 v = *reinterpret_cast<const float2*>(part_at(k) + at);
       o.x += w * v.x;
       o.y += w * v.y;
     }
-    const PartMeta& first = sh.part[sh.list[sh.run_first[run]]];
+    const PartMeta& first = sh.part[sh.slot[sh.run_first[run]]];
     if (whole(run)) {
-      store_pair<D>(p, first.b, first.hu, h, at % D, o, sh.run_m[run][h], sh.run_l[run][h], sh.run_any[run][h]);
+      store_pair(first, at, o, sh.run_factor[run], sh.run_any[run]);
     } else {
       // slot 0: what began in an earlier CTA, slot 1: what begins here and goes on
       float* dst = parts + ((int64_t)blockIdx.x * 2 + (first.u0 == first.seg0)) * C::kPartFloats;
@@ -728,12 +747,11 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   // CTAs from c0 to c1 share a run: CTA i holds [i U / G, (i + 1) U / G)
   auto first_cta = [&](const PartMeta& f) { return ((f.seg0 + 1) * G - 1) / U; };
   auto last_cta = [&](const PartMeta& f) { return ((f.seg0 + f.nb) * G - 1) / U; };
-  __threadfence();
-  __syncthreads();
+  __syncthreads();  // the fence below covers what the CTA wrote before
   if (lane == 0 && warp < 2) {
     sh.last[warp] = 0;
     if (warp ? shared1 : shared0) {
-      const PartMeta& f = sh.part[sh.list[sh.run_first[warp ? runs - 1 : 0]]];
+      const PartMeta& f = sh.part[sh.slot[sh.run_first[warp ? runs - 1 : 0]]];
       uint32_t* count = counters + first_cta(f);
       __threadfence();
       const bool last = atomicAdd(count, 1u) == (uint32_t)(last_cta(f) - first_cta(f));
@@ -744,9 +762,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   }
   __syncthreads();
   float* weight = reinterpret_cast<float*>(smem);  // [parts][8], in the place of the rings
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     if (!sh.last[which]) continue;
-    const PartMeta& f = sh.part[sh.list[sh.run_first[which ? runs - 1 : 0]]];
+    const PartMeta& f = sh.part[sh.slot[sh.run_first[which ? runs - 1 : 0]]];
     const int64_t c0 = first_cta(f);
     const int n = (int)(last_cta(f) - c0) + 1;
     // CTA c0's part is in its slot 1, the others' in their slot 0
@@ -754,10 +773,12 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
     for (int h = warp; h < kHeads; h += C::kWarps) {
       float m = -INFINITY, l = 0.0f;
       bool any = false;
+#pragma unroll 1
       for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(part_of(k) + kHeads * D + h));
 #pragma unroll
       for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
       const float ms = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
       for (int k = lane; k < n; k += 32) {
         const float* q = part_of(k) + kHeads * D + h;
         const float w = fast_exp2(__ldcg(q) - ms);
@@ -769,23 +790,22 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
       for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
       any = __any_sync(0xffffffffu, any);
       if (lane == 0) {
-        sh.run_m[which][h] = m;
-        sh.run_l[which][h] = l;
         sh.run_any[which][h] = any;
+        sh.run_factor[which][h] = f.place[h].factor(m, l);
       }
     }
     __syncthreads();
     for (int i = tid; i < kPairs; i += C::kThreads) {
       const int at = i * 2, h = at / D;
       float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 8
+#pragma unroll 4
       for (int k = 0; k < n; ++k) {
         const float2 v = __ldcg(reinterpret_cast<const float2*>(part_of(k) + at));
         const float w = weight[k * kHeads + h];
         o.x += w * v.x;
         o.y += w * v.y;
       }
-      store_pair<D>(p, f.b, f.hu, h, at % D, o, sh.run_m[which][h], sh.run_l[which][h], sh.run_any[which][h]);
+      store_pair(f, at, o, sh.run_factor[which], sh.run_any[which]);
     }
     __syncthreads();
   }
@@ -813,6 +833,7 @@ cudaError_t launch_attend_row(const AttendLaunch& L, int head_dim, cudaStream_t 
   RowParams p;
   p.a = L;
   p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
+  p.by_group = (uint32_t)(((uint64_t)1 << 32) / L.group + 1);
   return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
 }
 
