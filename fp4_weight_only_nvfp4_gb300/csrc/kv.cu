@@ -42,12 +42,38 @@ __device__ __forceinline__ void load_norm8(const void* w, int fp32, int d, float
   }
 }
 
-// (hi, lo) += v, hi + lo the exact sum but for the rounding of lo (Knuth's two-sum).
-__device__ __forceinline__ void two_add(float& hi, float& lo, float v) {
-  const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
-  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b));
-  hi = s;
-  lo = __fadd_rn(lo, e);
+// Largest magnitude pattern (sign cleared) among 8 bf16 values.
+__device__ __forceinline__ uint32_t magnitude8(const uint4 v) {
+  constexpr uint32_t M = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & M, v.y & M), __vmaxu2(v.z & M, v.w & M));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Sum of a vector's squares over its LANES lanes (8 bf16 values each), rounded to fp32 once.  The
+// values are taken times 2^-e, e the exponent of the largest (mag: its pattern), so that a square x^2
+// is below 4 and has 16 bits; it is cut at 2^-13 into a + b, a = (x^2 + C) - C.  256 a's add up without
+// a rounding (below 2^24 units of 2^-13), the b's with errors of 2^-23 of what is below 2^-6: the sum is held to 2^-32
+// of the largest square.
+template <int LANES>
+__device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) {
+  if (mag >= 0x7F80u) return __uint_as_float(mag << 16);  // inf or NaN
+  const int e = min(max((int)(mag >> 7) - 127, -126), 126);  // (at 2^127 the sum is inf in any case)
+  const float down = pow2f(-e), up = pow2f(e);
+  constexpr float C = 1.5f * 1024.0f;                      // its last bit is 2^-13
+  float a = 0.0f, b = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = x[i] * down;
+    const float t = __fsub_rn(__fmaf_rn(v, v, C), C);
+    a = __fadd_rn(a, t);
+    b = __fadd_rn(b, __fmaf_rn(v, v, -t));
+  }
+#pragma unroll
+  for (int m = 1; m < LANES; m <<= 1) {
+    a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, m));
+    b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, m));
+  }
+  return __fadd_rn(a, b) * up * up;
 }
 
 // D / 8 lanes take one head's vector of one token, 8 values each.  The decisions of the quantiser
@@ -58,33 +84,26 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendLaunch
   constexpr int LANES = D / 8;
   const int sub = threadIdx.x % LANES, d = sub * 8;
   const int per_token = p.q_heads + 2 * p.cache.heads;
-  const int64_t items = p.T * per_token;
-  const int64_t item = (blockIdx.x * (int64_t)kAppendThreads + threadIdx.x) / LANES;
   // every lane stays for the shuffles; one past the end repeats the last item and stores nothing
+  const int64_t items = p.T * per_token, item = (blockIdx.x * (int64_t)kAppendThreads + threadIdx.x) / LANES;
   const bool live = item < items;
   const int64_t it = live ? item : items - 1;
-  const int64_t t = it / per_token;
+  const int64_t t = it >> 32 ? it / per_token : (uint32_t)it / (uint32_t)per_token;
   const int h = (int)(it - t * per_token);
   const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.cache.heads;
   const int kvh = is_q ? 0 : (is_k ? h - p.q_heads : h - p.q_heads - p.cache.heads);
   const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_q ? p.q : is_k ? p.k : p.v) +
                              t * (is_q ? p.ldq : is_k ? p.ldk : p.ldv) + (int64_t)(is_q ? h : kvh) * D + d;
+  const uint4 raw = *reinterpret_cast<const uint4*>(src);
   float x[8];
-  unpack8(*reinterpret_cast<const uint4*>(src), x);
+  unpack8(raw, x);
   const bool turned = is_q || is_k;
 
   if (p.k_norm) {  // uniform over the grid: every lane takes part in the shuffles
-    // squares of bf16 values are exact in fp32; their sum is held in two words and rounded once
-    float hi = 0.0f, lo = 0.0f;
+    uint32_t mag = magnitude8(raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) two_add(hi, lo, __fmul_rn(x[i], x[i]));
-#pragma unroll
-    for (int m = 1; m < LANES; m <<= 1) {
-      const float ohi = __shfl_xor_sync(0xffffffffu, hi, m), olo = __shfl_xor_sync(0xffffffffu, lo, m);
-      two_add(hi, lo, ohi);
-      lo = __fadd_rn(lo, olo);
-    }
-    const float ms = __fmul_rn(__fadd_rn(hi, lo), 1.0f / D);
+    for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
+    const float ms = __fmul_rn(sum_squares<LANES>(x, mag), 1.0f / D);
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
     if (turned) {
       float w[8];

@@ -12,32 +12,72 @@ namespace vt {
 
 namespace {
 
-// V values of a row from element i on (V = 8: 16-byte loads; V = 1: any alignment and stride).
+// V values of a row as they lie (V = 8: 16-byte loads; V = 1: any alignment and stride), bf16 or
+// either type.
 template <int V>
-__device__ __forceinline__ void load_bf16(const void* base, int64_t at, float (&x)[V]) {
+struct Raw {
+  uint32_t w[V == 8 ? 4 : 1];
+};
+template <int V>
+struct RawAny {
+  uint32_t w[V];
+};
+template <int V>
+__device__ __forceinline__ void fetch(Raw<V>& r, const void* base, int64_t at) {
   const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(base) + at;
   if constexpr (V == 8) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+template <int V>
+__device__ __forceinline__ void widen(const Raw<V>& r, float (&x)[V]) {
+  if constexpr (V == 8) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      x[2 * q] = bf16_lo(w[q]);
-      x[2 * q + 1] = bf16_hi(w[q]);
+      x[2 * q] = bf16_lo(r.w[q]);
+      x[2 * q + 1] = bf16_hi(r.w[q]);
     }
   } else {
-    x[0] = __bfloat162float(*p);
+    x[0] = bf16_lo(r.w[0]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void fetch_any(RawAny<V>& r, const void* base, int fp32, int64_t at) {
+  if (fp32) {
+    const float* p = reinterpret_cast<const float*>(base) + at;
+    if constexpr (V == 8) {
+      const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+      r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w, r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+    } else {
+      r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  } else {
+    Raw<V> h;
+    fetch(h, base, at);
+#pragma unroll
+    for (int i = 0; i < (V == 8 ? 4 : 1); ++i) r.w[i] = h.w[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void widen_any(const RawAny<V>& r, int fp32, float (&x)[V]) {
+  if (fp32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __uint_as_float(r.w[i]);
+  } else {
+    Raw<V> h;
+#pragma unroll
+    for (int i = 0; i < (V == 8 ? 4 : 1); ++i) h.w[i] = r.w[i];
+    widen(h, x);
   }
 }
 template <int V>
 __device__ __forceinline__ void load_any(const void* base, int fp32, int64_t at, float (&x)[V]) {
-  if (!fp32) return load_bf16<V>(base, at, x);
-  const float* p = reinterpret_cast<const float*>(base) + at;
-  if constexpr (V == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    x[0] = *p;
-  }
+  RawAny<V> r;
+  fetch_any(r, base, fp32, at);
+  widen_any(r, fp32, x);
 }
 template <int V>
 __device__ __forceinline__ void store_any(void* base, int fp32, int64_t at, const float (&x)[V]) {
@@ -84,13 +124,25 @@ __global__ void __launch_bounds__(1024) k_norm(const NormLaunch p) {
   __shared__ float red[2][32];
   const int64_t t = blockIdx.x;
   const int H = (int)p.H, warps = blockDim.x >> 5;
+  // everything that the row needs is under way before the first sum
+  Raw<V> x[N], gate[N];
+  RawAny<V> res[N];
   float a[N][V];
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = (i * blockDim.x + threadIdx.x) * V;
     if (e < H) {
-      load_bf16<V>(p.x, t * p.ldx + e, a[i]);
+      fetch(x[i], p.x, t * p.ldx + e);
+      if (p.gate) fetch(gate[i], p.gate, t * p.ldg + e);
+      if (p.residual) fetch_any(res[i], p.residual, p.residual_fp32, t * p.ldr + e);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = (i * blockDim.x + threadIdx.x) * V;
+    if (e < H) {
+      widen(x[i], a[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) a[i][j] = 0.0f;
@@ -120,7 +172,7 @@ __global__ void __launch_bounds__(1024) k_norm(const NormLaunch p) {
     if (e < H) {
       if (p.gate) {
         float g[V];
-        load_bf16<V>(p.gate, t * p.ldg + e, g);
+        widen(gate[i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) a[i][j] *= g[j];
       }
@@ -128,7 +180,7 @@ __global__ void __launch_bounds__(1024) k_norm(const NormLaunch p) {
       for (int j = 0; j < V; ++j) a[i][j] *= p.scale;
       if (p.residual) {
         float r[V];
-        load_any<V>(p.residual, p.residual_fp32, t * p.ldr + e, r);
+        widen_any(res[i], p.residual_fp32, r);
 #pragma unroll
         for (int j = 0; j < V; ++j) a[i][j] += r[j];
         store_any<V>(p.h, p.residual_fp32, t * p.ldh + e, a[i]);
@@ -151,6 +203,8 @@ __global__ void __launch_bounds__(1024) k_norm(const NormLaunch p) {
   }
 }
 
+constexpr int kOne = 256;
+
 inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 }  // namespace
@@ -161,7 +215,7 @@ cudaError_t launch_norm(const NormLaunch& L, cudaStream_t s) {
                    on16(L.weight) && on16(L.post_weight) && on16(L.gate) && L.ldg % 8 == 0 &&
                    on16(L.residual) && on16(L.h) && (L.ldr & rm) == 0 && (L.ldh & rm) == 0;
   const int64_t chunks = vec ? L.H / 8 : L.H;
-  const int n = vec ? (chunks <= 1024 ? 1 : 2) : (chunks <= 2048 ? 2 : chunks <= 8192 ? 8 : 16);
+  const int n = vec ? (chunks <= kOne ? 1 : 2) : (chunks <= 2048 ? 2 : chunks <= 8192 ? 8 : 16);
   const int threads = (int)(((chunks + n - 1) / n + 31) / 32 * 32);
   const unsigned rows = (unsigned)L.T;
   if (vec) {

@@ -177,9 +177,10 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.
     """The values of tokens: (k, v) bf16 [T, heads, D]; zeros for slots outside the cache."""
     sp, shape = cache._slots(slots), (slots.shape[0], cache.heads, cache.head_dim)
     if out is None:
-        out = tuple(_empty(shape, _BF16, cache.device, stream) for _ in range(2))
-    for t, name in zip(out, ("k", "v")):
-        _need(t, name, _BF16, shape, cache.device)
+        out = _empty(shape, _BF16, cache.device, stream), _empty(shape, _BF16, cache.device, stream)
+    else:
+        for t, name in zip(out, ("k", "v")):
+            _need(t, name, _BF16, shape, cache.device)
     check(lib().vt_fp4_kv_read(cache.view, shape[0], sp, out[0].data_ptr(), out[1].data_ptr(),
                                _raw(stream, cache.gpu)), "vt_fp4_kv_read")
     return out

@@ -477,7 +477,7 @@ vt_status vt_fp4_kv_page_bytes(int64_t page_size, int64_t heads, int64_t head_di
  * Quantisation as vt_fp4_quantize_act, with the head's global as the activation global and without
  * a rounding of k' to bf16 before it: s = E4M3(amax_g / fl32(6 global)), code = E2M1(x / fl32(s
  * global)); a group holding an inf or NaN gets the NaN scale byte.  Every operation above is rounded to fp32
- * on its own (no contraction; the sum of squares is held to 2^-44 and rounded once), so that the
+ * on its own (no contraction; the sum of squares is held to 2^-32 and rounded once), so that the
  * result does not depend on how the work is laid out. */
 vt_status vt_fp4_kv_append(const vt_fp4_kv_cache* cache, int64_t T, const void* q, int64_t q_heads,
                            int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
