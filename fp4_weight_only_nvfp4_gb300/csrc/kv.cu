@@ -76,114 +76,140 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) 
   return __fadd_rn(a, b) * up * up;
 }
 
-// D / 8 lanes take one head's vector of one token, 8 values each.  The decisions of the quantiser
-// follow the vector's values, so each operation is rounded on its own: the result is that of the
-// formulas in fp32 whatever the layout.  Bound by memory: 2 bytes in per value, 2 (q) or 9/16 (k, v) out.
+// D / 8 lanes take one head's vector of one token, 8 values each; a warp takes `steps` times 32 / (D /
+// 8) heads of one token, so that the rotation's angles and the norms' weights are loaded once for them.
+// The decisions of the quantiser follow the vector's values, so each operation is rounded on its
+// own: the result is that of the formulas in fp32 whatever the layout.  Bound by instructions (the norm's two
+// sums, the rotation and the quotients of the codes) at about twice what its bytes need: 2 in per value, 2 (q) or 9/16 (k, v) out.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendLaunch p) {
-  constexpr int LANES = D / 8;
-  const int sub = threadIdx.x % LANES, d = sub * 8;
+__global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLaunch p, const int steps, const int units) {
+  constexpr int LANES = D / 8, HEADS = 32 / LANES;
+  const int lane = threadIdx.x & 31, sub = lane % LANES, d = sub * 8;
   const int per_token = p.q_heads + 2 * p.cache.heads;
-  // every lane stays for the shuffles; one past the end repeats the last item and stores nothing
-  const int64_t items = p.T * per_token, item = (blockIdx.x * (int64_t)kAppendThreads + threadIdx.x) / LANES;
-  const bool live = item < items;
-  const int64_t it = live ? item : items - 1;
-  const int64_t t = it >> 32 ? it / per_token : (uint32_t)it / (uint32_t)per_token;
-  const int h = (int)(it - t * per_token);
-  const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.cache.heads;
-  const int kvh = is_q ? 0 : (is_k ? h - p.q_heads : h - p.q_heads - p.cache.heads);
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_q ? p.q : is_k ? p.k : p.v) +
-                             t * (is_q ? p.ldq : is_k ? p.ldk : p.ldv) + (int64_t)(is_q ? h : kvh) * D + d;
-  const uint4 raw = *reinterpret_cast<const uint4*>(src);
-  float x[8];
-  unpack8(raw, x);
-  const bool turned = is_q || is_k;
+  const int64_t unit = blockIdx.x * (int64_t)(kAppendThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= p.T * units) return;
+  const int64_t t = unit >> 32 ? unit / units : (uint32_t)unit / (uint32_t)units;
+  int h = (int)(unit - t * units) * steps * HEADS + lane / LANES;
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + t * p.ldq + d;
+  const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + t * p.ldk + d;
+  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + t * p.ldv + d;
+  const int64_t slot = p.slots[t];
+  const bool kept = slot >= 0 && slot < p.cache.slots;
+  const int in = kept ? (int)(slot & (p.cache.page_size - 1)) : 0, r = in % kKvTile;
+  uint8_t* const tile0 = kv_tile<D>(p.cache, kept ? slot >> p.cache.page_shift : 0, 0, in);
 
-  if (p.k_norm) {  // uniform over the grid: every lane takes part in the shuffles
-    uint32_t mag = magnitude8(raw);
-#pragma unroll
-    for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
-    const float ms = __fmul_rn(sum_squares<LANES>(x, mag), 1.0f / D);
-    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
-    if (turned) {
-      float w[8];
-      load_norm8(is_q ? p.q_norm : p.k_norm, p.norms_fp32, d, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
-    }
-  }
-
+  // the rotation of this lane's columns
+  const int half = p.rot >> 1;
+  const bool inside = d < p.rot, low = d < half;
+  bool known = true;
+  int from = lane;        // the lane that holds the other of each pair
+  float c[8], sn[8];
   if (p.rot) {
-    const int half = p.rot >> 1;
-    const int pos = turned ? p.positions[t] : 0;
-    const bool known = pos >= 0 && pos < p.table_rows;
-    const float* row = p.table + (known ? (int64_t)pos * p.rot : 0);
-    const bool inside = turned && d < p.rot;
-    if (p.interleaved) {
-      if (inside) {
+    const int pos = p.positions[t];
+    known = pos >= 0 && pos < p.table_rows;
+    if (inside) {
+      const float* row = p.table + (known ? (int64_t)pos * p.rot : 0);
+      if (p.interleaved) {
         const float4 c4 = *reinterpret_cast<const float4*>(row + (d >> 1));
         const float4 s4 = *reinterpret_cast<const float4*>(row + half + (d >> 1));
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
-      }
-    } else {
-      // the other of each pair is half / 8 lanes away (rot is a multiple of 16)
-      const bool low = d < half;
-      const int lane = threadIdx.x & 31;
-      const int from = d < p.rot ? (low ? lane + half / 8 : lane - half / 8) : lane;
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], from);
-      if (inside) {
+        c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+        sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
+      } else {
+        // half / 8 lanes away (rot is a multiple of 16)
+        from = low ? lane + half / 8 : lane - half / 8;
         const int at = low ? d : d - half;
         const float4* cp = reinterpret_cast<const float4*>(row + at);
         const float4* sp = reinterpret_cast<const float4*>(row + half + at);
         const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
-        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+        // of a cos - b sin the second has a minus sign, of b cos + a sin a plus
+        const uint32_t sign = low ? 0x80000000u : 0u;
+        const float s8[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = __fmul_rn(x[i], c[i]), b = __fmul_rn(o[i], s[i]);
-          x[i] = low ? __fsub_rn(a, b) : __fadd_rn(a, b);
-        }
+        for (int i = 0; i < 8; ++i) sn[i] = __uint_as_float(__float_as_uint(s8[i]) ^ sign);
       }
-    }
-    if (inside && !known) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(0x7FC00000u);
     }
   }
 
-  // a scale group is two lanes; an inf or NaN in it shows in its exponent bits
-  uint32_t top = 0;
+  auto fetch = [&](int at) {
+    const int hh = min(at, per_token - 1), kv = hh - p.q_heads;
+    const __nv_bfloat16* src = kv < 0 ? q + (int64_t)hh * D : kv < p.cache.heads ? k + (int64_t)kv * D : v + (int64_t)(kv - p.cache.heads) * D;
+    return *reinterpret_cast<const uint4*>(src);
+  };
+  uint4 next = fetch(h);
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s, h += HEADS) {
+    // every lane stays for the shuffles; one past the last head repeats it and stores nothing
+    const bool live = h < per_token;
+    const int hh = live ? h : per_token - 1;
+    const bool is_q = hh < p.q_heads, is_k = !is_q && hh < p.q_heads + p.cache.heads;
+    const int kvh = hh - p.q_heads - (is_k ? 0 : p.cache.heads);
+    const uint4 raw = next;
+    if (s + 1 < steps) next = fetch(h + HEADS);
+    float x[8];
+    unpack8(raw, x);
+    const bool turned = is_q || is_k;
+    if (__any_sync(0xffffffffu, turned)) {
+      if (p.k_norm) {
+        uint32_t mag = magnitude8(raw);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  if (!live) return;
-  if (is_q) {
-    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.q_out) + t * p.ldo + (int64_t)h * D + d) = pack8(x);
-    return;
+        for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
+        const float ms = __fmul_rn(sum_squares<LANES>(x, mag), 1.0f / D);
+        const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
+        if (turned) {
+          float w[8];
+          load_norm8(is_q ? p.q_norm : p.k_norm, p.norms_fp32, d, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
+        }
+      }
+      if (p.rot) {
+        if (p.interleaved) {
+          if (inside && turned) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = x[2 * i], b = x[2 * i + 1];
+              x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, sn[i]));
+              x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, sn[i]));
+            }
+          }
+        } else {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], from);
+          if (inside && turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o[i], sn[i]));
+          }
+        }
+        if (inside && turned && !known) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(0x7FC00000u);
+        }
+      }
+    }
+    if (is_q && live)
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.q_out) + t * p.ldo + (int64_t)hh * D + d) = pack8(x);
+    if (!__any_sync(0xffffffffu, !is_q)) continue;
+
+    // a scale group is two lanes; an inf or NaN in it shows in its exponent bits
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (is_q || !live || !kept) continue;
+    const float g = (is_k ? p.cache.k_scale : p.cache.v_scale)[kvh];
+    const bool bad = top >= 0x7F800000u;
+    const AqNvGroup a = aq_nv_group(bad ? 0.0f : __uint_as_float(top), g, __fmul_rn(6.0f, g));
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __fdiv_rn(x[i], a.d);
+    const uint32_t codes = bad || a.step == 0.0f ? 0u : aq_e2m1x8(e);
+    uint8_t* tile = tile0 + (int64_t)kvh * (p.cache.page_size / kKvTile) * kv_tile_bytes(D);
+    *reinterpret_cast<uint32_t*>(tile + (is_k ? kv_k_code(D, r, d / 2) : kv_v_code(D, r, d / 2))) = codes;
+    if ((sub & 1) == 0)
+      tile[is_k ? kv_k_scale(D, r, d / 16) : kv_v_scale(D, r, d / 16)] = (uint8_t)(bad ? 0x7Fu : a.sbyte);
   }
-  const int64_t slot = p.slots[t];
-  if (slot < 0 || slot >= p.cache.slots) return;
-  const float g = (is_k ? p.cache.k_scale : p.cache.v_scale)[kvh];
-  const bool bad = top >= 0x7F800000u;
-  const AqNvGroup q = aq_nv_group(bad ? 0.0f : __uint_as_float(top), g, __fmul_rn(6.0f, g));
-  float c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = __fdiv_rn(x[i], q.d);
-  const uint32_t codes = bad || q.step == 0.0f ? 0u : aq_e2m1x8(c);
-  const int64_t page = slot >> p.cache.page_shift;
-  const int in = (int)(slot & (p.cache.page_size - 1)), r = in % kKvTile;
-  uint8_t* tile = kv_tile<D>(p.cache, page, kvh, in);
-  *reinterpret_cast<uint32_t*>(tile + (is_k ? kv_k_code(D, r, d / 2) : kv_v_code(D, r, d / 2))) = codes;
-  if ((sub & 1) == 0)
-    tile[is_k ? kv_k_scale(D, r, d / 16) : kv_v_scale(D, r, d / 16)] = (uint8_t)(bad ? 0x7Fu : q.sbyte);
 }
 
 // One thread per (token, head, 16 values): their 8 code bytes and scale byte of K and of V.
@@ -248,8 +274,12 @@ cudaError_t move(const KvMoveLaunch& L, int dir, cudaStream_t s) {
 
 template <int D>
 cudaError_t append(const AppendLaunch& L, cudaStream_t s) {
-  const int64_t threads = L.T * (L.q_heads + 2 * L.cache.heads) * (D / 8);
-  k_kv_append<D><<<(unsigned)((threads + kAppendThreads - 1) / kAppendThreads), kAppendThreads, 0, s>>>(L);
+  constexpr int kHeads = 32 / (D / 8), kWarps = kAppendThreads / 32;
+  const int64_t all = (L.q_heads + 2 * L.cache.heads + kHeads - 1) / kHeads;
+  // a few thousand warps fill the GPU; beyond them a warp takes up to 32 steps of its token (8192 tokens of 32 heads of 256: 148 us
+  // with 2 steps, 111 with 8, 103 with 32)
+  const int64_t fill = L.T * all / 8192, steps = fill < 1 ? 1 : fill > 32 ? 32 : fill, units = (all + steps - 1) / steps;
+  k_kv_append<D><<<(unsigned)((L.T * units + kWarps - 1) / kWarps), kAppendThreads, 0, s>>>(L, (int)steps, (int)units);
   return cudaGetLastError();
 }
 
