@@ -498,10 +498,16 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               if (edge) {  // scores that a row does not see become -inf in their place
 #pragma unroll 1
                 for (int c = 0; c < KB; c += 32) {
+                  // columns of these 32 that the row sees, a bit each
+                  uint32_t seen = hi - c >= 32 ? 0xFFFFFFFFu : hi <= c ? 0u : (1u << (hi - c)) - 1;
+                  if (lo > c) seen &= lo - c >= 32 ? 0u : 0xFFFFFFFFu << (lo - c);
+                  if ((gone >> (c >> 4)) & 1) seen &= 0xFFFF0000u;
+                  if ((gone >> (c >> 4)) & 2) seen &= 0x0000FFFFu;
+                  if (__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) continue;
                   tmem_ld32(tS + c, v[0]);
 #pragma unroll
                   for (int e = 0; e < 32; ++e)
-                    if (c + e < lo || c + e >= hi || ((gone >> ((c + e) >> 4)) & 1)) v[0][e] = 0xFF800000u;
+                    if (!((seen >> e) & 1)) v[0][e] = 0xFF800000u;
                   tmem_st32(tS + c, v[0]);
                 }
                 tmem_st_wait();
@@ -697,9 +703,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           const int64_t seg1 = w.seg0 + w.count;
           const int64_t total_units = *reinterpret_cast<volatile int64_t*>(&sh.total), ctas = *reinterpret_cast<volatile int64_t*>(&sh.G);
           const int64_t c0 = ((w.seg0 + 1) * ctas - 1) / total_units, c1 = (seg1 * ctas - 1) / total_units;
-          __threadfence();
           __syncwarp();
-          if (lane == 0) mbar_arrive(joined);
+          if (lane == 0) mbar_arrive(joined);  // (the fence below covers what these warps wrote before)
           if (warp == 0) {
             if (!(ok = warp_wait(joined, (st & kPart) != 0, abort, p.wait_ns))) break;
             if (lane == 0) {
