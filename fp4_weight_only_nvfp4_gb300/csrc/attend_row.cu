@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   RowShared& sh = *reinterpret_cast<RowShared*>(smem + C::kOffMeta);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int B = (int)p.a.B;
+  pdl_launch_dependents();
 
   // ---- the line: chunks of every sequence times its heads and sets, and where this CTA's warps begin
   auto units = [&](int b) -> int64_t {

@@ -1033,6 +1033,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
   tc_fence_after();
   __syncwarp();
   if (warp == C::kWarpMma) tmem_dealloc(tmem, 512);
+  pdl_wait();  // what follows this kernel in the stream follows the row kernel, too
 }
 
 template <int D>
@@ -1042,8 +1043,19 @@ cudaError_t go(TileParams p, cudaStream_t s) {
   constexpr size_t bytes = C::kOffMeta + sizeof(TileShared) + 1024;
   static_assert(bytes <= 232448, "shared memory");
   if (cudaError_t e = set_up_kernel(k_attend_tile<D>, bytes, done)) return e;
-  k_attend_tile<D><<<p.G, C::kThreads, bytes, s>>>(p);
-  return cudaGetLastError();
+  // The two kernels of a call share neither rows nor workspace: this one starts on the SMs that the
+  // row kernel leaves.  It is launched once every CTA of that one runs, so it may wait for its end.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.G);
+  cfg.blockDim = dim3((unsigned)C::kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend_tile<D>, p);
 }
 
 }  // namespace
