@@ -278,7 +278,9 @@ cudaError_t append(const AppendLaunch& L, cudaStream_t s) {
   const int64_t all = (L.q_heads + 2 * L.cache.heads + kHeads - 1) / kHeads;
   // a few thousand warps fill the GPU; beyond them a warp takes up to 32 steps of its token (8192 tokens of 32 heads of 256: 148 us
   // with 2 steps, 111 with 8, 103 with 32)
-  const int64_t fill = L.T * all / 8192, steps = fill < 1 ? 1 : fill > 32 ? 32 : fill, units = (all + steps - 1) / steps;
+  const int64_t fill = L.T * all / 8192;
+  int64_t steps = fill < 1 ? 1 : fill > 32 ? 32 : fill, units = (all + steps - 1) / steps;
+  if (L.T * units / kWarps > (int64_t)1 << 30) steps = all, units = 1;  // more blocks than a grid has
   k_kv_append<D><<<(unsigned)((L.T * units + kWarps - 1) / kWarps), kAppendThreads, 0, s>>>(L, (int)steps, (int)units);
   return cudaGetLastError();
 }

@@ -227,8 +227,8 @@ vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const 
   if (!starts && T != B) return fail(VT_ERR_INVALID_ARG, "without starts there is one row per sequence: T must be B");
   if (!isfinite(scale)) return fail(VT_ERR_INVALID_ARG, "scale must be finite");
   if (window < 0) return fail(VT_ERR_INVALID_ARG, "window must not be negative");
-  if (ldt < 1 || ldt >= ((int64_t)1 << 31) / cache->page_size)
-    return fail(VT_ERR_INVALID_ARG, "ldt must be at least 1 and ldt * page_size below 2^31");
+  if (ldt < 1 || ldt > ((int64_t)1 << 30) / cache->page_size)
+    return fail(VT_ERR_INVALID_ARG, "ldt must be at least 1 and ldt * page_size at most 2^30");
   if (T == 0 || B == 0) return VT_OK;
   if (vt_status st = check_heads(q, ldq, q_heads * cache->head_dim, "q")) return st;
   if (vt_status st = check_heads(out, ldo, q_heads * cache->head_dim, "out")) return st;

@@ -512,7 +512,7 @@ vt_status vt_fp4_attention_workspace_bytes(const vt_fp4_kv_cache* cache, int64_t
  * over the keys j that row t sees; head h reads key/value head h / (q_heads / heads).
  *   tables (device) int32 [B][ldt]: sequence b's key j is token j % page_size of page
  *     tables[b][j / page_size]; entries behind its last key are not read.  A key on a page
- *     outside [0, pages) is left out.
+ *     outside [0, pages) is left out.  ldt * page_size <= 2^30.
  *   lens   (device) int32 [B]: its number of keys (at most ldt * page_size are used).
  *   starts (device, optional) int32 [B + 1], ascending: rows starts[b] .. starts[b + 1] of q are its
  *     last ones, in order (the last row sees the last key, the one before it all but that, ...); NULL: one row each, T == B.

@@ -257,3 +257,67 @@ def test_short_calls_again_and_again(D):
     want = c.check()
     for _ in range(60):
         assert torch.equal(c.run(), want)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed one after another in a stream: single rows, and chunks of few and of many rows."""
+    rng = np.random.default_rng(18)
+    one, many = Case(rng, [300, 40, 1000], 8, 2, 128, 16), Case(rng, [300, 40, 1000], 8, 2, 128, 16, rows=[5, 1, 200])
+    ws = vt.attention_workspace(206, 3, 8, one.cache)
+    calls = []
+    for c in (one, many):
+        q, tables, lens = c.q.cuda(), gpu(c.tables), gpu(c.lens)
+        more = {} if c.starts is None else {"starts": gpu(c.starts)}
+        out = torch.empty_like(q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            vt.paged_attention(q, c.cache, tables, lens, out=out, workspace=ws, **more)
+        calls.append((graph, out, c.run(), (q, tables, lens, more)))
+    for _ in range(4):
+        for graph, out, want, _ in calls:
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want)
+    assert vt.workspace_status(ws) == 0
+
+
+def test_calls_on_two_streams_at_once():
+    rng = np.random.default_rng(19)
+    cases = [Case(rng, [3000, 40, 5000], 8, 2, 128, 16), Case(rng, [3000, 400, 1000], 8, 2, 128, 16, rows=[5, 300, 200])]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    held = [(c.q.cuda(), gpu(c.tables), gpu(c.lens), {} if c.starts is None else {"starts": gpu(c.starts)},
+             vt.attention_workspace(c.q.shape[0], 3, 8, c.cache)) for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, s, (q, tables, lens, more, ws) in zip(cases, streams, held):
+            got.append(vt.paged_attention(q, c.cache, tables, lens, workspace=ws, stream=s, **more))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 2])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_a_set_with_limits_of_their_own(D):
+    """Few rows of several heads share a set of columns: windows and NaN values that only some of them see."""
+    rng = np.random.default_rng(D + 7)
+    c = Case(rng, [70, 33, 200, 5], 6, 2, D, 16, rows=[3, 5, 4, 5])
+    vs = c.raw[3]
+    vs[c.slots(0)[68], 0, 1] = vs[c.slots(1)[32], 1, 0] = vs[c.slots(2)[198], 1, D // 16 - 1] = vs[c.slots(3)[0], 0, 2] = 0x7F
+    c.cache.put(gpu(np.arange(c.pages * c.page)), *(gpu(a) for a in c.raw))
+    for window in (0, 1, 2, 30):
+        got = f64(c.run(window=window))
+        ref, err = attention(f64(c.q), *c.kv(), c.tables, c.lens, c.starts, c.page, D ** -0.5, window)
+        lost = np.isnan(ref)
+        assert lost.any() and np.array_equal(np.isnan(got), lost)
+        assert_close(got[~lost], ref[~lost], err[~lost])
+
+
+def test_more_sequences_than_threads():
+    """The line of a thousand short sequences, some of them empty, takes several rounds of the prologue."""
+    rng = np.random.default_rng(20)
+    lens = rng.integers(0, 40, 1300).tolist()
+    Case(rng, lens, 2, 1, 64, 16).check()
+    rows = [min(n, int(r)) for n, r in zip(lens, rng.integers(0, 60, 1300))]
+    Case(rng, lens, 2, 1, 64, 16, rows=rows).check()
