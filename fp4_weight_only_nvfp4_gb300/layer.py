@@ -14,6 +14,12 @@ CLEARED = 4096  # bytes of an attention workspace that start as zeros
 _BF16, _F32 = torch.bfloat16, torch.float32
 
 
+def _on(t, name, gpu):
+    """gpu is a CUDA device's number, which no tensor of another kind returns as its own."""
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+
+
 def _heads(t, name, rows, heads, dim, gpu):
     """A bf16 [rows, heads, dim] tensor whose heads stand side by side; returns its row stride."""
     if t.dtype is not _BF16 or t.shape != (rows, heads, dim):
@@ -21,8 +27,7 @@ def _heads(t, name, rows, heads, dim, gpu):
     ld, between, inner = t.stride()
     if inner != 1 or (between != dim and heads > 1):
         raise ValueError(f"the heads of a row of {name} must stand side by side")
-    if t.get_device() != gpu or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+    _on(t, name, gpu)
     if rows <= 1:
         return heads * dim
     if ld < heads * dim:
@@ -33,17 +38,19 @@ def _heads(t, name, rows, heads, dim, gpu):
 def _vector(t, name, dtype, n, gpu):
     if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{n}]")
-    if t.get_device() != gpu or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+    _on(t, name, gpu)
     return t.data_ptr()
 
 
-def _weights(named, n, gpu):
-    """Weights [n], all bf16 or all fp32: (pointers, 1 if fp32)."""
-    kind = next((t.dtype for _, t in named if t is not None), _BF16)
-    if kind not in (_BF16, _F32):
-        raise ValueError(f"{' and '.join(m for m, _ in named)} must be bf16 or fp32")
-    return [0 if t is None else _vector(t, m, kind, n, gpu) for m, t in named], int(kind is _F32)
+def _weights(a, a_name, b, b_name, n, gpu):
+    """Two weights [n], either of which may be None, both bf16 or both fp32: (pointers, 1 if fp32)."""
+    if a is None and b is None:
+        return 0, 0, 0
+    kind = (b if a is None else a).dtype
+    if kind is not _BF16 and kind is not _F32:
+        raise ValueError(f"{a_name} and {b_name} must be bf16 or fp32")
+    return (0 if a is None else _vector(a, a_name, kind, n, gpu), 0 if b is None else _vector(b, b_name, kind, n, gpu),
+            int(kind is _F32))
 
 
 class KVCache:
@@ -140,7 +147,7 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
     do.  q_norm, k_norm [D] (bf16 or fp32): per-head norms first; positions int32 [T] and table
     (rope_table): then the rotation.  out may be q.  See vt_fp4_kv_append in include/vt_fp4.h."""
     T, D, gpu = k.shape[0], cache.head_dim, cache.gpu
-    ldk, ldv = (_heads(t, n, T, cache.heads, D, gpu) for t, n in ((k, "k"), (v, "v")))
+    ldk, ldv = _heads(k, "k", T, cache.heads, D, gpu), _heads(v, "v", T, cache.heads, D, gpu)
     sp = _vector(slots, "slots", torch.int64, T, gpu)
     if (positions is None) != (table is None):
         raise ValueError("positions and table go together")
@@ -149,9 +156,11 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: K
         if table.dim() != 2:
             raise ValueError("table must be fp32 [positions, rot]")
         rows, rot = table.shape
-        _need(table, "table", _F32, (rows, rot), cache.device)
+        if table.dtype is not _F32 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 tensor [positions, rot]")
+        _on(table, "table", gpu)
         pp, tp = _vector(positions, "positions", torch.int32, T, gpu), table.data_ptr()
-    (qn, kn), fp32 = _weights((("q_norm", q_norm), ("k_norm", k_norm)), D, gpu)
+    qn, kn, fp32 = _weights(q_norm, "q_norm", k_norm, "k_norm", D, gpu)
     heads = ldq = ldo = qp = op = 0
     if q is not None:
         if q.dim() != 3:
@@ -238,8 +247,7 @@ def _matrix(t, name, dtype, rows, cols, gpu):
         return _rows(t, name, rows, cols, gpu)
     if t.shape != (rows, cols) or (t.stride(1) != 1 and cols > 1) or (rows > 1 and t.stride(0) < cols):
         raise ValueError(f"{name} must be a [{rows}, {cols}] tensor with unit inner stride")
-    if t.get_device() != gpu or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{gpu} (got {t.device})")
+    _on(t, name, gpu)
     return t.stride(0) if rows > 1 else cols
 
 
@@ -254,7 +262,7 @@ def residual_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.
         raise ValueError("x must be a bf16 CUDA [T, H] tensor")
     (T, H), gpu = x.shape, x.get_device()
     ldx = _rows(x, "x", T, H, gpu)
-    (wp, pw), fp32 = _weights((("weight", weight), ("post_weight", post_weight)), H, gpu)
+    wp, pw, fp32 = _weights(weight, "weight", post_weight, "post_weight", H, gpu)
     gp = ldg = 0
     if gate is not None:
         gp = gate.data_ptr()
