@@ -52,10 +52,6 @@ __device__ __forceinline__ float out_factor(float value, float sink, float m, fl
   const float w = fast_exp2(m - ts);  // the row's sums are re-based where the sink is larger
   return value * w / (l * w + fast_exp2(s - ts + bias));
 }
-__device__ __forceinline__ float out_factor(const AttendLaunch& a, int head, int kvh, float m, float l, float bias) {
-  return out_factor(a.cache.v_scale[kvh], a.sinks ? a.sinks[head] : -INFINITY, m, l, bias);
-}
-
 // Sum over the CTA's threads, and the sum over the threads before this one.
 template <int WARPS>
 __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* scan, int64_t* total) {

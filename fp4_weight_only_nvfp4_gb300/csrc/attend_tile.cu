@@ -78,13 +78,15 @@ struct TileShared {
   int abort;
   alignas(8) uint64_t bars[24];
   alignas(16) uint8_t walk[8 * 96];  // of each softmax warp
-  alignas(16) int row[256][4];       // of each softmax thread: first key, end of the keys, factor of the scores
+  alignas(16) int row[256][4];       // of each softmax thread: first key, end of the keys, factor of the scores, sink
+  float value[8];                    // of each softmax warp: the values' global
 };
 
 struct TileParams {
   AttendLaunch a;
   int G;
   int tokens;     // of a row tile: 128 / group
+  uint32_t by_group;  // floor(2^32 / group) + 1: quotients of small numbers by it
   float* parts;
   uint64_t wait_ns;
 };
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
   const uint32_t q_full = bar0, k_full = q_full + 16, k_empty = k_full + 16, v_full = k_empty + 16, v_empty = v_full + 16;
   const uint32_t s_full = v_empty + 16;                  // [row tile or buffer]
   const uint32_t p_full = s_full + 16, pv_done = p_full + 16, joined = pv_done + 16, told = joined + 8;
-  const uint32_t half_full = told + 8, half_read = half_full + 8, drain = half_read + 8;
+  const uint32_t half_full = told + 8, half_read = half_full + 8, drain = half_read + 8, p_half = drain + 8;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
+      mbar_init(p_half + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
     }
     mbar_init(joined, C::kSoftWarps);
@@ -420,10 +423,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         const int b0 = w.at + (halved ? X : 0);
         const bool mine_seg = b0 < w.end;
         const int XR = halved ? 0 : X;                  // whose rows
-        const int idx = w.i * per_tile + XR * p.tokens + r / p.a.group;
-        const bool live = mine_seg && r / p.a.group < p.tokens && idx < w.q.n;
+        const int tok = p.a.group == 1 ? r : __umulhi(r, p.by_group), inner = r - tok * p.a.group;
+        const int idx = w.i * per_tile + XR * p.tokens + tok;
+        const bool live = mine_seg && tok < p.tokens && idx < w.q.n;
         auto at_row = [&](int64_t ld) {                 // of q or out, in elements
-          const int tok = r / p.a.group, inner = r - tok * p.a.group, row = halved ? 0 : X;
+          const int row = halved ? 0 : X;
           return (int64_t)(w.q.s0 + w.i * per_tile + row * p.tokens + tok) * ld + (int64_t)(w.h * p.a.group + inner) * D;
         };
         const int seen = w.q.len - w.q.n + idx + 1;       // keys up to the row's own
@@ -439,6 +443,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           const float unit = p.a.scale * kLog2e * p.a.cache.k_scale[w.h];
           const uint32_t sign = unit < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q: the largest product is the largest score
           const int64_t from = live ? at_row(p.a.ldq) : -1;
+          const float value_scale = __ldg(p.a.cache.v_scale + w.h);
+          const float sink = live && p.a.sinks ? __ldg(p.a.sinks + w.h * p.a.group + inner) : -INFINITY;
           int pw = 0;
 #pragma unroll 1
           for (int i0 = 0; i0 < 32; i0 += 8 * RI) {
@@ -463,7 +469,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           }
           float factor = fabsf(unit) * pow2f(pw);
           if (factor == 0.0f) factor = 1e-38f;  // every score 0, a masked one (-inf) stays out
-          st_shared_v4(row_at, row_lo, row_hi, __float_as_uint(factor), 0);
+          st_shared_v4(row_at, row_lo, row_hi, __float_as_uint(factor), __float_as_uint(sink));
+          if (lane == 0) sh.value[warp] = value_scale;
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -583,6 +590,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 if (c) tmem_ld32_issue(tS, v[0]);
                 probabilities(v[1], c + 32);
                 if (!c) break;
+                // the second half's products may begin
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_half + 8 * sbuf);
                 tmem_ld32_issue(tS + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_wait(v[1]);
@@ -591,6 +603,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               split(add2(sum[0], sum[1]), la, lb);
               l += la + lb;
               tmem_st_wait();
+            } else if (KB == 128) {
+              if (lane == 0) mbar_arrive(p_half + 8 * sbuf);
             }
             // With two score buffers this block's scores do not say that the last block's P V is done.  It is
             // waited for here, one phase at a time: a wait on a phase takes the one before it for done.
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         }
         const bool out = mine_seg && !(halved && X == 1);
         const bool whole = w.whole();
-        const int head = w.h * p.a.group + r % p.a.group;
+        auto sink_of = [&]() { return __uint_as_float(ld_shared_v2(row_at + 8).y); };
         float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w.at == 0)) * C::kPartFloats;
         uint32_t lost = 0;
         if (live && out && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
@@ -640,7 +654,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
         };
         if (out) {
-          const float f = whole && live && any ? out_factor(p.a, head, w.h, m, l, kPBias) : 0.0f;
+          const float f = whole && live && any ? out_factor(sh.value[warp], sink_of(), m, l, kPBias) : 0.0f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -737,7 +751,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 const float* st = part_of(k) + C::kRows * D + X * 128 + r;
                 lt += fast_exp2(__ldcg(st) - ms) * __ldcg(st + C::kRows);
               }
-              const float f = at ? out_factor(p.a, head, w.h, mt, lt, kPBias) : 0.0f;
+              const float f = at ? out_factor(sh.value[warp], sink_of(), mt, lt, kPBias) : 0.0f;
               __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.a.out) + at_row(p.a.ldo);
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
@@ -978,21 +992,26 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             if (u >= 2) {
               const int t = u - 2, blk = both ? t >> 1 : t;
               const uint32_t n = it + blk, sbuf = t & 1, X = C::kRowTiles == 2 ? sbuf : 0;
-              if (!wait(p_full + 8 * sbuf, (p_turn >> sbuf) & 1)) break;
+              if (!wait((KB == 128 ? p_half : p_full) + 8 * sbuf, (p_turn >> sbuf) & 1)) break;
               if (!(both && sbuf) && !wait(v_full + 8 * (n & 1), (n >> 1) & 1)) break;
-              p_turn ^= 1u << sbuf;
               tc_fence_after();
               uint32_t add = blk > (halved ? 1 : 0);
               const uint64_t vd = desc_sw128(sV + (n & 1) * C::kKvBytes);
               const uint32_t pt = tmem + sbuf * KB + KB / 2;
 #pragma unroll 1
-              for (int c = 0; c < KB / 64; ++c) {
+              for (int c = KB / 64 - 1; c >= 0; --c) {  // the keys whose probabilities come first
+                if (KB == 128 && c == 0) {
+                  if (!wait(p_full + 8 * sbuf, (p_turn >> sbuf) & 1)) break;
+                  tc_fence_after();
+                }
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                   mma_f16_ta(tmem + C::kTmemO + X * D, pt + (c * 4 + kk) * 8, vd + c * (D * 8) + 2 * kk, ido, add);
                   add = 1;
                 }
               }
+              if (!ok) break;
+              p_turn ^= 1u << sbuf;
               mma_commit(pv_done + 8 * X);
               if (!both || sbuf) mma_commit(v_empty + 8 * (n & 1));
             }
@@ -1070,6 +1089,7 @@ cudaError_t launch_attend_tile(const AttendLaunch& L, int head_dim, cudaStream_t
   p.a = L;
   p.G = sm_count() < kMaxAttendGrid ? sm_count() : kMaxAttendGrid;
   p.tokens = 128 / L.group;
+  p.by_group = (uint32_t)(((uint64_t)1 << 32) / L.group + 1);
   p.parts = reinterpret_cast<float*>(L.workspace + kAttendCleared + attend_row_parts_bytes(head_dim));
   p.wait_ns = kWaitNs;
   return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
