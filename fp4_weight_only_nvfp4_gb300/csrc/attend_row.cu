@@ -3,8 +3,8 @@
 //   S^T = K Q^T,  p = 2^(s - m),  O^T = V^T P^T,  out = O / sum p
 // with 16 tokens x 8 columns of one key/value head as one m16n8k16 product's rows and columns; a column is
 // a query head of a row, and a sequence's rows x heads go in sets of 8.
-// Bound by the cache's bytes (9/16 per value) and close behind by the instructions that turn them into f16: a
-// conversion and a product for every two values (c * s is exact in f16).  So the cache is read once
+// Bound by the instructions that turn the cache's codes (9/16 byte a value) into f16, a conversion and a product
+// for every two values (c * s is exact in f16), twice as long as HBM needs for the bytes.  So the cache is read once
 // for up to 8 columns, every lane's codes are fragments as they lie (see kv.cuh), and the
 // probabilities go from the first product's result to the second's operand by a transpose of
 // registers.
@@ -14,6 +14,11 @@
 // asynchronous copies, running maximum, sum and output, and meets the others only at its range's ends:
 // parts of one (sequence, head) in one CTA are joined in shared memory, those of several CTAs in the
 // workspace by the CTA that comes last, in the order of the line.  No wait for another CTA.
+//
+// Measured: 64 sequences of 2 to 8 thousand keys, 32 heads on 4 of 128: 51 us (3.7 TB/s), of which the
+// line's set-up, the first loads and the joins are some 15; one of 131071 keys, 24 heads on 4 of 256:
+// 51 us (2.9 TB/s; 8 warps a CTA, the output alone takes 64 registers a thread); 251 of up to 1500 keys,
+// 64 heads on 8 of 64, window 1024: 48 us (2.6 TB/s; half the values a score has at 128).
 #include <cuda_bf16.h>
 
 #include "actq.cuh"

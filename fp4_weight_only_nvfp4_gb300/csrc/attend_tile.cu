@@ -20,6 +20,11 @@
 // CTAs; the parts of a tile that CTAs share are joined by the CTA that comes last.  Each (tile,
 // head) stands there with kLead units more than its blocks, for its start and end.
 //
+// Measured: a prompt of 8192 rows, 32 heads on 4 of 128: 552 us, 996 TFLOP/s of its causal half, the
+// tensor pipe 42 % active; the products of one row tile wait for its softmax (some 3000 cycles a block) and
+// share the shared memory with the conversion's stores.  Five chunks of up to 900 rows behind 2500 keys, 64 heads
+// on 8 of 64, window 512 (five blocks a tile): 107 us, half of it a tile's start and end.
+//
 // Every wait inside the CTA is bounded (2 s); one that gives up sets the status word and ends every role.
 #include <cuda_bf16.h>
 
@@ -36,6 +41,7 @@ namespace vt {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
+// (8192 rows, 32 heads on 4: 634 us with 4, 602 with 6, 615 with 9)
 constexpr int kLead = 6;
 
 template <int D>
