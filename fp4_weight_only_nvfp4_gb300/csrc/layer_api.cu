@@ -232,6 +232,7 @@ vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const 
   if (T == 0 || B == 0) return VT_OK;
   if (vt_status st = check_heads(q, ldq, q_heads * cache->head_dim, "q")) return st;
   if (vt_status st = check_heads(out, ldo, q_heads * cache->head_dim, "out")) return st;
+  if (q == out && ldq != ldo) return fail(VT_ERR_INVALID_ARG, "out == q needs ldo == ldq");
   if (!tables || !lens) return fail(VT_ERR_INVALID_ARG, "tables and lens must be set");
   if (!aligned(tables, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(sinks, 4))
     return fail(VT_ERR_MISALIGNED, "tables, lens, starts and sinks must be 4-byte aligned");

@@ -213,7 +213,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, tables: torch.Tensor, lens:
     own: out bf16 [T, q_heads, D].  tables int32 [B, pages]: each sequence's pages, lens int32 [B]:
     its keys.  starts int32 [B + 1]: its rows are starts[b] to starts[b + 1] of q (None: one each).
     scale: D ** -0.5 by default; window: the number of latest keys a row sees (0: all); sinks fp32
-    [q_heads].  See vt_fp4_paged_attention in include/vt_fp4.h."""
+    [q_heads].  out may be q.  See vt_fp4_paged_attention in include/vt_fp4.h."""
     if q.dim() != 3:
         raise ValueError("q must be a bf16 [T, q_heads, head_dim] tensor")
     T, heads, D = q.shape

@@ -502,7 +502,8 @@ vt_status vt_fp4_kv_get(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* 
 
 /* Workspace of vt_fp4_paged_attention for up to T_max rows of q_heads heads and B_max sequences over
  * the cache; 256-byte aligned, its first VT_ATTENTION_CLEARED bytes zeroed once by the caller, reusable afterwards in stream order.
- * Its first word is the status word (vt_fp4_workspace_status). */
+ * Its first word is the status word (vt_fp4_workspace_status); after VT_ERR_TIMEOUT those bytes are
+ * zeroed again before it is reused. */
 #define VT_ATTENTION_CLEARED 4096
 vt_status vt_fp4_attention_workspace_bytes(const vt_fp4_kv_cache* cache, int64_t T_max, int64_t B_max,
                                            int64_t q_heads, size_t* bytes);
@@ -519,7 +520,7 @@ vt_status vt_fp4_attention_workspace_bytes(const vt_fp4_kv_cache* cache, int64_t
  *     Rows from starts[B] on are left as they were.
  *   window > 0: row at position p sees the keys (p - window, p]; 0: all up to p.
  *   sinks  (device, optional) fp32 [q_heads].
- * A row that sees no key gets zeros.  q, out (device) bf16 [T][ldq], [T][ldo], 16-byte aligned, strides
+ * A row that sees no key gets zeros.  out may be q itself (ldo == ldq).  q, out (device) bf16 [T][ldq], [T][ldo], 16-byte aligned, strides
  * multiples of 8, q_heads a multiple of heads, at most 64 times as many.  The scores, the softmax's sums and the output accumulate in
  * fp32; q enters the products in f16 times a power of two per row and head (values below 2^-28 of the row's largest are
  * rounded, by at most 2^-39 of it), p in f16.  Deterministic: the order of its sums follows from the call's sizes, lens and

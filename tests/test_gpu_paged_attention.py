@@ -321,3 +321,34 @@ def test_more_sequences_than_threads():
     Case(rng, lens, 2, 1, 64, 16).check()
     rows = [min(n, int(r)) for n, r in zip(lens, rng.integers(0, 60, 1300))]
     Case(rng, lens, 2, 1, 64, 16, rows=rows).check()
+
+
+@pytest.mark.parametrize("rows", [None, [3, 70, 9]])
+def test_the_output_in_the_place_of_q(rows):
+    rng = np.random.default_rng(21)
+    c = Case(rng, [3000, 400, 9], 8, 2, 128, 16, rows=rows)
+    want, q = c.run(), c.q.cuda()
+    more = {} if rows is None else {"starts": gpu(c.starts)}
+    for _ in range(10):
+        q.copy_(c.q)
+        assert vt.paged_attention(q, c.cache, gpu(c.tables), gpu(c.lens), out=q, **more) is q
+        assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [None, [2, 70, 5]])
+def test_infinities_in_queries_and_sinks(rows, D):
+    """An infinity in q makes its row and head NaN (or a product 0 * inf does), one in the sinks the head;
+    what stands beside them keeps its numbers."""
+    rng = np.random.default_rng(D + 2)
+    c = Case(rng, [100, 190, 40], 6, 2, D, 16, rows=rows)
+    T = c.q.shape[0]
+    c.q[1, 2, 5], c.q[T - 1, 0, 1], c.q[0, 4, 0] = float("inf"), -float("inf"), float("nan")
+    sinks = np.array([0.5, -np.inf, 1.0, np.inf, -2.0, np.nan], dtype=F)
+    got = f64(c.run(sinks=gpu(sinks)))
+    ref, err = attention(f64(c.q), *c.kv(), c.tables, c.lens, c.starts, c.page, D ** -0.5, 0, sinks)
+    lost = np.zeros(got.shape, dtype=bool)
+    lost[1, 2] = lost[T - 1, 0] = lost[0, 4] = True
+    lost[:, 3] = lost[:, 5] = True
+    assert np.isnan(got[lost]).all() and not np.isnan(got[~lost]).any()
+    assert_close(got[~lost], ref[~lost], err[~lost])

@@ -92,9 +92,9 @@ def _attend(L, cache=None, T=2, q=F, heads=8, ldq=1024, tables=F, ldt=3, lens=F,
 
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), INV), (dict(B=-1), INV), (dict(B=3), INV), (dict(B=2 ** 24 + 1, starts=F), INV), (dict(heads=7), INV), (dict(heads=260, ldq=2 ** 20), INV),
-    (dict(ldt=0), INV), (dict(ldt=2 ** 27), INV), (dict(scale=float("inf")), INV), (dict(window=-1), INV), (dict(q=None), INV),
+    (dict(ldt=0), INV), (dict(ldt=2 ** 27), INV), (dict(ldt=2 ** 26 + 1), INV), (dict(scale=float("inf")), INV), (dict(window=-1), INV), (dict(q=None), INV),
     (dict(out=None), INV), (dict(tables=None), INV), (dict(lens=None), INV), (dict(ws=None), INV), (dict(n=100), INV),
-    (dict(ldq=1016), INV), (dict(ldo=1020), INV), (dict(ldo=1028), MIS), (dict(q=OFF8), MIS), (dict(ws=ctypes.c_void_p(A0 + 128)), MIS),
+    (dict(ldq=1016), INV), (dict(ldo=1020), INV), (dict(ldo=1032), INV), (dict(ldo=1028), MIS), (dict(q=OFF8), MIS), (dict(ws=ctypes.c_void_p(A0 + 128)), MIS),
     (dict(tables=ODD), MIS), (dict(starts=ODD), MIS), (dict(sinks=ODD), MIS), (dict(T=0, B=0), OK), (dict(T=0, starts=F), OK)])
 def test_attention(L, kw, want):
     assert _attend(L, **kw) == want
