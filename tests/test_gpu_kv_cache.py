@@ -208,3 +208,32 @@ def test_another_stream_and_a_graph():
     assert torch.equal(out, want)
     for a, b in zip(other.get(everything), cache.get(everything)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_pages_and_rows_more_than_32_bits_apart(D):
+    rng = np.random.default_rng(D + 9)
+    pages, page, heads, T = 4, 16, 2, 9
+    one = _cache(rng, pages, page, heads, D)
+    n = one.data.shape[1]
+    room = torch.empty(((pages - 1) << 32) + n, dtype=torch.uint8, device="cuda")
+    far = room.as_strided((pages, n), (1 << 32, 1))
+    far.copy_(one.data)
+    cache = vt.KVCache(far, page, heads, D, one.k_scale, one.v_scale)
+    wide = torch.empty((T, 1 << 30), dtype=torch.bfloat16, device="cuda")
+    x = acts(rng, T, 4 * heads, D).cuda()
+    q, k, v = x.split([2 * heads, heads, heads], 1)
+    rows = wide[:, :6 * heads * D].unflatten(1, (6 * heads, D))
+    rows[:, :4 * heads] = x
+    slots = gpu(rng.permutation(pages * page)[:T])
+    want = vt.kv_append(q, k, v, one, slots)
+    got = vt.kv_append(rows[:, :2 * heads], rows[:, 2 * heads:3 * heads], rows[:, 3 * heads:4 * heads], cache, slots,
+                       out=rows[:, 4 * heads:])
+    assert torch.equal(got, want) and torch.equal(far, one.data)
+    for a, b in zip(vt.kv_read(cache, slots), vt.kv_read(one, slots)):
+        assert torch.equal(a, b)
+    for a, b in zip(cache.get(slots), one.get(slots)):
+        assert torch.equal(a, b)
+    raw = [t.flip(0).contiguous() for t in one.get(slots)]
+    cache.put(slots, *raw), one.put(slots, *raw)
+    assert torch.equal(far, one.data)

@@ -352,3 +352,37 @@ def test_infinities_in_queries_and_sinks(rows, D):
     lost[:, 3] = lost[:, 5] = True
     assert np.isnan(got[lost]).all() and not np.isnan(got[~lost]).any()
     assert_close(got[~lost], ref[~lost], err[~lost])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [None, [2, 70, 5]])
+def test_pages_and_rows_more_than_32_bits_apart(rows, D):
+    """Pages 2^32 bytes apart and rows of q and out whose offsets pass 2^32 elements give what dense ones do."""
+    rng = np.random.default_rng(D + 3)
+    c = Case(rng, [40, 75, 17], 8, 1, D, 32, rows=rows, spare=0)
+    want = c.run()
+    n = c.cache.data.shape[1]
+    room = torch.empty(((c.pages - 1) << 32) + n, dtype=torch.uint8, device="cuda")
+    far = room.as_strided((c.pages, n), (1 << 32, 1))
+    far.copy_(c.cache.data)
+    c.cache = vt.KVCache(far, c.page, 1, D, c.cache.k_scale, c.cache.v_scale)
+    assert torch.equal(c.run(), want)
+    T = c.q.shape[0]
+    ld = ((1 << 33) // T + 7) // 8 * 8
+    wide = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    q, out = wide[:, :8 * D].unflatten(1, (8, D)), wide[:, 8 * D:16 * D].unflatten(1, (8, D))
+    q.copy_(c.q)
+    more = {} if rows is None else {"starts": gpu(c.starts)}
+    vt.paged_attention(q, c.cache, gpu(c.tables), gpu(c.lens), out=out, **more)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows", [None, [3, 60, 40]])
+def test_sequences_that_share_pages(rows):
+    """A prefix in common: the same pages in several tables, and twice in one."""
+    rng = np.random.default_rng(22)
+    c = Case(rng, [100, 190, 130], 8, 2, 128, 16, rows=rows)
+    c.tables[1, :4] = c.tables[2, :4] = c.tables[0, :4]
+    c.tables[2, 5] = c.tables[2, 4]
+    c.check()
+    c.check(window=50)

@@ -104,3 +104,18 @@ def test_another_stream_and_a_graph():
     x.neg_()
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(out, vt.residual_norm(x, r, w)))
+
+
+@pytest.mark.parametrize("H", [96, 97])
+def test_rows_more_than_32_bits_apart(H):
+    rng = np.random.default_rng(H)
+    T = 9
+    x, r, g = (acts(rng, T, H).cuda() for _ in range(3))
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    want = vt.residual_norm(x, r, w, post_weight=w, gate=g)
+    wide = torch.empty((T, 1 << 30), dtype=torch.bfloat16, device="cuda")
+    part = [wide[:, 1000 * i:1000 * i + H] for i in range(5)]
+    for a, b in zip(part, (x, r, g)):
+        a.copy_(b)
+    got = vt.residual_norm(part[0], part[1], w, post_weight=w, gate=part[2], out=(part[3], part[4]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
