@@ -52,26 +52,38 @@ __device__ __forceinline__ uint32_t magnitude8(const uint4 v) {
 // Sum of a vector's squares over its LANES lanes (8 bf16 values each), rounded to fp32 once.  The
 // values are taken times 2^-e, e the exponent of the largest (mag: its pattern), so that a square x^2
 // is below 4 and has 16 bits; it is cut at 2^-13 into a + b, a = (x^2 + C) - C.  256 a's add up without
-// a rounding (below 2^24 units of 2^-13), the b's with errors of 2^-23 of what is below 2^-6: the sum is held to 2^-32
-// of the largest square.
+// a rounding (below 2^24 units of 2^-13), the b's with errors of 2^-23 of what is below 2^-6 (a lane's) and 2^-37 a lane: the
+// sum is held to 2^-32 of the largest square.  Where a vector takes the whole warp its lanes add integers, one instruction for
+// the ten of a sum by shuffles (8192 tokens of 32 heads of 256, read back: 99 us with shuffles and one value at a time, 98 with two at a
+// time, 91 so).
 template <int LANES>
 __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) {
   if (mag >= 0x7F80u) return __uint_as_float(mag << 16);  // inf or NaN
   const int e = min(max((int)(mag >> 7) - 127, -126), 126);  // (at 2^127 the sum is inf in any case)
   const float down = pow2f(-e), up = pow2f(e);
   constexpr float C = 1.5f * 1024.0f;                      // its last bit is 2^-13
-  float a = 0.0f, b = 0.0f;
+  const uint64_t down2 = pair(down, down), c2 = pair(C, C), minus = pair(-1.0f, -1.0f);
+  uint64_t na = 0, ab = 0;                                 // -a, b
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = x[i] * down;
-    const float t = __fsub_rn(__fmaf_rn(v, v, C), C);
-    a = __fadd_rn(a, t);
-    b = __fadd_rn(b, __fmaf_rn(v, v, -t));
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t v = mul2(pair(x[i], x[i + 1]), down2);
+    const uint64_t nt = fma2(fma2(v, v, c2), minus, c2);   // C - (x^2 + C)
+    na = add2(na, nt);
+    ab = add2(ab, fma2(v, v, nt));
   }
+  float a0, a1, b0, b1;
+  split(na, a0, a1);
+  split(ab, b0, b1);
+  float a = -__fadd_rn(a0, a1), b = __fadd_rn(b0, b1);
+  if constexpr (LANES == 32) {  // a whole warp adds integers in one instruction: units of 2^-13 and of 2^-36
+    a = (float)__reduce_add_sync(0xffffffffu, (int)(a * 8192.0f)) * (1.0f / 8192.0f);
+    b = (float)__reduce_add_sync(0xffffffffu, __float2int_rn(b * 0x1p36f)) * 0x1p-36f;
+  } else {
 #pragma unroll
-  for (int m = 1; m < LANES; m <<= 1) {
-    a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, m));
-    b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, m));
+    for (int m = 1; m < LANES; m <<= 1) {
+      a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, m));
+      b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, m));
+    }
   }
   return __fadd_rn(a, b) * up * up;
 }
@@ -81,7 +93,7 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) 
 // The decisions of the quantiser follow the vector's values, so each operation is rounded on its
 // own: the result is that of the formulas in fp32 whatever the layout.  Bound by instructions (the norm's two
 // sums, the rotation and the quotients of the codes) at some three times what its bytes need (2 in per
-// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 91 us, 72 % of the issue slots.
+// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 82 us, 73 % of the issue slots.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLaunch p, const int steps, const int units) {
   constexpr int LANES = D / 8, HEADS = 32 / LANES;
@@ -153,15 +165,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLau
     if (__any_sync(0xffffffffu, turned)) {
       if (p.k_norm) {
         uint32_t mag = magnitude8(raw);
+        if constexpr (LANES == 32) {
+          mag = __reduce_max_sync(0xffffffffu, mag);
+        } else {
 #pragma unroll
-        for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
+          for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
+        }
         const float ms = __fmul_rn(sum_squares<LANES>(x, mag), 1.0f / D);
         const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
         if (turned) {
           float w[8];
           load_norm8(is_q ? p.q_norm : p.k_norm, p.norms_fp32, d, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
+          for (int i = 0; i < 8; i += 2)
+            split(mul2(mul2(pair(x[i], x[i + 1]), pair(inv, inv)), pair(w[i], w[i + 1])), x[i], x[i + 1]);
         }
       }
       if (p.rot) {
