@@ -88,12 +88,34 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) 
   return __fadd_rn(a, b) * up * up;
 }
 
+// Codes of x / d, each quotient rounded to fp32 first.  x times the rounded 1 / d is off by less than 2^-22 of
+// the quotient, and the codes are monotone: where 2^-21 to both sides give the same ones, those are it.  Else, and
+// where 1 / d has fewer bits, the quotients themselves (the append of 8192 tokens of 24 + 2 * 4 heads of 256: 82 us with divisions alone,
+// 78 so, and 80 with a global of 1, where quotients of bf16 values meet borders often).
+__device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float d) {
+  const float inv = __frcp_rn(d);
+  const uint64_t less = pair(inv * (1.0f - 0x1p-21f), inv * (1.0f - 0x1p-21f)), more = pair(inv * (1.0f + 0x1p-21f), inv * (1.0f + 0x1p-21f));
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    split(mul2(pair(x[i], x[i + 1]), less), lo[i], lo[i + 1]);
+    split(mul2(pair(x[i], x[i + 1]), more), hi[i], hi[i + 1]);
+  }
+  uint32_t codes = aq_e2m1x8(lo);
+  if (codes != aq_e2m1x8(hi) || !(d >= 0x1p-120f && d <= 0x1p120f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = __fdiv_rn(x[i], d);
+    codes = aq_e2m1x8(lo);
+  }
+  return codes;
+}
+
 // D / 8 lanes take one head's vector of one token, 8 values each; a warp takes `steps` times 32 / (D /
 // 8) heads of one token, so that the rotation's angles and the norms' weights are loaded once for them.
 // The decisions of the quantiser follow the vector's values, so each operation is rounded on its
 // own: the result is that of the formulas in fp32 whatever the layout.  Bound by instructions (the norm's two
-// sums, the rotation and the quotients of the codes) at some three times what its bytes need (2 in per
-// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 82 us, 73 % of the issue slots.
+// sums, the rotation and the quotients of the codes; 73 % of the issue slots) at some twice to three times what its bytes need (2 in per
+// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 78 us.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLaunch p, const int steps, const int units) {
   constexpr int LANES = D / 8, HEADS = 32 / LANES;
@@ -219,10 +241,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLau
     const float g = (is_k ? p.cache.k_scale : p.cache.v_scale)[kvh];
     const bool bad = top >= 0x7F800000u;
     const AqNvGroup a = aq_nv_group(bad ? 0.0f : __uint_as_float(top), g, __fmul_rn(6.0f, g));
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = __fdiv_rn(x[i], a.d);
-    const uint32_t codes = bad || a.step == 0.0f ? 0u : aq_e2m1x8(e);
+    const uint32_t codes = bad || a.step == 0.0f ? 0u : quotient_codes(x, a.d);
     uint8_t* tile = tile0 + (int64_t)kvh * (p.cache.page_size / kKvTile) * kv_tile_bytes(D);
     *reinterpret_cast<uint32_t*>(tile + (is_k ? kv_k_code(D, r, d / 2) : kv_v_code(D, r, d / 2))) = codes;
     if ((sub & 1) == 0)

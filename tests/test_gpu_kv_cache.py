@@ -237,3 +237,22 @@ def test_pages_and_rows_more_than_32_bits_apart(D):
     raw = [t.flip(0).contiguous() for t in one.get(slots)]
     cache.put(slots, *raw), one.put(slots, *raw)
     assert torch.equal(far, one.data)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("g", [1.0, 2.0 ** -8, 0.0037, 1e-20, 1e20, 3e-37, 2.0 ** -126])
+def test_codes_on_and_beside_their_borders(g, D):
+    """Quotients that fall on the borders between codes (globals that are powers of two), and globals from the
+    smallest normal number on."""
+    rng = np.random.default_rng(D)
+    T, H = 500, 3
+    gs = torch.full((H,), g, dtype=torch.float32, device="cuda")
+    cache = vt.KVCache.empty(-(-T // 16), 16, H, D, gs, gs)
+    k = _bf16(rng.standard_normal((T, H, D)) * np.exp(rng.uniform(-6, 6, (T, H, 1))) * min(g * 100, 1e30))
+    v = _bf16(rng.integers(-60, 61, (T, H, D)) / 8 * g)
+    slots = torch.arange(T, device="cuda")
+    vt.kv_append(None, k.cuda(), v.cuda(), cache, slots)
+    kc, ks, vc, vs = (t.cpu().numpy() for t in cache.get(slots))
+    for x, codes, scales in ((k, kc, ks), (v, vc, vs)):
+        want = quantise(_f32(x), F(g))
+        assert np.array_equal(codes, want[0]) and np.array_equal(scales, want[1])
