@@ -115,7 +115,7 @@ __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float d)
 // The decisions of the quantiser follow the vector's values, so each operation is rounded on its
 // own: the result is that of the formulas in fp32 whatever the layout.  Bound by instructions (the norm's two
 // sums, the rotation and the quotients of the codes; 73 % of the issue slots) at some twice to three times what its bytes need (2 in per
-// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 78 us.
+// value, 2 or 9/16 out): 8192 tokens of 24 + 2 * 4 heads of 256, norms and a rotation of 64: 77 us.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLaunch p, const int steps, const int units) {
   constexpr int LANES = D / 8, HEADS = 32 / LANES;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLau
           for (int m = 1; m < LANES; m <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, m));
         }
         const float ms = __fmul_rn(sum_squares<LANES>(x, mag), 1.0f / D);
-        const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
+        const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(ms, p.eps)));
         if (turned) {
           float w[8];
           load_norm8(is_q ? p.q_norm : p.k_norm, p.norms_fp32, d, w);
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) k_kv_append(const AppendLau
 }
 
 // One thread per (token, head, 16 values): their 8 code bytes and scale byte of K and of V.
-template <int D, int DIR>  // 0 put, 1 get, 2 read
+template <int D, int DIR>  // 0 put, 1 get
 __global__ void __launch_bounds__(256) k_kv_move(const KvMoveLaunch p) {
   constexpr int GROUPS = D / 16;
   const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
@@ -275,37 +275,58 @@ __global__ void __launch_bounds__(256) k_kv_move(const KvMoveLaunch p) {
     } else {
       const uint2 c = there ? *codes : make_uint2(0, 0);
       const uint32_t sb = there ? tile[scale_at[w]] : 0;
-      if constexpr (DIR == 1) {
-        reinterpret_cast<uint2*>(w ? p.v_codes : p.k_codes)[i] = c;
-        (w ? p.v_scales : p.k_scales)[i] = (uint8_t)sb;
-      } else {
-        const float global = (w ? p.cache.v_scale : p.cache.k_scale)[h];
-        const float step = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(sb)));
-        uint32_t f[8];
-        e2m1x8_to_f16x8(c.x, f[0], f[1], f[2], f[3]);
-        e2m1x8_to_f16x8(c.y, f[4], f[5], f[6], f[7]);
-        float x[16];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 v = __half22float2(bits_h2(f[q]));
-          x[2 * q] = there ? v.x * step * global : 0.0f;
-          x[2 * q + 1] = there ? v.y * step * global : 0.0f;
-        }
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(w ? p.v : p.k) + i * 16);
-        dst[0] = pack8(reinterpret_cast<float(&)[8]>(x[0]));
-        dst[1] = pack8(reinterpret_cast<float(&)[8]>(x[8]));
-      }
+      reinterpret_cast<uint2*>(w ? p.v_codes : p.k_codes)[i] = c;
+      (w ? p.v_scales : p.k_scales)[i] = (uint8_t)sb;
     }
+  }
+}
+
+// One thread per (token, head, 8 values), of K and of V: a warp's stores are whole lines.  Bound by
+// the latency of slot, codes and store; 8192 tokens of 4 heads of 256: 10.6 us (13.4 with 16 values a thread).
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_read(const KvMoveLaunch p) {
+  constexpr int PARTS = D / 8;
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (i >= p.T * p.cache.heads * PARTS) return;
+  const int part = (int)(i % PARTS);
+  const int64_t th = i / PARTS, t = th >> 32 ? th / p.cache.heads : (uint32_t)th / (uint32_t)p.cache.heads;
+  const int h = (int)(th - t * p.cache.heads);
+  const int64_t slot = p.slots[t];
+  const bool there = slot >= 0 && slot < p.cache.slots;
+  const int in = there ? (int)(slot & (p.cache.page_size - 1)) : 0, r = in % kKvTile;
+  const uint8_t* tile = kv_tile<D>(p.cache, there ? slot >> p.cache.page_shift : 0, h, in);
+  const int code_at[2] = {kv_k_code(D, r, part * 4), kv_v_code(D, r, part * 4)};
+  const int scale_at[2] = {kv_k_scale(D, r, part >> 1), kv_v_scale(D, r, part >> 1)};
+  uint32_t codes[2], sb[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    codes[w] = there ? *reinterpret_cast<const uint32_t*>(tile + code_at[w]) : 0;
+    sb[w] = there ? tile[scale_at[w]] : 0;
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float global = (w ? p.cache.v_scale : p.cache.k_scale)[h];
+    const float step = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(sb[w])));
+    uint32_t f[4];
+    e2m1x8_to_f16x8(codes[w], f[0], f[1], f[2], f[3]);
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 v = __half22float2(bits_h2(f[q]));
+      x[2 * q] = there ? v.x * step * global : 0.0f;
+      x[2 * q + 1] = there ? v.y * step * global : 0.0f;
+    }
+    reinterpret_cast<uint4*>(w ? p.v : p.k)[i] = pack8(x);
   }
 }
 
 template <int D>
 cudaError_t move(const KvMoveLaunch& L, int dir, cudaStream_t s) {
-  const int64_t items = L.T * L.cache.heads * (D / 16);
+  const int64_t items = L.T * L.cache.heads * (dir == 2 ? D / 8 : D / 16);
   const unsigned blocks = (unsigned)((items + 255) / 256);
   if (dir == 0) k_kv_move<D, 0><<<blocks, 256, 0, s>>>(L);
   else if (dir == 1) k_kv_move<D, 1><<<blocks, 256, 0, s>>>(L);
-  else k_kv_move<D, 2><<<blocks, 256, 0, s>>>(L);
+  else k_kv_read<D><<<blocks, 256, 0, s>>>(L);
   return cudaGetLastError();
 }
 
