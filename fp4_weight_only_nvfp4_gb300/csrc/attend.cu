@@ -10,7 +10,9 @@ size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int 
 
 cudaError_t launch_attend(const AttendLaunch& L, int head_dim, cudaStream_t s) {
   if (cudaError_t e = launch_attend_row(L, head_dim, s)) return e;
-  return L.starts ? launch_attend_tile(L, head_dim, s) : cudaSuccess;
+  // no sequence has more rows than the call (4 rows of 32 heads on 8 of 128 behind 2000 keys: 14.4 us, 16.6 with
+  // both kernels)
+  return L.starts && L.T * L.group > kFewColumns ? launch_attend_tile(L, head_dim, s) : cudaSuccess;
 }
 
 }  // namespace vt
