@@ -56,9 +56,15 @@ __device__ __forceinline__ uint32_t magnitude8(const uint4 v) {
 // sum is held to 2^-32 of the largest square.  Where a vector takes the whole warp its lanes add integers, one instruction for
 // the ten of a sum by shuffles (8192 tokens of 32 heads of 256, read back: 99 us with shuffles and one value at a time, 98 with two at a
 // time, 91 so).
+// Every lane of the warp is in the sums over the lanes, whatever its vector holds: where the warp has several vectors,
+// one with an inf or NaN gets that in the place of its sum at the end, and no lane leaves before.
 template <int LANES>
 __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) {
-  if (mag >= 0x7F80u) return __uint_as_float(mag << 16);  // inf or NaN
+  const bool finite = mag < 0x7F80u;
+  const float special = __uint_as_float(mag << 16);  // inf or NaN
+  if constexpr (LANES == 32) {
+    if (!finite) return special;  // one vector, one mag: the whole warp
+  }
   const int e = min(max((int)(mag >> 7) - 127, -126), 126);  // (at 2^127 the sum is inf in any case)
   const float down = pow2f(-e), up = pow2f(e);
   constexpr float C = 1.5f * 1024.0f;                      // its last bit is 2^-13
@@ -85,7 +91,7 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8], uint32_t mag) 
       b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, m));
     }
   }
-  return __fadd_rn(a, b) * up * up;
+  return finite ? __fadd_rn(a, b) * up * up : special;
 }
 
 // Codes of x / d, each quotient rounded to fp32 first.  x times the rounded 1 / d is off by less than 2^-22 of
