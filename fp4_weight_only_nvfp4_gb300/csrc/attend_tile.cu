@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_half + 8 * sbuf);
+                __syncwarp();
                 tmem_ld32_issue(tS + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_wait(v[1]);
@@ -637,6 +638,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         if (live && out && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
           lost = nan_columns<D>(p.a, w.b, w.h, max(row_lo, (w.first + w.at) * KB),
                                 (int)min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB));
+        __syncwarp();  // lanes come back from that one by one; the loads from TMEM take the whole warp
         auto value = [&](uint32_t v, int col) {
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
         };
