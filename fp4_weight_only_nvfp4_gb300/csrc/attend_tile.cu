@@ -77,7 +77,7 @@ struct TileShared {
   int64_t G, total;    // CTAs in use, units in all
   int b, i;            // its tile
   int last;
-  int nan_seg[8];
+  unsigned long long nan_seg[8];   // of the segments under way: number + 1 in the upper word, columns below (see nan_columns)
   float half_m[128], half_l[128];  // of the row tile's second half of blocks
   int half_any[128];
   uint32_t tmem;
@@ -250,17 +250,41 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
 
-// NaN scales of the values that a row sees in this segment, read from the pages: a bit per 16
-// columns.  Only where a V warp met one: the products themselves take such a scale as zero, since
-// their other rows may not see it.
+// Keys [lo, hi), in whole blocks, that every row of the tile sees (none where lo >= hi).
 template <int D>
-__device__ __noinline__ uint32_t nan_columns(const AttendLaunch& a, int b, int h, int k0, int k1) {
-  uint32_t bits = 0;
-  for (int j = k0; j < k1; ++j) {
-    const int page = __ldg(a.tables + b * a.ldt + (j >> a.cache.page_shift));
+__device__ __forceinline__ void seen_by_all(const TileParams& p, const Walk<D>& w, int64_t* lo, int64_t* hi) {
+  constexpr int KB = TileCfg<D>::kKeys;
+  const int r0 = w.i * Walk<D>::per_tile(p), r1 = min(w.q.n, r0 + Walk<D>::per_tile(p));
+  const int64_t past = (int64_t)w.q.len - w.q.n, first = past + r0 + 1, last = past + r1;
+  *hi = first > 0 ? first / KB * KB : 0;
+  *lo = p.a.window > 0 && p.a.window < last ? (last - p.a.window + KB - 1) / KB * KB : 0;
+}
+
+// NaN scales of the values that a row sees in this segment: a bit per 16 columns.  The products take such a scale as
+// zero, since their other rows may not see it.  The V warps note which columns they met one in: `met`, bits 0 to 15, in
+// blocks that all of the tile's rows see; bit 16: in a block at the border of some row, and only the keys there are
+// looked up in the pages again.  They lie within the tile's rows and two blocks of either border: some hundreds, however
+// long the sequence is, so that no other role's wait runs out meanwhile.
+constexpr uint32_t kNanAtBorder = 1u << 16;
+template <int D>
+__device__ __noinline__ uint32_t nan_columns(const TileParams& p, const Walk<D>& w, uint32_t met, int row_lo, int row_hi) {
+  constexpr int KB = TileCfg<D>::kKeys;
+  uint32_t bits = met & (kNanAtBorder - 1);
+  if (!(met & kNanAtBorder)) return bits;
+  const AttendLaunch& a = p.a;
+  int64_t lo, hi;
+  seen_by_all(p, w, &lo, &hi);
+  const int64_t k0 = max((int64_t)row_lo, (int64_t)(w.first + w.at) * KB);
+  const int64_t k1 = min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB);
+  for (int64_t j = k0; j < k1; ++j) {
+    if (j >= lo && j < hi) {
+      j = hi - 1;
+      continue;
+    }
+    const int page = __ldg(a.tables + w.b * a.ldt + (j >> a.cache.page_shift));
     if (page < 0 || page >= a.cache.pages) continue;
-    const int in = j & (a.cache.page_size - 1);
-    const uint8_t* tile = kv_tile<D>(a.cache, page, h, in);
+    const int in = (int)j & (a.cache.page_size - 1);
+    const uint8_t* tile = kv_tile<D>(a.cache, page, w.h, in);
     for (int s = 0; s < D / 16; ++s)
       if ((tile[kv_v_scale(D, in % kKvTile, s)] & 0x7F) == 0x7F) bits |= 1u << s;
   }
@@ -633,9 +657,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         auto sink_of = [&]() { return __uint_as_float(ld_shared_v2(row_at + 8).y); };
         float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w.at == 0)) * C::kPartFloats;
         uint32_t lost = 0;
-        if (live && out && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
-          lost = nan_columns<D>(p.a, w.b, w.h, max(row_lo, (w.first + w.at) * KB),
-                                (int)min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB));
+        const unsigned long long met = *reinterpret_cast<volatile unsigned long long*>(&sh.nan_seg[w.no & 7]);
+        if (live && out && (uint32_t)(met >> 32) == (uint32_t)w.no + 1) lost = nan_columns<D>(p, w, (uint32_t)met, row_lo, row_hi);
         __syncwarp();  // lanes come back from that one by one; the loads from TMEM take the whole warp
         auto value = [&](uint32_t v, int col) {
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
@@ -855,6 +878,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       uint4 sc[C::kVJobs];
       int nvalid[C::kVJobs];   // of the lane's 8 tokens
       int segno;
+      bool seen;               // the block by every row of its tile
       // job vw + j * kVWarps: its tile (of 16 tokens) and, at head_dim 256, column block
       auto job_of = [&](int j) { return vw + j * C::kVWarps; };
       auto tile_of = [&](int j) { return D == 64 ? 2 * job_of(j) + (lane >> 4) : D == 128 ? job_of(j) : job_of(j) & 3; };
@@ -872,6 +896,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       };
       auto load = [&]() {
         segno = ld.no;
+        int64_t lo, hi;
+        seen_by_all(p, ld, &lo, &hi);
+        const int64_t k0 = (int64_t)(ld.first + lblk) * KB;
+        seen = k0 >= lo && k0 + KB <= hi;
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
           const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
@@ -920,7 +948,14 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           if (nan0 | nan1) {
             q[0] &= ~((nan0 >> 7) * 0xFFu);
             q[1] &= ~((nan1 >> 7) * 0xFFu);
-            *reinterpret_cast<volatile int*>(&sh.nan_seg[segno & 7]) = segno + 1;
+            const unsigned long long tag = (unsigned long long)((uint32_t)segno + 1) << 32;
+            const uint32_t bits = seen ? 1u << ((o >> 1) + 8 * block_of(j)) : kNanAtBorder;
+            unsigned long long* at = &sh.nan_seg[segno & 7];
+            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(at), was;
+            do {
+              was = old;
+              old = atomicCAS(at, was, (was >> 32 == tag >> 32 ? was : tag) | bits);
+            } while (old != was);
           }
           uint32_t x[4][4], y[4][4];  // [d][pair of tokens]
 #pragma unroll
