@@ -25,6 +25,11 @@
 // share the shared memory with the conversion's stores.  Five chunks of up to 900 rows behind 2500 keys, 64 heads
 // on 8 of 64, window 512 (five blocks a tile): 107 us, half of it a tile's start and end.
 //
+// The roles' loops together are about as long as the instruction cache, so code in them counts even where it is not
+// entered: 30 instructions more in the V warps' took 8192 rows from 537 to 565 us, with the stalls for instructions from 0.5
+// to 1.7 an issue.  So what a wait does when it is not over at once is a function of its own, and a pass that can
+// be a loop is one (565 to 513 us).
+//
 // Every wait inside the CTA is bounded (2 s); one that gives up sets the status word and ends every role.
 #include <cuda_bf16.h>
 
@@ -70,6 +75,7 @@ struct TileCfg {
   static constexpr int kPartFloats = kRows * (D + 4);     // O in columns of 4, then m, l, any
 };
 
+constexpr int kNanAtBorder = 16;
 struct TileShared {
   int64_t scan[32];
   int64_t seq_first[32 * 16 + 1];
@@ -77,7 +83,9 @@ struct TileShared {
   int64_t G, total;    // CTAs in use, units in all
   int b, i;            // its tile
   int last;
-  unsigned long long nan_seg[8];   // of the segments under way: number + 1 in the upper word, columns below (see nan_columns)
+  int2 v_seen[4][2];                // of each V warp, of two segments: its blocks that every row of the tile sees
+  // of the segments under way, that of number n in place n & 7: n + 1 where the values hold a NaN scale (see nan_columns)
+  int nan_seg[8], nan_what[8][17];
   float half_m[128], half_l[128];  // of the row tile's second half of blocks
   int half_any[128];
   uint32_t tmem;
@@ -214,7 +222,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
   tmem_st16(taddr + 16, b);
 }
 // Bounded wait; the warp sleeps in the barrier for up to 20 us at a time, so that those that wait take
-// no issue slots from those that work.
+// no issue slots from those that work.  What follows the first sleep is called, not inlined, for the code's size.
 __device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -225,8 +233,7 @@ __device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (try_wait_long(bar, parity)) return true;
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (try_wait_long(bar, parity)) return true;
@@ -236,6 +243,10 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (try_wait_long(bar, parity)) return true;
+  return wait_slow(bar, parity, abort, limit_ns);
 }
 // One answer for the warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
@@ -250,35 +261,37 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 constexpr uint32_t idesc_f16(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
 
-// Keys [lo, hi), in whole blocks, that every row of the tile sees (none where lo >= hi).
+// Blocks of keys [lo, hi) that every row of the tile sees (none where lo >= hi).
 template <int D>
-__device__ __forceinline__ void seen_by_all(const TileParams& p, const Walk<D>& w, int64_t* lo, int64_t* hi) {
+__device__ __forceinline__ void seen_by_all(const TileParams& p, const Walk<D>& w, int* lo, int* hi) {
   constexpr int KB = TileCfg<D>::kKeys;
   const int r0 = w.i * Walk<D>::per_tile(p), r1 = min(w.q.n, r0 + Walk<D>::per_tile(p));
-  const int64_t past = (int64_t)w.q.len - w.q.n, first = past + r0 + 1, last = past + r1;
-  *hi = first > 0 ? first / KB * KB : 0;
-  *lo = p.a.window > 0 && p.a.window < last ? (last - p.a.window + KB - 1) / KB * KB : 0;
+  const int past = w.q.len - w.q.n, first = past + r0 + 1, last = past + r1;
+  *hi = first > 0 ? first / KB : 0;
+  *lo = p.a.window > 0 && p.a.window < last ? (int)((uint32_t)(last - (int)p.a.window + KB - 1) / KB) : 0;
 }
 
 // NaN scales of the values that a row sees in this segment: a bit per 16 columns.  The products take such a scale as
-// zero, since their other rows may not see it.  The V warps note which columns they met one in: `met`, bits 0 to 15, in
-// blocks that all of the tile's rows see; bit 16: in a block at the border of some row, and only the keys there are
+// zero, since their other rows may not see it.  The V warps note the groups of columns that they met one in, in blocks
+// that all of the tile's rows see; for a block at the border of some row they note only that, and the keys there are
 // looked up in the pages again.  They lie within the tile's rows and two blocks of either border: some hundreds, however
 // long the sequence is, so that no other role's wait runs out meanwhile.
-constexpr uint32_t kNanAtBorder = 1u << 16;
 template <int D>
-__device__ __noinline__ uint32_t nan_columns(const TileParams& p, const Walk<D>& w, uint32_t met, int row_lo, int row_hi) {
+__device__ __noinline__ uint32_t nan_columns(const TileParams& p, const TileShared& sh, const Walk<D>& w, int row_lo, int row_hi) {
   constexpr int KB = TileCfg<D>::kKeys;
-  uint32_t bits = met & (kNanAtBorder - 1);
-  if (!(met & kNanAtBorder)) return bits;
+  const volatile int* what = sh.nan_what[w.no & 7];
+  uint32_t bits = 0;
+  for (int s = 0; s < D / 16; ++s)
+    if (what[s] == w.no + 1) bits |= 1u << s;
+  if (what[kNanAtBorder] != w.no + 1) return bits;
   const AttendLaunch& a = p.a;
-  int64_t lo, hi;
+  int lo, hi;
   seen_by_all(p, w, &lo, &hi);
   const int64_t k0 = max((int64_t)row_lo, (int64_t)(w.first + w.at) * KB);
   const int64_t k1 = min((int64_t)row_hi, (int64_t)(w.first + w.end) * KB);
   for (int64_t j = k0; j < k1; ++j) {
-    if (j >= lo && j < hi) {
-      j = hi - 1;
+    if (j >= (int64_t)lo * KB && j < (int64_t)hi * KB) {
+      j = (int64_t)hi * KB - 1;
       continue;
     }
     const int page = __ldg(a.tables + w.b * a.ldt + (j >> a.cache.page_shift));
@@ -334,7 +347,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
     mbar_init(half_read, 4);
     mbar_init(drain, 1);
     sh.abort = 0;
-    for (int i = 0; i < 8; ++i) sh.nan_seg[i] = 0;
+    for (int i = 0; i < 8; ++i) {
+      sh.nan_seg[i] = 0;
+      for (int k = 0; k <= kNanAtBorder; ++k) sh.nan_what[i][k] = 0;
+    }
   }
   if (warp == C::kWarpMma) tmem_alloc(smem_u32(&sh.tmem), 512);
   fence_mbar_init();
@@ -541,9 +557,9 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
               }
               // the maximum; the last 64 scores stay in registers.  Every load waits in its own statement: a load under
               // way writes its registers when it likes, and this loop has branches and loop edges that may move them
-              // (8192 rows, 32 heads on 4 of 128: 536 us; loads issued ahead of their wait took 552).
+              // (8192 rows, 32 heads on 4 of 128: loads issued ahead of their wait took 552 us, these 536).
               float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < KB; c += 64) {
                 tmem_ld32(tS + c, v[0]);
                 tmem_ld32(tS + c + 32, v[1]);
@@ -657,8 +673,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         auto sink_of = [&]() { return __uint_as_float(ld_shared_v2(row_at + 8).y); };
         float* part = p.parts + ((int64_t)blockIdx.x * 2 + (w.at == 0)) * C::kPartFloats;
         uint32_t lost = 0;
-        const unsigned long long met = *reinterpret_cast<volatile unsigned long long*>(&sh.nan_seg[w.no & 7]);
-        if (live && out && (uint32_t)(met >> 32) == (uint32_t)w.no + 1) lost = nan_columns<D>(p, w, (uint32_t)met, row_lo, row_hi);
+        if (live && out && *reinterpret_cast<volatile int*>(&sh.nan_seg[w.no & 7]) == w.no + 1)
+          lost = nan_columns<D>(p, sh, w, row_lo, row_hi);
         __syncwarp();  // lanes come back from that one by one; the loads from TMEM take the whole warp
         auto value = [&](uint32_t v, int col) {
           return (lost >> (col >> 4)) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(v);
@@ -878,7 +894,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       uint4 sc[C::kVJobs];
       int nvalid[C::kVJobs];   // of the lane's 8 tokens
       int segno;
-      bool seen;               // the block by every row of its tile
       // job vw + j * kVWarps: its tile (of 16 tokens) and, at head_dim 256, column block
       auto job_of = [&](int j) { return vw + j * C::kVWarps; };
       auto tile_of = [&](int j) { return D == 64 ? 2 * job_of(j) + (lane >> 4) : D == 128 ? job_of(j) : job_of(j) & 3; };
@@ -887,6 +902,13 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       bool more = ld.start(p, sh, cta0, cta1), pending = false;  // a block to load; one loaded
       int lblk = ld.at;
       int page[C::kVJobs];
+      uint32_t it = 0;
+      // which of the segment's blocks, the first being the warp's n-th, every row sees: for the rare block that holds a NaN
+      auto note = [&](uint32_t n) {
+        int lo, hi;
+        seen_by_all(p, ld, &lo, &hi);
+        sh.v_seen[vw][ld.no & 1] = make_int2(n + lo - ld.first - ld.at, n + hi - ld.first - ld.at);
+      };
       auto fetch = [&]() {
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
@@ -896,10 +918,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       };
       auto load = [&]() {
         segno = ld.no;
-        int64_t lo, hi;
-        seen_by_all(p, ld, &lo, &hi);
-        const int64_t k0 = (int64_t)(ld.first + lblk) * KB;
-        seen = k0 >= lo && k0 + KB <= hi;
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
           const int k = (ld.first + lblk) * KB + tile_of(j) * 16;
@@ -914,10 +932,11 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         if (++lblk == ld.end) {
           more = ld.next(p);
           lblk = ld.at;
+          if (more) note(it + 1);
         }
         if (more) fetch();
       };
-      if (more) fetch();
+      if (more) fetch(), note(0);
       const int rot = o & 3, odd = (o >> 2) & 1;
       uint32_t place[4];
 #pragma unroll
@@ -926,10 +945,10 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         place[e] = d0 * 128 + ((half ^ d0) << 4);
       }
       const uint32_t rsel = rot == 0 ? 0x3210 : rot == 1 ? 0x0321 : rot == 2 ? 0x1032 : 0x2103;
-      uint32_t it = 0;
       auto step = [&]() -> bool {
         const uint32_t stage = it & 1;
         if (!warp_wait(v_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
+        uint32_t met = 0;        // a NaN scale, a bit per column block
 #pragma unroll
         for (int j = 0; j < C::kVJobs; ++j) {
           if (job_of(j) >= C::kAllJobs) break;
@@ -948,14 +967,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
           if (nan0 | nan1) {
             q[0] &= ~((nan0 >> 7) * 0xFFu);
             q[1] &= ~((nan1 >> 7) * 0xFFu);
-            const unsigned long long tag = (unsigned long long)((uint32_t)segno + 1) << 32;
-            const uint32_t bits = seen ? 1u << ((o >> 1) + 8 * block_of(j)) : kNanAtBorder;
-            unsigned long long* at = &sh.nan_seg[segno & 7];
-            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(at), was;
-            do {
-              was = old;
-              old = atomicCAS(at, was, (was >> 32 == tag >> 32 ? was : tag) | bits);
-            } while (old != was);
+            met |= 1u << block_of(j);
           }
           uint32_t x[4][4], y[4][4];  // [d][pair of tokens]
 #pragma unroll
@@ -984,6 +996,15 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
             st_shared_v4(to | at, x[e][0], x[e][1], x[e][2], x[e][3]);
             st_shared_v4(to | (at ^ (128 + 16)), y[e][0], y[e][1], y[e][2], y[e][3]);
           }
+        }
+        // (noted behind the jobs, once: see the code's size above)
+        if (met) {
+          const int2 seen = sh.v_seen[vw][segno & 1];
+          const bool inside = (int)it >= seen.x && (int)it < seen.y;
+          for (int c = 0; c < 2; ++c)
+            if ((met >> c) & 1)
+              *reinterpret_cast<volatile int*>(&sh.nan_what[segno & 7][inside ? (o >> 1) + 8 * c : kNanAtBorder]) = segno + 1;
+          *reinterpret_cast<volatile int*>(&sh.nan_seg[segno & 7]) = segno + 1;
         }
         fence_proxy_async_smem();
         __syncwarp();
