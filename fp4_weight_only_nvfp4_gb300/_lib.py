@@ -100,6 +100,7 @@ SIGNATURES = {
     "vt_fp4_attention_workspace_bytes": (_ST, [_KV, _I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "vt_fp4_paged_attention": (_ST, [_KV, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _F32, _I64, _P,
                                      _P, _I64, _P, _SZ, _P]),
+    "vt_fp4_attention_test_hooks": (_ST, [ctypes.c_int, ctypes.c_int]),
     "vt_fp4_residual_norm": (_ST, [_P, _I64, _I64, _I64, _P, _I64, ctypes.c_int, _P, _P, _I64, _F32, _P,
                                    ctypes.c_int, _F32, _P, _I64, _P, _I64, _P]),
     "vt_fp4_last_error": (ctypes.c_char_p, []),

@@ -45,7 +45,8 @@ namespace vt {
 
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull, kPauseNs = 1000000ull;
+constexpr uint32_t kNoHold = 0xFFFFFFFFu;
 // (8192 rows, 32 heads on 4: 634 us with 4, 602 with 6, 615 with 9)
 constexpr int kLead = 6;
 
@@ -103,6 +104,8 @@ struct TileParams {
   uint32_t by_group;  // floor(2^32 / group) + 1: quotients of small numbers by it
   float* parts;
   uint64_t wait_ns;
+  uint32_t hold;      // test hook: the block before which the K warps stop,
+  int pause;          // or pause
 };
 
 // A sequence as this kernel takes it: n = 0 where the row kernel does.
@@ -247,6 +250,10 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (try_wait_long(bar, parity)) return true;
   return wait_slow(bar, parity, abort, limit_ns);
+}
+__device__ __noinline__ void pause() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kPauseNs) __nanosleep(1000);
 }
 // One answer for the warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
@@ -850,7 +857,15 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
       };
       if (more) fetch();
       uint32_t it = 0;
+      bool stopped = false;
       auto step = [&]() -> bool {
+        if (it == p.hold) {
+          if (!p.pause) {
+            stopped = true;
+            return false;
+          }
+          pause();
+        }
         const uint32_t stage = it & 1;
         if (!warp_wait(k_empty + 8 * stage, ((it >> 1) & 1) ^ 1, abort, p.wait_ns)) return false;
 #pragma unroll
@@ -882,7 +897,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         load();  // in flight while the stages are full
         pending = true;
       }
-      
+      ok |= stopped;  // (no wait of this warp's ran out)
     } else if (warp < C::kWarpMma) {
       // ------------------------------------------------------------ V to f16, turned
       const int vw = warp - C::kWarpV;
@@ -1016,7 +1031,6 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1) k_attend_tile(const T
         load();
         pending = true;
       }
-      
     } else {
       // ------------------------------------------------------------ the products
       if (elect_one()) {
@@ -1134,7 +1148,9 @@ cudaError_t launch_attend_tile(const AttendLaunch& L, int head_dim, cudaStream_t
   p.tokens = 128 / L.group;
   p.by_group = (uint32_t)(((uint64_t)1 << 32) / L.group + 1);
   p.parts = reinterpret_cast<float*>(L.workspace + kAttendCleared + attend_row_parts_bytes(head_dim));
-  p.wait_ns = kWaitNs;
+  p.wait_ns = L.wait_ns ? L.wait_ns : kWaitNs;
+  p.hold = L.withhold == 0 ? kNoHold : L.withhold > 0 ? L.withhold - 1 : -1 - L.withhold;
+  p.pause = L.withhold < 0;
   return head_dim == 64 ? go<64>(p, s) : head_dim == 128 ? go<128>(p, s) : go<256>(p, s);
 }
 

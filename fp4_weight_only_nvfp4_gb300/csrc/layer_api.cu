@@ -1,9 +1,12 @@
 // C entry points of what a decoder layer runs between its products (declared in include/vt_fp4.h):
 // the paged NVFP4 cache, the attention over it and the norms around the blocks.  Argument checks run
 // before any CUDA call.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
+
+#include <atomic>
 
 #include "handle.h"
 #include "kernels.h"
@@ -26,6 +29,8 @@ vt_status done(cudaError_t e, const char* where) {
   if (e == cudaSuccess) return VT_OK;
   return fail(VT_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+std::atomic<int> g_wait_us{0}, g_withhold{0};  // vt_fp4_attention_test_hooks
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxRows = (int64_t)1 << 24;       // tokens of a call
@@ -256,7 +261,17 @@ vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const 
   L.out = out;
   L.ldo = ldo;
   L.workspace = reinterpret_cast<uint8_t*>(workspace);
+  L.wait_ns = (uint64_t)g_wait_us.load() * 1000ull;
+  L.withhold = g_withhold.load();
   return done(launch_attend(L, (int)cache->head_dim, (cudaStream_t)s), "attention launch");
+}
+
+vt_status vt_fp4_attention_test_hooks(int wait_limit_us, int withhold) {
+  if (wait_limit_us < 0 || withhold == INT_MIN)
+    return fail(VT_ERR_INVALID_ARG, "wait_limit_us must be >= 0, withhold above INT_MIN");
+  g_wait_us.store(wait_limit_us);
+  g_withhold.store(withhold);
+  return VT_OK;
 }
 
 vt_status vt_fp4_residual_norm(const void* x, int64_t T, int64_t H, int64_t ldx, const void* residual,

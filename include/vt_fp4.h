@@ -532,6 +532,12 @@ vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const 
                                  const float* sinks, void* out, int64_t ldo, void* workspace,
                                  size_t ws_bytes, vt_stream_t s);
 
+/* Test hook of vt_fp4_paged_attention, whose signature has no options: for the calls made after it every
+ * bounded device-side wait gives up after wait_limit_us microseconds (0: the 2 s default), and withhold = n > 0
+ * makes the warps that load the keys of sequences of many rows stop before their n-th block of keys, n < 0 pause for a
+ * millisecond before their -n-th.  Process-wide; (0, 0) restores the defaults. */
+vt_status vt_fp4_attention_test_hooks(int wait_limit_us, int withhold);
+
 /* The norms around a block, with its gate and the residual sum:
  *   a = x, or norm(x) * post_weight;   h = residual + scale * gate * a;   y = norm(h) * weight,
  *   norm(x) = x / sqrt(sum x^2 / H + eps).
