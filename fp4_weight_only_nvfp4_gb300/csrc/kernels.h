@@ -257,7 +257,7 @@ struct AttendLaunch {
   uint64_t wait_ns;        // limit of the tile kernel's waits, 0: its own
   int withhold;            // test hook: n > 0: its K warps stop before their n-th block; -n: pause there
 };
-size_t attend_workspace_bytes(int64_t T, int64_t B, int q_heads, int heads, int head_dim);
+size_t attend_workspace_bytes(int64_t T, int group, int head_dim);
 cudaError_t launch_attend(const AttendLaunch& L, int head_dim, cudaStream_t s);
 
 struct NormLaunch {

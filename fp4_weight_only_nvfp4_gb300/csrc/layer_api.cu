@@ -215,7 +215,7 @@ vt_status vt_fp4_attention_workspace_bytes(const vt_fp4_kv_cache* cache, int64_t
   if (vt_status st = check_rows(T_max)) return st;
   if (vt_status st = check_rows(B_max)) return st;
   if (vt_status st = check_q_heads(q_heads, cache->heads)) return st;
-  *bytes = attend_workspace_bytes(T_max, B_max, (int)q_heads, (int)cache->heads, (int)cache->head_dim);
+  *bytes = attend_workspace_bytes(T_max, (int)(q_heads / cache->heads), (int)cache->head_dim);
   return VT_OK;
 }
 
@@ -241,7 +241,7 @@ vt_status vt_fp4_paged_attention(const vt_fp4_kv_cache* cache, int64_t T, const 
   if (!tables || !lens) return fail(VT_ERR_INVALID_ARG, "tables and lens must be set");
   if (!aligned(tables, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(sinks, 4))
     return fail(VT_ERR_MISALIGNED, "tables, lens, starts and sinks must be 4-byte aligned");
-  size_t need = attend_workspace_bytes(T, B, (int)q_heads, (int)cache->heads, (int)cache->head_dim);
+  const size_t need = attend_workspace_bytes(starts ? T : 0, (int)(q_heads / cache->heads), (int)cache->head_dim);
   if (!workspace) return fail(VT_ERR_INVALID_ARG, "workspace must be set");
   if (!aligned(workspace, 256)) return fail(VT_ERR_MISALIGNED, "workspace must be 256-byte aligned");
   if (ws_bytes < need) return fail(VT_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, need);

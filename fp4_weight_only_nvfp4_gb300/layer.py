@@ -196,7 +196,8 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.
 
 
 def attention_workspace(T_max: int, B_max: int, q_heads: int, cache: KVCache) -> torch.Tensor:
-    """A workspace for paged_attention of up to T_max rows of q_heads heads and B_max sequences."""
+    """A workspace for paged_attention of up to T_max rows of q_heads heads and B_max sequences; T_max = 0 for
+    calls without starts, whatever their rows."""
     n = ctypes.c_size_t(0)
     check(lib().vt_fp4_attention_workspace_bytes(cache.view, T_max, B_max, q_heads, ctypes.byref(n)),
           "vt_fp4_attention_workspace_bytes")
@@ -232,7 +233,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, tables: torch.Tensor, lens:
     ldo = _heads(out, "out", T, heads, D, gpu)
     if workspace is None:
         with _made_on(stream):
-            workspace = attention_workspace(T, B, heads, cache)
+            workspace = attention_workspace(0 if starts is None else T, B, heads, cache)
     wp, wn = _workspace(workspace, gpu)
     check(lib().vt_fp4_paged_attention(cache.view, T, q.data_ptr(), heads, ldq, tables.data_ptr(), ldt, lp, sp, B,
                                        D ** -0.5 if scale is None else scale, window, kp, out.data_ptr(),

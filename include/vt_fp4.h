@@ -501,7 +501,8 @@ vt_status vt_fp4_kv_get(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* 
                         uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, vt_stream_t s);
 
 /* Workspace of vt_fp4_paged_attention for up to T_max rows of q_heads heads and B_max sequences over
- * the cache; 256-byte aligned, its first VT_ATTENTION_CLEARED bytes zeroed once by the caller, reusable afterwards in stream order.
+ * the cache; T_max = 0 for calls without starts, whatever their rows.  Its size follows from head_dim and from whether T_max *
+ * q_heads / heads is above 32 (43 MB at head_dim 128, 1.4 MB up to there).  256-byte aligned, its first VT_ATTENTION_CLEARED bytes zeroed once by the caller, reusable afterwards in stream order.
  * Its first word is the status word (vt_fp4_workspace_status); after VT_ERR_TIMEOUT those bytes are
  * zeroed again before it is reused. */
 #define VT_ATTENTION_CLEARED 4096
