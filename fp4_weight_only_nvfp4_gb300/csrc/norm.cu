@@ -2,7 +2,9 @@
 //   a = x or norm(x) * post_weight,  h = residual + scale * gate * a,  y = norm(h) * weight.
 // One CTA per row; the row stays in registers in fp32 between its two sums, so that every input is
 // read once.  Bound by memory: x, residual and gate in, h and y out.  8192 rows of 5120, all in bf16:
-// 73 us, 5.8 TB/s (two vectors a thread: 74 us, one: 87).
+// 72 us, 5.8 TB/s.  Rows that no 16-byte load fits (an odd width, stride or offset) go one value at a time, which is bound by
+// instructions: 8192 rows of 5119 222 us, of 2001 63; above 8192 wide the 16 values a thread holds of x, residual and gate
+// spill (184 bytes): 4096 rows of 16383 479 us.
 #include <cuda_bf16.h>
 
 #include "actq.cuh"
@@ -216,15 +218,17 @@ cudaError_t launch_norm(const NormLaunch& L, cudaStream_t s) {
                    on16(L.weight) && on16(L.post_weight) && on16(L.gate) && L.ldg % 8 == 0 &&
                    on16(L.residual) && on16(L.h) && (L.ldr & rm) == 0 && (L.ldh & rm) == 0;
   const int64_t chunks = vec ? L.H / 8 : L.H;
-  const int n = vec ? (chunks <= kOne ? 1 : 2) : (chunks <= 2048 ? 2 : chunks <= 8192 ? 8 : 16);
+  // one vector a thread up to rows of 2048, two above (us, one and two: 203 rows of 2048 3.0 and 3.5, 8192 of 2048 34 and 29,
+  // 8192 of 4096 77 and 56); one value at a time, 8 a thread as long as 1024 threads are enough (8, 2 and 4 of them: 8192 rows
+  // of 1001 29, 43 and 33, of 2001 63, 95 and 65; 1 row of 2001 4.0, 3.6 and 3.4; 16 take 222 to 286 at 5119)
+  const int n = vec ? (chunks <= kOne ? 1 : 2) : (chunks <= 8192 ? 8 : 16);
   const int threads = (int)(((chunks + n - 1) / n + 31) / 32 * 32);
   const unsigned rows = (unsigned)L.T;
   if (vec) {
     if (n == 1) k_norm<8, 1><<<rows, threads, 0, s>>>(L);
     else k_norm<8, 2><<<rows, threads, 0, s>>>(L);
   } else {
-    if (n == 2) k_norm<1, 2><<<rows, threads, 0, s>>>(L);
-    else if (n == 8) k_norm<1, 8><<<rows, threads, 0, s>>>(L);
+    if (n == 8) k_norm<1, 8><<<rows, threads, 0, s>>>(L);
     else k_norm<1, 16><<<rows, threads, 0, s>>>(L);
   }
   return cudaGetLastError();
