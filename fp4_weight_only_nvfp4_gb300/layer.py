@@ -106,7 +106,7 @@ class KVCache:
     def put(self, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
             v_codes: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
         """Writes raw tokens: codes uint8 [T, heads, head_dim / 2] (low nibble = even), E4M3 bytes uint8 [T,
-        heads, head_dim / 16].  Slots outside the cache are skipped."""
+        heads, head_dim / 16].  Slots are distinct; those outside the cache are skipped."""
         sp, T = self._slots(slots), slots.shape[0]
         for t, name, n in ((k_codes, "k_codes", 2), (k_scales, "k_scales", 16), (v_codes, "v_codes", 2),
                            (v_scales, "v_scales", 16)):

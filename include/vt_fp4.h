@@ -493,7 +493,7 @@ vt_status vt_fp4_kv_read(const vt_fp4_kv_cache* cache, int64_t T, const int64_t*
 
 /* Raw tokens into and out of the cache: codes u8 [T][heads][head_dim / 2] (low nibble = even d, 8-byte
  * aligned) and scales u8 [T][heads][head_dim / 16] of keys and of values.  put skips a slot outside
- * the cache, get writes zeros for it. */
+ * the cache, get writes zeros for it.  Slots of put are distinct (two tokens of one slot leave a mixture of both). */
 vt_status vt_fp4_kv_put(const vt_fp4_kv_cache* cache, int64_t T, const int64_t* slots,
                         const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
                         const uint8_t* v_scales, vt_stream_t s);
