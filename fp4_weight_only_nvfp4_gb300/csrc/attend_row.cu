@@ -15,9 +15,9 @@
 // parts of one (sequence, head) in one CTA are joined in shared memory, those of several CTAs in the
 // workspace by the CTA that comes last, in the order of the line.  No wait for another CTA.
 //
-// Measured: 64 sequences of 2 to 8 thousand keys, 32 heads on 4 of 128: 51 us (3.7 TB/s), of which the
-// line's set-up, the first loads and the joins are some 15; one of 131071 keys, 24 heads on 4 of 256:
-// 51 us (2.9 TB/s; 8 warps a CTA, the output alone takes 64 registers a thread); 251 of up to 1500 keys,
+// Measured: 64 sequences of 2 to 8 thousand keys, 32 heads on 4 of 128: 50 us (3.8 TB/s), of which the
+// line's set-up, the first loads and the joins are over a third; one of 131071 keys, 24 heads on 4 of 256:
+// 50 us (3.0 TB/s; 8 warps a CTA, the output alone takes 64 registers a thread); 251 of up to 1500 keys,
 // 64 heads on 8 of 64, window 1024: 48 us (2.6 TB/s; half the values a score has at 128).
 #include <cuda_bf16.h>
 
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1) k_attend_row(const Row
   }
   if (U == 0) return;
   // a CTA has a chunk for every warp; as a multiple of the (head, set) lines, where there is room,
-  // equal lines end where CTAs end
+  // equal lines end where CTAs end (us, without and with: one sequence of 391 keys, 32 heads on 8 of 128, 14.9 and 10.2; 16 of 3000
+  // 24.4 and 20.2; one of 131071, 24 on 4 of 256, 49.4 and 50.0)
   int64_t G = min((int64_t)p.G, (U + C::kWarps - 1) / C::kWarps);
   const int64_t lines = (int64_t)B * p.a.cache.heads * row_sets(p.a, 1);
   if (lines <= p.G) G = min(U, min((G + lines - 1) / lines, (int64_t)p.G / lines) * lines);

@@ -20,15 +20,15 @@
 // CTAs; the parts of a tile that CTAs share are joined by the CTA that comes last.  Each (tile,
 // head) stands there with kLead units more than its blocks, for its start and end.
 //
-// Measured: a prompt of 8192 rows, 32 heads on 4 of 128: 552 us, 996 TFLOP/s of its causal half, the
-// tensor pipe 42 % active; the products of one row tile wait for its softmax (some 3000 cycles a block) and
+// Measured: a prompt of 8192 rows, 32 heads on 4 of 128: 502 us, 1095 TFLOP/s of its causal half, the
+// tensor pipe 48 % active; the products of one row tile wait for its softmax and
 // share the shared memory with the conversion's stores.  Five chunks of up to 900 rows behind 2500 keys, 64 heads
-// on 8 of 64, window 512 (five blocks a tile): 107 us, half of it a tile's start and end.
+// on 8 of 64, window 512 (five blocks a tile): 105 us, half of it a tile's start and end.  4096 rows, 24 heads on 4 of 256: 400 us.
 //
 // The roles' loops together are about as long as the instruction cache, so code in them counts even where it is not
-// entered: 30 instructions more in the V warps' took 8192 rows from 537 to 565 us, with the stalls for instructions from 0.5
-// to 1.7 an issue.  So what a wait does when it is not over at once is a function of its own, and a pass that can
-// be a loop is one (565 to 513 us).
+// entered: with 30 instructions more in the V warps' 8192 rows took 565 us instead of 537, and where the K warps' grew 635, with
+// 1.7 warps an issue waiting for instructions instead of 0.5.  So what a wait does when it is not over at once is a function
+// of its own, and a pass that can be a loop is one (565 to 513 us; 0.4 warps).
 //
 // Every wait inside the CTA is bounded (2 s); one that gives up sets the status word and ends every role.
 #include <cuda_bf16.h>
@@ -56,8 +56,8 @@ struct TileCfg {
   static constexpr int kSBufs = D == 256 ? 2 : 1;         // score buffers of a row tile
   static constexpr int kKeys = D == 256 ? 64 : 128;       // keys of a block
   static constexpr int kSoftWarps = 4 * kRowTiles;
-  // 16 warps for two row tiles: a 17th would leave every thread 96 registers, and the softmax
-  // spills with fewer than 128 (into an L1 that the shared memory leaves next to nothing).
+  // 16 warps for two row tiles: a 17th would leave every thread 96 registers, and the softmax takes all
+  // of its 128 (a spill goes into an L1 that the shared memory leaves next to nothing).
   static constexpr int kVWarps = kRowTiles == 2 ? 3 : 4;
   static constexpr int kWarpK = kSoftWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kVWarps;
   static constexpr int kThreads = (kWarpMma + 1) * 32;

@@ -117,7 +117,8 @@ __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float d)
 }
 
 // D / 8 lanes take one head's vector of one token, 8 values each; a warp takes `steps` times 32 / (D /
-// 8) heads of one token, so that the rotation's angles and the norms' weights are loaded once for them.
+// 8) heads of one token, so that the rotation's angles are loaded once for them.  (The norms' weights are loaded for every
+// head, from L1: the 64 registers a thread that four CTAs an SM leave have no room for them and spill 12 to 16 bytes as it is.)
 // The decisions of the quantiser follow the vector's values, so each operation is rounded on its
 // own: the result is that of the formulas in fp32 whatever the layout.  Bound by instructions (the norm's two
 // sums, the rotation and the quotients of the codes; 73 % of the issue slots) at some twice to three times what its bytes need (2 in per
